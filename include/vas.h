@@ -9,6 +9,12 @@
  *   paged_attn_fwd_tree, paged_attn_fwd_quant, paged_attn_fwd_static : the same
  *                     attention with draft-tree masks, over FP8 / INT8 pages, and
  *                     without a caller workspace.
+ *   paged_kv_append : the write side of the cache: per-head RMS norms of queries and
+ *                     keys, the position rotation and the store into the pages
+ *                     (quantised where the pool is), in one pass.
+ *   paged_kv_copy, paged_kv_keep_path : copies of whole or partly filled pages (forks,
+ *                     compaction) and the move of an accepted draft path to the slots
+ *                     after the context.
  *   spec_verify     : speculative-decoding modified rejection sampling with an
  *                     in-kernel Philox4x32-10 stream; spec_verify_tree, the same rule
  *                     over a draft tree.
@@ -61,7 +67,10 @@ typedef struct CUstream_st* vas_stream_t; /* identical to cudaStream_t */
 #define VAS_DEV_BAD_TOKEN 0x4      /* draft token outside [0, V)                       */
 #define VAS_DEV_EMPTY_ROW 0x8      /* the row to draw from has no positive mass        */
 #define VAS_DEV_TIMEOUT 0x10       /* a bounded in-kernel wait gave up                 */
-#define VAS_DEV_BAD_TREE 0x20      /* spec_verify_tree: a parent outside 0..node - 1     */
+#define VAS_DEV_BAD_TREE 0x20      /* spec_verify_tree: a parent outside 0..node - 1;    */
+                                   /* paged_kv_keep_path: a path that does not ascend,   */
+                                   /* leaves the window, or a sequence named twice       */
+#define VAS_DEV_BAD_POSITION 0x40  /* paged_kv_append: a position outside the table      */
 #define VAS_DEV_RESIDUAL_FALLBACK 0x100 /* informational: a zero residual after a       */
                                         /* rejection; the token was drawn from p_j      */
 
@@ -223,6 +232,121 @@ int paged_attn_fwd_static(const void* q, const void* k_pages, const void* v_page
                           const vas_attn_dims* dims, vas_stream_t stream);
 
 /* ==================================================================================
+ * Writing and moving the paged KV cache
+ *
+ * The pool of one layer is [num_pages, P, Hkv, D] for K and the same for V, as the
+ * attention entry points read it, with scales [num_pages, Hkv, P] when it is quantised
+ * ("llm-inference-optimization-batching" (tempatgunting.com), sections "Anatomy of the
+ * KV Cache" and "Quantization and Precision Choices for KV").
+ * ================================================================================== */
+typedef struct {
+  int32_t num_seqs;          /* B                                                     */
+  int32_t total_tokens;      /* T = sum of query_lens (rows of q, k and v)            */
+  int32_t num_q_heads;       /* Hq; 0: keys and values alone (q and q_out unused)     */
+  int32_t num_kv_heads;      /* Hkv                                                   */
+  int32_t head_dim;          /* D: 64 or 128                                          */
+  int32_t page_size;         /* P: 16 or 32                                           */
+  int32_t num_pages;
+  int32_t max_pages_per_seq;
+  int32_t kv_dtype;          /* of the pool: VAS_BF16, VAS_FP8_E4M3 or VAS_INT8 with  */
+                             /* bf16 q, k, v; VAS_F32 with fp32 q, k, v               */
+  int32_t rotary_dim;        /* leading elements of a head that are rotated: 0, or a  */
+                             /* multiple of 16 up to D                                */
+  int32_t interleaved;       /* 0: pairs (i, i + rotary_dim / 2); 1: (2i, 2i + 1)      */
+  int32_t max_position;      /* rows of cos_sin                                       */
+  int64_t q_stride;          /* elements from one token's row to the next; the heads   */
+  int64_t k_stride;          /* of a token are contiguous.  Multiples of 16 bytes.     */
+  int64_t v_stride;
+  float eps;                 /* added to the mean square of the norms, >= 0            */
+} vas_append_dims;
+
+/* Append this step's tokens to the cache.
+ *
+ * For token j of sequence i (packed row t, cache position pos = L_i - ql_i + j, exactly
+ * the tokens and positions of the paged_attn_fwd call that follows), and each head x of
+ * its q and k rows:
+ *     y = x * w / sqrt(mean(x^2) + eps)           (w: q_weight or k_weight; y = x if null)
+ *     (a, b) -> (a cos - b sin, b cos + a sin)    over the rotary pairs, angle number m of
+ *                                                 the pair: cos_sin[r][m], cos_sin[r][rotary_dim / 2 + m]
+ * with r = positions[t], or pos when positions is null (draft trees give the depth of a
+ * node; its slot stays pos).  q goes to q_out, k (so transformed) and v (as it is) to
+ * slot pos % P of page block_table[i][pos / P].  Arithmetic is fp32, with one rounding
+ * to the stored type at the end.  Quantised pools take, per token and head,
+ * scale = max |y| / 448 (E4M3) or / 127 (INT8), 1 if that is 0, and the codes
+ * y / scale rounded to nearest even; a row with an infinity or a NaN gets a scale that
+ * is not finite.  Nothing else of the pool is written.
+ *
+ * q, k, v     [T, heads, D] device, rows q_stride / k_stride / v_stride elements apart
+ *             (slices of one packed projection, say), 16-byte aligned.
+ * q_weight, k_weight [D] in the type of q, 16-byte aligned, or null.
+ * cos_sin     [max_position, rotary_dim] device fp32, 16-byte aligned: the cosines of
+ *             a row, then its sines.  Null with rotary_dim 0.
+ * positions   [T] device int32 or null.
+ * block_table, seq_lens, query_lens: as for paged_attn_fwd.
+ * q_out       [T, Hq, D] contiguous, 16-byte aligned; q itself if q is contiguous, and
+ *             otherwise apart from q, k and v.
+ * k_pages, v_pages, k_scale, v_scale: the pool (scales null unless it is quantised).
+ * Errors: VAS_E_INVALID_ARG, VAS_E_UNSUPPORTED, VAS_E_CUDA.  Device: a token whose
+ * sequence has inconsistent lengths (VAS_DEV_BAD_LENGTHS), whose page is outside the
+ * pool (VAS_DEV_BAD_PAGE) or whose position is outside the table (VAS_DEV_BAD_POSITION)
+ * is not stored and its q_out row is NaN.
+ * A page shared by several sequences is never a target of a correct step (vas_seq_fork
+ * gives every sequence its own last page); two tokens with one slot race.
+ */
+int paged_kv_append(const void* q, const void* k, const void* v, const void* q_weight,
+                    const void* k_weight, const float* cos_sin, const int32_t* positions,
+                    const int32_t* block_table, const int32_t* seq_lens,
+                    const int32_t* query_lens, void* q_out, void* k_pages, void* v_pages,
+                    float* k_scale, float* v_scale, const vas_append_dims* dims,
+                    vas_stream_t stream);
+
+typedef struct {
+  int32_t num_layers;        /* pools one behind the other: [num_layers, num_pages, ...] */
+  int32_t num_pages;
+  int32_t page_size;         /* P: 16 or 32                                           */
+  int32_t num_kv_heads;
+  int32_t head_dim;          /* 64 or 128                                             */
+  int32_t kv_dtype;          /* the four storage types                                */
+} vas_pool_dims;
+
+/* Copy pages src[i] -> dst[i], i < n, in K and V of every layer (with their scales when
+ * quantised): the tail of a fork, the moves of vas_pool_compact.
+ * src, dst, tokens: HOST arrays, read before the call returns.  tokens[i] in 1..P copies
+ * the first tokens[i] slots of the page and leaves the others; null copies whole pages.
+ * No page may be named twice among the destinations, or be both a source and a
+ * destination (VAS_E_INVALID_ARG, and nothing is copied): the copies run at once.
+ * k_pages, v_pages, k_scale, v_scale: device, 16-byte aligned; scales null unless the
+ * pool is quantised.
+ */
+int paged_kv_copy(void* k_pages, void* v_pages, float* k_scale, float* v_scale,
+                  const int32_t* src, const int32_t* dst, const int32_t* tokens, int32_t n,
+                  const vas_pool_dims* dims, vas_stream_t stream);
+
+/* After spec_verify_tree: move the accepted nodes of a draft tree to the slots behind
+ * the root, where the sequence's next tokens belong ("Continuous Batching & Speculative
+ * Decoding" (neuralmasteryai.com), section "4. Tree Attention & Medusa Heads").
+ * Row b of path [B, n] and accepted_len [B] (spec_verify_tree's outputs) belongs to
+ * sequence i = seq_index[b] of the batch (b itself when seq_index is null).  The window
+ * of ql_i tokens holds the root at position L_i - ql_i and node c at L_i - ql_i + c; for
+ * s < accepted_len[b], K and V (and scales) of node path[b][s] go to position
+ * L_i - ql_i + 1 + s, in every layer, as if all were read before any is written.  The
+ * caller then drops ql_i - 1 - accepted_len[b] tokens (vas_seq_rollback).
+ * accepted_len <= 0 moves nothing.
+ * block_table [num_seqs, max_pages_per_seq], seq_lens, query_lens [num_seqs]: device
+ * int32, those of the verification.
+ * Errors: VAS_E_INVALID_ARG, VAS_E_UNSUPPORTED, VAS_E_CUDA.  Device, and the row then
+ * moves nothing: VAS_DEV_BAD_TREE (accepted_len above n, a node outside 1..ql_i - 1 or
+ * not above the one before it, seq_index outside the batch, or naming a sequence that an
+ * earlier row names), VAS_DEV_BAD_LENGTHS, VAS_DEV_BAD_PAGE.
+ */
+int paged_kv_keep_path(void* k_pages, void* v_pages, float* k_scale, float* v_scale,
+                       const int32_t* block_table, const int32_t* seq_lens,
+                       const int32_t* query_lens, int32_t num_seqs, int32_t max_pages_per_seq,
+                       const int32_t* seq_index, const int32_t* path,
+                       const int32_t* accepted_len, int32_t B, int32_t n,
+                       const vas_pool_dims* dims, vas_stream_t stream);
+
+/* ==================================================================================
  * Speculative verification: modified rejection sampling
  *
  * Defined by: "Continuous Batching & Speculative Decoding" (neuralmasteryai.com),
@@ -347,6 +471,27 @@ int vas_pool_preempt_newest(vas_pool* pool, int64_t* victim);
  * (a common prefix) by reference; the remainder is copied into fresh pages by the
  * caller (the copies' ids are in the child's block table).  n_tokens <= parent length. */
 int vas_seq_fork(vas_pool* pool, int64_t parent_id, int64_t child_id, int32_t n_tokens);
+/* The copy that a fork leaves to the caller: the partly filled page of n_tokens tokens.
+ * Returns the tokens to copy (0..P-1; 0: none, *src = *dst = -1) and the parent's and
+ * the child's page that hold them, for paged_kv_copy.  Negative status: unknown id, or
+ * n_tokens past either length. */
+int32_t vas_seq_fork_tail(const vas_pool* pool, int64_t parent_id, int64_t child_id,
+                          int32_t n_tokens, int32_t* src, int32_t* dst);
+/* Compact the pool: the pages in use move to ids 0 .. used - 1, tables and free list
+ * follow, and free pages are handed out from the lowest id on.  src and dst [capacity]
+ * receive the copies to make (paged_kv_copy; no page is in both lists) before anything
+ * else touches the cache.  Returns their number.  With src or dst null nothing changes
+ * and the number of copies is returned; VAS_E_INVALID_ARG when capacity is below it. */
+int32_t vas_pool_compact(vas_pool* pool, int32_t* src, int32_t* dst, int32_t capacity);
+/* Groups of a batch for paged_attn_fwd_prefix: consecutive sequences of seq_ids whose
+ * tables start with the same pages.  A sequence joins the group before it when that
+ * leaves the pages saved, (members - 1) * prefix, no fewer.  query_lens (host, may be
+ * null: one token each) bounds each prefix to L_i - ql_i.  group_start [n + 1] and
+ * prefix_lens [n] are host arrays; prefixes are whole pages, in tokens (0 for a group
+ * of one).  Returns the number of groups, or a negative status. */
+int32_t vas_build_prefix_groups(const vas_pool* pool, const int64_t* seq_ids, int32_t n,
+                                const int32_t* query_lens, int32_t* group_start,
+                                int32_t* prefix_lens);
 /* Reference count of a page (0 = free). */
 int32_t vas_page_refcount(const vas_pool* pool, int32_t page);
 

@@ -39,6 +39,7 @@ VAS_DEV_BAD_TOKEN = 0x4
 VAS_DEV_EMPTY_ROW = 0x8
 VAS_DEV_TIMEOUT = 0x10
 VAS_DEV_BAD_TREE = 0x20
+VAS_DEV_BAD_POSITION = 0x40
 VAS_DEV_RESIDUAL_FALLBACK = 0x100
 VAS_F32 = 0
 VAS_BF16 = 1
@@ -57,13 +58,32 @@ class vas_attn_dims(ctypes.Structure):
                 ("scale", _f32)]
 
 
+class vas_append_dims(ctypes.Structure):
+    _fields_ = [("num_seqs", _i32), ("total_tokens", _i32), ("num_q_heads", _i32),
+                ("num_kv_heads", _i32), ("head_dim", _i32), ("page_size", _i32),
+                ("num_pages", _i32), ("max_pages_per_seq", _i32), ("kv_dtype", _i32),
+                ("rotary_dim", _i32), ("interleaved", _i32), ("max_position", _i32),
+                ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64), ("eps", _f32)]
+
+
+class vas_pool_dims(ctypes.Structure):
+    _fields_ = [("num_layers", _i32), ("num_pages", _i32), ("page_size", _i32),
+                ("num_kv_heads", _i32), ("head_dim", _i32), ("kv_dtype", _i32)]
+
+
 _P_dims = ctypes.POINTER(vas_attn_dims)
+_P_append = ctypes.POINTER(vas_append_dims)
+_P_pool = ctypes.POINTER(vas_pool_dims)
 _sig = {
     "paged_attn_workspace_size": ([_P_dims], _sz),
     "paged_attn_workspace_min": ([_P_dims], _sz),
     "paged_attn_fwd": ([_c_void_p] * 8 + [_P_dims, _c_void_p, _sz, _c_void_p], ctypes.c_int),
     "paged_attn_fwd_tree": ([_c_void_p] * 9 + [_P_dims, _c_void_p, _sz, _c_void_p], ctypes.c_int),
     "paged_attn_fwd_quant": ([_c_void_p] * 11 + [_P_dims, _c_void_p, _sz, _c_void_p], ctypes.c_int),
+    "paged_kv_append": ([_c_void_p] * 15 + [_P_append, _c_void_p], ctypes.c_int),
+    "paged_kv_copy": ([_c_void_p] * 7 + [_i32, _P_pool, _c_void_p], ctypes.c_int),
+    "paged_kv_keep_path": ([_c_void_p] * 7 + [_i32, _i32] + [_c_void_p] * 3 +
+                           [_i32, _i32, _P_pool, _c_void_p], ctypes.c_int),
     "spec_verify": ([_c_void_p, _c_void_p, _c_void_p, _u64, _c_void_p, _c_void_p, _i32, _i32, _i32,
                      _c_void_p], ctypes.c_int),
     "spec_verify_tree": ([_c_void_p] * 4 + [_u64] + [_c_void_p] * 3 + [_i32, _i32, _i32, _c_void_p],
@@ -84,6 +104,10 @@ _sig = {
     "vas_seq_free": ([_c_void_p, _i64], ctypes.c_int),
     "vas_pool_preempt_newest": ([_c_void_p, ctypes.POINTER(_i64)], ctypes.c_int),
     "vas_seq_fork": ([_c_void_p, _i64, _i64, _i32], ctypes.c_int),
+    "vas_seq_fork_tail": ([_c_void_p, _i64, _i64, _i32, ctypes.POINTER(_i32),
+                           ctypes.POINTER(_i32)], _i32),
+    "vas_pool_compact": ([_c_void_p, _c_void_p, _c_void_p, _i32], _i32),
+    "vas_build_prefix_groups": ([_c_void_p, _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p], _i32),
     "vas_page_refcount": ([_c_void_p, _i32], _i32),
     "vas_build_block_table": ([_c_void_p, _c_void_p, _i32, _c_void_p, _i32, _c_void_p], ctypes.c_int),
 }
@@ -223,6 +247,171 @@ def paged_attn_fwd_quant(q, k_pages, v_pages, k_scale, v_scale, block_table, seq
     _check("paged_attn_fwd_quant", st)
 
 
+def _same_device(**tensors) -> None:
+    """The calls run on the current device: every tensor has to be there."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+
+
+def _opt(t: Optional[torch.Tensor], name: str, dtype=None) -> ctypes.c_void_p:
+    return ctypes.c_void_p(0) if t is None else _dev(t, name, dtype)
+
+
+def _shape(t: Optional[torch.Tensor], name: str, shape) -> None:
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _heads(t: torch.Tensor, name: str, T: int, H: int, D: int, dtype):
+    """Pointer and token stride of a [T, H, D] tensor whose heads are contiguous."""
+    _shape(t, name, (T, H, D))
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if T * H > 0 and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if T > 1 else H * D)
+
+
+def paged_kv_append(q, k, v, block_table, seq_lens, query_lens, q_out, k_pages, v_pages, *,
+                    cos_sin=None, positions=None, q_weight=None, k_weight=None,
+                    interleaved: bool = False, eps: float = 1e-6, k_scale=None, v_scale=None,
+                    quant: Optional[str] = None, stream=None) -> None:
+    """Norms, rotation and store of this step's tokens (include/vas.h: paged_kv_append).
+    q [T, Hq, D], k and v [T, Hkv, D] (rows any 16-byte multiple apart, heads contiguous),
+    cos_sin [max_position, rotary_dim] fp32 or None, positions [T] int32 or None; q and
+    q_out may both be None.  k_pages / v_pages [num_pages, P, Hkv, D], with quant uint8
+    codes and k_scale / v_scale [num_pages, Hkv, P]."""
+    _same_device(q=q, k=k, v=v, block_table=block_table, seq_lens=seq_lens, query_lens=query_lens,
+                 q_out=q_out, k_pages=k_pages, v_pages=v_pages, cos_sin=cos_sin,
+                 positions=positions, q_weight=q_weight, k_weight=k_weight, k_scale=k_scale,
+                 v_scale=v_scale)
+    num_pages, P, Hkv, D = k_pages.shape
+    T, B = int(k.shape[0]), int(seq_lens.shape[0])
+    if quant is not None:
+        if quant not in _QUANT_CODES or k.dtype != torch.bfloat16 or k_pages.dtype != torch.uint8:
+            raise ValueError("a quantised pool is uint8 codes with bf16 q, k and v")
+        code = _QUANT_CODES[quant]
+    else:
+        if k.dtype not in _KV_CODES or k_pages.dtype != k.dtype:
+            raise ValueError("k and k_pages must share a dtype in {bf16, fp32}")
+        code = _KV_CODES[k.dtype]
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    Hq = 0 if q is None else int(q.shape[1])
+    kp, ks = _heads(k, "k", T, Hkv, D, k.dtype)
+    vp, vs = _heads(v, "v", T, Hkv, D, k.dtype)
+    qp, qs = _heads(q, "q", T, Hq, D, k.dtype) if Hq else (ctypes.c_void_p(0), 0)
+    _shape(q_out, "q_out", (T, Hq, D))
+    _shape(v_pages, "v_pages", k_pages.shape)
+    _shape(query_lens, "query_lens", (B,))
+    _shape(block_table, "block_table", (B, block_table.shape[-1]))
+    _shape(positions, "positions", (T,))
+    _shape(q_weight, "q_weight", (D,))
+    _shape(k_weight, "k_weight", (D,))
+    _shape(k_scale, "k_scale", (num_pages, Hkv, P))
+    _shape(v_scale, "v_scale", (num_pages, Hkv, P))
+    if cos_sin is not None and cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_position, rotary_dim]")
+    dims = vas_append_dims(num_seqs=B, total_tokens=T, num_q_heads=Hq, num_kv_heads=int(Hkv),
+                           head_dim=int(D), page_size=int(P), num_pages=int(num_pages),
+                           max_pages_per_seq=int(block_table.shape[1]), kv_dtype=code,
+                           rotary_dim=0 if cos_sin is None else int(cos_sin.shape[1]),
+                           interleaved=int(interleaved),
+                           max_position=0 if cos_sin is None else int(cos_sin.shape[0]),
+                           q_stride=qs, k_stride=ks, v_stride=vs, eps=float(eps))
+    st = _lib.paged_kv_append(
+        qp, kp, vp, _opt(q_weight, "q_weight", k.dtype), _opt(k_weight, "k_weight", k.dtype),
+        _opt(cos_sin, "cos_sin", torch.float32), _opt(positions, "positions", torch.int32),
+        _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32),
+        _dev(query_lens, "query_lens", torch.int32), _opt(q_out, "q_out", k.dtype),
+        _dev(k_pages, "k_pages"), _dev(v_pages, "v_pages", k_pages.dtype),
+        _opt(k_scale, "k_scale", torch.float32), _opt(v_scale, "v_scale", torch.float32),
+        ctypes.byref(dims), _stream_ptr(stream))
+    _check("paged_kv_append", st)
+
+
+def _pool_dims(k_pages, v_pages, k_scale, v_scale) -> vas_pool_dims:
+    """vas_pool_dims of [num_pages, P, Hkv, D] pools, or [layers, num_pages, P, Hkv, D]."""
+    if k_pages.dim() not in (4, 5):
+        raise ValueError("a pool is [num_pages, P, Hkv, D], or that for each layer")
+    _shape(v_pages, "v_pages", k_pages.shape)
+    *lead, n, P, Hkv, D = k_pages.shape
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale come together")
+    _shape(k_scale, "k_scale", (*lead, n, Hkv, P))
+    _shape(v_scale, "v_scale", (*lead, n, Hkv, P))
+    if k_pages.dtype == torch.uint8:
+        code = VAS_FP8_E4M3  # either kind of code: they are moved as bytes
+    elif k_pages.dtype in _KV_CODES:
+        code = _KV_CODES[k_pages.dtype]
+    else:
+        raise ValueError("k_pages must be bf16, fp32 or uint8 codes")
+    return vas_pool_dims(num_layers=int(lead[0]) if lead else 1, num_pages=int(n), page_size=int(P),
+                         num_kv_heads=int(Hkv), head_dim=int(D), kv_dtype=code)
+
+
+def paged_kv_copy(k_pages, v_pages, src, dst, *, tokens=None, k_scale=None, v_scale=None,
+                  stream=None) -> None:
+    """Copy pages src[i] -> dst[i] of K and V (include/vas.h: paged_kv_copy).  src, dst and
+    tokens are host sequences of integers; pools as in paged_kv_append, or with a leading
+    layer dimension."""
+    import numpy as np
+    _same_device(k_pages=k_pages, v_pages=v_pages, k_scale=k_scale, v_scale=v_scale)
+    dims = _pool_dims(k_pages, v_pages, k_scale, v_scale)
+
+    def host(x, name):
+        wide = np.ascontiguousarray(x)
+        if wide.size and wide.dtype.kind not in "iu":
+            raise ValueError(f"{name} must hold integers")
+        if wide.ndim != 1 or (wide.size and (wide.min() < 0 or wide.max() > 2**31 - 1)):
+            raise ValueError(f"{name} must be a list of page numbers")
+        return np.ascontiguousarray(wide, dtype=np.int32)
+
+    s, d = host(src, "src"), host(dst, "dst")
+    t = None if tokens is None else host(tokens, "tokens")
+    if len(s) != len(d) or (t is not None and len(t) != len(s)):
+        raise ValueError("src, dst and tokens differ in length")
+    ptr = lambda a: ctypes.c_void_p(0) if a is None else a.ctypes.data_as(_c_void_p)
+    st = _lib.paged_kv_copy(_dev(k_pages, "k_pages"), _dev(v_pages, "v_pages", k_pages.dtype),
+                            _opt(k_scale, "k_scale", torch.float32),
+                            _opt(v_scale, "v_scale", torch.float32), ptr(s), ptr(d), ptr(t),
+                            len(s), ctypes.byref(dims), _stream_ptr(stream))
+    _check("paged_kv_copy", st)
+
+
+def paged_kv_keep_path(k_pages, v_pages, block_table, seq_lens, query_lens, path, accepted_len, *,
+                       seq_index=None, k_scale=None, v_scale=None, stream=None) -> None:
+    """Move the accepted nodes of draft trees behind their roots (include/vas.h:
+    paged_kv_keep_path).  path [B, n] and accepted_len [B] int32 as spec_verify_tree writes
+    them; seq_index [B] int32 gives the batch row of each (default: row b); pools as in
+    paged_kv_copy."""
+    _same_device(k_pages=k_pages, v_pages=v_pages, block_table=block_table, seq_lens=seq_lens,
+                 query_lens=query_lens, path=path, accepted_len=accepted_len, seq_index=seq_index,
+                 k_scale=k_scale, v_scale=v_scale)
+    dims = _pool_dims(k_pages, v_pages, k_scale, v_scale)
+    B, n = path.shape
+    N = int(seq_lens.shape[0])
+    _shape(accepted_len, "accepted_len", (B,))
+    _shape(seq_index, "seq_index", (B,))
+    _shape(query_lens, "query_lens", (N,))
+    _shape(block_table, "block_table", (N, block_table.shape[-1]))
+    st = _lib.paged_kv_keep_path(
+        _dev(k_pages, "k_pages"), _dev(v_pages, "v_pages", k_pages.dtype),
+        _opt(k_scale, "k_scale", torch.float32), _opt(v_scale, "v_scale", torch.float32),
+        _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32),
+        _dev(query_lens, "query_lens", torch.int32), N, int(block_table.shape[1]),
+        _opt(seq_index, "seq_index", torch.int32), _dev(path, "path", torch.int32),
+        _dev(accepted_len, "accepted_len", torch.int32), B, n, ctypes.byref(dims),
+        _stream_ptr(stream))
+    _check("paged_kv_keep_path", st)
+
+
 def spec_verify_tree(p, q, draft_tokens, parents, seed: int, accepted_len, out_tokens, path, *,
                      stream=None) -> None:
     """Verification of a draft tree (include/vas.h: spec_verify_tree).  p [B, n+1, V] fp32,
@@ -323,6 +512,44 @@ class PagePool:
 
     def fork(self, parent: int, child: int, n_tokens: int) -> int:
         return int(_lib.vas_seq_fork(self._h, parent, child, n_tokens))
+
+    def fork_tail(self, parent: int, child: int, n_tokens: int):
+        """(source page, target page, tokens) of the copy a fork leaves, or None."""
+        a, b = _i32(-1), _i32(-1)
+        r = int(_lib.vas_seq_fork_tail(self._h, parent, child, n_tokens, ctypes.byref(a),
+                                       ctypes.byref(b)))
+        if r < 0:
+            raise VasError("vas_seq_fork_tail", r)
+        return (int(a.value), int(b.value), r) if r else None
+
+    def compact(self):
+        """Pages in use move to the lowest ids: (src, dst) of the copies to make."""
+        import numpy as np
+        n = int(_lib.vas_pool_compact(self._h, None, None, 0))
+        if n < 0:
+            raise VasError("vas_pool_compact", n)
+        src, dst = np.empty(n, dtype=np.int32), np.empty(n, dtype=np.int32)
+        r = int(_lib.vas_pool_compact(self._h, src.ctypes.data_as(_c_void_p),
+                                      dst.ctypes.data_as(_c_void_p), n))
+        if r < 0:
+            raise VasError("vas_pool_compact", r)
+        return src, dst
+
+    def prefix_groups(self, seq_ids, query_lens=None):
+        """(group_start, prefix_lens) of consecutive sequences with common first pages."""
+        import numpy as np
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        ql = None if query_lens is None else np.ascontiguousarray(query_lens, dtype=np.int32)
+        if ql is not None and ql.shape != ids.shape:
+            raise ValueError("query_lens needs one entry per sequence")
+        start, lens = np.zeros(len(ids) + 1, np.int32), np.zeros(max(len(ids), 1), np.int32)
+        g = int(_lib.vas_build_prefix_groups(
+            self._h, ids.ctypes.data_as(_c_void_p), len(ids),
+            ctypes.c_void_p(0) if ql is None else ql.ctypes.data_as(_c_void_p),
+            start.ctypes.data_as(_c_void_p), lens.ctypes.data_as(_c_void_p)))
+        if g < 0:
+            raise VasError("vas_build_prefix_groups", g)
+        return start[:g + 1], lens[:g]
 
     def refcount(self, page: int) -> int:
         return int(_lib.vas_page_refcount(self._h, page))

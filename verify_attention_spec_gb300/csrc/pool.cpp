@@ -12,6 +12,7 @@
 // waste is bounded by one partially filled page per sequence.
 #include <cstdint>
 #include <map>
+#include <new>
 #include <unordered_map>
 #include <vector>
 
@@ -209,6 +210,99 @@ int vas_seq_fork(vas_pool* pool, int64_t parent_id, int64_t child_id, int32_t n_
   pool->by_age[c.admitted] = child_id;
   pool->seqs.emplace(child_id, std::move(c));
   return VAS_OK;
+}
+
+int32_t vas_seq_fork_tail(const vas_pool* pool, int64_t parent_id, int64_t child_id,
+                          int32_t n_tokens, int32_t* src, int32_t* dst) {
+  if (!pool || !src || !dst || n_tokens < 0) return VAS_E_INVALID_ARG;
+  *src = *dst = -1;
+  auto p = pool->seqs.find(parent_id), c = pool->seqs.find(child_id);
+  if (p == pool->seqs.end() || c == pool->seqs.end()) return VAS_E_NOT_FOUND;
+  if (n_tokens > p->second.len || n_tokens > c->second.len) return VAS_E_INVALID_ARG;
+  const int32_t page = n_tokens / pool->page_size, tokens = n_tokens % pool->page_size;
+  if (tokens == 0) return 0;
+  // tokens > 0: both sequences reach into this page, so both tables have it.
+  const int32_t from = p->second.pages[page], to = c->second.pages[page];
+  if (from == to) return 0;
+  *src = from;
+  *dst = to;
+  return tokens;
+}
+
+int32_t vas_pool_compact(vas_pool* pool, int32_t* src, int32_t* dst, int32_t capacity) {
+  if (!pool || capacity < 0) return VAS_E_INVALID_ARG;
+  const int32_t used = pool->num_pages - static_cast<int32_t>(pool->free_list.size());
+  // Pages in use at or above `used` move to the free ids below it; there are as many of
+  // one as of the other, and no id is both.
+  int32_t moves = 0;
+  for (int32_t p = used; p < pool->num_pages; ++p) moves += pool->refcount[p] > 0;
+  if (!src || !dst) return moves;
+  if (moves > capacity) return VAS_E_INVALID_ARG;
+  std::vector<int32_t> to;
+  try {
+    to.resize(static_cast<size_t>(pool->num_pages));
+  } catch (const std::bad_alloc&) {
+    return VAS_E_NOMEM;
+  }
+  int32_t hole = 0, m = 0;
+  for (int32_t p = 0; p < pool->num_pages; ++p) to[p] = p;
+  for (int32_t p = used; p < pool->num_pages; ++p) {
+    if (pool->refcount[p] == 0) continue;
+    while (pool->refcount[hole] > 0) ++hole;
+    src[m] = p;
+    dst[m++] = hole;
+    to[p] = hole;
+    pool->refcount[hole] = pool->refcount[p];
+    pool->refcount[p] = 0;
+  }
+  for (auto& e : pool->seqs)
+    for (int32_t& pg : e.second.pages) pg = to[pg];
+  // The stack's back, handed out next, is the lowest free id.
+  const int32_t n_free = static_cast<int32_t>(pool->free_list.size());
+  for (int32_t i = 0; i < n_free; ++i) pool->free_list[i] = pool->num_pages - 1 - i;
+  return moves;
+}
+
+int32_t vas_build_prefix_groups(const vas_pool* pool, const int64_t* seq_ids, int32_t n,
+                                const int32_t* query_lens, int32_t* group_start,
+                                int32_t* prefix_lens) {
+  if (!pool || n < 0 || !group_start || (n > 0 && (!seq_ids || !prefix_lens)))
+    return VAS_E_INVALID_ARG;
+  const int32_t P = pool->page_size;
+  // Every id is known and every window fits before anything is written.
+  for (int32_t i = 0; i < n; ++i) {
+    auto it = pool->seqs.find(seq_ids[i]);
+    if (it == pool->seqs.end()) return VAS_E_NOT_FOUND;
+    const int32_t ql = query_lens ? query_lens[i] : 1;
+    if (ql < 0 || ql > it->second.len) return VAS_E_INVALID_ARG;
+  }
+  int32_t groups = 0;
+  const Seq* first = nullptr;     // of the open group
+  int64_t members = 0, limit = 0;  // its sequences, its prefix in pages
+  group_start[0] = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const Seq& s = pool->seqs.find(seq_ids[i])->second;
+    const int32_t ql = query_lens ? query_lens[i] : 1;
+    const int64_t most = (s.len - ql) / P;  // whole pages of context
+    if (first) {
+      int64_t common = 0;
+      const int64_t bound = limit < most ? limit : most;
+      while (common < bound && first->pages[common] == s.pages[common]) ++common;
+      if (common > 0 && members * common >= (members - 1) * limit) {
+        ++members;
+        limit = common;
+        prefix_lens[groups - 1] = static_cast<int32_t>(limit * P);
+        group_start[groups] = i + 1;
+        continue;
+      }
+    }
+    first = &s;
+    members = 1;
+    limit = most;
+    prefix_lens[groups++] = 0;
+    group_start[groups] = i + 1;
+  }
+  return groups;
 }
 
 int32_t vas_page_refcount(const vas_pool* pool, int32_t page) {
