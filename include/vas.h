@@ -9,6 +9,8 @@
  *   paged_attn_fwd_tree, paged_attn_fwd_quant, paged_attn_fwd_static : the same
  *                     attention with draft-tree masks, over FP8 / INT8 pages, and
  *                     without a caller workspace.
+ *   paged_attn_fwd_prefix : the same attention for groups of sequences that share a
+ *                     prefix, whose pages are read once per group.
  *   paged_kv_append : the write side of the cache: per-head RMS norms of queries and
  *                     keys, the position rotation and the store into the pages
  *                     (quantised where the pool is), in one pass.
@@ -230,6 +232,49 @@ int paged_attn_fwd_static(const void* q, const void* k_pages, const void* v_page
                           const int32_t* block_table, const int32_t* seq_lens,
                           const int32_t* query_lens, void* out, float* lse,
                           const vas_attn_dims* dims, vas_stream_t stream);
+
+/* paged_attn_fwd for a batch whose sequences share prefixes.
+ *
+ * Defined by: "llm-inference-optimization-batching" (tempatgunting.com), section
+ * "Anatomy of the KV Cache" -- block tables of several sequences point at the pages of a
+ * common prefix.  The result is that of paged_attn_fwd (paged_attn_fwd_tree,
+ * paged_attn_fwd_quant) on the same arguments; what changes is that a group's prefix
+ * pages are read once for all its members: with x the prefix positions and y the rest,
+ *     lse = ln(e^lse_x + e^lse_y),   out = e^(lse_x - lse) out_x + e^(lse_y - lse) out_y.
+ *
+ * group_start [num_groups + 1] device int32: group g is the sequences group_start[g] ..
+ *             group_start[g + 1] - 1 of the batch.  Ascending, within 0..num_seqs;
+ *             sequences outside every group have no shared prefix.
+ * prefix_lens [num_groups] device int32: tokens every member of group g shares, their
+ *             first prefix_lens[g] positions; at most L_i - ql_i of each member with
+ *             query tokens (the query tokens are never shared).  Only whole pages are
+ *             shared: the remainder is taken from each member's own table.  0: none.
+ *             Over these pages the tables of a group's members must agree; the first
+ *             member with query tokens is the one whose table is read there.
+ * k_scale, v_scale  as for paged_attn_fwd_quant; null for a bf16 pool.
+ * tree_mask   as for paged_attn_fwd_tree, or null.
+ * dims->kv_dtype is VAS_BF16, VAS_FP8_E4M3 or VAS_INT8 (VAS_F32: VAS_E_UNSUPPORTED).
+ * workspace   at least paged_attn_prefix_workspace_min(dims, num_groups) bytes.
+ * A group is computed with its members apart, as paged_attn_fwd does, where sharing
+ * would not pay (one member with query tokens, a short prefix) or the workspace has no
+ * room for its partials.
+ * Errors: those of paged_attn_fwd_quant.  A prefix_lens entry below 0 or past some
+ * member's L_i - ql_i, or group_start out of order, sets VAS_DEV_BAD_LENGTHS; then no
+ * group of the call is shared, and the members that their group's prefix does not fit,
+ * like the sequences that paged_attn_fwd refuses, get NaN rows.  A bad page in a shared
+ * prefix makes the rows of all its members NaN.
+ */
+int paged_attn_fwd_prefix(const void* q, const void* k_pages, const void* v_pages,
+                          const float* k_scale, const float* v_scale,
+                          const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* query_lens, const int32_t* group_start,
+                          const int32_t* prefix_lens, const uint64_t* tree_mask, void* out,
+                          float* lse, const vas_attn_dims* dims, int32_t num_groups,
+                          void* workspace, size_t workspace_bytes, vas_stream_t stream);
+
+/* Recommended and smallest workspace of paged_attn_fwd_prefix (0 for invalid dims). */
+size_t paged_attn_prefix_workspace_size(const vas_attn_dims* dims, int32_t num_groups);
+size_t paged_attn_prefix_workspace_min(const vas_attn_dims* dims, int32_t num_groups);
 
 /* ==================================================================================
  * Writing and moving the paged KV cache

@@ -217,3 +217,28 @@ def test_keep_path_refusals(vas_lib):
     assert keep(ptrs={"ks": FAKE}) == bad
     assert keep(head_dim=72) == v.VAS_E_UNSUPPORTED
     assert keep(B=0) == v.VAS_OK and keep(num_layers=0) == v.VAS_OK
+
+
+def test_prefix_attention_refusals(vas_lib):
+    v = vas_lib
+    d = dict(num_seqs=4, total_q_tokens=10, num_q_heads=32, num_kv_heads=8, head_dim=128, page_size=16,
+             num_pages=100, max_pages_per_seq=10, kv_dtype=v.VAS_BF16, scale=0.0)
+
+    def call(start=FAKE, lens=FAKE, groups=2, nbytes=1 << 30, q=FAKE, ks=NULL, **kw):
+        dims = v.vas_attn_dims(**{**d, **kw})
+        return v._lib.paged_attn_fwd_prefix(q, FAKE, FAKE, ks, NULL, FAKE, FAKE, FAKE, start, lens, NULL,
+                                            FAKE, FAKE, ctypes.byref(dims), groups, FAKE, nbytes, NULL)
+
+    bad, uns = v.VAS_E_INVALID_ARG, v.VAS_E_UNSUPPORTED
+    assert call(groups=-1) == bad and call(start=NULL) == bad and call(lens=NULL) == bad
+    assert call(start=P_((1 << 20) + 2)) == bad and call(q=NULL) == bad and call(ks=FAKE) == bad
+    assert call(num_q_heads=30) == bad and call(kv_dtype=v.VAS_FP8_E4M3) == bad
+    assert call(kv_dtype=v.VAS_F32) == uns and call(head_dim=80) == uns
+    assert call(nbytes=64) == v.VAS_E_WORKSPACE
+    assert call(num_seqs=0) == v.VAS_OK
+    dims = v.vas_attn_dims(**d)
+    sizes = [v.paged_attn_prefix_workspace_min(dims, g) for g in (0, 1, 1000)]
+    assert 0 < sizes[0] <= sizes[1] < sizes[2]
+    assert v.paged_attn_prefix_workspace_size(dims, 3) > v.paged_attn_prefix_workspace_min(dims, 3)
+    assert v.paged_attn_prefix_workspace_size(dims, -1) == 0
+    assert v.paged_attn_prefix_workspace_min(v.vas_attn_dims(**{**d, "kv_dtype": v.VAS_F32}), 1) == 0

@@ -80,6 +80,10 @@ _sig = {
     "paged_attn_fwd": ([_c_void_p] * 8 + [_P_dims, _c_void_p, _sz, _c_void_p], ctypes.c_int),
     "paged_attn_fwd_tree": ([_c_void_p] * 9 + [_P_dims, _c_void_p, _sz, _c_void_p], ctypes.c_int),
     "paged_attn_fwd_quant": ([_c_void_p] * 11 + [_P_dims, _c_void_p, _sz, _c_void_p], ctypes.c_int),
+    "paged_attn_fwd_prefix": ([_c_void_p] * 13 + [_P_dims, _i32, _c_void_p, _sz, _c_void_p],
+                              ctypes.c_int),
+    "paged_attn_prefix_workspace_size": ([_P_dims, _i32], _sz),
+    "paged_attn_prefix_workspace_min": ([_P_dims, _i32], _sz),
     "paged_kv_append": ([_c_void_p] * 15 + [_P_append, _c_void_p], ctypes.c_int),
     "paged_kv_copy": ([_c_void_p] * 7 + [_i32, _P_pool, _c_void_p], ctypes.c_int),
     "paged_kv_keep_path": ([_c_void_p] * 7 + [_i32, _i32] + [_c_void_p] * 3 +
@@ -266,6 +270,56 @@ def _opt(t: Optional[torch.Tensor], name: str, dtype=None) -> ctypes.c_void_p:
 def _shape(t: Optional[torch.Tensor], name: str, shape) -> None:
     if t is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def paged_attn_prefix_workspace_size(dims: vas_attn_dims, num_groups: int) -> int:
+    return int(_lib.paged_attn_prefix_workspace_size(ctypes.byref(dims), num_groups))
+
+
+def paged_attn_prefix_workspace_min(dims: vas_attn_dims, num_groups: int) -> int:
+    return int(_lib.paged_attn_prefix_workspace_min(ctypes.byref(dims), num_groups))
+
+
+def alloc_prefix_workspace(dims: vas_attn_dims, num_groups: int, device=None,
+                           nbytes: Optional[int] = None) -> torch.Tensor:
+    n = paged_attn_prefix_workspace_size(dims, num_groups) if nbytes is None else int(nbytes)
+    if n <= 0:
+        raise ValueError("invalid attention dims")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def paged_attn_fwd_prefix(q, k_pages, v_pages, block_table, seq_lens, query_lens, group_start,
+                          prefix_lens, out, lse, workspace, *, k_scale=None, v_scale=None,
+                          quant: Optional[str] = None, tree_mask=None, scale: float = 0.0,
+                          dims: Optional[vas_attn_dims] = None, stream=None) -> None:
+    """Attention of groups of sequences that share a prefix (include/vas.h:
+    paged_attn_fwd_prefix).  group_start [G + 1] and prefix_lens [G] int32; the other
+    arguments are those of paged_attn_fwd, or with quant those of paged_attn_fwd_quant."""
+    if dims is None:
+        dims = attn_dims(q, k_pages, block_table, seq_lens, scale, quant=quant)
+    _same_device(q=q, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
+                 seq_lens=seq_lens, query_lens=query_lens, group_start=group_start,
+                 prefix_lens=prefix_lens, out=out, lse=lse, workspace=workspace,
+                 k_scale=k_scale, v_scale=v_scale, tree_mask=tree_mask)
+    G = int(prefix_lens.shape[0])
+    _shape(group_start, "group_start", (G + 1,))
+    _shape(v_pages, "v_pages", k_pages.shape)
+    _shape(query_lens, "query_lens", seq_lens.shape)
+    _shape(out, "out", q.shape)
+    _shape(lse, "lse", q.shape[:2])
+    if tree_mask is not None and (tree_mask.numel() != q.shape[0] or tree_mask.element_size() != 8):
+        raise ValueError("tree_mask needs one 64-bit word per query token")
+    kv = torch.uint8 if quant is not None else q.dtype
+    st = _lib.paged_attn_fwd_prefix(
+        _dev(q, "q"), _dev(k_pages, "k_pages", kv), _dev(v_pages, "v_pages", kv),
+        _opt(k_scale, "k_scale", torch.float32), _opt(v_scale, "v_scale", torch.float32),
+        _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32),
+        _dev(query_lens, "query_lens", torch.int32), _dev(group_start, "group_start", torch.int32),
+        _dev(prefix_lens, "prefix_lens", torch.int32), _opt(tree_mask, "tree_mask"),
+        _dev(out, "out", q.dtype), _dev(lse, "lse", torch.float32), ctypes.byref(dims), G,
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _stream_ptr(stream))
+    _check("paged_attn_fwd_prefix", st)
 
 
 def _heads(t: torch.Tensor, name: str, T: int, H: int, D: int, dtype):

@@ -1,0 +1,88 @@
+// What the planner of paged attention leaves in the workspace, shared by the attention
+// kernels of paged_attn.cu and the shared-prefix kernel of prefix_attn.cu.
+#pragma once
+
+#include <cuda.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace vas {
+namespace attn {
+
+struct SeqPlan {
+  int32_t qrow0;         // first row of q / out / lse
+  int32_t nsplit;        // KV splits; 0 = nothing to compute (invalid or no query)
+  int32_t partial_base;  // first partial row (nsplit > 1)
+  int32_t len;           // L
+  int32_t qlen;          // ql
+  int32_t flags;         // kSeqInvalid
+  int32_t nrb;           // row blocks
+  int32_t item0;         // first work item (split 0, row block 0)
+};
+
+struct Item {
+  int32_t seq, page_begin, page_end, split_rb;  // split << kRbBits | row block (| kItemPrecise)
+};
+
+struct PlanHeader {
+  int32_t n_items;
+  int32_t work_counter;
+  int32_t chunk_pages;
+  int32_t n_partial_rows;
+  int32_t n_prefix_items;  // shared-prefix calls only
+};
+
+// A group of sequences whose shared pages are computed once (nsplit 0: it is not).  Its
+// rows, of one KV head, are its members' rows one after the other: row r is query token
+// qrow0 + r / G, query head head * G + r % G.
+struct PrefixGroup {
+  int32_t qrow0;      // first query token
+  int32_t rows;       // G * query tokens
+  int32_t leader;     // sequence whose table names the shared pages
+  int32_t pages;      // shared pages
+  int32_t nsplit;     // splits of them
+  int32_t seq0, seq1; // members
+};
+
+// One split of a group's shared pages and one row block of it, for every KV head.
+struct PrefixItem {
+  int32_t group, page_begin, page_end, split_rb;  // split << kPrefixRbBits | row block
+};
+constexpr int kPrefixRbBits = 16;
+constexpr int kPrefixRows = 256;  // rows of a row block
+
+// Partial rows of a sequence: [split][KV head][G * ql], from partial_base on.
+__device__ __forceinline__ size_t partial_index(const SeqPlan& sp, int Hkv, int G, int split,
+                                                int head, int r) {
+  return (size_t)sp.partial_base + ((size_t)split * Hkv + head) * ((size_t)G * sp.qlen) + r;
+}
+
+struct PrefixArgs {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_table;
+  const SeqPlan* seqplan;
+  const int32_t* row0;  // [B + 1] first query token of each sequence
+  const PrefixGroup* groups;
+  const PrefixItem* items;
+  const PlanHeader* header;
+  float* part_o;
+  float* part_lse;
+  int32_t Hq, Hkv, G, maxp, num_pages, P;
+  float scale_log2;  // softmax scale * log2(e)
+  int32_t* err;
+};
+
+// The shared prefixes of a planned call: partial rows of every member (prefix_attn.cu).
+// mk, mv: bf16 pools, boxes of one 64-column half of one page of one KV head; code pools,
+// boxes of one page of one KV head.  Returns a status code; kv_dtype VAS_BF16,
+// VAS_FP8_E4M3 or VAS_INT8.
+int launch_prefix(const CUtensorMap& mk, const CUtensorMap& mv, const PrefixArgs& args,
+                  int head_dim, int kv_dtype, void* stream);
+
+}  // namespace attn
+}  // namespace vas

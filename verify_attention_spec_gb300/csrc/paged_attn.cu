@@ -50,6 +50,7 @@
 #include <type_traits>
 
 #include "../../include/vas.h"
+#include "attn_plan.cuh"
 #include "device_util.cuh"
 #include "vas_internal.h"
 
@@ -101,28 +102,10 @@ constexpr int kOrderBuckets = 64;  // page-count classes of the work order
 constexpr int kWideOrderWeight = 2;  // a wide unit's page counts twice in the work order
 constexpr int kPlanSmemSeqs = 4096;
 constexpr int kSeqInvalid = 1;
-
-struct SeqPlan {
-  int32_t qrow0;         // first row of q / out / lse
-  int32_t nsplit;        // KV splits; 0 = nothing to compute (invalid or no query)
-  int32_t partial_base;  // first partial row (nsplit > 1)
-  int32_t len;           // L
-  int32_t qlen;          // ql
-  int32_t flags;         // kSeqInvalid
-  int32_t nrb;           // row blocks
-  int32_t item0;         // first work item (split 0, row block 0)
-};
-
-struct Item {
-  int32_t seq, page_begin, page_end, split_rb;  // split << kRbBits | row block (| kItemPrecise)
-};
-
-struct PlanHeader {
-  int32_t n_items;
-  int32_t work_counter;
-  int32_t chunk_pages;
-  int32_t n_partial_rows;
-};
+// Shared prefixes (paged_attn_fwd_prefix).
+constexpr int kMinPrefixTokens = 256;  // shorter ones are left to the members
+constexpr int kMinPrefixSplit = 256;   // tokens of a split, at least
+constexpr int kPrefixUnitTokens = 400; // what a unit's fixed costs weigh, in tokens
 
 // What the producer hands the consumers for one unit (u < 0: no more work).
 struct RingEntry {
@@ -134,7 +117,8 @@ struct RingEntry {
 
 struct Layout {
   size_t seqplan, token_seq, items, order, counters, part_lse, part_o, total;
-  int64_t items_cap, partial_cap;
+  size_t row0, shared, groups, pitems;  // shared-prefix calls only
+  int64_t items_cap, partial_cap, pitems_cap;
 };
 
 __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -157,11 +141,21 @@ struct PlanArgs {
   const uint64_t* tree_mask;  // draft-tree masks, or null
   int64_t items_cap, partial_cap;
   int32_t* err;
+  // Shared prefixes: the groups as the caller gives them, and what the plan makes of them.
+  const int32_t* group_start;
+  const int32_t* prefix_lens;
+  int32_t num_groups, sms;
+  int32_t* row0;        // [B + 1] first query token of each sequence
+  int32_t* shared;      // [B] group of a sequence whose prefix is shared, or -1
+  PrefixGroup* groups;  // [num_groups]
+  PrefixItem* pitems;
+  int64_t pitems_cap;
 };
 
 struct SeqShape {
   bool valid;
-  int32_t L, ql, npages, R, nrb;
+  int32_t L, ql, npages, R, nrb;  // npages: the sequence's own, without shared ones
+  int32_t page0, parts;           // first of its own pages; partials of the shared ones
 };
 
 __device__ __forceinline__ SeqShape seq_shape(const PlanArgs& a, int32_t L, int32_t ql) {
@@ -172,6 +166,7 @@ __device__ __forceinline__ SeqShape seq_shape(const PlanArgs& a, int32_t L, int3
   s.npages = s.valid ? (L + a.P - 1) / a.P : 0;
   s.R = s.valid ? a.G * ql : 0;
   s.nrb = (s.R + row_block(s.R) - 1) / row_block(s.R);
+  s.page0 = s.parts = 0;
   return s;
 }
 
@@ -273,6 +268,198 @@ __device__ __forceinline__ bool rb_precise(const PlanArgs& a, const SeqShape& s,
 }
 
 
+// The group of the caller that holds sequence i, or -1.  group_start has been checked.
+__device__ __forceinline__ int32_t group_of(const PlanArgs& a, int32_t i) {
+  int lo = 0, hi = a.num_groups;  // the last start at or below i
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.group_start[mid] <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  return a.group_start[lo] <= i && lo < a.num_groups ? lo : -1;
+}
+
+// Row blocks of a group of R rows per KV head.
+__host__ __device__ __forceinline__ int64_t prefix_blocks(int64_t R) {
+  return (R + kPrefixRows - 1) / kPrefixRows;
+}
+
+// Shared prefixes: which groups are computed once, in how many splits, and their items.
+// The whole block; leaves a.row0, a.shared, a.groups, a.pitems.  Returns whether the
+// groups themselves are consistent; when they or the lengths are not, nothing is shared,
+// and a sequence that its group's prefix_lens does not fit has shared[i] = -2.
+template <typename ShapeFn>
+__device__ bool plan_prefixes(const PlanArgs& a, bool lengths_ok, ShapeFn shape,
+                              int64_t (*red)[4]) {
+  __shared__ int32_t s_bad, s_best;
+  __shared__ float s_time[kPlanThreads / 32];
+  __shared__ int32_t s_splits[kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  for (int g = tid; g <= a.num_groups; g += kPlanThreads) {
+    const int32_t s0 = a.group_start[g];
+    const int32_t s1 = g < a.num_groups ? a.group_start[g + 1] : a.B;
+    if (s0 < 0 || s0 > s1 || s1 > a.B) s_bad = 1;
+    if (g < a.num_groups && a.prefix_lens[g] < 0) s_bad = 1;
+  }
+  __syncthreads();
+  const bool order_ok = s_bad == 0;
+  __syncthreads();
+  // First query token of each sequence; sequences a group's prefix does not fit.
+  int64_t carry[1] = {0};
+  bool misfit = false;
+  for (int base = 0; base < a.B; base += kPlanThreads) {
+    const int i = base + tid;
+    int64_t v[1] = {0}, t[1];
+    if (i < a.B) {
+      const SeqShape s = shape(i);
+      v[0] = s.ql > 0 ? s.ql : 0;
+      int32_t mark = -1;
+      if (order_ok && s.valid && s.ql > 0) {
+        const int32_t g = group_of(a, i);
+        if (g >= 0 && a.prefix_lens[g] > s.L - s.ql) mark = -2;
+      }
+      misfit |= mark == -2;
+      a.shared[i] = mark;
+    }
+    block_scan<1>(v, red, t);
+    const int64_t at = v[0] + carry[0];
+    if (i < a.B) a.row0[i] = (int32_t)(at < a.T ? at : a.T);
+    carry[0] += t[0];
+  }
+  if (tid == 0) a.row0[a.B] = (int32_t)(carry[0] < a.T ? carry[0] : a.T);
+  if (misfit) s_bad = 1;
+  __syncthreads();
+  const bool fine = s_bad == 0;
+  const bool share = fine && lengths_ok;
+  if (tid == 0) a.header->n_prefix_items = 0;
+  if (!share) return fine;
+
+  // The groups worth sharing: their rows, members with query tokens, leader.
+  for (int g = tid; g < a.num_groups; g += kPlanThreads) {
+    PrefixGroup pg;
+    pg.seq0 = a.group_start[g];
+    pg.seq1 = a.group_start[g + 1];
+    pg.qrow0 = a.row0[pg.seq0];
+    pg.rows = (int32_t)((a.row0[pg.seq1] - pg.qrow0) * (int64_t)a.G);
+    pg.pages = a.prefix_lens[g] / a.P;
+    pg.leader = -1;
+    pg.nsplit = 0;
+    if (pg.pages * a.P < kMinPrefixTokens || pg.rows == 0) pg.pages = 0;
+    a.groups[g] = pg;
+  }
+  __syncthreads();
+  // A group's leader is its first member with query tokens; a group whose leader has all
+  // of them is left alone.
+  for (int i = tid; i < a.B; i += kPlanThreads) {
+    if (a.row0[i + 1] == a.row0[i]) continue;
+    const int32_t g = group_of(a, i);
+    if (g < 0 || a.groups[g].pages == 0 || a.row0[i] != a.groups[g].qrow0) continue;
+    a.groups[g].leader = i;
+    if (a.row0[i + 1] == a.row0[a.groups[g].seq1]) a.groups[g].pages = 0;
+  }
+  __syncthreads();
+
+  // Splits: candidate k cuts the longest prefix in ns(k) and every other one in pieces no
+  // longer; each warp weighs every (kPlanThreads / 32)th candidate by
+  // waves of units * (a unit's tokens + its fixed costs), and the cheapest that fits the
+  // item list and the partial rows wins (the fewest splits among equals).
+  int64_t most[2] = {0, 0};  // longest prefix (max through the sum of one writer below)
+  {
+    int32_t m = 0;
+    for (int g = tid; g < a.num_groups; g += kPlanThreads) m = max(m, a.groups[g].pages);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (tid == 0) s_best = 0;
+    __syncthreads();
+    if (lane == 0) atomicMax(&s_best, m);
+    __syncthreads();
+    most[0] = s_best;
+    __syncthreads();
+  }
+  const int64_t longest = most[0];
+  if (longest == 0) return fine;
+  constexpr int kCandidates = 64, kWarps = kPlanThreads / 32;
+  float best_t = INFINITY;
+  int32_t best_c = 0;
+  for (int k = warp; k < kCandidates; k += kWarps) {
+    const int64_t ns = k < 32 ? k + 1 : (int64_t)(32.f * exp2f((k - 31) * 0.125f));
+    const int64_t c = (longest + ns - 1) / ns;
+    if (k > 0 && c * a.P < kMinPrefixSplit) continue;
+    int64_t units = 0, items = 0, parts = 0;
+    for (int g = lane; g < a.num_groups; g += 32) {
+      const PrefixGroup pg = a.groups[g];
+      if (pg.pages == 0) continue;
+      const int64_t n = (pg.pages + c - 1) / c;
+      items += n * prefix_blocks(pg.rows);
+      parts += (n + 1) * a.Hkv * pg.rows;  // and one of the members' own at least
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      items += __shfl_xor_sync(0xffffffffu, items, o);
+      parts += __shfl_xor_sync(0xffffffffu, parts, o);
+    }
+    if (items > a.pitems_cap || parts > a.partial_cap) continue;
+    units = items * a.Hkv;
+    const int64_t waves = (units + a.sms - 1) / a.sms;
+    const float t = (float)waves * (float)(c * a.P + kPrefixUnitTokens);
+    if (t < best_t) {
+      best_t = t;
+      best_c = (int32_t)c;
+    }
+  }
+  if (lane == 0) {
+    s_time[warp] = best_t;
+    s_splits[warp] = best_c;
+  }
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w)
+    if (s_time[w] < best_t || (s_time[w] == best_t && s_splits[w] > best_c)) {
+      best_t = s_time[w];
+      best_c = s_splits[w];
+    }
+  if (best_c == 0) return fine;  // no room for the partials: nothing is shared
+
+  // Items, group by group.
+  int64_t icarry[1] = {0};
+  for (int base = 0; base < a.num_groups; base += kPlanThreads) {
+    const int g = base + tid;
+    int64_t v[1] = {0}, t[1];
+    int32_t n = 0, nrb = 0, each = 0;
+    if (g < a.num_groups && a.groups[g].pages > 0) {
+      const PrefixGroup pg = a.groups[g];
+      n = (pg.pages + best_c - 1) / best_c;
+      each = (pg.pages + n - 1) / n;  // even pieces
+      n = (pg.pages + each - 1) / each;
+      nrb = (int32_t)prefix_blocks(pg.rows);
+      a.groups[g].nsplit = n;
+      v[0] = (int64_t)n * nrb;
+    }
+    block_scan<1>(v, red, t);
+    int64_t at = icarry[0] + v[0];
+    for (int sp = 0; sp < n; ++sp)
+      for (int rb = 0; rb < nrb; ++rb) {
+        PrefixItem it;
+        it.group = g;
+        it.page_begin = sp * each;
+        it.page_end = min((sp + 1) * each, a.groups[g].pages);
+        it.split_rb = (sp << kPrefixRbBits) | rb;
+        a.pitems[at++] = it;
+      }
+    icarry[0] += t[0];
+  }
+  if (tid == 0) a.header->n_prefix_items = (int32_t)icarry[0];
+  for (int i = tid; i < a.B; i += kPlanThreads) {
+    const int32_t g = group_of(a, i);
+    if (g >= 0 && a.groups[g].nsplit > 0) a.shared[i] = g;
+  }
+  __syncthreads();
+  return fine;
+}
+
+// PFX: a call with shared prefixes.
+template <bool PFX>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
   pdl_wait_prior_grid();    // the previous kernel in the stream has released the workspace
   pdl_launch_dependents();  // the attention grid may start its prologue
@@ -286,9 +473,38 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       s_ql[i] = a.query_lens[i];
     }
   __syncthreads();
-  auto shape = [&](int i) {
+  auto whole_shape = [&](int i) {
     return cached ? seq_shape(a, s_L[i], s_ql[i]) : seq_shape(a, a.seq_lens[i], a.query_lens[i]);
   };
+  bool planned = false;  // a.shared and a.groups hold this call's
+  auto shape = [&](int i) {
+    SeqShape s = whole_shape(i);
+    if (PFX && planned) {
+      const int32_t g = a.shared[i];
+      if (g == -2) {  // its group's prefix does not fit it
+        s.valid = false;
+        s.npages = s.R = s.nrb = 0;
+      } else if (g >= 0 && s.R > 0) {
+        s.page0 = a.groups[g].pages;
+        s.npages -= s.page0;
+        s.parts = a.groups[g].nsplit;
+      }
+    }
+    return s;
+  };
+  if constexpr (PFX) {
+    int64_t chk[2] = {0, 0};  // rows, bad
+    for (int i = tid; i < a.B; i += kPlanThreads) {
+      const SeqShape s = shape(i);
+      chk[1] += !s.valid;
+      chk[0] += s.ql > 0 ? s.ql : 0;
+    }
+    block_sum<2>(chk, red);
+    const bool fine = plan_prefixes(a, chk[0] == a.T && chk[1] == 0, whole_shape, red);
+    if (tid == 0 && !fine) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
+    planned = true;
+    __syncthreads();
+  }
 
   // Totals: work in page-row-blocks per KV head, packed query rows, invalid sequences.
   int64_t tot[3] = {0, 0, 0};  // cost, rows, bad
@@ -319,7 +535,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       const SeqShape s = shape(i);
       const int32_t ns = splits_for(s, seq_chunk(a, s, c));
       v[0] += (int64_t)ns * s.nrb;
-      if (ns > 1) v[1] += (int64_t)ns * a.Hkv * s.R;
+      if (ns + s.parts > 1) v[1] += (int64_t)(ns + s.parts) * a.Hkv * s.R;
     }
     block_sum<2>(v, red);
     if ((v[0] <= a.items_cap && v[1] <= a.partial_cap) || c >= INT_MAX / 2) break;
@@ -337,14 +553,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
     const int i = base + tid;
     SeqShape s;
     s.valid = false;
-    s.L = s.ql = s.npages = s.R = s.nrb = 0;
+    s.L = s.ql = s.npages = s.R = s.nrb = s.page0 = s.parts = 0;
     int32_t ns = 0, qrows = 0;
     if (i < a.B) {
       s = shape(i);
       qrows = s.ql > 0 ? s.ql : 0;
       ns = splits_for(s, seq_chunk(a, s, c));
     }
-    int64_t v[3] = {qrows, (int64_t)ns * s.nrb, ns > 1 ? (int64_t)ns * a.Hkv * s.R : 0};
+    const int32_t np = ns + s.parts;  // partials of a row
+    int64_t v[3] = {qrows, (int64_t)ns * s.nrb, np > 1 ? (int64_t)np * a.Hkv * s.R : 0};
     int64_t t[3];
     block_scan<3>(v, red, t);
     const int64_t my_row0 = v[0] + carry[0];
@@ -362,7 +579,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       const int64_t n_my_items = (int64_t)ns * s.nrb;
       const bool fits = my_row0 + qrows <= a.T && my_item0 + n_my_items <= a.items_cap;
       if (!fits) sp.flags |= kSeqInvalid;
-      sp.nsplit = (s.valid && fits) ? ns : 0;
+      sp.nsplit = (s.valid && fits) ? np : 0;
       sp.nrb = s.nrb;
       sp.partial_base = (int32_t)my_part0;
       sp.item0 = (int32_t)(my_item0 < a.items_cap ? my_item0 : 0);
@@ -381,15 +598,18 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
             const bool prec = a.is_bf16 && sp.nsplit > 0 && rb_precise(a, s, my_row0, rb);
             Item item;
             item.seq = sp.nsplit > 0 ? i : -1;
-            item.page_begin = pb;
-            item.page_end = pe;
+            item.page_begin = s.page0 + pb;
+            item.page_end = s.page0 + pe;
             item.split_rb = (sp_i << kRbBits) | rb | (prec ? kItemPrecise : 0);
             a.items[it++] = item;
           }
         }
       }
-      if (sp.nsplit > 1)  // arrival counters of the last-split merge
-        for (int k = 0; k < s.nrb * a.Hkv; ++k) a.counters[(size_t)sp.item0 * a.Hkv + k] = 0;
+      // Arrival counters of the last-split merge; the shared pages' partials are there
+      // before the first of the sequence's own splits starts.
+      if (sp.nsplit > 1)
+        for (int k = 0; k < s.nrb * a.Hkv; ++k)
+          a.counters[(size_t)sp.item0 * a.Hkv + k] = s.parts;
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) carry[k] += t[k];
@@ -955,7 +1175,7 @@ __device__ __forceinline__ size_t out_row(const AttnArgs& a, const SeqPlan& sp, 
 
 __device__ __forceinline__ size_t partial_row(const AttnArgs& a, const SeqPlan& sp, int split,
                                               int head, int r) {
-  return (size_t)sp.partial_base + ((size_t)split * a.Hkv + head) * ((size_t)a.G * sp.qlen) + r;
+  return partial_index(sp, a.Hkv, a.G, split, head, r);
 }
 
 // Merge the partials of every split of rows r0 .. r0+Rb-1 of one KV head (the caller is
@@ -2336,9 +2556,23 @@ int64_t items_min(const vas_attn_dims* d) {
 
 int64_t items_extra(int sms) { return 4LL * kUnitsPerSm * (sms > 0 ? sms : 160); }
 
-Layout make_layout(const vas_attn_dims* d, int64_t items_cap, int64_t partial_cap) {
+// num_groups < 0: no shared prefixes.
+Layout make_layout(const vas_attn_dims* d, int64_t items_cap, int64_t partial_cap,
+                   int32_t num_groups = -1, int64_t pitems_cap = 0) {
   Layout L;
   size_t off = align_up(sizeof(PlanHeader), 256);
+  L.row0 = L.shared = L.groups = L.pitems = 0;
+  L.pitems_cap = pitems_cap;
+  if (num_groups >= 0) {
+    L.row0 = off;
+    off = align_up(off + ((size_t)d->num_seqs + 1) * 4, 256);
+    L.shared = off;
+    off = align_up(off + (size_t)d->num_seqs * 4, 256);
+    L.groups = off;
+    off = align_up(off + (size_t)num_groups * sizeof(PrefixGroup), 256);
+    L.pitems = off;
+    off = align_up(off + (size_t)pitems_cap * sizeof(PrefixItem), 256);
+  }
   L.seqplan = off;
   off = align_up(off + (size_t)d->num_seqs * sizeof(SeqPlan), 256);
   L.token_seq = off;
@@ -2359,19 +2593,27 @@ Layout make_layout(const vas_attn_dims* d, int64_t items_cap, int64_t partial_ca
   return L;
 }
 
+// Items of shared prefixes: every row block once, and what two waves of splits add.
+int64_t pitems_cap(const vas_attn_dims* d, int32_t num_groups, int sms) {
+  if (num_groups < 0) return 0;
+  const int64_t G = d->num_q_heads / d->num_kv_heads;
+  return num_groups + prefix_blocks(G * d->total_q_tokens) + 2LL * (sms > 0 ? sms : 160);
+}
+
 // Largest layout that fits ws_bytes (partial capacity grows with the workspace).
-bool fit_layout(const vas_attn_dims* d, size_t ws_bytes, Layout* out) {
+bool fit_layout(const vas_attn_dims* d, size_t ws_bytes, Layout* out, int32_t num_groups = -1) {
   const int64_t imin = items_min(d);
   const int64_t icap_pref = imin + items_extra(num_sms());
+  const int64_t pcap_items = pitems_cap(d, num_groups, num_sms());
   for (int64_t icap : {icap_pref, imin}) {
-    const Layout base = make_layout(d, icap, 0);
+    const Layout base = make_layout(d, icap, 0, num_groups, pcap_items);
     if (base.total > ws_bytes) continue;
     const size_t per_row = (size_t)(d->head_dim + 1) * 4;
     int64_t pcap = (int64_t)((ws_bytes - base.total) / per_row);
-    while (pcap > 0 && make_layout(d, icap, pcap).total > ws_bytes) pcap -= 64;
+    while (pcap > 0 && make_layout(d, icap, pcap, num_groups, pcap_items).total > ws_bytes) pcap -= 64;
     if (pcap < 0) pcap = 0;
     if (pcap > INT32_MAX) pcap = INT32_MAX;
-    *out = make_layout(d, icap, pcap);
+    *out = make_layout(d, icap, pcap, num_groups, pcap_items);
     return true;
   }
   return false;
@@ -2394,15 +2636,17 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
 // 4-D view of a page pool with the token before the column half:
 // (64, num_pages * P, D/64, Hkv), strides (Hkv*D*2, 128, D*2) bytes, 128-byte swizzle.
 // A box of (64, P, D/64, 1) -- one page of one KV head -- then lands as
-// [half][token][64].
-bool encode_pool_map(CUtensorMap* map, const void* base, const vas_attn_dims* d) {
+// [half][token][64].  With `halves` 1 a box is one half of it.
+bool encode_pool_map(CUtensorMap* map, const void* base, const vas_attn_dims* d,
+                     int halves = 0) {
   auto fn = get_encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[4] = {64, (cuuint64_t)d->num_pages * d->page_size,
                               (cuuint64_t)d->head_dim / 64, (cuuint64_t)d->num_kv_heads};
   const cuuint64_t strides[3] = {(cuuint64_t)d->num_kv_heads * d->head_dim * 2, 128,
                                  (cuuint64_t)d->head_dim * 2};
-  const cuuint32_t box[4] = {64, (cuuint32_t)d->page_size, (cuuint32_t)d->head_dim / 64, 1};
+  const cuuint32_t box[4] = {64, (cuuint32_t)d->page_size,
+                             halves ? (cuuint32_t)halves : (cuuint32_t)d->head_dim / 64, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -2480,15 +2724,43 @@ size_t paged_attn_workspace_size(const vas_attn_dims* dims) {
       .total;
 }
 
+size_t paged_attn_prefix_workspace_min(const vas_attn_dims* dims, int32_t num_groups) {
+  if (!dims_ok(dims) || !dims_supported(dims) || dims->kv_dtype == VAS_F32 || num_groups < 0)
+    return 0;
+  return make_layout(dims, items_min(dims), 0, num_groups,
+                     pitems_cap(dims, num_groups, vas::num_sms()))
+      .total;
+}
+
+size_t paged_attn_prefix_workspace_size(const vas_attn_dims* dims, int32_t num_groups) {
+  if (!dims_ok(dims) || !dims_supported(dims) || dims->kv_dtype == VAS_F32 || num_groups < 0)
+    return 0;
+  // Room for every row to be split 8 ways on average, and for the rows of two waves of
+  // shared-prefix units beside them.
+  const int sms = vas::num_sms();
+  const int64_t pcap = (int64_t)dims->total_q_tokens * dims->num_q_heads * 9 +
+                       2LL * (sms > 0 ? sms : 160) * kPrefixRows;
+  return make_layout(dims, items_min(dims) + items_extra(sms), pcap < INT32_MAX ? pcap : INT32_MAX,
+                     num_groups, pitems_cap(dims, num_groups, sms))
+      .total;
+}
+
 }  // extern "C"
 
 namespace {
+
+// The groups of a paged_attn_fwd_prefix call.
+struct PrefixCall {
+  const int32_t* group_start;
+  const int32_t* prefix_lens;
+  int32_t num_groups;
+};
 
 int attn_launch(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
                 const float* v_scale, const int32_t* block_table, const int32_t* seq_lens,
                 const int32_t* query_lens, const uint64_t* tree_mask, void* out, float* lse,
                 const vas_attn_dims* dims, void* workspace, size_t workspace_bytes,
-                vas_stream_t stream_) {
+                vas_stream_t stream_, const PrefixCall* prefix = nullptr) {
   if (!dims_ok(dims)) return VAS_E_INVALID_ARG;
   if (!dims_supported(dims)) return VAS_E_UNSUPPORTED;
   const vas_attn_dims& d = *dims;
@@ -2508,7 +2780,8 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
   if ((int64_t)d.num_pages * d.page_size > INT32_MAX) return VAS_E_INVALID_ARG;
 
   Layout lay;
-  if (!fit_layout(dims, workspace_bytes, &lay)) return VAS_E_WORKSPACE;
+  if (!fit_layout(dims, workspace_bytes, &lay, prefix ? prefix->num_groups : -1))
+    return VAS_E_WORKSPACE;
   int32_t* err = vas::device_error_word();
   const int sms = vas::num_sms();
   if (!err || !sms) return VAS_E_CUDA;
@@ -2547,6 +2820,15 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
   pa.items_cap = lay.items_cap;
   pa.partial_cap = lay.partial_cap;
   pa.err = err;
+  pa.group_start = prefix ? prefix->group_start : nullptr;
+  pa.prefix_lens = prefix ? prefix->prefix_lens : nullptr;
+  pa.num_groups = prefix ? prefix->num_groups : 0;
+  pa.sms = sms;
+  pa.row0 = reinterpret_cast<int32_t*>(ws + lay.row0);
+  pa.shared = reinterpret_cast<int32_t*>(ws + lay.shared);
+  pa.groups = reinterpret_cast<PrefixGroup*>(ws + lay.groups);
+  pa.pitems = reinterpret_cast<PrefixItem*>(ws + lay.pitems);
+  pa.pitems_cap = lay.pitems_cap;
   // Tensor maps first, so that the plan and the attention grid are launched back to back.
   CUtensorMap mk, mv;
   if (quant && (!encode_code_map(&mk, k_pages, dims) || !encode_code_map(&mv, v_pages, dims)))
@@ -2564,7 +2846,9 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, plan_kernel, pa) != cudaSuccess) {
+    const cudaError_t st = prefix ? cudaLaunchKernelEx(&cfg, plan_kernel<true>, pa)
+                                  : cudaLaunchKernelEx(&cfg, plan_kernel<false>, pa);
+    if (st != cudaSuccess) {
       cudaGetLastError();
       return VAS_E_CUDA;
     }
@@ -2598,6 +2882,36 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
   aa.tree_mask = tree_mask;
   aa.k_scale = k_scale;
   aa.v_scale = v_scale;
+
+  if (prefix) {
+    PrefixArgs px;
+    px.q = q;
+    px.k_pages = k_pages;
+    px.v_pages = v_pages;
+    px.k_scale = k_scale;
+    px.v_scale = v_scale;
+    px.block_table = block_table;
+    px.seqplan = pa.seqplan;
+    px.row0 = pa.row0;
+    px.groups = pa.groups;
+    px.items = pa.pitems;
+    px.header = pa.header;
+    px.part_o = aa.part_o;
+    px.part_lse = aa.part_lse;
+    px.Hq = d.num_q_heads;
+    px.Hkv = d.num_kv_heads;
+    px.G = G;
+    px.maxp = d.max_pages_per_seq;
+    px.num_pages = d.num_pages;
+    px.P = d.page_size;
+    px.scale_log2 = aa.scale_log2;
+    px.err = err;
+    CUtensorMap pk = mk, pv = mv;
+    if (!quant && (!encode_pool_map(&pk, k_pages, dims, 1) || !encode_pool_map(&pv, v_pages, dims, 1)))
+      return VAS_E_CUDA;
+    const int st = launch_prefix(pk, pv, px, d.head_dim, d.kv_dtype, stream);
+    if (st != VAS_OK) return st;
+  }
 
   if (quant) {
     const int grid = sms;
@@ -2660,6 +2974,24 @@ int paged_attn_fwd_quant(const void* q, const void* k_pages, const void* v_pages
   if (!dims || !kv_quantized(dims) || !k_scale || !v_scale) return VAS_E_INVALID_ARG;
   return attn_launch(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, query_lens,
                      tree_mask, out, lse, dims, workspace, workspace_bytes, stream);
+}
+
+int paged_attn_fwd_prefix(const void* q, const void* k_pages, const void* v_pages,
+                          const float* k_scale, const float* v_scale,
+                          const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* query_lens, const int32_t* group_start,
+                          const int32_t* prefix_lens, const uint64_t* tree_mask, void* out,
+                          float* lse, const vas_attn_dims* dims, int32_t num_groups,
+                          void* workspace, size_t workspace_bytes, vas_stream_t stream) {
+  if (!dims || num_groups < 0) return VAS_E_INVALID_ARG;
+  if (dims->kv_dtype == VAS_F32) return VAS_E_UNSUPPORTED;
+  if (num_groups > 0 && (!group_start || !prefix_lens)) return VAS_E_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(group_start) | reinterpret_cast<uintptr_t>(prefix_lens)) & 3)
+    return VAS_E_INVALID_ARG;
+  const PrefixCall px{group_start, prefix_lens, num_groups};
+  return attn_launch(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, query_lens,
+                     tree_mask, out, lse, dims, workspace, workspace_bytes, stream,
+                     num_groups > 0 ? &px : nullptr);
 }
 
 }  // extern "C"
