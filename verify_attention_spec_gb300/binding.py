@@ -251,25 +251,28 @@ def paged_attn_fwd_quant(q, k_pages, v_pages, k_scale, v_scale, block_table, seq
     _check("paged_attn_fwd_quant", st)
 
 
-def _same_device(**tensors) -> None:
-    """The calls run on the current device: every tensor has to be there."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
+def _here(dev: int, t: Optional[torch.Tensor], name: str, shape=None, dtype=None):
+    """The address of a contiguous tensor on device `dev` (None: a null pointer)."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {t.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
-
-
-def _opt(t: Optional[torch.Tensor], name: str, dtype=None) -> ctypes.c_void_p:
-    return ctypes.c_void_p(0) if t is None else _dev(t, name, dtype)
-
-
-def _shape(t: Optional[torch.Tensor], name: str, shape) -> None:
-    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _stream_address(dev: int, stream: Optional[torch.cuda.Stream]) -> int:
+    """The cudaStream_t of `stream`, or of the current stream of device `dev`."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    return stream.cuda_stream
 
 
 def paged_attn_prefix_workspace_size(dims: vas_attn_dims, num_groups: int) -> int:
@@ -297,39 +300,41 @@ def paged_attn_fwd_prefix(q, k_pages, v_pages, block_table, seq_lens, query_lens
     arguments are those of paged_attn_fwd, or with quant those of paged_attn_fwd_quant."""
     if dims is None:
         dims = attn_dims(q, k_pages, block_table, seq_lens, scale, quant=quant)
-    _same_device(q=q, k_pages=k_pages, v_pages=v_pages, block_table=block_table,
-                 seq_lens=seq_lens, query_lens=query_lens, group_start=group_start,
-                 prefix_lens=prefix_lens, out=out, lse=lse, workspace=workspace,
-                 k_scale=k_scale, v_scale=v_scale, tree_mask=tree_mask)
-    G = int(prefix_lens.shape[0])
-    _shape(group_start, "group_start", (G + 1,))
-    _shape(v_pages, "v_pages", k_pages.shape)
-    _shape(query_lens, "query_lens", seq_lens.shape)
-    _shape(out, "out", q.shape)
-    _shape(lse, "lse", q.shape[:2])
+    dev = torch.cuda.current_device()
+    i32, f32 = torch.int32, torch.float32
+    G = prefix_lens.shape[0]
+    n, P, Hkv, _ = pool = k_pages.shape
     if tree_mask is not None and (tree_mask.numel() != q.shape[0] or tree_mask.element_size() != 8):
         raise ValueError("tree_mask needs one 64-bit word per query token")
     kv = torch.uint8 if quant is not None else q.dtype
+    B = seq_lens.shape
     st = _lib.paged_attn_fwd_prefix(
-        _dev(q, "q"), _dev(k_pages, "k_pages", kv), _dev(v_pages, "v_pages", kv),
-        _opt(k_scale, "k_scale", torch.float32), _opt(v_scale, "v_scale", torch.float32),
-        _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32),
-        _dev(query_lens, "query_lens", torch.int32), _dev(group_start, "group_start", torch.int32),
-        _dev(prefix_lens, "prefix_lens", torch.int32), _opt(tree_mask, "tree_mask"),
-        _dev(out, "out", q.dtype), _dev(lse, "lse", torch.float32), ctypes.byref(dims), G,
-        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-        _stream_ptr(stream))
+        _here(dev, q, "q"), _here(dev, k_pages, "k_pages", None, kv),
+        _here(dev, v_pages, "v_pages", pool, kv), _here(dev, k_scale, "k_scale", (n, Hkv, P), f32),
+        _here(dev, v_scale, "v_scale", (n, Hkv, P), f32),
+        _here(dev, block_table, "block_table", (*B, block_table.shape[-1]), i32),
+        _here(dev, seq_lens, "seq_lens", None, i32), _here(dev, query_lens, "query_lens", B, i32),
+        _here(dev, group_start, "group_start", (G + 1,), i32),
+        _here(dev, prefix_lens, "prefix_lens", (G,), i32), _here(dev, tree_mask, "tree_mask"),
+        _here(dev, out, "out", q.shape, q.dtype), _here(dev, lse, "lse", q.shape[:2], f32),
+        ctypes.byref(dims), G, _here(dev, workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream_address(dev, stream))
     _check("paged_attn_fwd_prefix", st)
 
 
-def _heads(t: torch.Tensor, name: str, T: int, H: int, D: int, dtype):
-    """Pointer and token stride of a [T, H, D] tensor whose heads are contiguous."""
-    _shape(t, name, (T, H, D))
-    if t.dtype != dtype:
+def _heads(dev: int, t: torch.Tensor, name: str, shape, dtype):
+    """Address and token stride of a [T, H, D] tensor whose heads are contiguous."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device, cuda:{dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if T * H > 0 and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+    T, H, D = shape
+    s = t.stride()
+    if T * H > 0 and (s[2] != 1 or (H > 1 and s[1] != D)):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if T > 1 else H * D)
+    return t.data_ptr(), (s[0] if T > 1 else H * D)
 
 
 def paged_kv_append(q, k, v, block_table, seq_lens, query_lens, q_out, k_pages, v_pages, *,
@@ -341,73 +346,77 @@ def paged_kv_append(q, k, v, block_table, seq_lens, query_lens, q_out, k_pages, 
     cos_sin [max_position, rotary_dim] fp32 or None, positions [T] int32 or None; q and
     q_out may both be None.  k_pages / v_pages [num_pages, P, Hkv, D], with quant uint8
     codes and k_scale / v_scale [num_pages, Hkv, P]."""
-    _same_device(q=q, k=k, v=v, block_table=block_table, seq_lens=seq_lens, query_lens=query_lens,
-                 q_out=q_out, k_pages=k_pages, v_pages=v_pages, cos_sin=cos_sin,
-                 positions=positions, q_weight=q_weight, k_weight=k_weight, k_scale=k_scale,
-                 v_scale=v_scale)
-    num_pages, P, Hkv, D = k_pages.shape
-    T, B = int(k.shape[0]), int(seq_lens.shape[0])
+    dev = torch.cuda.current_device()
+    i32, f32 = torch.int32, torch.float32
+    num_pages, P, Hkv, D = pool = k_pages.shape
+    T, B, act = k.shape[0], seq_lens.shape[0], k.dtype
     if quant is not None:
-        if quant not in _QUANT_CODES or k.dtype != torch.bfloat16 or k_pages.dtype != torch.uint8:
+        if quant not in _QUANT_CODES or act != torch.bfloat16 or k_pages.dtype != torch.uint8:
             raise ValueError("a quantised pool is uint8 codes with bf16 q, k and v")
         code = _QUANT_CODES[quant]
     else:
-        if k.dtype not in _KV_CODES or k_pages.dtype != k.dtype:
+        if act not in _KV_CODES or k_pages.dtype != act:
             raise ValueError("k and k_pages must share a dtype in {bf16, fp32}")
-        code = _KV_CODES[k.dtype]
+        code = _KV_CODES[act]
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out come together")
-    Hq = 0 if q is None else int(q.shape[1])
-    kp, ks = _heads(k, "k", T, Hkv, D, k.dtype)
-    vp, vs = _heads(v, "v", T, Hkv, D, k.dtype)
-    qp, qs = _heads(q, "q", T, Hq, D, k.dtype) if Hq else (ctypes.c_void_p(0), 0)
-    _shape(q_out, "q_out", (T, Hq, D))
-    _shape(v_pages, "v_pages", k_pages.shape)
-    _shape(query_lens, "query_lens", (B,))
-    _shape(block_table, "block_table", (B, block_table.shape[-1]))
-    _shape(positions, "positions", (T,))
-    _shape(q_weight, "q_weight", (D,))
-    _shape(k_weight, "k_weight", (D,))
-    _shape(k_scale, "k_scale", (num_pages, Hkv, P))
-    _shape(v_scale, "v_scale", (num_pages, Hkv, P))
+    Hq = 0 if q is None else q.shape[1]
+    kp, ks = _heads(dev, k, "k", (T, Hkv, D), act)
+    vp, vs = _heads(dev, v, "v", (T, Hkv, D), act)
+    qp, qs = _heads(dev, q, "q", (T, Hq, D), act) if Hq else (None, 0)
     if cos_sin is not None and cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_position, rotary_dim]")
-    dims = vas_append_dims(num_seqs=B, total_tokens=T, num_q_heads=Hq, num_kv_heads=int(Hkv),
-                           head_dim=int(D), page_size=int(P), num_pages=int(num_pages),
-                           max_pages_per_seq=int(block_table.shape[1]), kv_dtype=code,
-                           rotary_dim=0 if cos_sin is None else int(cos_sin.shape[1]),
-                           interleaved=int(interleaved),
-                           max_position=0 if cos_sin is None else int(cos_sin.shape[0]),
-                           q_stride=qs, k_stride=ks, v_stride=vs, eps=float(eps))
+    table = (0, 0) if cos_sin is None else cos_sin.shape
+    maxp = block_table.shape[-1]
+    dims = vas_append_dims(B, T, Hq, Hkv, D, P, num_pages, maxp, code, table[1], int(interleaved),
+                           table[0], qs, ks, vs, eps)
     st = _lib.paged_kv_append(
-        qp, kp, vp, _opt(q_weight, "q_weight", k.dtype), _opt(k_weight, "k_weight", k.dtype),
-        _opt(cos_sin, "cos_sin", torch.float32), _opt(positions, "positions", torch.int32),
-        _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32),
-        _dev(query_lens, "query_lens", torch.int32), _opt(q_out, "q_out", k.dtype),
-        _dev(k_pages, "k_pages"), _dev(v_pages, "v_pages", k_pages.dtype),
-        _opt(k_scale, "k_scale", torch.float32), _opt(v_scale, "v_scale", torch.float32),
-        ctypes.byref(dims), _stream_ptr(stream))
+        qp, kp, vp, _here(dev, q_weight, "q_weight", (D,), act),
+        _here(dev, k_weight, "k_weight", (D,), act), _here(dev, cos_sin, "cos_sin", None, f32),
+        _here(dev, positions, "positions", (T,), i32),
+        _here(dev, block_table, "block_table", (B, maxp), i32),
+        _here(dev, seq_lens, "seq_lens", None, i32), _here(dev, query_lens, "query_lens", (B,), i32),
+        _here(dev, q_out, "q_out", (T, Hq, D), act), _here(dev, k_pages, "k_pages"),
+        _here(dev, v_pages, "v_pages", pool, k_pages.dtype),
+        _here(dev, k_scale, "k_scale", (num_pages, Hkv, P), f32),
+        _here(dev, v_scale, "v_scale", (num_pages, Hkv, P), f32), ctypes.byref(dims),
+        _stream_address(dev, stream))
     _check("paged_kv_append", st)
 
 
-def _pool_dims(k_pages, v_pages, k_scale, v_scale) -> vas_pool_dims:
-    """vas_pool_dims of [num_pages, P, Hkv, D] pools, or [layers, num_pages, P, Hkv, D]."""
-    if k_pages.dim() not in (4, 5):
+def _pool(dev: int, k_pages, v_pages, k_scale, v_scale):
+    """Addresses and vas_pool_dims of [num_pages, P, Hkv, D] pools, or [layers, num_pages, P,
+    Hkv, D]."""
+    shape = k_pages.shape
+    if len(shape) not in (4, 5):
         raise ValueError("a pool is [num_pages, P, Hkv, D], or that for each layer")
-    _shape(v_pages, "v_pages", k_pages.shape)
-    *lead, n, P, Hkv, D = k_pages.shape
     if (k_scale is None) != (v_scale is None):
         raise ValueError("k_scale and v_scale come together")
-    _shape(k_scale, "k_scale", (*lead, n, Hkv, P))
-    _shape(v_scale, "v_scale", (*lead, n, Hkv, P))
+    *lead, n, P, Hkv, D = shape
     if k_pages.dtype == torch.uint8:
         code = VAS_FP8_E4M3  # either kind of code: they are moved as bytes
     elif k_pages.dtype in _KV_CODES:
         code = _KV_CODES[k_pages.dtype]
     else:
         raise ValueError("k_pages must be bf16, fp32 or uint8 codes")
-    return vas_pool_dims(num_layers=int(lead[0]) if lead else 1, num_pages=int(n), page_size=int(P),
-                         num_kv_heads=int(Hkv), head_dim=int(D), kv_dtype=code)
+    scales = (*lead, n, Hkv, P)
+    return (_here(dev, k_pages, "k_pages"), _here(dev, v_pages, "v_pages", shape, k_pages.dtype),
+            _here(dev, k_scale, "k_scale", scales, torch.float32),
+            _here(dev, v_scale, "v_scale", scales, torch.float32),
+            vas_pool_dims(lead[0] if lead else 1, n, P, Hkv, D, code))
+
+
+def _host_list(x, name: str):
+    """A host list of page numbers or token counts as int32 (kept alive by the caller)."""
+    import numpy as np
+    a = np.asarray(x)
+    if a.ndim != 1 or (a.size and a.dtype.kind not in "iu"):
+        raise ValueError(f"{name} must be a list of integers")
+    if a.dtype != np.int32:
+        if a.size and (a.min() < 0 or a.max() > 2**31 - 1):
+            raise ValueError(f"{name} is outside the range of page numbers")
+        a = a.astype(np.int32)
+    return np.ascontiguousarray(a)
 
 
 def paged_kv_copy(k_pages, v_pages, src, dst, *, tokens=None, k_scale=None, v_scale=None,
@@ -415,27 +424,15 @@ def paged_kv_copy(k_pages, v_pages, src, dst, *, tokens=None, k_scale=None, v_sc
     """Copy pages src[i] -> dst[i] of K and V (include/vas.h: paged_kv_copy).  src, dst and
     tokens are host sequences of integers; pools as in paged_kv_append, or with a leading
     layer dimension."""
-    import numpy as np
-    _same_device(k_pages=k_pages, v_pages=v_pages, k_scale=k_scale, v_scale=v_scale)
-    dims = _pool_dims(k_pages, v_pages, k_scale, v_scale)
-
-    def host(x, name):
-        wide = np.ascontiguousarray(x)
-        if wide.size and wide.dtype.kind not in "iu":
-            raise ValueError(f"{name} must hold integers")
-        if wide.ndim != 1 or (wide.size and (wide.min() < 0 or wide.max() > 2**31 - 1)):
-            raise ValueError(f"{name} must be a list of page numbers")
-        return np.ascontiguousarray(wide, dtype=np.int32)
-
-    s, d = host(src, "src"), host(dst, "dst")
-    t = None if tokens is None else host(tokens, "tokens")
+    dev = torch.cuda.current_device()
+    kp, vp, ks, vs, dims = _pool(dev, k_pages, v_pages, k_scale, v_scale)
+    s, d = _host_list(src, "src"), _host_list(dst, "dst")
+    t = None if tokens is None else _host_list(tokens, "tokens")
     if len(s) != len(d) or (t is not None and len(t) != len(s)):
         raise ValueError("src, dst and tokens differ in length")
-    ptr = lambda a: ctypes.c_void_p(0) if a is None else a.ctypes.data_as(_c_void_p)
-    st = _lib.paged_kv_copy(_dev(k_pages, "k_pages"), _dev(v_pages, "v_pages", k_pages.dtype),
-                            _opt(k_scale, "k_scale", torch.float32),
-                            _opt(v_scale, "v_scale", torch.float32), ptr(s), ptr(d), ptr(t),
-                            len(s), ctypes.byref(dims), _stream_ptr(stream))
+    st = _lib.paged_kv_copy(kp, vp, ks, vs, s.ctypes.data, d.ctypes.data,
+                            None if t is None else t.ctypes.data, len(s), ctypes.byref(dims),
+                            _stream_address(dev, stream))
     _check("paged_kv_copy", st)
 
 
@@ -445,24 +442,17 @@ def paged_kv_keep_path(k_pages, v_pages, block_table, seq_lens, query_lens, path
     paged_kv_keep_path).  path [B, n] and accepted_len [B] int32 as spec_verify_tree writes
     them; seq_index [B] int32 gives the batch row of each (default: row b); pools as in
     paged_kv_copy."""
-    _same_device(k_pages=k_pages, v_pages=v_pages, block_table=block_table, seq_lens=seq_lens,
-                 query_lens=query_lens, path=path, accepted_len=accepted_len, seq_index=seq_index,
-                 k_scale=k_scale, v_scale=v_scale)
-    dims = _pool_dims(k_pages, v_pages, k_scale, v_scale)
+    dev = torch.cuda.current_device()
+    i32 = torch.int32
+    kp, vp, ks, vs, dims = _pool(dev, k_pages, v_pages, k_scale, v_scale)
     B, n = path.shape
-    N = int(seq_lens.shape[0])
-    _shape(accepted_len, "accepted_len", (B,))
-    _shape(seq_index, "seq_index", (B,))
-    _shape(query_lens, "query_lens", (N,))
-    _shape(block_table, "block_table", (N, block_table.shape[-1]))
+    N, maxp = seq_lens.shape[0], block_table.shape[-1]
     st = _lib.paged_kv_keep_path(
-        _dev(k_pages, "k_pages"), _dev(v_pages, "v_pages", k_pages.dtype),
-        _opt(k_scale, "k_scale", torch.float32), _opt(v_scale, "v_scale", torch.float32),
-        _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32),
-        _dev(query_lens, "query_lens", torch.int32), N, int(block_table.shape[1]),
-        _opt(seq_index, "seq_index", torch.int32), _dev(path, "path", torch.int32),
-        _dev(accepted_len, "accepted_len", torch.int32), B, n, ctypes.byref(dims),
-        _stream_ptr(stream))
+        kp, vp, ks, vs, _here(dev, block_table, "block_table", (N, maxp), i32),
+        _here(dev, seq_lens, "seq_lens", None, i32), _here(dev, query_lens, "query_lens", (N,), i32),
+        N, maxp, _here(dev, seq_index, "seq_index", (B,), i32), _here(dev, path, "path", None, i32),
+        _here(dev, accepted_len, "accepted_len", (B,), i32), B, n, ctypes.byref(dims),
+        _stream_address(dev, stream))
     _check("paged_kv_keep_path", st)
 
 

@@ -30,6 +30,7 @@ namespace cache {
 // (a 16-term sum and 16 rotations a lane) hides behind the loads.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kAppendBlocks = 2;  // of an SM
 
 struct AppendArgs {
   const void* q;
@@ -49,59 +50,116 @@ struct AppendArgs {
   float* v_scale;
   int64_t q_stride, k_stride, v_stride;
   int32_t B, T, Hq, Hkv, P, num_pages, maxp, rot, max_position;
-  int32_t groups;      // work items of one token (each kRows * heads_per_task heads)
+  int32_t log2P;
+  int32_t parts, iters;  // a token is `parts` tasks of `iters` groups of rows
   float eps;
   int32_t* err;
 };
 
-// 8 elements as fp32.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  x[0] = bf16_lo_f32(u.x);
-  x[1] = bf16_hi_f32(u.x);
-  x[2] = bf16_lo_f32(u.y);
-  x[3] = bf16_hi_f32(u.y);
-  x[4] = bf16_lo_f32(u.z);
-  x[5] = bf16_hi_f32(u.z);
-  x[6] = bf16_lo_f32(u.w);
-  x[7] = bf16_hi_f32(u.w);
+// Eight fp32 values as four pairs, the operands of the packed instructions.
+struct F8 {
+  uint64_t p[4];
+};
+
+__device__ __forceinline__ F8 load_f8(const float* p) {
+  const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(p);
+  const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(p + 4);
+  return {{u.x, u.y, w.x, w.y}};
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 u = *reinterpret_cast<const float4*>(p);
-  const float4 w = *reinterpret_cast<const float4*>(p + 4);
-  x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
-  x[4] = w.x, x[5] = w.y, x[6] = w.z, x[7] = w.w;
+
+// 16 (bf16) or 32 (fp32) raw bytes of each of a lane's two chunks: what waits in registers
+// between the load and its use.
+template <typename T>
+struct Raw {
+  uint4 a[sizeof(T) / 2], b[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, int ca, int cb) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      a[i] = __ldcs(reinterpret_cast<const uint4*>(p + ca) + i);
+      b[i] = __ldcs(reinterpret_cast<const uint4*>(p + cb) + i);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) a[i] = b[i] = make_uint4(0, 0, 0, 0);
+  }
+};
+__device__ __forceinline__ F8 widen(const uint4 (&u)[1]) {
+  return {{pair(bf16_lo_f32(u[0].x), bf16_hi_f32(u[0].x)), pair(bf16_lo_f32(u[0].y), bf16_hi_f32(u[0].y)),
+           pair(bf16_lo_f32(u[0].z), bf16_hi_f32(u[0].z)), pair(bf16_lo_f32(u[0].w), bf16_hi_f32(u[0].w))}};
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                            pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ F8 widen(const uint4 (&u)[2]) {
+  auto f = [](uint32_t x, uint32_t y) { return pair(__uint_as_float(x), __uint_as_float(y)); };
+  return {{f(u[0].x, u[0].y), f(u[0].z, u[0].w), f(u[1].x, u[1].y), f(u[1].z, u[1].w)}};
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ F8 load_weights(const __nv_bfloat16* p) {
+  const uint4 u[1] = {*reinterpret_cast<const uint4*>(p)};
+  return widen(u);
+}
+__device__ __forceinline__ F8 load_weights(const float* p) { return load_f8(p); }
+
+__device__ __forceinline__ uint32_t bf16_pair(uint64_t v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const F8& x) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(bf16_pair(x.p[0]), bf16_pair(x.p[1]), bf16_pair(x.p[2]), bf16_pair(x.p[3]));
+}
+__device__ __forceinline__ void store8(float* p, const F8& x) {
+  *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x.p[0], x.p[1]);
+  *reinterpret_cast<ulonglong2*>(p + 4) = make_ulonglong2(x.p[2], x.p[3]);
+}
+
+// x / scale, rounded to nearest.  With the correctly rounded reciprocal r = 1 / scale, one
+// correction of x r by its exact remainder gives the correctly rounded quotient (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", IBM J. Res.
+// Dev. 34, 1990), three packed instructions for two elements; scales near the ends of the
+// range, where r or the remainder could leave it, and the not finite ones divide.
+__device__ __forceinline__ F8 quotients(const F8& x, float scale) {
+  F8 y;
+  if (scale > 0x1p-80f && scale < 0x1p80f) {
+    const float r = __frcp_rn(scale);
+    const uint64_t r2 = pair(r, r), ns2 = pair(-scale, -scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t q = mul2(x.p[i], r2);
+      y.p[i] = fma2(fma2(q, ns2, x.p[i]), r2, q);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      unpair(x.p[i], lo, hi);
+      y.p[i] = pair(__fdiv_rn(lo, scale), __fdiv_rn(hi, scale));
+    }
+  }
+  return y;
 }
 
 // 8 values as codes: E4M3 (round to nearest even, saturating; NaN stays NaN) or INT8.
 template <int KV>
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
-  float y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], scale);
+__device__ __forceinline__ uint2 codes8(const F8& x, float scale) {
+  const F8 q = quotients(x, scale);
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    float y[4];
+    unpair(q.p[2 * h], y[0], y[1]);
+    unpair(q.p[2 * h + 1], y[2], y[3]);
     if constexpr (KV == VAS_FP8_E4M3) {
       asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
           "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
           : "=r"(w[h])
-          : "f"(y[4 * h]), "f"(y[4 * h + 1]), "f"(y[4 * h + 2]), "f"(y[4 * h + 3]));
+          : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
     } else {
       w[h] = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         // |y| <= 127 (1 + 2^-23), or NaN, which converts to 0 under a scale that is not
         // finite.
-        const int c = max(-127, min(127, __float2int_rn(y[4 * h + i])));
+        const int c = max(-127, min(127, __float2int_rn(y[i])));
         w[h] |= (uint32_t)(c & 0xff) << (8 * i);
       }
     }
@@ -115,66 +173,96 @@ struct Place {
   int32_t err;  // device error bits; the token is not stored and its q_out row is NaN
 };
 
-// Exclusive prefix sums of max(query_lens, 0) at kAppendThreads evenly spaced sequences,
-// and whether all lengths are consistent.  sums[i] is the first packed row of sequence
-// i * step; sums[kAppendThreads] the total.
-__device__ __forceinline__ void scan_lengths(const AppendArgs& a, int64_t* sums, int32_t step) {
-  __shared__ int64_t wsum[kAppendWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t mine = 0;
-  for (int i = tid * step; i < min(a.B, (tid + 1) * step); ++i) {
-    const int32_t ql = a.query_lens[i];
-    mine += ql > 0 ? ql : 0;
-  }
-  int64_t inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t n = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += n;
-  }
-  if (lane == 31) wsum[warp] = inc;
-  __syncthreads();
-  int64_t base = 0;
-#pragma unroll
-  for (int w = 0; w < kAppendWarps; ++w)
-    if (w < warp) base += wsum[w];
-  sums[tid] = base + inc - mine;
-  if (tid == kAppendThreads - 1) sums[kAppendThreads] = base + inc;
-  __syncthreads();
-}
+// The packing of a call, in shared memory: the first row of every `step`th sequence, and
+// with step 1 (up to kAppendSeqs sequences) their lengths too.
+constexpr int kAppendSeqs = 1024;
+struct Packing {
+  int32_t row0[kAppendSeqs + 1];  // clamped to INT_MAX; the last one is the total
+  int32_t len[kAppendSeqs];
+  int64_t wsum[kAppendWarps];
+};
 
 __device__ __forceinline__ bool lengths_ok(const AppendArgs& a, int32_t L, int32_t ql) {
   return ql >= 0 && ql <= a.T && L >= ql && (int64_t)L <= (int64_t)a.maxp * a.P;
 }
 
-__device__ __forceinline__ Place place_of(const AppendArgs& a, const int64_t* sums, int32_t step,
-                                          int32_t t) {
+__device__ __forceinline__ void scan_lengths(const AppendArgs& a, Packing& pk, int32_t step) {
+  constexpr int kPer = kAppendSeqs / kAppendThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t mine[kPer], sum = 0;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int c = tid * kPer + e;
+    mine[e] = 0;
+    if (step == 1) {
+      if (c < a.B) {
+        mine[e] = max(a.query_lens[c], 0);
+        pk.len[c] = a.seq_lens[c];
+      }
+    } else {
+      for (int64_t i = (int64_t)c * step; i < a.B && i < ((int64_t)c + 1) * step; ++i)
+        mine[e] += max(a.query_lens[i], 0);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int64_t n = mine[e];
+    mine[e] = sum;
+    sum += n;
+  }
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t n = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += n;
+  }
+  if (lane == 31) pk.wsum[warp] = inc;
+  __syncthreads();
+  int64_t base = inc - sum;
+#pragma unroll
+  for (int w = 0; w < kAppendWarps; ++w)
+    if (w < warp) base += pk.wsum[w];
+  auto clamp = [](int64_t x) { return (int32_t)(x < INT_MAX ? x : INT_MAX); };
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) pk.row0[tid * kPer + e] = clamp(base + mine[e]);
+  if (tid == kAppendThreads - 1) pk.row0[kAppendSeqs] = clamp(base + sum);
+  __syncthreads();
+}
+
+// The whole warp: the place of packed row t.  The last start at or below t is found in two
+// rounds of 32 (sequences without tokens share their successor's start, so the last of
+// equal starts is the one that has tokens).
+__device__ __forceinline__ Place place_of(const AppendArgs& a, const Packing& pk, int32_t step,
+                                          int32_t t, int lane) {
   Place p{0, 0, 0, 0};
-  if (t >= sums[kAppendThreads]) {
+  if (t >= pk.row0[kAppendSeqs]) {
     p.err = VAS_DEV_BAD_LENGTHS;  // a row that no sequence owns
     return p;
   }
-  int lo = 0, hi = kAppendThreads - 1;  // the last thread's start at or below t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (sums[mid] <= t) lo = mid;
-    else hi = mid - 1;
+  constexpr int kBlock = kAppendSeqs / 32;
+  const int hi = __popc(__ballot_sync(0xffffffffu, pk.row0[lane * kBlock] <= t)) - 1;
+  static_assert(kBlock == 32, "one start a lane in the second round");
+  const int lo = __popc(__ballot_sync(0xffffffffu, pk.row0[hi * kBlock + lane] <= t)) - 1;
+  const int c = hi * kBlock + lo;
+  int64_t row = pk.row0[c];
+  int32_t i = c, ql, L;
+  if (step == 1) {
+    // A negative length counts as none, so a sequence found here has its true one.
+    ql = pk.row0[c + 1] - pk.row0[c];
+    L = pk.len[c];
+  } else {
+    for (i = c * step; i < a.B; ++i) {
+      ql = a.query_lens[i];
+      const int64_t n = ql > 0 ? ql : 0;
+      if (t < row + n) break;
+      row += n;
+    }
+    if (i >= a.B) {
+      p.err = VAS_DEV_BAD_LENGTHS;
+      return p;
+    }
+    L = a.seq_lens[i];
   }
-  // Sequences without tokens share a start with their successor: the search above ends on
-  // the last of equal starts, the walk below passes over the empty ones.
-  int64_t row = sums[lo];
-  int32_t i = lo * step, ql = 0;
-  for (; i < a.B; ++i) {
-    ql = a.query_lens[i];
-    const int64_t n = ql > 0 ? ql : 0;
-    if (t < row + n) break;
-    row += n;
-  }
-  if (i >= a.B) {
-    p.err = VAS_DEV_BAD_LENGTHS;
-    return p;
-  }
-  const int32_t L = a.seq_lens[i];
   if (!lengths_ok(a, L, ql) || row + ql > a.T) {
     p.err = VAS_DEV_BAD_LENGTHS;
     return p;
@@ -182,29 +270,32 @@ __device__ __forceinline__ Place place_of(const AppendArgs& a, const int64_t* su
   const int32_t pos = L - ql + (int32_t)(t - row);
   p.position = a.positions ? a.positions[t] : pos;
   if (a.rot && (p.position < 0 || p.position >= a.max_position)) p.err |= VAS_DEV_BAD_POSITION;
-  p.page = a.block_table[(size_t)i * a.maxp + pos / a.P];
-  p.slot = pos % a.P;
+  p.page = a.block_table[(size_t)i * a.maxp + (pos >> a.log2P)];
+  p.slot = pos & (a.P - 1);
   if (p.page < 0 || p.page >= a.num_pages) p.err |= VAS_DEV_BAD_PAGE;
   return p;
 }
 
 // KV: the pool's storage type; T: the activations' (float with VAS_F32, bf16 otherwise).
-// ROWS: head rows a lane takes per task; a task is 512 / D * ROWS consecutive rows (q
-// heads, then k, then v) of one token, one warp.  INTER: rotary pairs are neighbours.
+// ROWS: head rows a lane holds at a time, so a warp has a group of 512 / D * ROWS rows (q
+// heads, then k, then v) in flight.  A task is `iters` consecutive groups of one token: one
+// look-up of the token's place, one read of its table row.  A block scans the lengths once
+// and its warps take tasks gridDim apart; as soon as a row has been taken from its
+// registers the same row of the next group, or task, is fetched into them, so loads are
+// always under way.  INTER: rotary pairs are neighbours.
 template <typename T, int KV, int D, int ROWS, bool INTER>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(const AppendArgs a) {
   constexpr int kLanes = D / 16;     // lanes of a row
   constexpr int kSub = 32 / kLanes;  // rows of a warp at a time
   constexpr bool kQuant = KV == VAS_FP8_E4M3 || KV == VAS_INT8;
-  __shared__ int64_t sums[kAppendThreads + 1];
+  __shared__ Packing pk;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t task = (int64_t)blockIdx.x * kAppendWarps + warp;
-  const int32_t t = (int32_t)(task / a.groups);
-  const int32_t row0 = (int32_t)(task % a.groups) * (kSub * ROWS) + lane / kLanes;
   const int H = a.Hq + 2 * a.Hkv;
-  const bool live = t < a.T;
+  const uint32_t n_tasks = (uint32_t)a.T * (uint32_t)a.parts;  // at most INT_MAX
+  const uint32_t stride = gridDim.x * kAppendWarps;
+  uint32_t task = blockIdx.x * kAppendWarps + warp;
 
   // This lane's chunks of a row.  Split halves: rotated pairs (8c + e, 8c + e + rot / 2)
   // first, then the rest of the head.  Neighbours: 16 consecutive elements.
@@ -222,136 +313,163 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendArgs
     cb = ca + (D - a.rot) / 2;
   }
 
-  // The rows' values first: the look-up of the token's place overlaps their latency.
-  float xa[ROWS][8], xb[ROWS][8];
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int r = row0 + i * kSub;
-    if (live && r < H) {
+  // A row's values are on their way while the place of its token is looked up (and, for
+  // the first ones, while the block scans the lengths).
+  Raw<T> x[ROWS];
+  auto fetch = [&](Raw<T>& dst, int32_t t, int32_t r) {
+    if (t < a.T && r < H) {
       const T* p;
       if (r < a.Hq) p = static_cast<const T*>(a.q) + t * a.q_stride + r * D;
       else if (r < a.Hq + a.Hkv) p = static_cast<const T*>(a.k) + t * a.k_stride + (r - a.Hq) * D;
       else p = static_cast<const T*>(a.v) + t * a.v_stride + (r - a.Hq - a.Hkv) * D;
-      load8(p + ca, xa[i]);
-      load8(p + cb, xb[i]);
+      dst.load(p, ca, cb);
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) xa[i][e] = xb[i][e] = 0.f;
+      dst.zero();
     }
-  }
+  };
+  constexpr int kGroup = kSub * ROWS;
+  int32_t t = (int32_t)(task / (uint32_t)a.parts);
+  int32_t row0 = (int32_t)(task - (uint32_t)t * a.parts) * a.iters * kGroup + lane / kLanes;
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) fetch(x[i], t, row0 + i * kSub);
 
-  const int32_t step = (a.B + kAppendThreads - 1) / kAppendThreads;
-  scan_lengths(a, sums, step);
+  const int32_t step = (a.B + kAppendSeqs - 1) / kAppendSeqs;
+  scan_lengths(a, pk, step);
   if (blockIdx.x == 0) {  // the call's lengths as a whole
-    bool bad = threadIdx.x == 0 && sums[kAppendThreads] != a.T;
+    bool bad = threadIdx.x == 0 && pk.row0[kAppendSeqs] != a.T;
     for (int i = threadIdx.x; i < a.B; i += kAppendThreads)
       bad |= !lengths_ok(a, a.seq_lens[i], a.query_lens[i]);
     if (bad) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
   }
-  if (!live) return;
-  Place pl{0, 0, 0, 0};
-  if (lane == 0) {  // one lane looks the place up, the others take it from there
-    pl = place_of(a, sums, step, t);
-    if (pl.err) atomicOr(a.err, pl.err);
-  }
-  pl.page = __shfl_sync(0xffffffffu, pl.page, 0);
-  pl.slot = __shfl_sync(0xffffffffu, pl.slot, 0);
-  pl.position = __shfl_sync(0xffffffffu, pl.position, 0);
-  pl.err = __shfl_sync(0xffffffffu, pl.err, 0);
+  F8 wa{}, wb{};  // the weights of this lane's chunks, and whose they are
+  int kind = -1;  // 1: q, 0: k
+  while (task < n_tasks) {
+    const Place pl = place_of(a, pk, step, t, lane);
+    if (pl.err && lane == 0) atomicOr(a.err, pl.err);
 
-  // Cosines and sines of this lane's 8 pairs.
-  float cs[8], sn[8];
-  if (turned && !pl.err) {
-    const float* row = a.cos_sin + (size_t)pl.position * a.rot + 8 * c;
-    load8(row, cs);
-    load8(row + a.rot / 2, sn);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
-  }
+    // Cosines and sines of this lane's 8 pairs.
+    const uint64_t one = pair(1.f, 1.f);
+    F8 cs{{one, one, one, one}}, sn{{0, 0, 0, 0}};
+    if (turned && !pl.err) {
+      const float* row = a.cos_sin + (size_t)pl.position * a.rot + 8 * c;
+      cs = load_f8(row);
+      sn = load_f8(row + a.rot / 2);
+    }
 
+    task += stride;
+    int32_t t_task = (int32_t)(task / (uint32_t)a.parts);
+    const int32_t row_task =
+        (int32_t)(task - (uint32_t)t_task * a.parts) * a.iters * kGroup + lane / kLanes;
+    if (task >= n_tasks) t_task = a.T;
+    for (int it = 0; it < a.iters; ++it) {
+      const bool last = it + 1 == a.iters;
+      const int32_t t_next = last ? t_task : t, row_next = last ? row_task : row0 + kGroup;
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int r = row0 + i * kSub;
-    // Rows past H hold zeros and only take part in the shuffles.
-    const bool is_v = r >= a.Hq + a.Hkv, is_q = r < a.Hq;
-    const T* w = static_cast<const T*>(is_q ? a.q_weight : a.k_weight);
-    // Sum of squares over the row's lanes; every lane of the warp takes part.
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(xa[i][e], xa[i][e], fmaf(xb[i][e], xb[i][e], ss));
-#pragma unroll
-    for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!is_v) {
-      if (w != nullptr) {
-        const float inv = __fdiv_rn(1.f, __fsqrt_rn(ss * (1.f / D) + a.eps));
-        float wa[8], wb[8];
-        load8(w + ca, wa);
-        load8(w + cb, wb);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          xa[i][e] = xa[i][e] * inv * wa[e];
-          xb[i][e] = xb[i][e] * inv * wb[e];
+      for (int i = 0; i < ROWS; ++i) {
+        const int r = row0 + i * kSub;
+        // Rows past H hold zeros and only take part in the shuffles.
+        const bool is_v = r >= a.Hq + a.Hkv, is_q = r < a.Hq;
+        F8 xa = widen(x[i].a), xb = widen(x[i].b);
+        fetch(x[i], t_next, row_next + i * kSub);
+        const T* w = static_cast<const T*>(is_q ? a.q_weight : a.k_weight);
+        if (w != nullptr && kind != (int)is_q) {
+          kind = is_q;
+          wa = load_weights(w + ca);
+          wb = load_weights(w + cb);
         }
-      }
-      if (turned) {
-        if (INTER) {
+        // Sum of squares over the row's lanes; every lane of the warp takes part.
+        uint64_t s2 = mul2(xa.p[0], xa.p[0]);
+#pragma unroll
+        for (int e = 1; e < 4; ++e) s2 = fma2(xa.p[e], xa.p[e], s2);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s2 = fma2(xb.p[e], xb.p[e], s2);
+        float ss, hi;
+        unpair(s2, ss, hi);
+        ss += hi;
+#pragma unroll
+        for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (!is_v) {
+          if (w != nullptr) {
+            const float inv = rsqrtf(ss * (1.f / D) + a.eps);
+            const uint64_t inv2 = pair(inv, inv);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              xa.p[e] = mul2(mul2(xa.p[e], inv2), wa.p[e]);
+              xb.p[e] = mul2(mul2(xb.p[e], inv2), wb.p[e]);
+            }
+          }
+          if (turned) {
+            if (INTER) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float c0, c1, s0, s1, u0, u1;
+                unpair(cs.p[e], c0, c1);
+                unpair(sn.p[e], s0, s1);
+                // Pairs 2e and 2e + 1: chunk a holds pairs 0..3, chunk b 4..7.
+                uint64_t& y0 = e < 2 ? xa.p[2 * (e & 1)] : xb.p[2 * (e & 1)];
+                uint64_t& y1 = e < 2 ? xa.p[2 * (e & 1) + 1] : xb.p[2 * (e & 1) + 1];
+                unpair(y0, u0, u1);
+                y0 = pair(u0 * c0 - u1 * s0, u1 * c0 + u0 * s0);
+                unpair(y1, u0, u1);
+                y1 = pair(u0 * c1 - u1 * s1, u1 * c1 + u0 * s1);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint64_t u = xa.p[e], v = xb.p[e];
+                xa.p[e] = sub2(mul2(u, cs.p[e]), mul2(v, sn.p[e]));
+                xb.p[e] = fma2(v, cs.p[e], mul2(u, sn.p[e]));
+              }
+            }
+          }
+        }
+        float scale = 1.f;
+        if (kQuant && __any_sync(0xffffffffu, !is_q)) {
+          // The largest magnitude of the row, by the order of the bits (NaN above infinity).
+          uint32_t m = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float u0 = xa[i][2 * e], u1 = xa[i][2 * e + 1];
-            xa[i][2 * e] = u0 * cs[e] - u1 * sn[e];
-            xa[i][2 * e + 1] = u1 * cs[e] + u0 * sn[e];
-            const float w0 = xb[i][2 * e], w1 = xb[i][2 * e + 1];
-            xb[i][2 * e] = w0 * cs[4 + e] - w1 * sn[4 + e];
-            xb[i][2 * e + 1] = w1 * cs[4 + e] + w0 * sn[4 + e];
-          }
-        } else {
+            float y[4];
+            unpair(xa.p[e], y[0], y[1]);
+            unpair(xb.p[e], y[2], y[3]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float u = xa[i][e], v = xb[i][e];
-            xa[i][e] = u * cs[e] - v * sn[e];
-            xb[i][e] = v * cs[e] + u * sn[e];
+            for (int f = 0; f < 4; ++f) m = max(m, __float_as_uint(y[f]) & 0x7fffffffu);
           }
+#pragma unroll
+          for (int o = kLanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          scale = __fdiv_rn(__uint_as_float(m), KV == VAS_FP8_E4M3 ? 448.f : 127.f);
+          if (scale == 0.f) scale = 1.f;
+        }
+        if (r >= H) continue;
+        if (is_q) {
+          if (pl.err) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) xa.p[e] = xb.p[e] = pair(NAN, NAN);
+          }
+          T* p = static_cast<T*>(a.q_out) + ((size_t)t * a.Hq + r) * D;
+          store8(p + ca, xa);
+          store8(p + cb, xb);
+          continue;
+        }
+        if (pl.err) continue;
+        const int h = is_v ? r - a.Hq - a.Hkv : r - a.Hq;
+        const size_t at = (((size_t)pl.page * a.P + pl.slot) * a.Hkv + h) * D;
+        if constexpr (kQuant) {
+          uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) + at;
+          *reinterpret_cast<uint2*>(p + ca) = codes8<KV>(xa, scale);
+          *reinterpret_cast<uint2*>(p + cb) = codes8<KV>(xb, scale);
+          if (c == 0)
+            (is_v ? a.v_scale : a.k_scale)[((size_t)pl.page * a.Hkv + h) * a.P + pl.slot] = scale;
+        } else {
+          T* p = static_cast<T*>(is_v ? a.v_pages : a.k_pages) + at;
+          store8(p + ca, xa);
+          store8(p + cb, xb);
         }
       }
+      if (!last) row0 += kGroup;
     }
-    float scale = 1.f;
-    if constexpr (kQuant) {
-      // The largest magnitude of the row, by the order of the bits (NaN above infinity).
-      uint32_t m = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        m = max(m, max(__float_as_uint(xa[i][e]) & 0x7fffffffu, __float_as_uint(xb[i][e]) & 0x7fffffffu));
-#pragma unroll
-      for (int o = kLanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      scale = __fdiv_rn(__uint_as_float(m), KV == VAS_FP8_E4M3 ? 448.f : 127.f);
-      if (scale == 0.f) scale = 1.f;
-    }
-    if (r >= H) continue;
-    if (is_q) {
-      if (pl.err) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) xa[i][e] = xb[i][e] = NAN;
-      }
-      T* p = static_cast<T*>(a.q_out) + ((size_t)t * a.Hq + r) * D;
-      store8(p + ca, xa[i]);
-      store8(p + cb, xb[i]);
-      continue;
-    }
-    if (pl.err) continue;
-    const int h = is_v ? r - a.Hq - a.Hkv : r - a.Hq;
-    const size_t at = (((size_t)pl.page * a.P + pl.slot) * a.Hkv + h) * D;
-    if constexpr (kQuant) {
-      uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) + at;
-      *reinterpret_cast<uint2*>(p + ca) = codes8<KV>(xa[i], scale);
-      *reinterpret_cast<uint2*>(p + cb) = codes8<KV>(xb[i], scale);
-      if (c == 0)
-        (is_v ? a.v_scale : a.k_scale)[((size_t)pl.page * a.Hkv + h) * a.P + pl.slot] = scale;
-    } else {
-      T* p = static_cast<T*>(is_v ? a.v_pages : a.k_pages) + at;
-      store8(p + ca, xa[i]);
-      store8(p + cb, xb[i]);
-    }
+    t = t_task;
+    row0 = row_task;
   }
 }
 
@@ -566,37 +684,44 @@ bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
   return an > 0 && bn > 0 && x < y + (uintptr_t)bn && y < x + (uintptr_t)an;
 }
 
-// Rows of a lane per task.  With one row the most warps are in flight, which is what a
-// small step needs; with four, one look-up of the token's place and one read of its
-// table row serve four times the heads.
-constexpr int kAppendRows = 4;
-
-template <typename T, int KV, int D, bool INTER>
+template <typename T, int KV, int D, int ROWS, bool INTER>
 int launch_append_rows(AppendArgs& a, vas_stream_t stream) {
+  const int group = 32 / (D / 16) * ROWS;
+  const int64_t warps = (int64_t)vas::num_sms() * kAppendBlocks * kAppendWarps;
+  // Eight tasks a resident warp, where there are as many: the last round is then short
+  // against the whole.  Fewer where the tokens do not give them; never less than a group.
+  const int64_t groups = (a.Hq + 2 * a.Hkv + group - 1) / group;
+  int64_t parts = (8 * warps + a.T - 1) / a.T;
+  parts = parts < groups ? parts : groups;
+  if (parts * a.T > INT_MAX / 2) parts = 1;  // 32-bit task numbers, with room for the stride
+  a.iters = (int32_t)((groups + parts - 1) / parts);
+  a.parts = (int32_t)((groups + a.iters - 1) / a.iters);
+  const int64_t blocks = ((int64_t)a.T * a.parts + kAppendWarps - 1) / kAppendWarps;
+  const int64_t most = warps / kAppendWarps;
+  return launch(append_kernel<T, KV, D, ROWS, INTER>, dim3((unsigned)(blocks < most ? blocks : most)),
+                kAppendThreads, stream, a);
+}
+
+// Rows of a lane at a time.  With one the most warps share a small step's rows; with four
+// (fp32: two) a warp has the most bytes in flight and the fewest look-ups: a 768-token
+// step over FP8 pages 12.4 us against 13.7 (one) and 13.0 (two), eight 1024-token chunks
+// in bf16 60.9 against 62.7 and 65.1.
+template <typename T, int KV, int D, bool INTER>
+int launch_append_size(AppendArgs& a, vas_stream_t stream) {
   const int sub = 32 / (D / 16);
-  const int H = a.Hq + 2 * a.Hkv;
-  const int sms = vas::num_sms();
-  if (!sms) return VAS_E_CUDA;
-  const int64_t one = (int64_t)a.T * ((H + sub - 1) / sub);
-  const bool many = one > (int64_t)sms * 64;
-  const int rows = many ? kAppendRows : 1;
-  a.groups = (H + sub * rows - 1) / (sub * rows);
-  const int64_t blocks = ((int64_t)a.T * a.groups + kAppendWarps - 1) / kAppendWarps;
-  if (blocks > INT_MAX) return VAS_E_UNSUPPORTED;
-  if (many)
-    return launch(append_kernel<T, KV, D, kAppendRows, INTER>, dim3((unsigned)blocks),
-                  kAppendThreads, stream, a);
-  return launch(append_kernel<T, KV, D, 1, INTER>, dim3((unsigned)blocks), kAppendThreads, stream,
-                a);
+  const int64_t one = (int64_t)a.T * ((a.Hq + 2 * a.Hkv + sub - 1) / sub);
+  const bool many = one > (int64_t)vas::num_sms() * 64;
+  return many ? launch_append_rows<T, KV, D, sizeof(T) == 4 ? 2 : 4, INTER>(a, stream)
+              : launch_append_rows<T, KV, D, 1, INTER>(a, stream);
 }
 
 template <typename T, int KV>
 int launch_append(AppendArgs& a, int D, bool inter, vas_stream_t stream) {
   if (D == 128)
-    return inter ? launch_append_rows<T, KV, 128, true>(a, stream)
-                 : launch_append_rows<T, KV, 128, false>(a, stream);
-  return inter ? launch_append_rows<T, KV, 64, true>(a, stream)
-               : launch_append_rows<T, KV, 64, false>(a, stream);
+    return inter ? launch_append_size<T, KV, 128, true>(a, stream)
+                 : launch_append_size<T, KV, 128, false>(a, stream);
+  return inter ? launch_append_size<T, KV, 64, true>(a, stream)
+               : launch_append_size<T, KV, 64, false>(a, stream);
 }
 
 // The checks that paged_kv_copy and paged_kv_keep_path share; *token_bytes of one operand.
@@ -718,10 +843,11 @@ int paged_kv_append(const void* q, const void* k, const void* v, const void* q_w
   a.maxp = d.max_pages_per_seq;
   a.rot = d.rotary_dim;
   a.max_position = d.max_position;
-  a.groups = 0;
+  a.log2P = d.page_size == 16 ? 4 : 5;
+  a.parts = a.iters = 1;
   a.eps = d.eps;
   a.err = vas::device_error_word();
-  if (!a.err) return VAS_E_CUDA;
+  if (!a.err || !vas::num_sms()) return VAS_E_CUDA;
   const bool inter = d.interleaved != 0;
   switch (d.kv_dtype) {
     case VAS_F32: return launch_append<float, VAS_F32>(a, d.head_dim, inter, stream);

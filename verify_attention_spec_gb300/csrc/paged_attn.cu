@@ -1179,55 +1179,94 @@ __device__ __forceinline__ size_t partial_row(const AttnArgs& a, const SeqPlan& 
 }
 
 // Merge the partials of every split of rows r0 .. r0+Rb-1 of one KV head (the caller is
-// the last split to finish: all partials are in memory).  Four consumer warps.
+// the last split to finish: all partials are in memory).  Four consumer warps, each
+// kMergeRows rows at a time: the lses of all of them are loaded together (lane s holds
+// split s), then their O rows, so a row costs its share of two round trips to L2 and not
+// two for every split.  (One row and one split at a time took 40 us for 40 rows of ten
+// splits, as a window behind a long shared prefix has them.)  Every sum keeps the order of
+// the splits.
+constexpr int kMergeRows = 2;
 template <int D>
 __device__ void merge_splits(const AttnArgs& a, const SeqPlan& sp, int head, int r0, int Rb,
                              int warp, int lane) {
   constexpr int E = D / 32;
   const float kLn2 = 0.6931471805599453f;
-  for (int rr = warp; rr < Rb; rr += kConsumerWarps) {
-    const int r = r0 + rr;
-    float mx = -INFINITY;
-    bool bad = false;
-    for (int s = lane; s < sp.nsplit; s += 32) {
-      const float v = __ldcg(a.part_lse + partial_row(a, sp, s, head, r));
-      bad |= isnan(v);
-      mx = fmaxf(mx, v);
+  const int n = sp.nsplit;
+  const size_t step = (size_t)a.Hkv * ((size_t)a.G * sp.qlen);  // partial rows of a split
+  for (int rr = warp * kMergeRows; rr < Rb; rr += kConsumerWarps * kMergeRows) {
+    size_t row[kMergeRows];  // rows past the last repeat it and are not written
+    float mu[kMergeRows], first[kMergeRows], wsum[kMergeRows], acc[kMergeRows][E];
+    bool bad[kMergeRows];
+#pragma unroll
+    for (int k = 0; k < kMergeRows; ++k) {
+      row[k] = partial_row(a, sp, 0, head, r0 + min(rr + k, Rb - 1));
+      first[k] = lane < n ? __ldcg(a.part_lse + row[k] + lane * step) : -INFINITY;
     }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    bad = __any_sync(0xffffffffu, bad);
-    const float mu = mx == -INFINITY ? 0.f : mx;
-    float acc[E];
+    for (int k = 0; k < kMergeRows; ++k) {
+      float mx = fmaxf(first[k], -INFINITY);
+      bad[k] = isnan(first[k]);
+      for (int s = lane + 32; s < n; s += 32) {
+        const float v = __ldcg(a.part_lse + row[k] + s * step);
+        bad[k] |= isnan(v);
+        mx = fmaxf(mx, v);
+      }
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    float wsum = 0.f;
-    for (int s = 0; s < sp.nsplit; ++s) {
-      const size_t pr = partial_row(a, sp, s, head, r);
-      const float w = exp2f((__ldcg(a.part_lse + pr) - mu) * 1.4426950408889634f);
-      wsum += w;
-      const float* po = a.part_o + pr * D + lane * E;
-      if constexpr (E == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(po));
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
-        acc[2] = fmaf(w, v.z, acc[2]);
-        acc[3] = fmaf(w, v.w, acc[3]);
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(po));
-        acc[0] = fmaf(w, v.x, acc[0]);
-        acc[1] = fmaf(w, v.y, acc[1]);
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      bad[k] = __any_sync(0xffffffffu, bad[k]);
+      mu[k] = mx == -INFINITY ? 0.f : mx;
+      wsum[k] = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[k][e] = 0.f;
+    }
+    for (int s0 = 0; s0 < n; s0 += 32) {
+      float w[kMergeRows];
+#pragma unroll
+      for (int k = 0; k < kMergeRows; ++k) {
+        const float v = s0 == 0 ? first[k]
+                                : (s0 + lane < n ? __ldcg(a.part_lse + row[k] + (s0 + lane) * step)
+                                                 : -INFINITY);
+        w[k] = exp2f((v - mu[k]) * 1.4426950408889634f);
+      }
+#pragma unroll 4
+      for (int s = s0; s < min(n, s0 + 32); ++s) {
+        float4 v[kMergeRows];
+#pragma unroll
+        for (int k = 0; k < kMergeRows; ++k) {
+          const float* po = a.part_o + (row[k] + s * step) * D + lane * E;
+          if constexpr (E == 4) {
+            v[k] = __ldcg(reinterpret_cast<const float4*>(po));
+          } else {
+            const float2 h = __ldcg(reinterpret_cast<const float2*>(po));
+            v[k] = make_float4(h.x, h.y, 0.f, 0.f);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kMergeRows; ++k) {
+          const float ws = __shfl_sync(0xffffffffu, w[k], s - s0);
+          wsum[k] += ws;
+          acc[k][0] = fmaf(ws, v[k].x, acc[k][0]);
+          acc[k][1] = fmaf(ws, v[k].y, acc[k][1]);
+          if constexpr (E == 4) {
+            acc[k][2] = fmaf(ws, v[k].z, acc[k][2]);
+            acc[k][3] = fmaf(ws, v[k].w, acc[k][3]);
+          }
+        }
       }
     }
-    const float inv = 1.f / wsum;
-    const size_t orow = out_row(a, sp, head, r);
-    __nv_bfloat16* og = static_cast<__nv_bfloat16*>(a.out) + orow * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float x0 = bad ? NAN : acc[e] * inv, x1 = bad ? NAN : acc[e + 1] * inv;
-      *reinterpret_cast<uint32_t*>(og + e) = pack_bf16x2(x0, x1);
+    for (int k = 0; k < kMergeRows; ++k) {
+      if (rr + k >= Rb) break;
+      const float inv = 1.f / wsum[k];
+      const size_t orow = out_row(a, sp, head, r0 + rr + k);
+      __nv_bfloat16* og = static_cast<__nv_bfloat16*>(a.out) + orow * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const float x0 = bad[k] ? NAN : acc[k][e] * inv, x1 = bad[k] ? NAN : acc[k][e + 1] * inv;
+        *reinterpret_cast<uint32_t*>(og + e) = pack_bf16x2(x0, x1);
+      }
+      if (lane == 0) a.lse[orow] = bad[k] ? NAN : mu[k] + log2f(wsum[k]) * kLn2;
     }
-    if (lane == 0) a.lse[orow] = bad ? NAN : mu + log2f(wsum) * kLn2;
   }
 }
 

@@ -147,7 +147,12 @@ __global__ void __launch_bounds__(256) prefix_simple_kernel(const PrefixArgs a) 
 constexpr int kTile = 128;                  // tokens of a tile, rows of a stream
 constexpr int kStreamThreads = 128;
 constexpr int kProducerWarp = 8, kMmaWarp = 9;
-constexpr int kPrefixThreads = 320;
+constexpr int kPrefixThreads = 384;  // two warps idle: registers move by groups of four warps
+// Registers a thread: what the launch gives (168) is split between the streams, whose 128
+// scores live in registers, and the other four warps.  256 x 200 + 128 x 80 = 384 x 160.
+constexpr int kStreamRegs = 200, kOtherRegs = 80, kLaunchRegs = 160;
+static_assert(2 * kStreamThreads * kStreamRegs + 128 * kOtherRegs <= kPrefixThreads * kLaunchRegs,
+              "setmaxnreg draws on the registers of the launch");
 constexpr float kRebase = 8.f;  // a row's reference maximum may trail by this (log2 units)
 
 template <int D>
@@ -187,6 +192,30 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* r) {
         "=r"(r[62]), "=r"(r[63])
       : "r"(taddr)
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_st64(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x64.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,"
+      "%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,"
+      "%58,%59,%60,%61,%62,%63,%64};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(r[32]), "r"(r[33]), "r"(r[34]), "r"(r[35]),
+      "r"(r[36]), "r"(r[37]), "r"(r[38]), "r"(r[39]), "r"(r[40]), "r"(r[41]), "r"(r[42]),
+      "r"(r[43]), "r"(r[44]), "r"(r[45]), "r"(r[46]), "r"(r[47]), "r"(r[48]), "r"(r[49]),
+      "r"(r[50]), "r"(r[51]), "r"(r[52]), "r"(r[53]), "r"(r[54]), "r"(r[55]), "r"(r[56]),
+      "r"(r[57]), "r"(r[58]), "r"(r[59]), "r"(r[60]), "r"(r[61]), "r"(r[62]), "r"(r[63])
+      : "memory");
+}
+
+// The warps beside the streams hand registers over (every warp of the group executes it).
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
 }
 
 // What a unit is, the same for every role.
@@ -262,6 +291,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 
   if (warp == kProducerWarp) {
     // ------------------------------ producer ------------------------------
+    give_registers();
     // Lane e of a tile's boxes: page e % kPages, column half e / kPages.  The order of the
     // ring is the order the MMA warp asks in: K first, by one tile (both streams) or two.
     static_assert(kPages * S::kHalves <= 32, "one box a lane");
@@ -304,6 +334,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       mbar_wait(&full[f % kSlots], (f / kSlots) & 1);
   } else if (warp == kMmaWarp) {
     // ------------------------------ MMA warp ------------------------------
+    give_registers();
     // Per stream: S of its next tile is issued right behind the O product of the last one
     // (which is the last reader of the P it overwrites; products run in issue order), so
     // s_full also says that O may be rescaled.
@@ -421,8 +452,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     // Tensor memory is freed only after every product this warp issued has completed.
     commit(fin);
     if (!mbar_wait(fin, 0)) ok = false;
-  } else {
+  } else if (warp < 2 * kStreamThreads / 32) {
     // ------------------------------ softmax streams ------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStreamRegs));
     const int st = warp >> 2, row = threadIdx.x & (kStreamThreads - 1);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t s_at = tmem_s + lanes + st * kTile, o_at = tmem_o + lanes + st * D;
@@ -481,7 +513,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < kTile; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(sr[e]));
+        for (int e = 0; e < kTile; e += 2)
+          mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;  // c > 0
         const bool rebase = top > m + kRebase;
         const float alpha = rebase ? exp2f(m - top) : 1.f;
@@ -500,23 +533,23 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           }
         }
         const float mu = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t c2 = pair(c, c), mu2 = pair(-mu, -mu);
+        uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int e = 0; e < kTile; e += 2) {
-          const float p0 = ex2_approx(fmaf(__uint_as_float(sr[e]), c, -mu));
-          const float p1 = ex2_approx(fmaf(__uint_as_float(sr[e + 1]), c, -mu));
-          sum[e & 2] += p0;
-          sum[(e & 2) + 1] += p1;
+          float p0, p1;
+          unpair(fma2(pair(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, mu2), p0, p1);
+          p0 = ex2_approx(p0);
+          p1 = ex2_approx(p1);
+          sum[(e >> 1) & 3] = add2(sum[(e >> 1) & 3], pair(p0, p1));
           sr[e >> 1] = pack_bf16x2(p0, p1);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        uint32_t half[32];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) half[e] = sr[32 * h + e];
-          tmem_st32(s_at + 32 * h, half);
+        {
+          float lo, hi;
+          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), lo, hi);
+          l += lo + hi;
         }
+        tmem_st64(s_at, sr);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[st]);
@@ -588,6 +621,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       if (bad && row == 0 && st == 0) atomicOr(a.err, VAS_DEV_BAD_PAGE);
       if (!x.both) named_bar_sync(3, 2 * kStreamThreads);  // the dump is read: Q may be staged
     }
+  } else {
+    give_registers();
   }
   if (!ok && lane == 0) atomicOr(a.err, VAS_DEV_TIMEOUT);
   tc_fence_before();
@@ -605,8 +640,14 @@ int launch_tc(const CUtensorMap& mk, const CUtensorMap& mv, const PrefixArgs& a,
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return VAS_E_CUDA;
   std::call_once(once[dev & 63], [&] {
-    attr_err[dev & 63] = cudaFuncSetAttribute(
-        prefix_kernel<D, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem<D>::kDynBytes);
+    cudaFuncAttributes fa;
+    attr_err[dev & 63] = cudaFuncGetAttributes(&fa, prefix_kernel<D, P>);
+    // Fewer registers than the split counts on would leave setmaxnreg waiting.
+    if (attr_err[dev & 63] == cudaSuccess && fa.numRegs < kLaunchRegs)
+      attr_err[dev & 63] = cudaErrorInvalidConfiguration;
+    if (attr_err[dev & 63] == cudaSuccess)
+      attr_err[dev & 63] = cudaFuncSetAttribute(
+          prefix_kernel<D, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem<D>::kDynBytes);
   });
   if (attr_err[dev & 63] != cudaSuccess) return VAS_E_CUDA;
   cudaLaunchConfig_t cfg = {};
