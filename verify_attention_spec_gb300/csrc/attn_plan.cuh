@@ -30,27 +30,36 @@ struct PlanHeader {
   int32_t work_counter;
   int32_t chunk_pages;
   int32_t n_partial_rows;
-  int32_t n_prefix_items;  // shared-prefix calls only
+  // Shared-prefix calls: groups that are shared, and how their work is dealt out.
+  int32_t n_groups;
+  int64_t span, share;
 };
 
-// A group of sequences whose shared pages are computed once (nsplit 0: it is not).  Its
-// rows, of one KV head, are its members' rows one after the other: row r is query token
-// qrow0 + r / G, query head head * G + r % G.
+// A group of sequences whose shared pages are computed once.  Its rows, of one KV head, are
+// its members' rows one after the other: row r is query token qrow0 + r / G, query head
+// head * G + r % G.
+//
+// The work of all groups is one line of `span` units of weight: a group's blocks (KV head by
+// KV head, kPrefixRows rows each) one behind the other from `base` on, a block `tiles` tiles
+// of kPrefixTile tokens, a tile `weight` units.  CTA k takes the units k * share ..
+// (k + 1) * share - 1, so a block is computed in pieces by the CTAs its units fall to, piece
+// j by the (j + 1)th of them.  share and base are even, so no tile is cut.
 struct PrefixGroup {
-  int32_t qrow0;      // first query token
-  int32_t rows;       // G * query tokens
-  int32_t leader;     // sequence whose table names the shared pages
-  int32_t pages;      // shared pages
-  int32_t nsplit;     // splits of them
-  int32_t seq0, seq1; // members
+  int32_t qrow0;       // first query token
+  int32_t rows;        // G * query tokens
+  int32_t leader;      // sequence whose table names the shared pages
+  int32_t pages;       // shared pages
+  int32_t parts;       // partials of a row: the most pieces a block is cut into
+  int32_t seq0, seq1;  // members
+  int32_t tiles, blocks, weight;
+  int64_t base;
 };
+constexpr int kPrefixRows = 256;  // rows of a block
+constexpr int kPrefixTile = 128;  // tokens of a tile
 
-// One split of a group's shared pages and one row block of it, for every KV head.
-struct PrefixItem {
-  int32_t group, page_begin, page_end, split_rb;  // split << kPrefixRbBits | row block
-};
-constexpr int kPrefixRbBits = 16;
-constexpr int kPrefixRows = 256;  // rows of a row block
+__host__ __device__ __forceinline__ int64_t prefix_blocks(int64_t R) {
+  return (R + kPrefixRows - 1) / kPrefixRows;
+}
 
 // Partial rows of a sequence: [split][KV head][G * ql], from partial_base on.
 __device__ __forceinline__ size_t partial_index(const SeqPlan& sp, int Hkv, int G, int split,
@@ -68,7 +77,6 @@ struct PrefixArgs {
   const SeqPlan* seqplan;
   const int32_t* row0;  // [B + 1] first query token of each sequence
   const PrefixGroup* groups;
-  const PrefixItem* items;
   const PlanHeader* header;
   float* part_o;
   float* part_lse;

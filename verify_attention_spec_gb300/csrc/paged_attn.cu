@@ -104,8 +104,7 @@ constexpr int kPlanSmemSeqs = 4096;
 constexpr int kSeqInvalid = 1;
 // Shared prefixes (paged_attn_fwd_prefix).
 constexpr int kMinPrefixTokens = 256;  // shorter ones are left to the members
-constexpr int kMinPrefixSplit = 256;   // tokens of a split, at least
-constexpr int kPrefixUnitTokens = 400; // what a unit's fixed costs weigh, in tokens
+constexpr int kMinPrefixShare = 4;     // units of weight of a CTA, at least
 
 // What the producer hands the consumers for one unit (u < 0: no more work).
 struct RingEntry {
@@ -117,8 +116,8 @@ struct RingEntry {
 
 struct Layout {
   size_t seqplan, token_seq, items, order, counters, part_lse, part_o, total;
-  size_t row0, shared, groups, pitems;  // shared-prefix calls only
-  int64_t items_cap, partial_cap, pitems_cap;
+  size_t row0, shared, entry, groups;  // shared-prefix calls only
+  int64_t items_cap, partial_cap;
 };
 
 __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -146,10 +145,9 @@ struct PlanArgs {
   const int32_t* prefix_lens;
   int32_t num_groups, sms;
   int32_t* row0;        // [B + 1] first query token of each sequence
-  int32_t* shared;      // [B] group of a sequence whose prefix is shared, or -1
-  PrefixGroup* groups;  // [num_groups]
-  PrefixItem* pitems;
-  int64_t pitems_cap;
+  int32_t* shared;      // [B] entry of `groups` that shares a sequence's prefix; -1: none
+  int32_t* entry;       // [num_groups] entry of a group the caller gave, or -1
+  PrefixGroup* groups;  // the shared ones, at most num_groups
 };
 
 struct SeqShape {
@@ -279,46 +277,49 @@ __device__ __forceinline__ int32_t group_of(const PlanArgs& a, int32_t i) {
   return a.group_start[lo] <= i && lo < a.num_groups ? lo : -1;
 }
 
-// Row blocks of a group of R rows per KV head.
-__host__ __device__ __forceinline__ int64_t prefix_blocks(int64_t R) {
-  return (R + kPrefixRows - 1) / kPrefixRows;
-}
-
-// Shared prefixes: which groups are computed once, in how many splits, and their items.
-// The whole block; leaves a.row0, a.shared, a.groups, a.pitems.  Returns whether the
-// groups themselves are consistent; when they or the lengths are not, nothing is shared,
-// and a sequence that its group's prefix_lens does not fit has shared[i] = -2.
+// Shared prefixes: which groups are computed once and how their work is dealt out.  The
+// whole block; leaves a.row0, a.shared, a.groups and the header's part.  a.shared[i] = -2
+// marks a sequence that its group's prefix_lens does not fit; then, and when the groups or
+// the lengths are inconsistent, nothing is shared.  Returns whether the groups are
+// consistent.
 template <typename ShapeFn>
-__device__ bool plan_prefixes(const PlanArgs& a, bool lengths_ok, ShapeFn shape,
-                              int64_t (*red)[4]) {
-  __shared__ int32_t s_bad, s_best;
-  __shared__ float s_time[kPlanThreads / 32];
-  __shared__ int32_t s_splits[kPlanThreads / 32];
+__device__ bool plan_prefixes(const PlanArgs& a, ShapeFn shape, int64_t (*red)[4]) {
+  __shared__ int32_t s_bad;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) s_bad = 0;
+  if (tid == 0) {
+    s_bad = 0;
+    a.header->n_groups = 0;
+  }
   __syncthreads();
-  for (int g = tid; g <= a.num_groups; g += kPlanThreads) {
-    const int32_t s0 = a.group_start[g];
-    const int32_t s1 = g < a.num_groups ? a.group_start[g + 1] : a.B;
-    if (s0 < 0 || s0 > s1 || s1 > a.B) s_bad = 1;
-    if (g < a.num_groups && a.prefix_lens[g] < 0) s_bad = 1;
+  {
+    bool bad = false;
+    for (int g = tid; g <= a.num_groups; g += kPlanThreads) {
+      const int32_t s0 = a.group_start[g];
+      const int32_t s1 = g < a.num_groups ? a.group_start[g + 1] : a.B;
+      bad |= s0 < 0 || s0 > s1 || s1 > a.B;
+      if (g < a.num_groups) {
+        bad |= a.prefix_lens[g] < 0;
+        a.entry[g] = -1;
+      }
+    }
+    if (bad) s_bad = 1;
   }
   __syncthreads();
   const bool order_ok = s_bad == 0;
-  __syncthreads();
-  // First query token of each sequence; sequences a group's prefix does not fit.
+  // First query token of each sequence, its group, and whether the group's prefix fits it.
   int64_t carry[1] = {0};
-  bool misfit = false;
+  bool misfit = false, invalid = false;
   for (int base = 0; base < a.B; base += kPlanThreads) {
     const int i = base + tid;
     int64_t v[1] = {0}, t[1];
     if (i < a.B) {
       const SeqShape s = shape(i);
       v[0] = s.ql > 0 ? s.ql : 0;
+      invalid |= !s.valid;
       int32_t mark = -1;
       if (order_ok && s.valid && s.ql > 0) {
-        const int32_t g = group_of(a, i);
-        if (g >= 0 && a.prefix_lens[g] > s.L - s.ql) mark = -2;
+        mark = group_of(a, i);
+        if (mark >= 0 && a.prefix_lens[mark] > s.L - s.ql) mark = -2;
       }
       misfit |= mark == -2;
       a.shared[i] = mark;
@@ -329,132 +330,98 @@ __device__ bool plan_prefixes(const PlanArgs& a, bool lengths_ok, ShapeFn shape,
     carry[0] += t[0];
   }
   if (tid == 0) a.row0[a.B] = (int32_t)(carry[0] < a.T ? carry[0] : a.T);
-  if (misfit) s_bad = 1;
+  if (misfit) atomicOr(&s_bad, 1);   // groups that do not fit the batch
+  if (invalid) atomicOr(&s_bad, 2);  // lengths that paged_attn_fwd refuses
   __syncthreads();
-  const bool fine = s_bad == 0;
-  const bool share = fine && lengths_ok;
-  if (tid == 0) a.header->n_prefix_items = 0;
-  if (!share) return fine;
-
-  // The groups worth sharing: their rows, members with query tokens, leader.
-  for (int g = tid; g < a.num_groups; g += kPlanThreads) {
-    PrefixGroup pg;
-    pg.seq0 = a.group_start[g];
-    pg.seq1 = a.group_start[g + 1];
-    pg.qrow0 = a.row0[pg.seq0];
-    pg.rows = (int32_t)((a.row0[pg.seq1] - pg.qrow0) * (int64_t)a.G);
-    pg.pages = a.prefix_lens[g] / a.P;
-    pg.leader = -1;
-    pg.nsplit = 0;
-    if (pg.pages * a.P < kMinPrefixTokens || pg.rows == 0) pg.pages = 0;
-    a.groups[g] = pg;
-  }
-  __syncthreads();
-  // A group's leader is its first member with query tokens; a group whose leader has all
-  // of them is left alone.
-  for (int i = tid; i < a.B; i += kPlanThreads) {
-    if (a.row0[i + 1] == a.row0[i]) continue;
-    const int32_t g = group_of(a, i);
-    if (g < 0 || a.groups[g].pages == 0 || a.row0[i] != a.groups[g].qrow0) continue;
-    a.groups[g].leader = i;
-    if (a.row0[i + 1] == a.row0[a.groups[g].seq1]) a.groups[g].pages = 0;
-  }
-  __syncthreads();
-
-  // Splits: candidate k cuts the longest prefix in ns(k) and every other one in pieces no
-  // longer; each warp weighs every (kPlanThreads / 32)th candidate by
-  // waves of units * (a unit's tokens + its fixed costs), and the cheapest that fits the
-  // item list and the partial rows wins (the fewest splits among equals).
-  int64_t most[2] = {0, 0};  // longest prefix (max through the sum of one writer below)
-  {
-    int32_t m = 0;
-    for (int g = tid; g < a.num_groups; g += kPlanThreads) m = max(m, a.groups[g].pages);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (tid == 0) s_best = 0;
+  const bool fine = (s_bad & 1) == 0;
+  if (s_bad || carry[0] != a.T) {
     __syncthreads();
-    if (lane == 0) atomicMax(&s_best, m);
-    __syncthreads();
-    most[0] = s_best;
-    __syncthreads();
+    for (int i = tid; i < a.B; i += kPlanThreads)
+      if (a.shared[i] >= 0) a.shared[i] = -1;
+    return fine;
   }
-  const int64_t longest = most[0];
-  if (longest == 0) return fine;
-  constexpr int kCandidates = 64, kWarps = kPlanThreads / 32;
-  float best_t = INFINITY;
-  int32_t best_c = 0;
-  for (int k = warp; k < kCandidates; k += kWarps) {
-    const int64_t ns = k < 32 ? k + 1 : (int64_t)(32.f * exp2f((k - 31) * 0.125f));
-    const int64_t c = (longest + ns - 1) / ns;
-    if (k > 0 && c * a.P < kMinPrefixSplit) continue;
-    int64_t units = 0, items = 0, parts = 0;
-    for (int g = lane; g < a.num_groups; g += 32) {
-      const PrefixGroup pg = a.groups[g];
-      if (pg.pages == 0) continue;
-      const int64_t n = (pg.pages + c - 1) / c;
-      items += n * prefix_blocks(pg.rows);
-      parts += (n + 1) * a.Hkv * pg.rows;  // and one of the members' own at least
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      items += __shfl_xor_sync(0xffffffffu, items, o);
-      parts += __shfl_xor_sync(0xffffffffu, parts, o);
-    }
-    if (items > a.pitems_cap || parts > a.partial_cap) continue;
-    units = items * a.Hkv;
-    const int64_t waves = (units + a.sms - 1) / a.sms;
-    const float t = (float)waves * (float)(c * a.P + kPrefixUnitTokens);
-    if (t < best_t) {
-      best_t = t;
-      best_c = (int32_t)c;
-    }
-  }
-  if (lane == 0) {
-    s_time[warp] = best_t;
-    s_splits[warp] = best_c;
-  }
-  __syncthreads();
-  for (int w = 0; w < kWarps; ++w)
-    if (s_time[w] < best_t || (s_time[w] == best_t && s_splits[w] > best_c)) {
-      best_t = s_time[w];
-      best_c = s_splits[w];
-    }
-  if (best_c == 0) return fine;  // no room for the partials: nothing is shared
 
-  // Items, group by group.
-  int64_t icarry[1] = {0};
+  // The groups worth sharing, one behind the other, and their spans of work.
+  int64_t at[2] = {0, 0};  // entries, units of weight
   for (int base = 0; base < a.num_groups; base += kPlanThreads) {
     const int g = base + tid;
-    int64_t v[1] = {0}, t[1];
-    int32_t n = 0, nrb = 0, each = 0;
-    if (g < a.num_groups && a.groups[g].pages > 0) {
-      const PrefixGroup pg = a.groups[g];
-      n = (pg.pages + best_c - 1) / best_c;
-      each = (pg.pages + n - 1) / n;  // even pieces
-      n = (pg.pages + each - 1) / each;
-      nrb = (int32_t)prefix_blocks(pg.rows);
-      a.groups[g].nsplit = n;
-      v[0] = (int64_t)n * nrb;
-    }
-    block_scan<1>(v, red, t);
-    int64_t at = icarry[0] + v[0];
-    for (int sp = 0; sp < n; ++sp)
-      for (int rb = 0; rb < nrb; ++rb) {
-        PrefixItem it;
-        it.group = g;
-        it.page_begin = sp * each;
-        it.page_end = min((sp + 1) * each, a.groups[g].pages);
-        it.split_rb = (sp << kPrefixRbBits) | rb;
-        a.pitems[at++] = it;
+    PrefixGroup pg;
+    int64_t v[2] = {0, 0}, t[2];
+    if (g < a.num_groups) {
+      pg.seq0 = a.group_start[g];
+      pg.seq1 = a.group_start[g + 1];
+      pg.qrow0 = a.row0[pg.seq0];
+      pg.rows = (int32_t)((a.row0[pg.seq1] - pg.qrow0) * (int64_t)a.G);
+      pg.pages = a.prefix_lens[g] / a.P;
+      pg.leader = pg.seq0;
+      pg.parts = 0;
+      // The first member with query tokens is the leader; alone it has nothing to share.
+      int32_t first = pg.seq0;
+      while (first < pg.seq1 && a.row0[first + 1] == pg.qrow0) ++first;
+      const bool alone = first >= pg.seq1 || a.row0[first + 1] == a.row0[pg.seq1];
+      pg.leader = first;
+      pg.tiles = (pg.pages * a.P + kPrefixTile - 1) / kPrefixTile;
+      pg.blocks = (int32_t)prefix_blocks(pg.rows) * a.Hkv;
+      // A tile feeds one stream or two, according to the rows.
+      pg.weight = pg.rows > kPrefixRows / 2 ? 2 : 1;
+      if (!alone && pg.pages * a.P >= kMinPrefixTokens) {
+        v[0] = 1;
+        v[1] = ((int64_t)pg.blocks * pg.tiles * pg.weight + 1) & ~1ll;
       }
-    icarry[0] += t[0];
-  }
-  if (tid == 0) a.header->n_prefix_items = (int32_t)icarry[0];
-  for (int i = tid; i < a.B; i += kPlanThreads) {
-    const int32_t g = group_of(a, i);
-    if (g >= 0 && a.groups[g].nsplit > 0) a.shared[i] = g;
+    }
+    const bool share = v[0] != 0;
+    block_scan<2>(v, red, t);
+    if (share) {
+      const int32_t e = (int32_t)(at[0] + v[0]);
+      pg.base = at[1] + v[1];
+      a.entry[g] = e;
+      a.groups[e] = pg;
+    }
+    at[0] += t[0];
+    at[1] += t[1];
   }
   __syncthreads();
+  const int n = (int)at[0];
+  const int64_t span = at[1];
+  if (n > 0) {
+    // Every CTA the same share, as long as the partials fit the workspace; larger shares,
+    // so fewer pieces, until they do.
+    int64_t each = (span + a.sms - 1) / a.sms;
+    each = ((each > kMinPrefixShare ? each : kMinPrefixShare) + 1) & ~1ll;
+    for (;; each *= 2) {
+      int64_t need[1] = {0};
+      for (int e = warp; e < n; e += kPlanThreads / 32) {
+        const PrefixGroup pg = a.groups[e];
+        const int64_t len = (int64_t)pg.tiles * pg.weight;
+        int32_t parts = 1;
+        for (int b = lane; b < pg.blocks; b += 32) {
+          const int64_t first = pg.base + b * len;
+          parts = max(parts, (int32_t)((first + len - 1) / each - first / each) + 1);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) parts = max(parts, __shfl_xor_sync(0xffffffffu, parts, o));
+        if (lane == 0) {
+          a.groups[e].parts = parts;
+          need[0] += (int64_t)(parts + 1) * a.Hkv * pg.rows;  // and a split of the members' own
+        }
+      }
+      block_sum<1>(need, red);
+      if (need[0] <= a.partial_cap) {
+        if (tid == 0) {
+          a.header->n_groups = n;
+          a.header->span = span;
+          a.header->share = each;
+        }
+        break;
+      }
+      if (each >= span) {  // no room: nothing is shared
+        for (int i = tid; i < a.B; i += kPlanThreads) a.shared[i] = -1;
+        return fine;
+      }
+    }
+  }
+  for (int i = tid; i < a.B; i += kPlanThreads)
+    if (a.shared[i] >= 0) a.shared[i] = a.entry[a.shared[i]];
   return fine;
 }
 
@@ -487,20 +454,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       } else if (g >= 0 && s.R > 0) {
         s.page0 = a.groups[g].pages;
         s.npages -= s.page0;
-        s.parts = a.groups[g].nsplit;
+        s.parts = a.groups[g].parts;
       }
     }
     return s;
   };
   if constexpr (PFX) {
-    int64_t chk[2] = {0, 0};  // rows, bad
-    for (int i = tid; i < a.B; i += kPlanThreads) {
-      const SeqShape s = shape(i);
-      chk[1] += !s.valid;
-      chk[0] += s.ql > 0 ? s.ql : 0;
-    }
-    block_sum<2>(chk, red);
-    const bool fine = plan_prefixes(a, chk[0] == a.T && chk[1] == 0, whole_shape, red);
+    const bool fine = plan_prefixes(a, whole_shape, red);
     if (tid == 0 && !fine) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
     planned = true;
     __syncthreads();
@@ -2597,11 +2557,10 @@ int64_t items_extra(int sms) { return 4LL * kUnitsPerSm * (sms > 0 ? sms : 160);
 
 // num_groups < 0: no shared prefixes.
 Layout make_layout(const vas_attn_dims* d, int64_t items_cap, int64_t partial_cap,
-                   int32_t num_groups = -1, int64_t pitems_cap = 0) {
+                   int32_t num_groups = -1) {
   Layout L;
   size_t off = align_up(sizeof(PlanHeader), 256);
-  L.row0 = L.shared = L.groups = L.pitems = 0;
-  L.pitems_cap = pitems_cap;
+  L.row0 = L.shared = L.entry = L.groups = 0;
   if (num_groups >= 0) {
     L.row0 = off;
     off = align_up(off + ((size_t)d->num_seqs + 1) * 4, 256);
@@ -2609,8 +2568,8 @@ Layout make_layout(const vas_attn_dims* d, int64_t items_cap, int64_t partial_ca
     off = align_up(off + (size_t)d->num_seqs * 4, 256);
     L.groups = off;
     off = align_up(off + (size_t)num_groups * sizeof(PrefixGroup), 256);
-    L.pitems = off;
-    off = align_up(off + (size_t)pitems_cap * sizeof(PrefixItem), 256);
+    L.entry = off;
+    off = align_up(off + (size_t)num_groups * 4, 256);
   }
   L.seqplan = off;
   off = align_up(off + (size_t)d->num_seqs * sizeof(SeqPlan), 256);
@@ -2632,27 +2591,19 @@ Layout make_layout(const vas_attn_dims* d, int64_t items_cap, int64_t partial_ca
   return L;
 }
 
-// Items of shared prefixes: every row block once, and what two waves of splits add.
-int64_t pitems_cap(const vas_attn_dims* d, int32_t num_groups, int sms) {
-  if (num_groups < 0) return 0;
-  const int64_t G = d->num_q_heads / d->num_kv_heads;
-  return num_groups + prefix_blocks(G * d->total_q_tokens) + 2LL * (sms > 0 ? sms : 160);
-}
-
 // Largest layout that fits ws_bytes (partial capacity grows with the workspace).
 bool fit_layout(const vas_attn_dims* d, size_t ws_bytes, Layout* out, int32_t num_groups = -1) {
   const int64_t imin = items_min(d);
   const int64_t icap_pref = imin + items_extra(num_sms());
-  const int64_t pcap_items = pitems_cap(d, num_groups, num_sms());
   for (int64_t icap : {icap_pref, imin}) {
-    const Layout base = make_layout(d, icap, 0, num_groups, pcap_items);
+    const Layout base = make_layout(d, icap, 0, num_groups);
     if (base.total > ws_bytes) continue;
     const size_t per_row = (size_t)(d->head_dim + 1) * 4;
     int64_t pcap = (int64_t)((ws_bytes - base.total) / per_row);
-    while (pcap > 0 && make_layout(d, icap, pcap, num_groups, pcap_items).total > ws_bytes) pcap -= 64;
+    while (pcap > 0 && make_layout(d, icap, pcap, num_groups).total > ws_bytes) pcap -= 64;
     if (pcap < 0) pcap = 0;
     if (pcap > INT32_MAX) pcap = INT32_MAX;
-    *out = make_layout(d, icap, pcap, num_groups, pcap_items);
+    *out = make_layout(d, icap, pcap, num_groups);
     return true;
   }
   return false;
@@ -2766,21 +2717,20 @@ size_t paged_attn_workspace_size(const vas_attn_dims* dims) {
 size_t paged_attn_prefix_workspace_min(const vas_attn_dims* dims, int32_t num_groups) {
   if (!dims_ok(dims) || !dims_supported(dims) || dims->kv_dtype == VAS_F32 || num_groups < 0)
     return 0;
-  return make_layout(dims, items_min(dims), 0, num_groups,
-                     pitems_cap(dims, num_groups, vas::num_sms()))
-      .total;
+  return make_layout(dims, items_min(dims), 0, num_groups).total;
 }
 
 size_t paged_attn_prefix_workspace_size(const vas_attn_dims* dims, int32_t num_groups) {
   if (!dims_ok(dims) || !dims_supported(dims) || dims->kv_dtype == VAS_F32 || num_groups < 0)
     return 0;
-  // Room for every row to be split 8 ways on average, and for the rows of two waves of
-  // shared-prefix units beside them.
+  // Room for every row to be split 8 ways on average and, beside that, for the pieces of
+  // shared prefixes: a CTA adds a piece to a block that others work on too, and a block's
+  // rows may have a partial or two that stay empty.
   const int sms = vas::num_sms();
-  const int64_t pcap = (int64_t)dims->total_q_tokens * dims->num_q_heads * 9 +
-                       2LL * (sms > 0 ? sms : 160) * kPrefixRows;
+  const int64_t rows = (int64_t)dims->total_q_tokens * dims->num_q_heads;
+  const int64_t pcap = rows * 11 + 4LL * (sms > 0 ? sms : 160) * kPrefixRows;
   return make_layout(dims, items_min(dims) + items_extra(sms), pcap < INT32_MAX ? pcap : INT32_MAX,
-                     num_groups, pitems_cap(dims, num_groups, sms))
+                     num_groups)
       .total;
 }
 
@@ -2866,8 +2816,7 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
   pa.row0 = reinterpret_cast<int32_t*>(ws + lay.row0);
   pa.shared = reinterpret_cast<int32_t*>(ws + lay.shared);
   pa.groups = reinterpret_cast<PrefixGroup*>(ws + lay.groups);
-  pa.pitems = reinterpret_cast<PrefixItem*>(ws + lay.pitems);
-  pa.pitems_cap = lay.pitems_cap;
+  pa.entry = reinterpret_cast<int32_t*>(ws + lay.entry);
   // Tensor maps first, so that the plan and the attention grid are launched back to back.
   CUtensorMap mk, mv;
   if (quant && (!encode_code_map(&mk, k_pages, dims) || !encode_code_map(&mv, v_pages, dims)))
@@ -2933,7 +2882,6 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
     px.seqplan = pa.seqplan;
     px.row0 = pa.row0;
     px.groups = pa.groups;
-    px.items = pa.pitems;
     px.header = pa.header;
     px.part_o = aa.part_o;
     px.part_lse = aa.part_lse;

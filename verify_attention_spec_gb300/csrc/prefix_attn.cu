@@ -48,6 +48,75 @@ __device__ __forceinline__ float kv_value(const void* base, size_t i) {
   }
 }
 
+// A piece of a block: what one CTA computes of it at a time.
+struct Piece {
+  PrefixGroup g;
+  int head, r0, rows;      // KV head, first row and rows of the block
+  int page_begin, n_tiles, tokens;  // of the group's shared pages
+  int part;                // the piece's partial ...
+  int empty;               // ... and how many behind it stay empty (O 0, lse -inf)
+};
+
+// The pieces of a CTA's share, in order.  Every warp walks them by itself.
+struct Pieces {
+  int64_t x, end, share;
+  int e;
+  __device__ __forceinline__ Pieces(const PrefixArgs& a, int lane) {
+    share = a.header->share;
+    x = (int64_t)blockIdx.x * share;
+    end = min(x + share, a.header->span);
+    e = 0;
+    // The last entry whose base is at or below x, 32 entries at a time.
+    const int n = a.header->n_groups;
+    for (int s = 0; s < n; s += 32) {
+      const uint32_t m = __ballot_sync(0xffffffffu, s + lane < n && a.groups[s + lane].base <= x);
+      if (m == 0) break;
+      e = s + 31 - __clz(m);
+      if (m != 0xffffffffu) break;
+    }
+  }
+  // False at the end of the share.  A group's span may end in one unit of padding.
+  __device__ __forceinline__ bool next(const PrefixArgs& a, Piece& p) {
+    while (x < end) {
+      p.g = a.groups[e];
+      const int64_t len = (int64_t)p.g.tiles * p.g.weight;
+      const int64_t local = x - p.g.base, block = local / len;
+      if (block >= p.g.blocks) {
+        ++e;
+        x = p.g.base + ((len * p.g.blocks + 1) & ~1ll);
+        continue;
+      }
+      const int64_t first = p.g.base + block * len, stop = min(end, first + len);
+      const int per_head = p.g.blocks / a.Hkv;
+      p.head = (int)(block / per_head);
+      p.r0 = (int)(block % per_head) * kPrefixRows;
+      p.rows = min(kPrefixRows, p.g.rows - p.r0);
+      const int t0 = (int)((x - first) / p.g.weight), t1 = (int)((stop - first) / p.g.weight);
+      p.page_begin = t0 * (kPrefixTile / a.P);
+      p.n_tiles = t1 - t0;
+      p.tokens = min(p.g.pages * a.P, t1 * kPrefixTile) - t0 * kPrefixTile;
+      p.part = (int)(blockIdx.x - first / share);
+      p.empty = stop == first + len ? p.g.parts - 1 - p.part : 0;
+      x = stop;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Partial row of row r of a group, for partial `part` of its shared pages.
+__device__ __forceinline__ size_t part_row(const PrefixArgs& a, const Piece& p, int r, int part) {
+  const int t = p.g.qrow0 + r / a.G;
+  const SeqPlan sp = a.seqplan[member_of(a, p.g, t)];
+  return partial_index(sp, a.Hkv, a.G, sp.nsplit - p.g.parts + part, p.head,
+                       (t - sp.qrow0) * a.G + r % a.G);
+}
+// Partial rows from one partial of a row to the next.
+__device__ __forceinline__ size_t part_step(const PrefixArgs& a, const Piece& p, int r) {
+  const int t = p.g.qrow0 + r / a.G;
+  return (size_t)a.Hkv * ((size_t)a.G * a.seqplan[member_of(a, p.g, t)].qlen);
+}
+
 // One warp per row, CUDA-core arithmetic.
 template <int D, int KV>
 __global__ void __launch_bounds__(256) prefix_simple_kernel(const PrefixArgs a) {
@@ -56,18 +125,15 @@ __global__ void __launch_bounds__(256) prefix_simple_kernel(const PrefixArgs a) 
   __shared__ float qs[8][D];
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  const int32_t n_units = a.header->n_prefix_items * a.Hkv;
-  for (int32_t u = blockIdx.x; u < n_units; u += gridDim.x) {
-    const PrefixItem it = a.items[u / a.Hkv];
-    const int head = u % a.Hkv;
-    const PrefixGroup g = a.groups[it.group];
-    const int split = it.split_rb >> kPrefixRbBits;
-    const int r0 = (it.split_rb & ((1 << kPrefixRbBits) - 1)) * kPrefixRows;
-    const int r1 = min(r0 + kPrefixRows, g.rows);
-    const int32_t* bt = a.block_table + (size_t)g.leader * a.maxp;
-    for (int r = r0 + warp; r < r1; r += 8) {
-      const int t = g.qrow0 + r / a.G;
-      const int hh = head * a.G + r % a.G;
+  if (a.header->n_groups == 0) return;
+  Pieces it(a, lane);
+  Piece x;
+  while (it.next(a, x)) {
+    const int32_t* bt = a.block_table + (size_t)x.g.leader * a.maxp + x.page_begin;
+    for (int rr = warp; rr < x.rows; rr += 8) {
+      const int r = x.r0 + rr;
+      const int t = x.g.qrow0 + r / a.G;
+      const int hh = x.head * a.G + r % a.G;
       const __nv_bfloat16* q =
           static_cast<const __nv_bfloat16*>(a.q) + ((size_t)t * a.Hq + hh) * D;
       __syncwarp();
@@ -75,21 +141,21 @@ __global__ void __launch_bounds__(256) prefix_simple_kernel(const PrefixArgs a) 
       __syncwarp();
       float acc[E] = {}, m = -INFINITY, l = 0.f;
       bool bad = false;
-      for (int x0 = it.page_begin * a.P; x0 < it.page_end * a.P; x0 += 32) {
-        const int x = x0 + lane;
+      for (int y0 = 0; y0 < x.tokens; y0 += 32) {
+        const int y = y0 + lane;
         int page = -1;
         float s = -INFINITY;
-        if (x < it.page_end * a.P) {
-          page = bt[x / a.P];
+        if (y < x.tokens) {
+          page = bt[y / a.P];
           if (page < 0 || page >= a.num_pages) {
             bad = true;
             page = -1;
           } else {
-            const size_t at = (((size_t)page * a.P + x % a.P) * a.Hkv + head) * D;
+            const size_t at = (((size_t)page * a.P + y % a.P) * a.Hkv + x.head) * D;
             float dot = 0.f;
             for (int d = 0; d < D; ++d) dot = fmaf(qs[warp][d], kv_value<KV>(a.k_pages, at + d), dot);
             if constexpr (KV != VAS_BF16)
-              dot *= a.k_scale[((size_t)page * a.Hkv + head) * a.P + x % a.P];
+              dot *= a.k_scale[((size_t)page * a.Hkv + x.head) * a.P + y % a.P];
             s = dot * a.scale_log2;
           }
         }
@@ -103,27 +169,30 @@ __global__ void __launch_bounds__(256) prefix_simple_kernel(const PrefixArgs a) 
         l = l * f + ps;
         m = mn;
         if constexpr (KV != VAS_BF16) {
-          if (page >= 0) p *= a.v_scale[((size_t)page * a.Hkv + head) * a.P + x % a.P];
+          if (page >= 0) p *= a.v_scale[((size_t)page * a.Hkv + x.head) * a.P + y % a.P];
         }
         for (int e = 0; e < E; ++e) acc[e] *= f;
-        for (int j = 0; j < 32 && x0 + j < it.page_end * a.P; ++j) {
+        for (int j = 0; j < 32 && y0 + j < x.tokens; ++j) {
           const float pj = __shfl_sync(0xffffffffu, p, j);
           const int pg = __shfl_sync(0xffffffffu, page, j);
           if (pg < 0) continue;
-          const size_t at = (((size_t)pg * a.P + (x0 + j) % a.P) * a.Hkv + head) * D;
+          const size_t at = (((size_t)pg * a.P + (y0 + j) % a.P) * a.Hkv + x.head) * D;
           for (int e = 0; e < E; ++e)
             acc[e] = fmaf(pj, kv_value<KV>(a.v_pages, at + lane + 32 * e), acc[e]);
         }
       }
       bad = __any_sync(0xffffffffu, bad);
-      const SeqPlan sp = a.seqplan[member_of(a, g, t)];
-      const size_t row = partial_index(sp, a.Hkv, a.G, sp.nsplit - g.nsplit + split, head,
-                                       (t - sp.qrow0) * a.G + r % a.G);
+      const size_t row = part_row(a, x, r, x.part);
       for (int e = 0; e < E; ++e)
         a.part_o[row * D + lane + 32 * e] = bad ? NAN : (l > 0.f ? acc[e] / l : 0.f);
       if (lane == 0) {
         a.part_lse[row] = bad ? NAN : (m + log2f(l)) * 0.6931471805599453f;
         if (bad) atomicOr(a.err, VAS_DEV_BAD_PAGE);
+      }
+      for (int k = 1; k <= x.empty; ++k) {
+        const size_t none = row + k * part_step(a, x, r);
+        for (int e = 0; e < E; ++e) a.part_o[none * D + lane + 32 * e] = 0.f;
+        if (lane == 0) a.part_lse[none] = -INFINITY;
       }
     }
   }
@@ -132,25 +201,27 @@ __global__ void __launch_bounds__(256) prefix_simple_kernel(const PrefixArgs a) 
 // ------------------------------------------------------------------------------------
 // bf16 pages: both products on tcgen05
 // ------------------------------------------------------------------------------------
-// A CTA takes one unit (a split of a group's shared pages, a block of up to 256 of its rows,
-// one KV head) at a time and walks the split in tiles of 128 tokens.  Two streams of
-// S = Q K^T, softmax, O += P V run against each other, so that the tensor cores compute one
-// stream's products while the other stream's 128 threads are in their softmax:
+// A CTA takes its pieces one at a time and walks each in tiles of 128 tokens.  Two streams
+// of S = Q K^T, softmax, O += P V run against each other, so that the tensor cores compute
+// one stream's products while the other stream's threads are in their softmax:
 //   more than 128 rows: stream s holds rows 128 s .. 128 s + 127, every tile feeds both;
 //   otherwise both hold the same rows and take the tiles in turn, and their two results are
-//   merged in shared memory at the end of the unit.
-// Thread r of a stream owns row r, which is TMEM lane r: its 128 scores come to registers, go
-// back as 64 columns of bf16 pairs over the first half of S, and are the A operand of the
-// second product from there, so P never passes through shared memory.  TMEM: S 2 x 128, O 2 x
-// D columns.  Shared memory: the query tiles and a ring of K and V tiles, 128-byte swizzled
-// as the TMA boxes land.  A producer warp streams the pages, an MMA warp issues.
-constexpr int kTile = 128;                  // tokens of a tile, rows of a stream
-constexpr int kStreamThreads = 128;
-constexpr int kProducerWarp = 8, kMmaWarp = 9;
-constexpr int kPrefixThreads = 384;  // two warps idle: registers move by groups of four warps
-// Registers a thread: what the launch gives (168) is split between the streams, whose 128
-// scores live in registers, and the other four warps.  256 x 200 + 128 x 80 = 384 x 160.
-constexpr int kStreamRegs = 200, kOtherRegs = 80, kLaunchRegs = 160;
+//   merged in shared memory at the end of the piece.
+// A stream is 256 threads: thread r of each half owns row r, TMEM lane r, with 64 of the
+// tile's 128 scores; the halves exchange their maxima through shared memory.  (With one
+// thread a row, two warps a scheduler left the issue slots 72 % idle and the tensor cores
+// at 40 %.)  The scores come to registers and go back as bf16 pairs over the first columns
+// of S, which are the A operand of the second product from there, so P never passes through
+// shared memory.  TMEM: S 2 x 128, O 2 x D columns.  Shared memory: the query tiles and a
+// ring of K and V tiles, 128-byte swizzled as the TMA boxes land.  A producer warp streams
+// the pages, an MMA warp issues.
+constexpr int kTile = kPrefixTile;          // tokens of a tile, rows of a stream
+constexpr int kStreamThreads = 256, kStreamWarps = kStreamThreads / 32;
+constexpr int kProducerWarp = 2 * kStreamWarps, kMmaWarp = kProducerWarp + 1;
+constexpr int kPrefixThreads = 640;  // two warps idle: registers move by groups of four warps
+// Registers a thread: what the launch gives is split between the streams, whose scores live
+// in registers, and the other four warps.
+constexpr int kStreamRegs = 104, kOtherRegs = 64, kLaunchRegs = 96;
 static_assert(2 * kStreamThreads * kStreamRegs + 128 * kOtherRegs <= kPrefixThreads * kLaunchRegs,
               "setmaxnreg draws on the registers of the launch");
 constexpr float kRebase = 8.f;  // a row's reference maximum may trail by this (log2 units)
@@ -162,11 +233,12 @@ struct PSmem {
   static constexpr int kTileBytes = kHalves * kHalfBytes;  // one operand of a tile, a query tile
   static constexpr int kSlots = D == 128 ? 5 : 8;
   static constexpr int kRingOff = 2 * kTileBytes;
-  static constexpr int kStatOff = kRingOff + kSlots * kTileBytes;  // m and l of stream 1
-  static constexpr int kBarOff = kStatOff + 2 * kTile * 4;
+  // [stream][half][row]: maxima, at the end of a piece the sums
+  static constexpr int kStatOff = kRingOff + kSlots * kTileBytes;
+  static constexpr int kBarOff = kStatOff + 4 * kTile * 4;
   // full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], q_full[2], fin | TMEM base
   static constexpr int kBytes = kBarOff + (2 * kSlots + 9) * 8 + 16;
-  static constexpr int kDynBytes = kBytes + 1024;  // to align the tiles
+  static constexpr int kDynBytes = kBytes;
   static_assert(kDynBytes <= 227 * 1024, "shared memory of one CTA");
   static_assert(kTile * D * 4 <= 2 * kTileBytes, "stream 1's O fits over the query tiles");
 };
@@ -194,47 +266,9 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* r) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_st64(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x64.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,"
-      "%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,"
-      "%58,%59,%60,%61,%62,%63,%64};\n\t"
-      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(r[32]), "r"(r[33]), "r"(r[34]), "r"(r[35]),
-      "r"(r[36]), "r"(r[37]), "r"(r[38]), "r"(r[39]), "r"(r[40]), "r"(r[41]), "r"(r[42]),
-      "r"(r[43]), "r"(r[44]), "r"(r[45]), "r"(r[46]), "r"(r[47]), "r"(r[48]), "r"(r[49]),
-      "r"(r[50]), "r"(r[51]), "r"(r[52]), "r"(r[53]), "r"(r[54]), "r"(r[55]), "r"(r[56]),
-      "r"(r[57]), "r"(r[58]), "r"(r[59]), "r"(r[60]), "r"(r[61]), "r"(r[62]), "r"(r[63])
-      : "memory");
-}
-
 // The warps beside the streams hand registers over (every warp of the group executes it).
 __device__ __forceinline__ void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-}
-
-// What a unit is, the same for every role.
-struct Unit {
-  PrefixItem it;
-  PrefixGroup g;
-  int head, r0, rows, n_tiles;
-  bool both;  // two row tiles: every tile feeds both streams
-};
-__device__ __forceinline__ Unit unit_of(const PrefixArgs& a, int32_t u) {
-  Unit x;
-  x.it = a.items[u / a.Hkv];
-  x.head = u % a.Hkv;
-  x.g = a.groups[x.it.group];
-  x.r0 = (x.it.split_rb & ((1 << kPrefixRbBits) - 1)) * kPrefixRows;
-  x.rows = min(kPrefixRows, x.g.rows - x.r0);
-  x.both = x.rows > kTile;
-  x.n_tiles = ((x.it.page_end - x.it.page_begin) * a.P + kTile - 1) / kTile;
-  return x;
 }
 
 template <int D, int P>
@@ -244,9 +278,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   using S = PSmem<D>;
   constexpr int kSlots = S::kSlots;
   constexpr int kPages = kTile / P;  // pages of a tile
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle counts from 1024 bytes
   uint8_t* ring = smem + S::kRingOff;
   float* stat = reinterpret_cast<float*>(smem + S::kStatOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBarOff);
@@ -266,9 +298,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
-      mbar_init(&p_full[s], 4);
+      mbar_init(&p_full[s], kStreamWarps);
       mbar_init(&o_full[s], 1);
-      mbar_init(&q_full[s], 4);
+      mbar_init(&q_full[s], kStreamWarps);
     }
     mbar_init(fin, 1);
     mbar_fence_init();
@@ -279,8 +311,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   }
   pdl_wait_prior_grid();  // the plan of this call is complete and visible
   pdl_launch_dependents();
-  const int32_t n_units = a.header->n_prefix_items * a.Hkv;
-  if ((int)blockIdx.x >= n_units) return;  // the whole CTA, before it holds anything
+  // The whole CTA, before it holds anything.
+  if (smem_u32(smem) & 1023) {
+    if (threadIdx.x == 0) atomicOr(a.err, VAS_DEV_TIMEOUT);
+    return;
+  }
+  if (a.header->n_groups == 0 || (int64_t)blockIdx.x * a.header->share >= a.header->span) return;
   if (warp == kMmaWarp) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
@@ -297,9 +333,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     static_assert(kPages * S::kHalves <= 32, "one box a lane");
     const uint64_t pol_once = l2_policy_evict_first(), pol_again = l2_policy_evict_normal();
     uint32_t fill = 0;
-    for (int32_t u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-      const Unit x = unit_of(a, u);
-      const int32_t* bt = a.block_table + (size_t)x.g.leader * a.maxp;
+    Pieces it(a, lane);
+    Piece x;
+    while (ok && it.next(a, x)) {
+      const bool both = x.rows > kTile;
+      const int32_t* bt = a.block_table + (size_t)x.g.leader * a.maxp + x.page_begin;
+      const int n_pages = x.tokens / P;
       const uint64_t pol = x.g.rows > kPrefixRows ? pol_again : pol_once;
       const int e_page = lane % kPages, e_half = lane / kPages;
       auto load = [&](const CUtensorMap* map, int tile) {
@@ -309,9 +348,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           ok = false;
           return;
         }
-        const int pg = x.it.page_begin + tile * kPages + e_page;
+        const int pg = tile * kPages + e_page;
         int32_t id = -1;
-        if (e_half < S::kHalves && pg < x.it.page_end) id = bt[pg];
+        if (e_half < S::kHalves && pg < n_pages) id = bt[pg];
         const bool mine = id >= 0 && id < a.num_pages;  // bad pages: the rows end as NaN
         const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
         if (lane == 0) mbar_arrive_expect_tx(&full[slot], boxes * (P * 128));
@@ -322,7 +361,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         __syncwarp();
         ++fill;
       };
-      const int lead = min(x.both ? 1 : 2, x.n_tiles);
+      const int lead = min(both ? 1 : 2, x.n_tiles);
       for (int t = 0; t < lead && ok; ++t) load(&tm_k, t);
       for (int j = 0; j < x.n_tiles && ok; ++j) {
         load(&tm_v, j);
@@ -388,15 +427,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       if (lane == 0) umma_commit(bar);
       __syncwarp();
     };
-    for (int32_t u = blockIdx.x; u < n_units && ok; u += gridDim.x, ++n_q) {
-      const Unit x = unit_of(a, u);
-      const int n = x.n_tiles;
-      const int all = (x.it.page_end - x.it.page_begin) * P;
+    Pieces it(a, lane);
+    Piece x;
+    for (; ok && it.next(a, x); ++n_q) {
+      const int n = x.n_tiles, all = x.tokens;
       for (int st = 0; st < 2 && ok; ++st) {
         ok = mbar_wait(&q_full[st], n_q & 1);
         ok = __all_sync(0xffffffffu, ok);
       }
-      if (x.both) {
+      if (x.rows > kTile) {
         landed(use);
         if (!ok) break;
         scores(0, use);
@@ -452,28 +491,33 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     // Tensor memory is freed only after every product this warp issued has completed.
     commit(fin);
     if (!mbar_wait(fin, 0)) ok = false;
-  } else if (warp < 2 * kStreamThreads / 32) {
+  } else if (warp < 2 * kStreamWarps) {
     // ------------------------------ softmax streams ------------------------------
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStreamRegs));
-    const int st = warp >> 2, row = threadIdx.x & (kStreamThreads - 1);
+    const int st = warp / kStreamWarps, half = (warp >> 2) & 1;
+    const int row = threadIdx.x & (kTile - 1), tid = threadIdx.x & (kStreamThreads - 1);
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t s_at = tmem_s + lanes + st * kTile, o_at = tmem_o + lanes + st * D;
+    const uint32_t s_at = tmem_s + lanes + st * kTile, o_at = tmem_o + lanes + st * D + half * (D / 2);
+    float* const my_stat = stat + (2 * st + half) * kTile + row;
+    const float* const other_stat = stat + (2 * st + 1 - half) * kTile + row;
     const float c = a.scale_log2;
     uint32_t n_s = 0, n_o = 0;
     auto wait = [&](uint64_t* bar, uint32_t phase) {
       if (ok) ok = mbar_wait_fast(bar, phase & 1);
       ok = __all_sync(0xffffffffu, ok);
     };
-    for (int32_t u = blockIdx.x; u < n_units; u += gridDim.x) {
-      const Unit x = unit_of(a, u);
-      const int base = x.r0 + (x.both ? st * kTile : 0);  // the stream's first row
-      const int rows = min(kTile, x.g.rows - base);
+    Pieces it(a, lane);
+    Piece x;
+    while (it.next(a, x)) {
+      const bool both = x.rows > kTile;
+      const int base = x.r0 + (both ? st * kTile : 0);  // the stream's first row
+      const int rows = min(kTile, x.r0 + x.rows - base);
       {
         // The query tile, K-major 128-byte swizzled.  Rows past the last keep whatever was
         // there: they feed only their own scores, which nobody reads.
         const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(a.q);
         uint8_t* qt = smem + st * S::kTileBytes;
-        for (int e = row; e < rows * (D / 8); e += kStreamThreads) {
+        for (int e = tid; e < rows * (D / 8); e += kStreamThreads) {
           const int r = e / (D / 8), gc = e % (D / 8);
           const int rr = base + r;
           const uint4 v = *reinterpret_cast<const uint4*>(
@@ -486,36 +530,39 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[st]);
       }
-      // Bad pages of the split: this thread looks at every 128th.
+      // Bad pages of the piece: this thread looks at every 256th.
       bool bad = false;
       {
-        const int32_t* bt = a.block_table + (size_t)x.g.leader * a.maxp;
-        for (int pg = x.it.page_begin + row; pg < x.it.page_end; pg += kStreamThreads) {
+        const int32_t* bt = a.block_table + (size_t)x.g.leader * a.maxp + x.page_begin;
+        for (int pg = tid; pg < x.tokens / P; pg += kStreamThreads) {
           const int32_t id = bt[pg];
           bad |= id < 0 || id >= a.num_pages;
         }
       }
-      const int all = (x.it.page_end - x.it.page_begin) * P;
-      const int n_mine = x.both ? x.n_tiles : (x.n_tiles - st + 1) / 2;
+      const int n_mine = both ? x.n_tiles : (x.n_tiles - st + 1) / 2;
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n_mine; ++i, ++n_s) {
-        const int tile = x.both ? i : 2 * i + st;
-        const int nv = min(kTile, all - tile * kTile);
+        const int tile = both ? i : 2 * i + st;
+        const int nv = min(kTile, x.tokens - tile * kTile) - 64 * half;  // valid of this half
         wait(&s_full[st], n_s);
         tc_fence_after();
-        uint32_t sr[kTile];
-        tmem_ld64(s_at, sr);
-        tmem_ld64(s_at + 64, sr + 64);
-        if (nv < kTile) {
+        uint32_t sr[64];
+        tmem_ld64(s_at + 64 * half, sr);
+        if (nv < 64) {
 #pragma unroll
-          for (int e = 0; e < kTile; ++e)
+          for (int e = 0; e < 64; ++e)
             if (e >= nv) sr[e] = __float_as_uint(-INFINITY);
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < kTile; e += 2)
+        for (int e = 0; e < 64; e += 2)
           mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;  // c > 0
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;  // c > 0
+        // The row's maximum over both halves.  (The next write of this tile's slot comes
+        // after the next s_full, so after every thread's read here.)
+        *my_stat = top;
+        named_bar_sync(1 + st, kStreamThreads);
+        top = fmaxf(top, *other_stat);
         const bool rebase = top > m + kRebase;
         const float alpha = rebase ? exp2f(m - top) : 1.f;
         if (rebase) {
@@ -524,7 +571,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
         if (__any_sync(0xffffffffu, rebase && i > 0)) {
 #pragma unroll 1
-          for (int cc = 0; cc < D; cc += 32) {
+          for (int cc = 0; cc < D / 2; cc += 32) {
             uint32_t ov[32];
             tmem_ld32(o_at + cc, ov);
 #pragma unroll
@@ -534,22 +581,24 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
         const float mu = m == -INFINITY ? 0.f : m;
         const uint64_t c2 = pair(c, c), mu2 = pair(-mu, -mu);
-        uint64_t sum[4] = {0, 0, 0, 0};
+        uint64_t sum[2] = {0, 0};
+        uint32_t p[32];
 #pragma unroll
-        for (int e = 0; e < kTile; e += 2) {
+        for (int e = 0; e < 64; e += 2) {
           float p0, p1;
           unpair(fma2(pair(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, mu2), p0, p1);
           p0 = ex2_approx(p0);
           p1 = ex2_approx(p1);
-          sum[(e >> 1) & 3] = add2(sum[(e >> 1) & 3], pair(p0, p1));
-          sr[e >> 1] = pack_bf16x2(p0, p1);
+          sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(p0, p1));
+          p[e >> 1] = pack_bf16x2(p0, p1);
         }
         {
           float lo, hi;
-          unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), lo, hi);
+          unpair(add2(sum[0], sum[1]), lo, hi);
           l += lo + hi;
         }
-        tmem_st64(s_at, sr);
+        // P lies over S: the halves' barrier above followed every thread's read of S.
+        tmem_st32(s_at + 32 * half, p);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[st]);
@@ -560,28 +609,30 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       }
       tc_fence_after();
       bad = named_bar_or(1 + st, kStreamThreads, bad);
+      *my_stat = l;
+      named_bar_sync(1 + st, kStreamThreads);
+      l += *other_stat;
 
-      // Results: normalised partial rows.
-      float* dump = reinterpret_cast<float*>(smem);  // [D][128 rows] over the query tiles
+      // Results: normalised partial rows; each half of a stream writes half of the columns.
+      float* dump = reinterpret_cast<float*>(smem) + half * (D / 2) * kTile;  // [D][128 rows]
       bool merge = false;
       float f0 = 1.f, f1 = 0.f;
-      if (!x.both) {
+      if (!both) {
         named_bar_sync(3, 2 * kStreamThreads);  // neither stream reads its query tile again
+        if (st == 1 && half == 0) stat[row] = m;  // stream 0 has exchanged its sums
         if (st == 1 && n_mine > 0) {
 #pragma unroll 1
-          for (int cc = 0; cc < D; cc += 32) {
+          for (int cc = 0; cc < D / 2; cc += 32) {
             uint32_t ov[32];
             tmem_ld32(o_at + cc, ov);
 #pragma unroll
             for (int e = 0; e < 32; ++e) dump[(cc + e) * kTile + row] = __uint_as_float(ov[e]);
           }
-          stat[row] = m;
-          stat[kTile + row] = l;
         }
         named_bar_sync(3, 2 * kStreamThreads);
         if (st == 0 && x.n_tiles > 1) {
           merge = true;
-          const float m1 = stat[row], l1 = stat[kTile + row];
+          const float m1 = stat[row], l1 = stat[2 * kTile + row] + stat[3 * kTile + row];
           const float mm = fmaxf(m, m1), mu = mm == -INFINITY ? 0.f : mm;
           f0 = exp2f(m - mu);
           f1 = exp2f(m1 - mu);
@@ -589,37 +640,41 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           m = mm;
         }
       }
-      if (x.both || st == 0) {
+      if (both || st == 0) {
         const int r = base + row;
         const bool mine = row < rows;
-        size_t at = 0;
-        if (mine) {
-          const int t = x.g.qrow0 + r / a.G;
-          const SeqPlan sp = a.seqplan[member_of(a, x.g, t)];
-          at = partial_index(sp, a.Hkv, a.G, sp.nsplit - x.g.nsplit + (x.it.split_rb >> kPrefixRbBits),
-                             x.head, (t - sp.qrow0) * a.G + r % a.G);
-        }
+        const size_t at = mine ? part_row(a, x, r, x.part) : 0;
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // l NaN: NaN
 #pragma unroll 1
-        for (int cc = 0; cc < D; cc += 32) {
+        for (int cc = 0; cc < D / 2; cc += 32) {
           uint32_t ov[32];
           tmem_ld32(o_at + cc, ov);
           if (!mine) continue;
-          float v[32];
+          float4* po = reinterpret_cast<float4*>(a.part_o + at * D + half * (D / 2) + cc);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float o = __uint_as_float(ov[e]);
-            if (merge) o = o * f0 + dump[(cc + e) * kTile + row] * f1;
-            v[e] = bad ? NAN : o * inv;
+          for (int e = 0; e < 8; ++e) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float o = __uint_as_float(ov[4 * e + k]);
+              if (merge) o = o * f0 + dump[(cc + 4 * e + k) * kTile + row] * f1;
+              v[k] = bad ? NAN : o * inv;
+            }
+            po[e] = make_float4(v[0], v[1], v[2], v[3]);
           }
-          float4* po = reinterpret_cast<float4*>(a.part_o + at * D + cc);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) po[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
-        if (mine) a.part_lse[at] = bad ? NAN : (m + log2f(l)) * 0.6931471805599453f;
+        if (mine && half == 0) a.part_lse[at] = bad ? NAN : (m + log2f(l)) * 0.6931471805599453f;
+        if (mine && x.empty > 0) {
+          const size_t step = part_step(a, x, r);
+          for (int k = 1; k <= x.empty; ++k) {
+            float4* po = reinterpret_cast<float4*>(a.part_o + (at + k * step) * D + half * (D / 2));
+            for (int e = 0; e < D / 8; ++e) po[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (half == 0) a.part_lse[at + k * step] = -INFINITY;
+          }
+        }
       }
-      if (bad && row == 0 && st == 0) atomicOr(a.err, VAS_DEV_BAD_PAGE);
-      if (!x.both) named_bar_sync(3, 2 * kStreamThreads);  // the dump is read: Q may be staged
+      if (bad && tid == 0 && st == 0) atomicOr(a.err, VAS_DEV_BAD_PAGE);
+      if (!both) named_bar_sync(3, 2 * kStreamThreads);  // the dump is read: Q may be staged
     }
   } else {
     give_registers();
@@ -694,7 +749,7 @@ int launch_prefix(const CUtensorMap& mk, const CUtensorMap& mv, const PrefixArgs
       return a.P == 16 ? launch_tc<128, 16>(mk, mv, a, stream) : launch_tc<128, 32>(mk, mv, a, stream);
     return a.P == 16 ? launch_tc<64, 16>(mk, mv, a, stream) : launch_tc<64, 32>(mk, mv, a, stream);
   }
-  const int grid = 4 * num_sms();
+  const int grid = num_sms();
   if (head_dim == 128) {
     if (kv_dtype == VAS_FP8_E4M3)
       return launch(prefix_simple_kernel<128, VAS_FP8_E4M3>, a, grid, 256, stream);
