@@ -565,11 +565,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
           }
         }
       }
-      // Arrival counters of the last-split merge; the shared pages' partials are there
-      // before the first of the sequence's own splits starts.
+      // Arrival counters of the last-split merge.  Behind a shared prefix no split is the
+      // last (the count never gets to nsplit - 1): merge_shared_kernel merges those rows.
       if (sp.nsplit > 1)
-        for (int k = 0; k < s.nrb * a.Hkv; ++k)
-          a.counters[(size_t)sp.item0 * a.Hkv + k] = s.parts;
+        for (int k = 0; k < s.nrb * a.Hkv; ++k) a.counters[(size_t)sp.item0 * a.Hkv + k] = 0;
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) carry[k] += t[k];
@@ -1138,95 +1137,138 @@ __device__ __forceinline__ size_t partial_row(const AttnArgs& a, const SeqPlan& 
   return partial_index(sp, a.Hkv, a.G, split, head, r);
 }
 
-// Merge the partials of every split of rows r0 .. r0+Rb-1 of one KV head (the caller is
-// the last split to finish: all partials are in memory).  Four consumer warps, each
-// kMergeRows rows at a time: the lses of all of them are loaded together (lane s holds
-// split s), then their O rows, so a row costs its share of two round trips to L2 and not
-// two for every split.  (One row and one split at a time took 40 us for 40 rows of ten
-// splits, as a window behind a long shared prefix has them.)  Every sum keeps the order of
-// the splits.
-constexpr int kMergeRows = 2;
-template <int D>
-__device__ void merge_splits(const AttnArgs& a, const SeqPlan& sp, int head, int r0, int Rb,
-                             int warp, int lane) {
+// Merge ROWS rows of one KV head of a sequence, r, r + 1, ... (rows past r_end repeat the
+// last and are not written), over all of their partials; one warp.  The lses of all rows
+// are loaded together (lane s holds split s), then their O rows, so a row costs its share
+// of two round trips to L2 and not two for every split.  Sums keep the order of the splits.
+template <int D, int ROWS>
+__device__ __forceinline__ void merge_rows(const AttnArgs& a, const SeqPlan& sp, int head, int r,
+                                           int r_end, int lane) {
   constexpr int E = D / 32;
   const float kLn2 = 0.6931471805599453f;
   const int n = sp.nsplit;
   const size_t step = (size_t)a.Hkv * ((size_t)a.G * sp.qlen);  // partial rows of a split
-  for (int rr = warp * kMergeRows; rr < Rb; rr += kConsumerWarps * kMergeRows) {
-    size_t row[kMergeRows];  // rows past the last repeat it and are not written
-    float mu[kMergeRows], first[kMergeRows], wsum[kMergeRows], acc[kMergeRows][E];
-    bool bad[kMergeRows];
+  size_t row[ROWS];
+  float mu[ROWS], first[ROWS], wsum[ROWS], acc[ROWS][E];
+  bool bad[ROWS];
 #pragma unroll
-    for (int k = 0; k < kMergeRows; ++k) {
-      row[k] = partial_row(a, sp, 0, head, r0 + min(rr + k, Rb - 1));
-      first[k] = lane < n ? __ldcg(a.part_lse + row[k] + lane * step) : -INFINITY;
+  for (int k = 0; k < ROWS; ++k) {
+    row[k] = partial_row(a, sp, 0, head, min(r + k, r_end - 1));
+    first[k] = lane < n ? __ldcg(a.part_lse + row[k] + lane * step) : -INFINITY;
+  }
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    float mx = fmaxf(first[k], -INFINITY);
+    bad[k] = isnan(first[k]);
+    for (int s = lane + 32; s < n; s += 32) {
+      const float v = __ldcg(a.part_lse + row[k] + s * step);
+      bad[k] |= isnan(v);
+      mx = fmaxf(mx, v);
     }
 #pragma unroll
-    for (int k = 0; k < kMergeRows; ++k) {
-      float mx = fmaxf(first[k], -INFINITY);
-      bad[k] = isnan(first[k]);
-      for (int s = lane + 32; s < n; s += 32) {
-        const float v = __ldcg(a.part_lse + row[k] + s * step);
-        bad[k] |= isnan(v);
-        mx = fmaxf(mx, v);
-      }
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    bad[k] = __any_sync(0xffffffffu, bad[k]);
+    mu[k] = mx == -INFINITY ? 0.f : mx;
+    wsum[k] = 0.f;
 #pragma unroll
-      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      bad[k] = __any_sync(0xffffffffu, bad[k]);
-      mu[k] = mx == -INFINITY ? 0.f : mx;
-      wsum[k] = 0.f;
+    for (int e = 0; e < E; ++e) acc[k][e] = 0.f;
+  }
+  for (int s0 = 0; s0 < n; s0 += 32) {
+    float w[ROWS];
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[k][e] = 0.f;
+    for (int k = 0; k < ROWS; ++k) {
+      const float v = s0 == 0 ? first[k]
+                              : (s0 + lane < n ? __ldcg(a.part_lse + row[k] + (s0 + lane) * step)
+                                               : -INFINITY);
+      w[k] = exp2f((v - mu[k]) * 1.4426950408889634f);
     }
-    for (int s0 = 0; s0 < n; s0 += 32) {
-      float w[kMergeRows];
-#pragma unroll
-      for (int k = 0; k < kMergeRows; ++k) {
-        const float v = s0 == 0 ? first[k]
-                                : (s0 + lane < n ? __ldcg(a.part_lse + row[k] + (s0 + lane) * step)
-                                                 : -INFINITY);
-        w[k] = exp2f((v - mu[k]) * 1.4426950408889634f);
-      }
 #pragma unroll 4
-      for (int s = s0; s < min(n, s0 + 32); ++s) {
-        float4 v[kMergeRows];
+    for (int s = s0; s < min(n, s0 + 32); ++s) {
+      float4 v[ROWS];
 #pragma unroll
-        for (int k = 0; k < kMergeRows; ++k) {
-          const float* po = a.part_o + (row[k] + s * step) * D + lane * E;
-          if constexpr (E == 4) {
-            v[k] = __ldcg(reinterpret_cast<const float4*>(po));
-          } else {
-            const float2 h = __ldcg(reinterpret_cast<const float2*>(po));
-            v[k] = make_float4(h.x, h.y, 0.f, 0.f);
-          }
+      for (int k = 0; k < ROWS; ++k) {
+        const float* po = a.part_o + (row[k] + s * step) * D + lane * E;
+        if constexpr (E == 4) {
+          v[k] = __ldcg(reinterpret_cast<const float4*>(po));
+        } else {
+          const float2 h = __ldcg(reinterpret_cast<const float2*>(po));
+          v[k] = make_float4(h.x, h.y, 0.f, 0.f);
         }
+      }
 #pragma unroll
-        for (int k = 0; k < kMergeRows; ++k) {
-          const float ws = __shfl_sync(0xffffffffu, w[k], s - s0);
-          wsum[k] += ws;
-          acc[k][0] = fmaf(ws, v[k].x, acc[k][0]);
-          acc[k][1] = fmaf(ws, v[k].y, acc[k][1]);
-          if constexpr (E == 4) {
-            acc[k][2] = fmaf(ws, v[k].z, acc[k][2]);
-            acc[k][3] = fmaf(ws, v[k].w, acc[k][3]);
-          }
+      for (int k = 0; k < ROWS; ++k) {
+        const float ws = __shfl_sync(0xffffffffu, w[k], s - s0);
+        wsum[k] += ws;
+        acc[k][0] = fmaf(ws, v[k].x, acc[k][0]);
+        acc[k][1] = fmaf(ws, v[k].y, acc[k][1]);
+        if constexpr (E == 4) {
+          acc[k][2] = fmaf(ws, v[k].z, acc[k][2]);
+          acc[k][3] = fmaf(ws, v[k].w, acc[k][3]);
         }
       }
     }
+  }
 #pragma unroll
-    for (int k = 0; k < kMergeRows; ++k) {
-      if (rr + k >= Rb) break;
-      const float inv = 1.f / wsum[k];
-      const size_t orow = out_row(a, sp, head, r0 + rr + k);
-      __nv_bfloat16* og = static_cast<__nv_bfloat16*>(a.out) + orow * D + lane * E;
+  for (int k = 0; k < ROWS; ++k) {
+    if (r + k >= r_end) break;
+    const float inv = 1.f / wsum[k];
+    const size_t orow = out_row(a, sp, head, r + k);
+    __nv_bfloat16* og = static_cast<__nv_bfloat16*>(a.out) + orow * D + lane * E;
 #pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float x0 = bad[k] ? NAN : acc[k][e] * inv, x1 = bad[k] ? NAN : acc[k][e + 1] * inv;
-        *reinterpret_cast<uint32_t*>(og + e) = pack_bf16x2(x0, x1);
-      }
-      if (lane == 0) a.lse[orow] = bad[k] ? NAN : mu[k] + log2f(wsum[k]) * kLn2;
+    for (int e = 0; e < E; e += 2) {
+      const float x0 = bad[k] ? NAN : acc[k][e] * inv, x1 = bad[k] ? NAN : acc[k][e + 1] * inv;
+      *reinterpret_cast<uint32_t*>(og + e) = pack_bf16x2(x0, x1);
     }
+    if (lane == 0) a.lse[orow] = bad[k] ? NAN : mu[k] + log2f(wsum[k]) * kLn2;
+  }
+}
+
+// Merge the partials of every split of rows r0 .. r0+Rb-1 of one KV head (the caller is
+// the last split to finish: all partials are in memory).  Four consumer warps, two rows at
+// a time (more would cost the kernel register spills).
+constexpr int kMergeRows = 2;
+template <int D>
+__device__ void merge_splits(const AttnArgs& a, const SeqPlan& sp, int head, int r0, int Rb,
+                             int warp, int lane) {
+  for (int rr = warp * kMergeRows; rr < Rb; rr += kConsumerWarps * kMergeRows)
+    merge_rows<D, kMergeRows>(a, sp, head, r0 + rr, r0 + Rb, lane);
+}
+
+// Merge of the sequences with a shared prefix, whose rows all have partials: a warp takes
+// kSharedRows consecutive query heads of a token at a time.  On its own because the rows are
+// many and their partials few: merged by the last split in attn_bf16_kernel, four warps an
+// SM, 640 tokens of 64 heads behind a shared prefix cost that kernel 109 us (179 against
+// 70); bounded by the partials' bytes.
+constexpr int kSharedRows = 4;
+template <int D>
+__global__ void __launch_bounds__(256) merge_shared_kernel(const AttnArgs a, const int32_t* row0,
+                                                           const int32_t* shared, int B) {
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  if (a.header->n_groups == 0) return;
+  const int lane = threadIdx.x & 31;
+  // Tasks: (token, KV head, kSharedRows of its G query heads).
+  const uint32_t per_head = (a.G + kSharedRows - 1) / kSharedRows;
+  const uint32_t per_token = per_head * a.Hkv;
+  const uint64_t n_tasks = (uint64_t)a.T * per_token;
+  const uint64_t stride = (uint64_t)gridDim.x * (blockDim.x >> 5);
+  for (uint64_t w = (uint64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < n_tasks;
+       w += stride) {
+    const int t = (int)(n_tasks <= 0xffffffffu ? (uint32_t)w / per_token : w / per_token);
+    const uint32_t part = (uint32_t)(w - (uint64_t)t * per_token);
+    if (t >= row0[B]) return;  // rows that no sequence owns
+    int lo = 0, hi = B - 1;  // the last sequence whose first token is at or below t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (row0[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    if (shared[lo] < 0) continue;
+    const SeqPlan sp = a.seqplan[lo];
+    if (sp.nsplit < 2) continue;
+    const int j = t - sp.qrow0, h0 = (int)(part % per_head) * kSharedRows;
+    merge_rows<D, kSharedRows>(a, sp, (int)(part / per_head), j * a.G + h0,
+                               j * a.G + min(a.G, h0 + kSharedRows), lane);
   }
 }
 
@@ -2745,6 +2787,28 @@ struct PrefixCall {
   int32_t num_groups;
 };
 
+// Rows behind shared prefixes, after the attention of the call.
+template <int D>
+int launch_merge(const AttnArgs& aa, const PlanArgs& pa, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  const int64_t tasks = (int64_t)aa.T * aa.Hkv * ((aa.G + kSharedRows - 1) / kSharedRows);
+  const int64_t blocks = (tasks + 7) / 8, most = 8LL * pa.sms;
+  cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, merge_shared_kernel<D>, aa, (const int32_t*)pa.row0,
+                         (const int32_t*)pa.shared, (int)pa.B) != cudaSuccess) {
+    cudaGetLastError();
+    return VAS_E_CUDA;
+  }
+  return VAS_OK;
+}
+
 int attn_launch(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
                 const float* v_scale, const int32_t* block_table, const int32_t* seq_lens,
                 const int32_t* query_lens, const uint64_t* tree_mask, void* out, float* lse,
@@ -2900,28 +2964,32 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
     if (st != VAS_OK) return st;
   }
 
-  if (quant) {
-    const int grid = sms;
-    const bool fp8 = d.kv_dtype == VAS_FP8_E4M3;
-    if (d.head_dim == 128 && d.page_size == 16)
-      return fp8 ? launch_bf16<128, 16, kKvFp8>(mk, mv, aa, grid, stream)
-                 : launch_bf16<128, 16, kKvInt8>(mk, mv, aa, grid, stream);
-    if (d.head_dim == 128)
-      return fp8 ? launch_bf16<128, 32, kKvFp8>(mk, mv, aa, grid, stream)
-                 : launch_bf16<128, 32, kKvInt8>(mk, mv, aa, grid, stream);
-    if (d.page_size == 16)
-      return fp8 ? launch_bf16<64, 16, kKvFp8>(mk, mv, aa, grid, stream)
-                 : launch_bf16<64, 16, kKvInt8>(mk, mv, aa, grid, stream);
-    return fp8 ? launch_bf16<64, 32, kKvFp8>(mk, mv, aa, grid, stream)
-               : launch_bf16<64, 32, kKvInt8>(mk, mv, aa, grid, stream);
-  }
   if (bf16) {
     const int grid = sms;
-    if (d.head_dim == 128 && d.page_size == 16)
-      return launch_bf16<128, 16, kKvBf16>(mk, mv, aa, grid, stream);
-    if (d.head_dim == 128) return launch_bf16<128, 32, kKvBf16>(mk, mv, aa, grid, stream);
-    if (d.page_size == 16) return launch_bf16<64, 16, kKvBf16>(mk, mv, aa, grid, stream);
-    return launch_bf16<64, 32, kKvBf16>(mk, mv, aa, grid, stream);
+    int st;
+    if (quant) {
+      const bool fp8 = d.kv_dtype == VAS_FP8_E4M3;
+      if (d.head_dim == 128 && d.page_size == 16)
+        st = fp8 ? launch_bf16<128, 16, kKvFp8>(mk, mv, aa, grid, stream)
+                 : launch_bf16<128, 16, kKvInt8>(mk, mv, aa, grid, stream);
+      else if (d.head_dim == 128)
+        st = fp8 ? launch_bf16<128, 32, kKvFp8>(mk, mv, aa, grid, stream)
+                 : launch_bf16<128, 32, kKvInt8>(mk, mv, aa, grid, stream);
+      else if (d.page_size == 16)
+        st = fp8 ? launch_bf16<64, 16, kKvFp8>(mk, mv, aa, grid, stream)
+                 : launch_bf16<64, 16, kKvInt8>(mk, mv, aa, grid, stream);
+      else
+        st = fp8 ? launch_bf16<64, 32, kKvFp8>(mk, mv, aa, grid, stream)
+                 : launch_bf16<64, 32, kKvInt8>(mk, mv, aa, grid, stream);
+    } else if (d.head_dim == 128) {
+      st = d.page_size == 16 ? launch_bf16<128, 16, kKvBf16>(mk, mv, aa, grid, stream)
+                             : launch_bf16<128, 32, kKvBf16>(mk, mv, aa, grid, stream);
+    } else {
+      st = d.page_size == 16 ? launch_bf16<64, 16, kKvBf16>(mk, mv, aa, grid, stream)
+                             : launch_bf16<64, 32, kKvBf16>(mk, mv, aa, grid, stream);
+    }
+    if (st != VAS_OK || !prefix) return st;
+    return d.head_dim == 128 ? launch_merge<128>(aa, pa, stream) : launch_merge<64>(aa, pa, stream);
   }
   const int grid = 4 * sms;
   if (d.head_dim == 128) attn_f32_kernel<128><<<grid, 128, 0, stream>>>(aa);
