@@ -1093,26 +1093,6 @@ __device__ __forceinline__ float chunk_p_row(const uint32_t (&sr)[32], uint32_t 
   return (s4[0] + s4[1]) + (s4[2] + s4[3]);
 }
 
-// ---- quantised pools: the unit's Q in f16 ----------------------------------------------
-// Largest magnitude of eight bf16 values.
-__device__ __forceinline__ float absmax_bf16x8(uint4 v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(bf16_lo_f32(w[i])), fabsf(bf16_hi_f32(w[i]))));
-  return m;
-}
-// Eight bf16 values times mul (a power of two), as f16 (exact unless below the f16
-// normal range).
-__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v, float mul) {
-  uint4 r;
-  r.x = pack_f16x2(bf16_lo_f32(v.x) * mul, bf16_hi_f32(v.x) * mul);
-  r.y = pack_f16x2(bf16_lo_f32(v.y) * mul, bf16_hi_f32(v.y) * mul);
-  r.z = pack_f16x2(bf16_lo_f32(v.z) * mul, bf16_hi_f32(v.z) * mul);
-  r.w = pack_f16x2(bf16_lo_f32(v.w) * mul, bf16_hi_f32(v.w) * mul);
-  return r;
-}
-
 // ---- unit classification ------------------------------------------------------------
 // Draft-tree units: sequences with 2..64 query tokens when a tree is given; longer
 // query windows (prompt chunks) and decode rows keep the causal window.

@@ -9,12 +9,12 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/vas.h"
 #include "attn_plan.cuh"
@@ -35,17 +35,6 @@ __device__ __forceinline__ int member_of(const PrefixArgs& a, const PrefixGroup&
     else hi = mid - 1;
   }
   return lo;
-}
-
-template <int KV>
-__device__ __forceinline__ float kv_value(const void* base, size_t i) {
-  if constexpr (KV == VAS_BF16) {
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
-  } else if constexpr (KV == VAS_FP8_E4M3) {
-    return static_cast<float>(static_cast<const __nv_fp8_e4m3*>(base)[i]);
-  } else {
-    return static_cast<float>(static_cast<const int8_t*>(base)[i]);
-  }
 }
 
 // A piece of a block: what one CTA computes of it at a time.
@@ -117,89 +106,8 @@ __device__ __forceinline__ size_t part_step(const PrefixArgs& a, const Piece& p,
   return (size_t)a.Hkv * ((size_t)a.G * a.seqplan[member_of(a, p.g, t)].qlen);
 }
 
-// One warp per row, CUDA-core arithmetic.
-template <int D, int KV>
-__global__ void __launch_bounds__(256) prefix_simple_kernel(const PrefixArgs a) {
-  constexpr int E = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ float qs[8][D];
-  pdl_wait_prior_grid();
-  pdl_launch_dependents();
-  if (a.header->n_groups == 0) return;
-  Pieces it(a, lane);
-  Piece x;
-  while (it.next(a, x)) {
-    const int32_t* bt = a.block_table + (size_t)x.g.leader * a.maxp + x.page_begin;
-    for (int rr = warp; rr < x.rows; rr += 8) {
-      const int r = x.r0 + rr;
-      const int t = x.g.qrow0 + r / a.G;
-      const int hh = x.head * a.G + r % a.G;
-      const __nv_bfloat16* q =
-          static_cast<const __nv_bfloat16*>(a.q) + ((size_t)t * a.Hq + hh) * D;
-      __syncwarp();
-      for (int e = 0; e < E; ++e) qs[warp][lane + 32 * e] = __bfloat162float(q[lane + 32 * e]);
-      __syncwarp();
-      float acc[E] = {}, m = -INFINITY, l = 0.f;
-      bool bad = false;
-      for (int y0 = 0; y0 < x.tokens; y0 += 32) {
-        const int y = y0 + lane;
-        int page = -1;
-        float s = -INFINITY;
-        if (y < x.tokens) {
-          page = bt[y / a.P];
-          if (page < 0 || page >= a.num_pages) {
-            bad = true;
-            page = -1;
-          } else {
-            const size_t at = (((size_t)page * a.P + y % a.P) * a.Hkv + x.head) * D;
-            float dot = 0.f;
-            for (int d = 0; d < D; ++d) dot = fmaf(qs[warp][d], kv_value<KV>(a.k_pages, at + d), dot);
-            if constexpr (KV != VAS_BF16)
-              dot *= a.k_scale[((size_t)page * a.Hkv + x.head) * a.P + y % a.P];
-            s = dot * a.scale_log2;
-          }
-        }
-        float mx = s;
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(m - mu);
-        float p = exp2f(s - mu);
-        float ps = p;
-        for (int o = 16; o; o >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, o);
-        l = l * f + ps;
-        m = mn;
-        if constexpr (KV != VAS_BF16) {
-          if (page >= 0) p *= a.v_scale[((size_t)page * a.Hkv + x.head) * a.P + y % a.P];
-        }
-        for (int e = 0; e < E; ++e) acc[e] *= f;
-        for (int j = 0; j < 32 && y0 + j < x.tokens; ++j) {
-          const float pj = __shfl_sync(0xffffffffu, p, j);
-          const int pg = __shfl_sync(0xffffffffu, page, j);
-          if (pg < 0) continue;
-          const size_t at = (((size_t)pg * a.P + (y0 + j) % a.P) * a.Hkv + x.head) * D;
-          for (int e = 0; e < E; ++e)
-            acc[e] = fmaf(pj, kv_value<KV>(a.v_pages, at + lane + 32 * e), acc[e]);
-        }
-      }
-      bad = __any_sync(0xffffffffu, bad);
-      const size_t row = part_row(a, x, r, x.part);
-      for (int e = 0; e < E; ++e)
-        a.part_o[row * D + lane + 32 * e] = bad ? NAN : (l > 0.f ? acc[e] / l : 0.f);
-      if (lane == 0) {
-        a.part_lse[row] = bad ? NAN : (m + log2f(l)) * 0.6931471805599453f;
-        if (bad) atomicOr(a.err, VAS_DEV_BAD_PAGE);
-      }
-      for (int k = 1; k <= x.empty; ++k) {
-        const size_t none = row + k * part_step(a, x, r);
-        for (int e = 0; e < E; ++e) a.part_o[none * D + lane + 32 * e] = 0.f;
-        if (lane == 0) a.part_lse[none] = -INFINITY;
-      }
-    }
-  }
-}
-
 // ------------------------------------------------------------------------------------
-// bf16 pages: both products on tcgen05
+// The kernel: both products on tcgen05
 // ------------------------------------------------------------------------------------
 // A CTA takes its pieces one at a time and walks each in tiles of 128 tokens.  Two streams
 // of S = Q K^T, softmax, O += P V run against each other, so that the tensor cores compute
@@ -215,6 +123,12 @@ __global__ void __launch_bounds__(256) prefix_simple_kernel(const PrefixArgs a) 
 // shared memory.  TMEM: S 2 x 128, O 2 x D columns.  Shared memory: the query tiles and a
 // ring of K and V tiles, 128-byte swizzled as the TMA boxes land.  A producer warp streams
 // the pages, an MMA warp issues.
+//
+// Quantised pages (KV: VAS_FP8_E4M3, VAS_INT8): the producer lands a tile's codes beside its
+// 16-bit slot (with 128-wide heads in the upper half of it) and the scales of its tokens with
+// the V codes; two converter warps expand the codes, exact in f16, into the slot.  Products
+// are f16 (Q scaled into range by a power of two where it must be); scores are multiplied by
+// the K scale of their token, P by its V scale.
 constexpr int kTile = kPrefixTile;          // tokens of a tile, rows of a stream
 constexpr int kStreamThreads = 256, kStreamWarps = kStreamThreads / 32;
 constexpr int kProducerWarp = 2 * kStreamWarps, kMmaWarp = kProducerWarp + 1;
@@ -226,44 +140,78 @@ static_assert(2 * kStreamThreads * kStreamRegs + 128 * kOtherRegs <= kPrefixThre
               "setmaxnreg draws on the registers of the launch");
 constexpr float kRebase = 8.f;  // a row's reference maximum may trail by this (log2 units)
 
-template <int D>
+template <int D, int KV>
 struct PSmem {
+  static constexpr bool kQuant = KV != VAS_BF16;
   static constexpr int kHalves = D / 64;
   static constexpr int kHalfBytes = kTile * 128;
   static constexpr int kTileBytes = kHalves * kHalfBytes;  // one operand of a tile, a query tile
-  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kSlots = kQuant ? (D == 128 ? 4 : 6) : (D == 128 ? 5 : 8);
   static constexpr int kRingOff = 2 * kTileBytes;
+  // Codes [128 tokens][D]: a token's 128 codes lie where the second half of its row goes, so
+  // a row is expanded in place; its 64 codes have a place of their own.
+  static constexpr int kCodeOff = kRingOff + (D == 128 ? kHalfBytes : kSlots * kTileBytes);
+  static constexpr int kCodeStep = D == 128 ? kTileBytes : kTile * 64;
+  // [slot] K scales, V scales of the tile whose V the slot holds
+  static constexpr int kScaleOff =
+      kRingOff + kSlots * (kTileBytes + (kQuant && D == 64 ? kTile * 64 : 0));
   // [stream][half][row]: maxima, at the end of a piece the sums
-  static constexpr int kStatOff = kRingOff + kSlots * kTileBytes;
+  static constexpr int kStatOff = kScaleOff + (kQuant ? kSlots * 2 * kTile * 4 : 0);
   static constexpr int kBarOff = kStatOff + 4 * kTile * 4;
-  // full[kSlots], empty[kSlots], s_full[2], p_full[2], o_full[2], q_full[2], fin | TMEM base
-  static constexpr int kBytes = kBarOff + (2 * kSlots + 9) * 8 + 16;
-  static constexpr int kDynBytes = kBytes;
+  // full[kSlots], empty[kSlots], ready[kSlots], s_full[2], p_full[2], o_full[2], q_full[2],
+  // fin | TMEM base
+  static constexpr int kDynBytes = kBarOff + (3 * kSlots + 9) * 8 + 16;
   static_assert(kDynBytes <= 227 * 1024, "shared memory of one CTA");
   static_assert(kTile * D * 4 <= 2 * kTileBytes, "stream 1's O fits over the query tiles");
 };
 
-// 64 columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t* r) {
+// 64 columns of this thread's lane, as two groups of 32.
+__device__ __forceinline__ void tmem_ld2x32(uint32_t taddr, uint32_t (&x)[32], uint32_t (&y)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,"
-      "%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,"
-      "%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
+      "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]),
-        "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]),
-        "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]),
-        "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]),
-        "=r"(r[62]), "=r"(r[63])
-      : "r"(taddr)
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]),
+        "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]),
+        "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]),
+        "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]),
+        "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), "=r"(x[29]),
+        "=r"(x[30]), "=r"(x[31]),
+        "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]), "=r"(y[4]), "=r"(y[5]),
+        "=r"(y[6]), "=r"(y[7]), "=r"(y[8]), "=r"(y[9]), "=r"(y[10]), "=r"(y[11]),
+        "=r"(y[12]), "=r"(y[13]), "=r"(y[14]), "=r"(y[15]), "=r"(y[16]), "=r"(y[17]),
+        "=r"(y[18]), "=r"(y[19]), "=r"(y[20]), "=r"(y[21]), "=r"(y[22]), "=r"(y[23]),
+        "=r"(y[24]), "=r"(y[25]), "=r"(y[26]), "=r"(y[27]), "=r"(y[28]), "=r"(y[29]),
+        "=r"(y[30]), "=r"(y[31])
+      : "r"(taddr), "r"(taddr + 32)
       : "memory");
+}
+
+// 16 columns of this thread's lane, not waited for.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&x)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]),
+        "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]),
+        "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// 32 scores times the K scales of their tokens.
+__device__ __forceinline__ void scale32(uint32_t (&s)[32], const float* k) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(k + e);
+    s[e] = __float_as_uint(__uint_as_float(s[e]) * v.x);
+    s[e + 1] = __float_as_uint(__uint_as_float(s[e + 1]) * v.y);
+    s[e + 2] = __float_as_uint(__uint_as_float(s[e + 2]) * v.z);
+    s[e + 3] = __float_as_uint(__uint_as_float(s[e + 3]) * v.w);
+  }
 }
 
 // The warps beside the streams hand registers over (every warp of the group executes it).
@@ -271,11 +219,12 @@ __device__ __forceinline__ void give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
 }
 
-template <int D, int P>
+template <int D, int P, int KV>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
     prefix_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const PrefixArgs a) {
-  using S = PSmem<D>;
+  using S = PSmem<D, KV>;
+  constexpr bool kQuant = S::kQuant;
   constexpr int kSlots = S::kSlots;
   constexpr int kPages = kTile / P;  // pages of a tile
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle counts from 1024 bytes
@@ -283,7 +232,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   float* stat = reinterpret_cast<float*>(smem + S::kStatOff);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBarOff);
   uint64_t* empty = full + kSlots;
-  uint64_t* s_full = empty + kSlots;  // S of the stream is in TMEM, its last O product done
+  uint64_t* ready = empty + kSlots;   // quantised: the slot's codes are expanded
+  uint64_t* s_full = ready + kSlots;  // S of the stream is in TMEM, its last O product done
   uint64_t* p_full = s_full + 2;      // P of the stream is in TMEM
   uint64_t* o_full = p_full + 2;      // the stream's O of the unit is complete
   uint64_t* q_full = o_full + 2;      // the stream's query tile is staged
@@ -295,6 +245,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&ready[s], 2);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&s_full[s], 1);
@@ -341,7 +292,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       const int n_pages = x.tokens / P;
       const uint64_t pol = x.g.rows > kPrefixRows ? pol_again : pol_once;
       const int e_page = lane % kPages, e_half = lane / kPages;
-      auto load = [&](const CUtensorMap* map, int tile) {
+      constexpr int kBoxes = kQuant ? 1 : S::kHalves;  // of a page and operand
+      auto load = [&](bool v, int tile) {
         const int slot = fill % kSlots;
         ok = ok && mbar_wait(&empty[slot], ((fill / kSlots) & 1) ^ 1);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -350,22 +302,36 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
         const int pg = tile * kPages + e_page;
         int32_t id = -1;
-        if (e_half < S::kHalves && pg < n_pages) id = bt[pg];
+        if (e_half < kBoxes && pg < n_pages) id = bt[pg];
         const bool mine = id >= 0 && id < a.num_pages;  // bad pages: the rows end as NaN
         const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], boxes * (P * 128));
+        if (lane == 0)
+          mbar_arrive_expect_tx(&full[slot],
+                                boxes * (kQuant ? P * D + (v ? 2 * P * 4 : 0) : P * 128));
         __syncwarp();
-        if (mine)
-          tma_load_4d(ring + slot * S::kTileBytes + e_half * S::kHalfBytes + e_page * (P * 128), map,
-                      &full[slot], 0, id * P, e_half, x.head, pol);
+        if (mine) {
+          if constexpr (kQuant) {
+            tma_load_3d(smem + S::kCodeOff + slot * S::kCodeStep + e_page * (P * D),
+                        v ? &tm_v : &tm_k, &full[slot], 0, id * P, x.head, pol);
+            if (v) {  // the tile's scales, of K too: they live as long as its V
+              float* sc = reinterpret_cast<float*>(smem + S::kScaleOff) + slot * 2 * kTile + e_page * P;
+              const size_t at = ((size_t)id * a.Hkv + x.head) * P;
+              bulk_load(sc, a.k_scale + at, P * 4, &full[slot], pol);
+              bulk_load(sc + kTile, a.v_scale + at, P * 4, &full[slot], pol);
+            }
+          } else {
+            tma_load_4d(ring + slot * S::kTileBytes + e_half * S::kHalfBytes + e_page * (P * 128),
+                        v ? &tm_v : &tm_k, &full[slot], 0, id * P, e_half, x.head, pol);
+          }
+        }
         __syncwarp();
         ++fill;
       };
       const int lead = min(both ? 1 : 2, x.n_tiles);
-      for (int t = 0; t < lead && ok; ++t) load(&tm_k, t);
+      for (int t = 0; t < lead && ok; ++t) load(false, t);
       for (int j = 0; j < x.n_tiles && ok; ++j) {
-        load(&tm_v, j);
-        if (ok && j + lead < x.n_tiles) load(&tm_k, j + lead);
+        load(true, j);
+        if (ok && j + lead < x.n_tiles) load(false, j + lead);
       }
     }
     // Every copy this warp issued has landed before the CTA can exit.
@@ -377,15 +343,16 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     // Per stream: S of its next tile is issued right behind the O product of the last one
     // (which is the last reader of the P it overwrites; products run in issue order), so
     // s_full also says that O may be rescaled.
-    constexpr uint32_t kIdS = umma_idesc_bf16(128, kTile, false, false);
-    constexpr uint32_t kIdO = umma_idesc_bf16(128, D, false, true);
+    constexpr uint32_t kIdS = umma_idesc_bf16(128, kTile, false, false, kQuant);
+    constexpr uint32_t kIdO = umma_idesc_bf16(128, D, false, true, kQuant);
+    uint64_t* const landed_bar = kQuant ? ready : full;
     constexpr uint32_t kHi = umma_desc_hi_sw128(1024);
     const uint32_t q_lo = umma_desc_lo(smem_u32(smem), 16);
     const uint32_t ring_k = umma_desc_lo(smem_u32(ring), 16);
     const uint32_t ring_v = umma_desc_lo(smem_u32(ring), S::kHalfBytes);
     uint32_t use = 0, n_p[2] = {0, 0}, n_q = 0;
     auto landed = [&](uint32_t f) {
-      ok = ok && mbar_wait_fast(&full[f % kSlots], (f / kSlots) & 1);
+      ok = ok && mbar_wait_fast(&landed_bar[f % kSlots], (f / kSlots) & 1);
       ok = __all_sync(0xffffffffu, ok);
     };
     auto scores = [&](int st, uint32_t f) {  // S of stream st from the K tile of fill f
@@ -403,22 +370,22 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       __syncwarp();
     };
     auto outputs = [&](int st, uint32_t f, int tokens, bool first) {  // O += P V
+      landed(f);
+      const uint32_t v_lo = ring_v + (((f % kSlots) * S::kTileBytes) >> 4);
+      const uint32_t p = tmem_s + st * kTile, o = tmem_o + st * D;
       ok = ok && mbar_wait_fast(&p_full[st], n_p[st] & 1);
       ok = __all_sync(0xffffffffu, ok);
       ++n_p[st];
-      landed(f);
       if (!ok) return;
       if (lane == 0) {
         tc_fence_after();
-        const uint32_t v_lo = ring_v + (((f % kSlots) * S::kTileBytes) >> 4);
-        const uint32_t p = tmem_s + st * kTile, o = tmem_o + st * D;
         if (tokens == kTile) {
 #pragma unroll
           for (int ks = 0; ks < kTile / 16; ++ks)
-            umma_ts_lh(o, p + 8 * ks, v_lo + ((ks * 2048) >> 4), kHi, kIdO, !first || ks > 0);
+            umma_ts_lh(o, p + 8 * ks + (ks >= 4 ? 32 : 0), v_lo + ((ks * 2048) >> 4), kHi, kIdO, !first || ks > 0);
         } else {  // the V rows of pages that were not loaded are not read
           for (int ks = 0; ks < tokens / 16; ++ks)
-            umma_ts_lh(o, p + 8 * ks, v_lo + ((ks * 2048) >> 4), kHi, kIdO, !first || ks > 0);
+            umma_ts_lh(o, p + 8 * ks + (ks >= 4 ? 32 : 0), v_lo + ((ks * 2048) >> 4), kHi, kIdO, !first || ks > 0);
         }
       }
       __syncwarp();
@@ -500,8 +467,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const uint32_t s_at = tmem_s + lanes + st * kTile, o_at = tmem_o + lanes + st * D + half * (D / 2);
     float* const my_stat = stat + (2 * st + half) * kTile + row;
     const float* const other_stat = stat + (2 * st + 1 - half) * kTile + row;
-    const float c = a.scale_log2;
+    float c = a.scale_log2;
     uint32_t n_s = 0, n_o = 0;
+    uint32_t used = 0;  // fills of the ring before the piece in hand (quantised)
     auto wait = [&](uint64_t* bar, uint32_t phase) {
       if (ok) ok = mbar_wait_fast(bar, phase & 1);
       ok = __all_sync(0xffffffffu, ok);
@@ -513,17 +481,51 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       const int base = x.r0 + (both ? st * kTile : 0);  // the stream's first row
       const int rows = min(kTile, x.r0 + x.rows - base);
       {
-        // The query tile, K-major 128-byte swizzled.  Rows past the last keep whatever was
-        // there: they feed only their own scores, which nobody reads.
+        // The query tile, K-major 128-byte swizzled, zeros behind the last row.
         const __nv_bfloat16* qg = static_cast<const __nv_bfloat16*>(a.q);
         uint8_t* qt = smem + st * S::kTileBytes;
-        for (int e = tid; e < rows * (D / 8); e += kStreamThreads) {
-          const int r = e / (D / 8), gc = e % (D / 8);
+        constexpr int kEach = kTile * (D / 8) / kStreamThreads;
+        uint4 v[kEach];
+        float most = 0.f;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          const int e = tid + k * kStreamThreads, r = e / (D / 8), gc = e % (D / 8);
           const int rr = base + r;
-          const uint4 v = *reinterpret_cast<const uint4*>(
-              qg + ((size_t)(x.g.qrow0 + rr / a.G) * a.Hq + (size_t)x.head * a.G + rr % a.G) * D + gc * 8);
+          v[k] = make_uint4(0, 0, 0, 0);
+          if (r < rows)
+            v[k] = *reinterpret_cast<const uint4*>(
+                qg + ((size_t)(x.g.qrow0 + rr / a.G) * a.Hq + (size_t)x.head * a.G + rr % a.G) * D + gc * 8);
+          if constexpr (kQuant) most = fmaxf(most, absmax_bf16x8(v[k]));
+        }
+        if constexpr (kQuant) {
+          // Q goes to f16 times 2^-e, the power of two that brings the tile's largest |q| under
+          // 2^15 (1 for any ordinary Q); the scores are scaled back through c.
+#pragma unroll
+          for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          float* const peak = stat + 2 * st * kTile;
+          named_bar_sync(1 + st, kStreamThreads);  // the last piece's sums are read
+          if (lane == 0) peak[warp % kStreamWarps] = most;
+          named_bar_sync(1 + st, kStreamThreads);
+          most = peak[lane % kStreamWarps];
+#pragma unroll
+          for (int o = 4; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+          named_bar_sync(1 + st, kStreamThreads);  // read before the first maxima go there
+          float mul = 1.f;
+          c = a.scale_log2;
+          if (most > 32768.f && most <= 3.0e38f) {
+            int e;
+            frexpf(most, &e);  // most < 2^e
+            mul = ldexpf(1.f, 15 - e);
+            c = ldexpf(a.scale_log2, e - 15);
+          }
+#pragma unroll
+          for (int k = 0; k < kEach; ++k) v[k] = bf16x8_to_f16x8(v[k], mul);
+        }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          const int e = tid + k * kStreamThreads, r = e / (D / 8), gc = e % (D / 8);
           *reinterpret_cast<uint4*>(qt + (gc >> 3) * S::kHalfBytes + r * 128 +
-                                    (((gc & 7) ^ (r & 7)) << 4)) = v;
+                                    (((gc & 7) ^ (r & 7)) << 4)) = v[k];
         }
         fence_proxy_async_smem();
         tc_fence_before();  // this stream's reads of O are over
@@ -546,17 +548,30 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         const int nv = min(kTile, x.tokens - tile * kTile) - 64 * half;  // valid of this half
         wait(&s_full[st], n_s);
         tc_fence_after();
-        uint32_t sr[64];
-        tmem_ld64(s_at + 64 * half, sr);
-        if (nv < 64) {
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e >= nv) sr[e] = __float_as_uint(-INFINITY);
+        // Quantised: scales of this thread's 64 tokens.  They came with the tile's V, fill f of
+        // the ring, whose slot is not filled again before this tile's P is used.
+        const float* ksc = nullptr;
+        if constexpr (kQuant) {
+          const int lead = min(both ? 1 : 2, x.n_tiles);
+          const uint32_t f = used + lead + tile + min(tile, x.n_tiles - lead);
+          wait(&full[f % kSlots], f / kSlots);
+          ksc = reinterpret_cast<const float*>(smem + S::kScaleOff) + (f % kSlots) * 2 * kTile + 64 * half;
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 64; e += 2)
-          mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+        for (int h = 0; h < 2; ++h) {
+          uint32_t sc[32];
+          tmem_ld32(s_at + 64 * half + 32 * h, sc);
+          if constexpr (kQuant) scale32(sc, ksc + 32 * h);
+          if (nv < 64) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * h + e >= nv) sc[e] = __float_as_uint(-INFINITY);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(sc[e]), __uint_as_float(sc[e + 1]));
+        }
         float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;  // c > 0
         // The row's maximum over both halves.  (The next write of this tile's slot comes
         // after the next s_full, so after every thread's read here.)
@@ -582,27 +597,44 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         const float mu = m == -INFINITY ? 0.f : m;
         const uint64_t c2 = pair(c, c), mu2 = pair(-mu, -mu);
         uint64_t sum[2] = {0, 0};
-        uint32_t p[32];
+        // P lies over the first half of this thread's own scores.
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          float p0, p1;
-          unpair(fma2(pair(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, mu2), p0, p1);
-          p0 = ex2_approx(p0);
-          p1 = ex2_approx(p1);
-          sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(p0, p1));
-          p[e >> 1] = pack_bf16x2(p0, p1);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t p[16], sc[32];
+          tmem_ld32(s_at + 64 * half + 32 * h, sc);  // again: held, they would leave no registers
+          if constexpr (kQuant) scale32(sc, ksc + 32 * h);
+          if (nv < 64) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * h + e >= nv) sc[e] = __float_as_uint(-INFINITY);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float p0, p1;
+            unpair(fma2(pair(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1])), c2, mu2), p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(p0, p1));
+            if constexpr (kQuant) {
+              const float2 vs = *reinterpret_cast<const float2*>(ksc + kTile + 32 * h + e);
+              p[e >> 1] = pack_f16x2(p0 * vs.x, p1 * vs.y);
+            } else {
+              p[e >> 1] = pack_bf16x2(p0, p1);
+            }
+          }
+          tmem_st16(s_at + 64 * half + 16 * h, p);
         }
         {
           float lo, hi;
           unpair(add2(sum[0], sum[1]), lo, hi);
           l += lo + hi;
         }
-        // P lies over S: the halves' barrier above followed every thread's read of S.
-        tmem_st32(s_at + 32 * half, p);
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[st]);
       }
+      used += 2 * x.n_tiles;
       if (n_mine > 0) {
         wait(&o_full[st], n_o);
         ++n_o;
@@ -677,7 +709,60 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       if (!both) named_bar_sync(3, 2 * kStreamThreads);  // the dump is read: Q may be staged
     }
   } else {
+    // ------------------------------ converters ------------------------------
+    // Two warps, each every other 16 bytes-by-row group of a tile.  A row's codes are read by
+    // lanes of one warp before any of its f16 values is written.
     give_registers();
+    if constexpr (kQuant) {
+      constexpr int kChunks = D / 16;        // 16-code chunks of a row
+      constexpr int kRows = 32 / kChunks;    // rows of a warp at a time
+      constexpr int kBatch = 4;
+      const int cw = warp - kMmaWarp - 1;
+      uint32_t fill = 0;
+      Pieces it(a, lane);
+      Piece x;
+      while (ok && it.next(a, x)) {
+        for (int k = 0; k < 2 * x.n_tiles && ok; ++k, ++fill) {
+          const int slot = fill % kSlots;
+          ok = mbar_wait_fast(&full[slot], (fill / kSlots) & 1);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint8_t* codes = smem + S::kCodeOff + slot * S::kCodeStep;
+          uint8_t* out = ring + slot * S::kTileBytes;
+          const int c = lane % kChunks;
+#pragma unroll 1
+          for (int r0 = cw * kRows * kBatch; r0 < kTile; r0 += 2 * kRows * kBatch) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+              v[e] = *reinterpret_cast<const uint4*>(codes + (r0 + e * kRows + lane / kChunks) * D + c * 16);
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) {
+              const int r = r0 + e * kRows + lane / kChunks;
+              uint4 y0, y1;
+              if constexpr (KV == VAS_FP8_E4M3) {
+                e4m3x4_to_f16x4(v[e].x, y0.x, y0.y);
+                e4m3x4_to_f16x4(v[e].y, y0.z, y0.w);
+                e4m3x4_to_f16x4(v[e].z, y1.x, y1.y);
+                e4m3x4_to_f16x4(v[e].w, y1.z, y1.w);
+              } else {
+                s8x4_to_f16x4(v[e].x, y0.x, y0.y);
+                s8x4_to_f16x4(v[e].y, y0.z, y0.w);
+                s8x4_to_f16x4(v[e].z, y1.x, y1.y);
+                s8x4_to_f16x4(v[e].w, y1.z, y1.w);
+              }
+              uint8_t* row = out + (2 * c >> 3) * S::kHalfBytes + r * 128;
+              *reinterpret_cast<uint4*>(row + (((2 * c & 7) ^ (r & 7)) << 4)) = y0;
+              *reinterpret_cast<uint4*>(row + ((((2 * c + 1) & 7) ^ (r & 7)) << 4)) = y1;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ready[slot]);
+        }
+      }
+    }
   }
   if (!ok && lane == 0) atomicOr(a.err, VAS_DEV_TIMEOUT);
   tc_fence_before();
@@ -688,52 +773,34 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
   }
 }
 
-template <int D, int P>
-int launch_tc(const CUtensorMap& mk, const CUtensorMap& mv, const PrefixArgs& a, void* stream) {
+template <int D, int P, int KV>
+int launch_kernel(const CUtensorMap& mk, const CUtensorMap& mv, const PrefixArgs& a, void* stream) {
   static std::once_flag once[64];
   static cudaError_t attr_err[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return VAS_E_CUDA;
   std::call_once(once[dev & 63], [&] {
     cudaFuncAttributes fa;
-    attr_err[dev & 63] = cudaFuncGetAttributes(&fa, prefix_kernel<D, P>);
+    attr_err[dev & 63] = cudaFuncGetAttributes(&fa, prefix_kernel<D, P, KV>);
     // Fewer registers than the split counts on would leave setmaxnreg waiting.
     if (attr_err[dev & 63] == cudaSuccess && fa.numRegs < kLaunchRegs)
       attr_err[dev & 63] = cudaErrorInvalidConfiguration;
     if (attr_err[dev & 63] == cudaSuccess)
       attr_err[dev & 63] = cudaFuncSetAttribute(
-          prefix_kernel<D, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem<D>::kDynBytes);
+          prefix_kernel<D, P, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, PSmem<D, KV>::kDynBytes);
   });
   if (attr_err[dev & 63] != cudaSuccess) return VAS_E_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(num_sms());
   cfg.blockDim = dim3(kPrefixThreads);
-  cfg.dynamicSmemBytes = PSmem<D>::kDynBytes;
+  cfg.dynamicSmemBytes = PSmem<D, KV>::kDynBytes;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, prefix_kernel<D, P>, mk, mv, a) != cudaSuccess) {
-    cudaGetLastError();
-    return VAS_E_CUDA;
-  }
-  return VAS_OK;
-}
-
-template <typename K>
-int launch(K kernel, const PrefixArgs& a, int grid, int threads, void* stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, prefix_kernel<D, P, KV>, mk, mv, a) != cudaSuccess) {
     cudaGetLastError();
     return VAS_E_CUDA;
   }
@@ -744,20 +811,19 @@ int launch(K kernel, const PrefixArgs& a, int grid, int threads, void* stream) {
 
 int launch_prefix(const CUtensorMap& mk, const CUtensorMap& mv, const PrefixArgs& a,
                   int head_dim, int kv_dtype, void* stream) {
-  if (kv_dtype == VAS_BF16) {
+  auto kind = [&](auto kv) {
+    constexpr int KV = decltype(kv)::value;
     if (head_dim == 128)
-      return a.P == 16 ? launch_tc<128, 16>(mk, mv, a, stream) : launch_tc<128, 32>(mk, mv, a, stream);
-    return a.P == 16 ? launch_tc<64, 16>(mk, mv, a, stream) : launch_tc<64, 32>(mk, mv, a, stream);
+      return a.P == 16 ? launch_kernel<128, 16, KV>(mk, mv, a, stream)
+                       : launch_kernel<128, 32, KV>(mk, mv, a, stream);
+    return a.P == 16 ? launch_kernel<64, 16, KV>(mk, mv, a, stream)
+                     : launch_kernel<64, 32, KV>(mk, mv, a, stream);
+  };
+  switch (kv_dtype) {
+    case VAS_BF16: return kind(std::integral_constant<int, VAS_BF16>{});
+    case VAS_FP8_E4M3: return kind(std::integral_constant<int, VAS_FP8_E4M3>{});
+    default: return kind(std::integral_constant<int, VAS_INT8>{});
   }
-  const int grid = num_sms();
-  if (head_dim == 128) {
-    if (kv_dtype == VAS_FP8_E4M3)
-      return launch(prefix_simple_kernel<128, VAS_FP8_E4M3>, a, grid, 256, stream);
-    return launch(prefix_simple_kernel<128, VAS_INT8>, a, grid, 256, stream);
-  }
-  if (kv_dtype == VAS_FP8_E4M3)
-    return launch(prefix_simple_kernel<64, VAS_FP8_E4M3>, a, grid, 256, stream);
-  return launch(prefix_simple_kernel<64, VAS_INT8>, a, grid, 256, stream);
 }
 
 }  // namespace attn
