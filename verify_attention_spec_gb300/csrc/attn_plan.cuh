@@ -32,7 +32,7 @@ struct PlanHeader {
   int32_t n_partial_rows;
   // Shared-prefix calls: groups that are shared, and how their work is dealt out.
   int32_t n_groups;
-  int64_t span, share;
+  int32_t span, share;
 };
 
 // A group of sequences whose shared pages are computed once.  Its rows, of one KV head, are
@@ -51,8 +51,7 @@ struct PrefixGroup {
   int32_t pages;       // shared pages
   int32_t parts;       // partials of a row: the most pieces a block is cut into
   int32_t seq0, seq1;  // members
-  int32_t tiles, blocks, weight;
-  int64_t base;
+  int32_t tiles, blocks, weight, base;
 };
 constexpr int kPrefixRows = 256;  // rows of a block
 constexpr int kPrefixTile = 128;  // tokens of a tile
@@ -66,6 +65,21 @@ __device__ __forceinline__ size_t partial_index(const SeqPlan& sp, int Hkv, int 
                                                 int head, int r) {
   return (size_t)sp.partial_base + ((size_t)split * Hkv + head) * ((size_t)G * sp.qlen) + r;
 }
+
+// Division of 0 <= n < 2^31 by a divisor known to the host (Granlund and Montgomery, "Division
+// by invariant integers using multiplication", PLDI 1994): with 2^(l-1) < d <= 2^l and
+// m = floor(2^(31 + l) / d) + 1, n / d = floor(n m / 2^(31 + l)).
+struct Divisor {
+  uint32_t d, m, shift;
+  explicit Divisor(uint32_t divisor) : d(divisor), shift(31) {
+    while ((1ull << (shift - 31)) < d) ++shift;
+    m = (uint32_t)((1ull << shift) / d + 1);
+  }
+  Divisor() = default;
+  __device__ __forceinline__ uint32_t div(uint32_t n) const {
+    return (uint32_t)(((uint64_t)n * m) >> shift);
+  }
+};
 
 struct PrefixArgs {
   const void* q;
@@ -81,6 +95,7 @@ struct PrefixArgs {
   float* part_o;
   float* part_lse;
   int32_t Hq, Hkv, G, maxp, num_pages, P;
+  Divisor by_G;
   float scale_log2;  // softmax scale * log2(e)
   int32_t* err;
 };

@@ -373,7 +373,7 @@ __device__ bool plan_prefixes(const PlanArgs& a, ShapeFn shape, int64_t (*red)[4
     block_scan<2>(v, red, t);
     if (share) {
       const int32_t e = (int32_t)(at[0] + v[0]);
-      pg.base = at[1] + v[1];
+      pg.base = (int32_t)(at[1] + v[1] < INT_MAX ? at[1] + v[1] : INT_MAX);
       a.entry[g] = e;
       a.groups[e] = pg;
     }
@@ -383,6 +383,11 @@ __device__ bool plan_prefixes(const PlanArgs& a, ShapeFn shape, int64_t (*red)[4
   __syncthreads();
   const int n = (int)at[0];
   const int64_t span = at[1];
+  if (span > INT_MAX / 2) {  // past 32-bit unit numbers: minutes of work
+    for (int i = tid; i < a.B; i += kPlanThreads)
+      if (a.shared[i] >= 0) a.shared[i] = -1;
+    return fine;
+  }
   if (n > 0) {
     // Every CTA the same share, as long as the partials fit the workspace; larger shares,
     // so fewer pieces, until they do.
@@ -395,8 +400,9 @@ __device__ bool plan_prefixes(const PlanArgs& a, ShapeFn shape, int64_t (*red)[4
         const int64_t len = (int64_t)pg.tiles * pg.weight;
         int32_t parts = 1;
         for (int b = lane; b < pg.blocks; b += 32) {
-          const int64_t first = pg.base + b * len;
-          parts = max(parts, (int32_t)((first + len - 1) / each - first / each) + 1);
+          const int64_t first = pg.base + (int64_t)b * len;
+          parts = max(parts, (int32_t)((uint32_t)(first + len - 1) / (uint32_t)each -
+                                       (uint32_t)first / (uint32_t)each) + 1);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) parts = max(parts, __shfl_xor_sync(0xffffffffu, parts, o));
@@ -409,8 +415,8 @@ __device__ bool plan_prefixes(const PlanArgs& a, ShapeFn shape, int64_t (*red)[4
       if (need[0] <= a.partial_cap) {
         if (tid == 0) {
           a.header->n_groups = n;
-          a.header->span = span;
-          a.header->share = each;
+          a.header->span = (int32_t)span;
+          a.header->share = (int32_t)each;
         }
         break;
       }
@@ -1162,28 +1168,37 @@ __device__ __forceinline__ void merge_rows(const AttnArgs& a, const SeqPlan& sp,
                                                : -INFINITY);
       w[k] = exp2f((v - mu[k]) * 1.4426950408889634f);
     }
-#pragma unroll 4
-    for (int s = s0; s < min(n, s0 + 32); ++s) {
-      float4 v[ROWS];
+    for (int s1 = s0; s1 < min(n, s0 + 32); s1 += 4) {  // four splits' rows at once
+      float4 v[4][ROWS];
 #pragma unroll
-      for (int k = 0; k < ROWS; ++k) {
-        const float* po = a.part_o + (row[k] + s * step) * D + lane * E;
-        if constexpr (E == 4) {
-          v[k] = __ldcg(reinterpret_cast<const float4*>(po));
-        } else {
-          const float2 h = __ldcg(reinterpret_cast<const float2*>(po));
-          v[k] = make_float4(h.x, h.y, 0.f, 0.f);
+      for (int d = 0; d < 4; ++d) {
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+          v[d][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (s1 + d < n) {
+            const float* po = a.part_o + (row[k] + (s1 + d) * step) * D + lane * E;
+            if constexpr (E == 4) {
+              v[d][k] = __ldcg(reinterpret_cast<const float4*>(po));
+            } else {
+              const float2 h = __ldcg(reinterpret_cast<const float2*>(po));
+              v[d][k] = make_float4(h.x, h.y, 0.f, 0.f);
+            }
+          }
         }
       }
 #pragma unroll
-      for (int k = 0; k < ROWS; ++k) {
-        const float ws = __shfl_sync(0xffffffffu, w[k], s - s0);
-        wsum[k] += ws;
-        acc[k][0] = fmaf(ws, v[k].x, acc[k][0]);
-        acc[k][1] = fmaf(ws, v[k].y, acc[k][1]);
-        if constexpr (E == 4) {
-          acc[k][2] = fmaf(ws, v[k].z, acc[k][2]);
-          acc[k][3] = fmaf(ws, v[k].w, acc[k][3]);
+      for (int d = 0; d < 4; ++d) {
+        if (s1 + d >= n) break;
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+          const float ws = __shfl_sync(0xffffffffu, w[k], s1 + d - s0);
+          wsum[k] += ws;
+          acc[k][0] = fmaf(ws, v[d][k].x, acc[k][0]);
+          acc[k][1] = fmaf(ws, v[d][k].y, acc[k][1]);
+          if constexpr (E == 4) {
+            acc[k][2] = fmaf(ws, v[d][k].z, acc[k][2]);
+            acc[k][3] = fmaf(ws, v[d][k].w, acc[k][3]);
+          }
         }
       }
     }
@@ -1214,41 +1229,123 @@ __device__ void merge_splits(const AttnArgs& a, const SeqPlan& sp, int head, int
     merge_rows<D, kMergeRows>(a, sp, head, r0 + rr, r0 + Rb, lane);
 }
 
-// Merge of the sequences with a shared prefix, whose rows all have partials: a warp takes
-// kSharedRows consecutive query heads of a token at a time.  On its own because the rows are
-// many and their partials few: merged by the last split in attn_bf16_kernel, four warps an
-// SM, 640 tokens of 64 heads behind a shared prefix cost that kernel 109 us (179 against
-// 70); bounded by the partials' bytes.
-constexpr int kSharedRows = 4;
+// Merge of the sequences with a shared prefix, whose rows all have partials.  On its own
+// because the rows are many and their partials few: merged by the last split in
+// attn_bf16_kernel, four warps an SM, 640 tokens of 64 heads behind a shared prefix cost that
+// kernel 109 us (179 against 70).  A row is D / 8 lanes, 8 columns each; a warp holds
+// kMergeBatch groups of 32 / (D / 8) rows, four partials of each, in flight.  Bounded by the
+// partials' bytes.
+constexpr int kMergeBatch = 2;
 template <int D>
 __global__ void __launch_bounds__(256) merge_shared_kernel(const AttnArgs a, const int32_t* row0,
-                                                           const int32_t* shared, int B) {
+                                                           const int32_t* shared, int B,
+                                                           int heads, const Divisor by_G,
+                                                           const Divisor by_tasks) {
+  constexpr int kLanes = D / 8, kSub = 32 / kLanes;
+  const float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  if (a.header->n_groups == 0) return;
-  const int lane = threadIdx.x & 31;
-  // Tasks: (token, KV head, kSharedRows of its G query heads).
-  const uint32_t per_head = (a.G + kSharedRows - 1) / kSharedRows;
-  const uint32_t per_token = per_head * a.Hkv;
-  const uint64_t n_tasks = (uint64_t)a.T * per_token;
-  const uint64_t stride = (uint64_t)gridDim.x * (blockDim.x >> 5);
-  for (uint64_t w = (uint64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < n_tasks;
-       w += stride) {
-    const int t = (int)(n_tasks <= 0xffffffffu ? (uint32_t)w / per_token : w / per_token);
-    const uint32_t part = (uint32_t)(w - (uint64_t)t * per_token);
-    if (t >= row0[B]) return;  // rows that no sequence owns
-    int lo = 0, hi = B - 1;  // the last sequence whose first token is at or below t
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (row0[mid] <= t) lo = mid;
-      else hi = mid - 1;
+  const int n_groups = a.header->n_groups, tokens = row0[B];
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, col = lane % kLanes * 8;
+  if (n_groups == 0) return;
+  // A task is one token and `heads` of its KV heads (the host keeps their number below 2^31).
+  const uint32_t n_tasks = (uint32_t)a.T * by_tasks.d;
+  const uint32_t stride = gridDim.x * (blockDim.x >> 5);
+  for (uint32_t w = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < n_tasks; w += stride) {
+    const int t = (int)by_tasks.div(w);
+    const int h0 = (int)(w - t * by_tasks.d) * heads;
+    if (t >= tokens) return;  // rows that no sequence owns
+    // The last sequence whose first token is at or below t, 32 candidates at a time.
+    int lo = 0, n_seq = B;
+    while (n_seq > 1) {
+      const int each = (n_seq + 31) >> 5, i = lo + lane * each;
+      const uint32_t m = __ballot_sync(0xffffffffu, lane * each < n_seq && row0[i] <= t);
+      const int c = 31 - __clz(m);
+      lo += c * each;
+      n_seq = min(each, n_seq - c * each);
     }
-    if (shared[lo] < 0) continue;
+    const int group = shared[lo];
     const SeqPlan sp = a.seqplan[lo];
-    if (sp.nsplit < 2) continue;
-    const int j = t - sp.qrow0, h0 = (int)(part % per_head) * kSharedRows;
-    merge_rows<D, kSharedRows>(a, sp, (int)(part / per_head), j * a.G + h0,
-                               j * a.G + min(a.G, h0 + kSharedRows), lane);
+    const int n = sp.nsplit;
+    if (group < 0 || n < 2) continue;
+    const size_t per_head = (size_t)a.G * sp.qlen, step = a.Hkv * per_head;
+    const size_t base = sp.partial_base + (size_t)(t - sp.qrow0) * a.G;
+    const int rows = min(heads, a.Hkv - h0) * a.G;  // query heads of the task
+    for (int i0 = 0; i0 < rows; i0 += kSub * kMergeBatch) {
+      size_t row[kMergeBatch];
+      float mx[kMergeBatch], wsum[kMergeBatch], acc[kMergeBatch][8], l[4][kMergeBatch];
+      float4 v[4][kMergeBatch][2];
+      bool bad[kMergeBatch];
+#pragma unroll
+      for (int k = 0; k < kMergeBatch; ++k) {  // rows past the last repeat it, unwritten
+        const int i = min(i0 + k * kSub + sub, rows - 1), h = (int)by_G.div(i);
+        row[k] = base + (size_t)(h0 + h) * per_head + (i - h * a.G);
+      }
+      auto load = [&](int s0) {  // partials s0 .. s0 + 3
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+#pragma unroll
+          for (int k = 0; k < kMergeBatch; ++k) {
+            l[d][k] = -INFINITY;
+            v[d][k][0] = v[d][k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s0 + d < n) {
+              const size_t at = row[k] + (s0 + d) * step;
+              l[d][k] = __ldcg(a.part_lse + at);
+              const float4* po = reinterpret_cast<const float4*>(a.part_o + at * D + col);
+              v[d][k][0] = __ldcg(po);
+              v[d][k][1] = __ldcg(po + 1);
+            }
+          }
+      };
+      load(0);  // nearly always all of them
+#pragma unroll
+      for (int k = 0; k < kMergeBatch; ++k) {
+        mx[k] = fmaxf(fmaxf(l[0][k], l[1][k]), fmaxf(l[2][k], l[3][k]));
+        bad[k] = isnan(l[0][k]) || isnan(l[1][k]) || isnan(l[2][k]) || isnan(l[3][k]);
+        for (int s = 4; s < n; ++s) {
+          const float x = __ldcg(a.part_lse + row[k] + s * step);
+          bad[k] |= isnan(x);
+          mx[k] = fmaxf(mx[k], x);
+        }
+        mx[k] = mx[k] == -INFINITY ? 0.f : mx[k];
+        wsum[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[k][e] = 0.f;
+      }
+      for (int s0 = 0; s0 < n; s0 += 4) {
+        if (s0 > 0) load(s0);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          if (s0 + d >= n) break;
+#pragma unroll
+          for (int k = 0; k < kMergeBatch; ++k) {
+            const float f = exp2f((l[d][k] - mx[k]) * kLog2e);
+            wsum[k] += f;
+            acc[k][0] = fmaf(f, v[d][k][0].x, acc[k][0]);
+            acc[k][1] = fmaf(f, v[d][k][0].y, acc[k][1]);
+            acc[k][2] = fmaf(f, v[d][k][0].z, acc[k][2]);
+            acc[k][3] = fmaf(f, v[d][k][0].w, acc[k][3]);
+            acc[k][4] = fmaf(f, v[d][k][1].x, acc[k][4]);
+            acc[k][5] = fmaf(f, v[d][k][1].y, acc[k][5]);
+            acc[k][6] = fmaf(f, v[d][k][1].z, acc[k][6]);
+            acc[k][7] = fmaf(f, v[d][k][1].w, acc[k][7]);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kMergeBatch; ++k) {
+        const int i = i0 + k * kSub + sub;
+        if (i >= rows) continue;
+        const float inv = bad[k] ? NAN : 1.f / wsum[k];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[k][e] *= inv;
+        const size_t orow = (size_t)t * a.Hq + (size_t)h0 * a.G + i;
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + col) =
+            make_uint4(pack_bf16x2(acc[k][0], acc[k][1]), pack_bf16x2(acc[k][2], acc[k][3]),
+                       pack_bf16x2(acc[k][4], acc[k][5]), pack_bf16x2(acc[k][6], acc[k][7]));
+        if (col == 0) a.lse[orow] = bad[k] ? NAN : mx[k] + log2f(wsum[k]) * kLn2;
+      }
+    }
   }
 }
 
@@ -2771,8 +2868,13 @@ struct PrefixCall {
 template <int D>
 int launch_merge(const AttnArgs& aa, const PlanArgs& pa, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  const int64_t tasks = (int64_t)aa.T * aa.Hkv * ((aa.G + kSharedRows - 1) / kSharedRows);
-  const int64_t blocks = (tasks + 7) / 8, most = 8LL * pa.sms;
+  // As many KV heads a task as leave two tasks to every resident warp, and their number
+  // below 2^31 (T * Hq is).
+  const int64_t warps = 16LL * pa.sms;
+  int64_t heads = (int64_t)aa.T * aa.Hkv / (2 * warps);
+  heads = heads < 1 ? 1 : (heads > aa.Hkv ? aa.Hkv : heads);
+  const int64_t per_token = (aa.Hkv + heads - 1) / heads, tasks = aa.T * per_token;
+  const int64_t blocks = (tasks + 7) / 8, most = warps / 8;
   cfg.gridDim = dim3((unsigned)(blocks < most ? blocks : most));
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
@@ -2782,7 +2884,8 @@ int launch_merge(const AttnArgs& aa, const PlanArgs& pa, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, merge_shared_kernel<D>, aa, (const int32_t*)pa.row0,
-                         (const int32_t*)pa.shared, (int)pa.B) != cudaSuccess) {
+                         (const int32_t*)pa.shared, (int)pa.B, (int)heads, Divisor((uint32_t)aa.G),
+                         Divisor((uint32_t)per_token)) != cudaSuccess) {
     cudaGetLastError();
     return VAS_E_CUDA;
   }
@@ -2935,6 +3038,7 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
     px.maxp = d.max_pages_per_seq;
     px.num_pages = d.num_pages;
     px.P = d.page_size;
+    px.by_G = Divisor((uint32_t)G);
     px.scale_log2 = aa.scale_log2;
     px.err = err;
     CUtensorMap pk = mk, pv = mv;

@@ -25,18 +25,6 @@ namespace vas {
 namespace attn {
 namespace {
 
-// The sequence that owns query token t of a group: the last member whose first token is at
-// or below t (members without tokens start where their successor does).
-__device__ __forceinline__ int member_of(const PrefixArgs& a, const PrefixGroup& g, int32_t t) {
-  int lo = g.seq0, hi = g.seq1 - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.row0[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
-
 // A piece of a block: what one CTA computes of it at a time.
 struct Piece {
   PrefixGroup g;
@@ -48,17 +36,18 @@ struct Piece {
 
 // The pieces of a CTA's share, in order.  Every warp walks them by itself.
 struct Pieces {
-  int64_t x, end, share;
+  uint32_t x, end, share;
   int e;
   __device__ __forceinline__ Pieces(const PrefixArgs& a, int lane) {
     share = a.header->share;
-    x = (int64_t)blockIdx.x * share;
-    end = min(x + share, a.header->span);
+    x = blockIdx.x * share;
+    end = min(x + share, (uint32_t)a.header->span);
     e = 0;
     // The last entry whose base is at or below x, 32 entries at a time.
     const int n = a.header->n_groups;
     for (int s = 0; s < n; s += 32) {
-      const uint32_t m = __ballot_sync(0xffffffffu, s + lane < n && a.groups[s + lane].base <= x);
+      const uint32_t m =
+          __ballot_sync(0xffffffffu, s + lane < n && (uint32_t)a.groups[s + lane].base <= x);
       if (m == 0) break;
       e = s + 31 - __clz(m);
       if (m != 0xffffffffu) break;
@@ -68,19 +57,20 @@ struct Pieces {
   __device__ __forceinline__ bool next(const PrefixArgs& a, Piece& p) {
     while (x < end) {
       p.g = a.groups[e];
-      const int64_t len = (int64_t)p.g.tiles * p.g.weight;
-      const int64_t local = x - p.g.base, block = local / len;
-      if (block >= p.g.blocks) {
+      const uint32_t len = p.g.tiles * p.g.weight, base = p.g.base;
+      const uint32_t block = (x - base) / len;
+      if (block >= (uint32_t)p.g.blocks) {
         ++e;
-        x = p.g.base + ((len * p.g.blocks + 1) & ~1ll);
+        x = base + ((len * p.g.blocks + 1) & ~1u);
         continue;
       }
-      const int64_t first = p.g.base + block * len, stop = min(end, first + len);
-      const int per_head = p.g.blocks / a.Hkv;
+      const uint32_t first = base + block * len, stop = min(end, first + len);
+      const uint32_t per_head = (uint32_t)p.g.blocks / (uint32_t)a.Hkv;
       p.head = (int)(block / per_head);
-      p.r0 = (int)(block % per_head) * kPrefixRows;
+      p.r0 = (int)(block - p.head * per_head) * kPrefixRows;
       p.rows = min(kPrefixRows, p.g.rows - p.r0);
-      const int t0 = (int)((x - first) / p.g.weight), t1 = (int)((stop - first) / p.g.weight);
+      const int wide = p.g.weight - 1;  // weight 1 or 2
+      const int t0 = (int)(x - first) >> wide, t1 = (int)(stop - first) >> wide;
       p.page_begin = t0 * (kPrefixTile / a.P);
       p.n_tiles = t1 - t0;
       p.tokens = min(p.g.pages * a.P, t1 * kPrefixTile) - t0 * kPrefixTile;
@@ -93,17 +83,28 @@ struct Pieces {
   }
 };
 
-// Partial row of row r of a group, for partial `part` of its shared pages.
-__device__ __forceinline__ size_t part_row(const PrefixArgs& a, const Piece& p, int r, int part) {
-  const int t = p.g.qrow0 + r / a.G;
-  const SeqPlan sp = a.seqplan[member_of(a, p.g, t)];
-  return partial_index(sp, a.Hkv, a.G, sp.nsplit - p.g.parts + part, p.head,
-                       (t - sp.qrow0) * a.G + r % a.G);
-}
-// Partial rows from one partial of a row to the next.
-__device__ __forceinline__ size_t part_step(const PrefixArgs& a, const Piece& p, int r) {
-  const int t = p.g.qrow0 + r / a.G;
-  return (size_t)a.Hkv * ((size_t)a.G * a.seqplan[member_of(a, p.g, t)].qlen);
+// Partial row of row r of a group for the piece's partial, and how far the next partial of
+// the row is.  The whole warp, rows ascending with the lane: the member that owns the first
+// lane's token is searched 32 at a time (the last member whose first token is at or below
+// it; members without tokens start where their successor does), the others walk on from it.
+__device__ __forceinline__ size_t part_row(const PrefixArgs& a, const Piece& p, int r, int lane,
+                                           size_t* step) {
+  const int j = (int)a.by_G.div(r), t = p.g.qrow0 + j;
+  const int t_first = __shfl_sync(0xffffffffu, t, 0);
+  int lo = p.g.seq0, n = p.g.seq1 - p.g.seq0;
+  while (n > 1) {
+    const int each = (n + 31) >> 5;
+    const uint32_t m =
+        __ballot_sync(0xffffffffu, lane * each < n && a.row0[lo + lane * each] <= t_first);
+    const int c = 31 - __clz(m);
+    lo += c * each;
+    n = min(each, n - c * each);
+  }
+  while (lo + 1 < p.g.seq1 && a.row0[lo + 1] <= t) ++lo;
+  const SeqPlan sp = a.seqplan[lo];
+  *step = (size_t)a.Hkv * ((size_t)a.G * sp.qlen);
+  return partial_index(sp, a.Hkv, a.G, sp.nsplit - p.g.parts + p.part, p.head,
+                       (t - sp.qrow0) * a.G + (r - j * a.G));
 }
 
 // ------------------------------------------------------------------------------------
@@ -200,18 +201,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&x)[16
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// 32 scores times the K scales of their tokens.
-__device__ __forceinline__ void scale32(uint32_t (&s)[32], const float* k) {
-#pragma unroll
-  for (int e = 0; e < 32; e += 4) {
-    const float4 v = *reinterpret_cast<const float4*>(k + e);
-    s[e] = __float_as_uint(__uint_as_float(s[e]) * v.x);
-    s[e + 1] = __float_as_uint(__uint_as_float(s[e + 1]) * v.y);
-    s[e + 2] = __float_as_uint(__uint_as_float(s[e + 2]) * v.z);
-    s[e + 3] = __float_as_uint(__uint_as_float(s[e + 3]) * v.w);
-  }
 }
 
 // The warps beside the streams hand registers over (every warp of the group executes it).
@@ -467,6 +456,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     const uint32_t s_at = tmem_s + lanes + st * kTile, o_at = tmem_o + lanes + st * D + half * (D / 2);
     float* const my_stat = stat + (2 * st + half) * kTile + row;
     const float* const other_stat = stat + (2 * st + 1 - half) * kTile + row;
+    // What scores are multiplied by: the softmax scale in log2 units, or (quantised) what was
+    // taken out of Q, the scale being in the K scales.
     float c = a.scale_log2;
     uint32_t n_s = 0, n_o = 0;
     uint32_t used = 0;  // fills of the ring before the piece in hand (quantised)
@@ -494,7 +485,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           v[k] = make_uint4(0, 0, 0, 0);
           if (r < rows)
             v[k] = *reinterpret_cast<const uint4*>(
-                qg + ((size_t)(x.g.qrow0 + rr / a.G) * a.Hq + (size_t)x.head * a.G + rr % a.G) * D + gc * 8);
+                qg + ((size_t)x.g.qrow0 * a.Hq + (size_t)x.head * a.G + rr +
+                      (size_t)a.by_G.div(rr) * (a.Hq - a.G)) * D + gc * 8);
           if constexpr (kQuant) most = fmaxf(most, absmax_bf16x8(v[k]));
         }
         if constexpr (kQuant) {
@@ -511,12 +503,12 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           for (int o = 4; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
           named_bar_sync(1 + st, kStreamThreads);  // read before the first maxima go there
           float mul = 1.f;
-          c = a.scale_log2;
+          c = 1.f;
           if (most > 32768.f && most <= 3.0e38f) {
             int e;
             frexpf(most, &e);  // most < 2^e
             mul = ldexpf(1.f, 15 - e);
-            c = ldexpf(a.scale_log2, e - 15);
+            c = ldexpf(1.f, e - 15);
           }
 #pragma unroll
           for (int k = 0; k < kEach; ++k) v[k] = bf16x8_to_f16x8(v[k], mul);
@@ -541,6 +533,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           bad |= id < 0 || id >= a.num_pages;
         }
       }
+      // Where this thread's row goes: looked up while the first scores are computed.
+      size_t step;
+      const size_t at = part_row(a, x, base + min(row, rows - 1), lane, &step);
       const int n_mine = both ? x.n_tiles : (x.n_tiles - st + 1) / 2;
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n_mine; ++i, ++n_s) {
@@ -554,7 +549,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         if constexpr (kQuant) {
           const int lead = min(both ? 1 : 2, x.n_tiles);
           const uint32_t f = used + lead + tile + min(tile, x.n_tiles - lead);
-          wait(&full[f % kSlots], f / kSlots);
+          wait(&ready[f % kSlots], f / kSlots);
           ksc = reinterpret_cast<const float*>(smem + S::kScaleOff) + (f % kSlots) * 2 * kTile + 64 * half;
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -562,7 +557,17 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         for (int h = 0; h < 2; ++h) {
           uint32_t sc[32];
           tmem_ld32(s_at + 64 * half + 32 * h, sc);
-          if constexpr (kQuant) scale32(sc, ksc + 32 * h);
+          if constexpr (kQuant) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const ulonglong2 k = *reinterpret_cast<const ulonglong2*>(ksc + 32 * h + e);
+              float y[4];
+              unpair(mul2(pair(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1])), k.x), y[0], y[1]);
+              unpair(mul2(pair(__uint_as_float(sc[e + 2]), __uint_as_float(sc[e + 3])), k.y), y[2], y[3]);
+#pragma unroll
+              for (int d = 0; d < 4; ++d) sc[e + d] = __float_as_uint(y[d]);
+            }
+          }
           if (nv < 64) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -602,24 +607,40 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         for (int h = 0; h < 2; ++h) {
           uint32_t p[16], sc[32];
           tmem_ld32(s_at + 64 * half + 32 * h, sc);  // again: held, they would leave no registers
-          if constexpr (kQuant) scale32(sc, ksc + 32 * h);
           if (nv < 64) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (32 * h + e >= nv) sc[e] = __float_as_uint(-INFINITY);
+              if (32 * h + e >= nv) sc[e] = __float_as_uint(kQuant ? 0.f : -INFINITY);
           }
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float p0, p1;
-            unpair(fma2(pair(__uint_as_float(sc[e]), __uint_as_float(sc[e + 1])), c2, mu2), p0, p1);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], pair(p0, p1));
+          for (int e = 0; e < 32; e += 4) {
+            uint64_t k[2] = {c2, c2}, v[2];
             if constexpr (kQuant) {
-              const float2 vs = *reinterpret_cast<const float2*>(ksc + kTile + 32 * h + e);
-              p[e >> 1] = pack_f16x2(p0 * vs.x, p1 * vs.y);
-            } else {
-              p[e >> 1] = pack_bf16x2(p0, p1);
+              const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(ksc + 32 * h + e);
+              const ulonglong2 vs = *reinterpret_cast<const ulonglong2*>(ksc + kTile + 32 * h + e);
+              k[0] = ks.x, k[1] = ks.y, v[0] = vs.x, v[1] = vs.y;
+              if (c != 1.f) k[0] = mul2(k[0], c2), k[1] = mul2(k[1], c2);
+            }
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+              const int f = e + 2 * d;
+              float p0, p1;
+              unpair(fma2(pair(__uint_as_float(sc[f]), __uint_as_float(sc[f + 1])), k[d], mu2), p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              if (kQuant && nv < 64) {  // scales behind the last token may be anything
+                if (32 * h + f >= nv) p0 = 0.f;
+                if (32 * h + f + 1 >= nv) p1 = 0.f;
+              }
+              const uint64_t pp = pair(p0, p1);
+              sum[d] = add2(sum[d], pp);
+              if constexpr (kQuant) {
+                float w0, w1;
+                unpair(mul2(pp, v[d]), w0, w1);
+                p[f >> 1] = pack_f16x2(w0, w1);
+              } else {
+                p[f >> 1] = pack_bf16x2(p0, p1);
+              }
             }
           }
           tmem_st16(s_at + 64 * half + 16 * h, p);
@@ -673,9 +694,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
       }
       if (both || st == 0) {
-        const int r = base + row;
         const bool mine = row < rows;
-        const size_t at = mine ? part_row(a, x, r, x.part) : 0;
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // l NaN: NaN
 #pragma unroll 1
         for (int cc = 0; cc < D / 2; cc += 32) {
@@ -697,7 +716,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
         if (mine && half == 0) a.part_lse[at] = bad ? NAN : (m + log2f(l)) * 0.6931471805599453f;
         if (mine && x.empty > 0) {
-          const size_t step = part_step(a, x, r);
           for (int k = 1; k <= x.empty; ++k) {
             float4* po = reinterpret_cast<float4*>(a.part_o + (at + k * step) * D + half * (D / 2));
             for (int e = 0; e < D / 8; ++e) po[e] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -715,8 +733,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
     give_registers();
     if constexpr (kQuant) {
       constexpr int kChunks = D / 16;        // 16-code chunks of a row
-      constexpr int kRows = 32 / kChunks;    // rows of a warp at a time
+      constexpr int kRows = 32 / kChunks;    // rows of a warp at a time: 4 or 8
       constexpr int kBatch = 4;
+      // Of this lane: where its codes of a batch's first row lie, and its two 16-byte pieces
+      // of f16, for rows 0..3 and 4..7 of a swizzle atom (with 8 rows at a time both are the
+      // same).  Rows of a batch are immediates away.
+      const int lr = lane / kChunks, lc = lane % kChunks;
+      uint32_t at0[2], at1[2];
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {
+        const int r = (lr + (kRows == 4 ? 4 * o : 0)) & 7;
+        at0[o] = (2 * lc >> 3) * S::kHalfBytes + lr * 128 + (((2 * lc & 7) ^ r) << 4);
+        at1[o] = (2 * lc >> 3) * S::kHalfBytes + lr * 128 + ((((2 * lc + 1) & 7) ^ r) << 4);
+      }
       const int cw = warp - kMmaWarp - 1;
       uint32_t fill = 0;
       Pieces it(a, lane);
@@ -727,19 +756,18 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           ok = mbar_wait_fast(&full[slot], (fill / kSlots) & 1);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          const uint8_t* codes = smem + S::kCodeOff + slot * S::kCodeStep;
+          const uint8_t* codes = smem + S::kCodeOff + slot * S::kCodeStep + lr * D + lc * 16;
           uint8_t* out = ring + slot * S::kTileBytes;
-          const int c = lane % kChunks;
 #pragma unroll 1
           for (int r0 = cw * kRows * kBatch; r0 < kTile; r0 += 2 * kRows * kBatch) {
             uint4 v[kBatch];
 #pragma unroll
             for (int e = 0; e < kBatch; ++e)
-              v[e] = *reinterpret_cast<const uint4*>(codes + (r0 + e * kRows + lane / kChunks) * D + c * 16);
+              v[e] = *reinterpret_cast<const uint4*>(codes + (r0 + e * kRows) * D);
             __syncwarp();
 #pragma unroll
             for (int e = 0; e < kBatch; ++e) {
-              const int r = r0 + e * kRows + lane / kChunks;
+              const int o = kRows == 4 ? e & 1 : 0;  // a batch begins at a multiple of 8 rows
               uint4 y0, y1;
               if constexpr (KV == VAS_FP8_E4M3) {
                 e4m3x4_to_f16x4(v[e].x, y0.x, y0.y);
@@ -752,10 +780,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
                 s8x4_to_f16x4(v[e].z, y1.x, y1.y);
                 s8x4_to_f16x4(v[e].w, y1.z, y1.w);
               }
-              uint8_t* row = out + (2 * c >> 3) * S::kHalfBytes + r * 128;
-              *reinterpret_cast<uint4*>(row + (((2 * c & 7) ^ (r & 7)) << 4)) = y0;
-              *reinterpret_cast<uint4*>(row + ((((2 * c + 1) & 7) ^ (r & 7)) << 4)) = y1;
+              uint8_t* row = out + (r0 + e * kRows) * 128;
+              *reinterpret_cast<uint4*>(row + at0[o]) = y0;
+              *reinterpret_cast<uint4*>(row + at1[o]) = y1;
             }
+          }
+          // The K scales of a tile (they came with its V) take the softmax scale along, in
+          // log2 units.
+          const int lead = min(x.rows > kTile ? 1 : 2, x.n_tiles);
+          const bool is_v = k >= lead && (((k - lead) & 1) == 0 || k >= 2 * x.n_tiles - lead);
+          if (is_v) {
+            float* sc = reinterpret_cast<float*>(smem + S::kScaleOff) + slot * 2 * kTile + cw * 64 + lane;
+            sc[0] *= a.scale_log2;
+            sc[32] *= a.scale_log2;
           }
           fence_proxy_async_smem();
           __syncwarp();
