@@ -233,6 +233,9 @@ int paged_attn_fwd_static(const void* q, const void* k_pages, const void* v_page
                           const int32_t* query_lens, void* out, float* lse,
                           const vas_attn_dims* dims, vas_stream_t stream);
 
+#define VAS_SHARE_AUTO 0
+#define VAS_SHARE_ALWAYS 1
+
 /* paged_attn_fwd for a batch whose sequences share prefixes.
  *
  * Defined by: "llm-inference-optimization-batching" (tempatgunting.com), section
@@ -255,9 +258,14 @@ int paged_attn_fwd_static(const void* q, const void* k_pages, const void* v_page
  * tree_mask   as for paged_attn_fwd_tree, or null.
  * dims->kv_dtype is VAS_BF16, VAS_FP8_E4M3 or VAS_INT8 (VAS_F32: VAS_E_UNSUPPORTED).
  * workspace   at least paged_attn_prefix_workspace_min(dims, num_groups) bytes.
- * A group is computed with its members apart, as paged_attn_fwd does, where sharing
- * would not pay (one member with query tokens, a short prefix) or the workspace has no
- * room for its partials.
+ * share       VAS_SHARE_AUTO: the prefixes of a batch are shared when that pays for the
+ *             extra kernels: when 48 Mi elements of K are read less, or in a small batch
+ *             (fewer than 64 Mi elements of K in all) when a prefix has 2048 tokens (1024
+ *             if the members' windows have more than 16 rows per KV head on average).
+ *             VAS_SHARE_ALWAYS: whenever they can be.
+ * A group is computed with its members apart, as paged_attn_fwd does, when it has one
+ * member with query tokens, when its prefix is below 256 tokens, where sharing would not
+ * pay, and where the workspace has no room for the partials.
  * Errors: those of paged_attn_fwd_quant.  A prefix_lens entry below 0 or past some
  * member's L_i - ql_i, or group_start out of order, sets VAS_DEV_BAD_LENGTHS; then no
  * group of the call is shared, and the members that their group's prefix does not fit,
@@ -270,7 +278,8 @@ int paged_attn_fwd_prefix(const void* q, const void* k_pages, const void* v_page
                           const int32_t* query_lens, const int32_t* group_start,
                           const int32_t* prefix_lens, const uint64_t* tree_mask, void* out,
                           float* lse, const vas_attn_dims* dims, int32_t num_groups,
-                          void* workspace, size_t workspace_bytes, vas_stream_t stream);
+                          int32_t share, void* workspace, size_t workspace_bytes,
+                          vas_stream_t stream);
 
 /* Recommended and smallest workspace of paged_attn_fwd_prefix (0 for invalid dims). */
 size_t paged_attn_prefix_workspace_size(const vas_attn_dims* dims, int32_t num_groups);

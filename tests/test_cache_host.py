@@ -224,12 +224,13 @@ def test_prefix_attention_refusals(vas_lib):
     d = dict(num_seqs=4, total_q_tokens=10, num_q_heads=32, num_kv_heads=8, head_dim=128, page_size=16,
              num_pages=100, max_pages_per_seq=10, kv_dtype=v.VAS_BF16, scale=0.0)
 
-    def call(start=FAKE, lens=FAKE, groups=2, nbytes=1 << 30, q=FAKE, ks=NULL, **kw):
+    def call(start=FAKE, lens=FAKE, groups=2, nbytes=1 << 30, q=FAKE, ks=NULL, share=0, **kw):
         dims = v.vas_attn_dims(**{**d, **kw})
         return v._lib.paged_attn_fwd_prefix(q, FAKE, FAKE, ks, NULL, FAKE, FAKE, FAKE, start, lens, NULL,
-                                            FAKE, FAKE, ctypes.byref(dims), groups, FAKE, nbytes, NULL)
+                                            FAKE, FAKE, ctypes.byref(dims), groups, share, FAKE, nbytes, NULL)
 
     bad, uns = v.VAS_E_INVALID_ARG, v.VAS_E_UNSUPPORTED
+    assert call(share=2) == bad and call(share=-1) == bad
     assert call(groups=-1) == bad and call(start=NULL) == bad and call(lens=NULL) == bad
     assert call(start=P_((1 << 20) + 2)) == bad and call(q=NULL) == bad and call(ks=FAKE) == bad
     assert call(num_q_heads=30) == bad and call(kv_dtype=v.VAS_FP8_E4M3) == bad

@@ -29,7 +29,8 @@ def shared_inputs(groups, Hq, Hkv, D, P, kv, seed):
     return a, np.asarray(start, np.int32), np.asarray(prefix, np.int32)
 
 
-def run_prefix(vas, a, start, prefix, masks=None, workspace_bytes=None, out=None, lse=None, ws=None):
+def run_prefix(vas, a, start, prefix, masks=None, workspace_bytes=None, out=None, lse=None, ws=None,
+               share="always"):
     d = a.q.device
     t = lambda x: torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).to(d)
     out = torch.empty_like(a.q) if out is None else out
@@ -41,7 +42,7 @@ def run_prefix(vas, a, start, prefix, masks=None, workspace_bytes=None, out=None
     tm = None if masks is None else torch.from_numpy(np.ascontiguousarray(masks).view(np.int64)).to(d)
     vas.paged_attn_fwd_prefix(a.q, a.k_pages, a.v_pages, a.block_table, a.seq_lens, a.query_lens,
                               t(start), t(prefix), out, lse, ws, k_scale=a.k_scale, v_scale=a.v_scale,
-                              quant=quant, tree_mask=tm, dims=dims)
+                              quant=quant, tree_mask=tm, share=share, dims=dims)
     torch.cuda.synchronize()
     return out, lse
 
@@ -273,7 +274,7 @@ def test_streams_and_graphs(vas_lib):
     dims = v.attn_dims(ad.q, ad.k_pages, ad.block_table, ad.seq_lens)
     ws = v.alloc_prefix_workspace(dims, 1)
     call = lambda: v.paged_attn_fwd_prefix(ad.q, ad.k_pages, ad.v_pages, ad.block_table, ad.seq_lens,
-                                           ad.query_lens, st, pl, out, lse, ws, dims=dims)
+                                           ad.query_lens, st, pl, out, lse, ws, share="always", dims=dims)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
@@ -328,3 +329,89 @@ def test_shared70b_full_size(vas_lib):
     assert float((out.float() - o1.float()).abs().max()) <= 2e-2
     assert float((lse - l1).abs().max()) <= 4e-3
     assert float((out.float() - o1.float()).norm() / o1.float().norm()) <= 1e-2
+
+
+def test_auto_shares_where_it_pays(vas_lib):
+    """Little to save: paged_attn_fwd's bits, and every member's own table is read.  Enough
+    (100 members on 2048 tokens, 8 KV heads: 198 Mi elements of K), or a long prefix in a small
+    batch: the prefix pages are the leader's."""
+    from gpu_common import run_gpu_attention
+    v = vas_lib
+    a, start, prefix = shared_inputs([(600, [(9, 1)] * 5), (300, [(40, 5), (1, 1)])], 32, 8, 128, 16, wl.BF16, 18)
+    ad = to_device(a)
+    o1, l1 = run_gpu_attention(v, ad)
+    o2, l2 = run_prefix(v, ad, start, prefix, share="auto")
+    assert torch.equal(o1, o2) and torch.equal(l1, l2)
+    for groups in ([(2048, [D1] * 100)], [(2048, [(9, 1)] * 2)], [(1024, [(9, 9)] * 3)]):
+        a, start, prefix = shared_inputs(groups, 16, 8, 128, 16, wl.BF16, 19)
+        ref_o, ref_l = oracle_attention(a)
+        ad = to_device(a)
+        ad.block_table[1:, :groups[0][0] // 16] = -1
+        out, lse = run_prefix(v, ad, start, prefix, share="auto")
+        assert v.vas_last_device_error() == 0
+        compare_attention(out, lse, ref_o, ref_l, wl.BF16)
+
+
+@pytest.mark.parametrize("kv", [wl.FP8, wl.INT8])
+def test_queries_beyond_the_f16_range(vas_lib, kv):
+    """|q| near 2^18 with the softmax scale divided by 2^16, behind a shared prefix of
+    quantised pages: the queries are brought into f16's range by a power of two."""
+    import oracle
+    v = vas_lib
+    a, start, prefix = shared_inputs([(500, [(20, 3), (1, 1), (7, 2)])], 32, 8, 128, 16, kv, 20)
+    a.q = (a.q.float() * 65536.0).to(torch.bfloat16)  # exact: a power of two
+    a.q[0] /= 65536.0                                 # one row of ordinary size among them
+    scale = 1.0 / (65536.0 * np.sqrt(128))
+    ref_o, ref_l = oracle.paged_attn_quant(
+        wl.bf16_bits(a.q), a.k_pages.numpy(), a.v_pages.numpy(), a.k_scale.numpy(), a.v_scale.numpy(),
+        a.block_table.numpy(), a.seq_lens.numpy(), a.query_lens.numpy(),
+        fmt=oracle.Q_E4M3 if kv == wl.FP8 else oracle.Q_INT8, scale=scale)
+    ad = to_device(a)
+    dims = v.attn_dims(ad.q, ad.k_pages, ad.block_table, ad.seq_lens, scale=scale, quant=kv)
+    out, lse = torch.empty_like(ad.q), torch.empty(ad.q.shape[:2], device="cuda")
+    ws = v.alloc_prefix_workspace(dims, 1)
+    t = lambda x: torch.from_numpy(x).cuda()
+    v.paged_attn_fwd_prefix(ad.q, ad.k_pages, ad.v_pages, ad.block_table, ad.seq_lens, ad.query_lens, t(start),
+                            t(prefix), out, lse, ws, k_scale=ad.k_scale, v_scale=ad.v_scale, quant=kv,
+                            share="always", dims=dims)
+    torch.cuda.synchronize()
+    compare_attention(out, lse, ref_o, ref_l, kv)
+
+
+def test_two_layers_share_a_workspace_in_a_graph(vas_lib):
+    """Two captured calls on one workspace, one behind the other, and two graphs replayed in
+    turn: each gives its own result."""
+    v = vas_lib
+    cases = []
+    for seed, members in ((21, 9), (22, 30)):
+        a, start, prefix = shared_inputs([(800, [D1] * members + [(30, 5)])], 16, 2, 128, 16, wl.BF16, seed)
+        ad = to_device(a)
+        want = run_prefix(v, ad, start, prefix)
+        t = lambda x: torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()
+        cases.append((ad, t(start), t(prefix), torch.empty_like(want[0]), torch.empty_like(want[1]), want))
+    dims = [v.attn_dims(c[0].q, c[0].k_pages, c[0].block_table, c[0].seq_lens) for c in cases]
+    ws = torch.empty(max(v.paged_attn_prefix_workspace_size(d, 1) for d in dims), dtype=torch.uint8, device="cuda")
+
+    def call(c, d):
+        a = c[0]
+        v.paged_attn_fwd_prefix(a.q, a.k_pages, a.v_pages, a.block_table, a.seq_lens, a.query_lens, c[1], c[2],
+                                c[3], c[4], ws, share="always", dims=d)
+
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        graphs = []
+        for order in ((0, 1), (1, 0, 1)):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=s):
+                for i in order:
+                    call(cases[i], dims[i])
+            graphs.append(g)
+        for c in cases:
+            c[3].zero_()
+        for k in (0, 1, 0, 0, 1):
+            graphs[k].replay()
+    s.synchronize()
+    for c in cases:
+        assert torch.equal(c[3], c[5][0]) and torch.equal(c[4], c[5][1])
+    assert v.vas_last_device_error() == 0

@@ -45,6 +45,8 @@ VAS_F32 = 0
 VAS_BF16 = 1
 VAS_FP8_E4M3 = 2
 VAS_INT8 = 3
+VAS_SHARE_AUTO = 0
+VAS_SHARE_ALWAYS = 1
 
 _c_void_p, _i32, _i64, _u32, _u64, _f32, _sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                                                   ctypes.c_uint32, ctypes.c_uint64, ctypes.c_float,
@@ -80,7 +82,7 @@ _sig = {
     "paged_attn_fwd": ([_c_void_p] * 8 + [_P_dims, _c_void_p, _sz, _c_void_p], ctypes.c_int),
     "paged_attn_fwd_tree": ([_c_void_p] * 9 + [_P_dims, _c_void_p, _sz, _c_void_p], ctypes.c_int),
     "paged_attn_fwd_quant": ([_c_void_p] * 11 + [_P_dims, _c_void_p, _sz, _c_void_p], ctypes.c_int),
-    "paged_attn_fwd_prefix": ([_c_void_p] * 13 + [_P_dims, _i32, _c_void_p, _sz, _c_void_p],
+    "paged_attn_fwd_prefix": ([_c_void_p] * 13 + [_P_dims, _i32, _i32, _c_void_p, _sz, _c_void_p],
                               ctypes.c_int),
     "paged_attn_prefix_workspace_size": ([_P_dims, _i32], _sz),
     "paged_attn_prefix_workspace_min": ([_P_dims, _i32], _sz),
@@ -151,6 +153,7 @@ _KV_CODES = {torch.bfloat16: VAS_BF16, torch.float32: VAS_F32}
 
 
 _QUANT_CODES = {"fp8": VAS_FP8_E4M3, "int8": VAS_INT8}
+_SHARE_CODES = {"auto": VAS_SHARE_AUTO, "always": VAS_SHARE_ALWAYS}
 
 
 def attn_dims(q: torch.Tensor, k_pages: torch.Tensor, block_table: torch.Tensor,
@@ -293,11 +296,15 @@ def alloc_prefix_workspace(dims: vas_attn_dims, num_groups: int, device=None,
 
 def paged_attn_fwd_prefix(q, k_pages, v_pages, block_table, seq_lens, query_lens, group_start,
                           prefix_lens, out, lse, workspace, *, k_scale=None, v_scale=None,
-                          quant: Optional[str] = None, tree_mask=None, scale: float = 0.0,
-                          dims: Optional[vas_attn_dims] = None, stream=None) -> None:
+                          quant: Optional[str] = None, tree_mask=None, share: str = "auto",
+                          scale: float = 0.0, dims: Optional[vas_attn_dims] = None,
+                          stream=None) -> None:
     """Attention of groups of sequences that share a prefix (include/vas.h:
-    paged_attn_fwd_prefix).  group_start [G + 1] and prefix_lens [G] int32; the other
-    arguments are those of paged_attn_fwd, or with quant those of paged_attn_fwd_quant."""
+    paged_attn_fwd_prefix).  group_start [G + 1] and prefix_lens [G] int32; share "auto"
+    (where it pays) or "always"; the other arguments are those of paged_attn_fwd, or with
+    quant those of paged_attn_fwd_quant."""
+    if share not in _SHARE_CODES:
+        raise ValueError('share is "auto" or "always"')
     if dims is None:
         dims = attn_dims(q, k_pages, block_table, seq_lens, scale, quant=quant)
     dev = torch.cuda.current_device()
@@ -317,7 +324,7 @@ def paged_attn_fwd_prefix(q, k_pages, v_pages, block_table, seq_lens, query_lens
         _here(dev, group_start, "group_start", (G + 1,), i32),
         _here(dev, prefix_lens, "prefix_lens", (G,), i32), _here(dev, tree_mask, "tree_mask"),
         _here(dev, out, "out", q.shape, q.dtype), _here(dev, lse, "lse", q.shape[:2], f32),
-        ctypes.byref(dims), G, _here(dev, workspace, "workspace"),
+        ctypes.byref(dims), G, _SHARE_CODES[share], _here(dev, workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _stream_address(dev, stream))
     _check("paged_attn_fwd_prefix", st)
 

@@ -105,6 +105,16 @@ constexpr int kSeqInvalid = 1;
 // Shared prefixes (paged_attn_fwd_prefix).
 constexpr int kMinPrefixTokens = 256;  // shorter ones are left to the members
 constexpr int kMinPrefixShare = 4;     // units of weight of a CTA, at least
+// What makes sharing pay (VAS_SHARE_AUTO).  It costs two more kernels and a longer plan, 15 to
+// 20 us.  A large batch is bound by its reading: it has to read this many elements of K (and as
+// many of V) less.  64/8 heads, bf16, one group, shared against apart: 64 members on 1024 tokens
+// (63 Mi) 64 and 62 us, on 512 tokens (31 Mi) 60 and 46, 32 on 2048 (62 Mi) 55 and 64, eight
+// groups of 8 on 2048 (112 Mi) 63 and 109.  A small one, with fewer elements of K in all than
+// kSmallBatch, is bound by its longest unit: 4 members on 2048 tokens 39 and 48 us, on 1024
+// tokens 39 and 34, but 56 and 64 for windows of five tokens, whose units take twice as long.
+constexpr int64_t kMinPrefixSaved = 48ll << 20;
+constexpr int64_t kSmallBatch = 64ll << 20;
+constexpr int64_t kLongPrefix = 2048;
 
 // What the producer hands the consumers for one unit (u < 0: no more work).
 struct RingEntry {
@@ -116,7 +126,7 @@ struct RingEntry {
 
 struct Layout {
   size_t seqplan, token_seq, items, order, counters, part_lse, part_o, total;
-  size_t row0, shared, entry, groups;  // shared-prefix calls only
+  size_t row0, active0, shared, entry, groups;  // shared-prefix calls only
   int64_t items_cap, partial_cap;
 };
 
@@ -143,8 +153,9 @@ struct PlanArgs {
   // Shared prefixes: the groups as the caller gives them, and what the plan makes of them.
   const int32_t* group_start;
   const int32_t* prefix_lens;
-  int32_t num_groups, sms;
+  int32_t num_groups, sms, share;  // share: VAS_SHARE_AUTO or VAS_SHARE_ALWAYS
   int32_t* row0;        // [B + 1] first query token of each sequence
+  int32_t* active0;     // [B + 1] sequences with query tokens before each
   int32_t* shared;      // [B] entry of `groups` that shares a sequence's prefix; -1: none
   int32_t* entry;       // [num_groups] entry of a group the caller gave, or -1
   PrefixGroup* groups;  // the shared ones, at most num_groups
@@ -307,14 +318,16 @@ __device__ bool plan_prefixes(const PlanArgs& a, ShapeFn shape, int64_t (*red)[4
   __syncthreads();
   const bool order_ok = s_bad == 0;
   // First query token of each sequence, its group, and whether the group's prefix fits it.
-  int64_t carry[1] = {0};
+  int64_t carry[3] = {0, 0, 0};  // query tokens, sequences that have some, elements of K
   bool misfit = false, invalid = false;
   for (int base = 0; base < a.B; base += kPlanThreads) {
     const int i = base + tid;
-    int64_t v[1] = {0}, t[1];
+    int64_t v[3] = {0, 0, 0}, t[3];
     if (i < a.B) {
       const SeqShape s = shape(i);
       v[0] = s.ql > 0 ? s.ql : 0;
+      v[1] = s.ql > 0;
+      v[2] = s.valid && s.ql > 0 ? (int64_t)s.L * a.Hkv * a.D : 0;
       invalid |= !s.valid;
       int32_t mark = -1;
       if (order_ok && s.valid && s.ql > 0) {
@@ -324,12 +337,19 @@ __device__ bool plan_prefixes(const PlanArgs& a, ShapeFn shape, int64_t (*red)[4
       misfit |= mark == -2;
       a.shared[i] = mark;
     }
-    block_scan<1>(v, red, t);
+    block_scan<3>(v, red, t);
     const int64_t at = v[0] + carry[0];
-    if (i < a.B) a.row0[i] = (int32_t)(at < a.T ? at : a.T);
-    carry[0] += t[0];
+    if (i < a.B) {
+      a.row0[i] = (int32_t)(at < a.T ? at : a.T);
+      a.active0[i] = (int32_t)(v[1] + carry[1]);
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) carry[k] += t[k];
   }
-  if (tid == 0) a.row0[a.B] = (int32_t)(carry[0] < a.T ? carry[0] : a.T);
+  if (tid == 0) {
+    a.row0[a.B] = (int32_t)(carry[0] < a.T ? carry[0] : a.T);
+    a.active0[a.B] = (int32_t)carry[1];
+  }
   if (misfit) atomicOr(&s_bad, 1);   // groups that do not fit the batch
   if (invalid) atomicOr(&s_bad, 2);  // lengths that paged_attn_fwd refuses
   __syncthreads();
@@ -342,35 +362,36 @@ __device__ bool plan_prefixes(const PlanArgs& a, ShapeFn shape, int64_t (*red)[4
   }
 
   // The groups worth sharing, one behind the other, and their spans of work.
-  int64_t at[2] = {0, 0};  // entries, units of weight
+  int64_t at[3] = {0, 0, 0};  // entries, units of weight, elements of K not read again
   for (int base = 0; base < a.num_groups; base += kPlanThreads) {
     const int g = base + tid;
     PrefixGroup pg;
-    int64_t v[2] = {0, 0}, t[2];
+    int64_t v[3] = {0, 0, 0}, t[3];
     if (g < a.num_groups) {
       pg.seq0 = a.group_start[g];
       pg.seq1 = a.group_start[g + 1];
       pg.qrow0 = a.row0[pg.seq0];
       pg.rows = (int32_t)((a.row0[pg.seq1] - pg.qrow0) * (int64_t)a.G);
       pg.pages = a.prefix_lens[g] / a.P;
-      pg.leader = pg.seq0;
       pg.parts = 0;
       // The first member with query tokens is the leader; alone it has nothing to share.
-      int32_t first = pg.seq0;
-      while (first < pg.seq1 && a.row0[first + 1] == pg.qrow0) ++first;
-      const bool alone = first >= pg.seq1 || a.row0[first + 1] == a.row0[pg.seq1];
-      pg.leader = first;
+      pg.leader = pg.seq0;
+      while (pg.leader + 1 < pg.seq1 && a.row0[pg.leader + 1] == pg.qrow0) ++pg.leader;
+      const int32_t members = a.active0[pg.seq1] - a.active0[pg.seq0];
       pg.tiles = (pg.pages * a.P + kPrefixTile - 1) / kPrefixTile;
       pg.blocks = (int32_t)prefix_blocks(pg.rows) * a.Hkv;
       // A tile feeds one stream or two, according to the rows.
       pg.weight = pg.rows > kPrefixRows / 2 ? 2 : 1;
-      if (!alone && pg.pages * a.P >= kMinPrefixTokens) {
+      if (members > 1 && pg.pages * a.P >= kMinPrefixTokens) {
         v[0] = 1;
         v[1] = ((int64_t)pg.blocks * pg.tiles * pg.weight + 1) & ~1ll;
+        v[2] = (int64_t)(members - 1) * pg.pages * a.P * a.Hkv * a.D;
+        const int64_t reach = (int64_t)pg.pages * a.P * (pg.rows > kNarrowRows * members ? 2 : 1);
+        if (carry[2] < kSmallBatch && reach >= kLongPrefix) v[2] += kMinPrefixSaved;
       }
     }
     const bool share = v[0] != 0;
-    block_scan<2>(v, red, t);
+    block_scan<3>(v, red, t);
     if (share) {
       const int32_t e = (int32_t)(at[0] + v[0]);
       pg.base = (int32_t)(at[1] + v[1] < INT_MAX ? at[1] + v[1] : INT_MAX);
@@ -379,11 +400,13 @@ __device__ bool plan_prefixes(const PlanArgs& a, ShapeFn shape, int64_t (*red)[4
     }
     at[0] += t[0];
     at[1] += t[1];
+    at[2] += t[2];
   }
   __syncthreads();
   const int n = (int)at[0];
   const int64_t span = at[1];
-  if (span > INT_MAX / 2) {  // past 32-bit unit numbers: minutes of work
+  // Too little to gain, or work past 32-bit unit numbers (minutes of it).
+  if ((a.share == VAS_SHARE_AUTO && at[2] < kMinPrefixSaved) || span > INT_MAX / 2) {
     for (int i = tid; i < a.B; i += kPlanThreads)
       if (a.shared[i] >= 0) a.shared[i] = -1;
     return fine;
@@ -2679,9 +2702,11 @@ Layout make_layout(const vas_attn_dims* d, int64_t items_cap, int64_t partial_ca
                    int32_t num_groups = -1) {
   Layout L;
   size_t off = align_up(sizeof(PlanHeader), 256);
-  L.row0 = L.shared = L.entry = L.groups = 0;
+  L.row0 = L.active0 = L.shared = L.entry = L.groups = 0;
   if (num_groups >= 0) {
     L.row0 = off;
+    off = align_up(off + ((size_t)d->num_seqs + 1) * 4, 256);
+    L.active0 = off;
     off = align_up(off + ((size_t)d->num_seqs + 1) * 4, 256);
     L.shared = off;
     off = align_up(off + (size_t)d->num_seqs * 4, 256);
@@ -2861,7 +2886,7 @@ namespace {
 struct PrefixCall {
   const int32_t* group_start;
   const int32_t* prefix_lens;
-  int32_t num_groups;
+  int32_t num_groups, share;
 };
 
 // Rows behind shared prefixes, after the attention of the call.
@@ -2960,6 +2985,8 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
   pa.prefix_lens = prefix ? prefix->prefix_lens : nullptr;
   pa.num_groups = prefix ? prefix->num_groups : 0;
   pa.sms = sms;
+  pa.share = prefix ? prefix->share : VAS_SHARE_AUTO;
+  pa.active0 = reinterpret_cast<int32_t*>(ws + lay.active0);
   pa.row0 = reinterpret_cast<int32_t*>(ws + lay.row0);
   pa.shared = reinterpret_cast<int32_t*>(ws + lay.shared);
   pa.groups = reinterpret_cast<PrefixGroup*>(ws + lay.groups);
@@ -3121,13 +3148,15 @@ int paged_attn_fwd_prefix(const void* q, const void* k_pages, const void* v_page
                           const int32_t* query_lens, const int32_t* group_start,
                           const int32_t* prefix_lens, const uint64_t* tree_mask, void* out,
                           float* lse, const vas_attn_dims* dims, int32_t num_groups,
-                          void* workspace, size_t workspace_bytes, vas_stream_t stream) {
+                          int32_t share, void* workspace, size_t workspace_bytes,
+                          vas_stream_t stream) {
   if (!dims || num_groups < 0) return VAS_E_INVALID_ARG;
+  if (share != VAS_SHARE_AUTO && share != VAS_SHARE_ALWAYS) return VAS_E_INVALID_ARG;
   if (dims->kv_dtype == VAS_F32) return VAS_E_UNSUPPORTED;
   if (num_groups > 0 && (!group_start || !prefix_lens)) return VAS_E_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(group_start) | reinterpret_cast<uintptr_t>(prefix_lens)) & 3)
     return VAS_E_INVALID_ARG;
-  const PrefixCall px{group_start, prefix_lens, num_groups};
+  const PrefixCall px{group_start, prefix_lens, num_groups, share};
   return attn_launch(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, query_lens,
                      tree_mask, out, lse, dims, workspace, workspace_bytes, stream,
                      num_groups > 0 ? &px : nullptr);

@@ -166,30 +166,6 @@ struct PSmem {
   static_assert(kTile * D * 4 <= 2 * kTileBytes, "stream 1's O fits over the query tiles");
 };
 
-// 64 columns of this thread's lane, as two groups of 32.
-__device__ __forceinline__ void tmem_ld2x32(uint32_t taddr, uint32_t (&x)[32], uint32_t (&y)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,"
-      "%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]),
-        "=r"(x[6]), "=r"(x[7]), "=r"(x[8]), "=r"(x[9]), "=r"(x[10]), "=r"(x[11]),
-        "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]),
-        "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]),
-        "=r"(x[24]), "=r"(x[25]), "=r"(x[26]), "=r"(x[27]), "=r"(x[28]), "=r"(x[29]),
-        "=r"(x[30]), "=r"(x[31]),
-        "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]), "=r"(y[4]), "=r"(y[5]),
-        "=r"(y[6]), "=r"(y[7]), "=r"(y[8]), "=r"(y[9]), "=r"(y[10]), "=r"(y[11]),
-        "=r"(y[12]), "=r"(y[13]), "=r"(y[14]), "=r"(y[15]), "=r"(y[16]), "=r"(y[17]),
-        "=r"(y[18]), "=r"(y[19]), "=r"(y[20]), "=r"(y[21]), "=r"(y[22]), "=r"(y[23]),
-        "=r"(y[24]), "=r"(y[25]), "=r"(y[26]), "=r"(y[27]), "=r"(y[28]), "=r"(y[29]),
-        "=r"(y[30]), "=r"(y[31])
-      : "r"(taddr), "r"(taddr + 32)
-      : "memory");
-}
-
 // 16 columns of this thread's lane, not waited for.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&x)[16]) {
   asm volatile(
@@ -584,19 +560,21 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         named_bar_sync(1 + st, kStreamThreads);
         top = fmaxf(top, *other_stat);
         const bool rebase = top > m + kRebase;
-        const float alpha = rebase ? exp2f(m - top) : 1.f;
-        if (rebase) {
-          l *= alpha;
-          m = top;
-        }
-        if (__any_sync(0xffffffffu, rebase && i > 0)) {
+        if (__any_sync(0xffffffffu, rebase)) {
+          const float alpha = rebase ? exp2f(m - top) : 1.f;
+          if (rebase) {
+            l *= alpha;
+            m = top;
+          }
+          if (i > 0) {
 #pragma unroll 1
-          for (int cc = 0; cc < D / 2; cc += 32) {
-            uint32_t ov[32];
-            tmem_ld32(o_at + cc, ov);
+            for (int cc = 0; cc < D / 2; cc += 32) {
+              uint32_t ov[32];
+              tmem_ld32(o_at + cc, ov);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-            tmem_st32(o_at + cc, ov);
+              for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+              tmem_st32(o_at + cc, ov);
+            }
           }
         }
         const float mu = m == -INFINITY ? 0.f : m;
