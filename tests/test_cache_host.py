@@ -182,6 +182,10 @@ def test_copy_refusals(vas_lib):
     assert _copy(v, [1, 2], [3, 3]) == bad            # one target twice
     assert _copy(v, [1, 2], [2, 3]) == bad            # a target that is also a source
     assert _copy(v, [1], [1]) == bad
+    for pages in (100, 100000):                       # the pairs in a map of the pool, or sorted
+        assert _copy(v, [1, 2, 9], [3, 4, 3], num_pages=pages) == bad
+        assert _copy(v, [1, 2, 9], [3, 9, 5], num_pages=pages) == bad
+        assert _copy(v, [1, 2, 9], [3, 4, pages], num_pages=pages) == bad
     assert _copy(v, [1], [100]) == bad and _copy(v, [-1], [4]) == bad
     assert _copy(v, [1], [2], tokens=[0]) == bad and _copy(v, [1], [2], tokens=[17]) == bad
     assert _copy(v, [1], [2], n=-1) == bad

@@ -258,24 +258,31 @@ def _here(dev: int, t: Optional[torch.Tensor], name: str, shape=None, dtype=None
     """The address of a contiguous tensor on device `dev` (None: a null pointer)."""
     if t is None:
         return None
+    if (t.get_device() == dev and (shape is None or t.shape == shape) and
+            (dtype is None or t.dtype is dtype) and t.is_contiguous()):
+        return t.data_ptr()
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
     if t.get_device() != dev:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
+
+
+# The current stream as an address, without the Stream object around it (1 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_address(dev: int, stream: Optional[torch.cuda.Stream]) -> int:
     """The cudaStream_t of `stream`, or of the current stream of device `dev`."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(dev)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def paged_attn_prefix_workspace_size(dims: vas_attn_dims, num_groups: int) -> int:

@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -743,6 +744,26 @@ int check_pool(const vas_pool_dims* d, const void* k, const void* v, const float
   return VAS_OK;
 }
 
+// Whether the destinations are distinct and none is a source.  A few pairs are sorted, many
+// are marked in a map of the pool (which is cleared for it: 0.1 ms for a million pages).
+bool targets_apart(const int32_t* src, const int32_t* dst, int32_t n, int32_t num_pages) {
+  if ((int64_t)n * 32 < num_pages) {
+    std::vector<int32_t> d(dst, dst + n);
+    std::sort(d.begin(), d.end());
+    if (std::adjacent_find(d.begin(), d.end()) != d.end()) return false;
+    for (int32_t i = 0; i < n; ++i)
+      if (std::binary_search(d.begin(), d.end(), src[i])) return false;
+    return true;
+  }
+  std::vector<uint8_t> seen(static_cast<size_t>(num_pages), 0);
+  for (int32_t i = 0; i < n; ++i) seen[src[i]] = 1;
+  for (int32_t i = 0; i < n; ++i) {
+    if (seen[dst[i]]) return false;
+    seen[dst[i]] = 1;
+  }
+  return true;
+}
+
 template <int N>
 int launch_copy(CopyArgs a, const int32_t* src, const int32_t* dst, const int32_t* tokens,
                 int32_t n, int32_t layers, vas_stream_t stream) {
@@ -866,19 +887,13 @@ int paged_kv_copy(void* k_pages, void* v_pages, float* k_scale, float* v_scale,
   if (st != VAS_OK) return st;
   if (n < 0 || (n > 0 && (!src || !dst))) return VAS_E_INVALID_ARG;
   if (n == 0 || dims->num_layers == 0) return VAS_OK;
-  // Every id in the pool, destinations distinct and apart from the sources.
+  for (int32_t i = 0; i < n; ++i) {
+    if (src[i] < 0 || src[i] >= dims->num_pages || dst[i] < 0 || dst[i] >= dims->num_pages)
+      return VAS_E_INVALID_ARG;
+    if (tokens && (tokens[i] < 1 || tokens[i] > dims->page_size)) return VAS_E_INVALID_ARG;
+  }
   try {
-    std::vector<uint8_t> seen(static_cast<size_t>(dims->num_pages), 0);  // 1 source, 2 target
-    for (int32_t i = 0; i < n; ++i) {
-      if (src[i] < 0 || src[i] >= dims->num_pages || dst[i] < 0 || dst[i] >= dims->num_pages)
-        return VAS_E_INVALID_ARG;
-      if (tokens && (tokens[i] < 1 || tokens[i] > dims->page_size)) return VAS_E_INVALID_ARG;
-      seen[src[i]] |= 1;
-    }
-    for (int32_t i = 0; i < n; ++i) {
-      if (seen[dst[i]]) return VAS_E_INVALID_ARG;
-      seen[dst[i]] = 2;
-    }
+    if (!targets_apart(src, dst, n, dims->num_pages)) return VAS_E_INVALID_ARG;
   } catch (const std::bad_alloc&) {
     return VAS_E_NOMEM;
   }
