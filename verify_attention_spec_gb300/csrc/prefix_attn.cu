@@ -166,6 +166,19 @@ struct PSmem {
   static_assert(kTile * D * 4 <= 2 * kTileBytes, "stream 1's O fits over the query tiles");
 };
 
+// 16 columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // 16 columns of this thread's lane, not waited for.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&x)[16]) {
   asm volatile(
@@ -500,18 +513,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[st]);
       }
-      // Bad pages of the piece: this thread looks at every 256th.
-      bool bad = false;
-      {
-        const int32_t* bt = a.block_table + (size_t)x.g.leader * a.maxp + x.page_begin;
-        for (int pg = tid; pg < x.tokens / P; pg += kStreamThreads) {
-          const int32_t id = bt[pg];
-          bad |= id < 0 || id >= a.num_pages;
-        }
-      }
-      // Where this thread's row goes: looked up while the first scores are computed.
-      size_t step;
-      const size_t at = part_row(a, x, base + min(row, rows - 1), lane, &step);
       const int n_mine = both ? x.n_tiles : (x.n_tiles - st + 1) / 2;
       float m = -INFINITY, l = 0.f;
       for (int i = 0; i < n_mine; ++i, ++n_s) {
@@ -634,6 +635,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[st]);
       }
       used += 2 * x.n_tiles;
+      // While the last products run: bad pages of the piece, where the row goes.
+      // Bad pages of the piece: this thread looks at every 256th.
+      bool bad = false;
+      {
+        const int32_t* bt = a.block_table + (size_t)x.g.leader * a.maxp + x.page_begin;
+        for (int pg = tid; pg < x.tokens / P; pg += kStreamThreads) {
+          const int32_t id = bt[pg];
+          bad |= id < 0 || id >= a.num_pages;
+        }
+      }
+      // Where this thread's row goes.
+      size_t step;
+      const size_t at = part_row(a, x, base + min(row, rows - 1), lane, &step);
       if (n_mine > 0) {
         wait(&o_full[st], n_o);
         ++n_o;
@@ -674,23 +688,54 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
       if (both || st == 0) {
         const bool mine = row < rows;
         const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // l NaN: NaN
+        // A thread holds a row, but memory wants rows written by warps: kWide columns of the
+        // warp's 32 rows at a time go through shared memory, a line a row.  (A row a thread, 16
+        // bytes at a time, took 3.6 us of a piece.)  The lines are the stream's query tile, or
+        // in a merge the part of the dump that this warp alone reads.
+        constexpr int kWide = D / 4, kPer = kWide / 4;  // columns, 16-byte chunks of a line
+        constexpr int kAtOnce = 32 / kPer;              // lines of a store
+        auto swizzle = [](int r) { return kWide == 32 ? r & 7 : (r >> 1) & 3; };
 #pragma unroll 1
-        for (int cc = 0; cc < D / 2; cc += 32) {
-          uint32_t ov[32];
-          tmem_ld32(o_at + cc, ov);
-          if (!mine) continue;
-          float4* po = reinterpret_cast<float4*>(a.part_o + at * D + half * (D / 2) + cc);
+        for (int cc = 0; cc < D / 2; cc += kWide) {
+          uint32_t ov[kWide];
+          if constexpr (kWide == 32) tmem_ld32(o_at + cc, ov);
+          else tmem_ld16(o_at + cc, ov);
+          float4* lines;
+          int step16;  // 16-byte chunks from line to line
+          if (merge) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < kWide; ++e)
+              ov[e] = __float_as_uint(__uint_as_float(ov[e]) * f0 + dump[(cc + e) * kTile + row] * f1);
+            // Columns cc .. of rows 32 w ..: kWide lines of 128 bytes, two to a line if narrow.
+            lines = reinterpret_cast<float4*>(dump + cc * kTile + (row & ~31));
+            step16 = kTile / 4;
+            __syncwarp();
+          } else {
+            lines = reinterpret_cast<float4*>(smem + st * S::kTileBytes) +
+                    (warp % kStreamWarps) * (32 * kPer);
+            step16 = 8;
+          }
+          auto line = [&](int r) {  // of row r of the warp's 32
+            return kWide == 32 ? lines + r * step16 : lines + (r >> 1) * step16 + (r & 1) * kPer;
+          };
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
             float v[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float o = __uint_as_float(ov[4 * e + k]);
-              if (merge) o = o * f0 + dump[(cc + 4 * e + k) * kTile + row] * f1;
-              v[k] = bad ? NAN : o * inv;
-            }
-            po[e] = make_float4(v[0], v[1], v[2], v[3]);
+            for (int k = 0; k < 4; ++k) v[k] = bad ? NAN : __uint_as_float(ov[4 * e + k]) * inv;
+            line(lane)[e ^ swizzle(lane)] = make_float4(v[0], v[1], v[2], v[3]);
           }
+          __syncwarp();
+          const int r_last = rows - (row & ~31);  // of this warp's rows
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            const int r = k * kAtOnce + lane / kPer, e = lane % kPer;
+            const size_t to = __shfl_sync(0xffffffffu, at, r);
+            if (r < r_last)
+              *reinterpret_cast<float4*>(a.part_o + to * D + half * (D / 2) + cc + 4 * e) =
+                  line(r)[e ^ swizzle(r)];
+          }
+          __syncwarp();
         }
         if (mine && half == 0) a.part_lse[at] = bad ? NAN : (m + log2f(l)) * 0.6931471805599453f;
         if (mine && x.empty > 0) {
@@ -702,7 +747,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         }
       }
       if (bad && tid == 0 && st == 0) atomicOr(a.err, VAS_DEV_BAD_PAGE);
-      if (!both) named_bar_sync(3, 2 * kStreamThreads);  // the dump is read: Q may be staged
+      // The dump, or the stream's lines, are read: the next query tile may be staged.
+      if (both) named_bar_sync(1 + st, kStreamThreads);
+      else named_bar_sync(3, 2 * kStreamThreads);
     }
   } else {
     // ------------------------------ converters ------------------------------
