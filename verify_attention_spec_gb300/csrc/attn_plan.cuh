@@ -12,7 +12,9 @@ namespace attn {
 
 struct SeqPlan {
   int32_t qrow0;         // first row of q / out / lse
-  int32_t nsplit;        // KV splits; 0 = nothing to compute (invalid or no query)
+  int32_t nsplit;        // partials of a row; 0 = nothing to compute (invalid or no query);
+                         // negative: behind a shared prefix, merged by merge_shared_kernel
+                         // and not by the last split
   int32_t partial_base;  // first partial row (nsplit > 1)
   int32_t len;           // L
   int32_t qlen;          // ql

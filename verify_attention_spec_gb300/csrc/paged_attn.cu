@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
       const int64_t n_my_items = (int64_t)ns * s.nrb;
       const bool fits = my_row0 + qrows <= a.T && my_item0 + n_my_items <= a.items_cap;
       if (!fits) sp.flags |= kSeqInvalid;
-      sp.nsplit = (s.valid && fits) ? np : 0;
+      sp.nsplit = (s.valid && fits) ? (s.parts > 0 ? -np : np) : 0;
       sp.nrb = s.nrb;
       sp.partial_base = (int32_t)my_part0;
       sp.item0 = (int32_t)(my_item0 < a.items_cap ? my_item0 : 0);
@@ -584,9 +584,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
           const int32_t pb = (int32_t)(sp_i * cs);
           const int32_t pe = (int32_t)((sp_i + 1) * cs < s.npages ? (sp_i + 1) * cs : s.npages);
           for (int rb = 0; rb < s.nrb && it < a.items_cap; ++rb) {
-            const bool prec = a.is_bf16 && sp.nsplit > 0 && rb_precise(a, s, my_row0, rb);
+            const bool prec = a.is_bf16 && sp.nsplit != 0 && rb_precise(a, s, my_row0, rb);
             Item item;
-            item.seq = sp.nsplit > 0 ? i : -1;
+            item.seq = sp.nsplit != 0 ? i : -1;
             item.page_begin = s.page0 + pb;
             item.page_end = s.page0 + pe;
             item.split_rb = (sp_i << kRbBits) | rb | (prec ? kItemPrecise : 0);
@@ -594,9 +594,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs a) {
           }
         }
       }
-      // Arrival counters of the last-split merge.  Behind a shared prefix no split is the
-      // last (the count never gets to nsplit - 1): merge_shared_kernel merges those rows.
-      if (sp.nsplit > 1)
+      if (sp.nsplit > 1)  // arrival counters of the last-split merge
         for (int k = 0; k < s.nrb * a.Hkv; ++k) a.counters[(size_t)sp.item0 * a.Hkv + k] = 0;
     }
 #pragma unroll
@@ -1289,7 +1287,7 @@ __global__ void __launch_bounds__(256) merge_shared_kernel(const AttnArgs a, con
     }
     const int group = shared[lo];
     const SeqPlan sp = a.seqplan[lo];
-    const int n = sp.nsplit;
+    const int n = -sp.nsplit;
     if (group < 0 || n < 2) continue;
     const size_t per_head = (size_t)a.G * sp.qlen, step = a.Hkv * per_head;
     const size_t base = sp.partial_base + (size_t)(t - sp.qrow0) * a.G;

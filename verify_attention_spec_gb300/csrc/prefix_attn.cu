@@ -103,7 +103,7 @@ __device__ __forceinline__ size_t part_row(const PrefixArgs& a, const Piece& p, 
   while (lo + 1 < p.g.seq1 && a.row0[lo + 1] <= t) ++lo;
   const SeqPlan sp = a.seqplan[lo];
   *step = (size_t)a.Hkv * ((size_t)a.G * sp.qlen);
-  return partial_index(sp, a.Hkv, a.G, sp.nsplit - p.g.parts + p.part, p.head,
+  return partial_index(sp, a.Hkv, a.G, -sp.nsplit - p.g.parts + p.part, p.head,
                        (t - sp.qrow0) * a.G + (r - j * a.G));
 }
 
