@@ -220,7 +220,8 @@ class ClockSampler:
 # ncu evidence (committed summary): DRAM traffic per launch of the attention kernel,
 # valid only while the kernel source is unchanged.
 # ---------------------------------------------------------------------------------
-KERNEL_SOURCES = {"paged_attn": ["paged_attn.cu", "device_util.cuh"],
+KERNEL_SOURCES = {"paged_attn": ["paged_attn.cu", "attn_plan.cuh", "device_util.cuh",
+                                 "packed_math.cuh"],
                   "spec_verify": ["spec_verify.cu", "device_util.cuh", "philox.cuh"],
                   "spec_verify_tree": ["spec_verify_tree.cu", "device_util.cuh", "philox.cuh"]}
 

@@ -252,6 +252,15 @@ def test_binding_refusals(vas_lib):
         run_prefix(v, ad, start, np.array([300, 1]))
     with pytest.raises(ValueError):
         run_prefix(v, ad, start, prefix, out=torch.empty_like(ad.q)[:2])
+    other = v.attn_dims(ad.q[:2], ad.k_pages, ad.block_table[:2], ad.seq_lens[:2])
+    with pytest.raises(ValueError):
+        v.paged_attn_fwd_prefix(ad.q, ad.k_pages, ad.v_pages, ad.block_table, ad.seq_lens, ad.query_lens,
+                                torch.zeros(1, dtype=torch.int32, device="cuda"),
+                                torch.zeros(0, dtype=torch.int32, device="cuda"), ad.q.clone(),
+                                torch.empty(3, 8, device="cuda"), torch.empty(1 << 20, dtype=torch.uint8, device="cuda"),
+                                dims=other)
+    with pytest.raises(ValueError):
+        run_prefix(v, ad, start, prefix, share="sometimes")
     f = to_device(wl.attention_inputs([300] * 2, [1] * 2, num_q_heads=4, num_kv_heads=2, head_dim=64,
                                       page_size=16, kv_dtype=wl.F32, seed=1))
     with pytest.raises(v.VasError) as e:

@@ -18,7 +18,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libvas.so")
 SOURCES = ["abi.cu", "paged_attn.cu", "spec_verify.cu", "spec_verify_tree.cu", "static_ws.cu",
            "cache_ops.cu", "prefix_attn.cu", "pool.cpp"]
-HEADERS = ["attn_plan.cuh", "device_util.cuh", "philox.cuh", "vas_internal.h"]
+HEADERS = ["attn_plan.cuh", "device_util.cuh", "packed_math.cuh", "philox.cuh", "vas_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -322,6 +322,8 @@ def paged_attn_fwd_prefix(q, k_pages, v_pages, block_table, seq_lens, query_lens
         raise ValueError("tree_mask needs one 64-bit word per query token")
     kv = torch.uint8 if quant is not None else q.dtype
     B = seq_lens.shape
+    if (dims.num_seqs, dims.total_q_tokens, dims.num_pages) != (B[0], q.shape[0], n):
+        raise ValueError("dims are those of another batch")
     st = _lib.paged_attn_fwd_prefix(
         _here(dev, q, "q"), _here(dev, k_pages, "k_pages", None, kv),
         _here(dev, v_pages, "v_pages", pool, kv), _here(dev, k_scale, "k_scale", (n, Hkv, P), f32),
@@ -430,7 +432,11 @@ def _host_list(x, name: str):
         if a.size and (a.min() < 0 or a.max() > 2**31 - 1):
             raise ValueError(f"{name} is outside the range of page numbers")
         a = a.astype(np.int32)
-    return np.ascontiguousarray(a)
+    return a if a.flags.c_contiguous else np.ascontiguousarray(a)
+
+
+def _address(a) -> int:
+    return a.__array_interface__["data"][0]
 
 
 def paged_kv_copy(k_pages, v_pages, src, dst, *, tokens=None, k_scale=None, v_scale=None,
@@ -444,8 +450,8 @@ def paged_kv_copy(k_pages, v_pages, src, dst, *, tokens=None, k_scale=None, v_sc
     t = None if tokens is None else _host_list(tokens, "tokens")
     if len(s) != len(d) or (t is not None and len(t) != len(s)):
         raise ValueError("src, dst and tokens differ in length")
-    st = _lib.paged_kv_copy(kp, vp, ks, vs, s.ctypes.data, d.ctypes.data,
-                            None if t is None else t.ctypes.data, len(s), ctypes.byref(dims),
+    st = _lib.paged_kv_copy(kp, vp, ks, vs, _address(s), _address(d),
+                            None if t is None else _address(t), len(s), ctypes.byref(dims),
                             _stream_address(dev, stream))
     _check("paged_kv_copy", st)
 

@@ -14,6 +14,7 @@
 
 #include "../../include/vas.h"
 #include "device_util.cuh"
+#include "packed_math.cuh"
 #include "vas_internal.h"
 
 namespace vas {

@@ -37,6 +37,11 @@
 //                       O = sum_s e^{lse_s - m} O_s / sum_s e^{lse_s - m},
 //                       lse = m + ln sum_s e^{lse_s - m}.
 //      attn_f32_kernel  fp32 storage: CUDA-core FMA, one warp per query row, no split.
+//
+// With shared prefixes (paged_attn_fwd_prefix) the plan also decides which groups' prefixes
+// are computed once and deals that work out; prefix_attn.cu writes partials of every member's
+// rows for it, before attn_bf16_kernel, whose units of those sequences begin behind the prefix;
+// merge_shared_kernel then merges the partials of their rows.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -52,6 +57,7 @@
 #include "../../include/vas.h"
 #include "attn_plan.cuh"
 #include "device_util.cuh"
+#include "packed_math.cuh"
 #include "vas_internal.h"
 
 namespace vas {

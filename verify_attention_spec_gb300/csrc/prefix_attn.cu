@@ -19,6 +19,7 @@
 #include "../../include/vas.h"
 #include "attn_plan.cuh"
 #include "device_util.cuh"
+#include "packed_math.cuh"
 #include "vas_internal.h"
 
 namespace vas {
