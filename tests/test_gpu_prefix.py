@@ -108,6 +108,18 @@ def test_prompt_chunks_on_a_prefix(vas_lib):
     check(vas_lib, [(600, [(129, 129), (300, 200)])], 16, 2, 64, 32, wl.FP8, seed=4)
 
 
+@pytest.mark.parametrize("kv", [wl.BF16, wl.FP8])
+def test_last_blocks_of_every_size(vas_lib, kv):
+    """Groups of more rows than a block, whose last block has one row's heads, half a block,
+    a little more, and all: 256 rows a block, 4 a token.  Odd and even numbers of tiles, so
+    that heads begin behind padding, and groups one behind another."""
+    def members(tokens):
+        return [(40, tokens - 34)] + [(21, 17)] * 2 if tokens < 74 else [(90, tokens - 50), (60, 50)]
+    for pre in (400, 1024):
+        check(vas_lib, [(pre, members(t)) for t in (65, 96, 97, 128, 129)], 12, 3, 128, 16, kv, seed=pre)
+    check(vas_lib, [(640, members(70)), (300, [(1, 1)] * 4), (2000, members(120))], 32, 8, 64, 32, kv, seed=12)
+
+
 def test_many_groups(vas_lib):
     rng = np.random.default_rng(5)
     groups = [(int(rng.integers(256, 700)), [(int(rng.integers(1, 60)), 1) for _ in range(int(rng.integers(2, 6)))])

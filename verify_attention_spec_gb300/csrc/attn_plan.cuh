@@ -41,11 +41,12 @@ struct PlanHeader {
 // its members' rows one after the other: row r is query token qrow0 + r / G, query head
 // head * G + r % G.
 //
-// The work of all groups is one line of `span` units of weight: a group's blocks (KV head by
-// KV head, kPrefixRows rows each) one behind the other from `base` on, a block `tiles` tiles
-// of kPrefixTile tokens, a tile `weight` units.  CTA k takes the units k * share ..
-// (k + 1) * share - 1, so a block is computed in pieces by the CTAs its units fall to, piece
-// j by the (j + 1)th of them.  share and base are even, so no tile is cut.
+// The work of all groups is one line of `span` units: a group's KV heads one behind the other
+// from `base` on, head_units() each; of a head its blocks of kPrefixRows rows, a block `tiles`
+// tiles of kPrefixTile tokens.  A tile takes two units, or one in a last block of at most
+// kPrefixRows / 2 rows.  CTA k takes the units k * share .. (k + 1) * share - 1, so a block is
+// computed in pieces by the CTAs its units fall to, piece j by the (j + 1)th of them.  share,
+// base and head_units() are even, so no tile is cut.
 struct PrefixGroup {
   int32_t qrow0;       // first query token
   int32_t rows;        // G * query tokens
@@ -53,7 +54,12 @@ struct PrefixGroup {
   int32_t pages;       // shared pages
   int32_t parts;       // partials of a row: the most pieces a block is cut into
   int32_t seq0, seq1;  // members
-  int32_t tiles, blocks, weight, base;
+  int32_t tiles;       // of a block
+  int32_t full, tail;  // blocks of a head whose tiles take two units; 1: and one of one unit
+  int32_t base;
+  __device__ __forceinline__ uint32_t head_units() const {
+    return ((uint32_t)(2 * full + tail) * (uint32_t)tiles + 1) & ~1u;
+  }
 };
 constexpr int kPrefixRows = 256;  // rows of a block
 constexpr int kPrefixTile = 128;  // tokens of a tile

@@ -385,12 +385,12 @@ __device__ bool plan_prefixes(const PlanArgs& a, ShapeFn shape, int64_t (*red)[4
       while (pg.leader + 1 < pg.seq1 && a.row0[pg.leader + 1] == pg.qrow0) ++pg.leader;
       const int32_t members = a.active0[pg.seq1] - a.active0[pg.seq0];
       pg.tiles = (pg.pages * a.P + kPrefixTile - 1) / kPrefixTile;
-      pg.blocks = (int32_t)prefix_blocks(pg.rows) * a.Hkv;
-      // A tile feeds one stream or two, according to the rows.
-      pg.weight = pg.rows > kPrefixRows / 2 ? 2 : 1;
+      // A tile feeds two streams of rows, or one where a head's last block is that small.
+      pg.tail = (uint32_t)(pg.rows - 1) % kPrefixRows < kPrefixRows / 2;
+      pg.full = (int32_t)prefix_blocks(pg.rows) - pg.tail;
       if (members > 1 && pg.pages * a.P >= kMinPrefixTokens) {
         v[0] = 1;
-        v[1] = ((int64_t)pg.blocks * pg.tiles * pg.weight + 1) & ~1ll;
+        v[1] = (((2ll * pg.full + pg.tail) * pg.tiles + 1) & ~1ll) * a.Hkv;
         v[2] = (int64_t)(members - 1) * pg.pages * a.P * a.Hkv * a.D;
         const int64_t reach = (int64_t)pg.pages * a.P * (pg.rows > kNarrowRows * members ? 2 : 1);
         if (carry[2] < kSmallBatch && reach >= kLongPrefix) v[2] += kMinPrefixSaved;
@@ -426,10 +426,12 @@ __device__ bool plan_prefixes(const PlanArgs& a, ShapeFn shape, int64_t (*red)[4
       int64_t need[1] = {0};
       for (int e = warp; e < n; e += kPlanThreads / 32) {
         const PrefixGroup pg = a.groups[e];
-        const int64_t len = (int64_t)pg.tiles * pg.weight;
+        const int32_t per_head = pg.full + pg.tail;
         int32_t parts = 1;
-        for (int b = lane; b < pg.blocks; b += 32) {
-          const int64_t first = pg.base + (int64_t)b * len;
+        for (int b = lane; b < per_head * a.Hkv; b += 32) {
+          const int head = b / per_head, block = b - head * per_head;
+          const int64_t first = pg.base + (int64_t)head * pg.head_units() + 2ll * block * pg.tiles;
+          const int64_t len = (block < pg.full ? 2ll : 1ll) * pg.tiles;
           parts = max(parts, (int32_t)((uint32_t)(first + len - 1) / (uint32_t)each -
                                        (uint32_t)first / (uint32_t)each) + 1);
         }

@@ -54,23 +54,28 @@ struct Pieces {
       if (m != 0xffffffffu) break;
     }
   }
-  // False at the end of the share.  A group's span may end in one unit of padding.
+  // False at the end of the share.
   __device__ __forceinline__ bool next(const PrefixArgs& a, Piece& p) {
     while (x < end) {
       p.g = a.groups[e];
-      const uint32_t len = p.g.tiles * p.g.weight, base = p.g.base;
-      const uint32_t block = (x - base) / len;
-      if (block >= (uint32_t)p.g.blocks) {
+      const uint32_t base = p.g.base, units = p.g.head_units(), two = 2 * p.g.tiles;
+      const uint32_t head = (x - base) / units;
+      if (head >= (uint32_t)a.Hkv) {
         ++e;
-        x = base + ((len * p.g.blocks + 1) & ~1u);
+        continue;  // x is the next group's base
+      }
+      const uint32_t in_head = x - base - head * units;
+      const uint32_t block = min(in_head / two, (uint32_t)p.g.full);
+      const int wide = block < (uint32_t)p.g.full;
+      const uint32_t len = p.g.tiles << wide, first = base + head * units + block * two;
+      if (x >= first + len) {
+        ++x;  // a head may end in one unit of padding
         continue;
       }
-      const uint32_t first = base + block * len, stop = min(end, first + len);
-      const uint32_t per_head = (uint32_t)p.g.blocks / (uint32_t)a.Hkv;
-      p.head = (int)(block / per_head);
-      p.r0 = (int)(block - p.head * per_head) * kPrefixRows;
+      const uint32_t stop = min(end, first + len);
+      p.head = (int)head;
+      p.r0 = (int)block * kPrefixRows;
       p.rows = min(kPrefixRows, p.g.rows - p.r0);
-      const int wide = p.g.weight - 1;  // weight 1 or 2
       const int t0 = (int)(x - first) >> wide, t1 = (int)(stop - first) >> wide;
       p.page_begin = t0 * (kPrefixTile / a.P);
       p.n_tiles = t1 - t0;
@@ -522,7 +527,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         wait(&s_full[st], n_s);
         tc_fence_after();
         // Quantised: scales of this thread's 64 tokens.  They came with the tile's V, fill f of
-        // the ring, whose slot is not filled again before this tile's P is used.
+        // the ring, whose slot is not filled again before this tile's P is used.  (Not before S:
+        // its K tile lies at most three fills before f, so the slot's last phase is over.)
         const float* ksc = nullptr;
         if constexpr (kQuant) {
           const int lead = min(both ? 1 : 2, x.n_tiles);
@@ -545,6 +551,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
 #pragma unroll
               for (int d = 0; d < 4; ++d) sc[e + d] = __float_as_uint(y[d]);
             }
+            // Back for the second reading: with the K scales loaded once more there, the copies
+            // of a broadcast cost shared memory more than this (document on FP8 pages, 520 us
+            // against 492).
+            tmem_st32(s_at + 64 * half + 32 * h, sc);
           }
           if (nv < 64) {
 #pragma unroll
@@ -555,6 +565,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           for (int e = 0; e < 32; e += 2)
             mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(sc[e]), __uint_as_float(sc[e + 1]));
         }
+        if constexpr (kQuant) tmem_wait_st();
         float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;  // c > 0
         // The row's maximum over both halves.  (The next write of this tile's slot comes
         // after the next s_full, so after every thread's read here.)
@@ -590,33 +601,24 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           if (nv < 64) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (32 * h + e >= nv) sc[e] = __float_as_uint(kQuant ? 0.f : -INFINITY);
+              if (32 * h + e >= nv) sc[e] = __float_as_uint(-INFINITY);
           }
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            uint64_t k[2] = {c2, c2}, v[2];
-            if constexpr (kQuant) {
-              const ulonglong2 ks = *reinterpret_cast<const ulonglong2*>(ksc + 32 * h + e);
-              const ulonglong2 vs = *reinterpret_cast<const ulonglong2*>(ksc + kTile + 32 * h + e);
-              k[0] = ks.x, k[1] = ks.y, v[0] = vs.x, v[1] = vs.y;
-              if (c != 1.f) k[0] = mul2(k[0], c2), k[1] = mul2(k[1], c2);
-            }
+            ulonglong2 vs;
+            if constexpr (kQuant) vs = *reinterpret_cast<const ulonglong2*>(ksc + kTile + 32 * h + e);
 #pragma unroll
             for (int d = 0; d < 2; ++d) {
               const int f = e + 2 * d;
               float p0, p1;
-              unpair(fma2(pair(__uint_as_float(sc[f]), __uint_as_float(sc[f + 1])), k[d], mu2), p0, p1);
+              unpair(fma2(pair(__uint_as_float(sc[f]), __uint_as_float(sc[f + 1])), c2, mu2), p0, p1);
               p0 = ex2_approx(p0);
               p1 = ex2_approx(p1);
-              if (kQuant && nv < 64) {  // scales behind the last token may be anything
-                if (32 * h + f >= nv) p0 = 0.f;
-                if (32 * h + f + 1 >= nv) p1 = 0.f;
-              }
               const uint64_t pp = pair(p0, p1);
               sum[d] = add2(sum[d], pp);
               if constexpr (kQuant) {
                 float w0, w1;
-                unpair(mul2(pp, v[d]), w0, w1);
+                unpair(mul2(pp, d ? vs.y : vs.x), w0, w1);
                 p[f >> 1] = pack_f16x2(w0, w1);
               } else {
                 p[f >> 1] = pack_bf16x2(p0, p1);
@@ -812,13 +814,19 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             }
           }
           // The K scales of a tile (they came with its V) take the softmax scale along, in
-          // log2 units.
+          // log2 units.  Behind the last token, where anything may lie, the scales become 1 and
+          // 0: scores of -inf then give weights of 0 by themselves.  (Checks at each weight
+          // instead cost a tile 128 instructions a thread.)
           const int lead = min(x.rows > kTile ? 1 : 2, x.n_tiles);
           const bool is_v = k >= lead && (((k - lead) & 1) == 0 || k >= 2 * x.n_tiles - lead);
           if (is_v) {
-            float* sc = reinterpret_cast<float*>(smem + S::kScaleOff) + slot * 2 * kTile + cw * 64 + lane;
-            sc[0] *= a.scale_log2;
-            sc[32] *= a.scale_log2;
+            const int nv = x.tokens - ((k - lead + 1) >> 1) * kTile;
+            float* sc = reinterpret_cast<float*>(smem + S::kScaleOff) + slot * 2 * kTile;
+#pragma unroll
+            for (int t = cw * 64 + lane; t < cw * 64 + 64; t += 32) {
+              sc[t] = t < nv ? sc[t] * a.scale_log2 : 1.f;
+              if (t >= nv) sc[kTile + t] = 0.f;
+            }
           }
           fence_proxy_async_smem();
           __syncwarp();
