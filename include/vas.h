@@ -202,6 +202,7 @@ int paged_attn_fwd_tree(const void* q, const void* k_pages, const void* v_pages,
  * when its magnitude nears the f16 range), products accumulate in fp32, and P enters
  * the PV product as f16 after multiplication by the V scale of its token, so
  * |v_scale| * 256 must stay within the f16 range (|v| up to about 1e5).
+ * Weights times a V scale below 2^-14 lose bits there (f16 subnormals, steps of 2^-24).
  * Errors: those of paged_attn_fwd; a kv_dtype that is not quantised, or a null scale
  * array, is VAS_E_INVALID_ARG.  paged_attn_fwd and paged_attn_fwd_tree reject the
  * quantised kv_dtypes with VAS_E_INVALID_ARG.

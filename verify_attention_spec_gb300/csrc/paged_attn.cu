@@ -426,14 +426,13 @@ __device__ bool plan_prefixes(const PlanArgs& a, ShapeFn shape, int64_t (*red)[4
       int64_t need[1] = {0};
       for (int e = warp; e < n; e += kPlanThreads / 32) {
         const PrefixGroup pg = a.groups[e];
-        const int32_t per_head = pg.full + pg.tail;
+        const uint32_t per_head = pg.full + pg.tail, units = pg.head_units(), cut = (uint32_t)each;
         int32_t parts = 1;
-        for (int b = lane; b < per_head * a.Hkv; b += 32) {
-          const int head = b / per_head, block = b - head * per_head;
-          const int64_t first = pg.base + (int64_t)head * pg.head_units() + 2ll * block * pg.tiles;
-          const int64_t len = (block < pg.full ? 2ll : 1ll) * pg.tiles;
-          parts = max(parts, (int32_t)((uint32_t)(first + len - 1) / (uint32_t)each -
-                                       (uint32_t)first / (uint32_t)each) + 1);
+        for (uint32_t b = lane; b < per_head * a.Hkv; b += 32) {
+          const uint32_t head = b / per_head, block = b - head * per_head;
+          const uint32_t first = pg.base + head * units + 2 * block * pg.tiles;
+          const uint32_t last = first + (block < (uint32_t)pg.full ? 2 : 1) * pg.tiles - 1;
+          parts = max(parts, (int32_t)(last / cut - first / cut) + 1);
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) parts = max(parts, __shfl_xor_sync(0xffffffffu, parts, o));

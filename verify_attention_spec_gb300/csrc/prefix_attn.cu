@@ -67,16 +67,13 @@ struct Pieces {
       const uint32_t in_head = x - base - head * units;
       const uint32_t block = min(in_head / two, (uint32_t)p.g.full);
       const int wide = block < (uint32_t)p.g.full;
-      const uint32_t len = p.g.tiles << wide, first = base + head * units + block * two;
-      if (x >= first + len) {
-        ++x;  // a head may end in one unit of padding
-        continue;
-      }
+      // (A block of single units may end in one of padding.)
+      const uint32_t len = wide ? two : (two / 2 + 1) & ~1u, first = base + head * units + block * two;
       const uint32_t stop = min(end, first + len);
       p.head = (int)head;
       p.r0 = (int)block * kPrefixRows;
       p.rows = min(kPrefixRows, p.g.rows - p.r0);
-      const int t0 = (int)(x - first) >> wide, t1 = (int)(stop - first) >> wide;
+      const int t0 = (int)(x - first) >> wide, t1 = min((int)(stop - first) >> wide, p.g.tiles);
       p.page_begin = t0 * (kPrefixTile / a.P);
       p.n_tiles = t1 - t0;
       p.tokens = min(p.g.pages * a.P, t1 * kPrefixTile) - t0 * kPrefixTile;
