@@ -565,3 +565,55 @@ def test_a_serving_step(vas_lib, kv):
     ref_o, ref_l = oracle_attention(a)
     compare_attention(out, lse, ref_o, ref_l, kv)
     assert v.vas_last_device_error() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_offsets_past_32_bits(vas_lib, kv):
+    """The last pages of a pool of more than 2^32 elements: append, keep path, copy and
+    attention on a shared prefix give the bits that they give on the first pages of a small one."""
+    v = vas_lib
+    P, Hq, Hkv, D, N = 32, 16, 8, 128, 64
+    big = 2 ** 32 // (P * Hkv * D) + 512
+    quant = kv if kv in wl.QUANTIZED else None
+    g = torch.Generator().manual_seed(31)
+    L, ql = [300, 311, 290], [4, 5, 1]
+    # The members share 8 pages; each has two of its own behind them.
+    bt = np.array([list(range(8)) + [20 + 3 * i, 40 - i] for i in range(3)])
+    rows = torch.randn(sum(ql), Hq + 2 * Hkv, D, generator=g).to(torch.bfloat16).cuda()
+    cs = _cos_sin(400, D).cuda()
+    first = _pools(kv, N, P, Hkv, D, seed=32)
+    if quant:  # no NaN codes
+        for t in first[:2]:
+            t[(t & 0x7F) == 0x7F] = 0x3A
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()
+
+    def steps(pools, at):
+        kp, vp, ks, vs = pools
+        scales = dict(k_scale=ks, v_scale=vs)
+        table, lens, qlens = dev(bt + at), dev(L), dev(ql)
+        q = torch.empty(sum(ql), Hq, D, dtype=torch.bfloat16, device="cuda")
+        v.paged_kv_append(rows[:, :Hq], rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:], table, lens, qlens, q,
+                          kp, vp, cos_sin=cs, quant=quant, **scales)
+        v.paged_kv_keep_path(kp, vp, table, lens, qlens, dev([[2, 3], [3, 4], [-1, -1]]), dev([2, 2, 0]),
+                             **scales)
+        v.paged_kv_copy(kp, vp, [at + 20, at + 1], [at + 50, at + N - 1], tokens=[P, 7], **scales)
+        dims = v.attn_dims(q, kp, table, lens, quant=quant)
+        out = torch.empty_like(q)
+        lse = torch.empty(q.shape[:2], device="cuda")
+        v.paged_attn_fwd_prefix(q, kp, vp, table, lens, qlens, dev([0, 3]), dev([256]), out, lse,
+                                v.alloc_prefix_workspace(dims, 1), dims=dims, quant=quant,
+                                share="always", **scales)
+        assert v.vas_last_device_error() == 0
+        assert torch.isfinite(lse).all()
+        return [q, out, lse] + [t[at:at + N] for t in pools if t is not None]
+
+    last = [None if t is None else torch.zeros((big, *t.shape[1:]), dtype=t.dtype, device="cuda")
+            for t in first]
+    for small, large in zip(first, last):
+        if large is not None:
+            large[big - N:] = small
+    small, large = steps(first, 0), steps(last, big - N)
+    for x, y in zip(small, large):
+        assert torch.equal(x, y)
+    for t in last:
+        assert t is None or not t[:big - N].any()
