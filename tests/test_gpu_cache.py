@@ -223,6 +223,14 @@ def test_append_prompt(vas_lib):
     _run(vas_lib, Case([3000], [2999], 16, 2, 64, 16, "f32", seed=6))
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(16, 2, 64), (5, 1, 64), (33, 2, 128), (1, 1, 128)])
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_append_heads_that_leave_a_group_empty(vas_lib, Hq, Hkv, D, kv):
+    """Many tokens whose heads do not fill the last group of rows: a step of it has few heads
+    or none."""
+    _run(vas_lib, Case([2600, 901], [2560, 900], Hq, Hkv, D, 16, kv, rot=32, inter=Hq == 16, seed=Hq))
+
+
 def test_append_positions_and_tree_depths(vas_lib):
     """Explicit positions turn the rows; the slots stay where the packing puts them."""
     pos = np.concatenate([[9], [500, 501, 501, 502, 0]])
