@@ -29,7 +29,9 @@ namespace cache {
 // at a time and keeps the token's cosines and sines and the weights in registers for all
 // the heads it takes, so the table costs one read per warp and not one per head.
 // Bytes bound it: T (2 Hq + 2 Hkv) D in and out and the pages' T 2 Hkv D; the arithmetic
-// (a 16-term sum and 16 rotations a lane) hides behind the loads.
+// (a 16-term sum and 16 rotations a lane) hides behind the loads as long as tokens are many:
+// 8192 tokens of 64/8 heads of 128 in bf16, 336 MB, 61 us, 5.5 TB/s; 768 on FP8 pages, 30 MB,
+// 12.5 us, where the chain of one token's reads shows.
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
 constexpr int kAppendBlocks = 2;  // of an SM
@@ -483,7 +485,8 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(c
 // The pairs travel in the kernel's parameters, so the caller's lists are free when the
 // call returns and no device copy of them is needed.  A page of one operand is contiguous;
 // its first tokens are too.  A block moves segments of 16 KB, 4 x 16 bytes a thread in
-// flight (bounded by HBM: every byte once in and once out).
+// flight (bounded by HBM: every byte once in and once out; 2047 pages of 64 KB an operand,
+// 537 MB in all, 80 us, 6.7 TB/s).
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 4;
 constexpr int kCopySeg = kCopyThreads * kCopyUnroll * 16;
@@ -549,7 +552,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 // token row and takes the accepted nodes in order, kKeepUnroll at a time, all read before
 // any is written.  That equals reading everything first: nodes ascend, so path[s] >= s + 1
 // and a destination s + 1 is never the source of a later node (path[s'] >= s' + 1 > s + 1).
-// Latency bounds it (a few tokens per sequence): one launch, and four dependent reads.
+// Latency bounds it (a few tokens per sequence): one launch, and four dependent reads. (64
+// windows of a layer 2.7 us.)
 constexpr int kKeepThreads = 128;
 constexpr int kKeepUnroll = 4;
 constexpr int kKeepMaxNodes = 255;
