@@ -200,9 +200,10 @@ int paged_attn_fwd_tree(const void* q, const void* k_pages, const void* v_pages,
  * tree_mask   null (the causal window) or the draft-tree masks of paged_attn_fwd_tree.
  * Arithmetic: the codes are exact in f16; Q is taken to f16 (scaled by a power of two
  * when its magnitude nears the f16 range), products accumulate in fp32, and P enters
- * the PV product as f16 after multiplication by the V scale of its token, so
- * |v_scale| * 256 must stay within the f16 range (|v| up to about 1e5).
- * Weights times a V scale below 2^-14 lose bits there (f16 subnormals, steps of 2^-24).
+ * the PV product as f16 after multiplication by the V scale of its token and by a power
+ * of two that follows the V scales, so that the largest lie between 2^6 and 2^15 and the
+ * size of V does not matter (|v_scale| between 2^-60 and 2^66; weights times V scales
+ * 2^20 below the largest lose bits, steps of 2^-24).
  * Errors: those of paged_attn_fwd; a kv_dtype that is not quantised, or a null scale
  * array, is VAS_E_INVALID_ARG.  paged_attn_fwd and paged_attn_fwd_tree reject the
  * quantised kv_dtypes with VAS_E_INVALID_ARG.

@@ -153,3 +153,39 @@ def compare_verify(acc, out, ref):
             if acc[b] != ref.accepted_len[b] or not np.array_equal(out[b], ref.out_tokens[b]):
                 differ += 1
     return flagged, differ
+
+
+def add_sink(a: wl.AttentionInputs, weight: float, sink_v: float, amplitude: float, n: int):
+    """Turn quantised N(0, 1) inputs into those of an attention sink: the first token of
+    every sequence holds `weight` of the softmax over `n` positions (its K is aligned with
+    element 0 of every query, which no other K has), its V is `sink_v` of the others', and
+    every V is `amplitude` of what it was.  On the CPU, in place; the codes stay those of
+    the pool's format, so the oracle decodes the same values."""
+    e4m3 = a.kv_dtype == wl.FP8
+    a.q[..., 0] = 4.0
+    a.k_pages[..., 0] = 0
+    a.v_scale *= amplitude
+    # scores of the others are N(0, 1): their weights sum to n e^(1/2) on average
+    score = np.log(weight / (1.0 - weight) * n) + 0.5
+    k0 = score * np.sqrt(a.head_dim) / 4.0
+    for page in {int(p) for p in a.block_table[:, 0]}:
+        a.k_pages[page, 0] = 0
+        a.k_pages[page, 0, :, 0] = 0x7E if e4m3 else 127
+        a.k_scale[page, :, 0] = k0 / (448.0 if e4m3 else 127.0)
+        a.v_scale[page, :, 0] *= sink_v
+
+
+# Relative L2 error allowed of a quantised call whatever the size of its V.  The output's
+# rounding to bf16 is at most 2^-8 of each element, 3.9e-3 in the norm.  Each weight, an
+# f16 number relative to the largest V of its time, is off by 2^-11 of itself, at random:
+# a sum of n of them by 2^-11 sqrt(sum (w v)^2), which is 2^-11 of the sum's own size where
+# its terms have random signs, 5e-4; exponentials and fp32 sums stay below 2e-5.
+QUANT_REL_L2 = 4.5e-3
+
+
+def check_quant_rel_l2(out, lse, ref_out, ref_lse):
+    o = out.float().cpu().numpy().astype(np.float64)
+    assert np.all(np.isfinite(o))
+    rel = float(np.linalg.norm(o - ref_out) / np.linalg.norm(ref_out))
+    assert rel <= QUANT_REL_L2, f"rel-L2 {rel}"
+    assert float(np.abs(lse.cpu().numpy() - ref_lse).max()) <= TOL[wl.FP8]["lse"]

@@ -8,8 +8,8 @@ import torch
 
 from verify_attention_spec_gb300 import workloads as wl
 
-from gpu_common import (ancestor_masks, compare_attention, oracle_attention, run_gpu_attention,
-                        to_device)
+from gpu_common import (add_sink, ancestor_masks, check_quant_rel_l2, compare_attention,
+                        oracle_attention, run_gpu_attention, to_device)
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +118,48 @@ def test_stress70b_quant_full_size(vas_lib, name):
     assert vas_lib.vas_last_device_error() == 0
     ref_o, ref_l = oracle_attention(a)
     compare_attention(out, lse, ref_o, ref_l, a.kv_dtype)
+
+
+# The share of the first token, what its V is of the others', the size of V.
+SINKS = [(0.55, 0.02, 1.0), (0.9, 0.02, 0.25), (0.55, 0.02, 0.05), (0.9, 0.1, 0.05), (0.9, 0.02, 1e-12),
+         (0.55, 0.02, 1e6)]
+
+
+@pytest.mark.parametrize("kv", [wl.FP8, wl.INT8])
+@pytest.mark.parametrize("weight,sink_v,amplitude", SINKS)
+def test_weights_far_below_the_largest(vas_lib, kv, weight, sink_v, amplitude):
+    """A first token that takes most of the softmax and has a small V, as models have: the
+    output is made by the many small weights.  Decode rows, a window, a row block of 128,
+    with and without splits."""
+    a = _case([4000, 4000, 4000], [1, 5, 40], 32, 4, 128, 16, kv, seed=31)
+    add_sink(a, weight, sink_v, amplitude, 4000)
+    ref_o, ref_l = oracle_attention(a)
+    ad = to_device(a)
+    dims = vas_lib.attn_dims(ad.q, ad.k_pages, ad.block_table, ad.seq_lens, quant=kv)
+    for nbytes in (None, vas_lib.paged_attn_workspace_min(dims)):
+        out, lse = run_gpu_attention(vas_lib, ad, workspace_bytes=nbytes)
+        check_quant_rel_l2(out, lse, ref_o, ref_l)
+    assert vas_lib.vas_last_device_error() == 0
+
+
+@pytest.mark.parametrize("kv", [wl.FP8, wl.INT8])
+@pytest.mark.parametrize("D,P", [(128, 32), (64, 16)])
+def test_v_scales_that_change_along_a_sequence(vas_lib, kv, D, P):
+    """Pages whose V is up to 2^30 larger or smaller than their neighbours', growing, falling
+    and at random, some all zero."""
+    a = _case([1000, 900, 800, 700], [1, 5, 20, 2], 16, 2, D, P, kv, seed=32)
+    bt = a.block_table.numpy()
+    rng = np.random.default_rng(33)
+    for i, L in enumerate(a.seq_lens.tolist()):
+        n = -(-L // P)
+        e = [np.linspace(-30, 0, n), np.linspace(0, -30, n), rng.integers(-30, 1, n), np.full(n, -30.0)][i]
+        for c in range(n):
+            a.v_scale[bt[i, c]] *= float(2.0 ** np.round(e[c]))
+        a.v_scale[bt[i, n // 2]] = 0.0
+    ref_o, ref_l = oracle_attention(a)
+    out, lse = run_gpu_attention(vas_lib, to_device(a))
+    row = 0
+    for ql in a.query_lens.tolist():  # the sequences' sizes differ by 2^30
+        check_quant_rel_l2(out[row:row + ql], lse[row:row + ql], ref_o[row:row + ql], ref_l[row:row + ql])
+        row += ql
+    assert vas_lib.vas_last_device_error() == 0

@@ -1,5 +1,6 @@
 // Device helpers shared by the kernels that came after device_util.cuh's: packed fp32
-// arithmetic, tcgen05 products with A in tensor memory, and bf16 queries taken to f16.
+// arithmetic, tcgen05 products with A in tensor memory, the exponent of V scales, and bf16
+// queries taken to f16.
 #pragma once
 
 #include <cstdint>
@@ -58,6 +59,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+
+// Exponent e of a set of V scales, one or more a lane as their largest magnitude x: they
+// lie below 2^(e + 7).  The whole warp.  Between -60 and 60, so that the sums of weights
+// relative to 2^e stay within fp32; scales that are not finite count as the largest.
+__device__ __forceinline__ float v_exponent(float x) {
+  const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(x) & 0x7fffffffu);
+  return (float)max(-60, min(60, (int)(top >> 23) - 126 - 7));
+}
 
 // Largest magnitude of eight bf16 values.
 __device__ __forceinline__ float absmax_bf16x8(uint4 v) {

@@ -777,6 +777,12 @@ __host__ __device__ constexpr uint32_t tok_off(int t) {
 // that may trail the true running maximum by up to kRebase (log2 units, so p <= 2^8);
 // the accumulators are rescaled only when a new maximum exceeds the reference by more
 // than that.  Sum and output share the reference, so the normalised result is exact.
+// Quantised pools move the reference by the exponent of their V scales as well
+// (v_exponent): it is the maximum plus e, where 2^(e + 7) bounds the V scales of the tokens
+// at hand, so that P times a V scale, which the products take as f16, stays below 2^15 and
+// the largest P times the largest scale is 2^6 at least.  With the maximum alone, weights a
+// few nats below it times a scale of amax / 448 fall under f16's normal range: an output
+// made of many such weights lost up to a tenth of its value.
 constexpr float kRebase = 8.f;
 
 // Per-lane ldmatrix byte offsets (relative to a stage operand) for the narrow path:
@@ -819,6 +825,25 @@ __device__ __forceinline__ void unpack2(uint32_t v, float& lo, float& hi) {
   }
 }
 
+// What a warp of a narrow or wide unit of a quantised call checks a stage against: P times a V
+// scale stays below 2^15 while the scales lie below `limit`, 2^(e + 7), and no maximum passes
+// its reference by more than kRebase - e.  Otherwise the stage's own exponent decides which
+// rows move, and becomes e unless it lies within four below (so that V scales around a power
+// of two do not have every other stage looked at).  With v_exponent of each stage instead, 512
+// sequences of 64/8 heads on FP8 pages took 1617 us against 1574 (1576 with the maximum
+// alone).  In prompt chunks the branch costs more than v_exponent does: eight of 1024 tokens
+// 3106 us against 3059 (3030).
+struct VBound {
+  float limit = 0.f;
+  __device__ __forceinline__ float room() const {  // of a limit of 0, enough to be looked at
+    return kRebase + 134.f - (float)(__float_as_int(limit) >> 23);
+  }
+  __device__ __forceinline__ void take(float e) {
+    const int now = (__float_as_int(limit) >> 23) - 134;
+    if ((int)e > now || (int)e < now - 4) limit = __int_as_float(((int)e + 134) << 23);
+  }
+};
+
 // ---- narrow units: S^T = K Q^T, one warp per stage -------------------------------
 // Quantised pools (KQ): the stage holds the codes as f16; the scores are multiplied by
 // the K scale of their token (ks) and P by the V scale of its token (vs) before the
@@ -832,7 +857,7 @@ __device__ __forceinline__ void narrow_stage(uint32_t kbase, uint32_t vbase, int
                                              float (&l)[NN][2], int t_abs0,
                                              const int (&lim)[NN][2], float c, int lane,
                                              const uint64_t* tm, int ctx_end, const float* ks,
-                                             const float* vs) {
+                                             const float* vs, VBound& vb) {
   constexpr uint32_t kTile = tok_off<D, P>(16);  // 16 token rows
   const int g = lane >> 2;
   float s[2][NN][4];
@@ -897,14 +922,24 @@ __device__ __forceinline__ void narrow_stage(uint32_t kbase, uint32_t vbase, int
   // Rebase the rows whose maximum outgrew the reference.
   float mx[NN][2];
   bool up = false;
+  float room = kRebase;
+  if constexpr (KQ != kKvBf16) {
+    up = fabsf(vs[lane]) >= vb.limit;  // scales of no token are 0
+    room = vb.room();
+  }
 #pragma unroll
   for (int nn = 0; nn < NN; ++nn)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       mx[nn][h] = fmaxf(fmaxf(s[0][nn][h], s[0][nn][h + 2]), fmaxf(s[1][nn][h], s[1][nn][h + 2]));
-      up |= mx[nn][h] * c > mref[nn][h] + kRebase;
+      up |= mx[nn][h] * c > mref[nn][h] + room;
     }
   if (__any_sync(0xffffffffu, up)) {
+    float ve = 0.f;
+    if constexpr (KQ != kKvBf16) {
+      ve = v_exponent(vs[lane]);
+      vb.take(ve);
+    }
 #pragma unroll
     for (int nn = 0; nn < NN; ++nn)
 #pragma unroll
@@ -913,16 +948,16 @@ __device__ __forceinline__ void narrow_stage(uint32_t kbase, uint32_t vbase, int
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        const float vs = v * c;
-        if (vs > mref[nn][h] + kRebase) {  // same decision on all 8 lanes of the row
-          const float alpha = exp2f(mref[nn][h] - vs);
+        const float top = fmaf(v, c, ve);
+        if (top > mref[nn][h] + kRebase) {  // same decision on all 8 lanes of the row
+          const float alpha = exp2f(mref[nn][h] - top);
           l[nn][h] *= alpha;
 #pragma unroll
           for (int dt = 0; dt < D / 16; ++dt) {
             oT[dt][nn][h] *= alpha;
             oT[dt][nn][h + 2] *= alpha;
           }
-          mref[nn][h] = vs;
+          mref[nn][h] = top;
         }
       }
   }
@@ -994,7 +1029,7 @@ __device__ __forceinline__ void wide_s_step(const uint32_t (&kb)[2], int tvalid,
                                             int t_abs0, int limA, int limB, float c, int lane,
                                             uint8_t* prow, const uint64_t* tmw, int ctx_end,
                                             const float* ks0, const float* ks1,
-                                            const float* vs0, const float* vs1) {
+                                            const float* vs0, const float* vs1, VBound& vb) {
   constexpr int NT = 4 * NST;
   const int g = lane >> 2, tq = lane & 3;
   float s[NT][4];
@@ -1045,19 +1080,31 @@ __device__ __forceinline__ void wide_s_step(const uint32_t (&kb)[2], int tvalid,
     for (int e = 0; e < 4; ++e) mx[e >> 1] = fmaxf(mx[e >> 1], s[nt][e]);
   alpha[0] = alpha[1] = 1.f;
   rescale = false;
-  const bool up = mx[0] * c > mref[0] + kRebase || mx[1] * c > mref[1] + kRebase;
+  bool up = false;
+  float room = kRebase, vmax = 0.f;
+  if constexpr (KQ != kKvBf16) {
+    vmax = fmaxf(fabsf(vs0[lane]), fabsf(vs1[lane]));  // scales of no token are 0
+    up = vmax >= vb.limit;
+    room = vb.room();
+  }
+  up |= mx[0] * c > mref[0] + room || mx[1] * c > mref[1] + room;
   if (__any_sync(0xffffffffu, up)) {
+    float ve = 0.f;
+    if constexpr (KQ != kKvBf16) {
+      ve = v_exponent(vmax);
+      vb.take(ve);
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float v = mx[h];
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-      const float vs = v * c;
-      if (vs > mref[h] + kRebase) {  // same decision on the quad sharing the row
+      const float top = fmaf(v, c, ve);
+      if (top > mref[h] + kRebase) {  // same decision on the quad sharing the row
         if (mref[h] != -INFINITY) rescale = true;
-        alpha[h] = exp2f(mref[h] - vs);
+        alpha[h] = exp2f(mref[h] - top);
         l[h] *= alpha[h];
-        mref[h] = vs;
+        mref[h] = top;
       }
     }
   }
@@ -2141,7 +2188,8 @@ __global__ void __launch_bounds__(KQ == kKvBf16 ? kThreads : kThreadsQ, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             m4[i & 3] = fmaxf(m4[i & 3], (valid >> i) & 1 ? __uint_as_float(sr[i]) : -INFINITY);
-          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;  // c > 0
+          float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;  // c > 0
+          if constexpr (kQuant) mx += v_exponent(kss[kStageTokens + lane]);
           const bool rebase = mx > mref + kRebase;
           const bool rescale = rebase && si > 0 && mref != -INFINITY;
           const float alpha = rebase ? exp2f(mref - mx) : 1.f;
@@ -2251,6 +2299,7 @@ __global__ void __launch_bounds__(KQ == kKvBf16 ? kThreads : kThreadsQ, 1)
 #pragma unroll
           for (int nn = 0; nn < NN; ++nn) oT[dt][nn][0] = oT[dt][nn][1] = oT[dt][nn][2] = oT[dt][nn][3] = 0.f;
         float m[NN][2], l[NN][2];
+        VBound vb;
         int lim[NN][2];
 #pragma unroll
         for (int nn = 0; nn < NN; ++nn)
@@ -2290,10 +2339,10 @@ __global__ void __launch_bounds__(KQ == kKvBf16 ? kThreads : kThreadsQ, 1)
           const float* vss = kQuant ? kss + kStageTokens : nullptr;
           if (loaded == kStageTokens && t_abs0 + kStageTokens - 1 <= min_lim)
             narrow_stage<D, P, NN, false, KQ>(kbase, vbase, loaded, qb, koff, voff, oT, m, l,
-                                              t_abs0, lim, cunit, lane, tm, ctx_end, kss, vss);
+                                              t_abs0, lim, cunit, lane, tm, ctx_end, kss, vss, vb);
           else
             narrow_stage<D, P, NN, true, KQ>(kbase, vbase, loaded, qb, koff, voff, oT, m, l,
-                                             t_abs0, lim, cunit, lane, tm, ctx_end, kss, vss);
+                                             t_abs0, lim, cunit, lane, tm, ctx_end, kss, vss, vb);
           __syncwarp();
           if (lane == 0) mbar_arrive(&empty[slot_s]);
         }
@@ -2410,6 +2459,7 @@ __global__ void __launch_bounds__(KQ == kKvBf16 ? kThreads : kThreadsQ, 1)
       named_bar_sync(1, kConsumerThreads);  // the query staging becomes the P tiles
       const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
       float mref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      VBound vb;
       const int rA = r0 + 16 * warp + g, rB = rA + 8;
       const int limA = rA < R ? L - ql + rA / a.G : L - 1;
       const int limB = rB < R ? L - ql + rB / a.G : L - 1;
@@ -2470,11 +2520,11 @@ __global__ void __launch_bounds__(KQ == kKvBf16 ? kThreads : kThreadsQ, 1)
           if (nst == 2)
             wide_s_step<D, P, 2, KQ>(kb, loaded, masked, qa, kw, mref, l, alpha, rescale, t_abs0,
                                      limA, limB, cunit, lane, prow, tmw, ctx_end, ksp[0], ksp[1],
-                                     ksp[0] + kStageTokens, ksp[1] + kStageTokens);
+                                     ksp[0] + kStageTokens, ksp[1] + kStageTokens, vb);
           else
             wide_s_step<D, P, 1, KQ>(kb, loaded, true, qa, kw, mref, l, alpha, rescale, t_abs0,
                                      limA, limB, cunit, lane, prow, tmw, ctx_end, ksp[0], ksp[1],
-                                     ksp[0] + kStageTokens, ksp[1] + kStageTokens);
+                                     ksp[0] + kStageTokens, ksp[1] + kStageTokens, vb);
           if (__any_sync(0xffffffffu, rescale && sj > 0)) {
             // O holds the products up to the previous step: wait for the last of them,
             // then scale row 16 w + t (lane t < 16) by its factor (held by lane 4 (t % 8)).
