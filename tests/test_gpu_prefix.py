@@ -6,7 +6,8 @@ import torch
 
 from verify_attention_spec_gb300 import workloads as wl
 
-from gpu_common import ancestor_masks, compare_attention, oracle_attention, to_device
+from gpu_common import (add_sink, ancestor_masks, check_quant_rel_l2, compare_attention,
+                        oracle_attention, to_device)
 
 pytestmark = pytest.mark.gpu
 
@@ -436,3 +437,40 @@ def test_two_layers_share_a_workspace_in_a_graph(vas_lib):
     for c in cases:
         assert torch.equal(c[3], c[5][0]) and torch.equal(c[4], c[5][1])
     assert v.vas_last_device_error() == 0
+
+
+@pytest.mark.parametrize("kv", [wl.FP8, wl.INT8])
+@pytest.mark.parametrize("weight,sink_v,amplitude", [(0.55, 0.02, 1.0), (0.9, 0.02, 0.25), (0.55, 0.02, 0.05),
+                                                     (0.9, 0.02, 0.05), (0.9, 0.02, 1e-12), (0.55, 0.02, 1e6)])
+def test_weights_far_below_the_largest(vas_lib, kv, weight, sink_v, amplitude):
+    """A first token, in the shared prefix, that takes most of the softmax and has a small V:
+    the output is made by the many small weights.  One stream of rows and two."""
+    for members in (3, 12):
+        a, start, prefix = shared_inputs([(4000, [(17, 1), (40, 5), (3, 3)] * (members // 3))], 32, 4, 128, 16, kv, 31)
+        add_sink(a, weight, sink_v, amplitude, 4000)
+        ref_o, ref_l = oracle_attention(a)
+        out, lse = run_prefix(vas_lib, to_device(a), start, prefix)
+        check_quant_rel_l2(out, lse, ref_o, ref_l)
+    assert vas_lib.vas_last_device_error() == 0
+
+
+@pytest.mark.parametrize("kv", [wl.FP8, wl.INT8])
+@pytest.mark.parametrize("D,P", [(128, 32), (64, 16)])
+def test_v_scales_that_change_along_a_prefix(vas_lib, kv, D, P):
+    """Pages of a prefix whose V is up to 2^30 larger or smaller than their neighbours',
+    growing, falling, at random and all small, some all zero."""
+    rng = np.random.default_rng(33)
+    n = 1500 // P
+    for e in (np.linspace(-30, 0, n), np.linspace(0, -30, n), rng.integers(-30, 1, n), np.full(n, -30.0)):
+        for groups in ([(1500, [(20, 1)] * 3)], [(1500, [(20, 7)] * 5)]):
+            a, start, prefix = shared_inputs(groups, 16, 2, D, P, kv, 32)
+            for c in range(n):
+                a.v_scale[int(a.block_table[0, c])] *= float(2.0 ** np.round(e[c]))
+            a.v_scale[int(a.block_table[0, n // 2])] = 0.0
+            for i in range(len(a.seq_lens)):  # what follows the prefix is as small as its last page
+                for c in range(n, -(-int(a.seq_lens[i]) // P)):
+                    a.v_scale[int(a.block_table[i, c])] *= float(2.0 ** np.round(e[-1]))
+            ref_o, ref_l = oracle_attention(a)
+            out, lse = run_prefix(vas_lib, to_device(a), start, prefix)
+            check_quant_rel_l2(out, lse, ref_o, ref_l)
+    assert vas_lib.vas_last_device_error() == 0

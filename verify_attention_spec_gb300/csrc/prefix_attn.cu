@@ -164,8 +164,10 @@ struct PSmem {
   // [slot] K scales, V scales of the tile whose V the slot holds
   static constexpr int kScaleOff =
       kRingOff + kSlots * (kTileBytes + (kQuant && D == 64 ? kTile * 64 : 0));
+  // [slot] v_exponent of each half of those V scales
+  static constexpr int kExpOff = kScaleOff + (kQuant ? kSlots * 2 * kTile * 4 : 0);
   // [stream][half][row]: maxima, at the end of a piece the sums
-  static constexpr int kStatOff = kScaleOff + (kQuant ? kSlots * 2 * kTile * 4 : 0);
+  static constexpr int kStatOff = kExpOff + (kQuant ? kSlots * 8 : 0);
   static constexpr int kBarOff = kStatOff + 4 * kTile * 4;
   // full[kSlots], empty[kSlots], ready[kSlots], s_full[2], p_full[2], o_full[2], q_full[2],
   // fin | TMEM base
@@ -532,11 +534,14 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         // the ring, whose slot is not filled again before this tile's P is used.  (Not before S:
         // its K tile lies at most three fills before f, so the slot's last phase is over.)
         const float* ksc = nullptr;
+        float ve = 0.f;  // a reference moves by the exponent of the V scales, as in paged_attn.cu
         if constexpr (kQuant) {
           const int lead = min(both ? 1 : 2, x.n_tiles);
           const uint32_t f = used + lead + tile + min(tile, x.n_tiles - lead);
           wait(&ready[f % kSlots], f / kSlots);
           ksc = reinterpret_cast<const float*>(smem + S::kScaleOff) + (f % kSlots) * 2 * kTile + 64 * half;
+          const float2 e = *reinterpret_cast<const float2*>(smem + S::kExpOff + (f % kSlots) * 8);
+          ve = fmaxf(e.x, e.y);
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -574,6 +579,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         *my_stat = top;
         named_bar_sync(1 + st, kStreamThreads);
         top = fmaxf(top, *other_stat);
+        if constexpr (kQuant) top += ve;
         const bool rebase = top > m + kRebase;
         if (__any_sync(0xffffffffu, rebase)) {
           const float alpha = rebase ? exp2f(m - top) : 1.f;
@@ -824,11 +830,15 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
           if (is_v) {
             const int nv = x.tokens - ((k - lead + 1) >> 1) * kTile;
             float* sc = reinterpret_cast<float*>(smem + S::kScaleOff) + slot * 2 * kTile;
+            float most = 0.f;
 #pragma unroll
             for (int t = cw * 64 + lane; t < cw * 64 + 64; t += 32) {
               sc[t] = t < nv ? sc[t] * a.scale_log2 : 1.f;
-              if (t >= nv) sc[kTile + t] = 0.f;
+              if (t < nv) most = fmaxf(most, fabsf(sc[kTile + t]));
+              else sc[kTile + t] = 0.f;
             }
+            most = v_exponent(most);
+            if (lane == 0) reinterpret_cast<float*>(smem + S::kExpOff)[2 * slot + cw] = most;
           }
           fence_proxy_async_smem();
           __syncwarp();
