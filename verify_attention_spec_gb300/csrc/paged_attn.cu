@@ -948,7 +948,7 @@ __device__ __forceinline__ void narrow_stage(uint32_t kbase, uint32_t vbase, int
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        const float top = fmaf(v, c, ve);
+        const float top = KQ == kKvBf16 ? v * c : fmaf(v, c, ve);
         if (top > mref[nn][h] + kRebase) {  // same decision on all 8 lanes of the row
           const float alpha = exp2f(mref[nn][h] - top);
           l[nn][h] *= alpha;
@@ -1099,7 +1099,7 @@ __device__ __forceinline__ void wide_s_step(const uint32_t (&kb)[2], int tvalid,
       float v = mx[h];
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
       v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-      const float top = fmaf(v, c, ve);
+      const float top = KQ == kKvBf16 ? v * c : fmaf(v, c, ve);
       if (top > mref[h] + kRebase) {  // same decision on the quad sharing the row
         if (mref[h] != -INFINITY) rescale = true;
         alpha[h] = exp2f(mref[h] - top);
