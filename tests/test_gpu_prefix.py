@@ -474,3 +474,19 @@ def test_v_scales_that_change_along_a_prefix(vas_lib, kv, D, P):
             out, lse = run_prefix(vas_lib, to_device(a), start, prefix)
             check_quant_rel_l2(out, lse, ref_o, ref_l)
     assert vas_lib.vas_last_device_error() == 0
+
+
+@pytest.mark.parametrize("kv", [wl.FP8, wl.INT8])
+@pytest.mark.parametrize("size", [2.0 ** 17, 2.0 ** 60])
+def test_large_queries_of_one_member(vas_lib, kv, size):
+    """Queries of one member far outside f16's range, along an element that no K has, beside
+    ordinary ones of the other members: those keep all their bits."""
+    for members in ([(17, 1), (40, 5), (3, 3)], [(17, 1), (40, 5), (3, 3)] * 5):
+        a, start, prefix = shared_inputs([(700, members)], 32, 4, 128, 16, kv, 34)
+        a.k_pages[..., 0] = 0
+        a.q[0] = 0
+        a.q[0, :, 0] = size
+        ref_o, ref_l = oracle_attention(a)
+        out, lse = run_prefix(vas_lib, to_device(a), start, prefix)
+        check_quant_rel_l2(out, lse, ref_o, ref_l)
+    assert vas_lib.vas_last_device_error() == 0

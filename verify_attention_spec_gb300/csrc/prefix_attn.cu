@@ -135,7 +135,7 @@ __device__ __forceinline__ size_t part_row(const PrefixArgs& a, const Piece& p, 
 // Quantised pages (KV: VAS_FP8_E4M3, VAS_INT8): the producer lands a tile's codes beside its
 // 16-bit slot (with 128-wide heads in the upper half of it) and the scales of its tokens with
 // the V codes; two converter warps expand the codes, exact in f16, into the slot.  Products
-// are f16 (Q scaled into range by a power of two where it must be); scores are multiplied by
+// are f16 (a row of Q scaled into range by a power of two where it must be); scores are multiplied by
 // the K scale of their token, P by its V scale.  Bounded by the softmax, whose warps read each
 // scale as a broadcast: the whole call takes 491 us on FP8 pages, 370 on bf16.
 constexpr int kTile = kPrefixTile;          // tokens of a tile, rows of a stream
@@ -166,8 +166,10 @@ struct PSmem {
       kRingOff + kSlots * (kTileBytes + (kQuant && D == 64 ? kTile * 64 : 0));
   // [slot] v_exponent of each half of those V scales
   static constexpr int kExpOff = kScaleOff + (kQuant ? kSlots * 2 * kTile * 4 : 0);
+  // [stream][row] what a row's scores are multiplied by
+  static constexpr int kBackOff = kExpOff + (kQuant ? kSlots * 8 : 0);
   // [stream][half][row]: maxima, at the end of a piece the sums
-  static constexpr int kStatOff = kExpOff + (kQuant ? kSlots * 8 : 0);
+  static constexpr int kStatOff = kBackOff + (kQuant ? 2 * kTile * 4 : 0);
   static constexpr int kBarOff = kStatOff + 4 * kTile * 4;
   // full[kSlots], empty[kSlots], ready[kSlots], s_full[2], p_full[2], o_full[2], q_full[2],
   // fin | TMEM base
@@ -476,7 +478,6 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         uint8_t* qt = smem + st * S::kTileBytes;
         constexpr int kEach = kTile * (D / 8) / kStreamThreads;
         uint4 v[kEach];
-        float most = 0.f;
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
           const int e = tid + k * kStreamThreads, r = e / (D / 8), gc = e % (D / 8);
@@ -486,31 +487,30 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
             v[k] = *reinterpret_cast<const uint4*>(
                 qg + ((size_t)x.g.qrow0 * a.Hq + (size_t)x.head * a.G + rr +
                       (size_t)a.by_G.div(rr) * (a.Hq - a.G)) * D + gc * 8);
-          if constexpr (kQuant) most = fmaxf(most, absmax_bf16x8(v[k]));
         }
         if constexpr (kQuant) {
-          // Q goes to f16 times 2^-e, the power of two that brings the tile's largest |q| under
-          // 2^15 (1 for any ordinary Q); the scores are scaled back through c.
+          // A row goes to f16 times 2^-e, the power of two that brings its largest |q| under
+          // 2^15 (1 for any ordinary Q); its scores are scaled back through c.  By rows,
+          // because the rows of a tile are those of several sequences.  D / 8 lanes hold one.
+          float* const back = reinterpret_cast<float*>(smem + S::kBackOff) + st * kTile;
 #pragma unroll
-          for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-          float* const peak = stat + 2 * st * kTile;
-          named_bar_sync(1 + st, kStreamThreads);  // the last piece's sums are read
-          if (lane == 0) peak[warp % kStreamWarps] = most;
-          named_bar_sync(1 + st, kStreamThreads);
-          most = peak[lane % kStreamWarps];
+          for (int k = 0; k < kEach; ++k) {
+            const int e = tid + k * kStreamThreads;
+            float most = absmax_bf16x8(v[k]);
 #pragma unroll
-          for (int o = 4; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-          named_bar_sync(1 + st, kStreamThreads);  // read before the first maxima go there
-          float mul = 1.f;
-          c = 1.f;
-          if (most > 32768.f && most <= 3.0e38f) {
-            int e;
-            frexpf(most, &e);  // most < 2^e
-            mul = ldexpf(1.f, 15 - e);
-            c = ldexpf(1.f, e - 15);
+            for (int o = D / 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+            float mul = 1.f, up = 1.f;
+            if (most > 32768.f && most <= 3.0e38f) {
+              int x2;
+              frexpf(most, &x2);  // most < 2^x2
+              mul = ldexpf(1.f, 15 - x2);
+              up = ldexpf(1.f, x2 - 15);
+            }
+            v[k] = bf16x8_to_f16x8(v[k], mul);
+            if (e % (D / 8) == 0) back[e / (D / 8)] = up;  // this piece's; the last one's are read
           }
-#pragma unroll
-          for (int k = 0; k < kEach; ++k) v[k] = bf16x8_to_f16x8(v[k], mul);
+          named_bar_sync(1 + st, kStreamThreads);
+          c = back[row];
         }
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
