@@ -515,6 +515,27 @@ def test_keep_path_skips_bad_rows(vas_lib):
     outcome(setter("bt", 6, -1), v.VAS_DEV_BAD_PAGE, [6])
 
 
+
+@pytest.mark.parametrize("row", [0, 1])
+def test_keep_path_that_falls_in_a_full_table(vas_lib, row):
+    """A path that falls and rises again, in a sequence that fills its table: its later nodes
+    belong behind the last page, where no entry of the table is looked up (the next row's
+    first is none of the pool's pages)."""
+    v = vas_lib
+    lens, ql = np.array([64, 64]), np.array([6, 40])
+    bt, pages = wl.build_pool(lens, 16, 4)
+    path = np.full((2, 40), -1, np.int32)
+    path[0, :6] = [5, 1, 2, 3, 4, 5]                  # node 5 would go to position 64
+    path[1] = [38, *range(1, 40)]                     # node 39 to position 64
+    acc = np.array([6, 40]) * (np.arange(2) == row)
+    bt[1, 0] = -1 if row == 0 else bt[1, 0]
+    c = dict(bt=bt, lens=lens, ql=ql, path=path, acc=acc, index=[0, 1], pools=_pools("bf16", pages, 16, 2, 64))
+    before = [c["pools"][i].clone() for i in (0, 1)]
+    _keep_call(v, c)
+    assert v.vas_last_device_error() == v.VAS_DEV_BAD_TREE
+    assert torch.equal(c["pools"][0], before[0]) and torch.equal(c["pools"][1], before[1])
+
+
 # ---- together -------------------------------------------------------------------------------
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_a_serving_step(vas_lib, kv):

@@ -599,11 +599,12 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepArgs a) {
       const int32_t* bt = a.block_table + (size_t)i * a.maxp;
       for (int s = tid; s < acc; s += kKeepThreads) {
         const int32_t c = row[s], prev = s ? row[s - 1] : 0;
-        if (c <= prev || c >= ql) {
+        // An ascending path has s + 1 <= c < ql, so that both positions lie inside the
+        // sequence; one that fell before s may ascend here with c <= s.
+        if (c <= prev || c <= s || c >= ql) {
           err |= VAS_DEV_BAD_TREE;
           continue;
         }
-        // s + 1 <= c < ql: both positions lie inside the sequence.
         const int32_t p0 = L - ql + c, p1 = L - ql + 1 + s;
         const int32_t g0 = bt[p0 / a.P], g1 = bt[p1 / a.P];
         if (g0 < 0 || g0 >= a.num_pages || g1 < 0 || g1 >= a.num_pages) {
