@@ -371,6 +371,8 @@ typedef struct {
  * the first tokens[i] slots of the page and leaves the others; null copies whole pages.
  * No page may be named twice among the destinations, or be both a source and a
  * destination (VAS_E_INVALID_ARG, and nothing is copied): the copies run at once.
+ * A page of one layer and operand stays 16 KB below 2^31 bytes (VAS_E_UNSUPPORTED; in
+ * paged_kv_keep_path too).
  * k_pages, v_pages, k_scale, v_scale: device, 16-byte aligned; scales null unless the
  * pool is quantised.
  */

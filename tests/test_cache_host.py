@@ -202,6 +202,14 @@ def test_copy_refusals(vas_lib):
     assert v._lib.paged_kv_copy(FAKE, FAKE, NULL, NULL, None, None, None, 1, _pool(v), NULL) == bad
 
 
+def test_copy_refuses_pages_past_32_bits(vas_lib):
+    """Byte offsets in a page are 32 bits, up to the end of the 16 KB segment that the page
+    ends in: pages that end less than a segment below 2^31 are refused like larger ones."""
+    v = vas_lib
+    for heads in (262143, 262142, 262144, 1 << 30):   # 8192 bytes a head and page of 16 fp32 tokens
+        assert _copy(v, [1], [2], num_kv_heads=heads, kv_dtype=v.VAS_F32) == v.VAS_E_UNSUPPORTED, heads
+
+
 def test_keep_path_refusals(vas_lib):
     v = vas_lib
     bad = v.VAS_E_INVALID_ARG

@@ -742,7 +742,8 @@ int check_pool(const vas_pool_dims* d, const void* k, const void* v, const float
       d->kv_dtype < VAS_F32 || d->kv_dtype > VAS_INT8)
     return VAS_E_UNSUPPORTED;
   const int64_t tb = (int64_t)d->num_kv_heads * d->head_dim * element_size(d->kv_dtype);
-  if (tb * d->page_size > INT32_MAX || d->num_layers > 32767) return VAS_E_UNSUPPORTED;
+  // Offsets inside a page are 32 bits, up to the end of its last segment.
+  if (tb * d->page_size > INT32_MAX - kCopySeg || d->num_layers > 32767) return VAS_E_UNSUPPORTED;
   if (!k || !v || misaligned(k, 16) || misaligned(v, 16)) return VAS_E_INVALID_ARG;
   const bool quant = is_quant(d->kv_dtype);
   if (quant != (ks != nullptr) || quant != (vs != nullptr) || misaligned(ks, 16) ||
