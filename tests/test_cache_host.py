@@ -255,3 +255,34 @@ def test_prefix_attention_refusals(vas_lib):
     assert v.paged_attn_prefix_workspace_size(dims, 3) > v.paged_attn_prefix_workspace_min(dims, 3)
     assert v.paged_attn_prefix_workspace_size(dims, -1) == 0
     assert v.paged_attn_prefix_workspace_min(v.vas_attn_dims(**{**d, "kv_dtype": v.VAS_F32}), 1) == 0
+
+
+def test_prefix_binding_refuses_dims_of_other_tensors(vas_lib):
+    """dims kept from another batch, pool, table or code type are refused before anything is
+    looked at on a device: the kernels take their extents from them."""
+    import torch
+    v = vas_lib
+    z = lambda *s, t=torch.int32: torch.zeros(*s, dtype=t)
+    q, kv = z(6, 8, 64, t=torch.bfloat16), z(20, 16, 2, 64, t=torch.bfloat16)
+    bt, lens = z(3, 10), z(3)
+    base = v.attn_dims(q, kv, bt, lens)
+
+    def call(dims, q=q, kv=kv, bt=bt, lens=lens, **kw):
+        v.paged_attn_fwd_prefix(q, kv, kv, bt, lens, z(3), z(2), z(1), q, z(6, 8, t=torch.float32), z(64),
+                                dims=dims, **kw)
+
+    def refused(dims, **kw):
+        with pytest.raises(ValueError, match="dims"):
+            call(dims, **kw)
+
+    for name, value in dict(num_seqs=2, total_q_tokens=5, num_q_heads=4, num_kv_heads=4, head_dim=128,
+                            page_size=32, num_pages=21, max_pages_per_seq=11, kv_dtype=v.VAS_F32).items():
+        d = v.attn_dims(q, kv, bt, lens)
+        setattr(d, name, value)
+        refused(d)
+    refused(base, bt=z(3, 9))                            # a narrower table than that of the dims
+    refused(base, q=z(6, 16, 64, t=torch.bfloat16))
+    refused(base, kv=z(20, 32, 2, 64, t=torch.bfloat16))
+    codes = z(20, 16, 2, 64, t=torch.uint8)
+    refused(v.attn_dims(q, codes, bt, lens, quant="fp8"), kv=codes, quant="int8")
+    refused(v.attn_dims(q, codes, bt, lens, quant="fp8"), kv=codes)

@@ -301,6 +301,17 @@ def alloc_prefix_workspace(dims: vas_attn_dims, num_groups: int, device=None,
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
 
 
+def _dims_fit(d: vas_attn_dims, q, k_pages, block_table, seq_lens, quant: Optional[str]) -> bool:
+    """Whether every extent the kernels take from d is that of the tensors."""
+    T, Hq, D = q.shape
+    n, P, Hkv, Dk = k_pages.shape
+    code = _KV_CODES.get(q.dtype) if quant is None else _QUANT_CODES.get(quant)
+    return Dk == D and (
+        (d.num_seqs, d.total_q_tokens, d.num_q_heads, d.num_kv_heads, d.head_dim, d.page_size, d.num_pages,
+         d.max_pages_per_seq, d.kv_dtype) ==
+        (seq_lens.shape[0], T, Hq, Hkv, D, P, n, block_table.shape[-1], code))
+
+
 def paged_attn_fwd_prefix(q, k_pages, v_pages, block_table, seq_lens, query_lens, group_start,
                           prefix_lens, out, lse, workspace, *, k_scale=None, v_scale=None,
                           quant: Optional[str] = None, tree_mask=None, share: str = "auto",
@@ -309,11 +320,14 @@ def paged_attn_fwd_prefix(q, k_pages, v_pages, block_table, seq_lens, query_lens
     """Attention of groups of sequences that share a prefix (include/vas.h:
     paged_attn_fwd_prefix).  group_start [G + 1] and prefix_lens [G] int32; share "auto"
     (where it pays) or "always"; the other arguments are those of paged_attn_fwd, or with
-    quant those of paged_attn_fwd_quant."""
+    quant those of paged_attn_fwd_quant.  dims, when given, are those of these tensors
+    (attn_dims)."""
     if share not in _SHARE_CODES:
         raise ValueError('share is "auto" or "always"')
     if dims is None:
         dims = attn_dims(q, k_pages, block_table, seq_lens, scale, quant=quant)
+    elif not _dims_fit(dims, q, k_pages, block_table, seq_lens, quant):
+        raise ValueError("dims are those of another batch, pool or table")
     dev = torch.cuda.current_device()
     i32, f32 = torch.int32, torch.float32
     G = prefix_lens.shape[0]
@@ -322,8 +336,6 @@ def paged_attn_fwd_prefix(q, k_pages, v_pages, block_table, seq_lens, query_lens
         raise ValueError("tree_mask needs one 64-bit word per query token")
     kv = torch.uint8 if quant is not None else q.dtype
     B = seq_lens.shape
-    if (dims.num_seqs, dims.total_q_tokens, dims.num_pages) != (B[0], q.shape[0], n):
-        raise ValueError("dims are those of another batch")
     st = _lib.paged_attn_fwd_prefix(
         _here(dev, q, "q"), _here(dev, k_pages, "k_pages", None, kv),
         _here(dev, v_pages, "v_pages", pool, kv), _here(dev, k_scale, "k_scale", (n, Hkv, P), f32),
