@@ -345,7 +345,9 @@ typedef struct {
  * Errors: VAS_E_INVALID_ARG, VAS_E_UNSUPPORTED, VAS_E_CUDA.  Device: a token whose
  * sequence has inconsistent lengths (VAS_DEV_BAD_LENGTHS), whose page is outside the
  * pool (VAS_DEV_BAD_PAGE) or whose position is outside the table (VAS_DEV_BAD_POSITION)
- * is not stored and its q_out row is NaN.
+ * is not stored and its q_out row is NaN.  A call with num_seqs 0 or total_tokens 0 does
+ * nothing: with tokens but no sequences q_out keeps what it held (the Python binding
+ * refuses that).
  * A page shared by several sequences is never a target of a correct step (vas_seq_fork
  * gives every sequence its own last page); two tokens with one slot race.
  */

@@ -286,3 +286,15 @@ def test_prefix_binding_refuses_dims_of_other_tensors(vas_lib):
     codes = z(20, 16, 2, 64, t=torch.uint8)
     refused(v.attn_dims(q, codes, bt, lens, quant="fp8"), kv=codes, quant="int8")
     refused(v.attn_dims(q, codes, bt, lens, quant="fp8"), kv=codes)
+
+
+def test_append_binding_refuses_tokens_of_no_sequence(vas_lib):
+    """The C entry point does nothing for an empty batch; with tokens in hand that would leave
+    their q_out rows as they were."""
+    import torch
+    v = vas_lib
+    z = lambda *s, t=torch.int32: torch.zeros(*s, dtype=t)
+    bf = torch.bfloat16
+    kv, x = z(20, 16, 2, 64, t=bf), z(5, 2, 64, t=bf)
+    with pytest.raises(ValueError, match="5 tokens of no sequence"):
+        v.paged_kv_append(x, x, x, z(0, 4), z(0), z(0), x.clone(), kv, kv)

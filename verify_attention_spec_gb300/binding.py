@@ -374,10 +374,12 @@ def paged_kv_append(q, k, v, block_table, seq_lens, query_lens, q_out, k_pages, 
     cos_sin [max_position, rotary_dim] fp32 or None, positions [T] int32 or None; q and
     q_out may both be None.  k_pages / v_pages [num_pages, P, Hkv, D], with quant uint8
     codes and k_scale / v_scale [num_pages, Hkv, P]."""
-    dev = torch.cuda.current_device()
-    i32, f32 = torch.int32, torch.float32
     num_pages, P, Hkv, D = pool = k_pages.shape
     T, B, act = k.shape[0], seq_lens.shape[0], k.dtype
+    if B == 0 and T > 0:  # the call would do nothing, and leave q_out as it was
+        raise ValueError(f"{T} tokens of no sequence")
+    dev = torch.cuda.current_device()
+    i32, f32 = torch.int32, torch.float32
     if quant is not None:
         if quant not in _QUANT_CODES or act != torch.bfloat16 or k_pages.dtype != torch.uint8:
             raise ValueError("a quantised pool is uint8 codes with bf16 q, k and v")
