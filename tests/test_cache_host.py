@@ -298,3 +298,16 @@ def test_append_binding_refuses_tokens_of_no_sequence(vas_lib):
     kv, x = z(20, 16, 2, 64, t=bf), z(5, 2, 64, t=bf)
     with pytest.raises(ValueError, match="5 tokens of no sequence"):
         v.paged_kv_append(x, x, x, z(0, 4), z(0), z(0), x.clone(), kv, kv)
+
+
+def test_append_in_place_of_one_token_with_any_stride(vas_lib):
+    """One row is contiguous whatever its stride (a slice of one packed projection): q_out may
+    be q.  Without a device the call goes on to fail there.  Several rows may not."""
+    import torch
+    v = vas_lib
+    q = P_(1 << 30)
+    if not torch.cuda.is_available():  # the addresses are not those of any memory
+        assert _append(v, total_tokens=1, q_stride=48 * 128, ptrs={"out": q}) == v.VAS_E_CUDA
+        assert _append(v, total_tokens=1, ptrs={"out": q}) == v.VAS_E_CUDA
+    assert _append(v, total_tokens=2, q_stride=48 * 128, ptrs={"out": q}) == v.VAS_E_INVALID_ARG
+    assert _append(v, total_tokens=1, q_stride=48 * 128, ptrs={"out": P_((1 << 30) + 256)}) == v.VAS_E_INVALID_ARG

@@ -839,7 +839,7 @@ int paged_kv_append(const void* q, const void* k, const void* v, const void* q_w
     // same lanes, or apart.
     const int64_t T = d.total_tokens, out_bytes = T * qw * es;
     auto span = [&](int64_t stride, int64_t width) { return ((T - 1) * stride + width) * es; };
-    const bool in_place = q_out == q && d.q_stride == qw;
+    const bool in_place = q_out == q && (d.q_stride == qw || T == 1);  // one row is contiguous
     if ((!in_place && overlap(q_out, out_bytes, q, span(d.q_stride, qw))) ||
         overlap(q_out, out_bytes, k, span(d.k_stride, kw)) ||
         overlap(q_out, out_bytes, v, span(d.v_stride, kw)))
