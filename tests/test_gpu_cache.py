@@ -646,3 +646,52 @@ def test_offsets_past_32_bits(vas_lib, kv):
         assert torch.equal(x, y)
     for t in last:
         assert t is None or not t[:big - N].any()
+
+
+@pytest.mark.parametrize("B", [1024, 1025, 3000, 5003])
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_append_more_sequences_than_starts(vas_lib, B, kv):
+    """The first rows of up to 1024 sequences lie in shared memory; of more, only every 2nd
+    to 5th, the last chunk not filled evenly, with empty windows at the chunks' ends."""
+    rng = np.random.default_rng(B)
+    ql = (rng.random(B) < 0.6).astype(np.int64) * rng.integers(1, 4, B)
+    step = -(-B // 1024)
+    ql[0] = ql[step - 1::2 * step] = ql[2 * step::3 * step] = 0
+    ql[-1] = 2
+    _run(vas_lib, Case(ql + rng.integers(0, 20, B), ql, 3, 1, 64, 16, kv, seed=B))
+
+
+@pytest.mark.parametrize("B", [900, 1025, 2500])
+def test_append_bad_lengths_of_many_sequences(vas_lib, B):
+    """A window longer than its sequence, a table too short for it, windows that are too few
+    and too many for the rows: those tokens are refused, the rest stored."""
+    v = vas_lib
+    rng = np.random.default_rng(B)
+    ql = rng.integers(0, 3, B)
+    bad = [B // 3, B // 2]
+    ql[bad] = 2
+    c = Case(ql + rng.integers(0, 20, B), ql, 2, 1, 64, 16, "bf16", seed=B)
+    seq, pos = c.places()
+
+    def outcome(refused):
+        before = c.kp.clone()
+        c.q_out.fill_(7.0)
+        c.call(v)
+        assert v.vas_last_device_error() == v.VAS_DEV_BAD_LENGTHS
+        nan = torch.isnan(c.q_out.float()).flatten(1)
+        want = torch.from_numpy(refused).cuda()
+        assert torch.equal(nan.all(1), want) and torch.equal(nan.any(1), want)
+        page = torch.from_numpy(c.bt_np[seq[refused], pos[refused] // 16]).long().cuda()
+        slot = torch.from_numpy(pos[refused] % 16).cuda()
+        assert torch.equal(c.kp[page, slot], before[page, slot])
+
+    c.lens_t[bad[0]] = 1                                  # shorter than its window
+    c.lens_t[bad[1]] = 16 * c.bt.shape[1] + 1             # past the table
+    outcome(np.isin(seq, bad))
+    c.lens_t.copy_(torch.from_numpy(c.lens))
+    last = int(np.flatnonzero(ql)[-1])
+    c.ql_t[last] = 0                                      # the last rows have no sequence
+    outcome(seq == last)
+    c.ql_t[last] = int(ql[last]) + 1                      # a window past the last row
+    c.lens_t[last] = max(int(c.lens[last]), int(ql[last]) + 1)
+    outcome(seq == last)

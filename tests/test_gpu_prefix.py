@@ -490,3 +490,14 @@ def test_large_queries_of_one_member(vas_lib, kv, size):
         out, lse = run_prefix(vas_lib, to_device(a), start, prefix)
         check_quant_rel_l2(out, lse, ref_o, ref_l)
     assert vas_lib.vas_last_device_error() == 0
+
+
+def test_more_groups_than_threads_and_uncached_lengths(vas_lib):
+    """600 groups, and 5000 sequences, whose lengths the planner reads from memory each time
+    it needs them; groups with idle members among them."""
+    rng = np.random.default_rng(35)
+    groups = [(int(rng.integers(250, 330)), [(int(rng.integers(1, 40)), 1)] * int(rng.integers(1, 4)))
+              for _ in range(600)]
+    check(vas_lib, groups, 4, 1, 64, 16, wl.BF16, seed=35)
+    groups = [(256, [(2, int(q)) for q in rng.integers(0, 3, 50)]) for _ in range(100)]
+    check(vas_lib, groups, 2, 1, 64, 16, wl.FP8, seed=36)
