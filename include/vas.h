@@ -264,6 +264,8 @@ int paged_attn_fwd_static(const void* q, const void* k_pages, const void* v_page
  *             extra kernels: when 48 Mi elements of K are read less, or in a small batch
  *             (fewer than 64 Mi elements of K in all) when a prefix has 2048 tokens (1024
  *             if the members' windows have more than 16 rows per KV head on average).
+ *             The device decides; a batch that is not shared takes 5 to 6 us longer than
+ *             paged_attn_fwd, which is the call for batches known not to share.
  *             VAS_SHARE_ALWAYS: whenever they can be.
  * A group is computed with its members apart, as paged_attn_fwd does, when it has one
  * member with query tokens, when its prefix is below 256 tokens, where sharing would not
@@ -369,7 +371,8 @@ typedef struct {
 
 /* Copy pages src[i] -> dst[i], i < n, in K and V of every layer (with their scales when
  * quantised): the tail of a fork, the moves of vas_pool_compact.
- * src, dst, tokens: HOST arrays, read before the call returns.  tokens[i] in 1..P copies
+ * src, dst, tokens: HOST arrays, read before the call returns (a captured call keeps the
+ * pairs it was captured with, in every replay).  tokens[i] in 1..P copies
  * the first tokens[i] slots of the page and leaves the others; null copies whole pages.
  * No page may be named twice among the destinations, or be both a source and a
  * destination (VAS_E_INVALID_ARG, and nothing is copied): the copies run at once.

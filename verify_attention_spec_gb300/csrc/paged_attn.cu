@@ -118,6 +118,11 @@ constexpr int kMinPrefixShare = 4;     // units of weight of a CTA, at least
 // groups of 8 on 2048 (112 Mi) 63 and 109.  A small one, with fewer elements of K in all than
 // kSmallBatch, is bound by its longest unit: 4 members on 2048 tokens 39 and 48 us, on 1024
 // tokens 39 and 34, but 56 and 64 for windows of five tokens, whose units take twice as long.
+// 8-bit pages go by the same counts of elements, since the arithmetic of the conversion and not
+// the bytes bounds them apart; their borders lie a little lower (FP8: 64 members on 1024 tokens
+// 61 and 79, on 512 tokens 57 and 54; 32 on 2048 54 and 84; eight groups 66 and 146; 4 members on
+// 2048 tokens 46 and 70, on 1024 tokens 44 and 45).  Where `auto` declines, the longer plan and
+// two kernels with nothing to do cost 5 to 6 us.
 constexpr int64_t kMinPrefixSaved = 48ll << 20;
 constexpr int64_t kSmallBatch = 64ll << 20;
 constexpr int64_t kLongPrefix = 2048;

@@ -124,9 +124,11 @@ __device__ __forceinline__ size_t part_row(const PrefixArgs& a, const Piece& p, 
 // thread a row, two warps a scheduler left the issue slots 72 % idle and the tensor cores
 // at 40 %.)  The scores come to registers and go back as bf16 pairs over the first columns
 // of S, which are the A operand of the second product from there, so P never passes through
-// shared memory.  TMEM: S 2 x 128, O 2 x D columns.  Shared memory: the query tiles and a
-// ring of K and V tiles, 128-byte swizzled as the TMA boxes land.  A producer warp streams
-// the pages, an MMA warp issues.
+// shared memory.  (The rounding of P to bf16 is as in paged_attn.cu: 2^-8 of a weight at most,
+// as much as the output's own; shared parts have 256 tokens or more, over which it averages.)
+// TMEM: S 2 x 128, O 2 x D columns.  Shared memory: the query tiles and a ring of K and V tiles,
+// 128-byte swizzled as the TMA boxes land.  A producer warp streams the pages, an MMA warp
+// issues.
 //
 // Measured, 128 windows of 5 tokens and 64 heads on a 16384-token prefix (344 GFLOP, 67 MB of K
 // and V): 241 us, 1.43 PFLOP/s, the tensor pipe 64 % busy.  Bounded by the MMA warp: products
@@ -135,9 +137,9 @@ __device__ __forceinline__ size_t part_row(const PrefixArgs& a, const Piece& p, 
 // Quantised pages (KV: VAS_FP8_E4M3, VAS_INT8): the producer lands a tile's codes beside its
 // 16-bit slot (with 128-wide heads in the upper half of it) and the scales of its tokens with
 // the V codes; two converter warps expand the codes, exact in f16, into the slot.  Products
-// are f16 (a row of Q scaled into range by a power of two where it must be); scores are multiplied by
-// the K scale of their token, P by its V scale.  Bounded by the softmax, whose warps read each
-// scale as a broadcast: the whole call takes 491 us on FP8 pages, 370 on bf16.
+// are f16 (a row of Q scaled into range by a power of two where it must be, P relative to the
+// V scales by the references); scores are multiplied by the K scale of their token, P by its V
+// scale.  Bounded by the softmax, whose warps read each scale as a broadcast: the whole call takes 472 us on FP8 pages, 370 on bf16.
 constexpr int kTile = kPrefixTile;          // tokens of a tile, rows of a stream
 constexpr int kStreamThreads = 256, kStreamWarps = kStreamThreads / 32;
 constexpr int kProducerWarp = 2 * kStreamWarps, kMmaWarp = kProducerWarp + 1;
@@ -646,8 +648,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1)
         if (lane == 0) mbar_arrive(&p_full[st]);
       }
       used += 2 * x.n_tiles;
-      // While the last products run: bad pages of the piece, where the row goes.
-      // Bad pages of the piece: this thread looks at every 256th.
+      // While the last products run: bad pages of the piece (this thread looks at every
+      // 256th), where the row goes.
       bool bad = false;
       {
         const int32_t* bt = a.block_table + (size_t)x.g.leader * a.maxp + x.page_begin;
