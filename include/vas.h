@@ -14,9 +14,13 @@
  *   paged_kv_append : the write side of the cache: per-head RMS norms of queries and
  *                     keys, the position rotation and the store into the pages
  *                     (quantised where the pool is), in one pass.
+ *   paged_kv_read   : cached tokens of any storage type as bf16 or fp32 rows.
  *   paged_kv_copy, paged_kv_keep_path : copies of whole or partly filled pages (forks,
  *                     compaction) and the move of an accepted draft path to the slots
  *                     after the context.
+ *   spec_logits     : the logits of a verification window to the probabilities that
+ *                     spec_verify takes: penalties for repeated tokens, a bias, a grammar
+ *                     mask, temperature and softmax.
  *   spec_verify     : speculative-decoding modified rejection sampling with an
  *                     in-kernel Philox4x32-10 stream; spec_verify_tree, the same rule
  *                     over a draft tree.
@@ -82,6 +86,10 @@ typedef struct CUstream_st* vas_stream_t; /* identical to cudaStream_t */
 #define VAS_BF16 1
 #define VAS_FP8_E4M3 2 /* FP8 E4M3 codes + fp32 scales, paged_attn_fwd_quant only */
 #define VAS_INT8 3     /* INT8 codes + fp32 scales, paged_attn_fwd_quant only     */
+/* The same codes with one scale per page and KV head, [num_pages, Hkv], instead of one per
+ * token and head: paged_attn_fwd_quant, paged_kv_append, paged_kv_read and paged_kv_copy. */
+#define VAS_FP8_BLOCK 18
+#define VAS_INT8_BLOCK 19
 
 /* ==================================================================================
  * Paged decode / verify attention
@@ -113,7 +121,8 @@ typedef struct {
   int32_t num_pages;         /* physical pages in the pool                            */
   int32_t max_pages_per_seq; /* columns of block_table                                */
   int32_t kv_dtype;          /* VAS_BF16 or VAS_F32 (q and out share it), or          */
-                             /* VAS_FP8_E4M3 / VAS_INT8 (q and out bf16)              */
+                             /* VAS_FP8_E4M3 / VAS_INT8 (q and out bf16), or their    */
+                             /* block-scaled forms VAS_FP8_BLOCK / VAS_INT8_BLOCK     */
   float scale;               /* softmax scale; 0 selects 1/sqrt(head_dim)             */
 } vas_attn_dims;
 
@@ -195,6 +204,8 @@ int paged_attn_fwd_tree(const void* q, const void* k_pages, const void* v_pages,
  * v_pages     the same for V.
  * k_scale     [num_pages, Hkv, P] device fp32, 16-byte aligned.
  * v_scale     the same for V.  Scales of slots past a sequence's end are not used.
+ *             VAS_FP8_BLOCK, VAS_INT8_BLOCK: [num_pages, Hkv], one scale for the codes of a
+ *             page and head: k = k_scale[p * num_kv_heads + h] * code(k_pages[p][t][h][d]).
  * q, out      [T, Hq, D] bf16.  lse, block_table, seq_lens, query_lens, workspace: as for
  *             paged_attn_fwd (the workspace queries are the same for every kv_dtype).
  * tree_mask   null (the causal window) or the draft-tree masks of paged_attn_fwd_tree.
@@ -258,7 +269,8 @@ int paged_attn_fwd_static(const void* q, const void* k_pages, const void* v_page
  *             member with query tokens is the one whose table is read there.
  * k_scale, v_scale  as for paged_attn_fwd_quant; null for a bf16 pool.
  * tree_mask   as for paged_attn_fwd_tree, or null.
- * dims->kv_dtype is VAS_BF16, VAS_FP8_E4M3 or VAS_INT8 (VAS_F32: VAS_E_UNSUPPORTED).
+ * dims->kv_dtype is VAS_BF16, VAS_FP8_E4M3 or VAS_INT8 (VAS_F32 and the block-scaled types:
+ *             VAS_E_UNSUPPORTED; paged_attn_fwd_quant reads shared pages of those too).
  * workspace   at least paged_attn_prefix_workspace_min(dims, num_groups) bytes.
  * share       VAS_SHARE_AUTO: the prefixes of a batch are shared when that pays for the
  *             extra kernels: when 48 Mi elements of K are read less, or in a small batch
@@ -306,8 +318,9 @@ typedef struct {
   int32_t page_size;         /* P: 16 or 32                                           */
   int32_t num_pages;
   int32_t max_pages_per_seq;
-  int32_t kv_dtype;          /* of the pool: VAS_BF16, VAS_FP8_E4M3 or VAS_INT8 with  */
-                             /* bf16 q, k, v; VAS_F32 with fp32 q, k, v               */
+  int32_t kv_dtype;          /* of the pool: VAS_BF16, VAS_FP8_E4M3, VAS_INT8,        */
+                             /* VAS_FP8_BLOCK or VAS_INT8_BLOCK with bf16 q, k, v;    */
+                             /* VAS_F32 with fp32 q, k, v                             */
   int32_t rotary_dim;        /* leading elements of a head that are rotated: 0, or a  */
                              /* multiple of 16 up to D                                */
   int32_t interleaved;       /* 0: pairs (i, i + rotary_dim / 2); 1: (2i, 2i + 1)      */
@@ -333,6 +346,19 @@ typedef struct {
  * scale = max |y| / 448 (E4M3) or / 127 (INT8), 1 if that is 0, and the codes
  * y / scale rounded to nearest even; a row with an infinity or a NaN gets a scale that
  * is not finite.  Nothing else of the pool is written.
+ * Block-scaled pools (VAS_FP8_BLOCK, VAS_INT8_BLOCK) have one scale s per page and head.
+ * With m the largest finite |y| of the tokens that the call adds to a page, and top 448
+ * (E4M3) or 127 (INT8):
+ *   - the first token goes to slot 0: s is the smallest power of two with m <= 448 s (E4M3:
+ *     its precision does not depend on the size) or m / 127 (INT8), at least 2^-126;
+ *   - otherwise the page holds tokens, and s is its scale, doubled until m <= 448 s, or
+ *     m <= 127.5 s (which rounds to 127); the codes of the slots before the first new one are
+ *     then divided by the same power of two, rounded to nearest even (E4M3: exact unless
+ *     below 2^-6).  A scale that is not positive and finite is replaced as for a fresh page,
+ *     and the codes stay.
+ * Each token's codes are y / s rounded to nearest even; infinities and NaN become the NaN of
+ * E4M3, or 0 in INT8, and do not count for m.  s never falls while a page holds tokens.
+ * Slots behind the last new token are left as they are.
  *
  * q, k, v     [T, heads, D] device, rows q_stride / k_stride / v_stride elements apart
  *             (slices of one packed projection, say), 16-byte aligned.
@@ -366,7 +392,7 @@ typedef struct {
   int32_t page_size;         /* P: 16 or 32                                           */
   int32_t num_kv_heads;
   int32_t head_dim;          /* 64 or 128                                             */
-  int32_t kv_dtype;          /* the four storage types                                */
+  int32_t kv_dtype;          /* any of the storage types                              */
 } vas_pool_dims;
 
 /* Copy pages src[i] -> dst[i], i < n, in K and V of every layer (with their scales when
@@ -379,7 +405,8 @@ typedef struct {
  * A page of one layer and operand stays 16 KB below 2^31 bytes (VAS_E_UNSUPPORTED; in
  * paged_kv_keep_path too).
  * k_pages, v_pages, k_scale, v_scale: device, 16-byte aligned; scales null unless the
- * pool is quantised.
+ * pool is quantised.  In a block-scaled pool the target page takes the source's scales, so
+ * the slots of a partly copied page that are left as they are change their meaning.
  */
 int paged_kv_copy(void* k_pages, void* v_pages, float* k_scale, float* v_scale,
                   const int32_t* src, const int32_t* dst, const int32_t* tokens, int32_t n,
@@ -397,8 +424,9 @@ int paged_kv_copy(void* k_pages, void* v_pages, float* k_scale, float* v_scale,
  * accepted_len <= 0 moves nothing.
  * block_table [num_seqs, max_pages_per_seq], seq_lens, query_lens [num_seqs]: device
  * int32, those of the verification.
- * Errors: VAS_E_INVALID_ARG, VAS_E_UNSUPPORTED, VAS_E_CUDA.  Device, and the row then
- * moves nothing: VAS_DEV_BAD_TREE (accepted_len above n, a node outside 1..ql_i - 1 or
+ * Errors: VAS_E_INVALID_ARG, VAS_E_UNSUPPORTED (block-scaled pools among it: nodes of one
+ * page may go to a page of another scale; append the accepted tokens again instead),
+ * VAS_E_CUDA.  Device, and the row then moves nothing: VAS_DEV_BAD_TREE (accepted_len above n, a node outside 1..ql_i - 1 or
  * not above the one before it, seq_index outside the batch, or naming a sequence that an
  * earlier row names), VAS_DEV_BAD_LENGTHS, VAS_DEV_BAD_PAGE.
  */
@@ -408,6 +436,107 @@ int paged_kv_keep_path(void* k_pages, void* v_pages, float* k_scale, float* v_sc
                        const int32_t* seq_index, const int32_t* path,
                        const int32_t* accepted_len, int32_t B, int32_t n,
                        const vas_pool_dims* dims, vas_stream_t stream);
+
+typedef struct {
+  int32_t num_seqs;          /* B                                                     */
+  int32_t total_tokens;      /* T = sum of lens (rows of k_out and v_out)             */
+  int32_t num_kv_heads;      /* Hkv                                                   */
+  int32_t head_dim;          /* D: 64 or 128                                          */
+  int32_t page_size;         /* P: 16 or 32                                           */
+  int32_t num_pages;
+  int32_t max_pages_per_seq;
+  int32_t kv_dtype;          /* of the pool: any of the storage types                 */
+  int32_t out_dtype;         /* VAS_BF16 or VAS_F32                                   */
+  int64_t k_stride;          /* elements from one row of k_out to the next, a multiple */
+  int64_t v_stride;          /* of 16 bytes; and of v_out                             */
+} vas_read_dims;
+
+/* Read cached tokens back: positions starts[i] .. starts[i] + lens[i] - 1 of sequence i (from
+ * 0 when starts is null), packed by sequence in batch order.  Row t of k_out and v_out is
+ * [Hkv, D], the values the pool's codes stand for (the product of code and scale in fp32),
+ * rounded once to out_dtype.  For a cached prompt that another program takes, the host's
+ * copy of an evicted sequence, or pages that change their storage type.
+ *
+ * k_pages, v_pages, k_scale, v_scale, block_table [B, max_pages_per_seq]: as for
+ *             paged_attn_fwd_quant (scales null unless the pool is quantised).
+ * starts      [B] device int32 or null.
+ * lens        [B] device int32, 0 skips the sequence.
+ * k_out, v_out [T, Hkv, D] device, rows k_stride / v_stride elements apart, 16-byte aligned;
+ *             apart from the pool and from each other.
+ * Errors: VAS_E_INVALID_ARG (tokens without sequences among it), VAS_E_UNSUPPORTED,
+ * VAS_E_CUDA.  Device: rows of a sequence with a negative start or length, or one that ends
+ * past its table, and rows of no sequence, are NaN (VAS_DEV_BAD_LENGTHS), as are rows whose
+ * page is outside the pool (VAS_DEV_BAD_PAGE).
+ */
+int paged_kv_read(const void* k_pages, const void* v_pages, const float* k_scale,
+                  const float* v_scale, const int32_t* block_table, const int32_t* starts,
+                  const int32_t* lens, void* k_out, void* v_out, const vas_read_dims* dims,
+                  vas_stream_t stream);
+
+/* ==================================================================================
+ * Logits of a verification window
+ *
+ * What stands between the target's logits and spec_verify's p ("Continuous Batching &
+ * Speculative Decoding" (neuralmasteryai.com), section "3. Mathematical Proof": p is the
+ * target's distribution after its sampling parameters).  The web pages give no formulas for
+ * the parameters; these are the usual ones.
+ * ================================================================================== */
+#define VAS_LOGITS 0
+#define VAS_PROBS 1
+
+typedef struct {
+  int32_t num_seqs;          /* B                                                     */
+  int32_t num_drafts;        /* n: a sequence has n + 1 rows; 0..255                  */
+  int32_t vocab;             /* V, at most 1048576                                    */
+  int32_t dtype;             /* of logits: VAS_F32 or VAS_BF16                        */
+  int32_t out_kind;          /* VAS_LOGITS or VAS_PROBS                               */
+  int32_t max_tokens;        /* columns of tokens, below 2^20 - 255                   */
+  int32_t max_bias;          /* columns of bias_tokens and bias, at most 1024         */
+  int64_t row_stride;        /* elements from one row of logits to the next, >= V     */
+} vas_logits_dims;
+
+/* Row j of sequence b is the position behind draft j (behind the context for j = 0); with
+ * parents, behind node j of the draft tree.  count(x) is how often token x was generated:
+ * among tokens[b][prompt_lens[b]] .. tokens[b][token_lens[b] - 1] and among the drafts on the
+ * way to row j (drafts 0 .. j - 1, or node j and its ancestors).  In fp32, in this order:
+ *     z(x) = logits[b][j][x]
+ *     z(x) = z / repetition[b] if z > 0 else z * repetition[b],   if count(x) > 0 or x is in
+ *            the prompt, tokens[b][0] .. tokens[b][prompt_lens[b] - 1]
+ *     z(x) = z - frequency[b] count(x) - presence[b],             if count(x) > 0
+ *     z(x) = z + (sum of the biases that bias_tokens[b] gives x, in list order)
+ *     z(x) = -inf                                                 where the mask's bit is 0
+ * VAS_LOGITS: out = z.  VAS_PROBS: out = exp((z - max z) / temperature[b]) / sum; with
+ * temperature 0, 1 at the largest z (the first of equals) and 0 elsewhere; 0 everywhere when
+ * no token is left (spec_verify then sets VAS_DEV_EMPTY_ROW).  A row whose allowed z hold a
+ * NaN is NaN, and so is one with an infinite maximum or a temperature below 0 or NaN; what
+ * the mask takes away may be anything.
+ *
+ * logits      [B, n + 1, V] device, rows row_stride elements apart.
+ * tokens      [B, max_tokens] device int32, prompt first, or null (no history).  Values
+ *             outside 0..V - 1 name no logit and are skipped (placeholders).
+ * token_lens  [B] device int32, with tokens.  prompt_lens [B] or null (0).
+ * draft_tokens [B, n] device int32; needed when penalties are given and n > 0.
+ * parents     [B, n] device int32 as for spec_verify_tree, or null (a chain).
+ * repetition, frequency, presence  [B] device fp32, or null (1, 0, 0).  Without all three
+ *             tokens and drafts are not read.
+ * bias_tokens, bias [B, max_bias] device int32 and fp32, or both null; entries outside
+ *             0..V - 1 are skipped (pad with -1).
+ * mask        [B, n + 1, ceil(V / 32)] device 32-bit words, bit x % 32 of word x / 32 set where
+ *             token x is allowed, or null.
+ * temperature [B] device fp32, or null (1); null for VAS_LOGITS.
+ * out         [B, n + 1, V] device fp32, contiguous, apart from logits.
+ * Fastest with logits 16-byte aligned in every row and V a multiple of 4.
+ * Errors: VAS_E_INVALID_ARG, VAS_E_UNSUPPORTED, VAS_E_CUDA.  Device: VAS_DEV_BAD_LENGTHS
+ * (token_lens above max_tokens or prompt_lens above token_lens; the sequence's rows are NaN),
+ * VAS_DEV_BAD_TREE, VAS_DEV_BAD_TOKEN (a parent or a draft out of range on the way to a row,
+ * which is then NaN).
+ */
+int spec_logits(const void* logits, const int32_t* tokens, const int32_t* token_lens,
+                const int32_t* prompt_lens, const int32_t* draft_tokens, const int32_t* parents,
+                const float* repetition, const float* frequency, const float* presence,
+                const int32_t* bias_tokens, const float* bias, const uint32_t* mask,
+                const float* temperature, float* out, const vas_logits_dims* dims,
+                vas_stream_t stream);
 
 /* ==================================================================================
  * Speculative verification: modified rejection sampling

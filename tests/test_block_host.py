@@ -1,0 +1,126 @@
+"""Block-scaled caches, read-back and logits: what their entry points refuse on the host (no
+kernel is launched by these checks)."""
+import ctypes
+
+import pytest
+
+FAKE, NULL = ctypes.c_void_p(1 << 20), ctypes.c_void_p(0)
+ODD = ctypes.c_void_p((1 << 20) + 2)
+
+
+@pytest.fixture()
+def v(vas_lib):
+    return vas_lib
+
+
+def _append(v, ptrs=None, **kw):
+    d = dict(num_seqs=2, total_tokens=4, num_q_heads=32, num_kv_heads=8, head_dim=128, page_size=16,
+             num_pages=100, max_pages_per_seq=10, kv_dtype=v.VAS_FP8_BLOCK, rotary_dim=128, interleaved=0,
+             max_position=64, q_stride=4096, k_stride=1024, v_stride=1024, eps=1e-6)
+    d.update(kw)
+    p = dict(q=FAKE, k=FAKE, v=FAKE, qw=NULL, kw=NULL, cs=FAKE, pos=NULL, bt=FAKE, sl=FAKE, ql=FAKE,
+             qo=ctypes.c_void_p(1 << 30), kp=FAKE, vp=FAKE, ks=FAKE, vs=FAKE)
+    p.update(ptrs or {})
+    return v._lib.paged_kv_append(*p.values(), ctypes.byref(v.vas_append_dims(**d)), NULL)
+
+
+@pytest.mark.parametrize("kind", ["VAS_FP8_BLOCK", "VAS_INT8_BLOCK"])
+def test_append(v, kind):
+    kv = dict(kv_dtype=getattr(v, kind))
+    assert _append(v, {"ks": NULL}, **kv) == _append(v, {"vs": NULL}, **kv) == v.VAS_E_INVALID_ARG
+    assert _append(v, {"ks": ODD}, **kv) == _append(v, {"kp": ODD}, **kv) == v.VAS_E_INVALID_ARG
+    assert _append(v, head_dim=96, **kv) == _append(v, page_size=8, **kv) == v.VAS_E_UNSUPPORTED
+    assert _append(v, num_seqs=0, **kv) == _append(v, total_tokens=0, **kv) == v.VAS_OK
+    assert _append(v, kv_dtype=17) == _append(v, kv_dtype=20) == v.VAS_E_UNSUPPORTED
+
+
+@pytest.mark.parametrize("kind", ["VAS_FP8_BLOCK", "VAS_INT8_BLOCK"])
+def test_attention(v, kind):
+    d = dict(num_seqs=4, total_q_tokens=10, num_q_heads=32, num_kv_heads=8, head_dim=128, page_size=16,
+             num_pages=100, max_pages_per_seq=10, kv_dtype=getattr(v, kind), scale=0.0)
+    dims = lambda **kw: ctypes.byref(v.vas_attn_dims(**{**d, **kw}))  # noqa: E731
+
+    def call(ks=FAKE, vs=FAKE, q=FAKE, ws=1 << 30, **kw):
+        return v._lib.paged_attn_fwd_quant(q, FAKE, FAKE, ks, vs, FAKE, FAKE, FAKE, NULL, FAKE, FAKE,
+                                           dims(**kw), FAKE, ws, NULL)
+
+    bad, uns = v.VAS_E_INVALID_ARG, v.VAS_E_UNSUPPORTED
+    assert call(ks=NULL) == call(vs=NULL) == call(ks=ODD) == call(q=ODD) == call(num_q_heads=30) == bad
+    assert call(head_dim=96) == call(page_size=64) == uns and call(kv_dtype=16) == bad
+    assert call(ws=16) == v.VAS_E_WORKSPACE
+    assert call(num_seqs=0) == call(total_q_tokens=0) == v.VAS_OK
+    # only paged_attn_fwd_quant takes them
+    st = v._lib.paged_attn_fwd(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, dims(), FAKE, 1 << 30, NULL)
+    assert st == bad
+    st = v._lib.paged_attn_fwd_prefix(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, NULL, FAKE,
+                                      FAKE, dims(), 1, 0, FAKE, 1 << 30, NULL)
+    assert st == uns
+    ask = v.vas_attn_dims(**d)
+    assert 0 < v.paged_attn_workspace_min(ask) <= v.paged_attn_workspace_size(ask)
+    assert v.paged_attn_prefix_workspace_min(ask, 1) == v.paged_attn_prefix_workspace_size(ask, 1) == 0
+
+
+def test_copy_and_keep_path(v):
+    d = dict(num_layers=1, num_pages=10, page_size=16, num_kv_heads=2, head_dim=64, kv_dtype=v.VAS_INT8_BLOCK)
+    ids = (ctypes.c_int32 * 2)(1, 2)
+    at = lambda i: ctypes.c_void_p(ctypes.addressof(ids) + 4 * i)  # noqa: E731
+    pool = ctypes.byref(v.vas_pool_dims(**d))
+    assert v._lib.paged_kv_copy(FAKE, FAKE, NULL, NULL, at(0), at(1), NULL, 1, pool, NULL) == v.VAS_E_INVALID_ARG
+    assert v._lib.paged_kv_copy(FAKE, FAKE, FAKE, FAKE, at(0), at(1), NULL, 0, pool, NULL) == v.VAS_OK
+    st = v._lib.paged_kv_keep_path(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 4, NULL, FAKE, FAKE, 2, 3, pool, NULL)
+    assert st == v.VAS_E_UNSUPPORTED
+
+
+def test_read(v):
+    def call(ptrs=None, **kw):
+        d = dict(num_seqs=2, total_tokens=4, num_kv_heads=8, head_dim=128, page_size=16, num_pages=100,
+                 max_pages_per_seq=10, kv_dtype=v.VAS_FP8_BLOCK, out_dtype=v.VAS_BF16, k_stride=1024, v_stride=1024)
+        d.update(kw)
+        p = dict(kp=FAKE, vp=FAKE, ks=FAKE, vs=FAKE, bt=FAKE, st=NULL, ln=FAKE, ko=FAKE, vo=FAKE)
+        p.update(ptrs or {})
+        return v._lib.paged_kv_read(*p.values(), ctypes.byref(v.vas_read_dims(**d)), NULL)
+
+    bad, uns = v.VAS_E_INVALID_ARG, v.VAS_E_UNSUPPORTED
+    assert v._lib.paged_kv_read(*[FAKE] * 9, None, NULL) == bad
+    for p in ("kp", "vp", "ks", "vs", "bt", "ln", "ko", "vo"):
+        assert call({p: NULL}) == bad, p
+        assert call({p: ODD}) == bad, p
+    assert call({"st": ODD}) == bad
+    for kw in [dict(num_seqs=-1), dict(total_tokens=-1), dict(num_kv_heads=0), dict(num_seqs=0), dict(k_stride=1023),
+               dict(v_stride=1028), dict(num_pages=0), dict(max_pages_per_seq=0), dict(num_pages=1 << 28),
+               dict(kv_dtype=v.VAS_BF16)]:
+        assert call(**kw) == bad, kw
+    for kw in [dict(head_dim=96), dict(page_size=8), dict(kv_dtype=4), dict(out_dtype=v.VAS_FP8_E4M3)]:
+        assert call(**kw) == uns, kw
+    assert call(total_tokens=0) == call(num_seqs=0, total_tokens=0) == v.VAS_OK
+
+
+def test_logits(v):
+    names = ("logits tokens token_lens prompt_lens drafts parents repetition frequency presence bias_tokens bias "
+             "mask temperature out").split()
+
+    def call(given=(), ptrs=None, **kw):
+        d = dict(num_seqs=2, num_drafts=3, vocab=1000, dtype=v.VAS_BF16, out_kind=v.VAS_PROBS, max_tokens=10,
+                 max_bias=4, row_stride=1000)
+        d.update(kw)
+        p = {n: FAKE if n in given else NULL for n in names}
+        p.update(logits=FAKE, out=ctypes.c_void_p(1 << 30))
+        p.update(ptrs or {})
+        return v._lib.spec_logits(*p.values(), ctypes.byref(v.vas_logits_dims(**d)), NULL)
+
+    bad, uns = v.VAS_E_INVALID_ARG, v.VAS_E_UNSUPPORTED
+    assert v._lib.spec_logits(*[FAKE] * 14, None, NULL) == bad
+    for given in [("tokens",), ("token_lens",), ("prompt_lens",), ("bias",), ("bias_tokens",), ("parents",),
+                  ("repetition",), ("frequency",)]:  # parts of a whole
+        assert call(given) == bad, given
+    for p in ({"logits": NULL}, {"out": NULL}, {"logits": ctypes.c_void_p((1 << 20) + 1)}, {"out": ODD},
+              {"mask": ODD}, {"temperature": ODD}, {"out": FAKE}):
+        assert call(ptrs=p) == bad, p
+    for kw in [dict(num_seqs=-1), dict(num_drafts=-1), dict(num_drafts=256), dict(vocab=0), dict(row_stride=999),
+               dict(out_kind=2), dict(max_tokens=-1), dict(max_bias=-1)]:
+        assert call(**kw) == bad, kw
+    for kw in [dict(dtype=v.VAS_INT8), dict(vocab=1 << 21, row_stride=1 << 21), dict(max_bias=1025),
+               dict(max_tokens=1 << 20)]:
+        assert call(**kw) == uns, kw
+    assert call(("temperature",), out_kind=v.VAS_LOGITS) == bad
+    assert call(num_seqs=0) == v.VAS_OK

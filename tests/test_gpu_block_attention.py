@@ -1,0 +1,358 @@
+"""GPU parity of attention over block-scaled pages (include/vas.h: paged_attn_fwd_quant with
+VAS_FP8_BLOCK and VAS_INT8_BLOCK) against the float64 oracle, which decodes the same codes with
+each page's scale."""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from verify_attention_spec_gb300 import workloads as wl
+
+from gpu_common import ancestor_masks, check_quant_rel_l2, compare_attention
+
+pytestmark = pytest.mark.gpu
+
+KINDS = ["fp8_block", "int8_block"]
+
+
+@dataclasses.dataclass
+class Batch:
+    q: torch.Tensor
+    k: torch.Tensor
+    v: torch.Tensor
+    ks: torch.Tensor
+    vs: torch.Tensor
+    bt: np.ndarray
+    lens: np.ndarray
+    qlens: np.ndarray
+    kind: str
+
+    @property
+    def fp8(self):
+        return self.kind == "fp8_block"
+
+
+def _codes(x, kind):
+    if kind == "fp8_block":
+        return x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    return x.round().clamp(-127, 127).to(torch.int8).view(torch.uint8)
+
+
+def make(lens, qlens, Hq, Hkv, D, P, kind, seed, extra=0, amp=(1.0, 1.0)):
+    """N(0, 1) keys, values and queries, sizes of pages and heads a factor of e^0.3 apart."""
+    lens, qlens = np.asarray(lens), np.asarray(qlens)
+    bt, pages = wl.build_pool(lens, P, seed, int((-(-lens // P)).sum()) + extra)
+    g = torch.Generator().manual_seed(seed)
+    pool = []
+    for a in amp:
+        x = a * torch.randn(pages, P, Hkv, D, generator=g) * torch.exp(0.3 * torch.randn(pages, 1, Hkv, 1, generator=g))
+        s = x.abs().amax((1, 3)) / (448.0 if kind == "fp8_block" else 127.0)
+        pool.append((_codes(x / s[:, None, :, None], kind), s))
+    q = torch.randn(int(qlens.sum()), Hq, D, generator=g).to(torch.bfloat16)
+    return Batch(q, pool[0][0], pool[1][0], pool[0][1], pool[1][1], bt, lens, qlens, kind)
+
+
+def reference(b, parents=None, scale=None):
+    P = b.k.shape[1]
+    wide = lambda s: s[..., None].expand(-1, -1, P).contiguous().numpy()  # noqa: E731
+    return oracle.paged_attn_quant(wl.bf16_bits(b.q), b.k.numpy(), b.v.numpy(), wide(b.ks), wide(b.vs),
+                                   b.bt.astype(np.int32), b.lens.astype(np.int32), b.qlens.astype(np.int32),
+                                   fmt=oracle.Q_E4M3 if b.fp8 else oracle.Q_INT8, parents=parents, scale=scale)
+
+
+def run(vas, b, masks=None, nbytes=None, scale=0.0, dev=None):
+    i32 = lambda x: torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()  # noqa: E731
+    q, k, v, ks, vs = (x.cuda() for x in (b.q, b.k, b.v, b.ks, b.vs))
+    bt, lens, ql = i32(b.bt), i32(b.lens), i32(b.qlens)
+    out = torch.full_like(q, float("nan"))
+    lse = torch.full(q.shape[:2], float("nan"), device="cuda")
+    dims = vas.attn_dims(q, k, bt, lens, scale=scale, quant=b.kind)
+    ws = vas.alloc_workspace(dims, nbytes=nbytes)
+    ws.fill_(255)
+    tm = None if masks is None else torch.from_numpy(np.ascontiguousarray(masks).view(np.int64)).cuda()
+    vas.paged_attn_fwd_quant(q, k, v, ks, vs, bt, lens, ql, out, lse, ws, quant=b.kind, tree_mask=tm, dims=dims)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+def check(vas, b, masks=None, parents=None, **kw):
+    ref_o, ref_l = reference(b, parents)
+    out, lse = run(vas, b, masks, **kw)
+    compare_attention(out, lse, ref_o, ref_l, wl.FP8)
+    assert vas.vas_last_device_error() == 0
+    return out, lse
+
+
+# Decode rows, verify windows, prompt chunks, sequences shorter than a page and than a tile,
+# borders of pages and tiles, long contexts that are split, an empty query.
+LENS = [1, 16, 33, 5, 70, 300, 1500, 64, 9000, 130, 2100, 95, 128, 129, 257, 700]
+QLENS = [1, 1, 2, 5, 9, 1, 8, 0, 5, 17, 33, 64, 1, 128, 100, 650]
+
+
+@pytest.mark.parametrize("D,P,Hq,Hkv", [(128, 32, 64, 8), (128, 16, 32, 8), (64, 16, 4, 4), (64, 32, 16, 2),
+                                        (128, 16, 5, 1), (64, 32, 3, 3), (128, 32, 24, 2), (128, 16, 40, 1),
+                                        (64, 16, 96, 2)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_shapes(vas_lib, D, P, Hq, Hkv, kind):
+    check(vas_lib, make(LENS, QLENS, Hq, Hkv, D, P, kind, seed=D + P + Hq))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("B,hi", [(1, 1), (1, 40), (1, 30000), (3, 2000), (150, 700), (1500, 60), (5000, 40)])
+def test_decode_batches(vas_lib, kind, B, hi):
+    rng = np.random.default_rng(B + hi)
+    lens = rng.integers(max(1, hi // 2), hi + 1, B)
+    check(vas_lib, make(lens, np.ones(B, int), 8, 2, 128, 16, kind, seed=B))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,Hkv", [(128, 8), (64, 4)])
+def test_trees(vas_lib, kind, D, Hkv):
+    lens, qlens = [40, 3000, 64, 700, 130], [2, 9, 64, 33, 5]
+    b = make(lens, qlens, 8 * Hkv, Hkv, D, 32, kind, seed=29)
+    parents = wl.draft_tree_parents(qlens, seed=29, extra_roots=0.1)
+    check(vas_lib, b, ancestor_masks(parents, qlens), parents)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_smallest_workspace_and_repetition(vas_lib, kind):
+    b = make([9000, 30, 4100, 17], [1, 5, 5, 1], 32, 8, 128, 16, kind, seed=5)
+    dims = vas_lib.attn_dims(b.q, b.k, torch.from_numpy(b.bt), torch.from_numpy(b.lens), quant=kind)
+    check(vas_lib, b, nbytes=vas_lib.paged_attn_workspace_min(dims))
+    o1, l1 = check(vas_lib, b)
+    o2, l2 = run(vas_lib, b)
+    assert torch.equal(o1, o2) and torch.equal(l1, l2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [128, 64])
+def test_q_of_any_size(vas_lib, kind, D):
+    """Queries near 2^18 and 2^-40, the softmax scale divided by the same power; and one element
+    2^12 above the others."""
+    b = make([200, 50, 3000], [1, 5, 9], 16, 4, D, 16, kind, seed=7)
+    for e in (18, -40):
+        c = dataclasses.replace(b, q=(b.q.float() * 2.0 ** e).to(torch.bfloat16))
+        scale = 2.0 ** -e / np.sqrt(D)
+        ref_o, ref_l = reference(c, scale=scale)
+        out, lse = run(vas_lib, c, scale=scale)
+        compare_attention(out, lse, ref_o, ref_l, wl.FP8)
+    b.q[..., 3] *= 4096
+    b.k[..., 3] = 0
+    check(vas_lib, b)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,P", [(128, 16), (64, 32)])
+@pytest.mark.parametrize("qlens", [[1, 4, 2], [1, 1, 1], [17, 30, 33]])
+def test_slots_of_no_token_may_hold_anything(vas_lib, kind, D, P, qlens):
+    """NaN codes (E4M3) behind each sequence's last token, in pages of no sequence and in their
+    scales: nothing leaks."""
+    b = make([17, 300, 33], qlens, 8, 2, D, P, kind, seed=3, extra=4)
+    own = np.zeros(b.k.shape[:2], bool)
+    for i, L in enumerate(b.lens):
+        t = np.arange(L)
+        own[b.bt[i, t // P], t % P] = True
+    ref = make([17, 300, 33], qlens, 8, 2, D, P, kind, seed=3, extra=4)
+    ref_o, ref_l = reference(ref)
+    dead = torch.from_numpy(~own)
+    for x in (b.k, b.v):
+        x[dead] = 0x7F
+    unused = torch.from_numpy(~own.any(1))
+    b.ks[unused] = float("nan")
+    b.vs[unused] = float("inf")
+    out, lse = run(vas_lib, b)
+    compare_attention(out, lse, ref_o, ref_l, wl.FP8)
+
+
+def test_nan_codes_reach_only_the_rows_that_see_them(vas_lib):
+    """A window whose third token has NaN keys and values: the rows before it stay as they were,
+    the rows from it on are NaN."""
+    for D, Hq, lens in ((128, 8, [500]), (128, 64, [140]), (64, 8, [500])):
+        b = make(lens, [5], Hq, 2, D, 16, "fp8_block", seed=4)
+        ref_o, ref_l = reference(b)
+        pos = lens[0] - 5 + 2
+        for x in (b.k, b.v):
+            x[b.bt[0, pos // 16], pos % 16] = 0x7F
+        out, lse = run(vas_lib, b)
+        compare_attention(out[:2], lse[:2], ref_o[:2], ref_l[:2], wl.FP8)
+        assert torch.isnan(out[2:].float()).all() and torch.isnan(lse[2:]).all()
+
+
+def _sink(b, weight, sink_v, amplitude, n):
+    """The first page's tokens but one out of the way, and that one an attention sink."""
+    D = b.q.shape[-1]
+    b.q[..., 0] = 4.0
+    b.k[..., 0] = 0
+    b.vs *= amplitude
+    k0 = (np.log(weight / (1.0 - weight) * n) + 0.5) * np.sqrt(D) / 4.0
+    for page in {int(p) for p in b.bt[:, 0]}:  # its page takes the sink's scales
+        b.k[page] = 0
+        b.k[page, 0, :, 0] = 0x7E if b.fp8 else 127
+        b.ks[page] = k0 / (448.0 if b.fp8 else 127.0)
+        b.vs[page] *= sink_v
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("weight,sink_v,amplitude", [(0.55, 0.02, 1.0), (0.9, 0.02, 0.25), (0.9, 0.1, 0.05),
+                                                     (0.9, 0.02, 1e-12), (0.55, 0.02, 1e6), (0.999, 0.001, 1.0)])
+@pytest.mark.parametrize("D", [128, 64])
+def test_weights_far_below_the_largest(vas_lib, kind, weight, sink_v, amplitude, D):
+    """A first token that takes most of the softmax and has a small V: the output is made by the
+    many small weights."""
+    b = make([4000, 4000, 4000], [1, 5, 40], 32, 4, D, 16, kind, seed=31)
+    _sink(b, weight, sink_v, amplitude, 4000)
+    ref_o, ref_l = reference(b)
+    dims = vas_lib.attn_dims(b.q, b.k, torch.from_numpy(b.bt), torch.from_numpy(b.lens), quant=kind)
+    for nbytes in (None, vas_lib.paged_attn_workspace_min(dims)):
+        out, lse = run(vas_lib, b, nbytes=nbytes)
+        check_quant_rel_l2(out, lse, ref_o, ref_l)
+    assert vas_lib.vas_last_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,P", [(128, 32), (64, 16)])
+def test_v_scales_that_change_along_a_sequence(vas_lib, kind, D, P):
+    """Pages whose V is up to 2^30 larger or smaller than their neighbours', growing, falling and
+    at random, some all zero."""
+    b = make([1000, 900, 800, 700], [1, 5, 20, 2], 16, 2, D, P, kind, seed=32)
+    rng = np.random.default_rng(33)
+    for i, L in enumerate(b.lens.tolist()):
+        n = -(-L // P)
+        e = [np.linspace(-30, 0, n), np.linspace(0, -30, n), rng.integers(-30, 1, n), np.full(n, -30.0)][i]
+        for c in range(n):
+            b.vs[b.bt[i, c]] *= float(2.0 ** np.round(e[c]))
+        b.vs[b.bt[i, n // 2]] = 0.0
+    ref_o, ref_l = reference(b)
+    out, lse = run(vas_lib, b)
+    row = 0
+    for ql in b.qlens.tolist():  # the sequences' sizes differ by 2^30
+        check_quant_rel_l2(out[row:row + ql], lse[row:row + ql], ref_o[row:row + ql], ref_l[row:row + ql])
+        row += ql
+    assert vas_lib.vas_last_device_error() == 0
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_scores_that_rise_along_a_sequence(vas_lib, kind):
+    """Keys that grow page by page, so the running maximum rises again and again; and fall."""
+    for sign in (1, -1):
+        b = make([3000, 2000], [1, 6], 16, 2, 128, 16, kind, seed=8)
+        b.q = (b.q.float().abs()).to(torch.bfloat16)
+        for i, L in enumerate(b.lens):
+            n = -(-int(L) // 16)
+            order = np.arange(n)[::sign]
+            for c in range(n):
+                b.ks[b.bt[i, c]] *= 0.02 * (1 + float(order[c]))
+        ref_o, ref_l = reference(b)
+        out, lse = run(vas_lib, b)
+        check_quant_rel_l2(out, lse, ref_o, ref_l)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_bad_pages_and_lengths(vas_lib, kind):
+    v = vas_lib
+    b = make([300, 300, 3000, 40], [1, 5, 1, 1], 16, 2, 128, 16, kind, seed=2)
+    ref_o, ref_l = reference(b)
+    rows = [0, 1, 1, 1, 1, 1, 2, 3]
+    for seq, page in ((1, 3), (2, 100), (3, 2)):
+        c = dataclasses.replace(b, bt=b.bt.copy())
+        c.bt[seq, page] = [10 ** 7, -5, 1 << 30][seq - 1]
+        out, lse = run(v, c)
+        bad = np.array([r == seq for r in rows])
+        assert torch.isnan(out[bad].float()).all() and torch.isnan(lse[bad]).all()
+        compare_attention(out[~bad], lse[~bad], ref_o[~bad], ref_l[~bad], wl.FP8)
+        assert v.vas_last_device_error() == v.VAS_DEV_BAD_PAGE
+    for L in (3, -1, 10 ** 6):
+        c = dataclasses.replace(b, lens=b.lens.copy())
+        c.lens[1] = L
+        out, lse = run(v, c)
+        bad = np.array([r == 1 for r in rows])
+        assert torch.isnan(out[bad].float()).all() and torch.isnan(lse[bad]).all()
+        compare_attention(out[~bad], lse[~bad], ref_o[~bad], ref_l[~bad], wl.FP8)
+        assert v.vas_last_device_error() == v.VAS_DEV_BAD_LENGTHS
+    c = dataclasses.replace(b, qlens=np.array([1, 3, 1, 1]))  # two rows of no sequence
+    out, lse = run(v, c)
+    assert torch.isnan(out[6:].float()).all() and torch.isnan(lse[6:]).all()
+    assert torch.isfinite(out[:6].float()).all() and v.vas_last_device_error() == v.VAS_DEV_BAD_LENGTHS
+    c = dataclasses.replace(b, qlens=np.array([1, 5, 4, 1]))  # more rows than q has
+    run(v, c)
+    assert v.vas_last_device_error() == v.VAS_DEV_BAD_LENGTHS
+    check(v, b)
+
+
+def test_streams_and_graphs(vas_lib):
+    """Two calls at once on streams of their own, each with its workspace, and a captured one
+    replayed on new queries."""
+    v = vas_lib
+    cases = [make([700, 2000, 90], [1, 5, 1], 32, 8, 128, 16, kind, seed=6) for kind in KINDS]
+    dev, outs = [], []
+    for b in cases:
+        i32 = lambda x: torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()  # noqa: E731
+        a = [x.cuda() for x in (b.q, b.k, b.v, b.ks, b.vs)] + [i32(b.bt), i32(b.lens), i32(b.qlens)]
+        out, lse = torch.empty_like(a[0]), torch.empty(a[0].shape[:2], device="cuda")
+        ws = v.alloc_workspace(v.attn_dims(a[0], a[1], a[5], a[6], quant=b.kind))
+        dev.append((a, out, lse, ws, b.kind))
+    call = lambda d: v.paged_attn_fwd_quant(*d[0], d[1], d[2], d[3], quant=d[4])  # noqa: E731
+    for d in dev:
+        call(d)
+    torch.cuda.synchronize()
+    want = [(d[1].clone(), d[2].clone()) for d in dev]
+    for _ in range(5):
+        for d in dev:
+            d[1].zero_()
+        torch.cuda.synchronize()
+        for d in dev:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                call(d)
+                call(d)
+        torch.cuda.synchronize()
+        for d, (o, s) in zip(dev, want):
+            assert torch.equal(d[1], o) and torch.equal(d[2], s)
+    for d, b in zip(dev, cases):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(d)
+        d[0][0].copy_(d[0][0].flip(0))
+        call(d)
+        torch.cuda.synchronize()
+        eager = d[1].clone()
+        d[1].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(d[1], eager)
+
+
+def test_binding_refusals(vas_lib):
+    v = vas_lib
+    b = make([20], [1], 8, 2, 128, 16, "fp8_block", seed=1)
+    i32 = lambda x: torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()  # noqa: E731
+    a = [x.cuda() for x in (b.q, b.k, b.v, b.ks, b.vs)] + [i32(b.bt), i32(b.lens), i32(b.qlens)]
+    out, lse = torch.empty_like(a[0]), torch.empty(a[0].shape[:2], device="cuda")
+    ws = v.alloc_workspace(v.attn_dims(a[0], a[1], a[5], a[6], quant="fp8_block"))
+
+    def call(at=None, x=None, quant="fp8_block", **kw):
+        args = [*a, out, lse, ws]
+        if at is not None:
+            args[at] = x
+        v.paged_attn_fwd_quant(*args, quant=quant, **kw)
+
+    per_token = torch.ones(b.k.shape[0], 2, 16, device="cuda")
+    for at, x in [(3, per_token), (4, b.vs), (3, a[3].double()), (0, a[0].float()), (1, a[1].float()),
+                  (2, a[2][:1]), (5, a[5].long()), (7, i32([1, 1])), (8, out.float()), (9, lse.half()),
+                  (0, a[0].expand(2, -1, -1))]:
+        with pytest.raises(ValueError):
+            call(at, x)
+    with pytest.raises(ValueError):
+        call(quant="fp4_block")
+    with pytest.raises(ValueError):
+        call(tree_mask=torch.zeros(3, dtype=torch.int64, device="cuda"))
+    other = v.attn_dims(torch.empty(2, 8, 128, dtype=torch.bfloat16), a[1], a[5], a[6], quant="fp8_block")
+    with pytest.raises(ValueError):
+        call(dims=other)
+    with pytest.raises(v.VasError):
+        call(10, ws[:256])
+    call()
+    torch.cuda.synchronize()
+    ref_o, ref_l = reference(b)
+    compare_attention(out, lse, ref_o, ref_l, wl.FP8)

@@ -1,0 +1,458 @@
+"""GPU tests of block-scaled caches (8-bit pages with one scale per page and KV head): the
+append that quantises them as it writes, the read-back of cached tokens and the copy of pages
+(include/vas.h: paged_kv_append, paged_kv_read, paged_kv_copy), against the definitions in 64
+bits."""
+import numpy as np
+import pytest
+import torch
+
+from verify_attention_spec_gb300 import workloads as wl
+
+pytestmark = pytest.mark.gpu
+
+KINDS = ["fp8_block", "int8_block"]
+TOP = {"fp8_block": 448.0, "int8_block": 127.0}
+GROW = {"fp8_block": 448.0, "int8_block": 127.5}
+EPS = 1e-5
+# Norm and rotation in fp32, in units of 2^-24 of |u| + |v| of a rotated pair: 24 cover the sum
+# of up to 128 squares as 16 fused terms a lane and 3 exchanges, mean, root, reciprocal, two
+# products and the rotation.
+SLACK = 24 * 2.0 ** -24
+
+
+def _i32(x):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()
+
+
+def _values(codes, kind):
+    """The numbers that codes stand for, before their scale."""
+    t = torch.float8_e4m3fn if kind.startswith("fp8") else torch.int8
+    return codes.cpu().view(t).double().numpy()
+
+
+def _round(x, kind):
+    """Codes' numbers of x (64 bits), rounded to nearest even."""
+    if kind.startswith("fp8"):
+        return torch.from_numpy(x).clamp(-448, 448).to(torch.float32).to(torch.float8_e4m3fn).double().numpy()
+    return np.clip(np.rint(x), -127, 127)
+
+
+def _power(x):
+    """The smallest power of two at or above x > 0."""
+    m, e = np.frexp(x)
+    return np.ldexp(1.0, np.where(m == 0.5, e - 1, e))
+
+
+class Cache:
+    """A block-scaled pool on the device and what appends should make of it."""
+
+    def __init__(self, kind, pages, P, Hkv, D, seed):
+        g = torch.Generator().manual_seed(seed)
+        self.kind, self.P, self.Hkv, self.D = kind, P, Hkv, D
+        mk = lambda: torch.randint(0, 256, (pages, P, Hkv, D), generator=g, dtype=torch.uint8).cuda()  # noqa: E731
+        sc = lambda: (torch.rand(pages, Hkv, generator=g) + 0.01).cuda()  # noqa: E731
+        self.k, self.v, self.ks, self.vs = mk(), mk(), sc(), sc()
+
+    def clone(self):
+        c = object.__new__(Cache)
+        c.__dict__.update(self.__dict__)
+        c.k, c.v, c.ks, c.vs = (x.clone() for x in (self.k, self.v, self.ks, self.vs))
+        return c
+
+
+class Step:
+    """Tokens of one append."""
+
+    def __init__(self, lens, qlens, Hq, Hkv, D, P, *, rot=None, inter=False, norm=True, seed=0,
+                 positions=None, bt=None, spread=3.0):
+        self.lens, self.qlens = np.asarray(lens), np.asarray(qlens)
+        self.Hq, self.D, self.P, self.inter = Hq, D, P, inter
+        self.rot = D if rot is None else rot
+        g = torch.Generator().manual_seed(seed)
+        T = int(self.qlens.sum())
+        size = torch.exp2(spread * torch.randn(T, Hq + 2 * Hkv, 1, generator=g))
+        qkv = (torch.randn(T, Hq + 2 * Hkv, D, generator=g) * size).to(torch.bfloat16).cuda()
+        self.q, self.k, self.v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+        self.wq, self.wk = ((1 + 0.3 * torch.randn(D, generator=g)).to(torch.bfloat16).cuda() if norm
+                            else None for _ in range(2))
+        if bt is None:
+            bt, _ = wl.build_pool(self.lens, P, seed + 5, int((-(-self.lens // P)).sum()))
+        self.bt = np.asarray(bt)
+        self.pos = np.concatenate([np.arange(L - q, L) for L, q in zip(self.lens, self.qlens)]
+                                  or [np.zeros(0)]).astype(np.int64)
+        self.positions = positions
+        at = self.pos if positions is None else np.asarray(positions)
+        self.at = at
+        self.cs = None
+        if self.rot:
+            ang = np.arange(int(at.max(initial=0)) + 1)[:, None] * 1e4 ** (-np.arange(0, self.rot, 2) / self.rot)[None, :]
+            self.cs = torch.from_numpy(np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)).cuda()
+        self.q_out = torch.full((T, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+
+    def call(self, vas, c, **kw):
+        args = dict(cos_sin=self.cs, q_weight=self.wq, k_weight=self.wk, interleaved=self.inter, eps=EPS,
+                    k_scale=c.ks, v_scale=c.vs, quant=c.kind,
+                    positions=None if self.positions is None else _i32(self.positions))
+        args.update(kw)
+        vas.paged_kv_append(self.q, self.k, self.v, _i32(self.bt), _i32(self.lens), _i32(self.qlens),
+                            self.q_out, c.k, c.v, **args)
+
+    def head(self, x, w):
+        """The transformed rows in 64 bits, and the magnitudes that the fp32 error goes by."""
+        x = x.double().cpu().numpy()
+        if w is not None:
+            x = x / np.sqrt((x * x).mean(-1, keepdims=True) + EPS) * w.double().cpu().numpy()
+        y, mag, h = x.copy(), np.abs(x), self.rot // 2
+        if self.rot:
+            cs = self.cs.double().cpu().numpy()[self.at][:, None, :]
+            cos, sin = cs[..., :h], cs[..., h:]
+            e, o = (slice(0, self.rot, 2), slice(1, self.rot, 2)) if self.inter else (slice(0, h), slice(h, self.rot))
+            y[..., e], y[..., o] = x[..., e] * cos - x[..., o] * sin, x[..., o] * cos + x[..., e] * sin
+            mag[..., e] = mag[..., o] = mag[..., e] + mag[..., o]
+        return y, mag
+
+
+def _check(step, before, after):
+    """Every code and scale of the pool after the append."""
+    kind, P = before.kind, step.P
+    fp8 = kind.startswith("fp8")
+    for x, w, name in ((step.k, step.wk, "k"), (step.v, None, "v")):
+        if name == "k":
+            y, mag = step.head(x, w)
+        else:
+            y = x.double().cpu().numpy()
+            mag = np.zeros_like(y)
+        slack = SLACK * mag
+        old, got = _values(getattr(before, name), kind), _values(getattr(after, name), kind)
+        s_old = getattr(before, name + "s").double().cpu().numpy()
+        s_got = getattr(after, name + "s").double().cpu().numpy()
+        want, s_want, fresh_int8 = old.copy(), s_old.copy(), np.zeros(s_old.shape, bool)
+        new = np.zeros(old.shape[:2], bool)
+        row = 0
+        for i, (L, q) in enumerate(zip(step.lens, step.qlens)):
+            for p in range((L - q) // P, -(-L // P) if q else 0):
+                lo, hi = max(L - q, p * P), min(L, (p + 1) * P)
+                rows = slice(row + lo - (L - q), row + hi - (L - q))
+                page, first = step.bt[i, p], lo - p * P
+                m = np.abs(y[rows]).max((0, 2))
+                if first == 0:
+                    s = _power(m / 448) if fp8 else m / 127
+                    fresh_int8[page] = not fp8
+                else:
+                    s = s_old[page] * _power(np.maximum(m / (GROW[kind] * s_old[page]), 1))
+                    kept = _round(old[page, :first] * (s_old[page] / s)[:, None], kind)
+                    want[page, :first] = np.where((s > s_old[page])[:, None], kept, old[page, :first])
+                s_want[page] = s
+                # codes: half a step of the value, of the smallest subnormal (E4M3), or of s
+                sg = s_got[page][None, :, None]
+                half = np.maximum(2.0 ** -4 * np.abs(y[rows]), 2.0 ** -10 * sg) if fp8 else 0.5 * sg
+                err = np.abs(got[page, first:first + hi - lo] * sg - y[rows])
+                assert np.all(err <= half * (1 + 2.0 ** -12) + slack[rows] * 2), (name, i, p, err.max())
+                new[page, first:first + hi - lo] = True
+            row += q
+        tol = np.where(fresh_int8, 2 * SLACK, 0.0)
+        np.testing.assert_array_less(np.abs(s_got - s_want), tol * s_want + 1e-300, err_msg=name)
+        np.testing.assert_array_equal(got[~new], want[~new], err_msg=name)
+
+
+def _run(vas, kind, step, Hkv, seed=3):
+    before = Cache(kind, int(step.bt.max(initial=0)) + 3, step.P, Hkv, step.D, seed)
+    after = before.clone()
+    step.call(vas, after)
+    torch.cuda.synchronize()
+    _check(step, before, after)
+    y, mag = step.head(step.q, step.wq)
+    err = np.abs(step.q_out.double().cpu().numpy() - y)
+    assert np.all(err <= 2.0 ** -8 * np.abs(y) + 2 * SLACK * mag + 1e-30)
+    assert vas.vas_last_device_error() == 0
+    return after
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,Hkv,D,P", [(32, 8, 128, 16), (64, 8, 128, 32), (16, 2, 64, 16), (5, 1, 64, 32)])
+def test_append_shapes(vas_lib, kind, Hq, Hkv, D, P):
+    """One token to a fresh page, one behind others, runs that start and end inside pages, whole
+    pages, an empty sequence."""
+    lens = [1, 7, P, P + 1, 3 * P, 100, 77, 40, 5 * P + 3]
+    qlens = [1, 1, P, 1, 2 * P, 33, 0, 40, 4 * P]
+    _run(vas_lib, kind, Step(lens, qlens, Hq, Hkv, D, P, seed=D + P), Hkv)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rot,inter,norm", [(0, False, False), (128, True, True), (64, False, True),
+                                            (32, True, False), (16, False, False)])
+def test_append_rotations(vas_lib, kind, rot, inter, norm):
+    _run(vas_lib, kind, Step([90, 33, 16], [50, 2, 16], 8, 2, 128, 16, rot=rot, inter=inter, norm=norm), 2)
+
+
+@pytest.mark.parametrize("B", [1, 300, 1024, 1025, 5000])
+def test_append_many_sequences(vas_lib, B):
+    rng = np.random.default_rng(B)
+    qlens = rng.integers(0, 4, B)
+    _run(vas_lib, "fp8_block", Step(qlens + rng.integers(1, 40, B), qlens, 4, 1, 64, 16, seed=B), 1)
+
+
+def test_append_given_positions(vas_lib):
+    _run(vas_lib, "fp8_block", Step([40, 9], [5, 3], 8, 2, 128, 16, positions=[35, 36, 36, 37, 37, 6, 7, 7]), 2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("order", ["growing", "falling", "random"])
+def test_token_by_token(vas_lib, kind, order):
+    """A page filled one token at a time, with sizes up to 2^20 apart: at the end each token is
+    within the half steps of the scales it was requantised by."""
+    P, D, Hkv = 16, 64, 2
+    e = {"growing": np.arange(P) * 1.25, "falling": -np.arange(P) * 1.25,
+         "random": np.random.default_rng(5).uniform(-10, 10, P)}[order]
+    c = Cache(kind, 3, P, Hkv, D, 1)
+    g = torch.Generator().manual_seed(2)
+    rows = (torch.randn(P, Hkv, D, generator=g) * torch.exp2(torch.tensor(e)).float()[:, None, None]).to(torch.bfloat16)
+    bound = np.zeros((P, Hkv, D))
+    bt = np.array([[1]])
+    for t in range(P):
+        st = Step([t + 1], [1], 2, Hkv, D, P, rot=0, norm=False, bt=bt)
+        st.k, st.v = rows[t:t + 1].cuda(), rows[t:t + 1].cuda()
+        s_old = c.ks[1].double().cpu().numpy()
+        before = c.clone()
+        st.call(vas_lib, c)
+        torch.cuda.synchronize()
+        _check(st, before, c)
+        s = c.ks[1].double().cpu().numpy()
+        x = np.abs(rows.double().numpy())
+        step = lambda v: (np.maximum(2.0 ** -4 * v, 2.0 ** -10 * s[:, None]) if kind == "fp8_block"  # noqa: E731
+                          else np.broadcast_to(0.5 * s[:, None], v.shape))
+        grew = (s > s_old)[None, :, None] & (t > 0)
+        bound[:t] += np.where(grew, step(x[:t] + bound[:t]), 0) if t else 0
+        bound[t] = step(x[t])
+    got = _values(c.k[1], kind) * c.ks[1].double().cpu().numpy()[None, :, None]
+    assert np.all(np.abs(got - rows.double().numpy()) <= bound * (1 + 2.0 ** -12))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_append_extremes(vas_lib, kind):
+    """Zero rows, the largest and the smallest magnitudes, infinities and NaN: what is not
+    finite does not count for the scale and becomes NaN (E4M3) or 0 (INT8)."""
+    P, D = 16, 128
+    c = Cache(kind, 5, P, 1, D, 1)
+    st = Step([3, 2, 2, 1, 1], [3, 2, 2, 1, 1], 1, 1, D, P, rot=0, norm=False,
+              bt=np.array([[0], [1], [2], [3], [4]]), spread=0.0)
+    v = st.v.clone()
+    v[0:3] = 0
+    v[3, 0, :2] = torch.tensor([3e38, -1e38])
+    v[5, 0] = 1e-38
+    v[5, 0, 1] = 1e-39
+    v[6] = v[5]
+    v[7, 0, :3] = torch.tensor([float("inf"), float("nan"), float("-inf")])
+    v[8, 0] = float("nan")
+    st.v = v
+    st.call(vas_lib, c)
+    torch.cuda.synchronize()
+    got = _values(c.v, kind)
+    s = c.vs[:, 0].double().cpu().numpy()
+    x = v.double().cpu().numpy()[:, 0]
+    assert np.all(got[0, :3] == 0) and s[0] == 2.0 ** -126 and s[4] == 2.0 ** -126
+    wild = [got[3, 0, 0, :3], got[4, 0, 0]]
+    assert all(np.isnan(w).all() if kind == "fp8_block" else (w == 0).all() for w in wild)
+    for page, rows in ((1, x[3:5]), (2, x[5:7]), (3, x[7:8])):
+        fin = np.isfinite(rows)
+        y = got[page, :len(rows), 0] * s[page]
+        half = np.maximum(2.0 ** -4 * np.abs(rows), 2.0 ** -10 * s[page]) if kind == "fp8_block" else 0.5 * s[page]
+        assert np.all((np.abs(y - rows) <= half * (1 + 2.0 ** -12))[fin])
+    # A page whose scale is no scale is replaced as if it were fresh, and its codes stay.
+    c.vs[1] = float("nan")
+    old = c.v.clone()
+    st2 = Step([4], [1], 1, 1, D, P, rot=0, norm=False, bt=np.array([[1]]))
+    st2.call(vas_lib, c)
+    torch.cuda.synchronize()
+    m = st2.v.double().abs().max().item()
+    assert abs(c.vs[1].item() - (_power(m / 448) if kind == "fp8_block" else m / 127)) <= 2.0 ** -22 * m
+    assert torch.equal(c.v[1, :3], old[1, :3])
+
+
+def test_append_without_queries_is_repeatable_and_captures(vas_lib):
+    """The same call gives the same bits, eagerly, on another stream and replayed."""
+    st = Step([50, 33, 16], [20, 1, 16], 8, 2, 128, 16)
+    base = Cache("fp8_block", int(st.bt.max()) + 1, 16, 2, 128, 4)
+    args = [_i32(st.bt), _i32(st.lens), _i32(st.qlens)]
+
+    def call(c):
+        vas_lib.paged_kv_append(None, st.k, st.v, *args, None, c.k, c.v, cos_sin=st.cs, k_weight=st.wk,
+                                eps=EPS, k_scale=c.ks, v_scale=c.vs, quant="fp8_block")
+
+    first = base.clone()
+    call(first)
+    side, other = torch.cuda.Stream(), base.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        call(other)
+    replayed = base.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(replayed)
+    assert torch.equal(replayed.k, base.k)
+    graph.replay()
+    torch.cuda.synchronize()
+    for c in (other, replayed):
+        assert all(torch.equal(getattr(c, n), getattr(first, n)) for n in ("k", "v", "ks", "vs"))
+    _check(st, base, first)
+
+
+def test_append_reports_bad_tokens(vas_lib):
+    """A bad page, inconsistent lengths and a position outside the table leave the pool as it
+    was where they are, and say so."""
+    st = Step([20, 20, 20], [4, 4, 4], 4, 1, 64, 16)
+    base = Cache("fp8_block", int(st.bt.max()) + 1, 16, 1, 64, 4)
+    c = base.clone()
+    good = st.bt.copy()
+    st.bt[1, 1] = 10 ** 6
+    st.call(vas_lib, c)
+    torch.cuda.synchronize()
+    assert vas_lib.vas_last_device_error() == vas_lib.VAS_DEV_BAD_PAGE
+    p = good[1, 1]
+    assert torch.equal(c.k[p], base.k[p]) and torch.equal(c.ks[p], base.ks[p])
+    assert torch.isnan(st.q_out[4:8].float()).all() and not torch.isnan(st.q_out[:4].float()).any()
+    st.bt = good
+    c = base.clone()
+    st.lens = np.array([20, 3, 20])  # fewer tokens than the step brings
+    st.call(vas_lib, c)
+    torch.cuda.synchronize()
+    assert vas_lib.vas_last_device_error() == vas_lib.VAS_DEV_BAD_LENGTHS
+    assert torch.equal(c.k[good[1]], base.k[good[1]]) and not torch.equal(c.k[good[2, 1]], base.k[good[2, 1]])
+    st.lens = np.array([20, 20, 20])
+    c = base.clone()
+    st.positions = [16, 17, 18, 19, 16, 17, 999, 19, 16, 17, 18, 19]
+    st.call(vas_lib, c)
+    torch.cuda.synchronize()
+    assert vas_lib.vas_last_device_error() == vas_lib.VAS_DEV_BAD_POSITION
+    assert torch.equal(c.k[good[1, 1], 2], base.k[good[1, 1], 2])
+    assert torch.isnan(st.q_out[6].float()).all()
+
+
+# ---- read-back --------------------------------------------------------------------------
+def _any_pool(kind, pages, P, Hkv, D, seed):
+    """A pool of any storage type, its scales, and its values in fp32 (code times scale)."""
+    g = torch.Generator().manual_seed(seed)
+    shape = (pages, P, Hkv, D)
+    if kind in ("bf16", "f32"):
+        x = torch.randn(shape, generator=g).to(torch.bfloat16 if kind == "bf16" else torch.float32)
+        return x.cuda(), None, x.float()
+    codes = torch.randint(0, 256, shape, generator=g, dtype=torch.uint8)
+    if kind.startswith("fp8"):
+        codes[(codes & 0x7F) == 0x7F] = 0  # no NaN
+    sc = torch.exp(torch.randn((pages, Hkv) if kind.endswith("block") else (pages, Hkv, P), generator=g))
+    val = codes.view(torch.float8_e4m3fn if kind.startswith("fp8") else torch.int8).float()
+    full = sc[:, None, :, None] if kind.endswith("block") else sc.transpose(1, 2)[..., None]
+    return codes.cuda(), sc.cuda(), val * full
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "fp8", "int8", "fp8_block", "int8_block"])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("P,Hkv,D", [(16, 8, 128), (32, 2, 64), (32, 3, 128), (16, 1, 64)])
+def test_read(vas_lib, kind, out, P, Hkv, D):
+    """Exactly the values the codes stand for: rows that start and end anywhere, none, rows of a
+    wider buffer, neighbours untouched."""
+    starts, lens = np.array([0, 5, 17, 0, 100, 3]), np.array([1, 40, 0, 64, 150, 2])
+    bt, pages = wl.build_pool(starts + lens, P, 3, int((-(-(starts + lens) // P)).sum()))
+    k, ks, kf = _any_pool(kind, pages, P, Hkv, D, 1)
+    v, vs, vf = _any_pool(kind, pages, P, Hkv, D, 2)
+    T = int(lens.sum())
+    wide = torch.full((T, 2 * Hkv + 1, D), 9.0, dtype=out, device="cuda")
+    ko, vo = wide[:, :Hkv], wide[:, Hkv:2 * Hkv]
+    vas_lib.paged_kv_read(k, v, _i32(bt), _i32(lens), ko, vo, starts=_i32(starts), k_scale=ks, v_scale=vs,
+                          quant=kind if "8" in kind else None)
+    torch.cuda.synchronize()
+    seq = np.repeat(np.arange(len(lens)), lens)
+    pos = np.concatenate([np.arange(s, s + n) for s, n in zip(starts, lens)])
+    page, slot = bt[seq, pos // P], pos % P
+    assert torch.equal(ko.cpu(), kf[page, slot].to(out)) and torch.equal(vo.cpu(), vf[page, slot].to(out))
+    assert (wide[:, 2 * Hkv] == 9.0).all()
+    assert vas_lib.vas_last_device_error() == 0
+
+
+def test_read_many_sequences_from_their_start(vas_lib):
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 30, 3000)
+    bt, pages = wl.build_pool(lens, 16, 3, int((-(-lens // 16)).sum()))
+    k, ks, kf = _any_pool("fp8_block", pages, 16, 2, 64, 1)
+    T = int(lens.sum())
+    ko, vo = (torch.empty(T, 2, 64, device="cuda") for _ in range(2))
+    vas_lib.paged_kv_read(k, k, _i32(bt), _i32(lens), ko, vo, k_scale=ks, v_scale=ks, quant="fp8_block")
+    seq = np.repeat(np.arange(len(lens)), lens)
+    pos = np.concatenate([np.arange(n) for n in lens])
+    want = kf[bt[seq, pos // 16], pos % 16]
+    assert torch.equal(ko.cpu(), want) and torch.equal(vo.cpu(), want)
+
+
+def test_read_reports_bad_sequences(vas_lib):
+    k, ks, kf = _any_pool("int8_block", 8, 16, 2, 64, 1)
+    bt = np.array([[0, 1], [2, 99], [4, 5], [6, 7]])
+    out = lambda n: [torch.zeros(n, 2, 64, device="cuda") for _ in range(2)]  # noqa: E731
+
+    def read(starts, lens, T):
+        ko, vo = out(T)
+        vas_lib.paged_kv_read(k, k, _i32(bt), _i32(lens), ko, vo, starts=_i32(starts), k_scale=ks,
+                              v_scale=ks, quant="int8_block")
+        torch.cuda.synchronize()
+        assert torch.equal(torch.isnan(ko), torch.isnan(vo))
+        return torch.isnan(ko).all((1, 2)).tolist(), torch.isnan(ko).any().item()
+
+    rows, _ = read([0, 14, 0, 0], [1, 4, 2, 1], 8)  # two of the rows on the bad page
+    assert rows == [False] + [False, False, True, True] + [False] * 3
+    assert vas_lib.vas_last_device_error() == vas_lib.VAS_DEV_BAD_PAGE
+    for starts, lens in (([0, 0, -1, 0], [1, 2, 3, 1]), ([0, 0, 31, 0], [1, 2, 3, 1]),
+                         ([0, 0, 2 ** 31 - 2, 0], [1, 2, 3, 1])):
+        rows, _ = read(starts, lens, 7)
+        assert rows == [False] * 3 + [True] * 3 + [False]
+        assert vas_lib.vas_last_device_error() == vas_lib.VAS_DEV_BAD_LENGTHS
+    rows, _ = read([0, 0, 0, 0], [1, 2, 3, 1], 9)  # two rows too many
+    assert rows == [False] * 7 + [True] * 2
+    assert vas_lib.vas_last_device_error() == vas_lib.VAS_DEV_BAD_LENGTHS
+
+
+# ---- copies -----------------------------------------------------------------------------
+def test_copy_takes_the_scales_along(vas_lib):
+    c = Cache("fp8_block", 6, 16, 2, 64, 1)
+    k, ks = c.k.clone(), c.ks.clone()
+    vas_lib.paged_kv_copy(c.k, c.v, [0, 3], [2, 5], tokens=[16, 7], k_scale=c.ks, v_scale=c.vs)
+    torch.cuda.synchronize()
+    k[2], ks[2] = k[0], ks[0]
+    k[5, :7], ks[5] = k[3, :7], ks[3]
+    assert torch.equal(c.k, k) and torch.equal(c.ks, ks)
+    layers = [torch.stack([x, x.flip(0)]) for x in (c.k, c.v, c.ks, c.vs)]
+    want = [x.clone() for x in layers]
+    vas_lib.paged_kv_copy(layers[0], layers[1], [1], [4], k_scale=layers[2], v_scale=layers[3])
+    torch.cuda.synchronize()
+    for x, w in zip(layers, want):
+        w[:, 4] = w[:, 1]
+        assert torch.equal(x, w)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_page_written_then_read(vas_lib, kind):
+    """Append, fork the last page, append to the fork, read both back."""
+    P, Hkv, D, n = 16, 2, 128, 21
+    pool = vas_lib.PagePool(8, P, seed=1)
+    pool.admit(1, n)
+    bt, lens = pool.block_table([1], 4)
+    c = Cache(kind, 8, P, Hkv, D, 7)
+    st = Step([n], [n], 4, Hkv, D, P, bt=bt, rot=0, norm=False, spread=0.5)
+    st.call(vas_lib, c)
+    pool.fork(1, 2, n)
+    src, dst, tokens = pool.fork_tail(1, 2, n)
+    vas_lib.paged_kv_copy(c.k, c.v, [src], [dst], tokens=[tokens], k_scale=c.ks, v_scale=c.vs)
+    pool.grow(2, 2)
+    bt, lens = pool.block_table([1, 2], 4)
+    more = Step([n, n + 2], [0, 2], 4, Hkv, D, P, bt=bt, rot=0, norm=False, seed=9, spread=0.5)
+    more.call(vas_lib, c)
+    T = int(lens.sum())
+    ko, vo = (torch.empty(T, Hkv, D, device="cuda") for _ in range(2))
+    vas_lib.paged_kv_read(c.k, c.v, _i32(bt), _i32(lens), ko, vo, k_scale=c.ks, v_scale=c.vs, quant=kind)
+    torch.cuda.synchronize()
+    for out, x, y, s in ((ko, st.k, more.k, c.ks), (vo, st.v, more.v, c.vs)):
+        want = torch.cat([x, x, y]).double()
+        page = torch.from_numpy(np.concatenate([bt[0, np.arange(n) // P], bt[1, np.arange(n + 2) // P]])).long()
+        sc = s[page.cuda()].double()[..., None]
+        # one rounding, and one more for tokens whose page grew its scale afterwards
+        half = torch.maximum(2.0 ** -4 * want.abs(), 2.0 ** -10 * sc) if kind == "fp8_block" else 0.5 * sc
+        assert ((out.double() - want).abs() <= 2.07 * half).all()

@@ -1,0 +1,283 @@
+"""GPU tests of spec_logits (include/vas.h): penalties, bias, mask, temperature and softmax of
+the rows of a verification window, against the definition in 64 bits."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _dev(x, dtype=torch.int32):
+    return None if x is None else torch.from_numpy(np.ascontiguousarray(x)).to("cuda", dtype)
+
+
+class Case:
+    def __init__(self, B, n, V, *, dtype="f32", hist=60, bias=0, mask=False, tree=False, temps=True,
+                 pad=0, seed=0, penalties=True):
+        rng = np.random.default_rng([seed, B, n, V])
+        self.B, self.n, self.V = B, n, V
+        t = torch.from_numpy(rng.normal(0, 3, (B, n + 1, V + pad)).astype(np.float32))
+        t = t.to(torch.bfloat16) if dtype == "bf16" else t
+        self.logits = t.cuda()[..., :V]
+        self.hist = rng.integers(0, max(1, min(V, 50)), (B, hist)) if hist else None
+        self.hist_lens = rng.integers(0, hist + 1, B) if hist else None
+        self.prompt_lens = rng.integers(0, self.hist_lens + 1) if hist else None
+        self.drafts = rng.integers(0, min(V, 60), (B, n)) if n else None
+        self.parents = np.floor(rng.random((B, n)) * np.arange(1, n + 1)).astype(int) if tree else None
+        self.rep = rng.uniform(0.7, 1.5, B) if penalties else None
+        self.freq = rng.uniform(-0.5, 0.5, B) if penalties else None
+        self.pres = rng.uniform(-0.5, 0.5, B) if penalties else None
+        self.bias_tokens = self.bias = self.mask = None
+        if bias:
+            self.bias_tokens = rng.integers(-2, min(V, 30) + 2, (B, bias))  # some named often, some nothing
+            self.bias = rng.uniform(-4, 4, (B, bias))
+        if mask:
+            self.mask = rng.integers(-2**31, 2**31, (B, n + 1, -(-V // 32)))
+            self.mask[0, 0] = 0  # a row that nothing is left of
+        self.temps = None
+        if temps:
+            self.temps = rng.uniform(0.5, 2.0, B)
+            self.temps[::3] = 0.0
+        for x in ("rep", "freq", "pres", "bias", "temps"):  # the fp32 numbers that the call gets
+            if getattr(self, x) is not None:
+                setattr(self, x, getattr(self, x).astype(np.float32))
+
+    def call(self, vas, probs=True, **kw):
+        f = torch.float32
+        out = torch.full((self.B, self.n + 1, self.V), 5.0, device="cuda")
+        a = dict(tokens=_dev(self.hist), token_lens=_dev(self.hist_lens), prompt_lens=_dev(self.prompt_lens),
+                 draft_tokens=_dev(self.drafts), parents=_dev(self.parents), repetition_penalty=_dev(self.rep, f),
+                 frequency_penalty=_dev(self.freq, f), presence_penalty=_dev(self.pres, f),
+                 bias_tokens=_dev(self.bias_tokens), bias=_dev(self.bias, f), mask=_dev(self.mask),
+                 temperature=_dev(self.temps, f) if probs else None, probs=probs)
+        a.update(kw)
+        vas.spec_logits(self.logits, a.pop("out", out), **a)
+        torch.cuda.synchronize()
+        return out.cpu().double().numpy()
+
+    def reference(self, probs=True):
+        """(the outputs in 64 bits, a bound of the fp32 error of z)"""
+        V = self.V
+        z = self.logits.cpu().double().numpy()
+        size = np.abs(z)
+        for b in range(self.B):
+            for j in range(self.n + 1):
+                r, e = z[b, j], size[b, j]
+                if self.rep is not None:
+                    L, P = (int(self.hist_lens[b]), int(self.prompt_lens[b])) if self.hist is not None else (0, 0)
+                    h = self.hist[b] if self.hist is not None else np.zeros(0, int)
+                    count, u = np.zeros(V, int), j
+                    for x in h[P:L]:
+                        if 0 <= x < V:
+                            count[x] += 1
+                    while u > 0:
+                        count[self.drafts[b, u - 1]] += 1
+                        u = u - 1 if self.parents is None else int(self.parents[b, u - 1])
+                    seen = count > 0
+                    seen[[x for x in h[:P] if 0 <= x < V]] = True
+                    rep, fr, pr = (float(x[b]) for x in (self.rep, self.freq, self.pres))
+                    r[seen] = np.where(r[seen] > 0, r[seen] / rep, r[seen] * rep)
+                    e[seen] = np.maximum(e[seen], np.abs(r[seen]))
+                    r -= fr * count + pr * (count > 0)
+                    e += np.abs(fr) * count + np.abs(pr) * (count > 0)
+                if self.bias is not None:
+                    for x, y in zip(self.bias_tokens[b], self.bias[b].astype(float)):
+                        if 0 <= x < V:
+                            r[x] += y
+                            e[x] += np.abs(y)
+                if self.mask is not None:
+                    bits = (self.mask[b, j][:, None] >> np.arange(32)) & 1
+                    r[bits.reshape(-1)[:V] == 0] = -np.inf
+        size[~np.isfinite(z)] = 0.0  # taken away, or infinite: exact
+        # a quotient, a product, two sums, and up to `bias` sums: each half a step of at most e
+        err = (6 + (self.bias.shape[1] if self.bias is not None else 0)) * 2.0 ** -24 * size
+        if not probs:
+            return z, err
+        p, rel = np.zeros_like(z), np.zeros_like(z)
+        for b in range(self.B):
+            T = 1.0 if self.temps is None else float(self.temps[b])
+            for j in range(self.n + 1):
+                r = z[b, j]
+                m = r.max()
+                if m == -np.inf:
+                    continue
+                if T == 0.0:
+                    p[b, j, int(np.argmax(r))] = 1.0
+                    continue
+                w = np.exp((r - m) / T)
+                p[b, j] = w / w.sum()
+                # exponent: the errors of z and of the maximum, and three roundings of it; then
+                # exp2f (2 ulp), the sum (fewer than 64 roundings in a chain), the quotient
+                fin = np.isfinite(r)
+                arg = np.where(fin, (m - r) / T, 0.0)
+                rel[b, j] = (err[b, j] + err[b, j].max()) / T + 4 * 2.0 ** -24 * arg + 72 * 2.0 ** -24
+        return p, 2 * rel * p + 2.0 ** -126
+
+    def check(self, vas, probs=True, **kw):
+        want, tol = self.reference(probs)
+        got = self.call(vas, probs, **kw)
+        fin = np.isfinite(want)
+        np.testing.assert_array_equal(got[~fin], want[~fin])
+        err = np.abs(got[fin] - want[fin])
+        assert np.all(err <= tol[fin]), (err - tol[fin]).max()
+        assert vas.vas_last_device_error() == 0
+        return got
+
+
+SHAPES = [(3, 4, 1000), (2, 0, 32000), (1, 2, 128256), (4, 1, 50257), (2, 3, 8), (5, 2, 1), (2, 1, 33),
+          (1, 1, 151936), (2, 7, 4096), (1, 0, 300007)]
+
+
+@pytest.mark.parametrize("B,n,V", SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_probabilities(vas_lib, B, n, V, dtype):
+    got = Case(B, n, V, dtype=dtype, bias=9, mask=True).check(vas_lib)
+    s = got.sum(-1)
+    assert s[0, 0] == 0 and np.all(np.abs(s[s > 0] - 1) < 1e-4)
+
+
+@pytest.mark.parametrize("B,n,V", SHAPES)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_logits(vas_lib, B, n, V, dtype):
+    Case(B, n, V, dtype=dtype, bias=5, mask=V > 100, temps=False).check(vas_lib, probs=False)
+
+
+@pytest.mark.parametrize("kw", [dict(hist=0), dict(penalties=False, bias=3), dict(penalties=False, mask=True),
+                                dict(penalties=False, temps=False), dict(tree=True), dict(pad=8), dict(pad=3),
+                                dict(hist=5000, tree=True, bias=300), dict(bias=1024)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("probs", [True, False])
+def test_parts(vas_lib, kw, dtype, probs):
+    """Each argument missing or alone; trees; rows with padding behind them, aligned and not."""
+    Case(3, 6, 5000, dtype=dtype, **{"temps": probs, **kw}).check(vas_lib, probs)
+
+
+@pytest.mark.parametrize("n", [255])
+def test_long_windows(vas_lib, n):
+    Case(2, n, 500, tree=True).check(vas_lib)
+    Case(1, n, 500).check(vas_lib)
+
+
+def test_a_vocabulary_in_chunks(vas_lib):
+    """More logits than the registers of a row's threads hold, up to the largest vocabulary."""
+    Case(2, 1, 140001, dtype="bf16", bias=20, mask=True).check(vas_lib)
+    Case(1, 1, 1048576, dtype="bf16", bias=20, mask=True, tree=True).check(vas_lib)
+    Case(1, 0, 1048576, dtype="f32", temps=False).check(vas_lib, probs=False)
+
+
+def test_null_penalties_count_one_by_one(vas_lib):
+    c = Case(4, 2, 700)
+    one, zero = np.ones(4, np.float32), np.zeros(4, np.float32)
+    for keep in ("rep", "freq", "pres"):
+        d = Case(4, 2, 700)
+        d.rep, d.freq, d.pres = (getattr(c, x) if x == keep else y
+                                 for x, y in (("rep", one), ("freq", zero), ("pres", zero)))
+        names = dict(rep="repetition_penalty", freq="frequency_penalty", pres="presence_penalty")
+        d.check(vas_lib, **{v: None for k, v in names.items() if k != keep})
+
+
+def test_ties_placeholders_and_masked_values(vas_lib):
+    """Equal largest logits go to the first; token ids outside the vocabulary are skipped; what
+    the mask takes away may be infinite or NaN, what it leaves makes the row NaN."""
+    c = Case(4, 1, 3000, mask=True, bias=4)
+    c.temps[:] = [0.0, 0.0, 1.0, 0.0]
+    c.logits = c.logits.clone()
+    c.mask[1, 1] = -1
+    c.logits[1, 1, [5, 70, 2999]] = 40.0
+    c.hist[:, ::7] = [-1]
+    c.hist[:, 3::7] = 3000
+    bits = ((c.mask[..., None] >> np.arange(32)) & 1).reshape(4, 2, -1)[..., :3000] == 0
+    off = torch.from_numpy(bits)
+    c.logits[off.cuda()] = float("nan")
+    c.logits[:, :, ::2][off[:, :, ::2].cuda()] = float("inf")
+    got = c.check(vas_lib)
+    bits[1, 1, 5] or np.testing.assert_equal(got[1, 1, 5], 1.0)
+    for row, x in (((2, 1), float("nan")), ((3, 1), float("nan"))):
+        c.mask[row][0] = -1
+        c.logits[row[0], row[1], 7] = x
+        assert np.isnan(c.call(vas_lib)[row]).all()
+    assert np.isfinite(c.call(vas_lib)[0]).all()
+
+
+def test_infinite_and_extreme_logits(vas_lib):
+    c = Case(3, 0, 5000, penalties=False)
+    c.temps[:] = [1.0, 0.5, 3.0]
+    c.logits[0, 0] = -3e38
+    c.logits[0, 0, 17] = 3e38
+    c.logits[1, 0, 100:] = -float("inf")
+    got = c.check(vas_lib)
+    assert got[0, 0, 17] == 1.0 and (got[1, 0, 100:] == 0).all()
+    c.logits[2, 0, 3] = float("inf")
+    assert np.isnan(c.call(vas_lib)[2]).all()
+
+
+def test_bad_rows_are_reported_and_alone(vas_lib):
+    v = vas_lib
+    c = Case(4, 5, 900)
+    good = c.call(v)
+    rows = lambda got: {(b, j) for b in range(4) for j in range(6) if np.isnan(got[b, j]).any()}  # noqa: E731
+    d = Case(4, 5, 900)
+    d.drafts[1, 2] = 900
+    got = d.call(v)
+    assert rows(got) == {(1, 3), (1, 4), (1, 5)} and v.vas_last_device_error() == v.VAS_DEV_BAD_TOKEN
+    assert np.array_equal(got[[0, 2, 3]], good[[0, 2, 3]])
+    d = Case(4, 5, 900)
+    d.parents = np.tile([0, 1, 2, 0, 4], (4, 1))
+    d.parents[2, 4] = 5  # node 5 under itself
+    got = d.call(v)
+    assert rows(got) == {(2, 5)} and v.vas_last_device_error() == v.VAS_DEV_BAD_TREE
+    for lens, prompt in (([61, 0, 0, 0], [0] * 4), ([-1, 0, 0, 0], [0] * 4), ([9] * 4, [10, 9, 0, 1])):
+        d = Case(4, 5, 900)
+        d.hist_lens, d.prompt_lens = np.array(lens), np.array(prompt)
+        assert rows(d.call(v)) == {(0, j) for j in range(6)}
+        assert v.vas_last_device_error() == v.VAS_DEV_BAD_LENGTHS
+    d = Case(4, 5, 900)
+    d.temps[:] = [-1.0, float("nan"), 1.0, float("inf")]
+    got = d.call(v)
+    assert rows(got) == {(b, j) for b in (0, 1) for j in range(6)}
+    np.testing.assert_allclose(got[3], 1 / 900, rtol=1e-6)
+    assert v.vas_last_device_error() == 0
+
+
+def test_streams_graphs_and_repetition(vas_lib):
+    c = Case(6, 4, 20000, dtype="bf16", bias=30, mask=True, hist=3000)
+    first = c.call(vas_lib)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        assert np.array_equal(c.call(vas_lib), first)
+    f = torch.float32
+    keep = dict(tokens=_dev(c.hist), token_lens=_dev(c.hist_lens), prompt_lens=_dev(c.prompt_lens),
+                draft_tokens=_dev(c.drafts), repetition_penalty=_dev(c.rep, f), frequency_penalty=_dev(c.freq, f),
+                presence_penalty=_dev(c.pres, f), bias_tokens=_dev(c.bias_tokens), bias=_dev(c.bias, f),
+                mask=_dev(c.mask), temperature=_dev(c.temps, f))
+    out = torch.zeros(6, 5, 20000, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        vas_lib.spec_logits(c.logits, out, **keep)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(out.cpu().double().numpy(), first)
+
+
+def test_binding_refusals(vas_lib):
+    v = vas_lib
+    x, out = torch.zeros(2, 3, 64, device="cuda"), torch.zeros(2, 3, 64, device="cuda")
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    f = lambda *s: torch.zeros(*s, device="cuda")  # noqa: E731
+    for kw in [dict(tokens=i(2, 4)), dict(tokens=i(3, 4), token_lens=i(2)), dict(bias=f(2, 3)),
+               dict(bias=f(2, 3), bias_tokens=i(2, 4)), dict(mask=i(2, 3, 3)), dict(mask=f(2, 3, 2)),
+               dict(temperature=f(3)), dict(draft_tokens=i(2, 3)), dict(parents=i(2, 1), draft_tokens=i(2, 2)),
+               dict(temperature=torch.zeros(2)), dict(repetition_penalty=f(2, 2)[:, 0])]:
+        with pytest.raises(ValueError):
+            v.spec_logits(x, out, **kw)
+    for a, b in [(x.half(), out), (x.cpu(), out), (x, out[:, :2]), (x, out.double()),
+                 (x.transpose(1, 2).contiguous().transpose(1, 2), out), (torch.zeros(2, 6, 64, device="cuda")[:, :3], out)]:
+        with pytest.raises(ValueError):
+            v.spec_logits(a, b)
+    for kw in [dict(temperature=f(2), probs=False), dict(repetition_penalty=f(2)), dict(parents=i(2, 2))]:
+        with pytest.raises(v.VasError):
+            v.spec_logits(x, out, **kw)
+    with pytest.raises(v.VasError):
+        v.spec_logits(x, x)  # read and written

@@ -45,6 +45,10 @@ VAS_F32 = 0
 VAS_BF16 = 1
 VAS_FP8_E4M3 = 2
 VAS_INT8 = 3
+VAS_FP8_BLOCK = 18
+VAS_INT8_BLOCK = 19
+VAS_LOGITS = 0
+VAS_PROBS = 1
 VAS_SHARE_AUTO = 0
 VAS_SHARE_ALWAYS = 1
 
@@ -73,9 +77,23 @@ class vas_pool_dims(ctypes.Structure):
                 ("num_kv_heads", _i32), ("head_dim", _i32), ("kv_dtype", _i32)]
 
 
+class vas_read_dims(ctypes.Structure):
+    _fields_ = [("num_seqs", _i32), ("total_tokens", _i32), ("num_kv_heads", _i32),
+                ("head_dim", _i32), ("page_size", _i32), ("num_pages", _i32),
+                ("max_pages_per_seq", _i32), ("kv_dtype", _i32), ("out_dtype", _i32),
+                ("k_stride", _i64), ("v_stride", _i64)]
+
+
+class vas_logits_dims(ctypes.Structure):
+    _fields_ = [("num_seqs", _i32), ("num_drafts", _i32), ("vocab", _i32), ("dtype", _i32),
+                ("out_kind", _i32), ("max_tokens", _i32), ("max_bias", _i32), ("row_stride", _i64)]
+
+
 _P_dims = ctypes.POINTER(vas_attn_dims)
 _P_append = ctypes.POINTER(vas_append_dims)
 _P_pool = ctypes.POINTER(vas_pool_dims)
+_P_read = ctypes.POINTER(vas_read_dims)
+_P_logits = ctypes.POINTER(vas_logits_dims)
 _sig = {
     "paged_attn_workspace_size": ([_P_dims], _sz),
     "paged_attn_workspace_min": ([_P_dims], _sz),
@@ -90,6 +108,8 @@ _sig = {
     "paged_kv_copy": ([_c_void_p] * 7 + [_i32, _P_pool, _c_void_p], ctypes.c_int),
     "paged_kv_keep_path": ([_c_void_p] * 7 + [_i32, _i32] + [_c_void_p] * 3 +
                            [_i32, _i32, _P_pool, _c_void_p], ctypes.c_int),
+    "paged_kv_read": ([_c_void_p] * 9 + [_P_read, _c_void_p], ctypes.c_int),
+    "spec_logits": ([_c_void_p] * 14 + [_P_logits, _c_void_p], ctypes.c_int),
     "spec_verify": ([_c_void_p, _c_void_p, _c_void_p, _u64, _c_void_p, _c_void_p, _i32, _i32, _i32,
                      _c_void_p], ctypes.c_int),
     "spec_verify_tree": ([_c_void_p] * 4 + [_u64] + [_c_void_p] * 3 + [_i32, _i32, _i32, _c_void_p],
@@ -152,7 +172,8 @@ def _dev(t: torch.Tensor, name: str, dtype=None) -> ctypes.c_void_p:
 _KV_CODES = {torch.bfloat16: VAS_BF16, torch.float32: VAS_F32}
 
 
-_QUANT_CODES = {"fp8": VAS_FP8_E4M3, "int8": VAS_INT8}
+_QUANT_CODES = {"fp8": VAS_FP8_E4M3, "int8": VAS_INT8, "fp8_block": VAS_FP8_BLOCK,
+                "int8_block": VAS_INT8_BLOCK}
 _SHARE_CODES = {"auto": VAS_SHARE_AUTO, "always": VAS_SHARE_ALWAYS}
 
 
@@ -160,7 +181,8 @@ def attn_dims(q: torch.Tensor, k_pages: torch.Tensor, block_table: torch.Tensor,
               seq_lens: torch.Tensor, scale: float = 0.0, quant: Optional[str] = None) -> vas_attn_dims:
     """vas_attn_dims from tensor shapes: q [T, Hq, D], k_pages [num_pages, P, Hkv, D],
     block_table [B, max_pages], seq_lens [B].  quant: None (k_pages share q's dtype), or
-    "fp8" / "int8" for a pool of 8-bit codes (uint8 tensors) with a bf16 q."""
+    "fp8" / "int8" for a pool of 8-bit codes (uint8 tensors) with a bf16 q, "fp8_block" /
+    "int8_block" where it has one scale per page and head."""
     T, Hq, D = q.shape
     num_pages, P, Hkv, D2 = k_pages.shape
     if D2 != D:
@@ -235,7 +257,12 @@ def paged_attn_fwd_quant(q, k_pages, v_pages, k_scale, v_scale, block_table, seq
                          dims: Optional[vas_attn_dims] = None, stream=None) -> None:
     """Attention over a quantised pool (include/vas.h: paged_attn_fwd_quant).  k_pages /
     v_pages uint8 codes [num_pages, P, Hkv, D] ("fp8" E4M3 or "int8"); k_scale / v_scale
-    fp32 [num_pages, Hkv, P]; q and out bf16; tree_mask as for paged_attn_fwd_tree or None."""
+    fp32 [num_pages, Hkv, P], or with "fp8_block" / "int8_block" [num_pages, Hkv]; q and out
+    bf16; tree_mask as for paged_attn_fwd_tree or None."""
+    if quant in _BLOCK_QUANT:
+        _block_attn(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, query_lens, out,
+                    lse, workspace, quant, tree_mask, scale, dims, stream)
+        return
     if dims is None:
         dims = attn_dims(q, k_pages, block_table, seq_lens, scale, quant=quant)
     tm = ctypes.c_void_p(0)
@@ -283,6 +310,40 @@ def _stream_address(dev: int, stream: Optional[torch.cuda.Stream]) -> int:
     if _raw_stream is not None:
         return _raw_stream(dev)
     return torch.cuda.current_stream(dev).cuda_stream
+
+
+_BLOCK_QUANT = ("fp8_block", "int8_block")
+
+
+def _scale_shape(quant: Optional[str], n: int, Hkv: int, P: int):
+    return (n, Hkv) if quant in _BLOCK_QUANT else (n, Hkv, P)
+
+
+def _block_attn(q, k_pages, v_pages, k_scale, v_scale, block_table, seq_lens, query_lens, out, lse,
+                workspace, quant, tree_mask, scale, dims, stream) -> None:
+    """paged_attn_fwd_quant over a block-scaled pool, every tensor checked against the pool and
+    the batch."""
+    if dims is None:
+        dims = attn_dims(q, k_pages, block_table, seq_lens, scale, quant=quant)
+    elif not _dims_fit(dims, q, k_pages, block_table, seq_lens, quant):
+        raise ValueError("dims are those of another batch, pool or table")
+    dev = torch.cuda.current_device()
+    i32, f32, u8, bf16 = torch.int32, torch.float32, torch.uint8, torch.bfloat16
+    n, P, Hkv, _ = pool = k_pages.shape
+    if tree_mask is not None and (tree_mask.numel() != q.shape[0] or tree_mask.element_size() != 8):
+        raise ValueError("tree_mask needs one 64-bit word per query token")
+    B = seq_lens.shape
+    st = _lib.paged_attn_fwd_quant(
+        _here(dev, q, "q", None, bf16), _here(dev, k_pages, "k_pages", None, u8),
+        _here(dev, v_pages, "v_pages", pool, u8), _here(dev, k_scale, "k_scale", (n, Hkv), f32),
+        _here(dev, v_scale, "v_scale", (n, Hkv), f32),
+        _here(dev, block_table, "block_table", (*B, block_table.shape[-1]), i32),
+        _here(dev, seq_lens, "seq_lens", None, i32), _here(dev, query_lens, "query_lens", B, i32),
+        _here(dev, tree_mask, "tree_mask"), _here(dev, out, "out", q.shape, bf16),
+        _here(dev, lse, "lse", q.shape[:2], f32), ctypes.byref(dims),
+        _here(dev, workspace, "workspace"), workspace.numel() * workspace.element_size(),
+        _stream_address(dev, stream))
+    _check("paged_attn_fwd_quant", st)
 
 
 def paged_attn_prefix_workspace_size(dims: vas_attn_dims, num_groups: int) -> int:
@@ -373,7 +434,8 @@ def paged_kv_append(q, k, v, block_table, seq_lens, query_lens, q_out, k_pages, 
     q [T, Hq, D], k and v [T, Hkv, D] (rows any 16-byte multiple apart, heads contiguous),
     cos_sin [max_position, rotary_dim] fp32 or None, positions [T] int32 or None; q and
     q_out may both be None.  k_pages / v_pages [num_pages, P, Hkv, D], with quant uint8
-    codes and k_scale / v_scale [num_pages, Hkv, P]."""
+    codes and k_scale / v_scale [num_pages, Hkv, P] ("fp8", "int8"), or [num_pages, Hkv]
+    ("fp8_block", "int8_block": the scales of pages are read and written)."""
     num_pages, P, Hkv, D = pool = k_pages.shape
     T, B, act = k.shape[0], seq_lens.shape[0], k.dtype
     if B == 0 and T > 0:  # the call would do nothing, and leave q_out as it was
@@ -397,6 +459,7 @@ def paged_kv_append(q, k, v, block_table, seq_lens, query_lens, q_out, k_pages, 
     if cos_sin is not None and cos_sin.dim() != 2:
         raise ValueError("cos_sin must be [max_position, rotary_dim]")
     table = (0, 0) if cos_sin is None else cos_sin.shape
+    scales = _scale_shape(quant, num_pages, Hkv, P)
     maxp = block_table.shape[-1]
     dims = vas_append_dims(B, T, Hq, Hkv, D, P, num_pages, maxp, code, table[1], int(interleaved),
                            table[0], qs, ks, vs, eps)
@@ -408,10 +471,44 @@ def paged_kv_append(q, k, v, block_table, seq_lens, query_lens, q_out, k_pages, 
         _here(dev, seq_lens, "seq_lens", None, i32), _here(dev, query_lens, "query_lens", (B,), i32),
         _here(dev, q_out, "q_out", (T, Hq, D), act), _here(dev, k_pages, "k_pages"),
         _here(dev, v_pages, "v_pages", pool, k_pages.dtype),
-        _here(dev, k_scale, "k_scale", (num_pages, Hkv, P), f32),
-        _here(dev, v_scale, "v_scale", (num_pages, Hkv, P), f32), ctypes.byref(dims),
-        _stream_address(dev, stream))
+        _here(dev, k_scale, "k_scale", scales, f32), _here(dev, v_scale, "v_scale", scales, f32),
+        ctypes.byref(dims), _stream_address(dev, stream))
     _check("paged_kv_append", st)
+
+
+def paged_kv_read(k_pages, v_pages, block_table, lens, k_out, v_out, *, starts=None, k_scale=None,
+                  v_scale=None, quant: Optional[str] = None, stream=None) -> None:
+    """Cached tokens as rows (include/vas.h: paged_kv_read).  Positions starts[i] .. starts[i] +
+    lens[i] - 1 of each sequence ([B] int32; starts None: from 0), packed in k_out and v_out
+    [T, Hkv, D], bf16 or fp32, rows any 16-byte multiple apart, heads contiguous.  k_pages /
+    v_pages [num_pages, P, Hkv, D], with quant uint8 codes and their scales as in
+    paged_kv_append."""
+    num_pages, P, Hkv, D = pool = k_pages.shape
+    T, B, act = k_out.shape[0], lens.shape[0], k_out.dtype
+    dev = torch.cuda.current_device()
+    i32, f32 = torch.int32, torch.float32
+    if act not in _KV_CODES:
+        raise ValueError("k_out must be bf16 or fp32")
+    if quant is not None:
+        if quant not in _QUANT_CODES or k_pages.dtype != torch.uint8:
+            raise ValueError("a quantised pool is uint8 codes")
+        code = _QUANT_CODES[quant]
+    elif k_pages.dtype in _KV_CODES:
+        code = _KV_CODES[k_pages.dtype]
+    else:
+        raise ValueError("k_pages must be bf16, fp32, or with quant uint8 codes")
+    kp, ks = _heads(dev, k_out, "k_out", (T, Hkv, D), act)
+    vp, vs = _heads(dev, v_out, "v_out", (T, Hkv, D), act)
+    scales = _scale_shape(quant, num_pages, Hkv, P)
+    maxp = block_table.shape[-1]
+    dims = vas_read_dims(B, T, Hkv, D, P, num_pages, maxp, code, _KV_CODES[act], ks, vs)
+    st = _lib.paged_kv_read(
+        _here(dev, k_pages, "k_pages"), _here(dev, v_pages, "v_pages", pool, k_pages.dtype),
+        _here(dev, k_scale, "k_scale", scales, f32), _here(dev, v_scale, "v_scale", scales, f32),
+        _here(dev, block_table, "block_table", (B, maxp), i32),
+        _here(dev, starts, "starts", (B,), i32), _here(dev, lens, "lens", None, i32), kp, vp,
+        ctypes.byref(dims), _stream_address(dev, stream))
+    _check("paged_kv_read", st)
 
 
 def _pool(dev: int, k_pages, v_pages, k_scale, v_scale):
@@ -423,13 +520,14 @@ def _pool(dev: int, k_pages, v_pages, k_scale, v_scale):
     if (k_scale is None) != (v_scale is None):
         raise ValueError("k_scale and v_scale come together")
     *lead, n, P, Hkv, D = shape
-    if k_pages.dtype == torch.uint8:
-        code = VAS_FP8_E4M3  # either kind of code: they are moved as bytes
+    block = k_scale is not None and k_scale.shape == (*lead, n, Hkv)
+    if k_pages.dtype == torch.uint8:  # either kind of code: they are moved as bytes
+        code = VAS_FP8_BLOCK if block else VAS_FP8_E4M3
     elif k_pages.dtype in _KV_CODES:
         code = _KV_CODES[k_pages.dtype]
     else:
         raise ValueError("k_pages must be bf16, fp32 or uint8 codes")
-    scales = (*lead, n, Hkv, P)
+    scales = (*lead, n, Hkv) if block else (*lead, n, Hkv, P)
     return (_here(dev, k_pages, "k_pages"), _here(dev, v_pages, "v_pages", shape, k_pages.dtype),
             _here(dev, k_scale, "k_scale", scales, torch.float32),
             _here(dev, v_scale, "v_scale", scales, torch.float32),
@@ -456,8 +554,8 @@ def _address(a) -> int:
 def paged_kv_copy(k_pages, v_pages, src, dst, *, tokens=None, k_scale=None, v_scale=None,
                   stream=None) -> None:
     """Copy pages src[i] -> dst[i] of K and V (include/vas.h: paged_kv_copy).  src, dst and
-    tokens are host sequences of integers; pools as in paged_kv_append, or with a leading
-    layer dimension."""
+    tokens are host sequences of integers; pools as in paged_kv_append (which of the quantised
+    forms, the shape of the scales tells), or with a leading layer dimension."""
     dev = torch.cuda.current_device()
     kp, vp, ks, vs, dims = _pool(dev, k_pages, v_pages, k_scale, v_scale)
     s, d = _host_list(src, "src"), _host_list(dst, "dst")
@@ -504,6 +602,54 @@ def spec_verify_tree(p, q, draft_tokens, parents, seed: int, accepted_len, out_t
                                _dev(out_tokens, "out_tokens", torch.int32),
                                _dev(path, "path", torch.int32), B, n1 - 1, V, _stream_ptr(stream))
     _check("spec_verify_tree", st)
+
+
+def spec_logits(logits, out, *, tokens=None, token_lens=None, prompt_lens=None, draft_tokens=None,
+                parents=None, repetition_penalty=None, frequency_penalty=None,
+                presence_penalty=None, bias_tokens=None, bias=None, mask=None, temperature=None,
+                probs: bool = True, stream=None) -> None:
+    """Logits of a verification window to probabilities (include/vas.h: spec_logits).  logits
+    [B, n+1, V] bf16 or fp32 (rows any distance apart) -> out [B, n+1, V] fp32, spec_verify's p,
+    or with probs False the processed logits.  tokens [B, max_tokens] int32 (prompt first) with
+    token_lens and prompt_lens [B]; draft_tokens and parents [B, n] int32; the penalties and
+    temperature [B] fp32; bias_tokens int32 and bias fp32 [B, m]; mask [B, n+1, ceil(V / 32)]
+    int32, a bit per allowed token."""
+    B, rows, V = logits.shape
+    dev = torch.cuda.current_device()
+    i32, f32 = torch.int32, torch.float32
+    if logits.get_device() != dev:
+        raise ValueError(f"logits must be a CUDA tensor on the current device, cuda:{dev}")
+    if logits.dtype not in _KV_CODES:
+        raise ValueError("logits must be bf16 or fp32")
+    n, stride = rows - 1, logits.stride()
+    # Rows of all sequences are one list of rows, an equal distance apart.
+    row = stride[1] if rows > 1 else (stride[0] if B > 1 else V)
+    if V > 1 and stride[2] != 1:
+        raise ValueError("the logits of a row must be contiguous")
+    if B > 1 and rows > 1 and stride[0] != rows * row:
+        raise ValueError("rows of logits must be evenly spaced")
+    H = 0 if tokens is None else tokens.shape[-1]
+    m = 0 if bias_tokens is None else bias_tokens.shape[-1]
+    if (bias_tokens is None) != (bias is None):
+        raise ValueError("bias_tokens and bias come together")
+    if (tokens is None) != (token_lens is None):
+        raise ValueError("tokens and token_lens come together")
+    dims = vas_logits_dims(B, n, V, _KV_CODES[logits.dtype], VAS_PROBS if probs else VAS_LOGITS, H, m,
+                           row)
+    st = _lib.spec_logits(
+        logits.data_ptr(), _here(dev, tokens, "tokens", (B, H), i32),
+        _here(dev, token_lens, "token_lens", (B,), i32),
+        _here(dev, prompt_lens, "prompt_lens", (B,), i32),
+        _here(dev, draft_tokens, "draft_tokens", (B, n), i32),
+        _here(dev, parents, "parents", (B, n), i32),
+        _here(dev, repetition_penalty, "repetition_penalty", (B,), f32),
+        _here(dev, frequency_penalty, "frequency_penalty", (B,), f32),
+        _here(dev, presence_penalty, "presence_penalty", (B,), f32),
+        _here(dev, bias_tokens, "bias_tokens", (B, m), i32), _here(dev, bias, "bias", (B, m), f32),
+        _here(dev, mask, "mask", (B, rows, (V + 31) // 32), i32),
+        _here(dev, temperature, "temperature", (B,), f32), _here(dev, out, "out", (B, rows, V), f32),
+        ctypes.byref(dims), _stream_address(dev, stream))
+    _check("spec_logits", st)
 
 
 def spec_verify(p, q, draft_tokens, seed: int, accepted_len, out_tokens, *, stream=None) -> None:

@@ -1,0 +1,373 @@
+// Rows of the append kernels (cache_ops.cu, block_cache.cu): the call's arguments, a lane's
+// share of a head row, norm and rotation of a row, codes, and where a packed token goes.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "../../include/vas.h"
+#include "device_util.cuh"
+#include "packed_math.cuh"
+
+namespace vas {
+namespace cache {
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kAppendBlocks = 2;  // of an SM
+
+struct AppendArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* q_weight;
+  const void* k_weight;
+  const float* cos_sin;
+  const int32_t* positions;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* query_lens;
+  void* q_out;
+  void* k_pages;
+  void* v_pages;
+  float* k_scale;
+  float* v_scale;
+  int64_t q_stride, k_stride, v_stride;
+  int32_t B, T, Hq, Hkv, P, num_pages, maxp, rot, max_position;
+  int32_t log2P;
+  int32_t parts, iters;  // a token is `parts` tasks of `iters` groups of rows
+  float eps;
+  int32_t* err;
+  // Sequence i of the packing: its tokens, and its length with them.
+  __device__ __forceinline__ int32_t count(int64_t i) const { return query_lens[i]; }
+  __device__ __forceinline__ int64_t length(int64_t i) const { return seq_lens[i]; }
+};
+
+// Eight fp32 values as four pairs, the operands of the packed instructions.
+struct F8 {
+  uint64_t p[4];
+};
+
+__device__ __forceinline__ F8 load_f8(const float* p) {
+  const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(p);
+  const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(p + 4);
+  return {{u.x, u.y, w.x, w.y}};
+}
+
+// 16 (bf16) or 32 (fp32) raw bytes of each of a lane's two chunks: what waits in registers
+// between the load and its use.
+template <typename T>
+struct Raw {
+  uint4 a[sizeof(T) / 2], b[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p, int ca, int cb) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+      a[i] = __ldcs(reinterpret_cast<const uint4*>(p + ca) + i);
+      b[i] = __ldcs(reinterpret_cast<const uint4*>(p + cb) + i);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) a[i] = b[i] = make_uint4(0, 0, 0, 0);
+  }
+};
+__device__ __forceinline__ F8 widen(const uint4 (&u)[1]) {
+  return {{pair(bf16_lo_f32(u[0].x), bf16_hi_f32(u[0].x)), pair(bf16_lo_f32(u[0].y), bf16_hi_f32(u[0].y)),
+           pair(bf16_lo_f32(u[0].z), bf16_hi_f32(u[0].z)), pair(bf16_lo_f32(u[0].w), bf16_hi_f32(u[0].w))}};
+}
+__device__ __forceinline__ F8 widen(const uint4 (&u)[2]) {
+  auto f = [](uint32_t x, uint32_t y) { return pair(__uint_as_float(x), __uint_as_float(y)); };
+  return {{f(u[0].x, u[0].y), f(u[0].z, u[0].w), f(u[1].x, u[1].y), f(u[1].z, u[1].w)}};
+}
+__device__ __forceinline__ F8 load_weights(const __nv_bfloat16* p) {
+  const uint4 u[1] = {*reinterpret_cast<const uint4*>(p)};
+  return widen(u);
+}
+__device__ __forceinline__ F8 load_weights(const float* p) { return load_f8(p); }
+
+__device__ __forceinline__ uint32_t bf16_pair(uint64_t v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const F8& x) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(bf16_pair(x.p[0]), bf16_pair(x.p[1]), bf16_pair(x.p[2]), bf16_pair(x.p[3]));
+}
+__device__ __forceinline__ void store8(float* p, const F8& x) {
+  *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x.p[0], x.p[1]);
+  *reinterpret_cast<ulonglong2*>(p + 4) = make_ulonglong2(x.p[2], x.p[3]);
+}
+
+// x / scale, rounded to nearest.  With the correctly rounded reciprocal r = 1 / scale, one
+// correction of x r by its exact remainder gives the correctly rounded quotient (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", IBM J. Res.
+// Dev. 34, 1990), three packed instructions for two elements; scales near the ends of the
+// range, where r or the remainder could leave it, and the not finite ones divide.
+__device__ __forceinline__ F8 quotients(const F8& x, float scale) {
+  F8 y;
+  if (scale > 0x1p-80f && scale < 0x1p80f) {
+    const float r = __frcp_rn(scale);
+    const uint64_t r2 = pair(r, r), ns2 = pair(-scale, -scale);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t q = mul2(x.p[i], r2);
+      y.p[i] = fma2(fma2(q, ns2, x.p[i]), r2, q);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      unpair(x.p[i], lo, hi);
+      y.p[i] = pair(__fdiv_rn(lo, scale), __fdiv_rn(hi, scale));
+    }
+  }
+  return y;
+}
+
+// 8 values as codes: E4M3 (round to nearest even, saturating; NaN stays NaN) or INT8.
+template <int KV>
+__device__ __forceinline__ uint2 codes8(const F8& x, float scale) {
+  const F8 q = quotients(x, scale);
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float y[4];
+    unpair(q.p[2 * h], y[0], y[1]);
+    unpair(q.p[2 * h + 1], y[2], y[3]);
+    if constexpr (KV == VAS_FP8_E4M3) {
+      asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
+          : "=r"(w[h])
+          : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
+    } else {
+      w[h] = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // |y| <= 127 (1 + 2^-23), or NaN, which converts to 0 under a scale that is not
+        // finite.
+        const int c = max(-127, min(127, __float2int_rn(y[i])));
+        w[h] |= (uint32_t)(c & 0xff) << (8 * i);
+      }
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Where a token goes, or why it does not.
+struct Place {
+  int32_t page, slot, position;
+  int32_t err;  // device error bits; the token is not stored and its q_out row is NaN
+};
+
+// The packing of a call, in shared memory: the first row of every `step`th sequence, and
+// with step 1 (up to kAppendSeqs sequences) their lengths too (clamped: none above
+// INT_MAX is valid).
+constexpr int kAppendSeqs = 1024;
+struct Packing {
+  int32_t row0[kAppendSeqs + 1];  // clamped to INT_MAX; the last one is the total
+  int32_t len[kAppendSeqs];
+  int64_t wsum[kAppendWarps];
+};
+
+template <typename Args>
+__device__ __forceinline__ bool lengths_ok(const Args& a, int64_t L, int32_t ql) {
+  return ql >= 0 && ql <= a.T && L >= ql && L <= (int64_t)a.maxp * a.P && L <= INT_MAX;
+}
+
+__device__ __forceinline__ int32_t clamp_i32(int64_t x) {
+  return (int32_t)(x > INT_MAX ? INT_MAX : (x < INT_MIN ? INT_MIN : x));
+}
+
+// The whole block (kAppendThreads threads).  Args: the packing's B, T, maxp, P, count(i)
+// and length(i).
+template <typename Args>
+__device__ __forceinline__ void scan_lengths(const Args& a, Packing& pk, int32_t step) {
+  constexpr int kPer = kAppendSeqs / kAppendThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t mine[kPer], sum = 0;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int c = tid * kPer + e;
+    mine[e] = 0;
+    if (step == 1) {
+      if (c < a.B) {
+        mine[e] = max(a.count(c), 0);
+        pk.len[c] = clamp_i32(a.length(c));
+      }
+    } else {
+      for (int64_t i = (int64_t)c * step; i < a.B && i < ((int64_t)c + 1) * step; ++i)
+        mine[e] += max(a.count(i), 0);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int64_t n = mine[e];
+    mine[e] = sum;
+    sum += n;
+  }
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t n = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += n;
+  }
+  if (lane == 31) pk.wsum[warp] = inc;
+  __syncthreads();
+  int64_t base = inc - sum;
+#pragma unroll
+  for (int w = 0; w < kAppendWarps; ++w)
+    if (w < warp) base += pk.wsum[w];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) pk.row0[tid * kPer + e] = clamp_i32(base + mine[e]);
+  if (tid == kAppendThreads - 1) pk.row0[kAppendSeqs] = clamp_i32(base + sum);
+  __syncthreads();
+}
+
+// The sequence that owns packed row t.
+struct Owner {
+  int32_t seq, len, count;  // the sequence, its length and its tokens
+  int64_t row;              // its first packed row
+  bool ok;                  // false: no sequence, or one with inconsistent lengths
+};
+
+// The whole warp: the owner of packed row t.  The last start at or below t is found in two
+// rounds of 32 (sequences without tokens share their successor's start, so the last of
+// equal starts is the one that has tokens).
+template <typename Args>
+__device__ __forceinline__ Owner owner_of(const Args& a, const Packing& pk, int32_t step, int32_t t,
+                                          int lane) {
+  Owner o{0, 0, 0, 0, false};
+  if (t >= pk.row0[kAppendSeqs]) return o;
+  constexpr int kBlock = kAppendSeqs / 32;
+  const int hi = __popc(__ballot_sync(0xffffffffu, pk.row0[lane * kBlock] <= t)) - 1;
+  static_assert(kBlock == 32, "one start a lane in the second round");
+  const int lo = __popc(__ballot_sync(0xffffffffu, pk.row0[hi * kBlock + lane] <= t)) - 1;
+  const int c = hi * kBlock + lo;
+  int64_t L;
+  o.row = pk.row0[c];
+  o.seq = c;
+  if (step == 1) {
+    // A negative length counts as none, so a sequence found here has its true one.
+    o.count = pk.row0[c + 1] - pk.row0[c];
+    L = pk.len[c];
+  } else {
+    for (o.seq = c * step; o.seq < a.B; ++o.seq) {
+      o.count = a.count(o.seq);
+      const int64_t n = o.count > 0 ? o.count : 0;
+      if (t < o.row + n) break;
+      o.row += n;
+    }
+    if (o.seq >= a.B) return o;
+    L = a.length(o.seq);
+  }
+  o.ok = lengths_ok(a, L, o.count) && o.row + o.count <= a.T;
+  o.len = clamp_i32(L);
+  return o;
+}
+
+// The whole warp: the place of packed row t of an append.
+__device__ __forceinline__ Place place_of(const AppendArgs& a, const Packing& pk, int32_t step,
+                                          int32_t t, int lane) {
+  Place p{0, 0, 0, 0};
+  const Owner o = owner_of(a, pk, step, t, lane);
+  if (!o.ok) {
+    p.err = VAS_DEV_BAD_LENGTHS;
+    return p;
+  }
+  const int32_t pos = o.len - o.count + (int32_t)(t - o.row);
+  p.position = a.positions ? a.positions[t] : pos;
+  if (a.rot && (p.position < 0 || p.position >= a.max_position)) p.err |= VAS_DEV_BAD_POSITION;
+  p.page = a.block_table[(size_t)o.seq * a.maxp + (pos >> a.log2P)];
+  p.slot = pos & (a.P - 1);
+  if (p.page < 0 || p.page >= a.num_pages) p.err |= VAS_DEV_BAD_PAGE;
+  return p;
+}
+
+// A lane's two chunks of a head row.  Split halves: rotated pairs (8c + e, 8c + e + rot / 2)
+// first, then the rest of the head.  Neighbours (INTER): 16 consecutive elements.
+struct Chunks {
+  int a, b;     // first elements
+  bool turned;  // whether they are rotated
+};
+template <int D, bool INTER>
+__device__ __forceinline__ Chunks lane_chunks(int c, int rot) {
+  const int nrot = rot / 16;
+  Chunks k;
+  k.turned = c < nrot;
+  if (INTER) {
+    k.a = 16 * c;
+    k.b = k.a + 8;
+  } else if (k.turned) {
+    k.a = 8 * c;
+    k.b = k.a + rot / 2;
+  } else {
+    k.a = rot + 8 * (c - nrot);
+    k.b = k.a + (D - rot) / 2;
+  }
+  return k;
+}
+
+// Sum of squares of a row over its kLanes lanes; every lane of the warp takes part.
+template <int kLanes>
+__device__ __forceinline__ float row_squares(const F8& xa, const F8& xb) {
+  uint64_t s2 = mul2(xa.p[0], xa.p[0]);
+#pragma unroll
+  for (int e = 1; e < 4; ++e) s2 = fma2(xa.p[e], xa.p[e], s2);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) s2 = fma2(xb.p[e], xb.p[e], s2);
+  float ss, hi;
+  unpair(s2, ss, hi);
+  ss += hi;
+#pragma unroll
+  for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  return ss;
+}
+
+// The norm of a row with sum of squares ss, by the weights wa, wb.
+template <int D>
+__device__ __forceinline__ void norm_row(F8& xa, F8& xb, const F8& wa, const F8& wb, float ss,
+                                         float eps) {
+  const float inv = rsqrtf(ss * (1.f / D) + eps);
+  const uint64_t inv2 = pair(inv, inv);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    xa.p[e] = mul2(mul2(xa.p[e], inv2), wa.p[e]);
+    xb.p[e] = mul2(mul2(xb.p[e], inv2), wb.p[e]);
+  }
+}
+
+// The rotation of a lane's 8 pairs by the angles with cosines cs and sines sn.
+template <bool INTER>
+__device__ __forceinline__ void turn_row(F8& xa, F8& xb, const F8& cs, const F8& sn) {
+  if (INTER) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float c0, c1, s0, s1, u0, u1;
+      unpair(cs.p[e], c0, c1);
+      unpair(sn.p[e], s0, s1);
+      // Pairs 2e and 2e + 1: chunk a holds pairs 0..3, chunk b 4..7.
+      uint64_t& y0 = e < 2 ? xa.p[2 * (e & 1)] : xb.p[2 * (e & 1)];
+      uint64_t& y1 = e < 2 ? xa.p[2 * (e & 1) + 1] : xb.p[2 * (e & 1) + 1];
+      unpair(y0, u0, u1);
+      y0 = pair(u0 * c0 - u1 * s0, u1 * c0 + u0 * s0);
+      unpair(y1, u0, u1);
+      y1 = pair(u0 * c1 - u1 * s1, u1 * c1 + u0 * s1);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t u = xa.p[e], v = xb.p[e];
+      xa.p[e] = sub2(mul2(u, cs.p[e]), mul2(v, sn.p[e]));
+      xb.p[e] = fma2(v, cs.p[e], mul2(u, sn.p[e]));
+    }
+  }
+}
+
+// Keys and values of an append to block-scaled pages (block_cache.cu).
+int launch_append_block(const AppendArgs& a, int head_dim, bool fp8, bool inter, vas_stream_t stream);
+
+}  // namespace cache
+}  // namespace vas

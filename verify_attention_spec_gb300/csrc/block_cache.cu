@@ -1,0 +1,587 @@
+// Block-scaled caches (sm_103a): 8-bit pages with one fp32 scale per page and KV head.  The
+// append that quantises them as it writes (its part of paged_kv_append), and the read-back of
+// cached tokens of any storage type (paged_kv_read).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/vas.h"
+#include "append_rows.cuh"
+#include "device_util.cuh"
+#include "packed_math.cuh"
+#include "vas_internal.h"
+
+namespace vas {
+namespace cache {
+
+// ------------------------------------------------------------------------------------
+// Append to block-scaled pages: keys and values
+// ------------------------------------------------------------------------------------
+// A run is what one call adds to one page: consecutive slots of a sequence, from slot 0 of a
+// fresh page or behind the tokens a page already holds.  A task is one run of one head and
+// operand, and one warp's: it finds the largest magnitude of the run's rows (norm and rotation
+// applied), settles the scale, requantises the tokens the page held if the scale grew, and
+// writes the codes.  The rows are computed twice, once for the magnitude and once for the
+// codes: a page's values would take 128 registers a lane, and the second read comes from L1.
+struct Runs {
+  int32_t row0[kAppendSeqs + 1];  // first packed row of every `step`th sequence
+  int32_t run0[kAppendSeqs + 1];  // and its first run; the last ones are the totals
+  int64_t wsum[kAppendWarps][2];
+};
+
+__device__ __forceinline__ int32_t runs_of(const AppendArgs& a, int32_t L, int32_t ql) {
+  if (ql <= 0 || !lengths_ok(a, L, ql)) return 0;
+  return ((L - 1) >> a.log2P) - ((L - ql) >> a.log2P) + 1;
+}
+
+// The whole block.
+__device__ __forceinline__ void scan_runs(const AppendArgs& a, Runs& rs, int32_t step) {
+  constexpr int kPer = kAppendSeqs / kAppendThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int64_t rows[kPer], runs[kPer], row_sum = 0, run_sum = 0;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int64_t c = tid * kPer + e;
+    rows[e] = row_sum;
+    runs[e] = run_sum;
+    for (int64_t i = c * step; i < a.B && i < (c + 1) * step; ++i) {
+      const int32_t ql = a.query_lens[i];
+      row_sum += max(ql, 0);
+      run_sum += runs_of(a, a.seq_lens[i], ql);
+    }
+  }
+  int64_t row_inc = row_sum, run_inc = run_sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, row_inc, o);
+    const int64_t y = __shfl_up_sync(0xffffffffu, run_inc, o);
+    if (lane >= o) {
+      row_inc += x;
+      run_inc += y;
+    }
+  }
+  if (lane == 31) {
+    rs.wsum[warp][0] = row_inc;
+    rs.wsum[warp][1] = run_inc;
+  }
+  __syncthreads();
+  int64_t row_base = row_inc - row_sum, run_base = run_inc - run_sum;
+#pragma unroll
+  for (int w = 0; w < kAppendWarps; ++w)
+    if (w < warp) {
+      row_base += rs.wsum[w][0];
+      run_base += rs.wsum[w][1];
+    }
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    rs.row0[tid * kPer + e] = clamp_i32(row_base + rows[e]);
+    rs.run0[tid * kPer + e] = clamp_i32(run_base + runs[e]);
+  }
+  if (tid == kAppendThreads - 1) {
+    rs.row0[kAppendSeqs] = clamp_i32(row_base + row_sum);
+    rs.run0[kAppendSeqs] = clamp_i32(run_base + run_sum);
+  }
+  __syncthreads();
+}
+
+// Where a run's tokens come from and go.
+struct Run {
+  int32_t page, slot0, n;  // n = 0: nothing to store
+  int32_t t0;              // first packed row
+  int32_t pos0;            // and its cache position
+  int32_t err;
+};
+
+// The whole warp: run u.  The last start at or below u, as in owner_of.
+__device__ __forceinline__ Run run_at(const AppendArgs& a, const Runs& rs, int32_t step, int32_t u,
+                                      int lane) {
+  Run r{0, 0, 0, 0, 0, 0};
+  constexpr int kBlock = kAppendSeqs / 32;
+  static_assert(kBlock == 32, "one start a lane in the second round");
+  const int hi = __popc(__ballot_sync(0xffffffffu, rs.run0[lane * kBlock] <= u)) - 1;
+  const int lo = __popc(__ballot_sync(0xffffffffu, rs.run0[hi * kBlock + lane] <= u)) - 1;
+  const int c = hi * kBlock + lo;
+  int64_t row = rs.row0[c];
+  int32_t first = rs.run0[c], L = 0, ql = 0, n = 0;
+  int64_t i = (int64_t)c * step;
+  for (; i < a.B; ++i) {
+    L = a.seq_lens[i];
+    ql = a.query_lens[i];
+    n = runs_of(a, L, ql);
+    if (u < first + n) break;
+    first += n;
+    row += max(ql, 0);
+  }
+  if (i >= a.B || row + ql > a.T) return r;  // rows past T: the lengths are inconsistent
+  const int32_t p = ((L - ql) >> a.log2P) + (u - first);
+  const int32_t lo_pos = max(L - ql, p << a.log2P), hi_pos = min(L, (p + 1) << a.log2P);
+  r.page = a.block_table[(size_t)i * a.maxp + p];
+  r.slot0 = lo_pos & (a.P - 1);
+  r.n = hi_pos - lo_pos;
+  r.t0 = (int32_t)row + lo_pos - (L - ql);
+  r.pos0 = lo_pos;
+  if (r.page < 0 || r.page >= a.num_pages) {
+    r.err = VAS_DEV_BAD_PAGE;
+    r.n = 0;
+  }
+  return r;
+}
+
+// The scale of a fresh page with largest magnitude m (finite).  E4M3: the smallest power of
+// two with m <= 448 scale: a floating code loses nothing by it, and requantising for a larger
+// scale is then exact in the normal range.  INT8: m / 127.
+template <int KV>
+__device__ __forceinline__ float fresh_scale(float m) {
+  if constexpr (KV == VAS_FP8_E4M3) {
+    if (m == 0.f) return 0x1p-126f;
+    int e;
+    const float f = frexpf(m, &e);  // 448 = 0.875 * 2^9
+    const int k = f <= 0.875f ? e - 9 : e - 8;
+    return ldexpf(1.f, max(k, -126));
+  } else {
+    return fmaxf(__fdiv_rn(m, 127.f), 0x1p-126f);
+  }
+}
+
+// How often the scale s (positive, finite) of a page that holds tokens doubles for a largest
+// magnitude m of the new ones: until m / s is at most the largest code, 448, or for INT8 at
+// most 127.5, which rounds to 127 by half a step.
+template <int KV>
+__device__ __forceinline__ int scale_growth(float s, float m) {
+  if (m == 0.f) return 0;
+  int e, h;
+  const float f = frexpf(m, &e);
+  float b = frexpf(s, &h) * (KV == VAS_FP8_E4M3 ? 0.875f : 0.99609375f);
+  h += KV == VAS_FP8_E4M3 ? 9 : 7;
+  if (b < 0.5f) {
+    b *= 2.f;
+    h -= 1;
+  }
+  return max(0, e - h + (f > b ? 1 : 0));
+}
+
+// Sixteen codes times 2^-j, rounded to nearest even (j > 0).
+template <int KV>
+__device__ __forceinline__ uint4 shrink_codes(uint4 x, int j) {
+  const float mul = ldexpf(1.f, -min(j, 64));  // 2^-64 of any code rounds to zero
+  uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (KV == VAS_FP8_E4M3) {
+      uint32_t lo, hi;
+      float y[4];
+      e4m3x4_to_f16x4(w[i], lo, hi);
+      f16x2_to_f32(lo, y[0], y[1]);
+      f16x2_to_f32(hi, y[2], y[3]);
+      asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
+          : "=r"(w[i])
+          : "f"(y[0] * mul), "f"(y[1] * mul), "f"(y[2] * mul), "f"(y[3] * mul));
+    } else {
+      uint32_t out = 0;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int c = (int8_t)(w[i] >> (8 * b));
+        out |= (uint32_t)(__float2int_rn((float)c * mul) & 0xff) << (8 * b);
+      }
+      w[i] = out;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The largest finite magnitude of a lane's 16 values, as bits; *wild if one is not finite.
+__device__ __forceinline__ uint32_t finite_max(const F8& xa, const F8& xb, bool* wild) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float y[4];
+    unpair(xa.p[e], y[0], y[1]);
+    unpair(xb.p[e], y[2], y[3]);
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const uint32_t u = __float_as_uint(y[f]) & 0x7fffffffu;
+      if (u < 0x7f800000u) m = max(m, u);
+      else *wild = true;
+    }
+  }
+  return m;
+}
+
+// Infinities and NaN as what their codes stand for: NaN (E4M3), 0 (INT8).
+template <int KV>
+__device__ __forceinline__ void tame(F8& x) {
+  const float stand_in = KV == VAS_FP8_E4M3 ? NAN : 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float y[2];
+    unpair(x.p[e], y[0], y[1]);
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+      if ((__float_as_uint(y[f]) & 0x7fffffffu) >= 0x7f800000u) y[f] = stand_in;
+    x.p[e] = pair(y[0], y[1]);
+  }
+}
+
+template <int KV, int D, bool INTER>
+__global__ void __launch_bounds__(kAppendThreads) append_block_kernel(const AppendArgs a) {
+  using T = __nv_bfloat16;
+  constexpr int kLanes = D / 16;     // lanes of a row
+  constexpr int kSub = 32 / kLanes;  // rows of a warp at a time
+  __shared__ Runs rs;
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t step = (a.B + kAppendSeqs - 1) / kAppendSeqs;
+  scan_runs(a, rs, step);
+  if (blockIdx.x == 0) {  // the call's lengths as a whole
+    bool bad = threadIdx.x == 0 && rs.row0[kAppendSeqs] != a.T;
+    for (int64_t i = threadIdx.x; i < a.B; i += kAppendThreads)
+      bad |= !lengths_ok(a, a.seq_lens[i], a.query_lens[i]);
+    if (bad) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
+  }
+  const int c = lane % kLanes, sub = lane / kLanes;
+  const Chunks ch = lane_chunks<D, INTER>(c, a.rot);
+  const int64_t n_tasks = (int64_t)rs.run0[kAppendSeqs] * 2 * a.Hkv;
+  const int64_t stride = (int64_t)gridDim.x * kAppendWarps;
+  for (int64_t task = (int64_t)blockIdx.x * kAppendWarps + warp; task < n_tasks; task += stride) {
+    const int32_t u = (int32_t)(task / (2 * a.Hkv));
+    int32_t h = (int32_t)(task - (int64_t)u * 2 * a.Hkv);
+    const bool is_v = h >= a.Hkv;
+    if (is_v) h -= a.Hkv;
+    const Run r = run_at(a, rs, step, u, lane);
+    if (r.err && lane == 0) atomicOr(a.err, r.err);
+    if (r.n == 0) continue;
+    const T* src = is_v ? static_cast<const T*>(a.v) : static_cast<const T*>(a.k);
+    const int64_t src_stride = is_v ? a.v_stride : a.k_stride;
+    const T* w = is_v ? nullptr : static_cast<const T*>(a.k_weight);
+    F8 wa{}, wb{};
+    if (w != nullptr) {
+      wa = load_weights(w + ch.a);
+      wb = load_weights(w + ch.b);
+    }
+    // Row `row` of the run; false: it is not stored (none, or a position outside the table).
+    auto compute = [&](int row, F8& xa, F8& xb) {
+      Raw<T> x;
+      x.zero();
+      bool live = row < r.n;
+      int32_t at = 0;
+      if (live && a.rot) {  // a token without a place in the table stores no value either
+        at = a.positions ? a.positions[r.t0 + row] : r.pos0 + row;
+        if (at < 0 || at >= a.max_position) {
+          live = false;
+          if (c == 0) atomicOr(a.err, VAS_DEV_BAD_POSITION);
+        }
+      }
+      if (live) x.load(src + (int64_t)(r.t0 + row) * src_stride + (int64_t)h * D, ch.a, ch.b);
+      xa = widen(x.a);
+      xb = widen(x.b);
+      if (!is_v) {
+        const float ss = row_squares<kLanes>(xa, xb);
+        if (w != nullptr) norm_row<D>(xa, xb, wa, wb, ss, a.eps);
+        if (ch.turned && live) {
+          const float* angles = a.cos_sin + (size_t)at * a.rot + 8 * c;
+          turn_row<INTER>(xa, xb, load_f8(angles), load_f8(angles + a.rot / 2));
+        }
+      }
+      return live;
+    };
+    const size_t si = (size_t)r.page * a.Hkv + h;
+    float* scales = is_v ? a.v_scale : a.k_scale;
+    const float old = r.slot0 ? scales[si] : 0.f;
+    uint8_t* codes = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) +
+                     ((size_t)r.page * a.P * a.Hkv + h) * D;
+    const size_t row_bytes = (size_t)a.Hkv * D;
+
+    uint32_t m = 0;
+    bool wild = false;
+    F8 xa, xb;
+    bool live = false;
+    for (int r0 = 0; r0 < r.n; r0 += kSub) {
+      live = compute(r0 + sub, xa, xb);
+      if (live) m = max(m, finite_max(xa, xb, &wild));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    wild = __any_sync(0xffffffffu, wild);
+    const float top = __uint_as_float(m);
+    float scale;
+    if (r.slot0 && old > 0.f && old < INFINITY) {
+      const int grow = scale_growth<KV>(old, top);
+      scale = ldexpf(old, grow);
+      if (grow) {  // the tokens the page held, in the new scale
+        for (int s0 = 0; s0 < r.slot0; s0 += kSub)
+          if (s0 + sub < r.slot0) {
+            uint4* p = reinterpret_cast<uint4*>(codes + (s0 + sub) * row_bytes) + c;
+            *p = shrink_codes<KV>(*p, grow);
+          }
+      }
+    } else {
+      scale = fresh_scale<KV>(top);
+    }
+    for (int r0 = 0; r0 < r.n; r0 += kSub) {
+      if (r.n > kSub) live = compute(r0 + sub, xa, xb);
+      if (!live) continue;
+      if (wild) {
+        tame<KV>(xa);
+        tame<KV>(xb);
+      }
+      uint8_t* p = codes + (r.slot0 + r0 + sub) * row_bytes;
+      *reinterpret_cast<uint2*>(p + ch.a) = codes8<KV>(xa, scale);
+      *reinterpret_cast<uint2*>(p + ch.b) = codes8<KV>(xb, scale);
+    }
+    if (lane == 0 && scale != old) scales[si] = scale;
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// Read-back
+// ------------------------------------------------------------------------------------
+struct ReadArgs {
+  const void* k_pages;
+  const void* v_pages;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_table;
+  const int32_t* starts;
+  const int32_t* lens;
+  void* k_out;
+  void* v_out;
+  int64_t k_stride, v_stride;
+  int32_t B, T, Hkv, P, num_pages, maxp, log2P, log2D;
+  int32_t* err;
+  __device__ __forceinline__ int32_t count(int64_t i) const { return lens[i]; }
+  __device__ __forceinline__ int64_t length(int64_t i) const {
+    const int64_t at = starts ? starts[i] : 0;
+    return at < 0 ? -1 : at + lens[i];  // a negative start is inconsistent
+  }
+};
+
+// N consecutive elements of one head row as fp32.
+template <int KV, int N>
+__device__ __forceinline__ void read_elements(const void* pages, size_t at, float scale, float (&y)[N]) {
+  if constexpr (KV == VAS_F32) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(pages) + at + i));
+      y[i] = v.x, y[i + 1] = v.y, y[i + 2] = v.z, y[i + 3] = v.w;
+    }
+  } else if constexpr (KV == VAS_BF16) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(pages) + at + i));
+      y[i] = bf16_lo_f32(v.x), y[i + 1] = bf16_hi_f32(v.x);
+      y[i + 2] = bf16_lo_f32(v.y), y[i + 3] = bf16_hi_f32(v.y);
+    }
+  } else {
+    uint32_t w[N / 4];
+    const uint8_t* p = static_cast<const uint8_t*>(pages) + at;
+    if constexpr (N == 8) {
+      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
+      w[0] = v.x, w[1] = v.y;
+    } else {
+      w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      uint32_t lo, hi;
+      if constexpr (KV == VAS_FP8_E4M3) e4m3x4_to_f16x4(w[i], lo, hi);
+      else s8x4_to_f16x4(w[i], lo, hi);
+      f16x2_to_f32(lo, y[4 * i], y[4 * i + 1]);
+      f16x2_to_f32(hi, y[4 * i + 2], y[4 * i + 3]);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] *= scale;
+  }
+}
+
+__device__ __forceinline__ void write_elements(__nv_bfloat16* p, const float (&y)[8]) {
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                                 pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])));
+}
+__device__ __forceinline__ void write_elements(float* p, const float (&y)[4]) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(y[0], y[1], y[2], y[3]));
+}
+
+// KV: element type of the pool; BLOCK: one scale per page and head.  A warp takes one token
+// at a time; a lane 16 bytes of output at a time, of K and then of V.
+template <int KV, bool BLOCK, typename OUT>
+__global__ void __launch_bounds__(kAppendThreads) read_kernel(const ReadArgs a) {
+  constexpr int N = 16 / sizeof(OUT);  // elements of a lane's store
+  constexpr bool kQuant = KV == VAS_FP8_E4M3 || KV == VAS_INT8;
+  __shared__ Packing pk;
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int32_t step = (a.B + kAppendSeqs - 1) / kAppendSeqs;
+  scan_lengths(a, pk, step);
+  if (blockIdx.x == 0) {
+    bool bad = threadIdx.x == 0 && pk.row0[kAppendSeqs] != a.T;
+    for (int64_t i = threadIdx.x; i < a.B; i += kAppendThreads)
+      bad |= !lengths_ok(a, a.length(i), a.count(i));
+    if (bad) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
+  }
+  const int32_t E = a.Hkv << a.log2D;  // elements of a token's row
+  const int64_t stride = (int64_t)gridDim.x * kAppendWarps;
+  for (int64_t t = (int64_t)blockIdx.x * kAppendWarps + warp; t < a.T; t += stride) {
+    const Owner o = owner_of(a, pk, step, (int32_t)t, lane);
+    int32_t page = -1, slot = 0;
+    if (o.ok) {
+      const int32_t pos = o.len - o.count + (int32_t)(t - o.row);
+      page = a.block_table[(size_t)o.seq * a.maxp + (pos >> a.log2P)];
+      slot = pos & (a.P - 1);
+      if (page < 0 || page >= a.num_pages) {
+        page = -1;
+        if (lane == 0) atomicOr(a.err, VAS_DEV_BAD_PAGE);
+      }
+    }
+    for (int32_t e = lane * N; e < 2 * E; e += 32 * N) {
+      const bool is_v = e >= E;
+      const int32_t x = is_v ? e - E : e;
+      float y[N];
+      if (page >= 0) {
+        const int32_t h = x >> a.log2D;
+        float scale = 1.f;
+        if (kQuant) {
+          const size_t si = (size_t)page * a.Hkv + h;
+          scale = (is_v ? a.v_scale : a.k_scale)[BLOCK ? si : si * a.P + slot];
+        }
+        read_elements<KV, N>(is_v ? a.v_pages : a.k_pages, ((size_t)page * a.P + slot) * E + x, scale, y);
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = NAN;
+      }
+      OUT* out = static_cast<OUT*>(is_v ? a.v_out : a.k_out) + t * (is_v ? a.v_stride : a.k_stride) + x;
+      write_elements(out, y);
+    }
+  }
+}
+
+namespace {
+
+template <typename... P, typename... A>
+int launch_pdl(void (*kernel)(P...), int64_t blocks, vas_stream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3(kAppendThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return VAS_E_CUDA;
+  }
+  return VAS_OK;
+}
+
+bool misaligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0;
+}
+
+template <int KV, int D>
+int launch_block(const AppendArgs& a, bool inter, vas_stream_t stream) {
+  // At most ceil(ql / P) + 1 pages of a sequence, and no more than its tokens.
+  int64_t runs = (int64_t)a.T / a.P + 2 * (int64_t)a.B;
+  runs = runs < a.T ? runs : a.T;
+  const int64_t want = (runs * 2 * a.Hkv + kAppendWarps - 1) / kAppendWarps;
+  const int64_t most = 4LL * vas::num_sms();
+  const int64_t blocks = want < most ? want : most;
+  return inter ? launch_pdl(append_block_kernel<KV, D, true>, blocks, stream, a)
+               : launch_pdl(append_block_kernel<KV, D, false>, blocks, stream, a);
+}
+
+template <int KV, bool BLOCK>
+int launch_read(const ReadArgs& a, bool f32, vas_stream_t stream) {
+  const int64_t want = ((int64_t)a.T + kAppendWarps - 1) / kAppendWarps;
+  const int64_t most = 4LL * vas::num_sms();
+  const int64_t blocks = want < most ? want : most;
+  return f32 ? launch_pdl(read_kernel<KV, BLOCK, float>, blocks, stream, a)
+             : launch_pdl(read_kernel<KV, BLOCK, __nv_bfloat16>, blocks, stream, a);
+}
+
+}  // namespace
+
+int launch_append_block(const AppendArgs& a, int head_dim, bool fp8, bool inter, vas_stream_t stream) {
+  if (head_dim == 128)
+    return fp8 ? launch_block<VAS_FP8_E4M3, 128>(a, inter, stream)
+               : launch_block<VAS_INT8, 128>(a, inter, stream);
+  return fp8 ? launch_block<VAS_FP8_E4M3, 64>(a, inter, stream)
+             : launch_block<VAS_INT8, 64>(a, inter, stream);
+}
+
+}  // namespace cache
+}  // namespace vas
+
+extern "C" {
+
+int paged_kv_read(const void* k_pages, const void* v_pages, const float* k_scale,
+                  const float* v_scale, const int32_t* block_table, const int32_t* starts,
+                  const int32_t* lens, void* k_out, void* v_out, const vas_read_dims* dims,
+                  vas_stream_t stream) {
+  using namespace vas::cache;
+  if (!dims) return VAS_E_INVALID_ARG;
+  const vas_read_dims& d = *dims;
+  if (d.num_seqs < 0 || d.total_tokens < 0 || d.num_kv_heads <= 0 || d.num_pages < 0 ||
+      d.max_pages_per_seq < 0)
+    return VAS_E_INVALID_ARG;
+  const bool block = d.kv_dtype == VAS_FP8_BLOCK || d.kv_dtype == VAS_INT8_BLOCK;
+  const bool quant = block || d.kv_dtype == VAS_FP8_E4M3 || d.kv_dtype == VAS_INT8;
+  if ((d.head_dim != 64 && d.head_dim != 128) || (d.page_size != 16 && d.page_size != 32) ||
+      (!quant && d.kv_dtype != VAS_F32 && d.kv_dtype != VAS_BF16) ||
+      (d.out_dtype != VAS_F32 && d.out_dtype != VAS_BF16))
+    return VAS_E_UNSUPPORTED;
+  const int64_t width = (int64_t)d.num_kv_heads * d.head_dim;
+  if (width > INT32_MAX / 4) return VAS_E_UNSUPPORTED;
+  if (quant != (k_scale != nullptr) || quant != (v_scale != nullptr)) return VAS_E_INVALID_ARG;
+  if (d.total_tokens == 0) return VAS_OK;
+  if (d.num_seqs == 0) return VAS_E_INVALID_ARG;  // rows of no sequence
+  if (!k_pages || !v_pages || !block_table || !lens || !k_out || !v_out) return VAS_E_INVALID_ARG;
+  if (d.num_pages == 0 || d.max_pages_per_seq == 0) return VAS_E_INVALID_ARG;
+  if ((int64_t)d.num_pages * d.page_size > INT32_MAX) return VAS_E_INVALID_ARG;
+  const int es = d.out_dtype == VAS_F32 ? 4 : 2;
+  if (d.k_stride < width || d.v_stride < width || d.k_stride * es % 16 || d.v_stride * es % 16)
+    return VAS_E_INVALID_ARG;
+  if (misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(k_scale, 4) ||
+      misaligned(v_scale, 4) || misaligned(block_table, 4) || misaligned(starts, 4) ||
+      misaligned(lens, 4) || misaligned(k_out, 16) || misaligned(v_out, 16))
+    return VAS_E_INVALID_ARG;
+  ReadArgs a;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_table = block_table;
+  a.starts = starts;
+  a.lens = lens;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.k_stride = d.k_stride;
+  a.v_stride = d.v_stride;
+  a.B = d.num_seqs;
+  a.T = d.total_tokens;
+  a.Hkv = d.num_kv_heads;
+  a.P = d.page_size;
+  a.num_pages = d.num_pages;
+  a.maxp = d.max_pages_per_seq;
+  a.log2P = d.page_size == 16 ? 4 : 5;
+  a.log2D = d.head_dim == 64 ? 6 : 7;
+  a.err = vas::device_error_word();
+  if (!a.err || !vas::num_sms()) return VAS_E_CUDA;
+  const bool f32 = d.out_dtype == VAS_F32;
+  switch (d.kv_dtype) {
+    case VAS_F32: return launch_read<VAS_F32, false>(a, f32, stream);
+    case VAS_BF16: return launch_read<VAS_BF16, false>(a, f32, stream);
+    case VAS_FP8_E4M3: return launch_read<VAS_FP8_E4M3, false>(a, f32, stream);
+    case VAS_INT8: return launch_read<VAS_INT8, false>(a, f32, stream);
+    case VAS_FP8_BLOCK: return launch_read<VAS_FP8_E4M3, true>(a, f32, stream);
+    default: return launch_read<VAS_INT8, true>(a, f32, stream);
+  }
+}
+
+}  // extern "C"

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "../../include/vas.h"
+#include "append_rows.cuh"
 #include "device_util.cuh"
 #include "packed_math.cuh"
 #include "vas_internal.h"
@@ -32,254 +33,6 @@ namespace cache {
 // (a 16-term sum and 16 rotations a lane) hides behind the loads as long as tokens are many:
 // 8192 tokens of 64/8 heads of 128 in bf16, 336 MB, 61 us, 5.5 TB/s; 768 on FP8 pages, 30 MB,
 // 12.5 us, where the chain of one token's reads shows.
-constexpr int kAppendThreads = 256;
-constexpr int kAppendWarps = kAppendThreads / 32;
-constexpr int kAppendBlocks = 2;  // of an SM
-
-struct AppendArgs {
-  const void* q;
-  const void* k;
-  const void* v;
-  const void* q_weight;
-  const void* k_weight;
-  const float* cos_sin;
-  const int32_t* positions;
-  const int32_t* block_table;
-  const int32_t* seq_lens;
-  const int32_t* query_lens;
-  void* q_out;
-  void* k_pages;
-  void* v_pages;
-  float* k_scale;
-  float* v_scale;
-  int64_t q_stride, k_stride, v_stride;
-  int32_t B, T, Hq, Hkv, P, num_pages, maxp, rot, max_position;
-  int32_t log2P;
-  int32_t parts, iters;  // a token is `parts` tasks of `iters` groups of rows
-  float eps;
-  int32_t* err;
-};
-
-// Eight fp32 values as four pairs, the operands of the packed instructions.
-struct F8 {
-  uint64_t p[4];
-};
-
-__device__ __forceinline__ F8 load_f8(const float* p) {
-  const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(p);
-  const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(p + 4);
-  return {{u.x, u.y, w.x, w.y}};
-}
-
-// 16 (bf16) or 32 (fp32) raw bytes of each of a lane's two chunks: what waits in registers
-// between the load and its use.
-template <typename T>
-struct Raw {
-  uint4 a[sizeof(T) / 2], b[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* p, int ca, int cb) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-      a[i] = __ldcs(reinterpret_cast<const uint4*>(p + ca) + i);
-      b[i] = __ldcs(reinterpret_cast<const uint4*>(p + cb) + i);
-    }
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) a[i] = b[i] = make_uint4(0, 0, 0, 0);
-  }
-};
-__device__ __forceinline__ F8 widen(const uint4 (&u)[1]) {
-  return {{pair(bf16_lo_f32(u[0].x), bf16_hi_f32(u[0].x)), pair(bf16_lo_f32(u[0].y), bf16_hi_f32(u[0].y)),
-           pair(bf16_lo_f32(u[0].z), bf16_hi_f32(u[0].z)), pair(bf16_lo_f32(u[0].w), bf16_hi_f32(u[0].w))}};
-}
-__device__ __forceinline__ F8 widen(const uint4 (&u)[2]) {
-  auto f = [](uint32_t x, uint32_t y) { return pair(__uint_as_float(x), __uint_as_float(y)); };
-  return {{f(u[0].x, u[0].y), f(u[0].z, u[0].w), f(u[1].x, u[1].y), f(u[1].z, u[1].w)}};
-}
-__device__ __forceinline__ F8 load_weights(const __nv_bfloat16* p) {
-  const uint4 u[1] = {*reinterpret_cast<const uint4*>(p)};
-  return widen(u);
-}
-__device__ __forceinline__ F8 load_weights(const float* p) { return load_f8(p); }
-
-__device__ __forceinline__ uint32_t bf16_pair(uint64_t v) {
-  float lo, hi;
-  unpair(v, lo, hi);
-  return pack_bf16x2(lo, hi);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const F8& x) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(bf16_pair(x.p[0]), bf16_pair(x.p[1]), bf16_pair(x.p[2]), bf16_pair(x.p[3]));
-}
-__device__ __forceinline__ void store8(float* p, const F8& x) {
-  *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x.p[0], x.p[1]);
-  *reinterpret_cast<ulonglong2*>(p + 4) = make_ulonglong2(x.p[2], x.p[3]);
-}
-
-// x / scale, rounded to nearest.  With the correctly rounded reciprocal r = 1 / scale, one
-// correction of x r by its exact remainder gives the correctly rounded quotient (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor", IBM J. Res.
-// Dev. 34, 1990), three packed instructions for two elements; scales near the ends of the
-// range, where r or the remainder could leave it, and the not finite ones divide.
-__device__ __forceinline__ F8 quotients(const F8& x, float scale) {
-  F8 y;
-  if (scale > 0x1p-80f && scale < 0x1p80f) {
-    const float r = __frcp_rn(scale);
-    const uint64_t r2 = pair(r, r), ns2 = pair(-scale, -scale);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t q = mul2(x.p[i], r2);
-      y.p[i] = fma2(fma2(q, ns2, x.p[i]), r2, q);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float lo, hi;
-      unpair(x.p[i], lo, hi);
-      y.p[i] = pair(__fdiv_rn(lo, scale), __fdiv_rn(hi, scale));
-    }
-  }
-  return y;
-}
-
-// 8 values as codes: E4M3 (round to nearest even, saturating; NaN stays NaN) or INT8.
-template <int KV>
-__device__ __forceinline__ uint2 codes8(const F8& x, float scale) {
-  const F8 q = quotients(x, scale);
-  uint32_t w[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float y[4];
-    unpair(q.p[2 * h], y[0], y[1]);
-    unpair(q.p[2 * h + 1], y[2], y[3]);
-    if constexpr (KV == VAS_FP8_E4M3) {
-      asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
-          "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
-          : "=r"(w[h])
-          : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
-    } else {
-      w[h] = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // |y| <= 127 (1 + 2^-23), or NaN, which converts to 0 under a scale that is not
-        // finite.
-        const int c = max(-127, min(127, __float2int_rn(y[i])));
-        w[h] |= (uint32_t)(c & 0xff) << (8 * i);
-      }
-    }
-  }
-  return make_uint2(w[0], w[1]);
-}
-
-// Where a token goes, or why it does not.
-struct Place {
-  int32_t page, slot, position;
-  int32_t err;  // device error bits; the token is not stored and its q_out row is NaN
-};
-
-// The packing of a call, in shared memory: the first row of every `step`th sequence, and
-// with step 1 (up to kAppendSeqs sequences) their lengths too.
-constexpr int kAppendSeqs = 1024;
-struct Packing {
-  int32_t row0[kAppendSeqs + 1];  // clamped to INT_MAX; the last one is the total
-  int32_t len[kAppendSeqs];
-  int64_t wsum[kAppendWarps];
-};
-
-__device__ __forceinline__ bool lengths_ok(const AppendArgs& a, int32_t L, int32_t ql) {
-  return ql >= 0 && ql <= a.T && L >= ql && (int64_t)L <= (int64_t)a.maxp * a.P;
-}
-
-__device__ __forceinline__ void scan_lengths(const AppendArgs& a, Packing& pk, int32_t step) {
-  constexpr int kPer = kAppendSeqs / kAppendThreads;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t mine[kPer], sum = 0;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const int c = tid * kPer + e;
-    mine[e] = 0;
-    if (step == 1) {
-      if (c < a.B) {
-        mine[e] = max(a.query_lens[c], 0);
-        pk.len[c] = a.seq_lens[c];
-      }
-    } else {
-      for (int64_t i = (int64_t)c * step; i < a.B && i < ((int64_t)c + 1) * step; ++i)
-        mine[e] += max(a.query_lens[i], 0);
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    const int64_t n = mine[e];
-    mine[e] = sum;
-    sum += n;
-  }
-  int64_t inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t n = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += n;
-  }
-  if (lane == 31) pk.wsum[warp] = inc;
-  __syncthreads();
-  int64_t base = inc - sum;
-#pragma unroll
-  for (int w = 0; w < kAppendWarps; ++w)
-    if (w < warp) base += pk.wsum[w];
-  auto clamp = [](int64_t x) { return (int32_t)(x < INT_MAX ? x : INT_MAX); };
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) pk.row0[tid * kPer + e] = clamp(base + mine[e]);
-  if (tid == kAppendThreads - 1) pk.row0[kAppendSeqs] = clamp(base + sum);
-  __syncthreads();
-}
-
-// The whole warp: the place of packed row t.  The last start at or below t is found in two
-// rounds of 32 (sequences without tokens share their successor's start, so the last of
-// equal starts is the one that has tokens).
-__device__ __forceinline__ Place place_of(const AppendArgs& a, const Packing& pk, int32_t step,
-                                          int32_t t, int lane) {
-  Place p{0, 0, 0, 0};
-  if (t >= pk.row0[kAppendSeqs]) {
-    p.err = VAS_DEV_BAD_LENGTHS;  // a row that no sequence owns
-    return p;
-  }
-  constexpr int kBlock = kAppendSeqs / 32;
-  const int hi = __popc(__ballot_sync(0xffffffffu, pk.row0[lane * kBlock] <= t)) - 1;
-  static_assert(kBlock == 32, "one start a lane in the second round");
-  const int lo = __popc(__ballot_sync(0xffffffffu, pk.row0[hi * kBlock + lane] <= t)) - 1;
-  const int c = hi * kBlock + lo;
-  int64_t row = pk.row0[c];
-  int32_t i = c, ql, L;
-  if (step == 1) {
-    // A negative length counts as none, so a sequence found here has its true one.
-    ql = pk.row0[c + 1] - pk.row0[c];
-    L = pk.len[c];
-  } else {
-    for (i = c * step; i < a.B; ++i) {
-      ql = a.query_lens[i];
-      const int64_t n = ql > 0 ? ql : 0;
-      if (t < row + n) break;
-      row += n;
-    }
-    if (i >= a.B) {
-      p.err = VAS_DEV_BAD_LENGTHS;
-      return p;
-    }
-    L = a.seq_lens[i];
-  }
-  if (!lengths_ok(a, L, ql) || row + ql > a.T) {
-    p.err = VAS_DEV_BAD_LENGTHS;
-    return p;
-  }
-  const int32_t pos = L - ql + (int32_t)(t - row);
-  p.position = a.positions ? a.positions[t] : pos;
-  if (a.rot && (p.position < 0 || p.position >= a.max_position)) p.err |= VAS_DEV_BAD_POSITION;
-  p.page = a.block_table[(size_t)i * a.maxp + (pos >> a.log2P)];
-  p.slot = pos & (a.P - 1);
-  if (p.page < 0 || p.page >= a.num_pages) p.err |= VAS_DEV_BAD_PAGE;
-  return p;
-}
-
 // KV: the pool's storage type; T: the activations' (float with VAS_F32, bf16 otherwise).
 // ROWS: head rows a lane holds at a time, so a warp has a group of 512 / D * ROWS rows (q
 // heads, then k, then v) in flight.  A task is `iters` consecutive groups of one token: one
@@ -301,21 +54,10 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(c
   const uint32_t stride = gridDim.x * kAppendWarps;
   uint32_t task = blockIdx.x * kAppendWarps + warp;
 
-  // This lane's chunks of a row.  Split halves: rotated pairs (8c + e, 8c + e + rot / 2)
-  // first, then the rest of the head.  Neighbours: 16 consecutive elements.
-  const int c = lane % kLanes, nrot = a.rot / 16;
-  const bool turned = c < nrot;
-  int ca, cb;
-  if (INTER) {
-    ca = 16 * c;
-    cb = ca + 8;
-  } else if (turned) {
-    ca = 8 * c;
-    cb = ca + a.rot / 2;
-  } else {
-    ca = a.rot + 8 * (c - nrot);
-    cb = ca + (D - a.rot) / 2;
-  }
+  const int c = lane % kLanes;
+  const Chunks ch = lane_chunks<D, INTER>(c, a.rot);
+  const bool turned = ch.turned;
+  const int ca = ch.a, cb = ch.b;
 
   // A row's values are on their way while the place of its token is looked up (and, for
   // the first ones, while the block scans the lengths).
@@ -383,51 +125,10 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(c
           wa = load_weights(w + ca);
           wb = load_weights(w + cb);
         }
-        // Sum of squares over the row's lanes; every lane of the warp takes part.
-        uint64_t s2 = mul2(xa.p[0], xa.p[0]);
-#pragma unroll
-        for (int e = 1; e < 4; ++e) s2 = fma2(xa.p[e], xa.p[e], s2);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s2 = fma2(xb.p[e], xb.p[e], s2);
-        float ss, hi;
-        unpair(s2, ss, hi);
-        ss += hi;
-#pragma unroll
-        for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float ss = row_squares<kLanes>(xa, xb);
         if (!is_v) {
-          if (w != nullptr) {
-            const float inv = rsqrtf(ss * (1.f / D) + a.eps);
-            const uint64_t inv2 = pair(inv, inv);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              xa.p[e] = mul2(mul2(xa.p[e], inv2), wa.p[e]);
-              xb.p[e] = mul2(mul2(xb.p[e], inv2), wb.p[e]);
-            }
-          }
-          if (turned) {
-            if (INTER) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float c0, c1, s0, s1, u0, u1;
-                unpair(cs.p[e], c0, c1);
-                unpair(sn.p[e], s0, s1);
-                // Pairs 2e and 2e + 1: chunk a holds pairs 0..3, chunk b 4..7.
-                uint64_t& y0 = e < 2 ? xa.p[2 * (e & 1)] : xb.p[2 * (e & 1)];
-                uint64_t& y1 = e < 2 ? xa.p[2 * (e & 1) + 1] : xb.p[2 * (e & 1) + 1];
-                unpair(y0, u0, u1);
-                y0 = pair(u0 * c0 - u1 * s0, u1 * c0 + u0 * s0);
-                unpair(y1, u0, u1);
-                y1 = pair(u0 * c1 - u1 * s1, u1 * c1 + u0 * s1);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint64_t u = xa.p[e], v = xb.p[e];
-                xa.p[e] = sub2(mul2(u, cs.p[e]), mul2(v, sn.p[e]));
-                xb.p[e] = fma2(v, cs.p[e], mul2(u, sn.p[e]));
-              }
-            }
-          }
+          if (w != nullptr) norm_row<D>(xa, xb, wa, wb, ss, a.eps);
+          if (turned) turn_row<INTER>(xa, xb, cs, sn);
         }
         float scale = 1.f;
         if (kQuant && __any_sync(0xffffffffu, !is_q)) {
@@ -506,6 +207,7 @@ struct CopyArgs {
   int32_t n, segs;      // pairs; segments of a page
   int32_t token_bytes;  // Hkv * D * element size
   int32_t P, Hkv, num_pages;
+  int32_t block_scale;  // scales [Hkv] a page, not [Hkv][P]
 };
 
 template <int N>
@@ -539,9 +241,9 @@ __global__ void __launch_bounds__(kCopyThreads)
   }
   if (a.ks != nullptr && seg == 0) {  // scales [Hkv][P]: the first tokens of each head
     float* sc = is_v ? a.vs : a.ks;
-    const int n = a.Hkv * a.P;
+    const int n = a.block_scale ? a.Hkv : a.Hkv * a.P;
     for (int e = tid; e < n; e += kCopyThreads)
-      if (e % a.P < tokens) sc[to * n + e] = sc[from * n + e];
+      if (a.block_scale || e % a.P < tokens) sc[to * n + e] = sc[from * n + e];
   }
 }
 
@@ -664,7 +366,11 @@ bool misaligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0;
 }
 
-bool is_quant(int32_t kv) { return kv == VAS_FP8_E4M3 || kv == VAS_INT8; }
+bool is_block(int32_t kv) { return kv == VAS_FP8_BLOCK || kv == VAS_INT8_BLOCK; }
+
+bool is_quant(int32_t kv) { return kv == VAS_FP8_E4M3 || kv == VAS_INT8 || is_block(kv); }
+
+bool is_storage(int32_t kv) { return (kv >= VAS_F32 && kv <= VAS_INT8) || is_block(kv); }
 
 int32_t element_size(int32_t kv) { return kv == VAS_F32 ? 4 : (kv == VAS_BF16 ? 2 : 1); }
 
@@ -739,7 +445,7 @@ int check_pool(const vas_pool_dims* d, const void* k, const void* v, const float
   if (!d) return VAS_E_INVALID_ARG;
   if (d->num_layers < 0 || d->num_pages < 0 || d->num_kv_heads <= 0) return VAS_E_INVALID_ARG;
   if ((d->head_dim != 64 && d->head_dim != 128) || (d->page_size != 16 && d->page_size != 32) ||
-      d->kv_dtype < VAS_F32 || d->kv_dtype > VAS_INT8)
+      !is_storage(d->kv_dtype))
     return VAS_E_UNSUPPORTED;
   const int64_t tb = (int64_t)d->num_kv_heads * d->head_dim * element_size(d->kv_dtype);
   // Offsets inside a page are 32 bits, up to the end of its last segment.
@@ -809,7 +515,7 @@ int paged_kv_append(const void* q, const void* k, const void* v, const void* q_w
     return VAS_E_INVALID_ARG;
   if (!(d.eps >= 0.f) || std::isinf(d.eps)) return VAS_E_INVALID_ARG;
   if ((d.head_dim != 64 && d.head_dim != 128) || (d.page_size != 16 && d.page_size != 32) ||
-      d.kv_dtype < VAS_F32 || d.kv_dtype > VAS_INT8 || d.rotary_dim % 16 ||
+      !is_storage(d.kv_dtype) || d.rotary_dim % 16 ||
       d.rotary_dim > d.head_dim || (d.interleaved != 0 && d.interleaved != 1))
     return VAS_E_UNSUPPORTED;
   const int64_t heads = (int64_t)d.num_q_heads + 2 * (int64_t)d.num_kv_heads;
@@ -884,6 +590,16 @@ int paged_kv_append(const void* q, const void* k, const void* v, const void* q_w
     case VAS_BF16: return launch_append<__nv_bfloat16, VAS_BF16>(a, d.head_dim, inter, stream);
     case VAS_FP8_E4M3:
       return launch_append<__nv_bfloat16, VAS_FP8_E4M3>(a, d.head_dim, inter, stream);
+    case VAS_FP8_BLOCK:
+    case VAS_INT8_BLOCK: {
+      AppendArgs rows = a;  // the queries, which no page sees
+      rows.Hkv = 0;
+      const int st = a.Hq > 0
+                         ? launch_append<__nv_bfloat16, VAS_BF16>(rows, d.head_dim, inter, stream)
+                         : VAS_OK;
+      if (st != VAS_OK) return st;
+      return launch_append_block(a, d.head_dim, d.kv_dtype == VAS_FP8_BLOCK, inter, stream);
+    }
     default: return launch_append<__nv_bfloat16, VAS_INT8>(a, d.head_dim, inter, stream);
   }
 }
@@ -913,6 +629,7 @@ int paged_kv_copy(void* k_pages, void* v_pages, float* k_scale, float* v_scale,
   a.P = dims->page_size;
   a.Hkv = dims->num_kv_heads;
   a.num_pages = dims->num_pages;
+  a.block_scale = is_block(dims->kv_dtype) ? 1 : 0;
   a.n = a.segs = 0;
   for (int32_t i = 0; i < n;) {
     const int32_t left = n - i;
@@ -936,6 +653,8 @@ int paged_kv_keep_path(void* k_pages, void* v_pages, float* k_scale, float* v_sc
   KeepArgs a;
   const int st = check_pool(dims, k_pages, v_pages, k_scale, v_scale, &a.token_bytes);
   if (st != VAS_OK) return st;
+  // Nodes of one page may go to a page of another scale: their codes would not do there.
+  if (is_block(dims->kv_dtype)) return VAS_E_UNSUPPORTED;
   if (B < 0 || n < 1 || n > kKeepMaxNodes || num_seqs < 0 || max_pages_per_seq < 0)
     return VAS_E_INVALID_ARG;
   if (B == 0 || dims->num_layers == 0) return VAS_OK;

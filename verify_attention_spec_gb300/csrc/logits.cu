@@ -1,0 +1,554 @@
+// Logits of a verification window to the probabilities of the rejection rule (sm_103a):
+// spec_logits.  Penalties for repeated tokens, a sparse bias, a grammar mask, temperature and
+// softmax in one pass over the vocabulary.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "../../include/vas.h"
+#include "device_util.cuh"
+#include "vas_internal.h"
+
+namespace vas {
+namespace logits {
+
+// One cluster of C CTAs a row: CTA r holds the slice r of the vocabulary, 8 NV logits a thread
+// in registers as fp32 from the one read to the one write.  What the row's tokens need beside
+// the logits themselves -- how often a token was generated, whether the prompt has it, which
+// bias it gets -- is a table in shared memory with a word for every token of the slice, made
+// from the sequence's token list: each CTA reads 1 / C of the list and counts into the slices
+// of all (distributed shared memory), so the list is read once a row.  Vocabularies past the
+// registers' reach (8 * 512 * 32 = 131072 logits) are taken in chunks, the table made anew and
+// the logits read again for the second pass.
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kMaxBias = 1024;
+constexpr int kMaxTokens = 1 << 20;  // of a list: a count fits its field
+constexpr int kMaxNodes = 255;
+// A table word: count, prompt flag, bias entry + 1.
+constexpr uint32_t kCountMask = (1u << 20) - 1, kPrompt = 1u << 20;
+constexpr int kBiasShift = 21;
+
+struct Args {
+  const void* logits;
+  const int32_t* tokens;
+  const int32_t* token_lens;
+  const int32_t* prompt_lens;
+  const int32_t* drafts;
+  const int32_t* parents;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const int32_t* bias_tokens;
+  const float* bias;
+  const uint32_t* mask;
+  const float* temperature;
+  float* out;
+  int64_t row_stride;
+  int32_t n, V, max_tokens, max_bias, mask_words;
+  int32_t cluster, slice, chunks;  // CTAs of a row; tokens of a CTA (a multiple of 32); chunks of it
+  int32_t probs, counted;  // counted: penalties are in play
+  int32_t out_vec;         // rows of out are 16-byte aligned
+  int32_t* err;
+};
+
+struct Shared {
+  float bias[kMaxBias];
+  int32_t bias_tok[kMaxBias];
+  int32_t parent[kMaxNodes];
+  uint8_t on_path[kMaxNodes + 1];
+  float red_max[kWarps], red_sum[kWarps];
+  int32_t red_at[kWarps];
+  float peer_max[kMaxCluster], peer_sum[kMaxCluster];  // written by the cluster's CTAs
+  int32_t peer_at[kMaxCluster];
+  int32_t bad;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t peer_address(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void peer_add(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void peer_or(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void peer_store(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+
+// VEC: a thread's logits are runs of 8 neighbours, 16-byte aligned; else they are kThreads
+// apart.
+template <typename T, bool VEC, int NV>
+struct Tile {
+  static constexpr int kTokens = kThreads * 8 * NV;
+  // Token (of the chunk) of this thread's value 8 v + e.
+  static __device__ __forceinline__ int at(int v, int e) {
+    return VEC ? (v * kThreads + (int)threadIdx.x) * 8 + e
+               : (v * 8 + e) * kThreads + (int)threadIdx.x;
+  }
+};
+
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&y)[8]) {
+  const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[2 * i] = bf16_lo_f32(w[i]), y[2 * i + 1] = bf16_hi_f32(w[i]);
+}
+__device__ __forceinline__ void load8(const float* p, float (&y)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  y[0] = a.x, y[1] = a.y, y[2] = a.z, y[3] = a.w;
+  y[4] = b.x, y[5] = b.y, y[6] = b.z, y[7] = b.w;
+}
+__device__ __forceinline__ float widen1(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float widen1(float x) { return x; }
+
+template <typename T, bool VEC, int NV, bool MULTI>
+__global__ void __launch_bounds__(kThreads) spec_logits_kernel(const Args a) {
+  using L = Tile<T, VEC, NV>;
+  extern __shared__ uint32_t table[];  // L::kTokens words, if the row has a table
+  __shared__ Shared s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_rank();
+  const int C = a.cluster;
+  const int row = (int)(blockIdx.x / (unsigned)C), b = row / (a.n + 1), j = row - b * (a.n + 1);
+  const bool use_table = a.counted || a.max_bias > 0;
+  if (a.probs && !use_table) cluster_arrive();  // its wait: before the first store to a peer
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+
+  // The drafts on the way to row j: those before it, or its ancestors.
+  if (tid == 0) s.bad = 0;
+  const bool path = a.counted && j > 0;
+  if (path) {
+    if (a.parents)
+      for (int i = tid; i < a.n; i += kThreads) s.parent[i] = a.parents[(size_t)b * a.n + i];
+    for (int i = tid; i < a.n; i += kThreads) s.on_path[i] = !a.parents && i < j;
+  }
+  const int nb = a.max_bias;
+  for (int i = tid; i < nb; i += kThreads) {
+    s.bias_tok[i] = a.bias_tokens[(size_t)b * nb + i];
+    s.bias[i] = a.bias[(size_t)b * nb + i];
+  }
+  int32_t n_tok = 0, n_prompt = 0;
+  bool bad = false;
+  if (a.counted && a.tokens) {
+    n_tok = a.token_lens[b];
+    n_prompt = a.prompt_lens ? a.prompt_lens[b] : 0;
+    if (n_tok < 0 || n_tok > a.max_tokens || n_prompt < 0 || n_prompt > n_tok) {
+      bad = true;
+      n_tok = n_prompt = 0;
+      if (tid == 0 && rank == 0) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
+    }
+  }
+  __syncthreads();
+  if (path && a.parents && tid == 0) {
+    for (int u = j; u > 0;) {  // ascends: a parent precedes its child
+      const int p = s.parent[u - 1];
+      s.on_path[u - 1] = 1;
+      if (p < 0 || p >= u) {
+        s.bad = VAS_DEV_BAD_TREE;
+        break;
+      }
+      u = p;
+    }
+  }
+  __syncthreads();
+  if (path) {
+    int e = s.bad;
+    for (int i = tid; i < a.n; i += kThreads)
+      if (s.on_path[i]) {
+        const int x = a.drafts[(size_t)b * a.n + i];
+        if (x < 0 || x >= a.V) e = VAS_DEV_BAD_TOKEN;
+      }
+    if (e) {
+      atomicOr(&s.bad, e);
+      if (rank == 0) atomicOr(a.err, e);
+    }
+    __syncthreads();
+    bad |= s.bad != 0;
+  }
+
+  const float rep = a.repetition ? a.repetition[b] : 1.f;
+  const float freq = a.frequency ? a.frequency[b] : 0.f;
+  const float pres = a.presence ? a.presence[b] : 0.f;
+  const T* in = static_cast<const T*>(a.logits) + (size_t)row * a.row_stride;
+  float* out = a.out + (size_t)row * a.V;
+  const uint8_t* mask_bytes = reinterpret_cast<const uint8_t*>(a.mask + (size_t)row * a.mask_words);
+  const int first = rank * a.slice, last = min(a.V, first + a.slice);
+
+  // The table of chunk k of every slice.
+  auto make_table = [&](int k) {
+    uint4* t4 = reinterpret_cast<uint4*>(table);
+    __syncthreads();  // the chunk before has been read
+    for (int i = tid; i < L::kTokens / 4; i += kThreads) t4[i] = make_uint4(0, 0, 0, 0);
+    cluster_sync();  // all slices are clear
+    if (a.counted) {
+      auto mark = [&](int32_t x, bool prompt) {
+        if (x < 0 || x >= a.V) return;  // no logit: a placeholder
+        const uint32_t r = (uint32_t)x / (uint32_t)a.slice;
+        const int at = x - (int)r * a.slice - k * L::kTokens;
+        if (at < 0 || at >= L::kTokens) return;
+        const uint32_t word = peer_address(table + at, r);
+        if (prompt) peer_or(word, kPrompt);
+        else peer_add(word, 1);
+      };
+      for (int i = (int)rank * kThreads + tid; i < n_tok; i += C * kThreads)
+        mark(a.tokens[(size_t)b * a.max_tokens + i], i < n_prompt);
+      if (path && rank == 0)
+        for (int i = tid; i < a.n; i += kThreads)
+          if (s.on_path[i]) mark(a.drafts[(size_t)b * a.n + i], false);
+    }
+    // Biases of this slice: the first entry of a token gets the sum of all, in list order.
+    for (int i = tid; i < nb; i += kThreads) {
+      const int x = s.bias_tok[i], at = x - first - k * L::kTokens;
+      if (x < first || x >= last || at < 0 || at >= L::kTokens) continue;
+      bool head = true;
+      for (int e = 0; e < i; ++e) head &= s.bias_tok[e] != x;
+      if (head) atomicOr(table + at, (uint32_t)(i + 1) << kBiasShift);
+    }
+    cluster_sync();
+  };
+  auto bias_of = [&](int i) {
+    const int x = s.bias_tok[i];
+    float sum = s.bias[i];
+    for (int e = i + 1; e < nb; ++e)
+      if (s.bias_tok[e] == x) sum += s.bias[e];
+    return sum;
+  };
+  float z[NV][8];
+  auto load_chunk = [&](int k) {
+    const int base = first + k * L::kTokens;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int t0 = L::at(v, 0);
+      if (VEC && base + t0 + 8 <= last) {
+        load8(in + base + t0, z[v]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int x = base + L::at(v, e);
+          z[v][e] = x < last ? widen1(in[x]) : -INFINITY;
+        }
+      }
+    }
+    if (use_table) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t w = table[L::at(v, e)];
+          if (w == 0) continue;
+          float y = z[v][e];
+          if (w & (kCountMask | kPrompt)) y = y > 0.f ? y / rep : y * rep;
+          if (w & kCountMask) y = y - freq * (float)(w & kCountMask) - pres;
+          if (w >> kBiasShift) y += bias_of((int)(w >> kBiasShift) - 1);
+          z[v][e] = y;
+        }
+    }
+    if (a.mask) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        if (VEC) {
+          const int x = base + L::at(v, 0);
+          const uint32_t allowed = x < last ? mask_bytes[x >> 3] : 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (!((allowed >> e) & 1)) z[v][e] = -INFINITY;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int x = base + L::at(v, e);
+            if (x < last && !((mask_bytes[x >> 3] >> (x & 7)) & 1)) z[v][e] = -INFINITY;
+          }
+        }
+      }
+    }
+  };
+  auto store_chunk = [&](int k) {
+    const int base = first + k * L::kTokens;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int x0 = base + L::at(v, 0);
+      if (VEC && a.out_vec && x0 + 8 <= last) {
+        float4* p = reinterpret_cast<float4*>(out + x0);
+        __stcs(p, make_float4(z[v][0], z[v][1], z[v][2], z[v][3]));
+        __stcs(p + 1, make_float4(z[v][4], z[v][5], z[v][6], z[v][7]));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int x = base + L::at(v, e);
+          if (x < last) __stcs(out + x, z[v][e]);
+        }
+      }
+    }
+  };
+
+  const int chunks = MULTI ? a.chunks : 1;
+  if (!a.probs) {
+    for (int k = 0; k < chunks; ++k) {
+      if (use_table) make_table(k);
+      load_chunk(k);
+      if (bad) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[v][e] = NAN;
+      }
+      store_chunk(k);
+    }
+    return;
+  }
+
+  // Softmax: the slice's maximum (its first token too, for temperature 0) and its sum of
+  // exponentials, then those of the cluster.
+  const float temp = a.temperature ? a.temperature[b] : 1.f;
+  const bool greedy = temp == 0.f;
+  const float c = greedy ? 0.f : (temp > 0.f ? 1.4426950408889634f / temp : NAN);
+  float m = -INFINITY, sum = 0.f;
+  int best = 0x7fffffff;
+  for (int k = 0; k < chunks; ++k) {
+    if (use_table) make_table(k);
+    load_chunk(k);
+    float cm = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) cm = fmaxf(cm, z[v][e]);
+    if (greedy) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (isnan(z[v][e])) sum = NAN;
+          const int x = first + k * L::kTokens + L::at(v, e);
+          if (z[v][e] == cm && (cm > m || (cm == m && x < best))) {
+            best = x;
+            m = cm;
+          }
+        }
+    }
+    const float nm = fmaxf(m, cm);
+    if (!greedy) {
+      const float ref = nm == -INFINITY ? 0.f : nm;
+      if (m != -INFINITY) sum *= exp2f((m - ref) * c);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (z[v][e] != -INFINITY) sum += exp2f((z[v][e] - ref) * c);
+    }
+    m = nm;
+  }
+  // Lanes, then warps, then CTAs, each time by (maximum, first token) and rescaled sums.
+  auto join = [&](float om, float os, int ob) {
+    const float nm = fmaxf(m, om);
+    const float ref = nm == -INFINITY ? 0.f : nm;
+    if (greedy) {
+      sum += os;
+    } else {
+      // The sum of a part without finite values is 0, or NaN.
+      sum = (m == -INFINITY ? sum : sum * exp2f((m - ref) * c)) +
+            (om == -INFINITY ? os : os * exp2f((om - ref) * c));
+    }
+    best = om > m || (om == m && ob < best) ? ob : best;
+    m = nm;
+  };
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    join(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o),
+         __shfl_xor_sync(0xffffffffu, best, o));
+  if (lane == 0) {
+    s.red_max[warp] = m;
+    s.red_sum[warp] = sum;
+    s.red_at[warp] = best;
+  }
+  __syncthreads();
+  if (!use_table) cluster_wait();
+  if (warp == 0) {
+    m = lane < kWarps ? s.red_max[lane] : -INFINITY;
+    sum = lane < kWarps ? s.red_sum[lane] : 0.f;
+    best = lane < kWarps ? s.red_at[lane] : 0x7fffffff;
+#pragma unroll
+    for (int o = kWarps / 2; o; o >>= 1)
+      join(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o),
+           __shfl_xor_sync(0xffffffffu, best, o));
+    if (lane < C) {
+      peer_store(peer_address(&s.peer_max[rank], lane), __float_as_uint(m));
+      peer_store(peer_address(&s.peer_sum[rank], lane), __float_as_uint(sum));
+      peer_store(peer_address(&s.peer_at[rank], lane), (uint32_t)best);
+    }
+  }
+  cluster_sync();
+  m = s.peer_max[0], sum = s.peer_sum[0], best = s.peer_at[0];
+  for (int r = 1; r < C; ++r) join(s.peer_max[r], s.peer_sum[r], s.peer_at[r]);
+
+  for (int k = 0; k < chunks; ++k) {
+    if (MULTI) {
+      if (use_table) make_table(k);
+      load_chunk(k);
+    }
+    const float inv = bad ? NAN : (m == -INFINITY && !isnan(sum) ? 0.f : 1.f / sum);
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float p;
+        if (greedy) {
+          const int x = first + k * L::kTokens + L::at(v, e);
+          p = isnan(sum) || bad ? NAN : (x == best && m != -INFINITY ? 1.f : 0.f);
+        } else {
+          p = z[v][e] == -INFINITY ? 0.f * inv : exp2f((z[v][e] - m) * c) * inv;
+        }
+        z[v][e] = p;
+      }
+    store_chunk(k);
+  }
+}
+
+namespace {
+
+bool misaligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0;
+}
+
+template <typename T, bool VEC, int NV, bool MULTI>
+int launch(Args& a, int rows, int cluster, cudaStream_t stream) {
+  constexpr int kTokens = Tile<T, VEC, NV>::kTokens;
+  const bool table = a.counted || a.max_bias > 0;
+  const size_t smem = table ? kTokens * 4 : 0;
+  static std::once_flag once[kMaxCachedDevices];
+  static cudaError_t attr_err[kMaxCachedDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxCachedDevices) return VAS_E_CUDA;
+  std::call_once(once[dev], [&] {
+    attr_err[dev] = cudaFuncSetAttribute(spec_logits_kernel<T, VEC, NV, MULTI>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kTokens * 4);
+  });
+  if (attr_err[dev] != cudaSuccess) return VAS_E_CUDA;
+  a.chunks = (a.slice + kTokens - 1) / kTokens;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(cluster * rows));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, spec_logits_kernel<T, VEC, NV, MULTI>, a) != cudaSuccess) {
+    cudaGetLastError();
+    return VAS_E_CUDA;
+  }
+  return VAS_OK;
+}
+
+template <typename T, bool VEC>
+int launch_size(Args& a, int rows, cudaStream_t stream) {
+  // As many CTAs a row as have at least 8 logits a thread, at most a portable cluster.
+  int cluster = (a.V + kThreads * 8 - 1) / (kThreads * 8);
+  if (cluster > kMaxCluster) cluster = kMaxCluster;
+  a.slice = ((a.V + cluster - 1) / cluster + 31) / 32 * 32;
+  a.cluster = cluster;
+  const int per = (a.slice + kThreads * 8 - 1) / (kThreads * 8);
+  if (per <= 1) return launch<T, VEC, 1, false>(a, rows, cluster, stream);
+  if (per <= 2) return launch<T, VEC, 2, false>(a, rows, cluster, stream);
+  if (per <= 4) return launch<T, VEC, 4, false>(a, rows, cluster, stream);
+  return launch<T, VEC, 4, true>(a, rows, cluster, stream);
+}
+
+}  // namespace
+}  // namespace logits
+}  // namespace vas
+
+extern "C" int spec_logits(const void* logits, const int32_t* tokens, const int32_t* token_lens,
+                           const int32_t* prompt_lens, const int32_t* draft_tokens,
+                           const int32_t* parents, const float* repetition, const float* frequency,
+                           const float* presence, const int32_t* bias_tokens, const float* bias,
+                           const uint32_t* mask, const float* temperature, float* out,
+                           const vas_logits_dims* dims, vas_stream_t stream) {
+  using namespace vas::logits;
+  if (!dims) return VAS_E_INVALID_ARG;
+  const vas_logits_dims& d = *dims;
+  if (d.num_seqs < 0 || d.num_drafts < 0 || d.num_drafts > kMaxNodes || d.vocab <= 0 ||
+      d.max_tokens < 0 || d.max_bias < 0)
+    return VAS_E_INVALID_ARG;
+  if (d.out_kind != VAS_LOGITS && d.out_kind != VAS_PROBS) return VAS_E_INVALID_ARG;
+  if ((d.dtype != VAS_F32 && d.dtype != VAS_BF16) || d.vocab > 1048576 ||
+      d.max_tokens >= kMaxTokens - kMaxNodes || d.max_bias > kMaxBias)
+    return VAS_E_UNSUPPORTED;
+  if (d.row_stride < d.vocab) return VAS_E_INVALID_ARG;
+  if (d.out_kind == VAS_LOGITS && temperature) return VAS_E_INVALID_ARG;
+  if ((tokens != nullptr) != (token_lens != nullptr) || (prompt_lens && !tokens)) return VAS_E_INVALID_ARG;
+  if ((bias_tokens != nullptr) != (bias != nullptr)) return VAS_E_INVALID_ARG;
+  if (parents && !draft_tokens) return VAS_E_INVALID_ARG;
+  if (d.num_seqs == 0) return VAS_OK;
+  if (!logits || !out) return VAS_E_INVALID_ARG;
+  const bool counted = repetition || frequency || presence;
+  if (counted && d.num_drafts > 0 && !draft_tokens) return VAS_E_INVALID_ARG;
+  const int es = d.dtype == VAS_F32 ? 4 : 2;
+  if (misaligned(logits, es) || misaligned(tokens, 4) || misaligned(token_lens, 4) ||
+      misaligned(prompt_lens, 4) || misaligned(draft_tokens, 4) || misaligned(parents, 4) ||
+      misaligned(repetition, 4) || misaligned(frequency, 4) || misaligned(presence, 4) ||
+      misaligned(bias_tokens, 4) || misaligned(bias, 4) || misaligned(mask, 4) ||
+      misaligned(temperature, 4) || misaligned(out, 4))
+    return VAS_E_INVALID_ARG;
+  const int64_t rows = (int64_t)d.num_seqs * (d.num_drafts + 1);
+  if (rows > INT32_MAX / kMaxCluster) return VAS_E_UNSUPPORTED;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(logits), y = reinterpret_cast<uintptr_t>(out);
+  const uintptr_t xn = (uintptr_t)(((rows - 1) * d.row_stride + d.vocab) * es);
+  const uintptr_t yn = (uintptr_t)(rows * d.vocab * 4);
+  if (x < y + yn && y < x + xn) return VAS_E_INVALID_ARG;  // read and written
+  Args a;
+  a.logits = logits;
+  a.tokens = tokens;
+  a.token_lens = token_lens;
+  a.prompt_lens = prompt_lens;
+  a.drafts = draft_tokens;
+  a.parents = parents;
+  a.repetition = repetition;
+  a.frequency = frequency;
+  a.presence = presence;
+  a.bias_tokens = bias_tokens;
+  a.bias = bias;
+  a.mask = mask;
+  a.temperature = temperature;
+  a.out = out;
+  a.row_stride = d.row_stride;
+  a.n = d.num_drafts;
+  a.V = d.vocab;
+  a.max_tokens = d.max_tokens;
+  a.max_bias = bias_tokens ? d.max_bias : 0;
+  a.mask_words = (d.vocab + 31) / 32;
+  a.probs = d.out_kind == VAS_PROBS;
+  a.counted = counted ? 1 : 0;
+  a.out_vec = !misaligned(out, 16) && d.vocab % 4 == 0;
+  a.err = vas::device_error_word();
+  if (!a.err) return VAS_E_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool vec = !misaligned(logits, 16) && d.row_stride * es % 16 == 0;
+  if (d.dtype == VAS_F32)
+    return vec ? launch_size<float, true>(a, (int)rows, st) : launch_size<float, false>(a, (int)rows, st);
+  return vec ? launch_size<__nv_bfloat16, true>(a, (int)rows, st)
+             : launch_size<__nv_bfloat16, false>(a, (int)rows, st);
+}

@@ -698,8 +698,9 @@ struct AttnArgs {
   float scale;
   int32_t* err;
   const uint64_t* tree_mask;  // draft-tree visibility per query token, or null (causal)
-  const float* k_scale;       // quantised pools: [num_pages, Hkv, P] fp32
-  const float* v_scale;
+  const float* k_scale;       // quantised pools: [num_pages, Hkv, P] fp32, or with
+  const float* v_scale;       // block_scale [num_pages, Hkv]
+  int32_t block_scale;
 };
 
 template <int D, int KQ = kKvBf16>
@@ -1630,6 +1631,12 @@ __global__ void __launch_bounds__(KQ == kKvBf16 ? kThreads : kThreadsQ, 1)
           const int npg = min(32, it.page_end - pg0);
           const int32_t my_id =
               pg0 == it.page_begin ? bt_cur : (lane < npg ? bt_row[pg0 + lane] : 0);
+          // One scale a page and head: those of up to 32 pages, one a lane.
+          float my_ks = 0.f, my_vs = 0.f;
+          if (kQuant && a.block_scale && lane < npg && my_id >= 0 && my_id < a.num_pages) {
+            my_ks = a.k_scale[(size_t)my_id * a.Hkv + head];
+            my_vs = a.v_scale[(size_t)my_id * a.Hkv + head];
+          }
           for (int s0 = 0; s0 < npg; s0 += PPS) {
             const int slot_s = stage_it % kSlots;
             ok = mbar_wait(&empty[slot_s], ((stage_it / kSlots) & 1) ^ 1);
@@ -1643,8 +1650,15 @@ __global__ void __launch_bounds__(KQ == kKvBf16 ? kThreads : kThreadsQ, 1)
               ids[e] = __shfl_sync(0xffffffffu, my_id, (s0 + e) & 31);
               if (e < n_in) {
                 if (ids[e] < 0 || ids[e] >= a.num_pages) bad = 1;
-                else bytes += kQuant ? 2u * (P * D + P * 4) : 2u * kPageBytes;
+                else bytes += kQuant ? 2u * (P * D + (a.block_scale ? 0 : P * 4)) : 2u * kPageBytes;
               }
+            }
+            if (kQuant && a.block_scale) {  // lane: token of the stage
+              const int src = (s0 + lane / P) & 31;
+              float* sc = stage_scales + slot_s * 2 * kStageTokens + lane;
+              sc[0] = __shfl_sync(0xffffffffu, my_ks, src);
+              sc[kStageTokens] = __shfl_sync(0xffffffffu, my_vs, src);
+              __syncwarp();
             }
             if (kQuant && lane == 0) {
               // Codes: one box per page and operand, [P tokens][D bytes], into the upper
@@ -1661,9 +1675,11 @@ __global__ void __launch_bounds__(KQ == kKvBf16 ? kThreads : kThreadsQ, 1)
                 if (e < n_in && ids[e] >= 0 && ids[e] < a.num_pages) {
                   tma_load_3d(kdst + e * P * D, &tm_k, &full[slot_s], 0, ids[e] * P, head, pol);
                   tma_load_3d(vdst + e * P * D, &tm_v, &full[slot_s], 0, ids[e] * P, head, pol);
-                  const size_t so = ((size_t)ids[e] * a.Hkv + head) * P;
-                  bulk_load(ksd + e * P, a.k_scale + so, P * 4, &full[slot_s], pol);
-                  bulk_load(vsd + e * P, a.v_scale + so, P * 4, &full[slot_s], pol);
+                  if (!a.block_scale) {
+                    const size_t so = ((size_t)ids[e] * a.Hkv + head) * P;
+                    bulk_load(ksd + e * P, a.k_scale + so, P * 4, &full[slot_s], pol);
+                    bulk_load(vsd + e * P, a.v_scale + so, P * 4, &full[slot_s], pol);
+                  }
                 }
               }
             }
@@ -2743,11 +2759,15 @@ bool dims_ok(const vas_attn_dims* d) {
 bool dims_supported(const vas_attn_dims* d) {
   return (d->head_dim == 64 || d->head_dim == 128) && (d->page_size == 16 || d->page_size == 32) &&
          (d->kv_dtype == VAS_BF16 || d->kv_dtype == VAS_F32 || d->kv_dtype == VAS_FP8_E4M3 ||
-          d->kv_dtype == VAS_INT8);
+          d->kv_dtype == VAS_INT8 || d->kv_dtype == VAS_FP8_BLOCK || d->kv_dtype == VAS_INT8_BLOCK);
+}
+
+bool kv_block(const vas_attn_dims* d) {
+  return d->kv_dtype == VAS_FP8_BLOCK || d->kv_dtype == VAS_INT8_BLOCK;
 }
 
 bool kv_quantized(const vas_attn_dims* d) {
-  return d->kv_dtype == VAS_FP8_E4M3 || d->kv_dtype == VAS_INT8;
+  return d->kv_dtype == VAS_FP8_E4M3 || d->kv_dtype == VAS_INT8 || kv_block(d);
 }
 
 int64_t items_min(const vas_attn_dims* d) {
@@ -2919,13 +2939,13 @@ size_t paged_attn_workspace_size(const vas_attn_dims* dims) {
 }
 
 size_t paged_attn_prefix_workspace_min(const vas_attn_dims* dims, int32_t num_groups) {
-  if (!dims_ok(dims) || !dims_supported(dims) || dims->kv_dtype == VAS_F32 || num_groups < 0)
+  if (!dims_ok(dims) || !dims_supported(dims) || dims->kv_dtype == VAS_F32 || kv_block(dims) || num_groups < 0)
     return 0;
   return make_layout(dims, items_min(dims), 0, num_groups).total;
 }
 
 size_t paged_attn_prefix_workspace_size(const vas_attn_dims* dims, int32_t num_groups) {
-  if (!dims_ok(dims) || !dims_supported(dims) || dims->kv_dtype == VAS_F32 || num_groups < 0)
+  if (!dims_ok(dims) || !dims_supported(dims) || dims->kv_dtype == VAS_F32 || kv_block(dims) || num_groups < 0)
     return 0;
   // Room for every row to be split 8 ways on average and, beside that, for the pieces of
   // shared prefixes: a CTA adds a piece to a block that others work on too, and a block's
@@ -3104,6 +3124,7 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
   aa.tree_mask = tree_mask;
   aa.k_scale = k_scale;
   aa.v_scale = v_scale;
+  aa.block_scale = kv_block(dims) ? 1 : 0;
 
   if (prefix) {
     PrefixArgs px;
@@ -3139,7 +3160,7 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
     const int grid = sms;
     int st;
     if (quant) {
-      const bool fp8 = d.kv_dtype == VAS_FP8_E4M3;
+      const bool fp8 = d.kv_dtype == VAS_FP8_E4M3 || d.kv_dtype == VAS_FP8_BLOCK;
       if (d.head_dim == 128 && d.page_size == 16)
         st = fp8 ? launch_bf16<128, 16, kKvFp8>(mk, mv, aa, grid, stream)
                  : launch_bf16<128, 16, kKvInt8>(mk, mv, aa, grid, stream);
@@ -3212,7 +3233,7 @@ int paged_attn_fwd_prefix(const void* q, const void* k_pages, const void* v_page
                           vas_stream_t stream) {
   if (!dims || num_groups < 0) return VAS_E_INVALID_ARG;
   if (share != VAS_SHARE_AUTO && share != VAS_SHARE_ALWAYS) return VAS_E_INVALID_ARG;
-  if (dims->kv_dtype == VAS_F32) return VAS_E_UNSUPPORTED;
+  if (dims->kv_dtype == VAS_F32 || kv_block(dims)) return VAS_E_UNSUPPORTED;
   if (num_groups > 0 && (!group_start || !prefix_lens)) return VAS_E_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(group_start) | reinterpret_cast<uintptr_t>(prefix_lens)) & 3)
     return VAS_E_INVALID_ARG;
