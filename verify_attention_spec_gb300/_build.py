@@ -17,8 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libvas.so")
 SOURCES = ["abi.cu", "paged_attn.cu", "spec_verify.cu", "spec_verify_tree.cu", "static_ws.cu",
-           "cache_ops.cu", "prefix_attn.cu", "block_cache.cu", "logits.cu", "pool.cpp"]
-HEADERS = ["append_rows.cuh", "attn_plan.cuh", "device_util.cuh", "packed_math.cuh", "philox.cuh",
+           "cache_ops.cu", "prefix_attn.cu", "block_attn.cu", "block_cache.cu", "logits.cu", "pool.cpp"]
+HEADERS = ["append_rows.cuh", "attn_plan.cuh", "block_attn.cuh", "device_util.cuh", "packed_math.cuh", "philox.cuh",
            "vas_internal.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,0 +1,1101 @@
+// Attention over block-scaled 8-bit pages (sm_103a): FP8 E4M3 codes with one fp32 scale per page
+// and KV head (paged_attn_fwd_quant with VAS_FP8_BLOCK).
+//
+// A unit is a block of query rows of one KV head against a run of its sequence's tokens, in tiles
+// of 128 tokens.  Both products run on the tensor cores with the codes as they are in memory:
+//     S^T = K Q^T    tokens are the M side (128 of them), the rows N, the head the contraction
+//     O^T = V^T P^T  head elements are M, the rows N, the tile's tokens the contraction
+// so no code is ever expanded, and decode's few rows waste nothing but tensor-core time of which
+// there is plenty: a tile is 32 KB of HBM, 1400 clocks of an SM's share, against 8 products of
+// about 96.  What is not 8 bits wide is split into parts that are:
+//   Q   a row times a power of two as hi + lo / 32, both E4M3 (8 bits, those of bf16), in columns
+//       of their own; S is their sum.
+//   P   as f16 and that as E5M2 parts in columns of their own: the upper byte of an f16 is its
+//       truncation to E5M2, the remainder is exact, and four parts hold all 11 bits (three hold 9:
+//       a row of few tokens, values near 4, was then 4e-3 off before its rounding to bf16).
+// With one scale a page, a tile's scales are at most 8 numbers, one a thread: K's multiplies the
+// scores, V's the weights.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "../../include/vas.h"
+#include "block_attn.cuh"
+#include "device_util.cuh"
+#include "packed_math.cuh"
+#include "vas_internal.h"
+
+namespace vas {
+namespace battn {
+namespace {
+
+constexpr int kTile = 128;         // tokens of a tile, one a softmax thread
+constexpr int kSoftWarps = 4;
+constexpr int kProducer = 4;       // warp that streams the pages
+constexpr int kMma = 5;            // warp that issues the products
+constexpr int kThreads = 192;
+constexpr int kCtasPerSm = 2;
+constexpr int kRing = 4;           // units the producer may run ahead
+constexpr int kScaleTiles = 8;     // tiles whose scales are kept
+constexpr int kParts = 4;          // E5M2 parts of a weight
+constexpr int kTmemCols = 256;
+constexpr int kTmemS = 0, kTmemO = 128;  // S: two buffers of 64 columns
+// A row's reference moves when a weight times its V scale passes 2^kSlack of it; kBase places
+// the weights so that the largest stay below 2^15 in f16, and those 2^-28 of it still count.
+constexpr float kSlack = 3.f;
+constexpr float kBase = 4096.f;
+constexpr float kNoMax = -1e30f;   // reference of a row that has seen nothing
+constexpr int kUnitCost = 128;     // what a unit costs beside its tokens, in tokens
+constexpr int kWholeTiles = 8;     // units of at most so many tiles are never cut
+constexpr int kMinShare = 4 * kTile;
+
+// A stretch of one unit, as the producer hands it on.
+struct Unit {
+  int32_t tile0, tile1;  // tile0 >= tile1: no more work
+  int32_t head, r0;      // KV head; first row, j0 * G + the first query head of it
+  int32_t rows;
+  int32_t row0;          // first query token of the sequence
+  int32_t len, ql;
+  int32_t part;          // partial slot, or -1: the whole unit
+  int32_t pad[3];
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kOperand = kTile * D;  // K or V of a tile
+  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int kQBytes = 2 * kMaxRows * D;
+  static constexpr int kPBytes = kTile * kMaxRows * kParts;
+  static constexpr int kQOff = kSlots * kOperand;
+  static constexpr int kPOff = kQOff + kQBytes;
+  static constexpr int kMiscOff = kPOff + 2 * kPBytes;
+  static_assert(kQOff % 1024 == 0 && kPOff % 128 == 0, "operand tiles");
+};
+
+struct Misc {
+  uint64_t full[8], empty[8];
+  uint64_t ufull[kRing], uempty[kRing];
+  uint64_t fin, q_full, s_full[2], s_empty[2], p_full[2], pv_done[2];
+  uint64_t tree[kMaxRows];        // the rows' draft-tree masks, own bit set
+  Unit ring[kRing];
+  float scales[kScaleTiles][2][8];
+  int32_t bad[kScaleTiles];       // a page of the tile is outside the pool
+  float row_scale[kMaxRows];      // of a row's scores, base-2
+  float ref[kMaxRows];            // reference of a row's weights
+  float warp_max[kSoftWarps][kMaxRows];
+  float warp_sum[kSoftWarps][kMaxRows];
+  int32_t limit[kMaxRows];        // last position a row sees
+  uint32_t tmem;
+  int32_t start_seq;
+  int64_t start_at;               // where in it this CTA's share begins
+  int64_t start_row;              // its first query token
+  int64_t wsum[6][2];
+  int32_t any_bad;
+};
+
+template <int D>
+constexpr int smem_bytes() {
+  return Smem<D>::kMiscOff + (int)sizeof(Misc) + 1024;
+}
+
+// ---- the line of work -----------------------------------------------------------------
+// All units of a call are one line: sequences one behind the other, in a sequence its KV heads,
+// in a head its blocks of query tokens, in such a block the parts of a group of more than 32
+// heads.  A unit's length on the line is its visible tokens (rounded) plus kUnitCost.  CTA k takes
+// [k share, (k + 1) share): all end together whatever the lengths, and no counter is needed.
+struct Shape {
+  int32_t L, ql;
+  int32_t tb, nb;     // query tokens of a block; blocks
+  int64_t base;       // cost of block b: base + b * tb
+  int64_t head_cost;  // of all blocks of a head
+};
+
+__device__ __forceinline__ Shape shape_of(const Args& a, int32_t L, int32_t ql, int64_t row0) {
+  Shape s;
+  s.L = L;
+  s.ql = ql;
+  s.nb = s.tb = 0;
+  s.base = s.head_cost = 0;
+  if (ql <= 0 || L < ql || (int64_t)L > (int64_t)a.maxp * a.P || row0 + ql > a.T) return s;
+  const int32_t most = a.parts > 1 ? 1 : kMaxRows / a.G;
+  s.nb = (ql + most - 1) / most;
+  s.tb = (ql + s.nb - 1) / s.nb;  // even blocks: 5 tokens of 8 heads are 3 + 2 and not 4 + 1
+  s.nb = (ql + s.tb - 1) / s.tb;
+  s.base = (int64_t)L - ql + s.tb + kUnitCost;
+  s.head_cost = a.parts * (s.nb * s.base + (int64_t)s.tb * ((int64_t)s.nb * (s.nb - 1) / 2));
+  return s;
+}
+
+__device__ __forceinline__ bool bad_lengths(const Args& a, int32_t L, int32_t ql) {
+  return ql < 0 || ql > a.T || L < ql || (int64_t)L > (int64_t)a.maxp * a.P;
+}
+
+// Tiles of block b (it sees the tokens up to its last row's), and where a cut at x of its cost
+// falls: the same for both CTAs that meet there.
+__device__ __forceinline__ int tiles_of(const Shape& s, int64_t b) {
+  const int64_t seen = (int64_t)s.L - s.ql + min((int64_t)s.ql, (b + 1) * s.tb);
+  return (int)((seen + kTile - 1) / kTile);
+}
+__device__ __forceinline__ int cut_at(int64_t x, int64_t cost, int tiles) {
+  if (x <= 0) return 0;
+  if (x >= cost) return tiles;
+  if (tiles <= kWholeTiles) return 2 * x < cost ? 0 : tiles;
+  return (int)(x * tiles / cost);
+}
+
+// Bounded wait of one lane or a whole warp; false ends the role.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) { return mbar_wait_fast(bar, parity); }
+
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+
+// Instruction descriptor: fp32 accumulator, A E4M3, B E4M3 or E5M2.
+__device__ __forceinline__ uint32_t idesc_f8(int m, int n, bool mn_major, bool b_e5m2) {
+  return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | (mn_major ? (1u << 15) | (1u << 16) : 0u) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// Shared-memory matrix descriptors: rows of D bytes, swizzled over their length, 8-row groups
+// 8 D apart; and the weights' layout (no swizzle, 16-byte columns of tokens, column blocks
+// kTile * 16 apart).
+template <int D>
+__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
+  const uint32_t lo = ((addr >> 4) & 0x3FFFu) | (1u << 16);
+  const uint32_t hi = ((8u * D) >> 4) | (1u << 14) | ((D == 128 ? 2u : 4u) << 29);
+  return ((uint64_t)hi << 32) | lo;
+}
+__device__ __forceinline__ uint64_t desc_weights(uint32_t addr) {
+  const uint32_t lo = ((addr >> 4) & 0x3FFFu) | ((128u >> 4) << 16);
+  const uint32_t hi = ((kTile * 16u) >> 4) | (1u << 14);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
+  static_assert(N == 8 || N == 16 || N == 32, "columns of a load");
+  if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr)
+                 : "memory");
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+  }
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t prmt_odd(uint32_t a, uint32_t b) {  // bytes 1, 3 of a, 1, 3 of b
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, 0x7531;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Order of floats as order of ints, for the warp-wide maximum.
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x);
+  return i >= 0 ? i : i ^ 0x7fffffff;
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
+
+// Rows a unit is computed as (RP >= its rows).
+__device__ __forceinline__ int padded_rows(int rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 32); }
+
+template <int D>
+struct Ctx {
+  const Args& a;
+  uint8_t* smem;
+  Misc& m;
+  uint32_t tmem;
+  int warp, lane;
+};
+
+// ---- softmax warps -------------------------------------------------------------------
+// The unit's queries as E4M3 pairs in the K-major operand layout; the rows' scales, references,
+// limits and masks.
+template <int D, int RP>
+__device__ __forceinline__ void stage_queries(const Ctx<D>& x, const Unit& u) {
+  const Args& a = x.a;
+  Misc& m = x.m;
+  constexpr int kLanes = D / 8;             // of a row, 8 elements each
+  constexpr int kRowsAtOnce = 128 / kLanes;
+  const int tid = threadIdx.x, c = tid % kLanes;
+  uint8_t* q_tile = x.smem + Smem<D>::kQOff;
+  uint4 v[(RP + kRowsAtOnce - 1) / kRowsAtOnce];
+#pragma unroll
+  for (int i = 0; i < (RP + kRowsAtOnce - 1) / kRowsAtOnce; ++i) {
+    const int r = i * kRowsAtOnce + tid / kLanes;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (r < u.rows) {
+      const int g = u.r0 + r, j = g / a.G, h = g - j * a.G;
+      v[i] = *(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                              ((size_t)(u.row0 + j) * a.Hq + (size_t)u.head * a.G + h) * D) + c);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < (RP + kRowsAtOnce - 1) / kRowsAtOnce; ++i) {
+    const int r = i * kRowsAtOnce + tid / kLanes;
+    float top = absmax_bf16x8(v[i]);
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // 2^e brings the row's largest magnitude into [128, 256): a half step of hi is then at most
+    // 8, and its remainder times 32 is exact in E4M3 for elements down to 2^-15 of the largest.
+    const int e = max(-120, min(120, 7 - ((int)(__float_as_uint(top) >> 23) - 127)));
+    const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    uint32_t hi[2], lo[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float y[4] = {bf16_lo_f32(w[2 * k]) * mul, bf16_hi_f32(w[2 * k]) * mul,
+                    bf16_lo_f32(w[2 * k + 1]) * mul, bf16_hi_f32(w[2 * k + 1]) * mul};
+#pragma unroll
+      for (int f = 0; f < 4; ++f) y[f] += y[f] - y[f];  // an infinity becomes NaN, not 448
+      auto pack = [](const float (&z)[4]) {
+        uint32_t p;
+        asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+            "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
+            : "=r"(p)
+            : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
+        return p;
+      };
+      hi[k] = pack(y);
+      uint32_t f0, f1;
+      float b[4];
+      e4m3x4_to_f16x4(hi[k], f0, f1);
+      f16x2_to_f32(f0, b[0], b[1]);
+      f16x2_to_f32(f1, b[2], b[3]);
+#pragma unroll
+      for (int f = 0; f < 4; ++f) b[f] = (y[f] - b[f]) * 32.f;
+      lo[k] = pack(b);
+    }
+    if (RP % kRowsAtOnce == 0 || r < RP) {
+      // Row n of the operand: rows of D bytes, 16-byte chunks swizzled by the row.
+      auto at = [&](int n) {
+        const uint32_t off = (uint32_t)n * D + c * 8;
+        return q_tile + (off ^ (((off >> 7) & (D == 128 ? 7 : 3)) << 4));
+      };
+      *reinterpret_cast<uint2*>(at(r)) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(at(RP + r)) = make_uint2(lo[0], lo[1]);
+      if (c == 0) {
+        m.row_scale[r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+        m.ref[r] = kNoMax;
+        const int j = min((u.r0 + r) / a.G, u.ql - 1);
+        m.limit[r] = r < u.rows ? u.len - u.ql + j : -1;
+        const bool tree = a.tree_mask && u.ql > 1 && u.ql <= 64;
+        m.tree[r] = tree ? (a.tree_mask[u.row0 + j] & (j ? ~0ull >> (64 - j) : 0ull)) | (1ull << j) : ~0ull;
+      }
+    }
+  }
+}
+
+// One unit; false after a wait that ran out.  Such a warp waits no more but keeps to the barriers
+// of the others, which leave with it at the end of the unit.
+template <int D, int RP>
+__device__ __forceinline__ bool soft_unit(const Ctx<D>& x, const Unit& u, uint32_t& tile_it) {
+  constexpr int kN = RP * kParts;       // columns of O
+  using S = Smem<D>;
+  const Args& a = x.a;
+  Misc& m = x.m;
+  const int tid = threadIdx.x, warp = x.warp, lane = x.lane;
+  const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+
+  stage_queries<D, RP>(x, u);
+  fence_proxy_async_smem();
+  named_bar_sync(1, 128);  // the rows' numbers are read by all
+  if (tid == 0) mbar_arrive(&m.q_full);
+
+  float l[RP];
+#pragma unroll
+  for (int r = 0; r < RP; ++r) l[r] = 0.f;
+  bool bad = false, poison = false, ok = true;
+  auto wait_for = [&](uint64_t* bar, uint32_t parity) {
+    if (ok) ok = wait(bar, parity);
+  };
+  const int ctx = u.len - u.ql;
+  // The positions every row of the unit sees end here.
+  const bool tree = a.tree_mask && u.ql > 1 && u.ql <= 64;
+  const int seen_by_all = tree ? ctx - 1 : ctx + u.r0 / a.G;
+
+  for (int tile = u.tile0; tile < u.tile1; ++tile, ++tile_it) {
+    const int b = tile_it & 1;
+    const int slot_v = (2 * tile_it + 1) % S::kSlots;
+    wait_for(&m.full[slot_v], ((2 * tile_it + 1) / S::kSlots) & 1);
+    const int st = tile_it % kScaleTiles;
+    const float vs = m.scales[st][1][tid >> a.log2P];
+    const float ks = m.scales[st][0][tid >> a.log2P] + (vs - vs);  // a V scale that is not finite: NaN
+    bad |= m.bad[st] != 0;
+    const int pos = tile * kTile + tid;
+    const bool masked = tile * kTile + kTile - 1 > seen_by_all;
+    if (masked) {
+      // V rows that a weight of zero would not silence: slots of no token may hold NaN, and a
+      // token of the window may be NaN for the rows that do not see it.
+      uint8_t* v_row = x.smem + slot_v * S::kOperand + tid * D;
+      bool clear = pos >= u.len;
+      if (!clear && pos > seen_by_all) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint4 w = reinterpret_cast<const uint4*>(v_row)[i];
+          const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            poison |= __vcmpeq4(q[k] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+        }
+        clear = poison;
+      }
+      if (clear) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) reinterpret_cast<uint4*>(v_row)[i] = make_uint4(0, 0, 0, 0);
+      }
+      if (pos >= u.len) poison = false;
+    }
+    // Exponent of the token's V scale, |vs| < 2^ve.
+    const float ve = (float)max(-60, min(67, (int)((__float_as_uint(vs) >> 23) & 0xff) - 126));
+
+    wait_for(&m.s_full[b], (tile_it >> 1) & 1);
+    tc_fence_after();
+    float s[RP];
+    {
+      const uint32_t at = x.tmem + lanes + kTmemS + 64 * b;
+      constexpr int kLd = RP < 16 ? RP : 16;
+#pragma unroll
+      for (int r0 = 0; r0 < RP; r0 += kLd) {
+        uint32_t hi[kLd], lo[kLd];
+        tmem_ld<kLd>(at + r0, hi);
+        tmem_ld<kLd>(at + RP + r0, lo);
+        tmem_wait_ld();
+#pragma unroll
+        for (int r = 0; r < kLd; ++r)
+          s[r0 + r] = fmaf(__uint_as_float(lo[r]), 1.f / 32, __uint_as_float(hi[r])) * ks;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.s_empty[b]);
+    }
+    bool up = false;
+    auto dropped = [&](int r) {
+      if (pos > m.limit[r]) return true;
+      const int j = pos - ctx;
+      return tree && j >= 0 && !((m.tree[r] >> j) & 1);
+    };
+#pragma unroll
+    for (int r = 0; r < RP; ++r) {
+      s[r] *= m.row_scale[r];
+      if (masked && dropped(r)) s[r] = -INFINITY;
+      up |= s[r] + ve > m.ref[r] + kSlack;
+    }
+    if (named_bar_or(1, 128, up)) {
+      // Some weight outgrew its row's reference: the tile's maxima, and O in the new one.
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        const float v = s[r] == -INFINITY ? -INFINITY : s[r] + ve;
+        const int top = __reduce_max_sync(0xffffffffu, isnan(v) ? INT_MIN : ordered(v));
+        if (lane == 0) m.warp_max[warp][r] = top == INT_MIN ? -INFINITY : unordered(top);
+      }
+      named_bar_sync(1, 128);
+      const bool have_o = tile > u.tile0;
+      if (have_o) wait_for(&m.pv_done[b ^ 1], ((tile_it - 1) >> 1) & 1);
+      tc_fence_after();
+      float alpha[RP];
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        const float top = fmaxf(fmaxf(m.warp_max[0][r], m.warp_max[1][r]),
+                                fmaxf(m.warp_max[2][r], m.warp_max[3][r]));
+        const float old = m.ref[r];
+        alpha[r] = top > old + kSlack ? ex2_approx(old - top) : 1.f;
+        l[r] *= alpha[r];
+      }
+      if (have_o) {
+#pragma unroll
+        for (int c0 = 0; c0 < kN; c0 += 16) {
+          const uint32_t at = x.tmem + lanes + kTmemO + c0;
+          uint32_t o[16];
+          tmem_ld<16>(at, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[(c0 + c) % RP]);
+          tmem_st16(at, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+      }
+      named_bar_sync(1, 128);  // every thread has read the old references
+      if (tid < RP) {
+        const float top = fmaxf(fmaxf(m.warp_max[0][tid], m.warp_max[1][tid]),
+                                fmaxf(m.warp_max[2][tid], m.warp_max[3][tid]));
+        if (top > m.ref[tid] + kSlack) m.ref[tid] = top;
+      }
+      named_bar_sync(1, 128);
+    }
+    // Weights, their sums, and their parts as bytes.
+    const float vb = vs * kBase;
+    uint32_t part[kParts][RP / 4];
+#pragma unroll
+    for (int r = 0; r < RP; r += 4) {
+      uint32_t h[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float p[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int q = r + 2 * k + f;
+          p[f] = ex2_approx(s[q] - m.ref[q]);
+          if (masked && poison && s[q] != -INFINITY) p[f] = NAN;
+          l[q] += p[f];
+          p[f] = s[q] == -INFINITY ? 0.f : p[f] * vb;
+        }
+        h[k] = pack_f16x2(p[0], p[1]);
+        if (masked && poison) h[k] = 0;  // the row's NaN is in its sum
+      }
+#pragma unroll
+      for (int t = 0; t < kParts; ++t) {
+        part[t][r / 4] = prmt_odd(h[0], h[1]);
+        h[0] = sub_f16x2(h[0], h[0] & 0xff00ff00u);
+        h[1] = sub_f16x2(h[1], h[1] & 0xff00ff00u);
+      }
+    }
+    poison = false;
+    // The weights' buffer is free once the product of two tiles ago is done.
+    if (tile >= u.tile0 + 2) wait_for(&m.pv_done[b], ((tile_it - 2) >> 1) & 1);
+    uint8_t* p_tile = x.smem + S::kPOff + b * S::kPBytes + tid * 16;
+#pragma unroll
+    for (int n = 0; n < kN / 16; ++n) {  // 16 columns: part n * 16 / RP, rows (n * 16) % RP on
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = part[(16 * n + 4 * k) / RP][(16 * n + 4 * k) % RP / 4];
+      *reinterpret_cast<uint4*>(p_tile + n * (kTile * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&m.p_full[b]);
+  }
+
+  // The rows' sums over the threads, and the last product.
+#pragma unroll
+  for (int r = 0; r < RP; ++r) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+    if (lane == 0) m.warp_sum[warp][r] = l[r];
+  }
+  wait_for(&m.pv_done[(tile_it - 1) & 1], ((tile_it - 1) >> 1) & 1);
+  tc_fence_after();
+  named_bar_sync(1, 128);
+  const bool mine = D == 128 || lane < 16;  // D = 64: 16 rows of O^T a warp
+  const int d = D == 128 ? tid : 16 * warp + lane;
+  constexpr int kAt = RP < 16 ? RP : 16;
+#pragma unroll
+  for (int r0 = 0; r0 < RP; r0 += kAt) {
+    float o[kAt];
+#pragma unroll
+    for (int t = 0; t < kParts; ++t) {
+      uint32_t w[kAt];
+      tmem_ld<kAt>(x.tmem + lanes + kTmemO + t * RP + r0, w);
+      tmem_wait_ld();
+#pragma unroll
+      for (int r = 0; r < kAt; ++r) o[r] = t ? o[r] + __uint_as_float(w[r]) : __uint_as_float(w[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < kAt; ++r) {
+      const int q = r0 + r;
+      if (q >= u.rows) break;
+      const float sum = (m.warp_sum[0][q] + m.warp_sum[1][q]) + (m.warp_sum[2][q] + m.warp_sum[3][q]);
+      float y = sum == 0.f ? 0.f : o[r] / sum * (1.f / kBase);
+      float lse2 = sum == 0.f ? -INFINITY : m.ref[q] + log2f(sum);
+      if (bad || isnan(sum)) y = lse2 = NAN;
+      if (u.part >= 0) {
+        const size_t row = (size_t)u.part * kMaxRows + q;
+        if (mine) a.part_o[row * D + d] = y;
+        if (tid == 0) a.part_lse[row] = lse2;
+      } else {
+        const int g = u.r0 + q, j = g / a.G, h = g - j * a.G;
+        const size_t row = (size_t)(u.row0 + j) * a.Hq + (size_t)u.head * a.G + h;
+        if (mine) static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16(y);
+        if (tid == 0) a.lse[row] = lse2 * 0.6931471805599453f;
+      }
+    }
+  }
+  tc_fence_before();
+  if (bad && tid == 0) atomicOr(a.err, VAS_DEV_BAD_PAGE);
+  return !named_bar_or(1, 128, !ok);  // the rows' numbers may be overwritten
+}
+
+// ---- the CTA's share -------------------------------------------------------------------
+// All threads: totals of the call, the share, and where it begins.  The CTA 0 also reports
+// inconsistent lengths and fills the rows of no valid sequence with NaN.
+template <int D>
+__device__ __forceinline__ int64_t find_share(const Args& a, Misc& m, int64_t* end) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (a.B + kThreads - 1) / kThreads;
+  const int i0 = min(a.B, tid * per), i1 = min(a.B, i0 + per);
+  auto scan = [&](int64_t v, int k) {  // exclusive over the threads; the total in *end
+    int64_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t n = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += n;
+    }
+    if (lane == 31) m.wsum[warp][k] = inc;
+    __syncthreads();
+    int64_t base = inc - v, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) base += m.wsum[w][k];
+      total += m.wsum[w][k];
+    }
+    *end = total;
+    return base;
+  };
+  int64_t rows = 0;
+  bool bad = false;
+  for (int i = i0; i < i1; ++i) {
+    const int32_t ql = a.query_lens[i];
+    rows += max(ql, 0);
+    if (blockIdx.x == 0) bad |= bad_lengths(a, a.seq_lens[i], ql);
+  }
+  int64_t total_rows, total;
+  const int64_t row0 = scan(rows, 0);
+  total_rows = *end;
+  int64_t cost = 0, row = row0;
+  for (int i = i0; i < i1; ++i) {
+    const Shape s = shape_of(a, a.seq_lens[i], a.query_lens[i], row);
+    cost += s.head_cost * a.Hkv;
+    row += max(s.ql, 0);
+  }
+  const int64_t cost0 = scan(cost, 1);
+  total = *end;
+  int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  if (share < kMinShare) share = kMinShare;
+  const int64_t first = share * blockIdx.x;
+  if (cost0 <= first && first < cost0 + cost) {
+    int64_t at = cost0;
+    row = row0;
+    for (int i = i0; i < i1; ++i) {
+      const Shape s = shape_of(a, a.seq_lens[i], a.query_lens[i], row);
+      const int64_t c = s.head_cost * a.Hkv;
+      if (first < at + c) {
+        m.start_seq = i;
+        m.start_at = first - at;
+        m.start_row = row;
+        break;
+      }
+      at += c;
+      row += max(s.ql, 0);
+    }
+  }
+  if (blockIdx.x == 0) {
+    if (tid == 0) m.any_bad = 0;
+    __syncthreads();
+    if (bad || total_rows != a.T) m.any_bad = 1;
+    __syncthreads();
+    if (m.any_bad) {
+      if (tid == 0) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
+      auto fill = [&](int64_t t0, int64_t t1) {
+        for (int64_t t = t0; t < t1 && t < a.T; ++t)
+          for (int h = 0; h < a.Hq; ++h) {
+            const size_t r = (size_t)t * a.Hq + h;
+            a.lse[r] = NAN;
+            for (int d = 0; d < D; ++d)
+              static_cast<__nv_bfloat16*>(a.out)[r * D + d] = __float2bfloat16(NAN);
+          }
+      };
+      row = row0;
+      for (int i = i0; i < i1; ++i) {
+        const int32_t ql = a.query_lens[i];
+        if (ql > 0 && shape_of(a, a.seq_lens[i], ql, row).nb == 0) fill(row, row + ql);
+        row += max(ql, 0);
+      }
+      for (int64_t t = total_rows + tid; t < a.T; t += kThreads) fill(t, t + 1);
+    }
+  }
+  __syncthreads();
+  *end = min(total, first + share);
+  return first;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    block_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const Args a) {
+  using S = Smem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Misc& m = *reinterpret_cast<Misc*>(smem + S::kMiscOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&m.full[i], 1);
+      mbar_init(&m.empty[i], 1);
+    }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&m.ufull[i], 1);
+      mbar_init(&m.uempty[i], kSoftWarps + 1);
+    }
+    mbar_init(&m.q_full, 1);
+    mbar_init(&m.fin, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m.s_full[i], 1);
+      mbar_init(&m.s_empty[i], kSoftWarps);
+      mbar_init(&m.p_full[i], kSoftWarps);
+      mbar_init(&m.pv_done[i], 1);
+    }
+    mbar_fence_init();
+  }
+  if (warp == kProducer && lane == 0) {
+    prefetch_tensor_map(&tm_k);
+    prefetch_tensor_map(&tm_v);
+  }
+  if (warp == 0) tmem_alloc(&m.tmem, kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const Ctx<D> x{a, smem, m, m.tmem, warp, lane};
+  pdl_wait_prior_grid();
+  int64_t end;
+  const int64_t first = find_share<D>(a, m, &end);
+  bool ok = true;
+
+  if (warp == kProducer) {
+    // ---- producer: walks the share, posts its units and streams their pages ----
+    const uint64_t pol_once = l2_policy_evict_first(), pol_shared = l2_policy_evict_normal();
+    uint32_t unit_it = 0, tile_it = 0;  // a tile takes two slots: K, then V
+    Record rec[2] = {{-1, 0, 0, 0, 0, 0, 0, 0}, {-1, 0, 0, 0, 0, 0, 0, 0}};
+    int64_t pos = first, row = 0, in_seq = 0;
+    int seq = 0;
+    if (pos < end) {
+      seq = m.start_seq;
+      in_seq = m.start_at;
+      row = m.start_row;
+    }
+    while (pos < end && ok) {
+      const Shape s = shape_of(a, a.seq_lens[seq], a.query_lens[seq], row);
+      const int64_t seq_cost = s.head_cost * a.Hkv;
+      if (in_seq >= seq_cost) {
+        row += max(s.ql, 0);
+        in_seq -= seq_cost;
+        ++seq;
+        continue;
+      }
+      // The unit that holds in_seq: head, block, part.
+      const int head = (int)(in_seq / s.head_cost);
+      const int64_t in_head = in_seq - head * s.head_cost;
+      auto block_start = [&](int64_t b) { return a.parts * (b * s.base + (int64_t)s.tb * (b * (b - 1) / 2)); };
+      int64_t lo = 0, hi = s.nb - 1;
+      while (lo < hi) {  // the last block that starts at or before in_head
+        const int64_t mid = (lo + hi + 1) >> 1;
+        if (block_start(mid) <= in_head) lo = mid;
+        else hi = mid - 1;
+      }
+      int64_t b = lo;
+      const int64_t cost0 = s.base + b * s.tb;
+      int part = (int)((in_head - block_start(b)) / cost0);
+      int64_t off = in_head - block_start(b) - part * cost0;  // of the share's place in the unit
+      const int32_t* bt_row = a.block_table + (size_t)seq * a.maxp;
+      // From here on unit by unit through the head.
+      for (; b < s.nb && pos < end && ok;) {
+        const int64_t cost = s.base + b * s.tb;
+        const int tiles = tiles_of(s, b);
+        const int t0 = cut_at(off, cost, tiles), t1 = cut_at(off + (end - pos), cost, tiles);
+        const int64_t step = min(cost - off, end - pos);
+        const int j0 = (int)(b * s.tb), nj = min(s.tb, s.ql - j0);
+        Unit u;
+        u.tile0 = t0;
+        u.tile1 = t1;
+        u.head = head;
+        u.rows = a.parts > 1 ? min(a.part_rows, a.G - part * a.part_rows) : nj * a.G;
+        u.r0 = j0 * a.G + part * a.part_rows;
+        u.row0 = (int)row;
+        u.len = s.L;
+        u.ql = s.ql;
+        u.part = -1;
+        if (t0 > 0 || t1 < tiles) {
+          const int w = t0 > 0 ? 0 : 1;
+          u.part = 2 * blockIdx.x + w;
+          if (t0 < tiles && t1 > 0)
+            rec[w] = {head, u.r0, u.rows, u.row0, t0 == 0, t1 < tiles, t0 == t1, 0};
+        }
+        pos += step;
+        in_seq += step;
+        off = 0;
+        if (t0 < t1) {
+          const int slot_u = unit_it % kRing;
+          ok = wait(&m.uempty[slot_u], ((unit_it / kRing) & 1) ^ 1);
+          if (!ok) break;
+          if (lane == 0) {
+            m.ring[slot_u] = u;
+            mbar_arrive(&m.ufull[slot_u]);
+          }
+          __syncwarp();
+          ++unit_it;
+          const int per_tile = kTile >> a.log2P;
+          const int n_pages = (s.L + a.P - 1) >> a.log2P;
+          const uint64_t pol = s.nb > 1 ? pol_shared : pol_once;
+          const int p_end = min(t1 * per_tile, n_pages);
+          int next_id = 0;
+          {
+            const int p = t0 * per_tile + lane;
+            if (p < p_end) next_id = bt_row[p];
+          }
+          for (int tc = t0; tc < t1 && ok; tc += 32 / per_tile) {
+            // Up to 32 pages: their numbers, one a lane, and scales; the next ones on their way.
+            const int p0 = tc * per_tile;
+            const int id = next_id;
+            const bool has = p0 + lane < p_end;
+            const bool good = has && id >= 0 && id < a.num_pages;
+            float ks = 0.f, vs = 0.f;
+            if (good) {
+              ks = a.k_scale[(size_t)id * a.Hkv + head];
+              vs = a.v_scale[(size_t)id * a.Hkv + head];
+            }
+            if (p0 + 32 + lane < p_end) next_id = bt_row[p0 + 32 + lane];
+            const uint32_t wrong = __ballot_sync(0xffffffffu, has && !good);
+            const uint32_t right = __ballot_sync(0xffffffffu, good);
+            for (int t = tc; t < min(t1, tc + 32 / per_tile); ++t, ++tile_it) {
+              const int l0 = (t - tc) * per_tile;
+              const uint32_t in_tile = ((1u << per_tile) - 1) << l0;
+              const bool my = ((in_tile >> lane) & 1) && good;
+              const uint32_t bytes = (uint32_t)__popc(right & in_tile) * a.P * D;
+              const int st = tile_it % kScaleTiles;
+#pragma unroll
+              for (int o = 0; o < 2; ++o) {
+                const uint32_t it = 2 * tile_it + o;
+                const int slot = it % S::kSlots;
+                ok = wait(&m.empty[slot], ((it / S::kSlots) & 1) ^ 1);
+                if (!ok) break;
+                if ((in_tile >> lane) & 1) m.scales[st][o][lane - l0] = o ? vs : ks;
+                if (lane == 0 && o == 0) m.bad[st] = (wrong & in_tile) != 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(&m.full[slot], bytes);
+                __syncwarp();
+                if (my)
+                  tma_load_3d(smem + slot * S::kOperand + (lane - l0) * a.P * D, o ? &tm_v : &tm_k, &m.full[slot],
+                              0, id * a.P, head, pol);
+              }
+              if (!ok) break;
+            }
+          }
+        }
+        if (++part >= a.parts) {
+          part = 0;
+          ++b;
+        }
+      }
+    }
+    if (ok) {
+      const int slot_u = unit_it % kRing;
+      ok = wait(&m.uempty[slot_u], ((unit_it / kRing) & 1) ^ 1);
+      if (ok && lane == 0) {
+        m.ring[slot_u].tile0 = m.ring[slot_u].tile1 = 0;
+        mbar_arrive(&m.ufull[slot_u]);
+      }
+    }
+    if (lane < 2) a.records[2 * blockIdx.x + lane] = rec[lane];
+    // Every copy has landed before the CTA can end.
+    for (uint32_t it = 2 * tile_it > S::kSlots ? 2 * tile_it - S::kSlots : 0; it < 2 * tile_it; ++it)
+      mbar_wait(&m.full[it % S::kSlots], (it / S::kSlots) & 1);
+  } else if (warp == kMma) {
+    // ---- products: one lane ----
+    if (lane == 0) {
+      uint32_t unit_it = 0, tile_it = 0;
+      const uint32_t ring_at = smem_u32(smem);
+      const uint64_t q_desc = desc_rows<D>(smem_u32(smem + S::kQOff));
+      auto scores = [&](uint32_t it, uint32_t idesc) {
+        const uint32_t k_it = 2 * it;
+        const int slot = k_it % S::kSlots, b = it & 1;
+        if (!wait(&m.full[slot], (k_it / S::kSlots) & 1)) return false;
+        if (!wait(&m.s_empty[b], ((it >> 1) & 1) ^ 1)) return false;
+        tc_fence_after();
+        const uint64_t k_desc = desc_rows<D>(ring_at + slot * S::kOperand);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+          mma_f8(x.tmem + kTmemS + 64 * b, k_desc + 2 * k, q_desc + 2 * k, idesc, k > 0);
+        umma_commit(&m.empty[slot]);
+        umma_commit(&m.s_full[b]);
+        return true;
+      };
+      for (;;) {
+        const int slot_u = unit_it % kRing;
+        ok = wait(&m.ufull[slot_u], (unit_it / kRing) & 1);
+        if (!ok) break;
+        const int tile0 = m.ring[slot_u].tile0, tile1 = m.ring[slot_u].tile1, rows = m.ring[slot_u].rows;
+        mbar_arrive(&m.uempty[slot_u]);
+        if (tile0 >= tile1) break;
+        const int rp = padded_rows(rows);
+        const uint32_t id_s = idesc_f8(128, 2 * rp, false, false);
+        const uint32_t id_o = idesc_f8(D, kParts * rp, true, true);
+        ok = wait(&m.q_full, unit_it & 1);
+        ++unit_it;
+        if (!ok) break;
+        tc_fence_after();
+        const int n = tile1 - tile0;
+        ok = scores(tile_it, id_s);
+        for (int i = 0; i < n && ok; ++i, ++tile_it) {
+          if (i + 1 < n) ok = scores(tile_it + 1, id_s);
+          if (!ok) break;
+          const uint32_t v_it = 2 * tile_it + 1;
+          const int slot = v_it % S::kSlots, b = tile_it & 1;
+          ok = wait(&m.full[slot], (v_it / S::kSlots) & 1) && wait(&m.p_full[b], (tile_it >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t v_desc = desc_rows<D>(ring_at + slot * S::kOperand);
+          const uint64_t p_desc = desc_weights(smem_u32(smem + S::kPOff + b * S::kPBytes));
+#pragma unroll
+          for (int k = 0; k < kTile / 32; ++k)
+            mma_f8(x.tmem + kTmemO, v_desc + ((32 * D * k) >> 4), p_desc + ((512 * k) >> 4), id_o, i > 0 || k > 0);
+          umma_commit(&m.empty[slot]);
+          umma_commit(&m.pv_done[b]);
+        }
+        if (!ok) break;
+      }
+      // Products in flight end before the tensor memory is freed.
+      umma_commit(&m.fin);
+      mbar_wait(&m.fin, 0);
+    }
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+  } else {
+    // ---- softmax ----
+    uint32_t unit_it = 0, tile_it = 0;
+    for (;;) {
+      const int slot_u = unit_it % kRing;
+      ok = !named_bar_or(1, 128, !wait(&m.ufull[slot_u], (unit_it / kRing) & 1));
+      if (!ok) break;
+      const Unit u = m.ring[slot_u];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.uempty[slot_u]);
+      ++unit_it;
+      if (u.tile0 >= u.tile1) break;
+      if (u.rows <= 8) ok = soft_unit<D, 8>(x, u, tile_it);
+      else if (u.rows <= 16) ok = soft_unit<D, 16>(x, u, tile_it);
+      else ok = soft_unit<D, 32>(x, u, tile_it);
+      if (!ok) break;
+    }
+  }
+  if (!ok && lane == 0) atomicOr(a.err, VAS_DEV_TIMEOUT);
+  pdl_launch_dependents();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(x.tmem, kTmemCols);
+}
+
+// ---- merge ------------------------------------------------------------------------------
+// The units that were cut: block (k, y) takes rows y, y + gridDim.y * 4, ... of the unit that
+// begins in CTA k's share and goes on; its pieces are CTA k's second partial and the first
+// partials of the CTAs behind it.  A warp a row.
+constexpr int kMergeThreads = 128;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Args a, int ctas) {
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  const int k = blockIdx.x, lane = threadIdx.x & 31;
+  const Record head = a.records[2 * k + 1];
+  if (head.head < 0 || !head.begins) return;
+  // Pieces: CTAs k .. k + n - 1.
+  int n = 1;
+  for (;; n += 32) {
+    const int c = k + n + lane;
+    const bool ends = c >= ctas || a.records[2 * c].head < 0 || !a.records[2 * c].goes_on;
+    const uint32_t e = __ballot_sync(0xffffffffu, ends);
+    if (e) {
+      const int c0 = k + n + __ffs(e) - 1;
+      n = c0 - k + (c0 < ctas && a.records[2 * c0].head >= 0 ? 1 : 0);
+      break;
+    }
+  }
+  auto piece = [&](int p) { return (size_t)(p == 0 ? 2 * k + 1 : 2 * (k + p)) * kMaxRows; };
+  constexpr int E = D / 32;
+  for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < head.rows; r += gridDim.y * 4) {
+    float mx = -INFINITY;
+    bool bad = false;
+    for (int p = lane; p < n; p += 32) {
+      if (p && a.records[2 * (k + p)].empty) continue;
+      const float v = a.part_lse[piece(p) + r];
+      bad |= isnan(v);
+      mx = fmaxf(mx, v);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    bad = __any_sync(0xffffffffu, bad);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int p0 = 0; p0 < n; p0 += 32) {
+      float w = 0.f;
+      if (p0 + lane < n && !(p0 + lane && a.records[2 * (k + p0 + lane)].empty))
+        w = exp2f(a.part_lse[piece(p0 + lane) + r] - ref);
+      for (int p = p0; p < min(n, p0 + 32); ++p) {
+        const float ws = __shfl_sync(0xffffffffu, w, p - p0);
+        if (ws == 0.f) continue;  // nothing of the row, or an empty piece
+        sum += ws;
+        const float* o = a.part_o + (piece(p) + r) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(ws, o[e], acc[e]);
+      }
+    }
+    const int g = head.r0 + r, j = g / a.G, h = g - j * a.G;
+    const size_t row = (size_t)(head.row0 + j) * a.Hq + (size_t)head.head * a.G + h;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row * D + lane * E;
+    const float inv = 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < E; e += 2)
+      *reinterpret_cast<uint32_t*>(out + e) =
+          pack_bf16x2(bad ? NAN : acc[e] * inv, bad ? NAN : acc[e + 1] * inv);
+    if (lane == 0) a.lse[row] = bad ? NAN : (ref + log2f(sum)) * 0.6931471805599453f;
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// Codes as (D bytes, num_pages * P tokens, Hkv); a box, one page of one head, lands as P rows of
+// D bytes swizzled over their length.
+bool encode(CUtensorMap* map, const void* base, int D, int P, int Hkv, int num_pages) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)num_pages * P, (cuuint64_t)Hkv};
+  const cuuint64_t strides[2] = {(cuuint64_t)Hkv * D, (cuuint64_t)D};
+  const cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)P, 1};
+  const cuuint32_t one[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            // a row of one head is D <= 128 bytes: more would fetch the next head's too
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D>
+int launch_attn(Args& a, const void* k_pages, const void* v_pages, int sms, cudaStream_t stream) {
+  static std::once_flag once[kMaxCachedDevices];
+  static cudaError_t attr_err[kMaxCachedDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxCachedDevices) return VAS_E_CUDA;
+  std::call_once(once[dev], [&] {
+    attr_err[dev] = cudaFuncSetAttribute(block_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         smem_bytes<D>());
+  });
+  if (attr_err[dev] != cudaSuccess) return VAS_E_CUDA;
+  CUtensorMap mk, mv;
+  if (!encode(&mk, k_pages, D, a.P, a.Hkv, a.num_pages) || !encode(&mv, v_pages, D, a.P, a.Hkv, a.num_pages))
+    return VAS_E_CUDA;
+  const int ctas = kCtasPerSm * sms;
+  cudaError_t e = launch_pdl(block_attn_kernel<D>, dim3(ctas), kThreads, smem_bytes<D>(), stream, mk, mv, a);
+  // A sequence that fits the tables has at most maxp * P tokens: where that is what is never
+  // cut, nothing is to be merged.
+  if (e == cudaSuccess && (int64_t)a.maxp * a.P > kWholeTiles * kTile)
+    e = launch_pdl(merge_kernel<D>, dim3(ctas, a.G > 4 ? 2 : 1), kMergeThreads, 0, stream, a, ctas);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return VAS_E_CUDA;
+  }
+  return VAS_OK;
+}
+
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+int cta_count() {
+  const int sms = vas::num_sms();
+  return kCtasPerSm * (sms > 0 ? sms : 160);
+}
+
+}  // namespace
+
+size_t workspace_bytes(int head_dim) {
+  const size_t n = 2 * (size_t)cta_count();
+  return align_up(n * sizeof(Record), 256) + align_up(n * kMaxRows * sizeof(float), 256) +
+         n * kMaxRows * head_dim * sizeof(float);
+}
+
+int launch(Args a, const void* k_pages, const void* v_pages, int head_dim, void* workspace, cudaStream_t stream) {
+  const int sms = vas::num_sms();
+  if (!sms) return VAS_E_CUDA;
+  const size_t n = 2 * (size_t)cta_count();
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.records = reinterpret_cast<Record*>(ws);
+  ws += align_up(n * sizeof(Record), 256);
+  a.part_lse = reinterpret_cast<float*>(ws);
+  ws += align_up(n * kMaxRows * sizeof(float), 256);
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.log2P = a.P == 16 ? 4 : 5;
+  // A group of more heads than a unit has rows is taken in even parts, one token at a time.
+  a.parts = (a.G + kMaxRows - 1) / kMaxRows;
+  a.part_rows = (a.G + a.parts - 1) / a.parts;
+  a.parts = (a.G + a.part_rows - 1) / a.part_rows;
+  return head_dim == 128 ? launch_attn<128>(a, k_pages, v_pages, sms, stream)
+                         : launch_attn<64>(a, k_pages, v_pages, sms, stream);
+}
+
+}  // namespace battn
+}  // namespace vas

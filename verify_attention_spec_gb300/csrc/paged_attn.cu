@@ -56,6 +56,7 @@
 
 #include "../../include/vas.h"
 #include "attn_plan.cuh"
+#include "block_attn.cuh"
 #include "device_util.cuh"
 #include "packed_math.cuh"
 #include "vas_internal.h"
@@ -2766,6 +2767,8 @@ bool kv_block(const vas_attn_dims* d) {
   return d->kv_dtype == VAS_FP8_BLOCK || d->kv_dtype == VAS_INT8_BLOCK;
 }
 
+bool own_block_kernel(const vas_attn_dims* d) { return d->kv_dtype == VAS_FP8_BLOCK; }
+
 bool kv_quantized(const vas_attn_dims* d) {
   return d->kv_dtype == VAS_FP8_E4M3 || d->kv_dtype == VAS_INT8 || kv_block(d);
 }
@@ -2926,11 +2929,13 @@ extern "C" {
 
 size_t paged_attn_workspace_min(const vas_attn_dims* dims) {
   if (!dims_ok(dims) || !dims_supported(dims)) return 0;
+  if (own_block_kernel(dims)) return vas::battn::workspace_bytes(dims->head_dim);
   return make_layout(dims, items_min(dims), 0).total;
 }
 
 size_t paged_attn_workspace_size(const vas_attn_dims* dims) {
   if (!dims_ok(dims) || !dims_supported(dims)) return 0;
+  if (own_block_kernel(dims)) return vas::battn::workspace_bytes(dims->head_dim);
   // Room for every output row to be split 8 ways on average.
   const int64_t pcap = (int64_t)dims->total_q_tokens * dims->num_q_heads * 8;
   return make_layout(dims, items_min(dims) + items_extra(vas::num_sms()),
@@ -3019,6 +3024,34 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
     return VAS_E_INVALID_ARG;
   if (d.num_pages == 0 || d.max_pages_per_seq == 0) return VAS_E_INVALID_ARG;
   if ((int64_t)d.num_pages * d.page_size > INT32_MAX) return VAS_E_INVALID_ARG;
+
+  if (own_block_kernel(dims)) {
+    if (workspace_bytes < vas::battn::workspace_bytes(d.head_dim)) return VAS_E_WORKSPACE;
+    vas::battn::Args b{};
+    b.q = q;
+    b.out = out;
+    b.lse = lse;
+    b.block_table = block_table;
+    b.seq_lens = seq_lens;
+    b.query_lens = query_lens;
+    b.tree_mask = tree_mask;
+    b.k_scale = k_scale;
+    b.v_scale = v_scale;
+    b.B = d.num_seqs;
+    b.T = d.total_q_tokens;
+    b.Hq = d.num_q_heads;
+    b.Hkv = d.num_kv_heads;
+    b.G = d.num_q_heads / d.num_kv_heads;
+    b.P = d.page_size;
+    b.num_pages = d.num_pages;
+    b.maxp = d.max_pages_per_seq;
+    b.scale_log2 =
+        (d.scale > 0.f ? d.scale : 1.0f / std::sqrt((float)d.head_dim)) * 1.4426950408889634f;
+    b.err = vas::device_error_word();
+    if (!b.err) return VAS_E_CUDA;
+    return vas::battn::launch(b, k_pages, v_pages, d.head_dim, workspace,
+                              reinterpret_cast<cudaStream_t>(stream_));
+  }
 
   Layout lay;
   if (!fit_layout(dims, workspace_bytes, &lay, prefix ? prefix->num_groups : -1))
