@@ -8,11 +8,12 @@
 // so no code is ever expanded, and decode's few rows waste nothing but tensor-core time of which
 // there is plenty: a tile is 32 KB of HBM, 1400 clocks of an SM's share, against 8 products of
 // about 96.  What is not 8 bits wide is split into parts that are:
-//   Q   a row times a power of two as hi + lo / 32, both E4M3 (8 bits, those of bf16), in columns
-//       of their own; S is their sum.
+//   Q   times a power of two as hi + lo / 32, both E4M3 (8 bits, those of bf16), in columns of
+//       their own; S is their sum.
 //   P   as f16 and that as E5M2 parts in columns of their own: the upper byte of an f16 is its
-//       truncation to E5M2, the remainder is exact, and four parts hold all 11 bits (three hold 9:
-//       a row of few tokens, values near 4, was then 4e-3 off before its rounding to bf16).
+//       truncation to E5M2, the remainder is exact, eight times it is the next part's f16, and
+//       four parts hold all 11 bits (three hold 9: a row of few tokens, values near 4, was then
+//       4e-3 off before its rounding to bf16).
 // With one scale a page, a tile's scales are at most 8 numbers, one a thread: K's multiplies the
 // scores, V's the weights.
 #include <cuda.h>
@@ -47,9 +48,11 @@ constexpr int kParts = 4;          // E5M2 parts of a weight
 constexpr int kTmemCols = 256;
 constexpr int kTmemS = 0, kTmemO = 128;  // S: two buffers of 64 columns
 // A row's reference moves when a weight times its V scale passes 2^kSlack of it; kBase places
-// the weights so that the largest stay below 2^15 in f16, and those 2^-28 of it still count.
-constexpr float kSlack = 3.f;
-constexpr float kBase = 4096.f;
+// the weights so that the largest stay below 2^15 in f16, and those 2^-22 of the reference keep
+// all their bits (f16 counts to 2^-32 of it; the parts, each eight times what remains, to 2^-33).
+// With a slack of 3 rows of spread scores moved several times a unit, 600 instructions a time.
+constexpr float kSlack = 7.f;
+constexpr float kBase = 256.f;
 constexpr float kNoMax = -1e30f;   // reference of a row that has seen nothing
 constexpr int kUnitCost = 128;     // what a unit costs beside its tokens, in tokens
 constexpr int kWholeTiles = 8;     // units of at most so many tiles are never cut
@@ -86,8 +89,9 @@ struct Misc {
   Unit ring[kRing];
   float scales[kScaleTiles][2][8];
   int32_t bad[kScaleTiles];       // a page of the tile is outside the pool
-  float row_scale[kMaxRows];      // of a row's scores, base-2
-  float ref[kMaxRows];            // reference of a row's weights
+  alignas(16) float neg_ref[kMaxRows];  // minus the reference of a row's weights
+  alignas(16) float alpha[kMaxRows];    // what a new reference does to the old sums
+  uint32_t q_top[kSoftWarps];           // largest magnitudes of the unit's queries
   float warp_max[kSoftWarps][kMaxRows];
   float warp_sum[kSoftWarps][kMaxRows];
   int32_t limit[kMaxRows];        // last position a row sees
@@ -232,6 +236,11 @@ __device__ __forceinline__ uint32_t prmt_odd(uint32_t a, uint32_t b) {  // bytes
   asm("prmt.b32 %0, %1, %2, 0x7531;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -257,20 +266,22 @@ struct Ctx {
 };
 
 // ---- softmax warps -------------------------------------------------------------------
-// The unit's queries as E4M3 pairs in the K-major operand layout; the rows' scales, references,
-// limits and masks.
+// The unit's queries as E4M3 pairs in the K-major operand layout; the rows' references, limits
+// and masks.  Returns what brings a score to base 2.
 template <int D, int RP>
-__device__ __forceinline__ void stage_queries(const Ctx<D>& x, const Unit& u) {
+__device__ __forceinline__ float stage_queries(const Ctx<D>& x, const Unit& u) {
   const Args& a = x.a;
   Misc& m = x.m;
   constexpr int kLanes = D / 8;             // of a row, 8 elements each
-  constexpr int kRowsAtOnce = 128 / kLanes;
+  constexpr int kAtOnce = 128 / kLanes;     // rows
+  constexpr int kSteps = (RP + kAtOnce - 1) / kAtOnce;
   const int tid = threadIdx.x, c = tid % kLanes;
   uint8_t* q_tile = x.smem + Smem<D>::kQOff;
-  uint4 v[(RP + kRowsAtOnce - 1) / kRowsAtOnce];
+  uint4 v[kSteps];
+  float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < (RP + kRowsAtOnce - 1) / kRowsAtOnce; ++i) {
-    const int r = i * kRowsAtOnce + tid / kLanes;
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = i * kAtOnce + tid / kLanes;
     v[i] = make_uint4(0, 0, 0, 0);
     if (r < u.rows) {
       const int g = u.r0 + r, j = g / a.G, h = g - j * a.G;
@@ -278,16 +289,27 @@ __device__ __forceinline__ void stage_queries(const Ctx<D>& x, const Unit& u) {
                                               ((size_t)(u.row0 + j) * a.Hq + (size_t)u.head * a.G + h) * D) + c);
     }
   }
+  if (tid < RP) {
+    const int j = min((u.r0 + tid) / a.G, u.ql - 1);
+    m.neg_ref[tid] = -kNoMax;
+    m.limit[tid] = tid < u.rows ? u.len - u.ql + j : -1;
+    const bool tree = a.tree_mask && u.ql > 1 && u.ql <= 64;
+    m.tree[tid] = tree ? (a.tree_mask[u.row0 + j] & (j ? ~0ull >> (64 - j) : 0ull)) | (1ull << j) : ~0ull;
+  }
 #pragma unroll
-  for (int i = 0; i < (RP + kRowsAtOnce - 1) / kRowsAtOnce; ++i) {
-    const int r = i * kRowsAtOnce + tid / kLanes;
-    float top = absmax_bf16x8(v[i]);
+  for (int i = 0; i < kSteps; ++i) top = fmaxf(top, absmax_bf16x8(v[i]));
+  const uint32_t warp_top = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+  if (x.lane == 0) m.q_top[x.warp] = warp_top;
+  named_bar_sync(1, 128);
+  const uint32_t all = max(max(m.q_top[0], m.q_top[1]), max(m.q_top[2], m.q_top[3]));
+  // 2^e brings the unit's largest magnitude into [128, 256): the remainder of hi is then at most
+  // 8, and 32 of it exact in E4M3 for elements down to 2^-15 of the largest (below, 2^-24 of the
+  // largest is lost, as in an fp32 sum of the products).
+  const int e = max(-120, min(120, 7 - ((int)(all >> 23) - 127)));
+  const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
-    for (int o = kLanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // 2^e brings the row's largest magnitude into [128, 256): a half step of hi is then at most
-    // 8, and its remainder times 32 is exact in E4M3 for elements down to 2^-15 of the largest.
-    const int e = max(-120, min(120, 7 - ((int)(__float_as_uint(top) >> 23) - 127)));
-    const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = i * kAtOnce + tid / kLanes;
     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     uint32_t hi[2], lo[2];
 #pragma unroll
@@ -314,7 +336,7 @@ __device__ __forceinline__ void stage_queries(const Ctx<D>& x, const Unit& u) {
       for (int f = 0; f < 4; ++f) b[f] = (y[f] - b[f]) * 32.f;
       lo[k] = pack(b);
     }
-    if (RP % kRowsAtOnce == 0 || r < RP) {
+    if (RP % kAtOnce == 0 || r < RP) {
       // Row n of the operand: rows of D bytes, 16-byte chunks swizzled by the row.
       auto at = [&](int n) {
         const uint32_t off = (uint32_t)n * D + c * 8;
@@ -322,136 +344,153 @@ __device__ __forceinline__ void stage_queries(const Ctx<D>& x, const Unit& u) {
       };
       *reinterpret_cast<uint2*>(at(r)) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(at(RP + r)) = make_uint2(lo[0], lo[1]);
-      if (c == 0) {
-        m.row_scale[r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
-        m.ref[r] = kNoMax;
-        const int j = min((u.r0 + r) / a.G, u.ql - 1);
-        m.limit[r] = r < u.rows ? u.len - u.ql + j : -1;
-        const bool tree = a.tree_mask && u.ql > 1 && u.ql <= 64;
-        m.tree[r] = tree ? (a.tree_mask[u.row0 + j] & (j ? ~0ull >> (64 - j) : 0ull)) | (1ull << j) : ~0ull;
-      }
     }
   }
+  return a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+}
+
+// V rows of a tile that a weight of zero would not silence: slots of no token may hold NaN, and a
+// token of the window may be NaN for the rows that do not see it.  They are cleared; true where
+// that took a NaN from a token, whose rows are then NaN by their sums.
+template <int D>
+__device__ __noinline__ bool clear_row(uint8_t* v_row, bool token) {
+  bool wild = false;
+  if (token) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const uint4 w = reinterpret_cast<const uint4*>(v_row)[i];
+      const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) wild |= __vcmpeq4(q[k] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+    }
+    if (!wild) return false;
+  }
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) reinterpret_cast<uint4*>(v_row)[i] = make_uint4(0, 0, 0, 0);
+  return wild;
 }
 
 // One unit; false after a wait that ran out.  Such a warp waits no more but keeps to the barriers
 // of the others, which leave with it at the end of the unit.
 template <int D, int RP>
 __device__ __forceinline__ bool soft_unit(const Ctx<D>& x, const Unit& u, uint32_t& tile_it) {
-  constexpr int kN = RP * kParts;       // columns of O
   using S = Smem<D>;
+  constexpr int kN = RP * kParts;           // columns of O
+  constexpr int kLd = RP < 16 ? RP : 16;    // rows at a time
   const Args& a = x.a;
   Misc& m = x.m;
   const int tid = threadIdx.x, warp = x.warp, lane = x.lane;
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
 
-  stage_queries<D, RP>(x, u);
+  const float score_scale = stage_queries<D, RP>(x, u);
   fence_proxy_async_smem();
-  named_bar_sync(1, 128);  // the rows' numbers are read by all
+  named_bar_sync(1, 128);  // the queries are staged, the rows' numbers may be read
   if (tid == 0) mbar_arrive(&m.q_full);
 
-  float l[RP];
+  uint64_t l2[RP / 2];  // sums of the weights of this thread's tokens, two rows each
 #pragma unroll
-  for (int r = 0; r < RP; ++r) l[r] = 0.f;
-  bool bad = false, poison = false, ok = true;
+  for (int r = 0; r < RP / 2; ++r) l2[r] = 0;
+  bool bad = false, ok = true;
   auto wait_for = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = wait(bar, parity);
   };
   const int ctx = u.len - u.ql;
-  // The positions every row of the unit sees end here.
   const bool tree = a.tree_mask && u.ql > 1 && u.ql <= 64;
-  const int seen_by_all = tree ? ctx - 1 : ctx + u.r0 / a.G;
+  const int seen_by_all = tree ? ctx - 1 : ctx + u.r0 / a.G;  // the last position all rows see
 
   for (int tile = u.tile0; tile < u.tile1; ++tile, ++tile_it) {
     const int b = tile_it & 1;
     const int slot_v = (2 * tile_it + 1) % S::kSlots;
     wait_for(&m.full[slot_v], ((2 * tile_it + 1) / S::kSlots) & 1);
     const int st = tile_it % kScaleTiles;
-    const float vs = m.scales[st][1][tid >> a.log2P];
-    const float ks = m.scales[st][0][tid >> a.log2P] + (vs - vs);  // a V scale that is not finite: NaN
+    float vs = m.scales[st][1][tid >> a.log2P];
+    // A V scale that is not finite makes its tokens' scores, and so its rows, NaN.
+    const float ks = (m.scales[st][0][tid >> a.log2P] + (vs - vs)) * score_scale;
+    if (vs - vs != 0.f) vs = 0.f;
     bad |= m.bad[st] != 0;
     const int pos = tile * kTile + tid;
     const bool masked = tile * kTile + kTile - 1 > seen_by_all;
-    if (masked) {
-      // V rows that a weight of zero would not silence: slots of no token may hold NaN, and a
-      // token of the window may be NaN for the rows that do not see it.
-      uint8_t* v_row = x.smem + slot_v * S::kOperand + tid * D;
-      bool clear = pos >= u.len;
-      if (!clear && pos > seen_by_all) {
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint4 w = reinterpret_cast<const uint4*>(v_row)[i];
-          const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            poison |= __vcmpeq4(q[k] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
-        }
-        clear = poison;
-      }
-      if (clear) {
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) reinterpret_cast<uint4*>(v_row)[i] = make_uint4(0, 0, 0, 0);
-      }
-      if (pos >= u.len) poison = false;
-    }
+    bool poison = false;
+    if (masked && pos > seen_by_all)
+      poison = clear_row<D>(x.smem + slot_v * S::kOperand + tid * D, pos < u.len);
     // Exponent of the token's V scale, |vs| < 2^ve.
     const float ve = (float)max(-60, min(67, (int)((__float_as_uint(vs) >> 23) & 0xff) - 126));
+    auto dropped = [&](int r) {
+      const int j = pos - ctx;
+      return pos > m.limit[r] || (tree && j >= 0 && !((m.tree[r] >> (j & 63)) & 1));
+    };
 
     wait_for(&m.s_full[b], (tile_it >> 1) & 1);
     tc_fence_after();
-    float s[RP];
-    {
-      const uint32_t at = x.tmem + lanes + kTmemS + 64 * b;
-      constexpr int kLd = RP < 16 ? RP : 16;
+    const uint32_t s_at = x.tmem + lanes + kTmemS + 64 * b;
+    const uint64_t c32 = pair(1.f / 32, 1.f / 32), ks2 = pair(ks, ks);
+    uint64_t t2[RP / 2];  // scores relative to their rows' references
+    for (;;) {
+      float top = -INFINITY;
 #pragma unroll
       for (int r0 = 0; r0 < RP; r0 += kLd) {
         uint32_t hi[kLd], lo[kLd];
-        tmem_ld<kLd>(at + r0, hi);
-        tmem_ld<kLd>(at + RP + r0, lo);
+        tmem_ld<kLd>(s_at + r0, hi);
+        tmem_ld<kLd>(s_at + RP + r0, lo);
         tmem_wait_ld();
 #pragma unroll
-        for (int r = 0; r < kLd; ++r)
-          s[r0 + r] = fmaf(__uint_as_float(lo[r]), 1.f / 32, __uint_as_float(hi[r])) * ks;
+        for (int r = 0; r < kLd; r += 2) {
+          const uint64_t h2 = pair(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1]));
+          const uint64_t w2 = pair(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1]));
+          const uint64_t neg = *reinterpret_cast<const uint64_t*>(&m.neg_ref[r0 + r]);
+          t2[(r0 + r) / 2] = fma2(fma2(w2, c32, h2), ks2, neg);
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&m.s_empty[b]);
-    }
-    bool up = false;
-    auto dropped = [&](int r) {
-      if (pos > m.limit[r]) return true;
-      const int j = pos - ctx;
-      return tree && j >= 0 && !((m.tree[r] >> j) & 1);
-    };
+      if (masked) {
 #pragma unroll
-    for (int r = 0; r < RP; ++r) {
-      s[r] *= m.row_scale[r];
-      if (masked && dropped(r)) s[r] = -INFINITY;
-      up |= s[r] + ve > m.ref[r] + kSlack;
-    }
-    if (named_bar_or(1, 128, up)) {
-      // Some weight outgrew its row's reference: the tile's maxima, and O in the new one.
+        for (int r = 0; r < RP; r += 2) {
+          float y0, y1;
+          unpair(t2[r / 2], y0, y1);
+          if (poison) y0 = y1 = NAN;
+          t2[r / 2] = pair(dropped(r) ? -INFINITY : y0, dropped(r + 1) ? -INFINITY : y1);
+        }
+      }
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        const float v = s[r] == -INFINITY ? -INFINITY : s[r] + ve;
-        const int top = __reduce_max_sync(0xffffffffu, isnan(v) ? INT_MIN : ordered(v));
-        if (lane == 0) m.warp_max[warp][r] = top == INT_MIN ? -INFINITY : unordered(top);
+      for (int r = 0; r < RP; r += 2) {
+        float y0, y1;
+        unpair(t2[r / 2], y0, y1);
+        top = max3(top, y0, y1);
+      }
+      if (!named_bar_or(1, 128, top + ve > kSlack)) break;
+      // Some weight outgrew its row's reference.  The tile's maxima, the new references, and sums
+      // and O in them; then the scores once more.
+#pragma unroll 1
+      for (int r0 = 0; r0 < RP; r0 += 8) {
+        uint32_t hi[8], lo[8];
+        tmem_ld<8>(s_at + r0, hi);
+        tmem_ld<8>(s_at + RP + r0, lo);
+        tmem_wait_ld();
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          float y = fmaf(fmaf(__uint_as_float(lo[r]), 1.f / 32, __uint_as_float(hi[r])), ks, ve);
+          if (isnan(y) || (masked && (poison || dropped(r0 + r)))) y = -INFINITY;
+          const int most = __reduce_max_sync(0xffffffffu, ordered(y));
+          if (lane == 0) m.warp_max[warp][r0 + r] = unordered(most);
+        }
       }
       named_bar_sync(1, 128);
+      if (tid < RP) {
+        const float most = fmaxf(fmaxf(m.warp_max[0][tid], m.warp_max[1][tid]),
+                                 fmaxf(m.warp_max[2][tid], m.warp_max[3][tid]));
+        const float old = -m.neg_ref[tid];
+        const bool up = most > old + kSlack;
+        m.alpha[tid] = up ? ex2_approx(old - most) : 1.f;
+        if (up) m.neg_ref[tid] = -most;
+      }
       const bool have_o = tile > u.tile0;
       if (have_o) wait_for(&m.pv_done[b ^ 1], ((tile_it - 1) >> 1) & 1);
+      named_bar_sync(1, 128);
       tc_fence_after();
-      float alpha[RP];
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        const float top = fmaxf(fmaxf(m.warp_max[0][r], m.warp_max[1][r]),
-                                fmaxf(m.warp_max[2][r], m.warp_max[3][r]));
-        const float old = m.ref[r];
-        alpha[r] = top > old + kSlack ? ex2_approx(old - top) : 1.f;
-        l[r] *= alpha[r];
-      }
+      for (int r = 0; r < RP / 2; ++r)
+        l2[r] = mul2(l2[r], *reinterpret_cast<const uint64_t*>(&m.alpha[2 * r]));
       if (have_o) {
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < kN; c0 += 16) {
           const uint32_t at = x.tmem + lanes + kTmemO + c0;
           uint32_t o[16];
@@ -459,95 +498,106 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D>& x, const Unit& u, uint32
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < 16; ++c)
-            o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha[(c0 + c) % RP]);
+            o[c] = __float_as_uint(__uint_as_float(o[c]) * m.alpha[(c0 + c) % RP]);
           tmem_st16(at, o);
         }
         tmem_wait_st();
         tc_fence_before();
       }
-      named_bar_sync(1, 128);  // every thread has read the old references
-      if (tid < RP) {
-        const float top = fmaxf(fmaxf(m.warp_max[0][tid], m.warp_max[1][tid]),
-                                fmaxf(m.warp_max[2][tid], m.warp_max[3][tid]));
-        if (top > m.ref[tid] + kSlack) m.ref[tid] = top;
-      }
-      named_bar_sync(1, 128);
     }
-    // Weights, their sums, and their parts as bytes.
-    const float vb = vs * kBase;
-    uint32_t part[kParts][RP / 4];
-#pragma unroll
-    for (int r = 0; r < RP; r += 4) {
-      uint32_t h[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float p[2];
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const int q = r + 2 * k + f;
-          p[f] = ex2_approx(s[q] - m.ref[q]);
-          if (masked && poison && s[q] != -INFINITY) p[f] = NAN;
-          l[q] += p[f];
-          p[f] = s[q] == -INFINITY ? 0.f : p[f] * vb;
-        }
-        h[k] = pack_f16x2(p[0], p[1]);
-        if (masked && poison) h[k] = 0;  // the row's NaN is in its sum
-      }
-#pragma unroll
-      for (int t = 0; t < kParts; ++t) {
-        part[t][r / 4] = prmt_odd(h[0], h[1]);
-        h[0] = sub_f16x2(h[0], h[0] & 0xff00ff00u);
-        h[1] = sub_f16x2(h[1], h[1] & 0xff00ff00u);
-      }
-    }
-    poison = false;
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&m.s_empty[b]);
+
     // The weights' buffer is free once the product of two tiles ago is done.
     if (tile >= u.tile0 + 2) wait_for(&m.pv_done[b], ((tile_it - 2) >> 1) & 1);
     uint8_t* p_tile = x.smem + S::kPOff + b * S::kPBytes + tid * 16;
+    const uint64_t vb2 = pair(vs * kBase, vs * kBase);
+    // Weights, their sums, and their parts as bytes: the upper byte of an f16 pair's halves, then
+    // that of eight times the remainder.
 #pragma unroll
-    for (int n = 0; n < kN / 16; ++n) {  // 16 columns: part n * 16 / RP, rows (n * 16) % RP on
-      uint32_t w[4];
+    for (int r0 = 0; r0 < RP; r0 += kLd) {
+      uint32_t part[kParts][kLd / 4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = part[(16 * n + 4 * k) / RP][(16 * n + 4 * k) % RP / 4];
-      *reinterpret_cast<uint4*>(p_tile + n * (kTile * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int r = 0; r < kLd; r += 4) {
+        uint32_t h[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int q = (r0 + r) / 2 + k;
+          float y0, y1;
+          unpair(t2[q], y0, y1);
+          const uint64_t p2 = pair(ex2_approx(y0), ex2_approx(y1));
+          l2[q] = add2(l2[q], p2);
+          unpair(mul2(p2, vb2), y0, y1);
+          h[k] = pack_f16x2(y0, y1);
+          if (masked && poison) h[k] = 0;  // the rows' NaN is in their sums
+        }
+#pragma unroll
+        for (int t = 0; t < kParts; ++t) {
+          part[t][r / 4] = prmt_odd(h[0], h[1]);
+          if (t + 1 < kParts) {
+            h[0] = mul_f16x2(sub_f16x2(h[0], h[0] & 0xff00ff00u), 0x48004800u);
+            h[1] = mul_f16x2(sub_f16x2(h[1], h[1] & 0xff00ff00u), 0x48004800u);
+          }
+        }
+      }
+      // 16 columns a store: two parts of 8 rows, or one of 16.
+      if constexpr (RP == 8) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          *reinterpret_cast<uint4*>(p_tile + n * (kTile * 16)) =
+              make_uint4(part[2 * n][0], part[2 * n][1], part[2 * n + 1][0], part[2 * n + 1][1]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < kParts; ++t)
+          *reinterpret_cast<uint4*>(p_tile + (t * (RP / 16) + r0 / 16) * (kTile * 16)) =
+              make_uint4(part[t][0], part[t][1], part[t][2], part[t][3]);
+      }
     }
     fence_proxy_async_smem();
-    tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&m.p_full[b]);
   }
 
   // The rows' sums over the threads, and the last product.
 #pragma unroll
-  for (int r = 0; r < RP; ++r) {
+  for (int r = 0; r < RP; r += 2) {
+    float y0, y1;
+    unpair(l2[r / 2], y0, y1);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-    if (lane == 0) m.warp_sum[warp][r] = l[r];
+    for (int o = 16; o; o >>= 1) {
+      y0 += __shfl_xor_sync(0xffffffffu, y0, o);
+      y1 += __shfl_xor_sync(0xffffffffu, y1, o);
+    }
+    if (lane == 0) {
+      m.warp_sum[warp][r] = y0;
+      m.warp_sum[warp][r + 1] = y1;
+    }
   }
   wait_for(&m.pv_done[(tile_it - 1) & 1], ((tile_it - 1) >> 1) & 1);
   tc_fence_after();
   named_bar_sync(1, 128);
   const bool mine = D == 128 || lane < 16;  // D = 64: 16 rows of O^T a warp
   const int d = D == 128 ? tid : 16 * warp + lane;
-  constexpr int kAt = RP < 16 ? RP : 16;
+#pragma unroll 1
+  for (int r0 = 0; r0 < u.rows; r0 += 8) {
+    float o[8];
 #pragma unroll
-  for (int r0 = 0; r0 < RP; r0 += kAt) {
-    float o[kAt];
-#pragma unroll
-    for (int t = 0; t < kParts; ++t) {
-      uint32_t w[kAt];
-      tmem_ld<kAt>(x.tmem + lanes + kTmemO + t * RP + r0, w);
+    for (int t = kParts - 1; t >= 0; --t) {
+      uint32_t w[8];
+      tmem_ld<8>(x.tmem + lanes + kTmemO + t * RP + r0, w);
       tmem_wait_ld();
 #pragma unroll
-      for (int r = 0; r < kAt; ++r) o[r] = t ? o[r] + __uint_as_float(w[r]) : __uint_as_float(w[r]);
+      for (int r = 0; r < 8; ++r)
+        o[r] = t + 1 == kParts ? __uint_as_float(w[r]) : fmaf(o[r], 0.125f, __uint_as_float(w[r]));
     }
 #pragma unroll
-    for (int r = 0; r < kAt; ++r) {
+    for (int r = 0; r < 8; ++r) {
       const int q = r0 + r;
       if (q >= u.rows) break;
       const float sum = (m.warp_sum[0][q] + m.warp_sum[1][q]) + (m.warp_sum[2][q] + m.warp_sum[3][q]);
       float y = sum == 0.f ? 0.f : o[r] / sum * (1.f / kBase);
-      float lse2 = sum == 0.f ? -INFINITY : m.ref[q] + log2f(sum);
+      float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - m.neg_ref[q];
       if (bad || isnan(sum)) y = lse2 = NAN;
       if (u.part >= 0) {
         const size_t row = (size_t)u.part * kMaxRows + q;
