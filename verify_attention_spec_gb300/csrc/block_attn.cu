@@ -69,27 +69,34 @@ struct Unit {
   int32_t pad[3];
 };
 
-template <int D>
+// MR: the most rows a unit of the call has.  Two tiles in flight a CTA left decode waiting for
+// memory (70 us for 64 sequences of 2100 tokens); what the weights of few rows do not take is
+// room for a third.
+template <int D, int MR>
 struct Smem {
   static constexpr int kOperand = kTile * D;  // K or V of a tile
-  static constexpr int kSlots = D == 128 ? 4 : 8;
-  static constexpr int kQBytes = 2 * kMaxRows * D;
-  static constexpr int kPBytes = kTile * kMaxRows * kParts;
+  static constexpr int kSlots = (D == 128 ? 1 : 2) * (MR == 8 ? 6 : 5);
+  static constexpr int kQRows = 2 * MR;
+  static constexpr int kPBytes = kTile * MR * kParts;
   static constexpr int kQOff = kSlots * kOperand;
-  static constexpr int kPOff = kQOff + kQBytes;
-  static constexpr int kMiscOff = kPOff + 2 * kPBytes;
-  static_assert(kQOff % 1024 == 0 && kPOff % 128 == 0, "operand tiles");
+  static constexpr int kPOff = kQOff + kQRows * D;
+  static constexpr int kMiscOff = kPOff + kPBytes;
+  static_assert(kQOff % 1024 == 0 && kPOff % 128 == 0 && kMiscOff % 16 == 0, "operand tiles");
 };
 
+constexpr int kMostSlots = 12;
+
 struct Misc {
-  uint64_t full[8], empty[8];
+  uint64_t full[kMostSlots], empty[kMostSlots];
   uint64_t ufull[kRing], uempty[kRing];
-  uint64_t fin, q_full, s_full[2], s_empty[2], p_full[2], pv_done[2];
+  uint64_t fin, q_full, s_full[2], s_empty[2], p_full, pv_done;
   uint64_t tree[kMaxRows];        // the rows' draft-tree masks, own bit set
   Unit ring[kRing];
   float scales[kScaleTiles][2][8];
   int32_t bad[kScaleTiles];       // a page of the tile is outside the pool
   alignas(16) float neg_ref[kMaxRows];  // minus the reference of a row's weights
+  alignas(16) float inv[kMaxRows];      // what a row of O is multiplied by at the end
+  int64_t out_row[kMaxRows];            // its place in out, in rows
   alignas(16) float alpha[kMaxRows];    // what a new reference does to the old sums
   uint32_t q_top[kSoftWarps];           // largest magnitudes of the unit's queries
   float warp_max[kSoftWarps][kMaxRows];
@@ -103,9 +110,9 @@ struct Misc {
   int32_t any_bad;
 };
 
-template <int D>
+template <int D, int MR>
 constexpr int smem_bytes() {
-  return Smem<D>::kMiscOff + (int)sizeof(Misc) + 1024;
+  return Smem<D, MR>::kMiscOff + (int)sizeof(Misc) + 1024;
 }
 
 // ---- the line of work -----------------------------------------------------------------
@@ -127,7 +134,7 @@ __device__ __forceinline__ Shape shape_of(const Args& a, int32_t L, int32_t ql, 
   s.nb = s.tb = 0;
   s.base = s.head_cost = 0;
   if (ql <= 0 || L < ql || (int64_t)L > (int64_t)a.maxp * a.P || row0 + ql > a.T) return s;
-  const int32_t most = a.parts > 1 ? 1 : kMaxRows / a.G;
+  const int32_t most = a.parts > 1 ? 1 : a.max_rows / a.G;
   s.nb = (ql + most - 1) / most;
   s.tb = (ql + s.nb - 1) / s.nb;  // even blocks: 5 tokens of 8 heads are 3 + 2 and not 4 + 1
   s.nb = (ql + s.tb - 1) / s.tb;
@@ -256,7 +263,7 @@ __device__ __forceinline__ float unordered(int i) { return __int_as_float(i >= 0
 // Rows a unit is computed as (RP >= its rows).
 __device__ __forceinline__ int padded_rows(int rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 32); }
 
-template <int D>
+template <int D, int MR>
 struct Ctx {
   const Args& a;
   uint8_t* smem;
@@ -268,15 +275,15 @@ struct Ctx {
 // ---- softmax warps -------------------------------------------------------------------
 // The unit's queries as E4M3 pairs in the K-major operand layout; the rows' references, limits
 // and masks.  Returns what brings a score to base 2.
-template <int D, int RP>
-__device__ __forceinline__ float stage_queries(const Ctx<D>& x, const Unit& u) {
+template <int RP, int D, int MR>
+__device__ __forceinline__ float stage_queries(const Ctx<D, MR>& x, const Unit& u) {
   const Args& a = x.a;
   Misc& m = x.m;
   constexpr int kLanes = D / 8;             // of a row, 8 elements each
   constexpr int kAtOnce = 128 / kLanes;     // rows
   constexpr int kSteps = (RP + kAtOnce - 1) / kAtOnce;
   const int tid = threadIdx.x, c = tid % kLanes;
-  uint8_t* q_tile = x.smem + Smem<D>::kQOff;
+  uint8_t* q_tile = x.smem + Smem<D, MR>::kQOff;
   uint4 v[kSteps];
   float top = 0.f;
 #pragma unroll
@@ -284,14 +291,15 @@ __device__ __forceinline__ float stage_queries(const Ctx<D>& x, const Unit& u) {
     const int r = i * kAtOnce + tid / kLanes;
     v[i] = make_uint4(0, 0, 0, 0);
     if (r < u.rows) {
-      const int g = u.r0 + r, j = g / a.G, h = g - j * a.G;
+      const int g = u.r0 + r, j = a.by_G.div(g), h = g - j * a.G;
       v[i] = *(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
                                               ((size_t)(u.row0 + j) * a.Hq + (size_t)u.head * a.G + h) * D) + c);
     }
   }
   if (tid < RP) {
-    const int j = min((u.r0 + tid) / a.G, u.ql - 1);
+    const int g = u.r0 + tid, j = min((int)a.by_G.div(g), u.ql - 1);
     m.neg_ref[tid] = -kNoMax;
+    m.out_row[tid] = (int64_t)(u.row0 + j) * a.Hq + (int64_t)u.head * a.G + (g - j * a.G);
     m.limit[tid] = tid < u.rows ? u.len - u.ql + j : -1;
     const bool tree = a.tree_mask && u.ql > 1 && u.ql <= 64;
     m.tree[tid] = tree ? (a.tree_mask[u.row0 + j] & (j ? ~0ull >> (64 - j) : 0ull)) | (1ull << j) : ~0ull;
@@ -372,17 +380,17 @@ __device__ __noinline__ bool clear_row(uint8_t* v_row, bool token) {
 
 // One unit; false after a wait that ran out.  Such a warp waits no more but keeps to the barriers
 // of the others, which leave with it at the end of the unit.
-template <int D, int RP>
-__device__ __forceinline__ bool soft_unit(const Ctx<D>& x, const Unit& u, uint32_t& tile_it) {
-  using S = Smem<D>;
+template <int RP, int D, int MR>
+__device__ __forceinline__ bool soft_unit(const Ctx<D, MR>& x, const Unit& u, uint32_t& tile_it) {
+  using S = Smem<D, MR>;
   constexpr int kN = RP * kParts;           // columns of O
-  constexpr int kLd = RP < 16 ? RP : 16;    // rows at a time
+  constexpr int kLd = RP < 16 ? RP : 16;    // rows of weights at a time
   const Args& a = x.a;
   Misc& m = x.m;
   const int tid = threadIdx.x, warp = x.warp, lane = x.lane;
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
 
-  const float score_scale = stage_queries<D, RP>(x, u);
+  const float score_scale = stage_queries<RP>(x, u);
   fence_proxy_async_smem();
   named_bar_sync(1, 128);  // the queries are staged, the rows' numbers may be read
   if (tid == 0) mbar_arrive(&m.q_full);
@@ -396,7 +404,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D>& x, const Unit& u, uint32
   };
   const int ctx = u.len - u.ql;
   const bool tree = a.tree_mask && u.ql > 1 && u.ql <= 64;
-  const int seen_by_all = tree ? ctx - 1 : ctx + u.r0 / a.G;  // the last position all rows see
+  const int seen_by_all = tree ? ctx - 1 : ctx + (int)a.by_G.div(u.r0);  // the last position all rows see
 
   for (int tile = u.tile0; tile < u.tile1; ++tile, ++tile_it) {
     const int b = tile_it & 1;
@@ -427,18 +435,17 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D>& x, const Unit& u, uint32
     uint64_t t2[RP / 2];  // scores relative to their rows' references
     for (;;) {
       float top = -INFINITY;
-#pragma unroll
-      for (int r0 = 0; r0 < RP; r0 += kLd) {
-        uint32_t hi[kLd], lo[kLd];
-        tmem_ld<kLd>(s_at + r0, hi);
-        tmem_ld<kLd>(s_at + RP + r0, lo);
+      {
+        uint32_t hi[RP], lo[RP];
+        tmem_ld<RP>(s_at, hi);
+        tmem_ld<RP>(s_at + RP, lo);
         tmem_wait_ld();
 #pragma unroll
-        for (int r = 0; r < kLd; r += 2) {
+        for (int r = 0; r < RP; r += 2) {
           const uint64_t h2 = pair(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1]));
           const uint64_t w2 = pair(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1]));
-          const uint64_t neg = *reinterpret_cast<const uint64_t*>(&m.neg_ref[r0 + r]);
-          t2[(r0 + r) / 2] = fma2(fma2(w2, c32, h2), ks2, neg);
+          const uint64_t neg = *reinterpret_cast<const uint64_t*>(&m.neg_ref[r]);
+          t2[r / 2] = fma2(fma2(w2, c32, h2), ks2, neg);
         }
       }
       if (masked) {
@@ -483,7 +490,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D>& x, const Unit& u, uint32
         if (up) m.neg_ref[tid] = -most;
       }
       const bool have_o = tile > u.tile0;
-      if (have_o) wait_for(&m.pv_done[b ^ 1], ((tile_it - 1) >> 1) & 1);
+      if (have_o) wait_for(&m.pv_done, (tile_it - 1) & 1);
       named_bar_sync(1, 128);
       tc_fence_after();
 #pragma unroll
@@ -509,9 +516,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D>& x, const Unit& u, uint32
     __syncwarp();
     if (lane == 0) mbar_arrive(&m.s_empty[b]);
 
-    // The weights' buffer is free once the product of two tiles ago is done.
-    if (tile >= u.tile0 + 2) wait_for(&m.pv_done[b], ((tile_it - 2) >> 1) & 1);
-    uint8_t* p_tile = x.smem + S::kPOff + b * S::kPBytes + tid * 16;
+    uint8_t* p_tile = x.smem + S::kPOff + tid * 16;
     const uint64_t vb2 = pair(vs * kBase, vs * kBase);
     // Weights, their sums, and their parts as bytes: the upper byte of an f16 pair's halves, then
     // that of eight times the remainder.
@@ -541,6 +546,8 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D>& x, const Unit& u, uint32
           }
         }
       }
+      // The weights' buffer is free once the product of the tile before is done.
+      if (r0 == 0 && tile > u.tile0) wait_for(&m.pv_done, (tile_it - 1) & 1);
       // 16 columns a store: two parts of 8 rows, or one of 16.
       if constexpr (RP == 8) {
 #pragma unroll
@@ -556,7 +563,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D>& x, const Unit& u, uint32
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&m.p_full[b]);
+    if (lane == 0) mbar_arrive(&m.p_full);
   }
 
   // The rows' sums over the threads, and the last product.
@@ -574,40 +581,37 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D>& x, const Unit& u, uint32
       m.warp_sum[warp][r + 1] = y1;
     }
   }
-  wait_for(&m.pv_done[(tile_it - 1) & 1], ((tile_it - 1) >> 1) & 1);
+  wait_for(&m.pv_done, (tile_it - 1) & 1);
   tc_fence_after();
+  // (The threads of the first warp need every warp's word of a bad page.)
+  bad = named_bar_or(1, 128, bad);
+  if (tid < u.rows) {
+    const float sum = (m.warp_sum[0][tid] + m.warp_sum[1][tid]) + (m.warp_sum[2][tid] + m.warp_sum[3][tid]);
+    float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - m.neg_ref[tid];
+    if (bad) lse2 = NAN;
+    m.inv[tid] = isnan(lse2) ? NAN : (sum == 0.f ? 0.f : 1.f / (sum * kBase));
+    if (u.part >= 0) a.part_lse[(size_t)u.part * kMaxRows + tid] = lse2;
+    else a.lse[m.out_row[tid]] = lse2 * 0.6931471805599453f;
+  }
   named_bar_sync(1, 128);
   const bool mine = D == 128 || lane < 16;  // D = 64: 16 rows of O^T a warp
   const int d = D == 128 ? tid : 16 * warp + lane;
 #pragma unroll 1
   for (int r0 = 0; r0 < u.rows; r0 += 8) {
-    float o[8];
+    uint32_t w[kParts][8];
 #pragma unroll
-    for (int t = kParts - 1; t >= 0; --t) {
-      uint32_t w[8];
-      tmem_ld<8>(x.tmem + lanes + kTmemO + t * RP + r0, w);
-      tmem_wait_ld();
-#pragma unroll
-      for (int r = 0; r < 8; ++r)
-        o[r] = t + 1 == kParts ? __uint_as_float(w[r]) : fmaf(o[r], 0.125f, __uint_as_float(w[r]));
-    }
+    for (int t = 0; t < kParts; ++t) tmem_ld<8>(x.tmem + lanes + kTmemO + t * RP + r0, w[t]);
+    tmem_wait_ld();
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
       const int q = r0 + r;
-      if (q >= u.rows) break;
-      const float sum = (m.warp_sum[0][q] + m.warp_sum[1][q]) + (m.warp_sum[2][q] + m.warp_sum[3][q]);
-      float y = sum == 0.f ? 0.f : o[r] / sum * (1.f / kBase);
-      float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - m.neg_ref[q];
-      if (bad || isnan(sum)) y = lse2 = NAN;
-      if (u.part >= 0) {
-        const size_t row = (size_t)u.part * kMaxRows + q;
-        if (mine) a.part_o[row * D + d] = y;
-        if (tid == 0) a.part_lse[row] = lse2;
-      } else {
-        const int g = u.r0 + q, j = g / a.G, h = g - j * a.G;
-        const size_t row = (size_t)(u.row0 + j) * a.Hq + (size_t)u.head * a.G + h;
-        if (mine) static_cast<__nv_bfloat16*>(a.out)[row * D + d] = __float2bfloat16(y);
-        if (tid == 0) a.lse[row] = lse2 * 0.6931471805599453f;
+      float y = __uint_as_float(w[kParts - 1][r]);
+#pragma unroll
+      for (int t = kParts - 2; t >= 0; --t) y = fmaf(y, 0.125f, __uint_as_float(w[t][r]));
+      if (q < u.rows && mine) {
+        y *= m.inv[q];
+        if (u.part >= 0) a.part_o[((size_t)u.part * kMaxRows + q) * D + d] = y;
+        else static_cast<__nv_bfloat16*>(a.out)[m.out_row[q] * D + d] = __float2bfloat16(y);
       }
     }
   }
@@ -709,11 +713,11 @@ __device__ __forceinline__ int64_t find_share(const Args& a, Misc& m, int64_t* e
   return first;
 }
 
-template <int D>
+template <int D, int MR>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     block_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const Args a) {
-  using S = Smem<D>;
+  using S = Smem<D, MR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -733,9 +737,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&m.s_full[i], 1);
       mbar_init(&m.s_empty[i], kSoftWarps);
-      mbar_init(&m.p_full[i], kSoftWarps);
-      mbar_init(&m.pv_done[i], 1);
     }
+    mbar_init(&m.p_full, kSoftWarps);
+    mbar_init(&m.pv_done, 1);
     mbar_fence_init();
   }
   if (warp == kProducer && lane == 0) {
@@ -746,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Ctx<D> x{a, smem, m, m.tmem, warp, lane};
+  const Ctx<D, MR> x{a, smem, m, m.tmem, warp, lane};
   pdl_wait_prior_grid();
   int64_t end;
   const int64_t first = find_share<D>(a, m, &end);
@@ -930,17 +934,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           if (i + 1 < n) ok = scores(tile_it + 1, id_s);
           if (!ok) break;
           const uint32_t v_it = 2 * tile_it + 1;
-          const int slot = v_it % S::kSlots, b = tile_it & 1;
-          ok = wait(&m.full[slot], (v_it / S::kSlots) & 1) && wait(&m.p_full[b], (tile_it >> 1) & 1);
+          const int slot = v_it % S::kSlots;
+          ok = wait(&m.full[slot], (v_it / S::kSlots) & 1) && wait(&m.p_full, tile_it & 1);
           if (!ok) break;
           tc_fence_after();
           const uint64_t v_desc = desc_rows<D>(ring_at + slot * S::kOperand);
-          const uint64_t p_desc = desc_weights(smem_u32(smem + S::kPOff + b * S::kPBytes));
+          const uint64_t p_desc = desc_weights(smem_u32(smem + S::kPOff));
 #pragma unroll
           for (int k = 0; k < kTile / 32; ++k)
             mma_f8(x.tmem + kTmemO, v_desc + ((32 * D * k) >> 4), p_desc + ((512 * k) >> 4), id_o, i > 0 || k > 0);
           umma_commit(&m.empty[slot]);
-          umma_commit(&m.pv_done[b]);
+          umma_commit(&m.pv_done);
         }
         if (!ok) break;
       }
@@ -961,9 +965,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       if (lane == 0) mbar_arrive(&m.uempty[slot_u]);
       ++unit_it;
       if (u.tile0 >= u.tile1) break;
-      if (u.rows <= 8) ok = soft_unit<D, 8>(x, u, tile_it);
-      else if (u.rows <= 16) ok = soft_unit<D, 16>(x, u, tile_it);
-      else ok = soft_unit<D, 32>(x, u, tile_it);
+      if constexpr (MR == 8) {
+        ok = soft_unit<8>(x, u, tile_it);
+      } else {
+        if (u.rows <= 8) ok = soft_unit<8>(x, u, tile_it);
+        else if (u.rows <= 16) ok = soft_unit<16>(x, u, tile_it);
+        else ok = soft_unit<32>(x, u, tile_it);
+      }
       if (!ok) break;
     }
   }
@@ -1087,22 +1095,22 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, int smem, c
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D>
+template <int D, int MR>
 int launch_attn(Args& a, const void* k_pages, const void* v_pages, int sms, cudaStream_t stream) {
   static std::once_flag once[kMaxCachedDevices];
   static cudaError_t attr_err[kMaxCachedDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxCachedDevices) return VAS_E_CUDA;
   std::call_once(once[dev], [&] {
-    attr_err[dev] = cudaFuncSetAttribute(block_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes<D>());
+    attr_err[dev] = cudaFuncSetAttribute(block_attn_kernel<D, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         smem_bytes<D, MR>());
   });
   if (attr_err[dev] != cudaSuccess) return VAS_E_CUDA;
   CUtensorMap mk, mv;
   if (!encode(&mk, k_pages, D, a.P, a.Hkv, a.num_pages) || !encode(&mv, v_pages, D, a.P, a.Hkv, a.num_pages))
     return VAS_E_CUDA;
   const int ctas = kCtasPerSm * sms;
-  cudaError_t e = launch_pdl(block_attn_kernel<D>, dim3(ctas), kThreads, smem_bytes<D>(), stream, mk, mv, a);
+  cudaError_t e = launch_pdl(block_attn_kernel<D, MR>, dim3(ctas), kThreads, smem_bytes<D, MR>(), stream, mk, mv, a);
   // A sequence that fits the tables has at most maxp * P tokens: where that is what is never
   // cut, nothing is to be merged.
   if (e == cudaSuccess && (int64_t)a.maxp * a.P > kWholeTiles * kTile)
@@ -1139,12 +1147,19 @@ int launch(Args a, const void* k_pages, const void* v_pages, int head_dim, void*
   ws += align_up(n * kMaxRows * sizeof(float), 256);
   a.part_o = reinterpret_cast<float*>(ws);
   a.log2P = a.P == 16 ? 4 : 5;
+  a.by_G = Divisor((uint32_t)a.G);
+  // Units of few rows where the batch can only be decoding: a token a sequence, or fewer.
+  const bool few = a.T <= a.B && a.G <= 8;
+  a.max_rows = few ? 8 : kMaxRows;
   // A group of more heads than a unit has rows is taken in even parts, one token at a time.
   a.parts = (a.G + kMaxRows - 1) / kMaxRows;
   a.part_rows = (a.G + a.parts - 1) / a.parts;
   a.parts = (a.G + a.part_rows - 1) / a.part_rows;
-  return head_dim == 128 ? launch_attn<128>(a, k_pages, v_pages, sms, stream)
-                         : launch_attn<64>(a, k_pages, v_pages, sms, stream);
+  if (head_dim == 128)
+    return few ? launch_attn<128, 8>(a, k_pages, v_pages, sms, stream)
+               : launch_attn<128, kMaxRows>(a, k_pages, v_pages, sms, stream);
+  return few ? launch_attn<64, 8>(a, k_pages, v_pages, sms, stream)
+             : launch_attn<64, kMaxRows>(a, k_pages, v_pages, sms, stream);
 }
 
 }  // namespace battn

@@ -6,8 +6,12 @@
 #include <cstddef>
 #include <cstdint>
 
+#include "attn_plan.cuh"
+
 namespace vas {
 namespace battn {
+
+using attn::Divisor;
 
 constexpr int kMaxRows = 32;  // query rows of a unit
 
@@ -35,7 +39,9 @@ struct Args {
   float scale_log2;  // softmax scale * log2(e)
   int32_t* err;
   // Filled by launch().
-  int32_t log2P, parts, part_rows;  // parts of a group of heads, and heads of a part
+  int32_t log2P, max_rows;
+  int32_t parts, part_rows;  // parts of a group of heads, and heads of a part
+  Divisor by_G;
   Record* records;
   float* part_lse;
   float* part_o;
