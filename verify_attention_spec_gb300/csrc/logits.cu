@@ -17,13 +17,17 @@ namespace vas {
 namespace logits {
 
 // One cluster of C CTAs a row: CTA r holds the slice r of the vocabulary, 8 NV logits a thread
-// in registers as fp32 from the one read to the one write.  What the row's tokens need beside
-// the logits themselves -- how often a token was generated, whether the prompt has it, which
-// bias it gets -- is a table in shared memory with a word for every token of the slice, made
-// from the sequence's token list: each CTA reads 1 / C of the list and counts into the slices
-// of all (distributed shared memory), so the list is read once a row.  Vocabularies past the
-// registers' reach (8 * 512 * 32 = 131072 logits) are taken in chunks, the table made anew and
-// the logits read again for the second pass.
+// in registers as fp32 from the one read to the one write.  The logits of few tokens change by
+// more than the mask and the temperature, so those are set apart: the sequence's token list is
+// counted into a table in shared memory with a word for every token of the slice (each CTA reads
+// 1 / C of the list and counts into the slices of all, through distributed shared memory), a bit
+// map says which words count, and a word's logit is adjusted once, by the thread that owns its
+// part of the map, and left in the table for the thread that holds the row's.  The others cost a
+// look at a byte for eight of them.  Exponentials are taken once, relative to the thread's own
+// maximum, and scaled by one product when the row's maximum and sum are known.
+// Bytes bound it: V (2 or 4 + 4) a row.  Vocabularies past the registers' reach (8 * 512 * 32 =
+// 131072 logits) are taken in chunks, the table made anew and the logits read again for the
+// second pass.
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
@@ -88,11 +92,6 @@ __device__ __forceinline__ void peer_or(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ void peer_store(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ void cluster_sync() {
-  cluster_arrive();
-  cluster_wait();
-}
-
 // VEC: a thread's logits are runs of 8 neighbours, 16-byte aligned; else they are kThreads
 // apart.
 template <typename T, bool VEC, int NV>
@@ -122,16 +121,60 @@ __device__ __forceinline__ float widen1(float x) { return x; }
 template <typename T, bool VEC, int NV, bool MULTI>
 __global__ void __launch_bounds__(kThreads) spec_logits_kernel(const Args a) {
   using L = Tile<T, VEC, NV>;
-  extern __shared__ uint32_t table[];  // L::kTokens words, if the row has a table
+  // The table's words and, behind them, a bit for each; if the row has a table.
+  extern __shared__ uint32_t table[];
+  uint32_t* const map = table + L::kTokens;
   __shared__ Shared s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   const int C = a.cluster;
   const int row = (int)(blockIdx.x / (unsigned)C), b = row / (a.n + 1), j = row - b * (a.n + 1);
   const bool use_table = a.counted || a.max_bias > 0;
-  if (a.probs && !use_table) cluster_arrive();  // its wait: before the first store to a peer
+  auto clear_table = [&] {
+    uint4* t4 = reinterpret_cast<uint4*>(table);
+    for (int i = tid; i < L::kTokens / 4 + L::kTokens / 128; i += kThreads) t4[i] = make_uint4(0, 0, 0, 0);
+  };
+  // The cluster's CTAs are all there, and their tables clear, before the first word of a peer's
+  // shared memory is touched.
+  if (use_table) clear_table();
+  if (use_table || a.probs) cluster_arrive();
   pdl_wait_prior_grid();
   pdl_launch_dependents();
+
+  const T* in = static_cast<const T*>(a.logits) + (size_t)row * a.row_stride;
+  float* out = a.out + (size_t)row * a.V;
+  const uint8_t* mask_bytes = reinterpret_cast<const uint8_t*>(a.mask + (size_t)row * a.mask_words);
+  const int first = rank * a.slice, last = min(a.V, first + a.slice);
+  float z[NV][8];
+  uint32_t allowed[NV];  // mask bits of a run of 8
+  auto load_chunk = [&](int k) {
+    const int base = first + k * L::kTokens;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int x0 = base + L::at(v, 0);
+      if (VEC && x0 + 8 <= last) {
+        load8(in + x0, z[v]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int x = base + L::at(v, e);
+          z[v][e] = x < last ? widen1(in[x]) : -INFINITY;
+        }
+      }
+      allowed[v] = 0xff;
+      if (VEC) {
+        if (a.mask) allowed[v] = x0 < last ? mask_bytes[x0 >> 3] : 0;
+      } else if (a.mask) {
+        allowed[v] = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int x = base + L::at(v, e);
+          if (x < last) allowed[v] |= (uint32_t)((mask_bytes[x >> 3] >> (x & 7)) & 1) << e;
+        }
+      }
+    }
+  };
+  load_chunk(0);  // on their way while the table is made
 
   // The drafts on the way to row j: those before it, or its ancestors.
   if (tid == 0) s.bad = 0;
@@ -157,48 +200,43 @@ __global__ void __launch_bounds__(kThreads) spec_logits_kernel(const Args a) {
       if (tid == 0 && rank == 0) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
     }
   }
-  __syncthreads();
-  if (path && a.parents && tid == 0) {
-    for (int u = j; u > 0;) {  // ascends: a parent precedes its child
-      const int p = s.parent[u - 1];
-      s.on_path[u - 1] = 1;
-      if (p < 0 || p >= u) {
-        s.bad = VAS_DEV_BAD_TREE;
-        break;
-      }
-      u = p;
-    }
-  }
-  __syncthreads();
+  if (path || nb) __syncthreads();
   if (path) {
+    if (a.parents) {
+      if (tid == 0) {
+        for (int u = j; u > 0;) {  // ascends: a parent precedes its child
+          const int p = s.parent[u - 1];
+          s.on_path[u - 1] = 1;
+          if (p < 0 || p >= u) {
+            s.bad = VAS_DEV_BAD_TREE;
+            break;
+          }
+          u = p;
+        }
+      }
+      __syncthreads();
+    }
     int e = s.bad;
     for (int i = tid; i < a.n; i += kThreads)
       if (s.on_path[i]) {
         const int x = a.drafts[(size_t)b * a.n + i];
         if (x < 0 || x >= a.V) e = VAS_DEV_BAD_TOKEN;
       }
-    if (e) {
-      atomicOr(&s.bad, e);
-      if (rank == 0) atomicOr(a.err, e);
-    }
-    __syncthreads();
-    bad |= s.bad != 0;
+    if (e && rank == 0) atomicOr(a.err, e);
+    bad |= __syncthreads_or(e != 0);
   }
 
-  const float rep = a.repetition ? a.repetition[b] : 1.f;
-  const float freq = a.frequency ? a.frequency[b] : 0.f;
-  const float pres = a.presence ? a.presence[b] : 0.f;
-  const T* in = static_cast<const T*>(a.logits) + (size_t)row * a.row_stride;
-  float* out = a.out + (size_t)row * a.V;
-  const uint8_t* mask_bytes = reinterpret_cast<const uint8_t*>(a.mask + (size_t)row * a.mask_words);
-  const int first = rank * a.slice, last = min(a.V, first + a.slice);
-
-  // The table of chunk k of every slice.
+  bool used = false;  // a table has been made
+  // The table of chunk k of every slice: counts of the cluster's lists, then the adjusted logits
+  // of this CTA's tokens.
   auto make_table = [&](int k) {
-    uint4* t4 = reinterpret_cast<uint4*>(table);
-    __syncthreads();  // the chunk before has been read
-    for (int i = tid; i < L::kTokens / 4; i += kThreads) t4[i] = make_uint4(0, 0, 0, 0);
-    cluster_sync();  // all slices are clear
+    if (used) {  // (the first one is clear)
+      __syncthreads();  // the chunk before has been read
+      clear_table();
+      cluster_arrive();
+    }
+    used = true;
+    cluster_wait();  // all slices are clear
     if (a.counted) {
       auto mark = [&](int32_t x, bool prompt) {
         if (x < 0 || x >= a.V) return;  // no logit: a placeholder
@@ -208,6 +246,7 @@ __global__ void __launch_bounds__(kThreads) spec_logits_kernel(const Args a) {
         const uint32_t word = peer_address(table + at, r);
         if (prompt) peer_or(word, kPrompt);
         else peer_add(word, 1);
+        peer_or(peer_address(map + (at >> 5), r), 1u << (at & 31));
       };
       for (int i = (int)rank * kThreads + tid; i < n_tok; i += C * kThreads)
         mark(a.tokens[(size_t)b * a.max_tokens + i], i < n_prompt);
@@ -215,69 +254,64 @@ __global__ void __launch_bounds__(kThreads) spec_logits_kernel(const Args a) {
         for (int i = tid; i < a.n; i += kThreads)
           if (s.on_path[i]) mark(a.drafts[(size_t)b * a.n + i], false);
     }
-    // Biases of this slice: the first entry of a token gets the sum of all, in list order.
+    // Biases of this slice: the first entry of a token stands for all of them.
+    const int base = first + k * L::kTokens;
     for (int i = tid; i < nb; i += kThreads) {
-      const int x = s.bias_tok[i], at = x - first - k * L::kTokens;
+      const int x = s.bias_tok[i], at = x - base;
       if (x < first || x >= last || at < 0 || at >= L::kTokens) continue;
       bool head = true;
       for (int e = 0; e < i; ++e) head &= s.bias_tok[e] != x;
-      if (head) atomicOr(table + at, (uint32_t)(i + 1) << kBiasShift);
-    }
-    cluster_sync();
-  };
-  auto bias_of = [&](int i) {
-    const int x = s.bias_tok[i];
-    float sum = s.bias[i];
-    for (int e = i + 1; e < nb; ++e)
-      if (s.bias_tok[e] == x) sum += s.bias[e];
-    return sum;
-  };
-  float z[NV][8];
-  auto load_chunk = [&](int k) {
-    const int base = first + k * L::kTokens;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int t0 = L::at(v, 0);
-      if (VEC && base + t0 + 8 <= last) {
-        load8(in + base + t0, z[v]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int x = base + L::at(v, e);
-          z[v][e] = x < last ? widen1(in[x]) : -INFINITY;
-        }
+      if (head) {
+        atomicOr(table + at, (uint32_t)(i + 1) << kBiasShift);
+        atomicOr(map + (at >> 5), 1u << (at & 31));
       }
     }
-    if (use_table) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t w = table[L::at(v, e)];
-          if (w == 0) continue;
-          float y = z[v][e];
-          if (w & (kCountMask | kPrompt)) y = y > 0.f ? y / rep : y * rep;
-          if (w & kCountMask) y = y - freq * (float)(w & kCountMask) - pres;
-          if (w >> kBiasShift) y += bias_of((int)(w >> kBiasShift) - 1);
-          z[v][e] = y;
+    cluster_arrive();
+    cluster_wait();
+    const float rep = a.repetition ? a.repetition[b] : 1.f;
+    const float freq = a.frequency ? a.frequency[b] : 0.f;
+    const float pres = a.presence ? a.presence[b] : 0.f;
+    for (int i = tid; i < L::kTokens / 32; i += kThreads)
+      for (uint32_t bits = map[i]; bits; bits &= bits - 1) {
+        const int at = 32 * i + __ffs(bits) - 1;
+        const uint32_t w = table[at];
+        float y = widen1(in[base + at]);
+        if (w & (kCountMask | kPrompt)) y = y > 0.f ? y / rep : y * rep;
+        if (w & kCountMask) y = y - freq * (float)(w & kCountMask) - pres;
+        if (w >> kBiasShift) {
+          const int head = (int)(w >> kBiasShift) - 1;
+          float sum = s.bias[head];  // in list order
+          for (int e = head + 1; e < nb; ++e)
+            if (s.bias_tok[e] == base + at) sum += s.bias[e];
+          y += sum;
         }
-    }
-    if (a.mask) {
+        table[at] = __float_as_uint(y);
+      }
+    __syncthreads();
+  };
+  auto adjust_chunk = [&] {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
+    for (int v = 0; v < NV; ++v) {
+      if (use_table) {
         if (VEC) {
-          const int x = base + L::at(v, 0);
-          const uint32_t allowed = x < last ? mask_bytes[x >> 3] : 0;
+          const uint32_t bits = reinterpret_cast<const uint8_t*>(map)[L::at(v, 0) >> 3];
+          if (bits) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (!((allowed >> e) & 1)) z[v][e] = -INFINITY;
+            for (int e = 0; e < 8; ++e)
+              if ((bits >> e) & 1) z[v][e] = __uint_as_float(table[L::at(v, e)]);
+          }
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int x = base + L::at(v, e);
-            if (x < last && !((mask_bytes[x >> 3] >> (x & 7)) & 1)) z[v][e] = -INFINITY;
+            const int at = L::at(v, e);
+            if ((map[at >> 5] >> (at & 31)) & 1) z[v][e] = __uint_as_float(table[at]);
           }
         }
+      }
+      if (a.mask) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (!((allowed[v] >> e) & 1)) z[v][e] = -INFINITY;
       }
     }
   };
@@ -299,12 +333,16 @@ __global__ void __launch_bounds__(kThreads) spec_logits_kernel(const Args a) {
       }
     }
   };
+  auto take_chunk = [&](int k, bool loaded) {
+    if (use_table) make_table(k);
+    if (!loaded) load_chunk(k);
+    adjust_chunk();
+  };
 
   const int chunks = MULTI ? a.chunks : 1;
   if (!a.probs) {
     for (int k = 0; k < chunks; ++k) {
-      if (use_table) make_table(k);
-      load_chunk(k);
+      take_chunk(k, k == 0);
       if (bad) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
@@ -316,60 +354,56 @@ __global__ void __launch_bounds__(kThreads) spec_logits_kernel(const Args a) {
     return;
   }
 
-  // Softmax: the slice's maximum (its first token too, for temperature 0) and its sum of
-  // exponentials, then those of the cluster.
+  // Softmax: m is the maximum of what a thread, a warp, a CTA, the cluster holds, sum its
+  // exponentials relative to m (0, or NaN, without a finite value); with temperature 0 best is the
+  // first token at the maximum, and sum only carries a NaN.
   const float temp = a.temperature ? a.temperature[b] : 1.f;
   const bool greedy = temp == 0.f;
-  const float c = greedy ? 0.f : (temp > 0.f ? 1.4426950408889634f / temp : NAN);
-  float m = -INFINITY, sum = 0.f;
+  // (An infinite temperature keeps the sign of -inf.)
+  const float c = temp > 0.f ? fmaxf(1.4426950408889634f / temp, 0x1p-149f) : NAN;
+  float m = -INFINITY, sum = 0.f, ref = 0.f;  // ref: m, or 0 where that is not finite
   int best = 0x7fffffff;
+  auto join = [&](float om, float os, int ob) {
+    const float nm = fmaxf(m, om), r = nm == -INFINITY ? 0.f : nm;
+    if (greedy) sum += os;
+    else
+      sum = (m == -INFINITY ? sum : sum * exp2f((m - r) * c)) +
+            (om == -INFINITY ? os : os * exp2f((om - r) * c));
+    best = om > m || (om == m && ob < best) ? ob : best;
+    m = nm;
+  };
   for (int k = 0; k < chunks; ++k) {
-    if (use_table) make_table(k);
-    load_chunk(k);
+    take_chunk(k, k == 0);
     float cm = -INFINITY;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e) cm = fmaxf(cm, z[v][e]);
     if (greedy) {
+      int at = 0x7fffffff;
+      float wild = 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          if (isnan(z[v][e])) sum = NAN;
-          const int x = first + k * L::kTokens + L::at(v, e);
-          if (z[v][e] == cm && (cm > m || (cm == m && x < best))) {
-            best = x;
-            m = cm;
-          }
+          if (isnan(z[v][e])) wild = NAN;
+          if (z[v][e] == cm) at = min(at, first + k * L::kTokens + L::at(v, e));
         }
-    }
-    const float nm = fmaxf(m, cm);
-    if (!greedy) {
-      const float ref = nm == -INFINITY ? 0.f : nm;
-      if (m != -INFINITY) sum *= exp2f((m - ref) * c);
+      join(cm, wild, at);
+    } else {
+      ref = cm == -INFINITY ? 0.f : cm;
+      float cs = 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (z[v][e] != -INFINITY) sum += exp2f((z[v][e] - ref) * c);
+        for (int e = 0; e < 8; ++e) {
+          const float y = ex2_approx((z[v][e] - ref) * c);
+          if (!MULTI) z[v][e] = y;
+          cs += y;
+        }
+      join(cm, cs, 0);
     }
-    m = nm;
   }
-  // Lanes, then warps, then CTAs, each time by (maximum, first token) and rescaled sums.
-  auto join = [&](float om, float os, int ob) {
-    const float nm = fmaxf(m, om);
-    const float ref = nm == -INFINITY ? 0.f : nm;
-    if (greedy) {
-      sum += os;
-    } else {
-      // The sum of a part without finite values is 0, or NaN.
-      sum = (m == -INFINITY ? sum : sum * exp2f((m - ref) * c)) +
-            (om == -INFINITY ? os : os * exp2f((om - ref) * c));
-    }
-    best = om > m || (om == m && ob < best) ? ob : best;
-    m = nm;
-  };
 #pragma unroll
   for (int o = 16; o; o >>= 1)
     join(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o),
@@ -395,28 +429,31 @@ __global__ void __launch_bounds__(kThreads) spec_logits_kernel(const Args a) {
       peer_store(peer_address(&s.peer_at[rank], lane), (uint32_t)best);
     }
   }
-  cluster_sync();
+  cluster_arrive();
+  cluster_wait();
   m = s.peer_max[0], sum = s.peer_sum[0], best = s.peer_at[0];
   for (int r = 1; r < C; ++r) join(s.peer_max[r], s.peer_sum[r], s.peer_at[r]);
+  const float row_ref = m == -INFINITY ? 0.f : m;
+  const bool wild = bad || isnan(sum);
+  // A row without a token is 0 throughout.
+  const float inv = wild ? NAN : (m == -INFINITY ? 0.f : 1.f / sum);
 
   for (int k = 0; k < chunks; ++k) {
-    if (MULTI) {
-      if (use_table) make_table(k);
-      load_chunk(k);
-    }
-    const float inv = bad ? NAN : (m == -INFINITY && !isnan(sum) ? 0.f : 1.f / sum);
+    if (MULTI) take_chunk(k, false);
+    // What the held exponentials, relative to the thread's maximum, are short of the row's.
+    const float f = MULTI ? 0.f : exp2f((ref - row_ref) * c) * inv;
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        float p;
         if (greedy) {
           const int x = first + k * L::kTokens + L::at(v, e);
-          p = isnan(sum) || bad ? NAN : (x == best && m != -INFINITY ? 1.f : 0.f);
+          z[v][e] = wild ? NAN : (x == best && m != -INFINITY ? 1.f : 0.f);
+        } else if (MULTI) {
+          z[v][e] = ex2_approx((z[v][e] - row_ref) * c) * inv;
         } else {
-          p = z[v][e] == -INFINITY ? 0.f * inv : exp2f((z[v][e] - m) * c) * inv;
+          z[v][e] *= f;
         }
-        z[v][e] = p;
       }
     store_chunk(k);
   }
@@ -432,14 +469,15 @@ template <typename T, bool VEC, int NV, bool MULTI>
 int launch(Args& a, int rows, int cluster, cudaStream_t stream) {
   constexpr int kTokens = Tile<T, VEC, NV>::kTokens;
   const bool table = a.counted || a.max_bias > 0;
-  const size_t smem = table ? kTokens * 4 : 0;
+  const size_t smem = table ? kTokens * 4 + kTokens / 8 : 0;
   static std::once_flag once[kMaxCachedDevices];
   static cudaError_t attr_err[kMaxCachedDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxCachedDevices) return VAS_E_CUDA;
   std::call_once(once[dev], [&] {
     attr_err[dev] = cudaFuncSetAttribute(spec_logits_kernel<T, VEC, NV, MULTI>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kTokens * 4);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kTokens * 4 + kTokens / 8);
   });
   if (attr_err[dev] != cudaSuccess) return VAS_E_CUDA;
   a.chunks = (a.slice + kTokens - 1) / kTokens;
