@@ -22,12 +22,13 @@ namespace logits {
 // rows each; CTA r of a cluster holds slice r of the vocabulary, 8 NV logits a thread in registers
 // as fp32 from the one read to the one write.  While a row is reduced and written, the next one's
 // logits are on their way into shared memory by bulk copy.
-// The logits of few tokens change by more than the mask and the temperature, so those are set
-// apart: when a cluster comes to a sequence its token list is counted into a table in shared
-// memory with a word for every token of the slice (each CTA reads 1 / C of the list and counts
-// into the slices of all, through distributed shared memory), and a bit map says which words
-// count.  A thread's dense logits leave those tokens out; the thread that owns their word of the
-// map takes them, in both passes.  From row to row of a sequence only the drafts change.
+// The logits of few tokens change by more than the mask and the temperature.  When a CTA comes to
+// a sequence it marks those of its slice in a bit map (from the token list, the drafts and the
+// biases), gives each an entry, in the order of the vocabulary, and counts the list into the
+// entries.  For a row the threads adjust the entries' logits, an even share each (text uses few
+// tokens much, so their owners would have most of them); a thread whose run of 8 has a bit in the
+// map takes its logit from the entry, found by counting bits.  From row to row of a sequence only
+// the drafts' counts change.
 // Exponentials are taken once, relative to the thread's own maximum, and scaled by one product
 // when the row's maximum and sum are known.
 // Bytes bound it: V (2 or 4 + 4) a row.  Vocabularies past the registers' reach (8 * 512 * 64 =
@@ -39,7 +40,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxBias = 1024;
 constexpr int kMaxTokens = 1 << 20;  // of a list: a count fits its field
 constexpr int kMaxNodes = 255;
-// A table word: count, prompt flag, bias entry + 1.
+// The word of an entry: count, prompt flag, bias entry + 1.
 constexpr uint32_t kCountMask = (1u << 20) - 1, kPrompt = 1u << 20;
 constexpr int kBiasShift = 21;
 
@@ -65,7 +66,7 @@ struct Args {
   int32_t probs, counted;  // counted: penalties are in play
   int32_t out_vec;         // rows of out are 16-byte aligned
   int32_t staged;          // rows come by bulk copy; bytes of a slice's place
-  int32_t words;           // of the table
+  int32_t entries;         // room for the entries of a slice, or 0: none are needed
   int32_t* err;
 };
 
@@ -80,6 +81,7 @@ struct Shared {
   float peer_max[2][kMaxCluster], peer_sum[2][kMaxCluster];
   int32_t peer_at[2][kMaxCluster];
   uint64_t landed;
+  int32_t scan[kWarps];
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -92,15 +94,16 @@ __device__ __forceinline__ uint32_t peer_address(const void* p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void peer_add(uint32_t addr, uint32_t v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ void peer_or(uint32_t addr, uint32_t v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
 __device__ __forceinline__ void peer_store(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+// Order of floats as order of ints, for the warp-wide maximum.
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x);
+  return i >= 0 ? i : i ^ 0x7fffffff;
+}
+__device__ __forceinline__ float unordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
+
 // VEC: a thread's logits are runs of 8 neighbours, 16-byte aligned; else they are kThreads
 // apart.
 template <typename T, bool VEC, int NV>
@@ -130,32 +133,29 @@ __device__ __forceinline__ float widen1(float x) { return x; }
 template <typename T, bool VEC, int NV, bool MULTI>
 __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logits_kernel(const Args a) {
   using L = Tile<T, VEC, NV>;
-  constexpr int kKeep = 4;  // adjusted logits a thread keeps between the passes
-  // The table's words, a bit for each, and the place of a row's slice.
-  extern __shared__ __align__(16) uint32_t table[];
-  uint32_t* const map = table + a.words;
-  const T* const stage = reinterpret_cast<const T*>(map + a.words / 32);
+  constexpr int kMapWords = L::kTokens / 32;
+  // The entries' words, adjusted logits and places, and the place of a row's slice.
+  extern __shared__ __align__(16) uint32_t words[];
+  float* const values = reinterpret_cast<float*>(words + a.entries);
+  uint16_t* const places = reinterpret_cast<uint16_t*>(values + a.entries);
+  const T* const stage = reinterpret_cast<const T*>(places + a.entries);
   __shared__ Shared s;
+  __shared__ uint32_t map[kMapWords];
+  __shared__ uint16_t rank0[kMapWords];  // entries before a word of the map
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_rank();
   const int C = a.cluster;
   const int cluster = (int)(blockIdx.x / (unsigned)C);
-  const bool use_table = a.counted || a.max_bias > 0;
+  const bool listed = a.entries > 0;
   const int nb = a.max_bias;
-  auto clear_table = [&] {
-    uint4* t4 = reinterpret_cast<uint4*>(table);
-    for (int i = tid; i < a.words / 4 + a.words / 128; i += kThreads) t4[i] = make_uint4(0, 0, 0, 0);
-  };
   if (tid == 0) {
     mbar_init(&s.landed, 1);
     mbar_fence_init();
   }
-  if (use_table) clear_table();
   __syncthreads();
-  // The cluster's CTAs are all there, and their tables clear, before the first word of a peer's
-  // shared memory is touched: every arrival below has its wait.
-  if (use_table || a.probs) cluster_arrive();
-  bool arrived = use_table || a.probs;
+  // The cluster's CTAs are all there before the first word of a peer's shared memory is touched.
+  if (a.probs) cluster_arrive();
+  bool arrived = a.probs;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
 
@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
   };
   if (a.staged && tid == 0 && row0 < row1) fetch(row0);
 
-  int seq = -1;  // the sequence that the table counts
+  int n_entries = 0;
+  int seq = -1;      // the sequence that the entries are of
   uint32_t nth = 0;  // rows taken
   int32_t n_tok = 0, n_prompt = 0;
   float rep = 1.f, freq = 0.f, pres = 0.f, temp = 1.f;
@@ -186,6 +187,8 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
     const T* in = row_in(row);
     float* out = a.out + (size_t)row * a.V;
     const uint8_t* mask_bytes = reinterpret_cast<const uint8_t*>(a.mask + (size_t)row * a.mask_words);
+    const int32_t* drafts = a.drafts + (size_t)b * a.n;
+    const int32_t* tokens = a.tokens + (size_t)b * a.max_tokens;
     const bool other = b != seq;
     if (other) {
       rep = a.repetition ? a.repetition[b] : 1.f;
@@ -230,93 +233,98 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
       }
       for (int i = tid; i < a.n; i += kThreads)
         if (s.on_path[i] & 1) {
-          const int x = a.drafts[(size_t)b * a.n + i];
+          const int x = drafts[i];
           if (x < 0 || x >= a.V) e |= VAS_DEV_BAD_TOKEN;
         }
       if (e && rank == 0) atomicOr(a.err, e);
       bad |= __syncthreads_or(e != 0) != 0;
     }
 
-    // The table of chunk k: the cluster's counts of the sequence's list and its biases when the
-    // table is another sequence's (or chunk's), and the row's drafts.
-    auto make_table = [&](int k, bool anew) {
-      const int base = first + k * L::kTokens;
+    // The entries of chunk k of the slice, anew or with the drafts of another row.
+    auto make_entries = [&](int k, bool anew) {
+      const int base = first + k * L::kTokens, end = min(last, base + L::kTokens);
+      auto mine = [&](int32_t x) { return x >= base && x < end; };
+      auto entry = [&](int32_t x) {
+        const int at = x - base;
+        return (int)rank0[at >> 5] + __popc(map[at >> 5] & ((1u << (at & 31)) - 1));
+      };
       if (anew) {
-        if (nb) {
-          __syncthreads();
-          for (int i = tid; i < nb; i += kThreads) {
-            s.bias_tok[i] = a.bias_tokens[(size_t)b * nb + i];
-            s.bias[i] = a.bias[(size_t)b * nb + i];
-          }
-        }
-        if (!arrived) {
-          __syncthreads();  // the table has been read
-          clear_table();
-          cluster_arrive();
+        __syncthreads();  // the entries before have been read
+        for (int i = tid; i < kMapWords; i += kThreads) map[i] = 0;
+        for (int i = tid; i < nb; i += kThreads) {
+          s.bias_tok[i] = a.bias_tokens[(size_t)b * nb + i];
+          s.bias[i] = a.bias[(size_t)b * nb + i];
         }
         __syncthreads();
-        arrived = false;
-        cluster_wait();  // all slices are clear
-        if (a.counted) {
-          for (int i = (int)rank * kThreads + tid; i < n_tok; i += C * kThreads) {
-            const int32_t x = a.tokens[(size_t)b * a.max_tokens + i];
-            if (x < 0 || x >= a.V) continue;  // no logit: a placeholder
-            const uint32_t r = (uint32_t)x / (uint32_t)a.slice;
-            const int at = x - (int)r * a.slice - k * L::kTokens;
-            if (at < 0 || at >= L::kTokens) continue;
-            const uint32_t word = peer_address(table + at, r);
-            if (i < n_prompt) peer_or(word, kPrompt);
-            else peer_add(word, 1);
-            peer_or(peer_address(map + (at >> 5), r), 1u << (at & 31));
+        auto mark = [&](int32_t x) {
+          if (mine(x)) atomicOr(map + ((x - base) >> 5), 1u << ((x - base) & 31));
+        };
+        for (int i = tid; i < n_tok; i += kThreads) mark(tokens[i]);
+        if (a.counted)
+          for (int i = tid; i < a.n; i += kThreads) mark(drafts[i]);
+        for (int i = tid; i < nb; i += kThreads) mark(s.bias_tok[i]);
+        __syncthreads();
+        // A scan of the map words' counts (two a thread at most).
+        constexpr int kPer = (kMapWords + kThreads - 1) / kThreads;
+        uint32_t w[kPer];
+        int sum = 0;
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+          const int i = tid * kPer + p;
+          w[p] = i < kMapWords ? map[i] : 0;
+          sum += __popc(w[p]);
+        }
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        if (lane == 31) s.scan[warp] = inc;
+        __syncthreads();
+        int at = inc - sum;
+        n_entries = 0;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) {
+          if (v < warp) at += s.scan[v];
+          n_entries += s.scan[v];
+        }
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+          const int i = tid * kPer + p;
+          if (i < kMapWords) rank0[i] = (uint16_t)at;
+          for (uint32_t bits = w[p]; bits; bits &= bits - 1) {
+            words[at] = 0;
+            places[at++] = (uint16_t)(32 * i + __ffs(bits) - 1);
           }
         }
-        // Biases of this slice: the first entry of a token stands for all of them.
+        __syncthreads();
+        for (int i = tid; i < n_tok; i += kThreads) {
+          const int32_t x = tokens[i];
+          if (!mine(x)) continue;
+          if (i < n_prompt) atomicOr(words + entry(x), kPrompt);
+          else atomicAdd(words + entry(x), 1u);
+        }
+        // Of a token's biases the first stands for all of them.
         for (int i = tid; i < nb; i += kThreads) {
-          const int x = s.bias_tok[i], at = x - base;
-          if (x < first || x >= last || at < 0 || at >= L::kTokens) continue;
+          const int x = s.bias_tok[i];
+          if (!mine(x)) continue;
           bool head = true;
           for (int e = 0; e < i; ++e) head &= s.bias_tok[e] != x;
-          if (head) {
-            atomicOr(table + at, (uint32_t)(i + 1) << kBiasShift);
-            atomicOr(map + (at >> 5), 1u << (at & 31));
-          }
+          if (head) atomicOr(words + entry(x), (uint32_t)(i + 1) << kBiasShift);
         }
       }
       if (a.counted)
         for (int i = tid; i < a.n; i += kThreads) {
           const int now = s.on_path[i] & 1, was = anew ? 0 : s.on_path[i] >> 1;
-          if (now == was) continue;
-          const int x = a.drafts[(size_t)b * a.n + i], at = x - base;
-          if (x < first || x >= last || at < 0 || at >= L::kTokens) continue;
-          atomicAdd(table + at, (uint32_t)(now - was));
-          atomicOr(map + (at >> 5), 1u << (at & 31));
+          if (now != was && mine(drafts[i])) atomicAdd(words + entry(drafts[i]), (uint32_t)(now - was));
         }
-      if (anew) {
-        cluster_arrive();
-        cluster_wait();
-      } else {
-        __syncthreads();
-      }
-    };
-    auto adjusted = [&](float y, int x, int base) {
-      const uint32_t w = table[x - base];
-      if (w & (kCountMask | kPrompt)) y = y > 0.f ? y / rep : y * rep;
-      if (w & kCountMask) y = y - freq * (float)(w & kCountMask) - pres;
-      if (w >> kBiasShift) {
-        const int head = (int)(w >> kBiasShift) - 1;
-        float sum = s.bias[head];  // in list order
-        for (int e = head + 1; e < nb; ++e)
-          if (s.bias_tok[e] == x) sum += s.bias[e];
-        y += sum;
-      }
-      if (a.mask && !((mask_bytes[x >> 3] >> (x & 7)) & 1)) y = -INFINITY;
-      return y;
+      __syncthreads();
     };
 
-    float z[NV][8], keep[kKeep];
-    // Logits of chunk k: the dense ones in z, -inf where the mask or the table takes them away;
-    // the table's, taken one by one by each(y, i), i counting this thread's.
-    auto take_chunk = [&](int k, bool table_kept, auto&& each) {
+    float z[NV][8];
+    // The logits of chunk k as they are after penalties, biases and the mask.
+    auto take_chunk = [&](int k) {
       const int base = first + k * L::kTokens;
       uint32_t allowed[NV];
 #pragma unroll
@@ -334,10 +342,27 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
           }
         }
       }
-      if (use_table && !table_kept) make_table(k, other || MULTI);
+      if (listed) make_entries(k, other || MULTI);
       const bool staged = !MULTI && a.staged;
       if (staged && bulk && !mbar_wait(&s.landed, nth & 1) && lane == 0)
         atomicOr(a.err, VAS_DEV_TIMEOUT);
+      if (listed)
+        for (int e = tid; e < n_entries; e += kThreads) {
+          const int at = places[e];
+          const uint32_t w = words[e];
+          const bool here = staged && (uint32_t)((at + 1) * sizeof(T)) <= bulk;
+          float y = widen1(here ? stage[at] : in[base + at]);
+          if (w & (kCountMask | kPrompt)) y = y > 0.f ? y / rep : y * rep;
+          if (w & kCountMask) y = y - freq * (float)(w & kCountMask) - pres;
+          if (w >> kBiasShift) {
+            const int head = (int)(w >> kBiasShift) - 1;
+            float sum = s.bias[head];  // in list order
+            for (int i = head + 1; i < nb; ++i)
+              if (s.bias_tok[i] == base + at) sum += s.bias[i];
+            y += sum;
+          }
+          values[e] = y;
+        }
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int x0 = base + L::at(v, 0);
@@ -351,34 +376,34 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
           }
         }
       }
-      if (use_table)
-        for (int i = tid; i < a.words / 32; i += kThreads) {
-          int nth_one = 0;
-          for (uint32_t bits = map[i]; bits; bits &= bits - 1, ++nth_one) {
-            const int x = base + 32 * i + __ffs(bits) - 1;
-            each(adjusted(widen1(in[x]), x, base), i == tid ? nth_one : kKeep, x);
-          }
-        }
+      if (listed || staged) __syncthreads();  // the entries are adjusted, the row has been read
+      if (staged && tid == 0 && row + 1 < row1) fetch(row + 1);
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
-        uint32_t on = allowed[v];
-        if (use_table) {
-          // (The table ends with the slice, before the registers' last places may.)
+        if (listed) {
           if (VEC) {
             const int at = L::at(v, 0);
-            if (at < a.words) on &= ~(uint32_t)reinterpret_cast<const uint8_t*>(map)[at >> 3];
+            const uint32_t w = map[at >> 5];
+            uint32_t bits = (w >> (at & 31)) & 0xff;
+            if (bits) {
+              int e0 = (int)rank0[at >> 5] + __popc(w & ((1u << (at & 31)) - 1));
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if ((bits >> e) & 1) z[v][e] = values[e0++];
+            }
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int at = L::at(v, e);
-              if (at < a.words) on &= ~(((map[at >> 5] >> (at & 31)) & 1) << e);
+              const uint32_t w = map[at >> 5], below = (1u << (at & 31)) - 1;
+              if (w & (below + 1)) z[v][e] = values[(int)rank0[at >> 5] + __popc(w & below)];
             }
           }
         }
-        if (on != 0xff) {
+        if (allowed[v] != 0xff) {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            if (!((on >> e) & 1)) z[v][e] = -INFINITY;
+            if (!((allowed[v] >> e) & 1)) z[v][e] = -INFINITY;
         }
       }
     };
@@ -400,41 +425,12 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
         }
       }
     };
-    // The table's tokens behind the dense ones, whose stores they replace.
-    auto store_table = [&](int k, auto&& value) {
-      if (!use_table) return;
-      const int base = first + k * L::kTokens;
-      __syncthreads();
-      for (int i = tid; i < a.words / 32; i += kThreads) {
-        int nth_one = 0;
-        for (uint32_t bits = map[i]; bits; bits &= bits - 1, ++nth_one) {
-          const int x = base + 32 * i + __ffs(bits) - 1;
-          float y;
-          if (!MULTI && i == tid && nth_one < kKeep)
-            y = nth_one == 0 ? keep[0] : (nth_one == 1 ? keep[1] : (nth_one == 2 ? keep[2] : keep[3]));
-          else y = adjusted(widen1(in[x]), x, base);
-          out[x] = value(y, x);
-        }
-      }
-    };
-    auto held = [&](float y, int i) {
-      if (i == 0) keep[0] = y;
-      else if (i == 1) keep[1] = y;
-      else if (i == 2) keep[2] = y;
-      else if (i == 3) keep[3] = y;
-    };
-    // The next row into the place that all threads have read.
-    auto fetch_next = [&] {
-      if (MULTI || !a.staged) return;
-      __syncthreads();
-      if (tid == 0 && row + 1 < row1) fetch(row + 1);
-    };
 
     const int chunks = MULTI ? a.chunks : 1;
+    seq = b;
     if (!a.probs) {
       for (int k = 0; k < chunks; ++k) {
-        take_chunk(k, false, [&](float y, int i, int) { held(y, i); });
-        fetch_next();
+        take_chunk(k);
         if (bad) {
 #pragma unroll
           for (int v = 0; v < NV; ++v)
@@ -442,9 +438,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
             for (int e = 0; e < 8; ++e) z[v][e] = NAN;
         }
         store_chunk(k);
-        store_table(k, [&](float y, int) { return bad ? NAN : y; });
       }
-      seq = b;
       continue;
     }
 
@@ -456,40 +450,28 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
     const float c = temp > 0.f ? fmaxf(1.4426950408889634f / temp, 0x1p-149f) : NAN;
     float m = -INFINITY, sum = 0.f, ref = 0.f;  // ref: the thread's, 0 where that is not finite
     int best = 0x7fffffff;
-    auto join = [&](float om, float os, int ob) {
-      const float nm = fmaxf(m, om), r = nm == -INFINITY ? 0.f : nm;
-      if (greedy) sum += os;
-      else
-        sum = (m == -INFINITY ? sum : sum * exp2f((m - r) * c)) +
-              (om == -INFINITY ? os : os * exp2f((om - r) * c));
-      best = om > m || (om == m && ob < best) ? ob : best;
-      m = nm;
+    auto rescaled = [&](float v, float from, float to) {
+      return greedy || from == -INFINITY ? v : v * exp2f((from - to) * c);
     };
     for (int k = 0; k < chunks; ++k) {
-      take_chunk(k, false, [&](float y, int i, int x) {
-        held(y, i);
-        join(y, isnan(y) ? NAN : (greedy || y == -INFINITY ? 0.f : 1.f), x);
-      });
-      fetch_next();
-      float cm = -INFINITY;
+      take_chunk(k);
+      float cm = -INFINITY, cs = 0.f;
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int e = 0; e < 8; ++e) cm = fmaxf(cm, z[v][e]);
       if (greedy) {
         int at = 0x7fffffff;
-        float wild = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            if (isnan(z[v][e])) wild = NAN;
+            if (isnan(z[v][e])) cs = NAN;
             if (z[v][e] == cm) at = min(at, first + k * L::kTokens + L::at(v, e));
           }
-        join(cm, wild, at);
+        best = cm > m || (cm == m && at < best) ? at : best;
       } else {
         ref = cm == -INFINITY ? 0.f : cm;
-        float cs = 0.f;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -498,20 +480,28 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
             if (!MULTI) z[v][e] = y;
             cs += y;
           }
-        join(cm, cs, 0);
       }
+      const float nm = fmaxf(m, cm);
+      sum = MULTI ? rescaled(sum, m, nm) + rescaled(cs, cm, nm) : cs;
+      m = nm;
     }
+    // Within the lanes of a warp that hold (m, sum, best); lanes without have -inf, 0 and no token.
+    auto join_warp = [&] {
+      const float top = unordered(__reduce_max_sync(0xffffffffu, ordered(m)));
+      sum = rescaled(sum, m, top);
 #pragma unroll
-    for (int o = 16; o; o >>= 1)
-      join(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o),
-           __shfl_xor_sync(0xffffffffu, best, o));
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      best = (int)__reduce_min_sync(0xffffffffu, m == top ? (uint32_t)best : 0x7fffffffu);
+      m = top;
+    };
+    join_warp();
     if (lane == 0) {
       s.red_max[warp] = m;
       s.red_sum[warp] = sum;
       s.red_at[warp] = best;
     }
     __syncthreads();
-    if (arrived) {  // no table: the cluster is there
+    if (arrived) {
       arrived = false;
       cluster_wait();
     }
@@ -520,10 +510,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
       m = lane < kWarps ? s.red_max[lane] : -INFINITY;
       sum = lane < kWarps ? s.red_sum[lane] : 0.f;
       best = lane < kWarps ? s.red_at[lane] : 0x7fffffff;
-#pragma unroll
-      for (int o = kWarps / 2; o; o >>= 1)
-        join(__shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, sum, o),
-             __shfl_xor_sync(0xffffffffu, best, o));
+      join_warp();
       if (lane < C) {
         peer_store(peer_address(&s.peer_max[side][rank], lane), __float_as_uint(m));
         peer_store(peer_address(&s.peer_sum[side][rank], lane), __float_as_uint(sum));
@@ -532,31 +519,33 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
     }
     cluster_arrive();
     cluster_wait();
-    m = s.peer_max[side][0], sum = s.peer_sum[side][0], best = s.peer_at[side][0];
-    for (int r = 1; r < C; ++r) join(s.peer_max[side][r], s.peer_sum[side][r], s.peer_at[side][r]);
+    m = lane < C ? s.peer_max[side][lane] : -INFINITY;
+    sum = lane < C ? s.peer_sum[side][lane] : 0.f;
+    best = lane < C ? s.peer_at[side][lane] : 0x7fffffff;
+    join_warp();
     const float row_ref = m == -INFINITY ? 0.f : m;
     const bool wild = bad || isnan(sum);
     // A row without a token is 0 throughout.
     const float inv = wild ? NAN : (m == -INFINITY ? 0.f : 1.f / sum);
     // What the held exponentials, relative to the thread's maximum, are short of the row's.
     const float f = exp2f((ref - row_ref) * c) * inv;
-    auto hot = [&](int x) { return wild ? NAN : (x == best && m != -INFINITY ? 1.f : 0.f); };
     for (int k = 0; k < chunks; ++k) {
-      if (MULTI) take_chunk(k, false, [](float, int, int) {});
+      if (MULTI) take_chunk(k);
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          if (greedy) z[v][e] = hot(first + k * L::kTokens + L::at(v, e));
-          else if (MULTI) z[v][e] = ex2_approx((z[v][e] - row_ref) * c) * inv;
-          else z[v][e] *= f;
+          if (greedy) {
+            const int x = first + k * L::kTokens + L::at(v, e);
+            z[v][e] = wild ? NAN : (x == best && m != -INFINITY ? 1.f : 0.f);
+          } else if (MULTI) {
+            z[v][e] = ex2_approx((z[v][e] - row_ref) * c) * inv;
+          } else {
+            z[v][e] *= f;
+          }
         }
       store_chunk(k);
-      store_table(k, [&](float y, int x) {
-        return greedy ? hot(x) : ex2_approx((y - row_ref) * c) * inv;
-      });
     }
-    seq = b;
   }
   if (arrived) cluster_wait();
 }
@@ -565,6 +554,14 @@ namespace {
 
 bool misaligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0;
+}
+
+// Entries that a stretch of so many tokens can have, in whole groups of 16 bytes of places.
+constexpr int kEntryBytes = 10;
+int entries_of(const Args& a, int tokens) {
+  if (!a.counted && a.max_bias == 0) return 0;
+  const int64_t most = (int64_t)(a.counted ? a.max_tokens + a.n : 0) + a.max_bias;
+  return (int)((std::min<int64_t>(most, tokens) + 8) / 8 * 8);
 }
 
 template <typename T, bool VEC, int NV, bool MULTI>
@@ -580,14 +577,12 @@ int launch(Args& a, cudaStream_t stream) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   });
   if (attr_err[dev] != cudaSuccess) return VAS_E_CUDA;
-  const bool table = a.counted || a.max_bias > 0;
   a.chunks = MULTI ? (a.slice + kTokens - 1) / kTokens : 1;
-  // Whole 16-byte groups of map words.
-  a.words = table ? ((MULTI ? kTokens : a.slice) + 127) / 128 * 128 : 0;
-  const int fixed = a.words * 4 + a.words / 8;
+  a.entries = entries_of(a, MULTI ? kTokens : a.slice);
+  const int fixed = a.entries * kEntryBytes;
   const int place = (int)((a.slice * sizeof(T) + 15) / 16 * 16);
   // Rows by bulk copy where two CTAs of an SM still have room for it.
-  a.staged = VEC && !MULTI && fixed + place <= 100 * 1024;
+  a.staged = VEC && !MULTI && fixed + place <= 96 * 1024;
   const int smem = fixed + (a.staged ? place : 0);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.cluster);
@@ -635,7 +630,7 @@ int launch_size(Args& a, cudaStream_t stream) {
   const int per = (a.slice + kThreads * 8 - 1) / (kThreads * 8);
   if (per <= 1) return launch<T, VEC, 1, false>(a, stream);
   if (per <= 4) return launch<T, VEC, 4, false>(a, stream);
-  if (per <= 8) return launch<T, VEC, 8, false>(a, stream);
+  if (per <= 8 && entries_of(a, a.slice) * kEntryBytes <= 180 * 1024) return launch<T, VEC, 8, false>(a, stream);
   return launch<T, VEC, 4, true>(a, stream);
 }
 
