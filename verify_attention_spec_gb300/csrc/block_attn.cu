@@ -1,19 +1,22 @@
-// Attention over block-scaled 8-bit pages (sm_103a): FP8 E4M3 codes with one fp32 scale per page
-// and KV head (paged_attn_fwd_quant with VAS_FP8_BLOCK).
+// Attention over block-scaled 8-bit pages (sm_103a): FP8 E4M3 or INT8 codes with one fp32 scale per
+// page and KV head (paged_attn_fwd_quant with VAS_FP8_BLOCK and VAS_INT8_BLOCK).
 //
 // A unit is a block of query rows of one KV head against a run of its sequence's tokens, in tiles
 // of 128 tokens.  Both products run on the tensor cores with the codes as they are in memory:
 //     S^T = K Q^T    tokens are the M side (128 of them), the rows N, the head the contraction
 //     O^T = V^T P^T  head elements are M, the rows N, the tile's tokens the contraction
-// so no code is ever expanded, and decode's few rows waste nothing but tensor-core time of which
-// there is plenty: a tile is 32 KB of HBM, 1400 clocks of an SM's share, against 8 products of
-// about 96.  What is not 8 bits wide is split into parts that are:
+// so decode's few rows waste nothing but tensor-core time of which there is plenty: a tile is 32 KB
+// of HBM, 1400 clocks of an SM's share, against 8 products of about 96.
+// FP8: no code is ever expanded; what is not 8 bits wide is split into parts that are:
 //   Q   times a power of two as hi + lo / 32, both E4M3 (8 bits, those of bf16), in columns of
 //       their own; S is their sum.
 //   P   as f16 and that as E5M2 parts in columns of their own: the upper byte of an f16 is its
 //       truncation to E5M2, the remainder is exact, eight times it is the next part's f16, and
 //       four parts hold all 11 bits (three hold 9: a row of few tokens, values near 4, was then
 //       4e-3 off before its rounding to bf16).
+// INT8 (whose own products are slow on this part): four more warps expand the codes to f16, exactly,
+// beside the ring; Q is f16 times a power of two and P f16, one part each.  The expanded operands
+// take the room of a second CTA of the SM.
 // With one scale a page, a tile's scales are at most 8 numbers, one a thread: K's multiplies the
 // scores, V's the weights.
 #include <cuda.h>
@@ -40,11 +43,13 @@ constexpr int kTile = 128;         // tokens of a tile, one a softmax thread
 constexpr int kSoftWarps = 4;
 constexpr int kProducer = 4;       // warp that streams the pages
 constexpr int kMma = 5;            // warp that issues the products
-constexpr int kThreads = 192;
-constexpr int kCtasPerSm = 2;
+constexpr int kConv = 6;            // first of the warps that expand INT8 codes
+constexpr int kConvWarps = 4;
+__host__ __device__ constexpr int threads_of(int kv) { return kv == VAS_FP8_E4M3 ? 192 : 192 + 32 * kConvWarps; }
+__host__ __device__ constexpr int ctas_of(int kv) { return kv == VAS_FP8_E4M3 ? 2 : 1; }  // of an SM
 constexpr int kRing = 4;           // units the producer may run ahead
 constexpr int kScaleTiles = 8;     // tiles whose scales are kept
-constexpr int kParts = 4;          // E5M2 parts of a weight
+__host__ __device__ constexpr int parts_of(int kv) { return kv == VAS_FP8_E4M3 ? 4 : 1; }  // of a weight
 constexpr int kTmemCols = 256;
 constexpr int kTmemS = 0, kTmemO = 128;  // S: two buffers of 64 columns
 // A row's reference moves when a weight times its V scale passes 2^kSlack of it; kBase places
@@ -72,14 +77,19 @@ struct Unit {
 // MR: the most rows a unit of the call has.  Two tiles in flight a CTA left decode waiting for
 // memory (70 us for 64 sequences of 2100 tokens); what the weights of few rows do not take is
 // room for a third.
-template <int D, int MR>
+template <int D, int MR, int KV>
 struct Smem {
+  static constexpr bool kFp8 = KV == VAS_FP8_E4M3;
   static constexpr int kOperand = kTile * D;  // K or V of a tile
   static constexpr int kSlots = (D == 128 ? 1 : 2) * (MR == 8 ? 6 : 5);
-  static constexpr int kQRows = 2 * MR;
-  static constexpr int kPBytes = kTile * MR * kParts;
-  static constexpr int kQOff = kSlots * kOperand;
-  static constexpr int kPOff = kQOff + kQRows * D;
+  static constexpr int kWide = kFp8 ? 0 : 2 * kOperand;  // K or V of a tile in f16
+  // Q: two E4M3 rows a row, or one of f16, at least 16 for the product's N.
+  static constexpr int kQBytes = kFp8 ? 2 * MR * D : (MR < 16 ? 16 : MR) * D * 2;
+  static constexpr int kPBytes = kFp8 ? kTile * MR * 4 : kTile * (MR < 16 ? 16 : MR) * 2;
+  static constexpr int kKOff = kSlots * kOperand;  // expanded K, V (INT8)
+  static constexpr int kVOff = kKOff + kWide;
+  static constexpr int kQOff = kVOff + kWide;
+  static constexpr int kPOff = kQOff + kQBytes;
   static constexpr int kMiscOff = kPOff + kPBytes;
   static_assert(kQOff % 1024 == 0 && kPOff % 128 == 0 && kMiscOff % 16 == 0, "operand tiles");
 };
@@ -89,6 +99,7 @@ constexpr int kMostSlots = 12;
 struct Misc {
   uint64_t full[kMostSlots], empty[kMostSlots];
   uint64_t ufull[kRing], uempty[kRing];
+  uint64_t k_wide, k_free, v_wide;  // INT8: the tile's expanded K is there, is read; V is there
   uint64_t fin, q_full, s_full[2], s_empty[2], p_full, pv_done;
   uint64_t tree[kMaxRows];        // the rows' draft-tree masks, own bit set
   Unit ring[kRing];
@@ -106,13 +117,13 @@ struct Misc {
   int32_t start_seq;
   int64_t start_at;               // where in it this CTA's share begins
   int64_t start_row;              // its first query token
-  int64_t wsum[6][2];
+  int64_t wsum[10][2];
   int32_t any_bad;
 };
 
-template <int D, int MR>
+template <int D, int MR, int KV>
 constexpr int smem_bytes() {
-  return Smem<D, MR>::kMiscOff + (int)sizeof(Misc) + 1024;
+  return Smem<D, MR, KV>::kMiscOff + (int)sizeof(Misc) + 1024;
 }
 
 // ---- the line of work -----------------------------------------------------------------
@@ -175,6 +186,21 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
 __device__ __forceinline__ uint32_t idesc_f8(int m, int n, bool mn_major, bool b_e5m2) {
   return (1u << 4) | (b_e5m2 ? 1u << 10 : 0u) | (mn_major ? (1u << 15) | (1u << 16) : 0u) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// The same of kind::f16 with f16 operands.
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      : "memory");
+}
+// f16 rows of 128 bytes (64 elements), 128-byte swizzle; column blocks `lbo` apart.
+__device__ __forceinline__ uint64_t desc_f16(uint32_t addr, uint32_t lbo) {
+  const uint32_t lo = ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
+  const uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  return ((uint64_t)hi << 32) | lo;
 }
 
 // Shared-memory matrix descriptors: rows of D bytes, swizzled over their length, 8-row groups
@@ -263,7 +289,7 @@ __device__ __forceinline__ float unordered(int i) { return __int_as_float(i >= 0
 // Rows a unit is computed as (RP >= its rows).
 __device__ __forceinline__ int padded_rows(int rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 32); }
 
-template <int D, int MR>
+template <int D, int MR, int KV>
 struct Ctx {
   const Args& a;
   uint8_t* smem;
@@ -275,15 +301,17 @@ struct Ctx {
 // ---- softmax warps -------------------------------------------------------------------
 // The unit's queries as E4M3 pairs in the K-major operand layout; the rows' references, limits
 // and masks.  Returns what brings a score to base 2.
-template <int RP, int D, int MR>
-__device__ __forceinline__ float stage_queries(const Ctx<D, MR>& x, const Unit& u) {
+template <int RP, int D, int MR, int KV>
+__device__ __forceinline__ float stage_queries(const Ctx<D, MR, KV>& x, const Unit& u) {
+  constexpr bool kFp8 = KV == VAS_FP8_E4M3;
   const Args& a = x.a;
   Misc& m = x.m;
   constexpr int kLanes = D / 8;             // of a row, 8 elements each
   constexpr int kAtOnce = 128 / kLanes;     // rows
-  constexpr int kSteps = (RP + kAtOnce - 1) / kAtOnce;
+  constexpr int kRows = !kFp8 && RP < 16 ? 16 : RP;  // of the operand
+  constexpr int kSteps = (kRows + kAtOnce - 1) / kAtOnce;
   const int tid = threadIdx.x, c = tid % kLanes;
-  uint8_t* q_tile = x.smem + Smem<D, MR>::kQOff;
+  uint8_t* q_tile = x.smem + Smem<D, MR, KV>::kQOff;
   uint4 v[kSteps];
   float top = 0.f;
 #pragma unroll
@@ -312,12 +340,18 @@ __device__ __forceinline__ float stage_queries(const Ctx<D, MR>& x, const Unit& 
   const uint32_t all = max(max(m.q_top[0], m.q_top[1]), max(m.q_top[2], m.q_top[3]));
   // 2^e brings the unit's largest magnitude into [128, 256): the remainder of hi is then at most
   // 8, and 32 of it exact in E4M3 for elements down to 2^-15 of the largest (below, 2^-24 of the
-  // largest is lost, as in an fp32 sum of the products).
-  const int e = max(-120, min(120, 7 - ((int)(all >> 23) - 127)));
+  // largest is lost, as in an fp32 sum of the products).  f16: [2^14, 2^15), exact down to 2^-28.
+  const int e = max(-112, min(112, (kFp8 ? 7 : 14) - ((int)(all >> 23) - 127)));
   const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
   for (int i = 0; i < kSteps; ++i) {
     const int r = i * kAtOnce + tid / kLanes;
+    if constexpr (!kFp8) {
+      // Rows of D elements in column blocks of 64: chunk c of 16 bytes.
+      if (kRows % kAtOnce == 0 || r < kRows)
+        *reinterpret_cast<uint4*>(q_tile + (c / 8) * (kRows * 128) + r * 128 + (((c ^ r) & 7) << 4)) =
+            bf16x8_to_f16x8(v[i], mul);
+    } else {
     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     uint32_t hi[2], lo[2];
 #pragma unroll
@@ -353,6 +387,7 @@ __device__ __forceinline__ float stage_queries(const Ctx<D, MR>& x, const Unit& 
       *reinterpret_cast<uint2*>(at(r)) = make_uint2(hi[0], hi[1]);
       *reinterpret_cast<uint2*>(at(RP + r)) = make_uint2(lo[0], lo[1]);
     }
+    }
   }
   return a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
 }
@@ -380,9 +415,11 @@ __device__ __noinline__ bool clear_row(uint8_t* v_row, bool token) {
 
 // One unit; false after a wait that ran out.  Such a warp waits no more but keeps to the barriers
 // of the others, which leave with it at the end of the unit.
-template <int RP, int D, int MR>
-__device__ __forceinline__ bool soft_unit(const Ctx<D, MR>& x, const Unit& u, uint32_t& tile_it) {
-  using S = Smem<D, MR>;
+template <int RP, int D, int MR, int KV>
+__device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u, uint32_t& tile_it) {
+  using S = Smem<D, MR, KV>;
+  constexpr bool kFp8 = KV == VAS_FP8_E4M3;
+  constexpr int kParts = parts_of(KV);
   constexpr int kN = RP * kParts;           // columns of O
   constexpr int kLd = RP < 16 ? RP : 16;    // rows of weights at a time
   const Args& a = x.a;
@@ -409,7 +446,9 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR>& x, const Unit& u, ui
   for (int tile = u.tile0; tile < u.tile1; ++tile, ++tile_it) {
     const int b = tile_it & 1;
     const int slot_v = (2 * tile_it + 1) % S::kSlots;
-    wait_for(&m.full[slot_v], ((2 * tile_it + 1) / S::kSlots) & 1);
+    // V is there, and with it the scales.
+    if (kFp8) wait_for(&m.full[slot_v], ((2 * tile_it + 1) / S::kSlots) & 1);
+    else wait_for(&m.v_wide, tile_it & 1);
     const int st = tile_it % kScaleTiles;
     float vs = m.scales[st][1][tid >> a.log2P];
     // A V scale that is not finite makes its tokens' scores, and so its rows, NaN.
@@ -419,7 +458,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR>& x, const Unit& u, ui
     const int pos = tile * kTile + tid;
     const bool masked = tile * kTile + kTile - 1 > seen_by_all;
     bool poison = false;
-    if (masked && pos > seen_by_all)
+    if (kFp8 && masked && pos > seen_by_all)  // (INT8 codes are numbers, whatever they are)
       poison = clear_row<D>(x.smem + slot_v * S::kOperand + tid * D, pos < u.len);
     // Exponent of the token's V scale, |vs| < 2^ve.
     const float ve = (float)max(-60, min(67, (int)((__float_as_uint(vs) >> 23) & 0xff) - 126));
@@ -438,14 +477,18 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR>& x, const Unit& u, ui
       {
         uint32_t hi[RP], lo[RP];
         tmem_ld<RP>(s_at, hi);
-        tmem_ld<RP>(s_at + RP, lo);
+        if (kFp8) tmem_ld<RP>(s_at + RP, lo);
         tmem_wait_ld();
 #pragma unroll
         for (int r = 0; r < RP; r += 2) {
           const uint64_t h2 = pair(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1]));
-          const uint64_t w2 = pair(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1]));
           const uint64_t neg = *reinterpret_cast<const uint64_t*>(&m.neg_ref[r]);
-          t2[r / 2] = fma2(fma2(w2, c32, h2), ks2, neg);
+          if constexpr (kFp8) {
+            const uint64_t w2 = pair(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1]));
+            t2[r / 2] = fma2(fma2(w2, c32, h2), ks2, neg);
+          } else {
+            t2[r / 2] = fma2(h2, ks2, neg);
+          }
         }
       }
       if (masked) {
@@ -470,11 +513,13 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR>& x, const Unit& u, ui
       for (int r0 = 0; r0 < RP; r0 += 8) {
         uint32_t hi[8], lo[8];
         tmem_ld<8>(s_at + r0, hi);
-        tmem_ld<8>(s_at + RP + r0, lo);
+        if (kFp8) tmem_ld<8>(s_at + RP + r0, lo);
         tmem_wait_ld();
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-          float y = fmaf(fmaf(__uint_as_float(lo[r]), 1.f / 32, __uint_as_float(hi[r])), ks, ve);
+          const float raw = kFp8 ? fmaf(__uint_as_float(lo[r]), 1.f / 32, __uint_as_float(hi[r]))
+                                 : __uint_as_float(hi[r]);
+          float y = fmaf(raw, ks, ve);
           if (isnan(y) || (masked && (poison || dropped(r0 + r)))) y = -INFINITY;
           const int most = __reduce_max_sync(0xffffffffu, ordered(y));
           if (lane == 0) m.warp_max[warp][r0 + r] = unordered(most);
@@ -498,7 +543,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR>& x, const Unit& u, ui
         l2[r] = mul2(l2[r], *reinterpret_cast<const uint64_t*>(&m.alpha[2 * r]));
       if (have_o) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < kN; c0 += 16) {
+        for (int c0 = 0; c0 < kN; c0 += 16) {  // (8 rows of INT8: columns 8 on are of none)
           const uint32_t at = x.tmem + lanes + kTmemO + c0;
           uint32_t o[16];
           tmem_ld<16>(at, o);
@@ -522,7 +567,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR>& x, const Unit& u, ui
     // that of eight times the remainder.
 #pragma unroll
     for (int r0 = 0; r0 < RP; r0 += kLd) {
-      uint32_t part[kParts][kLd / 4];
+      uint32_t part[kParts][kLd / 4], half[kLd / 2];
 #pragma unroll
       for (int r = 0; r < kLd; r += 4) {
         uint32_t h[2];
@@ -537,19 +582,29 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR>& x, const Unit& u, ui
           h[k] = pack_f16x2(y0, y1);
           if (masked && poison) h[k] = 0;  // the rows' NaN is in their sums
         }
+        if constexpr (kFp8) {
 #pragma unroll
-        for (int t = 0; t < kParts; ++t) {
-          part[t][r / 4] = prmt_odd(h[0], h[1]);
-          if (t + 1 < kParts) {
-            h[0] = mul_f16x2(sub_f16x2(h[0], h[0] & 0xff00ff00u), 0x48004800u);
-            h[1] = mul_f16x2(sub_f16x2(h[1], h[1] & 0xff00ff00u), 0x48004800u);
+          for (int t = 0; t < kParts; ++t) {
+            part[t][r / 4] = prmt_odd(h[0], h[1]);
+            if (t + 1 < kParts) {
+              h[0] = mul_f16x2(sub_f16x2(h[0], h[0] & 0xff00ff00u), 0x48004800u);
+              h[1] = mul_f16x2(sub_f16x2(h[1], h[1] & 0xff00ff00u), 0x48004800u);
+            }
           }
+        } else {
+          half[r / 2] = h[0];
+          half[r / 2 + 1] = h[1];
         }
       }
       // The weights' buffer is free once the product of the tile before is done.
       if (r0 == 0 && tile > u.tile0) wait_for(&m.pv_done, (tile_it - 1) & 1);
-      // 16 columns a store: two parts of 8 rows, or one of 16.
-      if constexpr (RP == 8) {
+      // 16 bytes a store: 8 rows of f16; or two parts of 8 rows, or one of 16.
+      if constexpr (!kFp8) {
+#pragma unroll
+        for (int n = 0; n < kLd / 8; ++n)
+          *reinterpret_cast<uint4*>(p_tile + (r0 / 8 + n) * (kTile * 16)) =
+              make_uint4(half[4 * n], half[4 * n + 1], half[4 * n + 2], half[4 * n + 3]);
+      } else if constexpr (RP == 8) {
 #pragma unroll
         for (int n = 0; n < 2; ++n)
           *reinterpret_cast<uint4*>(p_tile + n * (kTile * 16)) =
@@ -623,7 +678,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR>& x, const Unit& u, ui
 // ---- the CTA's share -------------------------------------------------------------------
 // All threads: totals of the call, the share, and where it begins.  The CTA 0 also reports
 // inconsistent lengths and fills the rows of no valid sequence with NaN.
-template <int D>
+template <int D, int kThreads>
 __device__ __forceinline__ int64_t find_share(const Args& a, Misc& m, int64_t* end) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.B + kThreads - 1) / kThreads;
@@ -713,11 +768,12 @@ __device__ __forceinline__ int64_t find_share(const Args& a, Misc& m, int64_t* e
   return first;
 }
 
-template <int D, int MR>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+template <int D, int MR, int KV>
+__global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
     block_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const Args a) {
-  using S = Smem<D, MR>;
+  using S = Smem<D, MR, KV>;
+  constexpr bool kFp8 = KV == VAS_FP8_E4M3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -726,14 +782,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(&m.full[i], 1);
-      mbar_init(&m.empty[i], 1);
+      mbar_init(&m.empty[i], kFp8 ? 1 : kConvWarps);
     }
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&m.ufull[i], 1);
-      mbar_init(&m.uempty[i], kSoftWarps + 1);
+      mbar_init(&m.uempty[i], kSoftWarps + 1 + (kFp8 ? 0 : kConvWarps));
     }
     mbar_init(&m.q_full, 1);
     mbar_init(&m.fin, 1);
+    mbar_init(&m.k_wide, kConvWarps);
+    mbar_init(&m.k_free, 1);
+    mbar_init(&m.v_wide, kConvWarps);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&m.s_full[i], 1);
       mbar_init(&m.s_empty[i], kSoftWarps);
@@ -750,10 +809,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Ctx<D, MR> x{a, smem, m, m.tmem, warp, lane};
+  const Ctx<D, MR, KV> x{a, smem, m, m.tmem, warp, lane};
   pdl_wait_prior_grid();
   int64_t end;
-  const int64_t first = find_share<D>(a, m, &end);
+  const int64_t first = find_share<D, threads_of(KV)>(a, m, &end);
   bool ok = true;
 
   if (warp == kProducer) {
@@ -898,19 +957,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // ---- products: one lane ----
     if (lane == 0) {
       uint32_t unit_it = 0, tile_it = 0;
-      const uint32_t ring_at = smem_u32(smem);
-      const uint64_t q_desc = desc_rows<D>(smem_u32(smem + S::kQOff));
-      auto scores = [&](uint32_t it, uint32_t idesc) {
+      const uint32_t ring_at = smem_u32(smem), q_at = smem_u32(smem + S::kQOff);
+      auto scores = [&](uint32_t it, int rp) {
         const uint32_t k_it = 2 * it;
         const int slot = k_it % S::kSlots, b = it & 1;
-        if (!wait(&m.full[slot], (k_it / S::kSlots) & 1)) return false;
+        if (!(kFp8 ? wait(&m.full[slot], (k_it / S::kSlots) & 1) : wait(&m.k_wide, it & 1))) return false;
         if (!wait(&m.s_empty[b], ((it >> 1) & 1) ^ 1)) return false;
         tc_fence_after();
-        const uint64_t k_desc = desc_rows<D>(ring_at + slot * S::kOperand);
+        if constexpr (kFp8) {
+          const uint32_t idesc = idesc_f8(128, 2 * rp, false, false);
+          const uint64_t k_desc = desc_rows<D>(ring_at + slot * S::kOperand), q_desc = desc_rows<D>(q_at);
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-          mma_f8(x.tmem + kTmemS + 64 * b, k_desc + 2 * k, q_desc + 2 * k, idesc, k > 0);
-        umma_commit(&m.empty[slot]);
+          for (int k = 0; k < D / 32; ++k)
+            mma_f8(x.tmem + kTmemS + 64 * b, k_desc + 2 * k, q_desc + 2 * k, idesc, k > 0);
+          umma_commit(&m.empty[slot]);
+        } else {
+          const int n = max(rp, 16);
+          const uint32_t idesc = umma_idesc_bf16(128, n, false, false, true);
+          const uint64_t k_desc = desc_f16(ring_at + S::kKOff, 16), q_desc = desc_f16(q_at, 16);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)  // 64 elements a column block
+            mma_f16(x.tmem + kTmemS + 64 * b, k_desc + (k / 4) * ((kTile * 128) >> 4) + 2 * (k % 4),
+                    q_desc + (k / 4) * ((n * 128) >> 4) + 2 * (k % 4), idesc, k > 0);
+          umma_commit(&m.k_free);
+        }
         umma_commit(&m.s_full[b]);
         return true;
       };
@@ -922,28 +992,36 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         mbar_arrive(&m.uempty[slot_u]);
         if (tile0 >= tile1) break;
         const int rp = padded_rows(rows);
-        const uint32_t id_s = idesc_f8(128, 2 * rp, false, false);
-        const uint32_t id_o = idesc_f8(D, kParts * rp, true, true);
         ok = wait(&m.q_full, unit_it & 1);
         ++unit_it;
         if (!ok) break;
         tc_fence_after();
         const int n = tile1 - tile0;
-        ok = scores(tile_it, id_s);
+        ok = scores(tile_it, rp);
         for (int i = 0; i < n && ok; ++i, ++tile_it) {
-          if (i + 1 < n) ok = scores(tile_it + 1, id_s);
+          if (i + 1 < n) ok = scores(tile_it + 1, rp);
           if (!ok) break;
           const uint32_t v_it = 2 * tile_it + 1;
           const int slot = v_it % S::kSlots;
-          ok = wait(&m.full[slot], (v_it / S::kSlots) & 1) && wait(&m.p_full, tile_it & 1);
+          ok = (kFp8 ? wait(&m.full[slot], (v_it / S::kSlots) & 1) : wait(&m.v_wide, tile_it & 1)) &&
+               wait(&m.p_full, tile_it & 1);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t v_desc = desc_rows<D>(ring_at + slot * S::kOperand);
           const uint64_t p_desc = desc_weights(smem_u32(smem + S::kPOff));
+          if constexpr (kFp8) {
+            const uint32_t idesc = idesc_f8(D, 4 * rp, true, true);
+            const uint64_t v_desc = desc_rows<D>(ring_at + slot * S::kOperand);
 #pragma unroll
-          for (int k = 0; k < kTile / 32; ++k)
-            mma_f8(x.tmem + kTmemO, v_desc + ((32 * D * k) >> 4), p_desc + ((512 * k) >> 4), id_o, i > 0 || k > 0);
-          umma_commit(&m.empty[slot]);
+            for (int k = 0; k < kTile / 32; ++k)
+              mma_f8(x.tmem + kTmemO, v_desc + ((32 * D * k) >> 4), p_desc + ((512 * k) >> 4), idesc, i > 0 || k > 0);
+            umma_commit(&m.empty[slot]);
+          } else {
+            const uint32_t idesc = umma_idesc_bf16(D, max(rp, 16), true, true, true);
+            const uint64_t v_desc = desc_f16(ring_at + S::kVOff, kTile * 128);
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_f16(x.tmem + kTmemO, v_desc + ((16 * 128 * k) >> 4), p_desc + ((256 * k) >> 4), idesc, i > 0 || k > 0);
+          }
           umma_commit(&m.pv_done);
         }
         if (!ok) break;
@@ -953,6 +1031,61 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       mbar_wait(&m.fin, 0);
     }
     ok = __shfl_sync(0xffffffffu, ok, 0);
+  } else if (warp >= kConv) {
+    // ---- INT8: codes to f16, 16 a lane at a time, into the 128-byte-swizzled operands ----
+    if constexpr (!kFp8) {
+      uint32_t unit_it = 0, tile_it = 0;
+      const int cw = warp - kConv;
+      auto expand = [&](const uint8_t* raw, uint8_t* wide) {
+        constexpr int kC = D / 16, kPer = kTile * kC / (32 * kConvWarps);
+        uint4 v[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          v[i] = reinterpret_cast<const uint4*>(raw)[(i * kConvWarps + cw) * 32 + lane];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int at = (i * kConvWarps + cw) * 32 + lane, t = at / kC, c = at % kC;
+          uint4 y[2];
+          s8x4_to_f16x4(v[i].x, y[0].x, y[0].y);
+          s8x4_to_f16x4(v[i].y, y[0].z, y[0].w);
+          s8x4_to_f16x4(v[i].z, y[1].x, y[1].y);
+          s8x4_to_f16x4(v[i].w, y[1].z, y[1].w);
+          uint8_t* row = wide + (c / 4) * (kTile * 128) + t * 128;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<uint4*>(row + (((2 * (c % 4) + h) ^ (t & 7)) << 4)) = y[h];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      for (;;) {
+        const int slot_u = unit_it % kRing;
+        ok = wait(&m.ufull[slot_u], (unit_it / kRing) & 1);
+        if (!ok) break;
+        const int n = m.ring[slot_u].tile1 - m.ring[slot_u].tile0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.uempty[slot_u]);
+        ++unit_it;
+        if (n <= 0) break;
+        for (int i = 0; i < n && ok; ++i, ++tile_it) {
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const uint32_t it = 2 * tile_it + o;
+            const int slot = it % S::kSlots;
+            // The operand of the tile before has been read: by its scores, by its product.
+            ok = wait(&m.full[slot], (it / S::kSlots) & 1) &&
+                 wait(o ? &m.pv_done : &m.k_free, (tile_it & 1) ^ 1);
+            if (!ok) break;
+            expand(smem + slot * S::kOperand, smem + (o ? S::kVOff : S::kKOff));
+            if (lane == 0) {
+              mbar_arrive(&m.empty[slot]);
+              mbar_arrive(o ? &m.v_wide : &m.k_wide);
+            }
+          }
+        }
+        if (!ok) break;
+      }
+    }
   } else {
     // ---- softmax ----
     uint32_t unit_it = 0, tile_it = 0;
@@ -1065,8 +1198,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // Codes as (D bytes, num_pages * P tokens, Hkv); a box, one page of one head, lands as P rows of
-// D bytes swizzled over their length.
-bool encode(CUtensorMap* map, const void* base, int D, int P, int Hkv, int num_pages) {
+// D bytes, swizzled over their length (FP8) or as they are.
+bool encode(CUtensorMap* map, const void* base, int D, int P, int Hkv, int num_pages, bool swizzled) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)num_pages * P, (cuuint64_t)Hkv};
@@ -1075,7 +1208,8 @@ bool encode(CUtensorMap* map, const void* base, int D, int P, int Hkv, int num_p
   const cuuint32_t one[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE,
-            D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE
+                      : (D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B),
             // a row of one head is D <= 128 bytes: more would fetch the next head's too
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1095,22 +1229,24 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, int smem, c
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D, int MR>
+template <int D, int MR, int KV>
 int launch_attn(Args& a, const void* k_pages, const void* v_pages, int sms, cudaStream_t stream) {
   static std::once_flag once[kMaxCachedDevices];
   static cudaError_t attr_err[kMaxCachedDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxCachedDevices) return VAS_E_CUDA;
   std::call_once(once[dev], [&] {
-    attr_err[dev] = cudaFuncSetAttribute(block_attn_kernel<D, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes<D, MR>());
+    attr_err[dev] = cudaFuncSetAttribute(block_attn_kernel<D, MR, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         smem_bytes<D, MR, KV>());
   });
   if (attr_err[dev] != cudaSuccess) return VAS_E_CUDA;
   CUtensorMap mk, mv;
-  if (!encode(&mk, k_pages, D, a.P, a.Hkv, a.num_pages) || !encode(&mv, v_pages, D, a.P, a.Hkv, a.num_pages))
+  constexpr bool kFp8 = KV == VAS_FP8_E4M3;
+  if (!encode(&mk, k_pages, D, a.P, a.Hkv, a.num_pages, kFp8) ||
+      !encode(&mv, v_pages, D, a.P, a.Hkv, a.num_pages, kFp8))
     return VAS_E_CUDA;
-  const int ctas = kCtasPerSm * sms;
-  cudaError_t e = launch_pdl(block_attn_kernel<D, MR>, dim3(ctas), kThreads, smem_bytes<D, MR>(), stream, mk, mv, a);
+  const int ctas = ctas_of(KV) * sms;
+  cudaError_t e = launch_pdl(block_attn_kernel<D, MR, KV>, dim3(ctas), threads_of(KV), smem_bytes<D, MR, KV>(), stream, mk, mv, a);
   // A sequence that fits the tables has at most maxp * P tokens: where that is what is never
   // cut, nothing is to be merged.
   if (e == cudaSuccess && (int64_t)a.maxp * a.P > kWholeTiles * kTile)
@@ -1125,7 +1261,7 @@ int launch_attn(Args& a, const void* k_pages, const void* v_pages, int sms, cuda
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 int cta_count() {
   const int sms = vas::num_sms();
-  return kCtasPerSm * (sms > 0 ? sms : 160);
+  return ctas_of(VAS_FP8_E4M3) * (sms > 0 ? sms : 160);  // INT8 has fewer
 }
 
 }  // namespace
@@ -1136,7 +1272,8 @@ size_t workspace_bytes(int head_dim) {
          n * kMaxRows * head_dim * sizeof(float);
 }
 
-int launch(Args a, const void* k_pages, const void* v_pages, int head_dim, void* workspace, cudaStream_t stream) {
+int launch(Args a, const void* k_pages, const void* v_pages, int head_dim, bool fp8, void* workspace,
+           cudaStream_t stream) {
   const int sms = vas::num_sms();
   if (!sms) return VAS_E_CUDA;
   const size_t n = 2 * (size_t)cta_count();
@@ -1155,11 +1292,18 @@ int launch(Args a, const void* k_pages, const void* v_pages, int head_dim, void*
   a.parts = (a.G + kMaxRows - 1) / kMaxRows;
   a.part_rows = (a.G + a.parts - 1) / a.parts;
   a.parts = (a.G + a.part_rows - 1) / a.part_rows;
+  if (fp8) {
+    if (head_dim == 128)
+      return few ? launch_attn<128, 8, VAS_FP8_E4M3>(a, k_pages, v_pages, sms, stream)
+                 : launch_attn<128, kMaxRows, VAS_FP8_E4M3>(a, k_pages, v_pages, sms, stream);
+    return few ? launch_attn<64, 8, VAS_FP8_E4M3>(a, k_pages, v_pages, sms, stream)
+               : launch_attn<64, kMaxRows, VAS_FP8_E4M3>(a, k_pages, v_pages, sms, stream);
+  }
   if (head_dim == 128)
-    return few ? launch_attn<128, 8>(a, k_pages, v_pages, sms, stream)
-               : launch_attn<128, kMaxRows>(a, k_pages, v_pages, sms, stream);
-  return few ? launch_attn<64, 8>(a, k_pages, v_pages, sms, stream)
-             : launch_attn<64, kMaxRows>(a, k_pages, v_pages, sms, stream);
+    return few ? launch_attn<128, 8, VAS_INT8>(a, k_pages, v_pages, sms, stream)
+               : launch_attn<128, kMaxRows, VAS_INT8>(a, k_pages, v_pages, sms, stream);
+  return few ? launch_attn<64, 8, VAS_INT8>(a, k_pages, v_pages, sms, stream)
+             : launch_attn<64, kMaxRows, VAS_INT8>(a, k_pages, v_pages, sms, stream);
 }
 
 }  // namespace battn

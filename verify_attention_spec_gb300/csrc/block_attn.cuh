@@ -49,7 +49,7 @@ struct Args {
 
 size_t workspace_bytes(int head_dim);
 // Returns a status code; the workspace holds workspace_bytes(head_dim).
-int launch(Args a, const void* k_pages, const void* v_pages, int head_dim, void* workspace,
+int launch(Args a, const void* k_pages, const void* v_pages, int head_dim, bool fp8, void* workspace,
            cudaStream_t stream);
 
 }  // namespace battn

@@ -699,9 +699,8 @@ struct AttnArgs {
   float scale;
   int32_t* err;
   const uint64_t* tree_mask;  // draft-tree visibility per query token, or null (causal)
-  const float* k_scale;       // quantised pools: [num_pages, Hkv, P] fp32, or with
-  const float* v_scale;       // block_scale [num_pages, Hkv]
-  int32_t block_scale;
+  const float* k_scale;       // quantised pools: [num_pages, Hkv, P] fp32
+  const float* v_scale;
 };
 
 template <int D, int KQ = kKvBf16>
@@ -1632,12 +1631,6 @@ __global__ void __launch_bounds__(KQ == kKvBf16 ? kThreads : kThreadsQ, 1)
           const int npg = min(32, it.page_end - pg0);
           const int32_t my_id =
               pg0 == it.page_begin ? bt_cur : (lane < npg ? bt_row[pg0 + lane] : 0);
-          // One scale a page and head: those of up to 32 pages, one a lane.
-          float my_ks = 0.f, my_vs = 0.f;
-          if (kQuant && a.block_scale && lane < npg && my_id >= 0 && my_id < a.num_pages) {
-            my_ks = a.k_scale[(size_t)my_id * a.Hkv + head];
-            my_vs = a.v_scale[(size_t)my_id * a.Hkv + head];
-          }
           for (int s0 = 0; s0 < npg; s0 += PPS) {
             const int slot_s = stage_it % kSlots;
             ok = mbar_wait(&empty[slot_s], ((stage_it / kSlots) & 1) ^ 1);
@@ -1651,15 +1644,8 @@ __global__ void __launch_bounds__(KQ == kKvBf16 ? kThreads : kThreadsQ, 1)
               ids[e] = __shfl_sync(0xffffffffu, my_id, (s0 + e) & 31);
               if (e < n_in) {
                 if (ids[e] < 0 || ids[e] >= a.num_pages) bad = 1;
-                else bytes += kQuant ? 2u * (P * D + (a.block_scale ? 0 : P * 4)) : 2u * kPageBytes;
+                else bytes += kQuant ? 2u * (P * D + P * 4) : 2u * kPageBytes;
               }
-            }
-            if (kQuant && a.block_scale) {  // lane: token of the stage
-              const int src = (s0 + lane / P) & 31;
-              float* sc = stage_scales + slot_s * 2 * kStageTokens + lane;
-              sc[0] = __shfl_sync(0xffffffffu, my_ks, src);
-              sc[kStageTokens] = __shfl_sync(0xffffffffu, my_vs, src);
-              __syncwarp();
             }
             if (kQuant && lane == 0) {
               // Codes: one box per page and operand, [P tokens][D bytes], into the upper
@@ -1676,11 +1662,9 @@ __global__ void __launch_bounds__(KQ == kKvBf16 ? kThreads : kThreadsQ, 1)
                 if (e < n_in && ids[e] >= 0 && ids[e] < a.num_pages) {
                   tma_load_3d(kdst + e * P * D, &tm_k, &full[slot_s], 0, ids[e] * P, head, pol);
                   tma_load_3d(vdst + e * P * D, &tm_v, &full[slot_s], 0, ids[e] * P, head, pol);
-                  if (!a.block_scale) {
-                    const size_t so = ((size_t)ids[e] * a.Hkv + head) * P;
-                    bulk_load(ksd + e * P, a.k_scale + so, P * 4, &full[slot_s], pol);
-                    bulk_load(vsd + e * P, a.v_scale + so, P * 4, &full[slot_s], pol);
-                  }
+                  const size_t so = ((size_t)ids[e] * a.Hkv + head) * P;
+                  bulk_load(ksd + e * P, a.k_scale + so, P * 4, &full[slot_s], pol);
+                  bulk_load(vsd + e * P, a.v_scale + so, P * 4, &full[slot_s], pol);
                 }
               }
             }
@@ -2767,8 +2751,6 @@ bool kv_block(const vas_attn_dims* d) {
   return d->kv_dtype == VAS_FP8_BLOCK || d->kv_dtype == VAS_INT8_BLOCK;
 }
 
-bool own_block_kernel(const vas_attn_dims* d) { return d->kv_dtype == VAS_FP8_BLOCK; }
-
 bool kv_quantized(const vas_attn_dims* d) {
   return d->kv_dtype == VAS_FP8_E4M3 || d->kv_dtype == VAS_INT8 || kv_block(d);
 }
@@ -2929,13 +2911,13 @@ extern "C" {
 
 size_t paged_attn_workspace_min(const vas_attn_dims* dims) {
   if (!dims_ok(dims) || !dims_supported(dims)) return 0;
-  if (own_block_kernel(dims)) return vas::battn::workspace_bytes(dims->head_dim);
+  if (kv_block(dims)) return vas::battn::workspace_bytes(dims->head_dim);
   return make_layout(dims, items_min(dims), 0).total;
 }
 
 size_t paged_attn_workspace_size(const vas_attn_dims* dims) {
   if (!dims_ok(dims) || !dims_supported(dims)) return 0;
-  if (own_block_kernel(dims)) return vas::battn::workspace_bytes(dims->head_dim);
+  if (kv_block(dims)) return vas::battn::workspace_bytes(dims->head_dim);
   // Room for every output row to be split 8 ways on average.
   const int64_t pcap = (int64_t)dims->total_q_tokens * dims->num_q_heads * 8;
   return make_layout(dims, items_min(dims) + items_extra(vas::num_sms()),
@@ -3025,7 +3007,7 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
   if (d.num_pages == 0 || d.max_pages_per_seq == 0) return VAS_E_INVALID_ARG;
   if ((int64_t)d.num_pages * d.page_size > INT32_MAX) return VAS_E_INVALID_ARG;
 
-  if (own_block_kernel(dims)) {
+  if (kv_block(dims)) {
     if (workspace_bytes < vas::battn::workspace_bytes(d.head_dim)) return VAS_E_WORKSPACE;
     vas::battn::Args b{};
     b.q = q;
@@ -3049,8 +3031,8 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
         (d.scale > 0.f ? d.scale : 1.0f / std::sqrt((float)d.head_dim)) * 1.4426950408889634f;
     b.err = vas::device_error_word();
     if (!b.err) return VAS_E_CUDA;
-    return vas::battn::launch(b, k_pages, v_pages, d.head_dim, workspace,
-                              reinterpret_cast<cudaStream_t>(stream_));
+    return vas::battn::launch(b, k_pages, v_pages, d.head_dim, d.kv_dtype == VAS_FP8_BLOCK,
+                              workspace, reinterpret_cast<cudaStream_t>(stream_));
   }
 
   Layout lay;
@@ -3157,7 +3139,6 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
   aa.tree_mask = tree_mask;
   aa.k_scale = k_scale;
   aa.v_scale = v_scale;
-  aa.block_scale = kv_block(dims) ? 1 : 0;
 
   if (prefix) {
     PrefixArgs px;
@@ -3193,7 +3174,7 @@ int attn_launch(const void* q, const void* k_pages, const void* v_pages, const f
     const int grid = sms;
     int st;
     if (quant) {
-      const bool fp8 = d.kv_dtype == VAS_FP8_E4M3 || d.kv_dtype == VAS_FP8_BLOCK;
+      const bool fp8 = d.kv_dtype == VAS_FP8_E4M3;
       if (d.head_dim == 128 && d.page_size == 16)
         st = fp8 ? launch_bf16<128, 16, kKvFp8>(mk, mv, aa, grid, stream)
                  : launch_bf16<128, 16, kKvInt8>(mk, mv, aa, grid, stream);
