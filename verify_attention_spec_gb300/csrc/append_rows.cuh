@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 
 #include <climits>
+#include <cmath>
 #include <cstdint>
 
 #include "../../include/vas.h"
@@ -366,7 +367,154 @@ __device__ __forceinline__ void turn_row(F8& xa, F8& xb, const F8& cs, const F8&
   }
 }
 
-// Keys and values of an append to block-scaled pages (block_cache.cu).
+// KV: the pool's storage type; T: the activations' (float with VAS_F32, bf16 otherwise).
+// ROWS: head rows a lane holds at a time, so a warp has a group of 512 / D * ROWS rows (q
+// heads, then k, then v) in flight.  A task is `iters` consecutive groups of one token: one
+// look-up of the token's place, one read of its table row.  A block scans the lengths once
+// and its warps take tasks gridDim apart; as soon as a row has been taken from its
+// registers the same row of the next group, or task, is fetched into them, so loads are
+// always under way.  INTER: rotary pairs are neighbours.  QUERIES: the rows are the queries'
+// alone.  The whole block: all its warps scan the lengths, those that `takes` tell take the tasks
+// from first_task on, task_stride apart.
+template <typename T, int KV, int D, int ROWS, bool INTER, bool QUERIES>
+__device__ __forceinline__ void append_rows(const AppendArgs& a, Packing& pk, int32_t first_task,
+                                            int32_t task_stride, bool takes) {
+  constexpr int kLanes = D / 16;     // lanes of a row
+  constexpr int kSub = 32 / kLanes;  // rows of a warp at a time
+  constexpr bool kQuant = KV == VAS_FP8_E4M3 || KV == VAS_INT8;
+  const int lane = threadIdx.x & 31;
+  const int H = QUERIES ? a.Hq : a.Hq + 2 * a.Hkv;
+  const uint32_t n_tasks = takes ? (uint32_t)a.T * (uint32_t)a.parts : 0;  // at most INT_MAX
+  const uint32_t stride = task_stride;
+  uint32_t task = takes ? first_task : 0;
+
+  const int c = lane % kLanes;
+  const Chunks ch = lane_chunks<D, INTER>(c, a.rot);
+  const bool turned = ch.turned;
+  const int ca = ch.a, cb = ch.b;
+
+  // A row's values are on their way while the place of its token is looked up (and, for
+  // the first ones, while the block scans the lengths).
+  Raw<T> x[ROWS];
+  auto fetch = [&](Raw<T>& dst, int32_t t, int32_t r) {
+    if (t < a.T && r < H) {
+      const T* p;
+      if (QUERIES || r < a.Hq) p = static_cast<const T*>(a.q) + t * a.q_stride + r * D;
+      else if (r < a.Hq + a.Hkv) p = static_cast<const T*>(a.k) + t * a.k_stride + (r - a.Hq) * D;
+      else p = static_cast<const T*>(a.v) + t * a.v_stride + (r - a.Hq - a.Hkv) * D;
+      dst.load(p, ca, cb);
+    } else {
+      dst.zero();
+    }
+  };
+  constexpr int kGroup = kSub * ROWS;
+  int32_t t = (int32_t)(task / (uint32_t)a.parts);
+  int32_t row0 = (int32_t)(task - (uint32_t)t * a.parts) * a.iters * kGroup + lane / kLanes;
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) fetch(x[i], takes ? t : a.T, row0 + i * kSub);
+
+  const int32_t step = (a.B + kAppendSeqs - 1) / kAppendSeqs;
+  scan_lengths(a, pk, step);
+  if (blockIdx.x == 0) {  // the call's lengths as a whole
+    bool bad = threadIdx.x == 0 && pk.row0[kAppendSeqs] != a.T;
+    for (int i = threadIdx.x; i < a.B; i += kAppendThreads)
+      bad |= !lengths_ok(a, a.seq_lens[i], a.query_lens[i]);
+    if (bad) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
+  }
+  F8 wa{}, wb{};  // the weights of this lane's chunks, and whose they are
+  int kind = -1;  // 1: q, 0: k
+  while (task < n_tasks) {
+    const Place pl = place_of(a, pk, step, t, lane);
+    if (pl.err && lane == 0) atomicOr(a.err, pl.err);
+
+    // Cosines and sines of this lane's 8 pairs.
+    const uint64_t one = pair(1.f, 1.f);
+    F8 cs{{one, one, one, one}}, sn{{0, 0, 0, 0}};
+    if (turned && !pl.err) {
+      const float* row = a.cos_sin + (size_t)pl.position * a.rot + 8 * c;
+      cs = load_f8(row);
+      sn = load_f8(row + a.rot / 2);
+    }
+
+    task += stride;
+    int32_t t_task = (int32_t)(task / (uint32_t)a.parts);
+    const int32_t row_task =
+        (int32_t)(task - (uint32_t)t_task * a.parts) * a.iters * kGroup + lane / kLanes;
+    if (task >= n_tasks) t_task = a.T;
+    for (int it = 0; it < a.iters; ++it) {
+      const bool last = it + 1 == a.iters;
+      const int32_t t_next = last ? t_task : t, row_next = last ? row_task : row0 + kGroup;
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        const int r = row0 + i * kSub;
+        // A warp's rows past H hold zeros and only take part in the shuffles.
+        const bool is_v = !QUERIES && r >= a.Hq + a.Hkv, is_q = QUERIES || r < a.Hq;
+        F8 xa = widen(x[i].a), xb = widen(x[i].b);
+        fetch(x[i], t_next, row_next + i * kSub);
+        // Nothing for the whole warp (20 heads of 64, 10141 tokens: 21.3 -> 19.7 us).
+        if (r - lane / kLanes >= H) continue;
+        const T* w = static_cast<const T*>(is_q ? a.q_weight : a.k_weight);
+        if (w != nullptr && kind != (int)is_q) {
+          kind = is_q;
+          wa = load_weights(w + ca);
+          wb = load_weights(w + cb);
+        }
+        const float ss = row_squares<kLanes>(xa, xb);
+        if (!is_v) {
+          if (w != nullptr) norm_row<D>(xa, xb, wa, wb, ss, a.eps);
+          if (turned) turn_row<INTER>(xa, xb, cs, sn);
+        }
+        float scale = 1.f;
+        if (!QUERIES && kQuant && __any_sync(0xffffffffu, !is_q)) {
+          // The largest magnitude of the row, by the order of the bits (NaN above infinity).
+          uint32_t m = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float y[4];
+            unpair(xa.p[e], y[0], y[1]);
+            unpair(xb.p[e], y[2], y[3]);
+#pragma unroll
+            for (int f = 0; f < 4; ++f) m = max(m, __float_as_uint(y[f]) & 0x7fffffffu);
+          }
+#pragma unroll
+          for (int o = kLanes / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          scale = __fdiv_rn(__uint_as_float(m), KV == VAS_FP8_E4M3 ? 448.f : 127.f);
+          if (scale == 0.f) scale = 1.f;
+        }
+        if (r >= H) continue;
+        if (is_q) {
+          if (pl.err) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) xa.p[e] = xb.p[e] = pair(NAN, NAN);
+          }
+          T* p = static_cast<T*>(a.q_out) + ((size_t)t * a.Hq + r) * D;
+          store8(p + ca, xa);
+          store8(p + cb, xb);
+          continue;
+        }
+        if (pl.err) continue;
+        const int h = is_v ? r - a.Hq - a.Hkv : r - a.Hq;
+        const size_t at = (((size_t)pl.page * a.P + pl.slot) * a.Hkv + h) * D;
+        if constexpr (kQuant) {
+          uint8_t* p = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) + at;
+          *reinterpret_cast<uint2*>(p + ca) = codes8<KV>(xa, scale);
+          *reinterpret_cast<uint2*>(p + cb) = codes8<KV>(xb, scale);
+          if (c == 0)
+            (is_v ? a.v_scale : a.k_scale)[((size_t)pl.page * a.Hkv + h) * a.P + pl.slot] = scale;
+        } else {
+          T* p = static_cast<T*>(is_v ? a.v_pages : a.k_pages) + at;
+          store8(p + ca, xa);
+          store8(p + cb, xb);
+        }
+      }
+      if (!last) row0 += kGroup;
+    }
+    t = t_task;
+    row0 = row_task;
+  }
+}
+
+// An append to block-scaled pages (block_cache.cu).
 int launch_append_block(const AppendArgs& a, int head_dim, bool fp8, bool inter, vas_stream_t stream);
 
 }  // namespace cache

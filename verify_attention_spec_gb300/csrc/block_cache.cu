@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -25,8 +26,10 @@ namespace cache {
 // fresh page or behind the tokens a page already holds.  A task is one run of one head and
 // operand, and one warp's: it finds the largest magnitude of the run's rows (norm and rotation
 // applied), settles the scale, requantises the tokens the page held if the scale grew, and
-// writes the codes.  The rows are computed twice, once for the magnitude and once for the
-// codes: a page's values would take 128 registers a lane, and the second read comes from L1.
+// writes the codes.  The rows stay in registers as they came, half the size of their values, and
+// are computed twice, for the magnitude and for the codes.
+// Beside these warps, kv_warps of a block's eight, the others take the queries' rows as
+// append_kernel does: one launch, and the pages' chains of look-ups run under the queries' stream.
 struct Runs {
   int32_t row0[kAppendSeqs + 1];  // first packed row of every `step`th sequence
   int32_t run0[kAppendSeqs + 1];  // and its first run; the last ones are the totals
@@ -90,7 +93,7 @@ __device__ __forceinline__ void scan_runs(const AppendArgs& a, Runs& rs, int32_t
 
 // Where a run's tokens come from and go.
 struct Run {
-  int32_t page, slot0, n;  // n = 0: nothing to store
+  int32_t page, slot0, n;  // n = 0, or err: nothing to store
   int32_t t0;              // first packed row
   int32_t pos0;            // and its cache position
   int32_t err;
@@ -124,10 +127,7 @@ __device__ __forceinline__ Run run_at(const AppendArgs& a, const Runs& rs, int32
   r.n = hi_pos - lo_pos;
   r.t0 = (int32_t)row + lo_pos - (L - ql);
   r.pos0 = lo_pos;
-  if (r.page < 0 || r.page >= a.num_pages) {
-    r.err = VAS_DEV_BAD_PAGE;
-    r.n = 0;
-  }
+  if (r.page < 0 || r.page >= a.num_pages) r.err = VAS_DEV_BAD_PAGE;
   return r;
 }
 
@@ -227,83 +227,103 @@ __device__ __forceinline__ void tame(F8& x) {
   }
 }
 
-template <int KV, int D, bool INTER>
-__global__ void __launch_bounds__(kAppendThreads) append_block_kernel(const AppendArgs a) {
+// MAXP: the most tokens of a page.
+template <int KV, int D, int MAXP, int ROWS, bool INTER>
+__global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
+    append_block_kernel(const AppendArgs a, const int kv_warps) {
   using T = __nv_bfloat16;
   constexpr int kLanes = D / 16;     // lanes of a row
   constexpr int kSub = 32 / kLanes;  // rows of a warp at a time
+  constexpr int kSteps = MAXP / kSub;
   __shared__ Runs rs;
+  __shared__ Packing pk;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t step = (a.B + kAppendSeqs - 1) / kAppendSeqs;
   scan_runs(a, rs, step);
-  if (blockIdx.x == 0) {  // the call's lengths as a whole
+  const bool queries = warp >= kv_warps;
+  if (kv_warps < kAppendWarps) {
+    append_rows<T, VAS_BF16, D, ROWS, INTER, true>(a, pk, blockIdx.x * (kAppendWarps - kv_warps) + warp - kv_warps,
+                                                   gridDim.x * (kAppendWarps - kv_warps), queries);
+  } else if (blockIdx.x == 0) {  // the call's lengths as a whole
     bool bad = threadIdx.x == 0 && rs.row0[kAppendSeqs] != a.T;
     for (int64_t i = threadIdx.x; i < a.B; i += kAppendThreads)
       bad |= !lengths_ok(a, a.seq_lens[i], a.query_lens[i]);
     if (bad) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
   }
+  if (queries) return;
   const int c = lane % kLanes, sub = lane / kLanes;
   const Chunks ch = lane_chunks<D, INTER>(c, a.rot);
   const int64_t n_tasks = (int64_t)rs.run0[kAppendSeqs] * 2 * a.Hkv;
-  const int64_t stride = (int64_t)gridDim.x * kAppendWarps;
-  for (int64_t task = (int64_t)blockIdx.x * kAppendWarps + warp; task < n_tasks; task += stride) {
+  const int64_t stride = (int64_t)gridDim.x * kv_warps;
+  F8 wa{}, wb{};
+  if (a.k_weight != nullptr) {
+    wa = load_weights(static_cast<const T*>(a.k_weight) + ch.a);
+    wb = load_weights(static_cast<const T*>(a.k_weight) + ch.b);
+  }
+  for (int64_t task = (int64_t)blockIdx.x * kv_warps + warp; task < n_tasks; task += stride) {
     const int32_t u = (int32_t)(task / (2 * a.Hkv));
     int32_t h = (int32_t)(task - (int64_t)u * 2 * a.Hkv);
     const bool is_v = h >= a.Hkv;
     if (is_v) h -= a.Hkv;
     const Run r = run_at(a, rs, step, u, lane);
-    if (r.err && lane == 0) atomicOr(a.err, r.err);
     if (r.n == 0) continue;
     const T* src = is_v ? static_cast<const T*>(a.v) : static_cast<const T*>(a.k);
     const int64_t src_stride = is_v ? a.v_stride : a.k_stride;
-    const T* w = is_v ? nullptr : static_cast<const T*>(a.k_weight);
-    F8 wa{}, wb{};
-    if (w != nullptr) {
-      wa = load_weights(w + ch.a);
-      wb = load_weights(w + ch.b);
+    // The run's rows; bit i of live: this lane's row of step i is stored (there is one, and its
+    // position is in the table).
+    Raw<T> raw[kSteps];
+    uint32_t live = 0;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      raw[i].zero();
+      const int row = i * kSub + sub;
+      if (row >= r.n) continue;
+      bool ok = true;
+      if (a.rot && a.positions) {
+        const int32_t at = a.positions[r.t0 + row];
+        ok = at >= 0 && at < a.max_position;
+      } else if (a.rot) {
+        ok = r.pos0 + row < a.max_position;
+      }
+      if (!ok && c == 0) atomicOr(a.err, VAS_DEV_BAD_POSITION);
+      if (!ok) continue;
+      live |= 1u << i;
+      raw[i].load(src + (int64_t)(r.t0 + row) * src_stride + (int64_t)h * D, ch.a, ch.b);
     }
-    // Row `row` of the run; false: it is not stored (none, or a position outside the table).
-    auto compute = [&](int row, F8& xa, F8& xb) {
-      Raw<T> x;
-      x.zero();
-      bool live = row < r.n;
-      int32_t at = 0;
-      if (live && a.rot) {  // a token without a place in the table stores no value either
-        at = a.positions ? a.positions[r.t0 + row] : r.pos0 + row;
-        if (at < 0 || at >= a.max_position) {
-          live = false;
-          if (c == 0) atomicOr(a.err, VAS_DEV_BAD_POSITION);
-        }
-      }
-      if (live) x.load(src + (int64_t)(r.t0 + row) * src_stride + (int64_t)h * D, ch.a, ch.b);
-      xa = widen(x.a);
-      xb = widen(x.b);
-      if (!is_v) {
-        const float ss = row_squares<kLanes>(xa, xb);
-        if (w != nullptr) norm_row<D>(xa, xb, wa, wb, ss, a.eps);
-        if (ch.turned && live) {
-          const float* angles = a.cos_sin + (size_t)at * a.rot + 8 * c;
-          turn_row<INTER>(xa, xb, load_f8(angles), load_f8(angles + a.rot / 2));
-        }
-      }
-      return live;
-    };
+    if (r.err) {
+      if (lane == 0) atomicOr(a.err, r.err);
+      continue;
+    }
     const size_t si = (size_t)r.page * a.Hkv + h;
     float* scales = is_v ? a.v_scale : a.k_scale;
     const float old = r.slot0 ? scales[si] : 0.f;
     uint8_t* codes = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) +
                      ((size_t)r.page * a.P * a.Hkv + h) * D;
     const size_t row_bytes = (size_t)a.Hkv * D;
+    auto compute = [&](int i, F8& xa, F8& xb) {
+      xa = widen(raw[i].a);
+      xb = widen(raw[i].b);
+      if (is_v) return;
+      const float ss = row_squares<kLanes>(xa, xb);
+      if (a.k_weight != nullptr) norm_row<D>(xa, xb, wa, wb, ss, a.eps);
+      if (ch.turned && ((live >> i) & 1)) {
+        const int row = i * kSub + sub;
+        const int32_t at = a.positions ? a.positions[r.t0 + row] : r.pos0 + row;
+        const float* angles = a.cos_sin + (size_t)at * a.rot + 8 * c;
+        turn_row<INTER>(xa, xb, load_f8(angles), load_f8(angles + a.rot / 2));
+      }
+    };
 
     uint32_t m = 0;
     bool wild = false;
-    F8 xa, xb;
-    bool live = false;
-    for (int r0 = 0; r0 < r.n; r0 += kSub) {
-      live = compute(r0 + sub, xa, xb);
-      if (live) m = max(m, finite_max(xa, xb, &wild));
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (i * kSub >= r.n) break;
+      F8 xa, xb;
+      compute(i, xa, xb);
+      if ((live >> i) & 1) m = max(m, finite_max(xa, xb, &wild));
     }
     m = __reduce_max_sync(0xffffffffu, m);
     wild = __any_sync(0xffffffffu, wild);
@@ -322,14 +342,17 @@ __global__ void __launch_bounds__(kAppendThreads) append_block_kernel(const Appe
     } else {
       scale = fresh_scale<KV>(top);
     }
-    for (int r0 = 0; r0 < r.n; r0 += kSub) {
-      if (r.n > kSub) live = compute(r0 + sub, xa, xb);
-      if (!live) continue;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (i * kSub >= r.n) break;
+      F8 xa, xb;
+      compute(i, xa, xb);
+      if (!((live >> i) & 1)) continue;
       if (wild) {
         tame<KV>(xa);
         tame<KV>(xb);
       }
-      uint8_t* p = codes + (r.slot0 + r0 + sub) * row_bytes;
+      uint8_t* p = codes + (r.slot0 + i * kSub + sub) * row_bytes;
       *reinterpret_cast<uint2*>(p + ch.a) = codes8<KV>(xa, scale);
       *reinterpret_cast<uint2*>(p + ch.b) = codes8<KV>(xb, scale);
     }
@@ -360,43 +383,48 @@ struct ReadArgs {
   }
 };
 
-// N consecutive elements of one head row as fp32.
+// N consecutive elements of a head row as they are stored ...
 template <int KV, int N>
-__device__ __forceinline__ void read_elements(const void* pages, size_t at, float scale, float (&y)[N]) {
-  if constexpr (KV == VAS_F32) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(pages) + at + i));
-      y[i] = v.x, y[i + 1] = v.y, y[i + 2] = v.z, y[i + 3] = v.w;
-    }
-  } else if constexpr (KV == VAS_BF16) {
-#pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(pages) + at + i));
-      y[i] = bf16_lo_f32(v.x), y[i + 1] = bf16_hi_f32(v.x);
-      y[i + 2] = bf16_lo_f32(v.y), y[i + 3] = bf16_hi_f32(v.y);
-    }
-  } else {
-    uint32_t w[N / 4];
-    const uint8_t* p = static_cast<const uint8_t*>(pages) + at;
-    if constexpr (N == 8) {
+struct Stored {
+  static constexpr int kWords = N * (KV == VAS_F32 ? 4 : (KV == VAS_BF16 ? 2 : 1)) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void* pages, size_t at) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(pages) + at * (kWords * 4 / N));
+    if constexpr (kWords == 1) {
+      w[0] = __ldcs(p);
+    } else if constexpr (kWords == 2) {
       const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
       w[0] = v.x, w[1] = v.y;
     } else {
-      w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
-    }
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      uint32_t lo, hi;
-      if constexpr (KV == VAS_FP8_E4M3) e4m3x4_to_f16x4(w[i], lo, hi);
-      else s8x4_to_f16x4(w[i], lo, hi);
-      f16x2_to_f32(lo, y[4 * i], y[4 * i + 1]);
-      f16x2_to_f32(hi, y[4 * i + 2], y[4 * i + 3]);
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p + i));
+        w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+      }
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) y[i] *= scale;
   }
-}
+  // ... and as fp32.
+  __device__ __forceinline__ void values(float scale, float (&y)[N]) const {
+    if constexpr (KV == VAS_F32) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = __uint_as_float(w[i]);
+    } else if constexpr (KV == VAS_BF16) {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) y[2 * i] = bf16_lo_f32(w[i]), y[2 * i + 1] = bf16_hi_f32(w[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) {
+        uint32_t lo, hi;
+        if constexpr (KV == VAS_FP8_E4M3) e4m3x4_to_f16x4(w[i], lo, hi);
+        else s8x4_to_f16x4(w[i], lo, hi);
+        f16x2_to_f32(lo, y[4 * i], y[4 * i + 1]);
+        f16x2_to_f32(hi, y[4 * i + 2], y[4 * i + 3]);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] *= scale;
+    }
+  }
+};
 
 __device__ __forceinline__ void write_elements(__nv_bfloat16* p, const float (&y)[8]) {
   __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
@@ -407,7 +435,9 @@ __device__ __forceinline__ void write_elements(float* p, const float (&y)[4]) {
 }
 
 // KV: element type of the pool; BLOCK: one scale per page and head.  A warp takes one token
-// at a time; a lane 16 bytes of output at a time, of K and then of V.
+// at a time; a lane 16 bytes of output at a time, of K and then of V, kReadBatch of them in
+// flight, while the next token's page is looked up.  Bytes bound it.
+constexpr int kReadBatch = 4;
 template <int KV, bool BLOCK, typename OUT>
 __global__ void __launch_bounds__(kAppendThreads) read_kernel(const ReadArgs a) {
   constexpr int N = 16 / sizeof(OUT);  // elements of a lane's store
@@ -426,36 +456,56 @@ __global__ void __launch_bounds__(kAppendThreads) read_kernel(const ReadArgs a) 
   }
   const int32_t E = a.Hkv << a.log2D;  // elements of a token's row
   const int64_t stride = (int64_t)gridDim.x * kAppendWarps;
-  for (int64_t t = (int64_t)blockIdx.x * kAppendWarps + warp; t < a.T; t += stride) {
+  // Page and slot of token t; slot -1: of no sequence, or of one with inconsistent lengths.
+  auto place = [&](int64_t t, int32_t& page, int32_t& slot) {
+    page = slot = -1;
+    if (t >= a.T) return;
     const Owner o = owner_of(a, pk, step, (int32_t)t, lane);
-    int32_t page = -1, slot = 0;
-    if (o.ok) {
-      const int32_t pos = o.len - o.count + (int32_t)(t - o.row);
-      page = a.block_table[(size_t)o.seq * a.maxp + (pos >> a.log2P)];
-      slot = pos & (a.P - 1);
-      if (page < 0 || page >= a.num_pages) {
-        page = -1;
-        if (lane == 0) atomicOr(a.err, VAS_DEV_BAD_PAGE);
-      }
-    }
-    for (int32_t e = lane * N; e < 2 * E; e += 32 * N) {
-      const bool is_v = e >= E;
-      const int32_t x = is_v ? e - E : e;
-      float y[N];
-      if (page >= 0) {
-        const int32_t h = x >> a.log2D;
-        float scale = 1.f;
-        if (kQuant) {
-          const size_t si = (size_t)page * a.Hkv + h;
-          scale = (is_v ? a.v_scale : a.k_scale)[BLOCK ? si : si * a.P + slot];
-        }
-        read_elements<KV, N>(is_v ? a.v_pages : a.k_pages, ((size_t)page * a.P + slot) * E + x, scale, y);
-      } else {
+    if (!o.ok) return;
+    const int32_t pos = o.len - o.count + (int32_t)(t - o.row);
+    page = a.block_table[(size_t)o.seq * a.maxp + (pos >> a.log2P)];
+    slot = pos & (a.P - 1);
+  };
+  int32_t next_page, next_slot;
+  int64_t t = (int64_t)blockIdx.x * kAppendWarps + warp;
+  place(t, next_page, next_slot);
+  for (; t < a.T; t += stride) {
+    const int32_t page = next_page;
+    const int32_t slot = next_slot;
+    const bool known = slot >= 0 && page >= 0 && page < a.num_pages;  // else the row is NaN
+    place(t + stride, next_page, next_slot);
+    if (!known && slot >= 0 && lane == 0) atomicOr(a.err, VAS_DEV_BAD_PAGE);
+    for (int32_t e0 = lane * N; e0 < 2 * E; e0 += 32 * N * kReadBatch) {
+      Stored<KV, N> x[kReadBatch];
+      float scale[kReadBatch];
 #pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = NAN;
+      for (int i = 0; i < kReadBatch; ++i) {
+        const int32_t e = e0 + i * 32 * N;
+        const bool is_v = e >= E;
+        const int32_t at = is_v ? e - E : e;
+        scale[i] = 1.f;
+        if (!known || e >= 2 * E) continue;
+        if (kQuant) {
+          const size_t si = (size_t)page * a.Hkv + (at >> a.log2D);
+          scale[i] = (is_v ? a.v_scale : a.k_scale)[BLOCK ? si : si * a.P + slot];
+        }
+        x[i].load(is_v ? a.v_pages : a.k_pages, ((size_t)page * a.P + slot) * E + at);
       }
-      OUT* out = static_cast<OUT*>(is_v ? a.v_out : a.k_out) + t * (is_v ? a.v_stride : a.k_stride) + x;
-      write_elements(out, y);
+#pragma unroll
+      for (int i = 0; i < kReadBatch; ++i) {
+        const int32_t e = e0 + i * 32 * N;
+        if (e >= 2 * E) break;
+        const bool is_v = e >= E;
+        float y[N];
+        if (known) {
+          x[i].values(scale[i], y);
+        } else {
+#pragma unroll
+          for (int k = 0; k < N; ++k) y[k] = NAN;
+        }
+        OUT* out = static_cast<OUT*>(is_v ? a.v_out : a.k_out) + t * (is_v ? a.v_stride : a.k_stride) + (is_v ? e - E : e);
+        write_elements(out, y);
+      }
     }
   }
 }
@@ -484,16 +534,38 @@ bool misaligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0;
 }
 
-template <int KV, int D>
-int launch_block(const AppendArgs& a, bool inter, vas_stream_t stream) {
+template <int KV, int D, int MAXP, int ROWS>
+int launch_block_rows(AppendArgs a, bool inter, vas_stream_t stream) {
   // At most ceil(ql / P) + 1 pages of a sequence, and no more than its tokens.
   int64_t runs = (int64_t)a.T / a.P + 2 * (int64_t)a.B;
   runs = runs < a.T ? runs : a.T;
-  const int64_t want = (runs * 2 * a.Hkv + kAppendWarps - 1) / kAppendWarps;
-  const int64_t most = 4LL * vas::num_sms();
-  const int64_t blocks = want < most ? want : most;
-  return inter ? launch_pdl(append_block_kernel<KV, D, true>, blocks, stream, a)
-               : launch_pdl(append_block_kernel<KV, D, false>, blocks, stream, a);
+  const int64_t kv_tasks = runs * 2 * a.Hkv;
+  // Query rows as in append_kernel: groups of 512 / D * ROWS rows, one or more tasks a token.
+  const int group = 32 / (D / 16) * ROWS;
+  const int64_t most = (int64_t)kAppendBlocks * vas::num_sms();
+  const int64_t groups = (a.Hq + group - 1) / group;
+  int64_t parts = (6 * most * 8 + a.T - 1) / a.T;
+  parts = parts < groups ? parts : groups;
+  if (parts < 1 || parts * a.T > INT_MAX / 2) parts = 1;
+  a.iters = (int32_t)((groups + parts - 1) / parts);
+  a.parts = a.Hq ? (int32_t)((groups + a.iters - 1) / a.iters) : 1;
+  const int64_t q_tasks = a.Hq ? (int64_t)a.T * a.parts : 0;
+  // Two warps of a block for the pages when the queries' bytes are the most of the call; more when
+  // tasks are few and their latency counts.
+  const int kv_warps = !a.Hq ? 8 : (kv_tasks > most * 16 ? 2 : 6);
+  int64_t blocks = (kv_tasks + kv_warps - 1) / kv_warps;
+  if (a.Hq) blocks = std::max(blocks, (q_tasks + 8 - kv_warps - 1) / (8 - kv_warps));
+  blocks = std::min(blocks, most);
+  return inter ? launch_pdl(append_block_kernel<KV, D, MAXP, ROWS, true>, blocks, stream, a, kv_warps)
+               : launch_pdl(append_block_kernel<KV, D, MAXP, ROWS, false>, blocks, stream, a, kv_warps);
+}
+
+template <int KV, int D>
+int launch_block(const AppendArgs& a, bool inter, vas_stream_t stream) {
+  const bool many = (int64_t)a.T * a.Hq * D > (int64_t)vas::num_sms() * 64 * 512;
+  if (a.P == 16)
+    return many ? launch_block_rows<KV, D, 16, 4>(a, inter, stream) : launch_block_rows<KV, D, 16, 1>(a, inter, stream);
+  return many ? launch_block_rows<KV, D, 32, 4>(a, inter, stream) : launch_block_rows<KV, D, 32, 1>(a, inter, stream);
 }
 
 template <int KV, bool BLOCK>
