@@ -9,6 +9,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "../../include/vas.h"
 #include "append_rows.cuh"
@@ -26,8 +27,9 @@ namespace cache {
 // fresh page or behind the tokens a page already holds.  A task is one run of one head and
 // operand, and one warp's: it finds the largest magnitude of the run's rows (norm and rotation
 // applied), settles the scale, requantises the tokens the page held if the scale grew, and
-// writes the codes.  The rows stay in registers as they came, half the size of their values, and
-// are computed twice, for the magnitude and for the codes.
+// writes the codes.  Between the magnitude and the codes the values wait in shared memory, each
+// lane's own (computed twice instead, with the rows held as they came, the angles' second reads
+// made eight 1024-token chunks 124 us and not 105).
 // Beside these warps, kv_warps of a block's eight, the others take the queries' rows as
 // append_kernel does: one launch, and the pages' chains of look-ups run under the queries' stream.
 struct Runs {
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
   using T = __nv_bfloat16;
   constexpr int kLanes = D / 16;     // lanes of a row
   constexpr int kSub = 32 / kLanes;  // rows of a warp at a time
-  constexpr int kSteps = MAXP / kSub;
+  extern __shared__ float4 values[];  // of the runs' warps
   __shared__ Runs rs;
   __shared__ Packing pk;
   pdl_wait_prior_grid();
@@ -271,27 +273,34 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
     if (r.n == 0) continue;
     const T* src = is_v ? static_cast<const T*>(a.v) : static_cast<const T*>(a.k);
     const int64_t src_stride = is_v ? a.v_stride : a.k_stride;
-    // The run's rows; bit i of live: this lane's row of step i is stored (there is one, and its
-    // position is in the table).
-    Raw<T> raw[kSteps];
-    uint32_t live = 0;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      raw[i].zero();
+    // Step i: this lane's row i * kSub + sub of the run.  It is stored if there is one and its
+    // position is in the table.
+    auto position = [&](int i) {
       const int row = i * kSub + sub;
-      if (row >= r.n) continue;
-      bool ok = true;
-      if (a.rot && a.positions) {
-        const int32_t at = a.positions[r.t0 + row];
-        ok = at >= 0 && at < a.max_position;
-      } else if (a.rot) {
-        ok = r.pos0 + row < a.max_position;
+      return a.positions && row < r.n ? a.positions[r.t0 + row] : r.pos0 + row;
+    };
+    auto stored = [&](int i, int32_t at) {
+      return i * kSub + sub < r.n && (!a.rot || (at >= 0 && at < a.max_position));
+    };
+    Raw<T> raw;
+    F8 cs{}, sn{};
+    bool live;
+    auto fetch = [&](int i) {
+      const int32_t at = position(i);
+      live = stored(i, at);
+      raw.zero();
+      if (!live) {
+        if (i * kSub + sub < r.n && c == 0) atomicOr(a.err, VAS_DEV_BAD_POSITION);
+        return;
       }
-      if (!ok && c == 0) atomicOr(a.err, VAS_DEV_BAD_POSITION);
-      if (!ok) continue;
-      live |= 1u << i;
-      raw[i].load(src + (int64_t)(r.t0 + row) * src_stride + (int64_t)h * D, ch.a, ch.b);
-    }
+      raw.load(src + (int64_t)(r.t0 + i * kSub + sub) * src_stride + (int64_t)h * D, ch.a, ch.b);
+      if (!is_v && ch.turned) {
+        const float* angles = a.cos_sin + (size_t)at * a.rot + 8 * c;
+        cs = load_f8(angles);
+        sn = load_f8(angles + a.rot / 2);
+      }
+    };
+    fetch(0);
     if (r.err) {
       if (lane == 0) atomicOr(a.err, r.err);
       continue;
@@ -302,28 +311,33 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
     uint8_t* codes = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) +
                      ((size_t)r.page * a.P * a.Hkv + h) * D;
     const size_t row_bytes = (size_t)a.Hkv * D;
-    auto compute = [&](int i, F8& xa, F8& xb) {
-      xa = widen(raw[i].a);
-      xb = widen(raw[i].b);
-      if (is_v) return;
-      const float ss = row_squares<kLanes>(xa, xb);
-      if (a.k_weight != nullptr) norm_row<D>(xa, xb, wa, wb, ss, a.eps);
-      if (ch.turned && ((live >> i) & 1)) {
-        const int row = i * kSub + sub;
-        const int32_t at = a.positions ? a.positions[r.t0 + row] : r.pos0 + row;
-        const float* angles = a.cos_sin + (size_t)at * a.rot + 8 * c;
-        turn_row<INTER>(xa, xb, load_f8(angles), load_f8(angles + a.rot / 2));
-      }
-    };
-
-    uint32_t m = 0;
+    // Values of step i, and where they wait.
+    float4* const wait_at = values + (size_t)warp * (MAXP * D / 4) + lane;
+    uint32_t m = 0, kept = 0;
     bool wild = false;
+#pragma unroll 2
+    for (int i = 0; i * kSub < r.n; ++i) {
+      F8 xa = widen(raw.a), xb = widen(raw.b);
+      const F8 c8 = cs, s8 = sn;
+      const bool here = live;
+      if ((i + 1) * kSub < r.n) fetch(i + 1);
+      if (!is_v) {
+        const float ss = row_squares<kLanes>(xa, xb);
+        if (a.k_weight != nullptr) norm_row<D>(xa, xb, wa, wb, ss, a.eps);
+        if (ch.turned && here) turn_row<INTER>(xa, xb, c8, s8);
+      }
+      if (here) {
+        m = max(m, finite_max(xa, xb, &wild));
+        kept |= 1u << i;
+      }
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      if (i * kSub >= r.n) break;
-      F8 xa, xb;
-      compute(i, xa, xb);
-      if ((live >> i) & 1) m = max(m, finite_max(xa, xb, &wild));
+      for (int q = 0; q < 4; ++q) {
+        const uint64_t* p = q < 2 ? &xa.p[2 * q] : &xb.p[2 * q - 4];
+        float4 y;
+        unpair(p[0], y.x, y.y);
+        unpair(p[1], y.z, y.w);
+        wait_at[(i * 4 + q) * 32] = y;
+      }
     }
     m = __reduce_max_sync(0xffffffffu, m);
     wild = __any_sync(0xffffffffu, wild);
@@ -342,12 +356,17 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
     } else {
       scale = fresh_scale<KV>(top);
     }
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      if (i * kSub >= r.n) break;
+#pragma unroll 2
+    for (int i = 0; i * kSub < r.n; ++i) {
+      if (!((kept >> i) & 1)) continue;
       F8 xa, xb;
-      compute(i, xa, xb);
-      if (!((live >> i) & 1)) continue;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 y = wait_at[(i * 4 + q) * 32];
+        uint64_t* p = q < 2 ? &xa.p[2 * q] : &xb.p[2 * q - 4];
+        p[0] = pair(y.x, y.y);
+        p[1] = pair(y.z, y.w);
+      }
       if (wild) {
         tame<KV>(xa);
         tame<KV>(xb);
@@ -513,10 +532,11 @@ __global__ void __launch_bounds__(kAppendThreads) read_kernel(const ReadArgs a) 
 namespace {
 
 template <typename... P, typename... A>
-int launch_pdl(void (*kernel)(P...), int64_t blocks, vas_stream_t stream, A&&... args) {
+int launch_pdl(void (*kernel)(P...), int64_t blocks, int smem, vas_stream_t stream, A&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kAppendThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -532,6 +552,22 @@ int launch_pdl(void (*kernel)(P...), int64_t blocks, vas_stream_t stream, A&&...
 
 bool misaligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0;
+}
+
+template <int KV, int D, int MAXP, int ROWS, bool INTER>
+int launch_block_kernel(int64_t blocks, int kv_warps, vas_stream_t stream, const AppendArgs& a) {
+  constexpr int kWarpBytes = MAXP * D * 4;  // of each of the runs' warps
+  auto kernel = append_block_kernel<KV, D, MAXP, ROWS, INTER>;
+  static std::once_flag once[kMaxCachedDevices];
+  static cudaError_t attr_err[kMaxCachedDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxCachedDevices) return VAS_E_CUDA;
+  std::call_once(once[dev], [&] {
+    attr_err[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kAppendWarps * kWarpBytes);
+  });
+  if (attr_err[dev] != cudaSuccess) return VAS_E_CUDA;
+  return launch_pdl(kernel, blocks, kv_warps * kWarpBytes, stream, a, kv_warps);
 }
 
 template <int KV, int D, int MAXP, int ROWS>
@@ -556,8 +592,8 @@ int launch_block_rows(AppendArgs a, bool inter, vas_stream_t stream) {
   int64_t blocks = (kv_tasks + kv_warps - 1) / kv_warps;
   if (a.Hq) blocks = std::max(blocks, (q_tasks + 8 - kv_warps - 1) / (8 - kv_warps));
   blocks = std::min(blocks, most);
-  return inter ? launch_pdl(append_block_kernel<KV, D, MAXP, ROWS, true>, blocks, stream, a, kv_warps)
-               : launch_pdl(append_block_kernel<KV, D, MAXP, ROWS, false>, blocks, stream, a, kv_warps);
+  return inter ? launch_block_kernel<KV, D, MAXP, ROWS, true>(blocks, kv_warps, stream, a)
+               : launch_block_kernel<KV, D, MAXP, ROWS, false>(blocks, kv_warps, stream, a);
 }
 
 template <int KV, int D>
@@ -573,8 +609,8 @@ int launch_read(const ReadArgs& a, bool f32, vas_stream_t stream) {
   const int64_t want = ((int64_t)a.T + kAppendWarps - 1) / kAppendWarps;
   const int64_t most = 4LL * vas::num_sms();
   const int64_t blocks = want < most ? want : most;
-  return f32 ? launch_pdl(read_kernel<KV, BLOCK, float>, blocks, stream, a)
-             : launch_pdl(read_kernel<KV, BLOCK, __nv_bfloat16>, blocks, stream, a);
+  return f32 ? launch_pdl(read_kernel<KV, BLOCK, float>, blocks, 0, stream, a)
+             : launch_pdl(read_kernel<KV, BLOCK, __nv_bfloat16>, blocks, 0, stream, a);
 }
 
 }  // namespace
