@@ -227,6 +227,14 @@ __device__ __forceinline__ void scan_lengths(const Args& a, Packing& pk, int32_t
   __syncthreads();
 }
 
+// The call's lengths as a whole, after the scan: the first block's job.
+template <typename Args>
+__device__ __forceinline__ void check_lengths(const Args& a, int32_t total) {
+  bool bad = threadIdx.x == 0 && total != a.T;
+  for (int64_t i = threadIdx.x; i < a.B; i += kAppendThreads) bad |= !lengths_ok(a, a.length(i), a.count(i));
+  if (bad) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
+}
+
 // The sequence that owns packed row t.
 struct Owner {
   int32_t seq, len, count;  // the sequence, its length and its tokens
@@ -374,19 +382,17 @@ __device__ __forceinline__ void turn_row(F8& xa, F8& xb, const F8& cs, const F8&
 // and its warps take tasks gridDim apart; as soon as a row has been taken from its
 // registers the same row of the next group, or task, is fetched into them, so loads are
 // always under way.  INTER: rotary pairs are neighbours.  QUERIES: the rows are the queries'
-// alone.  The whole block: all its warps scan the lengths, those that `takes` tell take the tasks
-// from first_task on, task_stride apart.
-template <typename T, int KV, int D, int ROWS, bool INTER, bool QUERIES>
-__device__ __forceinline__ void append_rows(const AppendArgs& a, Packing& pk, int32_t first_task,
-                                            int32_t task_stride, bool takes) {
+// alone.  next() gives the warp its tasks, one after the other; ready() is called when the first
+// rows are on their way, and pk holds the packing after it.
+template <typename T, int KV, int D, int ROWS, bool INTER, bool QUERIES, typename Next, typename Ready>
+__device__ __forceinline__ void append_rows(const AppendArgs& a, const Packing& pk, Next next, Ready ready) {
   constexpr int kLanes = D / 16;     // lanes of a row
   constexpr int kSub = 32 / kLanes;  // rows of a warp at a time
   constexpr bool kQuant = KV == VAS_FP8_E4M3 || KV == VAS_INT8;
   const int lane = threadIdx.x & 31;
   const int H = QUERIES ? a.Hq : a.Hq + 2 * a.Hkv;
-  const uint32_t n_tasks = takes ? (uint32_t)a.T * (uint32_t)a.parts : 0;  // at most INT_MAX
-  const uint32_t stride = task_stride;
-  uint32_t task = takes ? first_task : 0;
+  const uint32_t n_tasks = (uint32_t)a.T * (uint32_t)a.parts;  // at most INT_MAX
+  uint32_t task = next();
 
   const int c = lane % kLanes;
   const Chunks ch = lane_chunks<D, INTER>(c, a.rot);
@@ -411,16 +417,10 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, Packing& pk, in
   int32_t t = (int32_t)(task / (uint32_t)a.parts);
   int32_t row0 = (int32_t)(task - (uint32_t)t * a.parts) * a.iters * kGroup + lane / kLanes;
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) fetch(x[i], takes ? t : a.T, row0 + i * kSub);
+  for (int i = 0; i < ROWS; ++i) fetch(x[i], t, row0 + i * kSub);
 
   const int32_t step = (a.B + kAppendSeqs - 1) / kAppendSeqs;
-  scan_lengths(a, pk, step);
-  if (blockIdx.x == 0) {  // the call's lengths as a whole
-    bool bad = threadIdx.x == 0 && pk.row0[kAppendSeqs] != a.T;
-    for (int i = threadIdx.x; i < a.B; i += kAppendThreads)
-      bad |= !lengths_ok(a, a.seq_lens[i], a.query_lens[i]);
-    if (bad) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
-  }
+  ready();
   F8 wa{}, wb{};  // the weights of this lane's chunks, and whose they are
   int kind = -1;  // 1: q, 0: k
   while (task < n_tasks) {
@@ -436,7 +436,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, Packing& pk, in
       sn = load_f8(row + a.rot / 2);
     }
 
-    task += stride;
+    task = next();
     int32_t t_task = (int32_t)(task / (uint32_t)a.parts);
     const int32_t row_task =
         (int32_t)(task - (uint32_t)t_task * a.parts) * a.iters * kGroup + lane / kLanes;

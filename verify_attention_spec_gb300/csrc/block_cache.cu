@@ -30,8 +30,9 @@ namespace cache {
 // writes the codes.  Between the magnitude and the codes the values wait in shared memory, each
 // lane's own (computed twice instead, with the rows held as they came, the angles' second reads
 // made eight 1024-token chunks 124 us and not 105).
-// Beside these warps, kv_warps of a block's eight, the others take the queries' rows as
-// append_kernel does: one launch, and the pages' chains of look-ups run under the queries' stream.
+// A block's first kv_warps warps take runs, the others the queries' rows as append_kernel does, and
+// so do the first when the runs are done: the pages' chains of look-ups go on under the queries'
+// stream.  A block has its tasks of either kind, its warps take the next one as they come to it.
 struct Runs {
   int32_t row0[kAppendSeqs + 1];  // first packed row of every `step`th sequence
   int32_t run0[kAppendSeqs + 1];  // and its first run; the last ones are the totals
@@ -244,27 +245,27 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t step = (a.B + kAppendSeqs - 1) / kAppendSeqs;
   scan_runs(a, rs, step);
-  const bool queries = warp >= kv_warps;
-  if (kv_warps < kAppendWarps) {
-    append_rows<T, VAS_BF16, D, ROWS, INTER, true>(a, pk, blockIdx.x * (kAppendWarps - kv_warps) + warp - kv_warps,
-                                                   gridDim.x * (kAppendWarps - kv_warps), queries);
-  } else if (blockIdx.x == 0) {  // the call's lengths as a whole
-    bool bad = threadIdx.x == 0 && rs.row0[kAppendSeqs] != a.T;
-    for (int64_t i = threadIdx.x; i < a.B; i += kAppendThreads)
-      bad |= !lengths_ok(a, a.seq_lens[i], a.query_lens[i]);
-    if (bad) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
-  }
-  if (queries) return;
+  if (a.Hq > 0) scan_lengths(a, pk, step);
+  if (blockIdx.x == 0) check_lengths(a, rs.row0[kAppendSeqs]);
+  __shared__ uint32_t taken[2];  // of the block's runs, and of its queries' tasks
+  if (threadIdx.x < 2) taken[threadIdx.x] = 0;
+  __syncthreads();
+  auto next = [&](int kind) {  // the warp's next task of the grid's
+    uint32_t k = 0;
+    if (lane == 0) k = atomicAdd(&taken[kind], 1u);
+    return (int64_t)__shfl_sync(0xffffffffu, k, 0) * gridDim.x + blockIdx.x;
+  };
   const int c = lane % kLanes, sub = lane / kLanes;
   const Chunks ch = lane_chunks<D, INTER>(c, a.rot);
   const int64_t n_tasks = (int64_t)rs.run0[kAppendSeqs] * 2 * a.Hkv;
-  const int64_t stride = (int64_t)gridDim.x * kv_warps;
   F8 wa{}, wb{};
   if (a.k_weight != nullptr) {
     wa = load_weights(static_cast<const T*>(a.k_weight) + ch.a);
     wb = load_weights(static_cast<const T*>(a.k_weight) + ch.b);
   }
-  for (int64_t task = (int64_t)blockIdx.x * kv_warps + warp; task < n_tasks; task += stride) {
+  while (warp < kv_warps) {
+    const int64_t task = next(0);
+    if (task >= n_tasks) break;
     const int32_t u = (int32_t)(task / (2 * a.Hkv));
     int32_t h = (int32_t)(task - (int64_t)u * 2 * a.Hkv);
     const bool is_v = h >= a.Hkv;
@@ -377,6 +378,9 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks)
     }
     if (lane == 0 && scale != old) scales[si] = scale;
   }
+  if (a.Hq > 0)
+    append_rows<T, VAS_BF16, D, ROWS, INTER, true>(
+        a, pk, [&] { return (uint32_t)min(next(1), (int64_t)INT_MAX); }, [] {});
 }
 
 // ------------------------------------------------------------------------------------
@@ -467,12 +471,7 @@ __global__ void __launch_bounds__(kAppendThreads) read_kernel(const ReadArgs a) 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int32_t step = (a.B + kAppendSeqs - 1) / kAppendSeqs;
   scan_lengths(a, pk, step);
-  if (blockIdx.x == 0) {
-    bool bad = threadIdx.x == 0 && pk.row0[kAppendSeqs] != a.T;
-    for (int64_t i = threadIdx.x; i < a.B; i += kAppendThreads)
-      bad |= !lengths_ok(a, a.length(i), a.count(i));
-    if (bad) atomicOr(a.err, VAS_DEV_BAD_LENGTHS);
-  }
+  if (blockIdx.x == 0) check_lengths(a, pk.row0[kAppendSeqs]);
   const int32_t E = a.Hkv << a.log2D;  // elements of a token's row
   const int64_t stride = (int64_t)gridDim.x * kAppendWarps;
   // Page and slot of token t; slot -1: of no sequence, or of one with inconsistent lengths.
@@ -586,9 +585,9 @@ int launch_block_rows(AppendArgs a, bool inter, vas_stream_t stream) {
   a.iters = (int32_t)((groups + parts - 1) / parts);
   a.parts = a.Hq ? (int32_t)((groups + a.iters - 1) / a.iters) : 1;
   const int64_t q_tasks = a.Hq ? (int64_t)a.T * a.parts : 0;
-  // Two warps of a block for the pages when the queries' bytes are the most of the call; more when
-  // tasks are few and their latency counts.
-  const int kv_warps = !a.Hq ? 8 : (kv_tasks > most * 16 ? 2 : 6);
+  // Two warps of a block for the pages where the queries' rows are the most of many; more where tasks
+  // are few and their latency counts.
+  const int kv_warps = !a.Hq ? 8 : (kv_tasks <= most * 16 ? 6 : (a.Hq >= 3 * a.Hkv ? 2 : 4));
   int64_t blocks = (kv_tasks + kv_warps - 1) / kv_warps;
   if (a.Hq) blocks = std::max(blocks, (q_tasks + 8 - kv_warps - 1) / (8 - kv_warps));
   blocks = std::min(blocks, most);

@@ -38,8 +38,19 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendBlocks) append_kernel(c
   __shared__ Packing pk;
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  append_rows<T, KV, D, ROWS, INTER, false>(a, pk, blockIdx.x * kAppendWarps + (threadIdx.x >> 5),
-                                            gridDim.x * kAppendWarps, true);
+  uint32_t task = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+  const uint32_t stride = gridDim.x * kAppendWarps;
+  append_rows<T, KV, D, ROWS, INTER, false>(
+      a, pk,
+      [&] {
+        const uint32_t t = task;
+        task += stride;
+        return t;
+      },
+      [&] {
+        scan_lengths(a, pk, (a.B + kAppendSeqs - 1) / kAppendSeqs);
+        if (blockIdx.x == 0) check_lengths(a, pk.row0[kAppendSeqs]);
+      });
 }
 
 // ------------------------------------------------------------------------------------
