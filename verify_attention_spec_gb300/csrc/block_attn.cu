@@ -109,7 +109,7 @@ struct Misc {
   alignas(16) float inv[kMaxRows];      // what a row of O is multiplied by at the end
   int64_t out_row[kMaxRows];            // its place in out, in rows
   alignas(16) float alpha[kMaxRows];    // what a new reference does to the old sums
-  uint32_t q_top[kSoftWarps];           // largest magnitudes of the unit's queries
+  float score_scale[2];                 // what brings a score to base 2, by the unit's parity
   float warp_max[kSoftWarps][kMaxRows];
   float warp_sum[kSoftWarps][kMaxRows];
   int32_t limit[kMaxRows];        // last position a row sees
@@ -299,97 +299,103 @@ struct Ctx {
 };
 
 // ---- softmax warps -------------------------------------------------------------------
-// The unit's queries as E4M3 pairs in the K-major operand layout; the rows' references, limits
-// and masks.  Returns what brings a score to base 2.
-template <int RP, int D, int MR, int KV>
-__device__ __forceinline__ float stage_queries(const Ctx<D, MR, KV>& x, const Unit& u) {
-  constexpr bool kFp8 = KV == VAS_FP8_E4M3;
-  const Args& a = x.a;
-  Misc& m = x.m;
-  constexpr int kLanes = D / 8;             // of a row, 8 elements each
-  constexpr int kAtOnce = 128 / kLanes;     // rows
-  constexpr int kRows = !kFp8 && RP < 16 ? 16 : RP;  // of the operand
-  constexpr int kSteps = (kRows + kAtOnce - 1) / kAtOnce;
-  const int tid = threadIdx.x, c = tid % kLanes;
-  uint8_t* q_tile = x.smem + Smem<D, MR, KV>::kQOff;
+// A unit's queries on their way to the operand: the MMA warp loads them while the unit before is
+// in its last tiles, and stages them when that has issued its last product.
+template <int D, int MR, int KV>
+struct Queries {
+  static constexpr bool kFp8 = KV == VAS_FP8_E4M3;
+  static constexpr int kLanes = D / 8;            // of a row, 8 elements each
+  static constexpr int kAtOnce = 32 / kLanes;     // rows
+  static constexpr int kSteps = MR / kAtOnce;
   uint4 v[kSteps];
-  float top = 0.f;
+
+  __device__ __forceinline__ void load(const Args& a, const Unit& u, int lane) {
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int r = i * kAtOnce + tid / kLanes;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (r < u.rows) {
-      const int g = u.r0 + r, j = a.by_G.div(g), h = g - j * a.G;
-      v[i] = *(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                              ((size_t)(u.row0 + j) * a.Hq + (size_t)u.head * a.G + h) * D) + c);
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = i * kAtOnce + lane / kLanes;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (r < u.rows) {
+        const int g = u.r0 + r, j = a.by_G.div(g), h = g - j * a.G;
+        v[i] = *(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
+                                                ((size_t)(u.row0 + j) * a.Hq + (size_t)u.head * a.G + h) * D) +
+                 lane % kLanes);
+      }
     }
   }
-  if (tid < RP) {
-    const int g = u.r0 + tid, j = min((int)a.by_G.div(g), u.ql - 1);
-    m.neg_ref[tid] = -kNoMax;
-    m.out_row[tid] = (int64_t)(u.row0 + j) * a.Hq + (int64_t)u.head * a.G + (g - j * a.G);
-    m.limit[tid] = tid < u.rows ? u.len - u.ql + j : -1;
-    const bool tree = a.tree_mask && u.ql > 1 && u.ql <= 64;
-    m.tree[tid] = tree ? (a.tree_mask[u.row0 + j] & (j ? ~0ull >> (64 - j) : 0ull)) | (1ull << j) : ~0ull;
-  }
+
+  // As E4M3 pairs, or f16, in the K-major operand layout of rp rows.  Returns what brings a score
+  // to base 2.
+  __device__ __forceinline__ float stage(const Args& a, uint8_t* q_tile, int rp, int lane) const {
+    const int c = lane % kLanes;
+    float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) top = fmaxf(top, absmax_bf16x8(v[i]));
-  const uint32_t warp_top = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-  if (x.lane == 0) m.q_top[x.warp] = warp_top;
-  named_bar_sync(1, 128);
-  const uint32_t all = max(max(m.q_top[0], m.q_top[1]), max(m.q_top[2], m.q_top[3]));
-  // 2^e brings the unit's largest magnitude into [128, 256): the remainder of hi is then at most
-  // 8, and 32 of it exact in E4M3 for elements down to 2^-15 of the largest (below, 2^-24 of the
-  // largest is lost, as in an fp32 sum of the products).  f16: [2^14, 2^15), exact down to 2^-28.
-  const int e = max(-112, min(112, (kFp8 ? 7 : 14) - ((int)(all >> 23) - 127)));
-  const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
+    for (int i = 0; i < kSteps; ++i) top = fmaxf(top, absmax_bf16x8(v[i]));
+    const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    // 2^e brings the unit's largest magnitude into [128, 256): the remainder of hi is then at most
+    // 8, and 32 of it exact in E4M3 for elements down to 2^-15 of the largest (below, 2^-24 of the
+    // largest is lost, as in an fp32 sum of the products).  f16: [2^14, 2^15), exact to 2^-28.
+    const int e = max(-112, min(112, (kFp8 ? 7 : 14) - ((int)(all >> 23) - 127)));
+    const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
+    const int rows = kFp8 ? rp : max(rp, 16);  // of the operand
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) {
-    const int r = i * kAtOnce + tid / kLanes;
-    if constexpr (!kFp8) {
-      // Rows of D elements in column blocks of 64: chunk c of 16 bytes.
-      if (kRows % kAtOnce == 0 || r < kRows)
-        *reinterpret_cast<uint4*>(q_tile + (c / 8) * (kRows * 128) + r * 128 + (((c ^ r) & 7) << 4)) =
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = i * kAtOnce + lane / kLanes;
+      if (r >= rows) break;
+      if constexpr (!kFp8) {
+        // Rows of D elements in column blocks of 64: chunk c of 16 bytes.
+        *reinterpret_cast<uint4*>(q_tile + (c / 8) * (rows * 128) + r * 128 + (((c ^ r) & 7) << 4)) =
             bf16x8_to_f16x8(v[i], mul);
-    } else {
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    uint32_t hi[2], lo[2];
+      } else {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t hi[2], lo[2];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      float y[4] = {bf16_lo_f32(w[2 * k]) * mul, bf16_hi_f32(w[2 * k]) * mul,
-                    bf16_lo_f32(w[2 * k + 1]) * mul, bf16_hi_f32(w[2 * k + 1]) * mul};
+        for (int k = 0; k < 2; ++k) {
+          float y[4] = {bf16_lo_f32(w[2 * k]) * mul, bf16_hi_f32(w[2 * k]) * mul,
+                        bf16_lo_f32(w[2 * k + 1]) * mul, bf16_hi_f32(w[2 * k + 1]) * mul};
 #pragma unroll
-      for (int f = 0; f < 4; ++f) y[f] += y[f] - y[f];  // an infinity becomes NaN, not 448
-      auto pack = [](const float (&z)[4]) {
-        uint32_t p;
-        asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
-            "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
-            : "=r"(p)
-            : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
-        return p;
-      };
-      hi[k] = pack(y);
-      uint32_t f0, f1;
-      float b[4];
-      e4m3x4_to_f16x4(hi[k], f0, f1);
-      f16x2_to_f32(f0, b[0], b[1]);
-      f16x2_to_f32(f1, b[2], b[3]);
+          for (int f = 0; f < 4; ++f) y[f] += y[f] - y[f];  // an infinity becomes NaN, not 448
+          auto pack = [](const float (&z)[4]) {
+            uint32_t p;
+            asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
+                "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
+                : "=r"(p)
+                : "f"(z[0]), "f"(z[1]), "f"(z[2]), "f"(z[3]));
+            return p;
+          };
+          hi[k] = pack(y);
+          uint32_t f0, f1;
+          float b[4];
+          e4m3x4_to_f16x4(hi[k], f0, f1);
+          f16x2_to_f32(f0, b[0], b[1]);
+          f16x2_to_f32(f1, b[2], b[3]);
 #pragma unroll
-      for (int f = 0; f < 4; ++f) b[f] = (y[f] - b[f]) * 32.f;
-      lo[k] = pack(b);
+          for (int f = 0; f < 4; ++f) b[f] = (y[f] - b[f]) * 32.f;
+          lo[k] = pack(b);
+        }
+        // Row n of the operand: rows of D bytes, 16-byte chunks swizzled by the row.
+        auto at = [&](int n) {
+          const uint32_t off = (uint32_t)n * D + c * 8;
+          return q_tile + (off ^ (((off >> 7) & (D == 128 ? 7 : 3)) << 4));
+        };
+        *reinterpret_cast<uint2*>(at(r)) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(at(rp + r)) = make_uint2(lo[0], lo[1]);
+      }
     }
-    if (RP % kAtOnce == 0 || r < RP) {
-      // Row n of the operand: rows of D bytes, 16-byte chunks swizzled by the row.
-      auto at = [&](int n) {
-        const uint32_t off = (uint32_t)n * D + c * 8;
-        return q_tile + (off ^ (((off >> 7) & (D == 128 ? 7 : 3)) << 4));
-      };
-      *reinterpret_cast<uint2*>(at(r)) = make_uint2(hi[0], hi[1]);
-      *reinterpret_cast<uint2*>(at(RP + r)) = make_uint2(lo[0], lo[1]);
-    }
-    }
+    fence_proxy_async_smem();
+    return a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
   }
-  return a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+};
+
+// The rows' references, limits, masks and places, by the softmax threads.
+template <int RP>
+__device__ __forceinline__ void start_rows(const Args& a, Misc& m, const Unit& u, bool tree) {
+  const int tid = threadIdx.x;
+  if (tid >= RP) return;
+  const int g = u.r0 + tid, j = min((int)a.by_G.div(g), u.ql - 1);
+  m.neg_ref[tid] = -kNoMax;
+  m.out_row[tid] = (int64_t)(u.row0 + j) * a.Hq + (int64_t)u.head * a.G + (g - j * a.G);
+  m.limit[tid] = tid < u.rows ? u.len - u.ql + j : -1;
+  m.tree[tid] = tree ? (a.tree_mask[u.row0 + j] & (j ? ~0ull >> (64 - j) : 0ull)) | (1ull << j) : ~0ull;
 }
 
 // V rows of a tile that a weight of zero would not silence: slots of no token may hold NaN, and a
@@ -416,7 +422,7 @@ __device__ __noinline__ bool clear_row(uint8_t* v_row, bool token) {
 // One unit; false after a wait that ran out.  Such a warp waits no more but keeps to the barriers
 // of the others, which leave with it at the end of the unit.
 template <int RP, int D, int MR, int KV>
-__device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u, uint32_t& tile_it) {
+__device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u, uint32_t nth_unit, uint32_t& tile_it) {
   using S = Smem<D, MR, KV>;
   constexpr bool kFp8 = KV == VAS_FP8_E4M3;
   constexpr int kParts = parts_of(KV);
@@ -427,10 +433,9 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
   const int tid = threadIdx.x, warp = x.warp, lane = x.lane;
   const uint32_t lanes = (uint32_t)(32 * warp) << 16;
 
-  const float score_scale = stage_queries<RP>(x, u);
-  fence_proxy_async_smem();
-  named_bar_sync(1, 128);  // the queries are staged, the rows' numbers may be read
-  if (tid == 0) mbar_arrive(&m.q_full);
+  const bool tree = a.tree_mask && u.ql > 1 && u.ql <= 64;
+  start_rows<RP>(a, m, u, tree);
+  named_bar_sync(1, 128);  // the rows' numbers may be read
 
   uint64_t l2[RP / 2];  // sums of the weights of this thread's tokens, two rows each
 #pragma unroll
@@ -439,8 +444,9 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
   auto wait_for = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = wait(bar, parity);
   };
+  wait_for(&m.q_full, nth_unit & 1);
+  const float score_scale = m.score_scale[nth_unit & 1];
   const int ctx = u.len - u.ql;
-  const bool tree = a.tree_mask && u.ql > 1 && u.ql <= 64;
   const int seen_by_all = tree ? ctx - 1 : ctx + (int)a.by_G.div(u.r0);  // the last position all rows see
 
   for (int tile = u.tile0; tile < u.tile1; ++tile, ++tile_it) {
@@ -472,9 +478,9 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
     const uint32_t s_at = x.tmem + lanes + kTmemS + 64 * b;
     const uint64_t c32 = pair(1.f / 32, 1.f / 32), ks2 = pair(ks, ks);
     uint64_t t2[RP / 2];  // scores relative to their rows' references
-    for (;;) {
-      float top = -INFINITY;
-      {
+    for (bool first = tile == u.tile0;; first = false) {
+      if (!first) {  // (the first tile's maxima come first)
+        float top = -INFINITY;
         uint32_t hi[RP], lo[RP];
         tmem_ld<RP>(s_at, hi);
         if (kFp8) tmem_ld<RP>(s_at + RP, lo);
@@ -490,23 +496,23 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
             t2[r / 2] = fma2(h2, ks2, neg);
           }
         }
-      }
-      if (masked) {
+        if (masked) {
+#pragma unroll
+          for (int r = 0; r < RP; r += 2) {
+            float y0, y1;
+            unpair(t2[r / 2], y0, y1);
+            if (poison) y0 = y1 = NAN;
+            t2[r / 2] = pair(dropped(r) ? -INFINITY : y0, dropped(r + 1) ? -INFINITY : y1);
+          }
+        }
 #pragma unroll
         for (int r = 0; r < RP; r += 2) {
           float y0, y1;
           unpair(t2[r / 2], y0, y1);
-          if (poison) y0 = y1 = NAN;
-          t2[r / 2] = pair(dropped(r) ? -INFINITY : y0, dropped(r + 1) ? -INFINITY : y1);
+          top = max3(top, y0, y1);
         }
+        if (!named_bar_or(1, 128, top + ve > kSlack)) break;
       }
-#pragma unroll
-      for (int r = 0; r < RP; r += 2) {
-        float y0, y1;
-        unpair(t2[r / 2], y0, y1);
-        top = max3(top, y0, y1);
-      }
-      if (!named_bar_or(1, 128, top + ve > kSlack)) break;
       // Some weight outgrew its row's reference.  The tile's maxima, the new references, and sums
       // and O in them; then the scores once more.
 #pragma unroll 1
@@ -954,83 +960,137 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
     for (uint32_t it = 2 * tile_it > S::kSlots ? 2 * tile_it - S::kSlots : 0; it < 2 * tile_it; ++it)
       mbar_wait(&m.full[it % S::kSlots], (it / S::kSlots) & 1);
   } else if (warp == kMma) {
-    // ---- products: one lane ----
-    if (lane == 0) {
-      uint32_t unit_it = 0, tile_it = 0;
-      const uint32_t ring_at = smem_u32(smem), q_at = smem_u32(smem + S::kQOff);
-      auto scores = [&](uint32_t it, int rp) {
-        const uint32_t k_it = 2 * it;
-        const int slot = k_it % S::kSlots, b = it & 1;
-        if (!(kFp8 ? wait(&m.full[slot], (k_it / S::kSlots) & 1) : wait(&m.k_wide, it & 1))) return false;
-        if (!wait(&m.s_empty[b], ((it >> 1) & 1) ^ 1)) return false;
-        tc_fence_after();
-        if constexpr (kFp8) {
-          const uint32_t idesc = idesc_f8(128, 2 * rp, false, false);
-          const uint64_t k_desc = desc_rows<D>(ring_at + slot * S::kOperand), q_desc = desc_rows<D>(q_at);
+    // ---- products, and the queries' way to their operand; lane 0 issues ----
+    // Scores of tile qk and O of tile pv are issued as what they need comes in: K and a free S
+    // buffer, V and the weights.  (With O behind the next tile's scores, it waited for K from
+    // memory, and its V held a slot meanwhile: 64 decodes 63 us.)
+    uint32_t unit_it = 0, tile_it = 0;
+    const uint32_t ring_at = smem_u32(smem), q_at = smem_u32(smem + S::kQOff);
+    auto scores = [&](uint32_t it, int rp) {
+      const int slot = 2 * it % S::kSlots, b = it & 1;
+      tc_fence_after();
+      if constexpr (kFp8) {
+        const uint32_t idesc = idesc_f8(128, 2 * rp, false, false);
+        const uint64_t k_desc = desc_rows<D>(ring_at + slot * S::kOperand), q_desc = desc_rows<D>(q_at);
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            mma_f8(x.tmem + kTmemS + 64 * b, k_desc + 2 * k, q_desc + 2 * k, idesc, k > 0);
-          umma_commit(&m.empty[slot]);
-        } else {
-          const int n = max(rp, 16);
-          const uint32_t idesc = umma_idesc_bf16(128, n, false, false, true);
-          const uint64_t k_desc = desc_f16(ring_at + S::kKOff, 16), q_desc = desc_f16(q_at, 16);
+        for (int k = 0; k < D / 32; ++k)
+          mma_f8(x.tmem + kTmemS + 64 * b, k_desc + 2 * k, q_desc + 2 * k, idesc, k > 0);
+        umma_commit(&m.empty[slot]);
+      } else {
+        const int n = max(rp, 16);
+        const uint32_t idesc = umma_idesc_bf16(128, n, false, false, true);
+        const uint64_t k_desc = desc_f16(ring_at + S::kKOff, 16), q_desc = desc_f16(q_at, 16);
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)  // 64 elements a column block
-            mma_f16(x.tmem + kTmemS + 64 * b, k_desc + (k / 4) * ((kTile * 128) >> 4) + 2 * (k % 4),
-                    q_desc + (k / 4) * ((n * 128) >> 4) + 2 * (k % 4), idesc, k > 0);
-          umma_commit(&m.k_free);
-        }
-        umma_commit(&m.s_full[b]);
-        return true;
-      };
-      for (;;) {
-        const int slot_u = unit_it % kRing;
-        ok = wait(&m.ufull[slot_u], (unit_it / kRing) & 1);
-        if (!ok) break;
-        const int tile0 = m.ring[slot_u].tile0, tile1 = m.ring[slot_u].tile1, rows = m.ring[slot_u].rows;
-        mbar_arrive(&m.uempty[slot_u]);
-        if (tile0 >= tile1) break;
-        const int rp = padded_rows(rows);
-        ok = wait(&m.q_full, unit_it & 1);
-        ++unit_it;
-        if (!ok) break;
-        tc_fence_after();
-        const int n = tile1 - tile0;
-        ok = scores(tile_it, rp);
-        for (int i = 0; i < n && ok; ++i, ++tile_it) {
-          if (i + 1 < n) ok = scores(tile_it + 1, rp);
-          if (!ok) break;
-          const uint32_t v_it = 2 * tile_it + 1;
-          const int slot = v_it % S::kSlots;
-          ok = (kFp8 ? wait(&m.full[slot], (v_it / S::kSlots) & 1) : wait(&m.v_wide, tile_it & 1)) &&
-               wait(&m.p_full, tile_it & 1);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t p_desc = desc_weights(smem_u32(smem + S::kPOff));
-          if constexpr (kFp8) {
-            const uint32_t idesc = idesc_f8(D, 4 * rp, true, true);
-            const uint64_t v_desc = desc_rows<D>(ring_at + slot * S::kOperand);
-#pragma unroll
-            for (int k = 0; k < kTile / 32; ++k)
-              mma_f8(x.tmem + kTmemO, v_desc + ((32 * D * k) >> 4), p_desc + ((512 * k) >> 4), idesc, i > 0 || k > 0);
-            umma_commit(&m.empty[slot]);
-          } else {
-            const uint32_t idesc = umma_idesc_bf16(D, max(rp, 16), true, true, true);
-            const uint64_t v_desc = desc_f16(ring_at + S::kVOff, kTile * 128);
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_f16(x.tmem + kTmemO, v_desc + ((16 * 128 * k) >> 4), p_desc + ((256 * k) >> 4), idesc, i > 0 || k > 0);
-          }
-          umma_commit(&m.pv_done);
-        }
-        if (!ok) break;
+        for (int k = 0; k < D / 16; ++k)  // 64 elements a column block
+          mma_f16(x.tmem + kTmemS + 64 * b, k_desc + (k / 4) * ((kTile * 128) >> 4) + 2 * (k % 4),
+                  q_desc + (k / 4) * ((n * 128) >> 4) + 2 * (k % 4), idesc, k > 0);
+        umma_commit(&m.k_free);
       }
-      // Products in flight end before the tensor memory is freed.
+      umma_commit(&m.s_full[b]);
+    };
+    auto output = [&](uint32_t it, int rp, bool more) {
+      const int slot = (2 * it + 1) % S::kSlots;
+      tc_fence_after();
+      const uint64_t p_desc = desc_weights(smem_u32(smem + S::kPOff));
+      if constexpr (kFp8) {
+        const uint32_t idesc = idesc_f8(D, 4 * rp, true, true);
+        const uint64_t v_desc = desc_rows<D>(ring_at + slot * S::kOperand);
+#pragma unroll
+        for (int k = 0; k < kTile / 32; ++k)
+          mma_f8(x.tmem + kTmemO, v_desc + ((32 * D * k) >> 4), p_desc + ((512 * k) >> 4), idesc, more || k > 0);
+        umma_commit(&m.empty[slot]);
+      } else {
+        const uint32_t idesc = umma_idesc_bf16(D, max(rp, 16), true, true, true);
+        const uint64_t v_desc = desc_f16(ring_at + S::kVOff, kTile * 128);
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k)
+          mma_f16(x.tmem + kTmemO, v_desc + ((16 * 128 * k) >> 4), p_desc + ((256 * k) >> 4), idesc, more || k > 0);
+      }
+      umma_commit(&m.pv_done);
+    };
+    auto k_there = [&](uint32_t it) {
+      return kFp8 ? mbar_test_wait(&m.full[2 * it % S::kSlots], (2 * it / S::kSlots) & 1)
+                  : mbar_test_wait(&m.k_wide, it & 1);
+    };
+    auto v_there = [&](uint32_t it) {
+      const uint32_t v_it = 2 * it + 1;
+      return kFp8 ? mbar_test_wait(&m.full[v_it % S::kSlots], (v_it / S::kSlots) & 1)
+                  : mbar_test_wait(&m.v_wide, it & 1);
+    };
+    Unit u{}, next{};
+    Queries<D, MR, KV> q;
+    auto take_unit = [&] {  // after its ufull
+      next = m.ring[unit_it % kRing];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.uempty[unit_it % kRing]);
+      ++unit_it;
+      if (next.tile0 < next.tile1) q.load(a, next, lane);
+    };
+    ok = wait(&m.ufull[0], 0);
+    if (ok) take_unit();
+    while (ok && next.tile0 < next.tile1) {
+      u = next;
+      const int rp = padded_rows(u.rows), n = u.tile1 - u.tile0;
+      {  // every product that read the queries before is done: their scores have been taken
+        const float scale = q.stage(a, smem + S::kQOff, rp, lane);
+        __syncwarp();
+        if (lane == 0) {
+          m.score_scale[(unit_it - 1) & 1] = scale;
+          mbar_arrive(&m.q_full);
+        }
+      }
+      bool have_next = false;
+      uint64_t t0 = 0;
+      uint32_t idle = 0;
+      for (int qk = 0, pv = 0; pv < n;) {
+        uint32_t can = 0;
+        if (lane == 0) {
+          if (pv < qk && mbar_test_wait(&m.p_full, (tile_it + pv) & 1) && v_there(tile_it + pv)) {
+            output(tile_it + pv, rp, pv > 0);
+            can |= 1;
+          }
+          const uint32_t it = tile_it + qk;
+          if (qk < n && qk < pv + 2 && k_there(it) && mbar_test_wait(&m.s_empty[it & 1], ((it >> 1) & 1) ^ 1)) {
+            scores(it, rp);
+            can |= 2;
+          }
+          if (qk == n && !have_next && mbar_test_wait(&m.ufull[unit_it % kRing], (unit_it / kRing) & 1)) can |= 4;
+        }
+        can = __shfl_sync(0xffffffffu, can, 0);
+        pv += can & 1;
+        qk += (can >> 1) & 1;
+        if (can & 4) {
+          ok = mbar_test_wait(&m.ufull[unit_it % kRing], (unit_it / kRing) & 1);  // for every lane
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = true;
+          } else {
+            take_unit();
+            have_next = true;
+          }
+        }
+        if (can) {
+          idle = 0;
+        } else if ((++idle & 1023) == 0) {
+          const uint64_t now = global_timer_ns();
+          if (idle == 1024) t0 = now;
+          ok = __shfl_sync(0xffffffffu, (int)(now - t0 < kWaitLimitNs), 0) != 0;
+          if (!ok) break;
+        }
+      }
+      tile_it += n;
+      if (!ok) break;
+      if (!have_next) {
+        ok = wait(&m.ufull[unit_it % kRing], (unit_it / kRing) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) take_unit();
+      }
+    }
+    // Products in flight end before the tensor memory is freed.
+    if (lane == 0) {
       umma_commit(&m.fin);
       mbar_wait(&m.fin, 0);
     }
-    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();
   } else if (warp >= kConv) {
     // ---- INT8: codes to f16, 16 a lane at a time, into the 128-byte-swizzled operands ----
     if constexpr (!kFp8) {
@@ -1096,15 +1156,15 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
       const Unit u = m.ring[slot_u];
       __syncwarp();
       if (lane == 0) mbar_arrive(&m.uempty[slot_u]);
-      ++unit_it;
       if (u.tile0 >= u.tile1) break;
       if constexpr (MR == 8) {
-        ok = soft_unit<8>(x, u, tile_it);
+        ok = soft_unit<8>(x, u, unit_it, tile_it);
       } else {
-        if (u.rows <= 8) ok = soft_unit<8>(x, u, tile_it);
-        else if (u.rows <= 16) ok = soft_unit<16>(x, u, tile_it);
-        else ok = soft_unit<32>(x, u, tile_it);
+        if (u.rows <= 8) ok = soft_unit<8>(x, u, unit_it, tile_it);
+        else if (u.rows <= 16) ok = soft_unit<16>(x, u, unit_it, tile_it);
+        else ok = soft_unit<32>(x, u, unit_it, tile_it);
       }
+      ++unit_it;
       if (!ok) break;
     }
   }
