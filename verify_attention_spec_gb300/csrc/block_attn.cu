@@ -309,9 +309,10 @@ struct Queries {
   static constexpr int kSteps = MR / kAtOnce;
   uint4 v[kSteps];
 
-  __device__ __forceinline__ void load(const Args& a, const Unit& u, int lane) {
+  __device__ __forceinline__ void load(const Args& a, const Unit& u, int rp, int lane) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
+      if (i * kAtOnce >= rp) break;
       const int r = i * kAtOnce + lane / kLanes;
       v[i] = make_uint4(0, 0, 0, 0);
       if (r < u.rows) {
@@ -329,18 +330,21 @@ struct Queries {
     const int c = lane % kLanes;
     float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) top = fmaxf(top, absmax_bf16x8(v[i]));
+    for (int i = 0; i < kSteps; ++i) {
+      if (i * kAtOnce >= rp) break;
+      top = fmaxf(top, absmax_bf16x8(v[i]));
+    }
     const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
     // 2^e brings the unit's largest magnitude into [128, 256): the remainder of hi is then at most
     // 8, and 32 of it exact in E4M3 for elements down to 2^-15 of the largest (below, 2^-24 of the
     // largest is lost, as in an fp32 sum of the products).  f16: [2^14, 2^15), exact to 2^-28.
     const int e = max(-112, min(112, (kFp8 ? 7 : 14) - ((int)(all >> 23) - 127)));
     const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
-    const int rows = kFp8 ? rp : max(rp, 16);  // of the operand
+    const int rows = kFp8 ? rp : max(rp, 16);  // of the operand (those from rp on may be anything)
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
+      if (i * kAtOnce >= rp) break;
       const int r = i * kAtOnce + lane / kLanes;
-      if (r >= rows) break;
       if constexpr (!kFp8) {
         // Rows of D elements in column blocks of 64: chunk c of 16 bytes.
         *reinterpret_cast<uint4*>(q_tile + (c / 8) * (rows * 128) + r * 128 + (((c ^ r) & 7) << 4)) =
@@ -481,19 +485,22 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
     for (bool first = tile == u.tile0;; first = false) {
       if (!first) {  // (the first tile's maxima come first)
         float top = -INFINITY;
-        uint32_t hi[RP], lo[RP];
-        tmem_ld<RP>(s_at, hi);
-        if (kFp8) tmem_ld<RP>(s_at + RP, lo);
-        tmem_wait_ld();
 #pragma unroll
-        for (int r = 0; r < RP; r += 2) {
-          const uint64_t h2 = pair(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1]));
-          const uint64_t neg = *reinterpret_cast<const uint64_t*>(&m.neg_ref[r]);
-          if constexpr (kFp8) {
-            const uint64_t w2 = pair(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1]));
-            t2[r / 2] = fma2(fma2(w2, c32, h2), ks2, neg);
-          } else {
-            t2[r / 2] = fma2(h2, ks2, neg);
+        for (int r0 = 0; r0 < RP; r0 += kLd) {
+          uint32_t hi[kLd], lo[kLd];
+          tmem_ld<kLd>(s_at + r0, hi);
+          if (kFp8) tmem_ld<kLd>(s_at + RP + r0, lo);
+          tmem_wait_ld();
+#pragma unroll
+          for (int r = 0; r < kLd; r += 2) {
+            const uint64_t h2 = pair(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1]));
+            const uint64_t neg = *reinterpret_cast<const uint64_t*>(&m.neg_ref[r0 + r]);
+            if constexpr (kFp8) {
+              const uint64_t w2 = pair(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1]));
+              t2[(r0 + r) / 2] = fma2(fma2(w2, c32, h2), ks2, neg);
+            } else {
+              t2[(r0 + r) / 2] = fma2(h2, ks2, neg);
+            }
           }
         }
         if (masked) {
@@ -1024,7 +1031,7 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
       __syncwarp();
       if (lane == 0) mbar_arrive(&m.uempty[unit_it % kRing]);
       ++unit_it;
-      if (next.tile0 < next.tile1) q.load(a, next, lane);
+      if (next.tile0 < next.tile1) q.load(a, next, padded_rows(next.rows), lane);
     };
     ok = wait(&m.ufull[0], 0);
     if (ok) take_unit();
