@@ -109,6 +109,7 @@ struct Misc {
   alignas(16) float inv[kMaxRows];      // what a row of O is multiplied by at the end
   int64_t out_row[kMaxRows];            // its place in out, in rows
   alignas(16) float alpha[kMaxRows];    // what a new reference does to the old sums
+  uint32_t q_top[kSoftWarps];           // largest magnitudes of the unit's queries
   float score_scale[2];                 // what brings a score to base 2, by the unit's parity
   float warp_max[kSoftWarps][kMaxRows];
   float warp_sum[kSoftWarps][kMaxRows];
@@ -279,13 +280,6 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// Order of floats as order of ints, for the warp-wide maximum.
-__device__ __forceinline__ int ordered(float x) {
-  const int i = __float_as_int(x);
-  return i >= 0 ? i : i ^ 0x7fffffff;
-}
-__device__ __forceinline__ float unordered(int i) { return __int_as_float(i >= 0 ? i : i ^ 0x7fffffff); }
-
 // Rows a unit is computed as (RP >= its rows).
 __device__ __forceinline__ int padded_rows(int rows) { return rows <= 8 ? 8 : (rows <= 16 ? 16 : 32); }
 
@@ -299,42 +293,47 @@ struct Ctx {
 };
 
 // ---- softmax warps -------------------------------------------------------------------
-// A unit's queries on their way to the operand: the MMA warp loads them while the unit before is
-// in its last tiles, and stages them when that has issued its last product.
+// A unit's queries on their way to the operand, THREADS threads at work.  Units of at most 8 rows:
+// the MMA warp loads them while the unit before is in its last tiles, and stages them when that has
+// issued its last product, beside the softmax warps' end of it.  Others: the softmax threads load
+// them before they end the unit before (32 rows are 10000 clocks of one warp).
 template <int D, int MR, int KV>
 struct Queries {
   static constexpr bool kFp8 = KV == VAS_FP8_E4M3;
-  static constexpr int kLanes = D / 8;            // of a row, 8 elements each
-  static constexpr int kAtOnce = 32 / kLanes;     // rows
-  static constexpr int kSteps = MR / kAtOnce;
+  static constexpr int kThreads = MR == 8 ? 32 : 128;
+  static constexpr int kLanes = D / 8;                // of a row, 8 elements each
+  static constexpr int kAtOnce = kThreads / kLanes;   // rows
+  static constexpr int kSteps = (MR + kAtOnce - 1) / kAtOnce;
   uint4 v[kSteps];
 
-  __device__ __forceinline__ void load(const Args& a, const Unit& u, int rp, int lane) {
+  __device__ __forceinline__ void load(const Args& a, const Unit& u, int rp, int thread) {
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      if (i * kAtOnce >= rp) break;
-      const int r = i * kAtOnce + lane / kLanes;
       v[i] = make_uint4(0, 0, 0, 0);
+      if (i * kAtOnce >= rp) continue;
+      const int r = i * kAtOnce + thread / kLanes;
       if (r < u.rows) {
         const int g = u.r0 + r, j = a.by_G.div(g), h = g - j * a.G;
         v[i] = *(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
                                                 ((size_t)(u.row0 + j) * a.Hq + (size_t)u.head * a.G + h) * D) +
-                 lane % kLanes);
+                 thread % kLanes);
       }
     }
   }
 
-  // As E4M3 pairs, or f16, in the K-major operand layout of rp rows.  Returns what brings a score
-  // to base 2.
-  __device__ __forceinline__ float stage(const Args& a, uint8_t* q_tile, int rp, int lane) const {
-    const int c = lane % kLanes;
-    float top = 0.f;
+  // Largest magnitude of a warp's, as bits.
+  __device__ __forceinline__ uint32_t top() const {
+    float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      if (i * kAtOnce >= rp) break;
-      top = fmaxf(top, absmax_bf16x8(v[i]));
-    }
-    const uint32_t all = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+    for (int i = 0; i < kSteps; ++i) t = fmaxf(t, absmax_bf16x8(v[i]));
+    return __reduce_max_sync(0xffffffffu, __float_as_uint(t));
+  }
+
+  // As E4M3 pairs, or f16, in the K-major operand layout of rp rows; all is the unit's top().
+  // Returns what brings a score to base 2.
+  __device__ __forceinline__ float stage(const Args& a, uint8_t* q_tile, int rp, int thread,
+                                         uint32_t all) const {
+    const int c = thread % kLanes;
     // 2^e brings the unit's largest magnitude into [128, 256): the remainder of hi is then at most
     // 8, and 32 of it exact in E4M3 for elements down to 2^-15 of the largest (below, 2^-24 of the
     // largest is lost, as in an fp32 sum of the products).  f16: [2^14, 2^15), exact to 2^-28.
@@ -343,8 +342,8 @@ struct Queries {
     const int rows = kFp8 ? rp : max(rp, 16);  // of the operand (those from rp on may be anything)
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      if (i * kAtOnce >= rp) break;
-      const int r = i * kAtOnce + lane / kLanes;
+      const int r = i * kAtOnce + thread / kLanes;
+      if (r >= rp) continue;
       if constexpr (!kFp8) {
         // Rows of D elements in column blocks of 64: chunk c of 16 bytes.
         *reinterpret_cast<uint4*>(q_tile + (c / 8) * (rows * 128) + r * 128 + (((c ^ r) & 7) << 4)) =
@@ -426,7 +425,8 @@ __device__ __noinline__ bool clear_row(uint8_t* v_row, bool token) {
 // One unit; false after a wait that ran out.  Such a warp waits no more but keeps to the barriers
 // of the others, which leave with it at the end of the unit.
 template <int RP, int D, int MR, int KV>
-__device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u, uint32_t nth_unit, uint32_t& tile_it) {
+__device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u, uint32_t nth_unit,
+                                          uint32_t& tile_it, Queries<D, MR, KV>& q, bool& have_next) {
   using S = Smem<D, MR, KV>;
   constexpr bool kFp8 = KV == VAS_FP8_E4M3;
   constexpr int kParts = parts_of(KV);
@@ -439,7 +439,16 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
 
   const bool tree = a.tree_mask && u.ql > 1 && u.ql <= 64;
   start_rows<RP>(a, m, u, tree);
-  named_bar_sync(1, 128);  // the rows' numbers may be read
+  float score_scale = 0.f;
+  if constexpr (MR != 8) {
+    const uint32_t top = q.top();
+    if (lane == 0) m.q_top[warp] = top;
+    named_bar_sync(1, 128);
+    const uint32_t all = max(max(m.q_top[0], m.q_top[1]), max(m.q_top[2], m.q_top[3]));
+    score_scale = q.stage(a, x.smem + S::kQOff, RP, tid, all);
+  }
+  named_bar_sync(1, 128);  // the rows' numbers may be read, the queries are staged
+  if (MR != 8 && tid == 0) mbar_arrive(&m.q_full);
 
   uint64_t l2[RP / 2];  // sums of the weights of this thread's tokens, two rows each
 #pragma unroll
@@ -448,8 +457,10 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
   auto wait_for = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = wait(bar, parity);
   };
-  wait_for(&m.q_full, nth_unit & 1);
-  const float score_scale = m.score_scale[nth_unit & 1];
+  if constexpr (MR == 8) {
+    wait_for(&m.q_full, nth_unit & 1);
+    score_scale = m.score_scale[nth_unit & 1];
+  }
   const int ctx = u.len - u.ql;
   const int seen_by_all = tree ? ctx - 1 : ctx + (int)a.by_G.div(u.r0);  // the last position all rows see
 
@@ -522,21 +533,39 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
       }
       // Some weight outgrew its row's reference.  The tile's maxima, the new references, and sums
       // and O in them; then the scores once more.
-#pragma unroll 1
-      for (int r0 = 0; r0 < RP; r0 += 8) {
-        uint32_t hi[8], lo[8];
-        tmem_ld<8>(s_at + r0, hi);
-        if (kFp8) tmem_ld<8>(s_at + RP + r0, lo);
-        tmem_wait_ld();
+      {
+        float y[RP];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float raw = kFp8 ? fmaf(__uint_as_float(lo[r]), 1.f / 32, __uint_as_float(hi[r]))
-                                 : __uint_as_float(hi[r]);
-          float y = fmaf(raw, ks, ve);
-          if (isnan(y) || (masked && (poison || dropped(r0 + r)))) y = -INFINITY;
-          const int most = __reduce_max_sync(0xffffffffu, ordered(y));
-          if (lane == 0) m.warp_max[warp][r0 + r] = unordered(most);
+        for (int r0 = 0; r0 < RP; r0 += kLd) {
+          uint32_t hi[kLd], lo[kLd];
+          tmem_ld<kLd>(s_at + r0, hi);
+          if (kFp8) tmem_ld<kLd>(s_at + RP + r0, lo);
+          tmem_wait_ld();
+#pragma unroll
+          for (int r = 0; r < kLd; ++r) {
+            const float raw = kFp8 ? fmaf(__uint_as_float(lo[r]), 1.f / 32, __uint_as_float(hi[r]))
+                                   : __uint_as_float(hi[r]);
+            y[r0 + r] = fmaxf(fmaf(raw, ks, ve), -INFINITY);  // (not a NaN)
+          }
         }
+        if (masked) {
+#pragma unroll
+          for (int r = 0; r < RP; ++r)
+            if (poison || dropped(r)) y[r] = -INFINITY;
+        }
+        // Lanes exchange halves of their rows until each has one: lane / (32 / RP) its row.
+#pragma unroll
+        for (int half = RP / 2, o = 16; half; half >>= 1, o >>= 1) {
+          const bool upper = lane & o;
+#pragma unroll
+          for (int r = 0; r < half; ++r) {
+            const float other = __shfl_xor_sync(0xffffffffu, upper ? y[r] : y[r + half], o);
+            y[r] = fmaxf(upper ? y[r + half] : y[r], other);
+          }
+        }
+#pragma unroll
+        for (int o = 16 / RP; o; o >>= 1) y[0] = fmaxf(y[0], __shfl_xor_sync(0xffffffffu, y[0], o));
+        if (lane % (32 / RP) == 0) m.warp_max[warp][lane / (32 / RP)] = y[0];
       }
       named_bar_sync(1, 128);
       if (tid < RP) {
@@ -634,6 +663,14 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
     if (lane == 0) mbar_arrive(&m.p_full);
   }
 
+  if constexpr (MR != 8) {  // the next unit's queries are on their way while this one ends
+    const uint32_t n = nth_unit + 1;
+    have_next = mbar_test_wait(&m.ufull[n % kRing], (n / kRing) & 1);
+    if (have_next) {
+      const Unit& next = m.ring[n % kRing];
+      if (next.tile0 < next.tile1) q.load(a, next, padded_rows(next.rows), tid);
+    }
+  }
   // The rows' sums over the threads, and the last product.
 #pragma unroll
   for (int r = 0; r < RP; r += 2) {
@@ -1031,15 +1068,20 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
       __syncwarp();
       if (lane == 0) mbar_arrive(&m.uempty[unit_it % kRing]);
       ++unit_it;
-      if (next.tile0 < next.tile1) q.load(a, next, padded_rows(next.rows), lane);
+      if constexpr (MR == 8)
+        if (next.tile0 < next.tile1) q.load(a, next, 8, lane);
     };
     ok = wait(&m.ufull[0], 0);
     if (ok) take_unit();
     while (ok && next.tile0 < next.tile1) {
       u = next;
       const int rp = padded_rows(u.rows), n = u.tile1 - u.tile0;
-      {  // every product that read the queries before is done: their scores have been taken
-        const float scale = q.stage(a, smem + S::kQOff, rp, lane);
+      // Every product that read the queries before is done: their scores have been taken.
+      if constexpr (MR != 8) {
+        ok = wait(&m.q_full, (unit_it - 1) & 1);
+        ok = __all_sync(0xffffffffu, ok);
+      } else {
+        const float scale = q.stage(a, smem + S::kQOff, rp, lane, q.top());
         __syncwarp();
         if (lane == 0) {
           m.score_scale[(unit_it - 1) & 1] = scale;
@@ -1049,7 +1091,7 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
       bool have_next = false;
       uint64_t t0 = 0;
       uint32_t idle = 0;
-      for (int qk = 0, pv = 0; pv < n;) {
+      for (int qk = 0, pv = 0; ok && pv < n;) {
         uint32_t can = 0;
         if (lane == 0) {
           if (pv < qk && mbar_test_wait(&m.p_full, (tile_it + pv) & 1) && v_there(tile_it + pv)) {
@@ -1156,6 +1198,8 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
   } else {
     // ---- softmax ----
     uint32_t unit_it = 0, tile_it = 0;
+    Queries<D, MR, KV> q;
+    bool have_q = false;  // q holds the next unit's
     for (;;) {
       const int slot_u = unit_it % kRing;
       ok = !named_bar_or(1, 128, !wait(&m.ufull[slot_u], (unit_it / kRing) & 1));
@@ -1165,11 +1209,12 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
       if (lane == 0) mbar_arrive(&m.uempty[slot_u]);
       if (u.tile0 >= u.tile1) break;
       if constexpr (MR == 8) {
-        ok = soft_unit<8>(x, u, unit_it, tile_it);
+        ok = soft_unit<8>(x, u, unit_it, tile_it, q, have_q);
       } else {
-        if (u.rows <= 8) ok = soft_unit<8>(x, u, unit_it, tile_it);
-        else if (u.rows <= 16) ok = soft_unit<16>(x, u, unit_it, tile_it);
-        else ok = soft_unit<32>(x, u, unit_it, tile_it);
+        if (!have_q) q.load(a, u, padded_rows(u.rows), threadIdx.x);
+        if (u.rows <= 8) ok = soft_unit<8>(x, u, unit_it, tile_it, q, have_q);
+        else if (u.rows <= 16) ok = soft_unit<16>(x, u, unit_it, tile_it, q, have_q);
+        else ok = soft_unit<32>(x, u, unit_it, tile_it, q, have_q);
       }
       ++unit_it;
       if (!ok) break;
