@@ -44,7 +44,7 @@ constexpr int kSoftWarps = 4;
 constexpr int kProducer = 4;       // warp that streams the pages
 constexpr int kMma = 5;            // warp that issues the products
 constexpr int kConv = 6;            // first of the warps that expand INT8 codes
-constexpr int kConvWarps = 4;
+constexpr int kConvWarps = 6;      // (with 8 the softmax threads had 128 registers, and spilled)
 __host__ __device__ constexpr int threads_of(int kv) { return kv == VAS_FP8_E4M3 ? 192 : 192 + 32 * kConvWarps; }
 __host__ __device__ constexpr int ctas_of(int kv) { return kv == VAS_FP8_E4M3 ? 2 : 1; }  // of an SM
 constexpr int kRing = 4;           // units the producer may run ahead
@@ -81,14 +81,15 @@ template <int D, int MR, int KV>
 struct Smem {
   static constexpr bool kFp8 = KV == VAS_FP8_E4M3;
   static constexpr int kOperand = kTile * D;  // K or V of a tile
-  static constexpr int kSlots = (D == 128 ? 1 : 2) * (MR == 8 ? 6 : 5);
-  static constexpr int kWide = kFp8 ? 0 : 2 * kOperand;  // K or V of a tile in f16
+  // (INT8: two more tiles wait expanded.)
+  static constexpr int kSlots = (D == 128 ? 1 : 2) * (!kFp8 ? 4 : (MR == 8 ? 6 : 5));
+  static constexpr int kWide = kFp8 ? 0 : 2 * kOperand;  // K or V of a tile in f16, two of each
   // Q: two E4M3 rows a row, or one of f16, at least 16 for the product's N.
   static constexpr int kQBytes = kFp8 ? 2 * MR * D : (MR < 16 ? 16 : MR) * D * 2;
   static constexpr int kPBytes = kFp8 ? kTile * MR * 4 : kTile * (MR < 16 ? 16 : MR) * 2;
   static constexpr int kKOff = kSlots * kOperand;  // expanded K, V (INT8)
-  static constexpr int kVOff = kKOff + kWide;
-  static constexpr int kQOff = kVOff + kWide;
+  static constexpr int kVOff = kKOff + 2 * kWide;
+  static constexpr int kQOff = kVOff + 2 * kWide;
   static constexpr int kPOff = kQOff + kQBytes;
   static constexpr int kMiscOff = kPOff + kPBytes;
   static_assert(kQOff % 1024 == 0 && kPOff % 128 == 0 && kMiscOff % 16 == 0, "operand tiles");
@@ -99,7 +100,9 @@ constexpr int kMostSlots = 12;
 struct Misc {
   uint64_t full[kMostSlots], empty[kMostSlots];
   uint64_t ufull[kRing], uempty[kRing];
-  uint64_t k_wide, k_free, v_wide;  // INT8: the tile's expanded K is there, is read; V is there
+  uint64_t scaled[kScaleTiles];     // a tile's scales are there
+  // INT8, by the tile's parity: its expanded K, V are there, have been read.
+  uint64_t k_wide[2], k_free[2], v_wide[2], v_free[2];
   uint64_t fin, q_full, s_full[2], s_empty[2], p_full, pv_done;
   uint64_t tree[kMaxRows];        // the rows' draft-tree masks, own bit set
   Unit ring[kRing];
@@ -118,7 +121,7 @@ struct Misc {
   int32_t start_seq;
   int64_t start_at;               // where in it this CTA's share begins
   int64_t start_row;              // its first query token
-  int64_t wsum[10][2];
+  int64_t wsum[14][2];
   int32_t any_bad;
 };
 
@@ -422,6 +425,24 @@ __device__ __noinline__ bool clear_row(uint8_t* v_row, bool token) {
   return wild;
 }
 
+// Rows' values over the lanes of a warp: lanes exchange halves of their rows until each has one,
+// lane / (32 / RP) its row (31 shuffles for 32 rows, and not 160).
+template <int RP, typename Op>
+__device__ __forceinline__ float over_lanes(float (&v)[RP], int lane, Op op) {
+#pragma unroll
+  for (int half = RP / 2, o = 16; half; half >>= 1, o >>= 1) {
+    const bool upper = lane & o;
+#pragma unroll
+    for (int r = 0; r < half; ++r) {
+      const float other = __shfl_xor_sync(0xffffffffu, upper ? v[r] : v[r + half], o);
+      v[r] = op(upper ? v[r + half] : v[r], other);
+    }
+  }
+#pragma unroll
+  for (int o = 16 / RP; o; o >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  return v[0];
+}
+
 // One unit; false after a wait that ran out.  Such a warp waits no more but keeps to the barriers
 // of the others, which leave with it at the end of the unit.
 template <int RP, int D, int MR, int KV>
@@ -467,10 +488,8 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
   for (int tile = u.tile0; tile < u.tile1; ++tile, ++tile_it) {
     const int b = tile_it & 1;
     const int slot_v = (2 * tile_it + 1) % S::kSlots;
-    // V is there, and with it the scales.
-    if (kFp8) wait_for(&m.full[slot_v], ((2 * tile_it + 1) / S::kSlots) & 1);
-    else wait_for(&m.v_wide, tile_it & 1);
     const int st = tile_it % kScaleTiles;
+    wait_for(&m.scaled[st], (tile_it / kScaleTiles) & 1);
     float vs = m.scales[st][1][tid >> a.log2P];
     // A V scale that is not finite makes its tokens' scores, and so its rows, NaN.
     const float ks = (m.scales[st][0][tid >> a.log2P] + (vs - vs)) * score_scale;
@@ -479,6 +498,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
     const int pos = tile * kTile + tid;
     const bool masked = tile * kTile + kTile - 1 > seen_by_all;
     bool poison = false;
+    if (kFp8 && masked) wait_for(&m.full[slot_v], ((2 * tile_it + 1) / S::kSlots) & 1);
     if (kFp8 && masked && pos > seen_by_all)  // (INT8 codes are numbers, whatever they are)
       poison = clear_row<D>(x.smem + slot_v * S::kOperand + tid * D, pos < u.len);
     // Exponent of the token's V scale, |vs| < 2^ve.
@@ -553,19 +573,8 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
           for (int r = 0; r < RP; ++r)
             if (poison || dropped(r)) y[r] = -INFINITY;
         }
-        // Lanes exchange halves of their rows until each has one: lane / (32 / RP) its row.
-#pragma unroll
-        for (int half = RP / 2, o = 16; half; half >>= 1, o >>= 1) {
-          const bool upper = lane & o;
-#pragma unroll
-          for (int r = 0; r < half; ++r) {
-            const float other = __shfl_xor_sync(0xffffffffu, upper ? y[r] : y[r + half], o);
-            y[r] = fmaxf(upper ? y[r + half] : y[r], other);
-          }
-        }
-#pragma unroll
-        for (int o = 16 / RP; o; o >>= 1) y[0] = fmaxf(y[0], __shfl_xor_sync(0xffffffffu, y[0], o));
-        if (lane % (32 / RP) == 0) m.warp_max[warp][lane / (32 / RP)] = y[0];
+        const float most = over_lanes<RP>(y, lane, [](float p, float q) { return fmaxf(p, q); });
+        if (lane % (32 / RP) == 0) m.warp_max[warp][lane / (32 / RP)] = most;
       }
       named_bar_sync(1, 128);
       if (tid < RP) {
@@ -672,19 +681,12 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
     }
   }
   // The rows' sums over the threads, and the last product.
+  {
+    float y[RP];
 #pragma unroll
-  for (int r = 0; r < RP; r += 2) {
-    float y0, y1;
-    unpair(l2[r / 2], y0, y1);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      y0 += __shfl_xor_sync(0xffffffffu, y0, o);
-      y1 += __shfl_xor_sync(0xffffffffu, y1, o);
-    }
-    if (lane == 0) {
-      m.warp_sum[warp][r] = y0;
-      m.warp_sum[warp][r + 1] = y1;
-    }
+    for (int r = 0; r < RP; r += 2) unpair(l2[r / 2], y[r], y[r + 1]);
+    const float sum = over_lanes<RP>(y, lane, [](float p, float q) { return p + q; });
+    if (lane % (32 / RP) == 0) m.warp_sum[warp][lane / (32 / RP)] = sum;
   }
   wait_for(&m.pv_done, (tile_it - 1) & 1);
   tc_fence_after();
@@ -706,17 +708,23 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
     uint32_t w[kParts][8];
 #pragma unroll
     for (int t = 0; t < kParts; ++t) tmem_ld<8>(x.tmem + lanes + kTmemO + t * RP + r0, w[t]);
+    float inv[8];
+    int64_t at[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      inv[r] = m.inv[r0 + r];
+      at[r] = (u.part >= 0 ? (int64_t)u.part * kMaxRows + r0 + r : m.out_row[r0 + r]) * D + d;
+    }
     tmem_wait_ld();
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      const int q = r0 + r;
       float y = __uint_as_float(w[kParts - 1][r]);
 #pragma unroll
       for (int t = kParts - 2; t >= 0; --t) y = fmaf(y, 0.125f, __uint_as_float(w[t][r]));
-      if (q < u.rows && mine) {
-        y *= m.inv[q];
-        if (u.part >= 0) a.part_o[((size_t)u.part * kMaxRows + q) * D + d] = y;
-        else static_cast<__nv_bfloat16*>(a.out)[m.out_row[q] * D + d] = __float2bfloat16(y);
+      y *= inv[r];
+      if (r0 + r < u.rows && mine) {
+        if (u.part >= 0) a.part_o[at[r]] = y;
+        else static_cast<__nv_bfloat16*>(a.out)[at[r]] = __float2bfloat16(y);
       }
     }
   }
@@ -840,9 +848,13 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
     }
     mbar_init(&m.q_full, 1);
     mbar_init(&m.fin, 1);
-    mbar_init(&m.k_wide, kConvWarps);
-    mbar_init(&m.k_free, 1);
-    mbar_init(&m.v_wide, kConvWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m.k_wide[i], kConvWarps);
+      mbar_init(&m.v_wide[i], kConvWarps);
+      mbar_init(&m.k_free[i], 1);
+      mbar_init(&m.v_free[i], 1);
+    }
+    for (int i = 0; i < kScaleTiles; ++i) mbar_init(&m.scaled[i], 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&m.s_full[i], 1);
       mbar_init(&m.s_empty[i], kSoftWarps);
@@ -966,15 +978,22 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
               const bool my = ((in_tile >> lane) & 1) && good;
               const uint32_t bytes = (uint32_t)__popc(right & in_tile) * a.P * D;
               const int st = tile_it % kScaleTiles;
+              // (The ring keeps the producer fewer than kScaleTiles tiles ahead.)
 #pragma unroll
               for (int o = 0; o < 2; ++o) {
                 const uint32_t it = 2 * tile_it + o;
                 const int slot = it % S::kSlots;
                 ok = wait(&m.empty[slot], ((it / S::kSlots) & 1) ^ 1);
                 if (!ok) break;
-                if ((in_tile >> lane) & 1) m.scales[st][o][lane - l0] = o ? vs : ks;
-                if (lane == 0 && o == 0) m.bad[st] = (wrong & in_tile) != 0;
-                __syncwarp();
+                if (o == 0) {
+                  if ((in_tile >> lane) & 1) {
+                    m.scales[st][0][lane - l0] = ks;
+                    m.scales[st][1][lane - l0] = vs;
+                  }
+                  if (lane == 0) m.bad[st] = (wrong & in_tile) != 0;
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(&m.scaled[st]);
+                }
                 if (lane == 0) mbar_arrive_expect_tx(&m.full[slot], bytes);
                 __syncwarp();
                 if (my)
@@ -1023,12 +1042,12 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
       } else {
         const int n = max(rp, 16);
         const uint32_t idesc = umma_idesc_bf16(128, n, false, false, true);
-        const uint64_t k_desc = desc_f16(ring_at + S::kKOff, 16), q_desc = desc_f16(q_at, 16);
+        const uint64_t k_desc = desc_f16(ring_at + S::kKOff + b * S::kWide, 16), q_desc = desc_f16(q_at, 16);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)  // 64 elements a column block
           mma_f16(x.tmem + kTmemS + 64 * b, k_desc + (k / 4) * ((kTile * 128) >> 4) + 2 * (k % 4),
                   q_desc + (k / 4) * ((n * 128) >> 4) + 2 * (k % 4), idesc, k > 0);
-        umma_commit(&m.k_free);
+        umma_commit(&m.k_free[b]);
       }
       umma_commit(&m.s_full[b]);
     };
@@ -1045,21 +1064,22 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
         umma_commit(&m.empty[slot]);
       } else {
         const uint32_t idesc = umma_idesc_bf16(D, max(rp, 16), true, true, true);
-        const uint64_t v_desc = desc_f16(ring_at + S::kVOff, kTile * 128);
+        const uint64_t v_desc = desc_f16(ring_at + S::kVOff + (it & 1) * S::kWide, kTile * 128);
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
           mma_f16(x.tmem + kTmemO, v_desc + ((16 * 128 * k) >> 4), p_desc + ((256 * k) >> 4), idesc, more || k > 0);
+        umma_commit(&m.v_free[it & 1]);
       }
       umma_commit(&m.pv_done);
     };
     auto k_there = [&](uint32_t it) {
       return kFp8 ? mbar_test_wait(&m.full[2 * it % S::kSlots], (2 * it / S::kSlots) & 1)
-                  : mbar_test_wait(&m.k_wide, it & 1);
+                  : mbar_test_wait(&m.k_wide[it & 1], (it >> 1) & 1);
     };
     auto v_there = [&](uint32_t it) {
       const uint32_t v_it = 2 * it + 1;
       return kFp8 ? mbar_test_wait(&m.full[v_it % S::kSlots], (v_it / S::kSlots) & 1)
-                  : mbar_test_wait(&m.v_wide, it & 1);
+                  : mbar_test_wait(&m.v_wide[it & 1], (it >> 1) & 1);
     };
     Unit u{}, next{};
     Queries<D, MR, KV> q;
@@ -1146,14 +1166,16 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
       uint32_t unit_it = 0, tile_it = 0;
       const int cw = warp - kConv;
       auto expand = [&](const uint8_t* raw, uint8_t* wide) {
-        constexpr int kC = D / 16, kPer = kTile * kC / (32 * kConvWarps);
+        constexpr int kC = D / 16, kAll = kTile * kC, kPer = (kAll / 32 + kConvWarps - 1) / kConvWarps;
         uint4 v[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-          v[i] = reinterpret_cast<const uint4*>(raw)[(i * kConvWarps + cw) * 32 + lane];
+          if ((i * kConvWarps + cw) * 32 < kAll)
+            v[i] = reinterpret_cast<const uint4*>(raw)[(i * kConvWarps + cw) * 32 + lane];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int at = (i * kConvWarps + cw) * 32 + lane, t = at / kC, c = at % kC;
+          if (at >= kAll) break;
           uint4 y[2];
           s8x4_to_f16x4(v[i].x, y[0].x, y[0].y);
           s8x4_to_f16x4(v[i].y, y[0].z, y[0].w);
@@ -1181,14 +1203,15 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
           for (int o = 0; o < 2; ++o) {
             const uint32_t it = 2 * tile_it + o;
             const int slot = it % S::kSlots;
-            // The operand of the tile before has been read: by its scores, by its product.
+            const int w = tile_it & 1;
+            // The operand of two tiles ago has been read: by its scores, by its product.
             ok = wait(&m.full[slot], (it / S::kSlots) & 1) &&
-                 wait(o ? &m.pv_done : &m.k_free, (tile_it & 1) ^ 1);
+                 wait(o ? &m.v_free[w] : &m.k_free[w], ((tile_it >> 1) & 1) ^ 1);
             if (!ok) break;
-            expand(smem + slot * S::kOperand, smem + (o ? S::kVOff : S::kKOff));
+            expand(smem + slot * S::kOperand, smem + (o ? S::kVOff : S::kKOff) + w * S::kWide);
             if (lane == 0) {
               mbar_arrive(&m.empty[slot]);
-              mbar_arrive(o ? &m.v_wide : &m.k_wide);
+              mbar_arrive(o ? &m.v_wide[w] : &m.k_wide[w]);
             }
           }
         }
