@@ -108,6 +108,13 @@ def test_decode_batches(vas_lib, kind, B, hi):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,Hkv", [(8, 8), (16, 2), (24, 2)])
+def test_fewer_tokens_than_sequences(vas_lib, kind, Hq, Hkv):
+    """Windows among sequences without query tokens: as many rows as a decode batch has."""
+    check(vas_lib, make([700, 33, 3000, 5, 129, 64], [3, 0, 2, 0, 0, 1], Hq, Hkv, 128, 16, kind, seed=Hq))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("D,Hkv", [(128, 8), (64, 4)])
 def test_trees(vas_lib, kind, D, Hkv):
     lens, qlens = [40, 3000, 64, 700, 130], [2, 9, 64, 33, 5]

@@ -1,0 +1,156 @@
+"""One iteration of a server on a block-scaled cache: append, attention, read-back, logits to
+probabilities, verification, each step on what the one before it wrote."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from verify_attention_spec_gb300 import workloads as wl
+
+from gpu_common import compare_attention, compare_verify
+
+pytestmark = pytest.mark.gpu
+
+P, HQ, HKV, D, V, K = 16, 16, 2, 128, 1000, 3
+
+
+def _i32(x):
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()
+
+
+@pytest.mark.parametrize("quant", ["fp8_block", "int8_block"])
+def test_iterations(vas_lib, quant):
+    """Three requests, prompts of 40, 7 and 16 tokens, then three verification steps.  Attention is
+    held to the oracle on the pool as it is, the probabilities to their definition in 64 bits, the
+    tokens to the oracle's walk on those probabilities."""
+    v = vas_lib
+    g = torch.Generator().manual_seed(3)
+    pool = v.PagePool(32, P, seed=5)
+    mk = lambda: torch.full((32, P, HKV, D), 0x7F, dtype=torch.uint8, device="cuda")  # noqa: E731
+    kp, vp, ks, vs = mk(), mk(), torch.zeros(32, HKV, device="cuda"), torch.zeros(32, HKV, device="cuda")
+    head = (torch.randn(HQ * D, V, generator=g) / 8).cuda()
+    ids, text = [1, 2, 3], []
+    fmt = oracle.Q_E4M3 if quant == "fp8_block" else oracle.Q_INT8
+    rng = np.random.default_rng(1)
+    for i, n in zip(ids, (40, 7, 16)):
+        pool.admit(i, n)
+        text.append(list(rng.integers(0, V, n)))
+    prompts = [len(t) for t in text]
+    kept = {i: [] for i in ids}  # K rows of each request's tokens, as the model gave them
+
+    def forward(qlens):
+        bt, lens = pool.block_table(ids, 8)
+        T = int(sum(qlens))
+        qkv = torch.randn(T, HQ + 2 * HKV, D, generator=g).to(torch.bfloat16).cuda()
+        a = [_i32(bt), _i32(lens), _i32(qlens)]
+        q = torch.empty(T, HQ, D, dtype=torch.bfloat16, device="cuda")
+        v.paged_kv_append(qkv[:, :HQ], qkv[:, HQ:HQ + HKV], qkv[:, HQ + HKV:], *a, q, kp, vp, k_scale=ks,
+                          v_scale=vs, quant=quant)
+        dims = v.attn_dims(q, kp, a[0], a[1], quant=quant)
+        out, lse = torch.empty_like(q), torch.empty(T, HQ, device="cuda")
+        v.paged_attn_fwd_quant(q, kp, vp, ks, vs, *a, out, lse, v.alloc_workspace(dims), quant=quant, dims=dims)
+        wide = lambda s: s[..., None].expand(-1, -1, P).contiguous().cpu().numpy()  # noqa: E731
+        ref_o, ref_l = oracle.paged_attn_quant(wl.bf16_bits(q.cpu()), kp.cpu().numpy(), vp.cpu().numpy(), wide(ks),
+                                               wide(vs), bt, lens, np.asarray(qlens, np.int32), fmt=fmt)
+        compare_attention(out, lse, ref_o, ref_l, wl.FP8)
+        row = 0
+        for i, n in zip(ids, qlens):
+            kept[i].append(qkv[row:row + n, HQ:HQ + HKV].float().cpu())
+            row += n
+        return out.float().flatten(1) @ head
+
+    forward(prompts)
+    for step in range(3):
+        drafts = rng.integers(0, V, (3, K)).astype(np.int32)
+        for i in ids:
+            assert pool.grow(i, K + 1) == 0
+        logits = forward([K + 1] * 3).reshape(3, K + 1, V).contiguous()
+        m = max(len(t) for t in text)
+        tokens = np.array([t + [-1] * (m - len(t)) for t in text])
+        par = dict(rep=np.array([1.2, 1.0, 0.9]), freq=np.array([0.1, 0.0, 0.3]), temp=np.array([1.0, 0.7, 0.0]))
+        f = lambda x: torch.from_numpy(x.astype(np.float32)).cuda()  # noqa: E731
+        p = torch.empty(3, K + 1, V, device="cuda")
+        v.spec_logits(logits, p, tokens=_i32(tokens), token_lens=_i32([len(t) for t in text]),
+                      prompt_lens=_i32(prompts), draft_tokens=_i32(drafts), repetition_penalty=f(par["rep"]),
+                      frequency_penalty=f(par["freq"]), temperature=f(par["temp"]))
+        want = np.zeros((3, K + 1, V))
+        for b in range(3):
+            for j in range(K + 1):
+                z = logits[b, j].double().cpu().numpy()
+                count = np.bincount(np.concatenate([text[b][prompts[b]:], drafts[b, :j]]).astype(int), minlength=V)
+                seen = (count > 0) | (np.bincount(text[b][:prompts[b]], minlength=V) > 0)
+                r, fr, T = (float(np.float32(par[x][b])) for x in ("rep", "freq", "temp"))
+                z[seen] = np.where(z[seen] > 0, z[seen] / r, z[seen] * r)
+                z -= fr * count
+                if T == 0:
+                    want[b, j, np.argmax(z)] = 1
+                else:
+                    e = np.exp((z - z.max()) / T)
+                    want[b, j] = e / e.sum()
+        # |z| below 2^5 and T above 1/2: the exponent is off by a few 2^-24 of 2^6
+        np.testing.assert_allclose(p.cpu().double().numpy(), want, rtol=2.0 ** -14, atol=2.0 ** -40)
+        q = torch.full((3, K, V), 1.0 / V, device="cuda")
+        acc = torch.empty(3, dtype=torch.int32, device="cuda")
+        got = torch.empty(3, K + 1, dtype=torch.int32, device="cuda")
+        v.spec_verify(p, q, _i32(drafts), 17 + step, acc, got)
+        torch.cuda.synchronize()
+        ref = oracle.spec_verify(p.cpu().numpy(), q.cpu().numpy(), drafts, 17 + step)
+        compare_verify(acc.cpu().numpy(), got.cpu().numpy(), ref)
+        for b, i in enumerate(ids):
+            n = int(acc[b])
+            text[b] += [int(x) for x in got[b, :n + 1]]
+            assert pool.rollback(i, K - n) == 0
+            last = kept[i].pop()
+            kept[i].append(last[:n + 1])
+        # (the slot of the token that was drawn is written by the next step's first row)
+    bt, lens = pool.block_table(ids, 8)
+    T = int(lens.sum())
+    ko, vo = (torch.empty(T, HKV, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    v.paged_kv_read(kp, vp, _i32(bt), _i32(lens), ko, vo, k_scale=ks, v_scale=vs, quant=quant)
+    row = 0
+    for b, i in enumerate(ids):
+        want = torch.cat(kept[i])
+        n = len(want)
+        page = torch.from_numpy(bt[b, np.arange(n) // P]).long().cuda()
+        sc = ks[page].cpu()[..., None]
+        # The scale grew with the page's later tokens a few times at most: a rounding each, none
+        # above half a step of the last scale (INT8) or of the value (E4M3), and bf16's at the end.
+        half = torch.maximum(want.abs() / 16, sc / 1024) if quant == "fp8_block" else sc.expand_as(want)
+        assert ((ko[row:row + n].float().cpu() - want).abs() <= 1.1 * half + want.abs() / 128).all()
+        row += int(lens[b])
+    assert v.vas_last_device_error() == 0
+
+
+@pytest.mark.parametrize("quant", ["fp8_block", "int8_block"])
+def test_offsets_past_32_bits(vas_lib, quant):
+    """A pool of 5 GB an operand: the pages in use lie behind 2^32 bytes."""
+    v = vas_lib
+    pages, p2, h2 = 163840, 32, 8
+    kp = torch.zeros(pages, p2, h2, D, dtype=torch.uint8, device="cuda")
+    vp = torch.zeros_like(kp)
+    ks, vs = torch.ones(pages, h2, device="cuda"), torch.ones(pages, h2, device="cuda")
+    bt = np.array([[pages - 1, pages - 7, pages - 3], [pages - 2, pages - 5, -1]])
+    lens = qlens = [70, 40]
+    g = torch.Generator().manual_seed(1)
+    qkv = torch.randn(110, 3 * h2, D, generator=g).to(torch.bfloat16).cuda()
+    a = [_i32(bt), _i32(lens), _i32(qlens)]
+    v.paged_kv_append(None, qkv[:, h2:2 * h2], qkv[:, 2 * h2:], *a, None, kp, vp, k_scale=ks, v_scale=vs, quant=quant)
+    ko, vo = (torch.empty(110, h2, D, device="cuda") for _ in range(2))
+    v.paged_kv_read(kp, vp, a[0], a[1], ko, vo, k_scale=ks, v_scale=vs, quant=quant)
+    for out, x in ((ko, qkv[:, h2:2 * h2]), (vo, qkv[:, 2 * h2:])):
+        assert (out - x.float()).norm() <= (0.04 if quant == "fp8_block" else 0.02) * x.float().norm()
+    assert int(kp[:pages - 7].max()) == 0
+    q = qkv[:, :h2].contiguous()
+    dims = v.attn_dims(q, kp, a[0], a[1], quant=quant)
+    out, lse = torch.empty_like(q), torch.empty(110, h2, device="cuda")
+    v.paged_attn_fwd_quant(q, kp, vp, ks, vs, *a, out, lse, v.alloc_workspace(dims), quant=quant, dims=dims)
+    row = 0
+    for n in lens:
+        k, x = ko[row:row + n].double(), vo[row:row + n].double()
+        s = torch.einsum("ihd,jhd->hij", q[row:row + n].double(), k) / np.sqrt(D)
+        s = s.masked_fill(torch.triu(torch.ones(n, n, dtype=torch.bool, device="cuda"), 1), -np.inf)
+        want = torch.einsum("hij,jhd->ihd", torch.softmax(s, -1), x)
+        err = (out[row:row + n].double() - want).abs()
+        assert (err <= want.abs() / 256 + 2e-3).all()
+        row += n
+    assert v.vas_last_device_error() == 0

@@ -425,21 +425,22 @@ __device__ __noinline__ bool clear_row(uint8_t* v_row, bool token) {
   return wild;
 }
 
-// Rows' values over the lanes of a warp: lanes exchange halves of their rows until each has one,
-// lane / (32 / RP) its row (31 shuffles for 32 rows, and not 160).
-template <int RP, typename Op>
-__device__ __forceinline__ float over_lanes(float (&v)[RP], int lane, Op op) {
+// The largest of each row over the lanes of a warp: lanes exchange halves of their rows until each
+// has one, lane / (32 / RP) its row (31 shuffles for 32 rows, and not 160.  For the sums at the end
+// of a unit, where the selections are in the way of nothing else, it took longer).
+template <int RP>
+__device__ __forceinline__ float row_maxima(float (&v)[RP], int lane) {
 #pragma unroll
   for (int half = RP / 2, o = 16; half; half >>= 1, o >>= 1) {
     const bool upper = lane & o;
 #pragma unroll
     for (int r = 0; r < half; ++r) {
       const float other = __shfl_xor_sync(0xffffffffu, upper ? v[r] : v[r + half], o);
-      v[r] = op(upper ? v[r + half] : v[r], other);
+      v[r] = fmaxf(upper ? v[r + half] : v[r], other);
     }
   }
 #pragma unroll
-  for (int o = 16 / RP; o; o >>= 1) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+  for (int o = 16 / RP; o; o >>= 1) v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
   return v[0];
 }
 
@@ -573,7 +574,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
           for (int r = 0; r < RP; ++r)
             if (poison || dropped(r)) y[r] = -INFINITY;
         }
-        const float most = over_lanes<RP>(y, lane, [](float p, float q) { return fmaxf(p, q); });
+        const float most = row_maxima<RP>(y, lane);
         if (lane % (32 / RP) == 0) m.warp_max[warp][lane / (32 / RP)] = most;
       }
       named_bar_sync(1, 128);
@@ -681,12 +682,19 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
     }
   }
   // The rows' sums over the threads, and the last product.
-  {
-    float y[RP];
 #pragma unroll
-    for (int r = 0; r < RP; r += 2) unpair(l2[r / 2], y[r], y[r + 1]);
-    const float sum = over_lanes<RP>(y, lane, [](float p, float q) { return p + q; });
-    if (lane % (32 / RP) == 0) m.warp_sum[warp][lane / (32 / RP)] = sum;
+  for (int r = 0; r < RP; r += 2) {
+    float y0, y1;
+    unpair(l2[r / 2], y0, y1);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      y0 += __shfl_xor_sync(0xffffffffu, y0, o);
+      y1 += __shfl_xor_sync(0xffffffffu, y1, o);
+    }
+    if (lane == 0) {
+      m.warp_sum[warp][r] = y0;
+      m.warp_sum[warp][r + 1] = y1;
+    }
   }
   wait_for(&m.pv_done, (tile_it - 1) & 1);
   tc_fence_after();
