@@ -71,10 +71,11 @@ struct Args {
 };
 
 struct Shared {
-  float bias[kMaxBias];
+  float bias[kMaxBias], bias_sum[kMaxBias];  // bias_sum: of a token's first entry, all of them
   int32_t bias_tok[kMaxBias];
-  int32_t parent[kMaxNodes];
-  uint8_t on_path[kMaxNodes + 1];
+  int32_t draft[kMaxNodes], parent[kMaxNodes];
+  uint8_t on_path[kMaxNodes + 1];  // trees: drafts on the way to the row, and (bit 1) to the one before
+  int32_t first_bad;               // the first draft out of range
   float red_max[kWarps], red_sum[kWarps];
   int32_t red_at[kWarps];
   // Written by the cluster's CTAs, by the row's parity.
@@ -208,17 +209,25 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
       }
     }
     bool bad = bad_seq;
-    // The drafts on the way to row j: those before it, or its ancestors.  on_path: now and (bit 1)
-    // at the row before of the same sequence.
+    // The drafts on the way to row j: those before it, or its ancestors.
     if (a.counted && a.n > 0) {
-      __syncthreads();  // the row before is done with these
-      for (int i = tid; i < a.n; i += kThreads) {
-        if (other && a.parents) s.parent[i] = a.parents[(size_t)b * a.n + i];
-        s.on_path[i] = (other ? 0 : (s.on_path[i] & 1) << 1) | (!a.parents && i < j);
+      if (other) {
+        __syncthreads();  // the row before is done with these
+        if (tid == 0) s.first_bad = kMaxNodes;
+        for (int i = tid; i < a.n; i += kThreads) {
+          s.draft[i] = drafts[i];
+          if (a.parents) s.parent[i] = a.parents[(size_t)b * a.n + i];
+        }
+        __syncthreads();
+        for (int i = tid; i < a.n; i += kThreads)
+          if (s.draft[i] < 0 || s.draft[i] >= a.V) atomicMin(&s.first_bad, i);
+        __syncthreads();
       }
-      __syncthreads();
       int e = 0;
       if (a.parents) {
+        __syncthreads();
+        for (int i = tid; i < a.n; i += kThreads) s.on_path[i] = other ? 0 : (s.on_path[i] & 1) << 1;
+        __syncthreads();
         if (tid == 0)
           for (int u = j; u > 0;) {  // ascends: a parent precedes its child
             const int p = s.parent[u - 1];
@@ -230,14 +239,15 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
             u = p;
           }
         __syncthreads();
+        if (s.first_bad < kMaxNodes)
+          for (int i = tid; i < a.n; i += kThreads)
+            if ((s.on_path[i] & 1) && (s.draft[i] < 0 || s.draft[i] >= a.V)) e |= VAS_DEV_BAD_TOKEN;
+        if (e && rank == 0) atomicOr(a.err, e);
+        bad |= __syncthreads_or(e != 0) != 0;
+      } else if (s.first_bad < j) {
+        if (tid == 0 && rank == 0) atomicOr(a.err, VAS_DEV_BAD_TOKEN);
+        bad = true;
       }
-      for (int i = tid; i < a.n; i += kThreads)
-        if (s.on_path[i] & 1) {
-          const int x = drafts[i];
-          if (x < 0 || x >= a.V) e |= VAS_DEV_BAD_TOKEN;
-        }
-      if (e && rank == 0) atomicOr(a.err, e);
-      bad |= __syncthreads_or(e != 0) != 0;
     }
 
     // The entries of chunk k of the slice, anew or with the drafts of another row.
@@ -261,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
         };
         for (int i = tid; i < n_tok; i += kThreads) mark(tokens[i]);
         if (a.counted)
-          for (int i = tid; i < a.n; i += kThreads) mark(drafts[i]);
+          for (int i = tid; i < a.n; i += kThreads) mark(s.draft[i]);
         for (int i = tid; i < nb; i += kThreads) mark(s.bias_tok[i]);
         __syncthreads();
         // A scan of the map words' counts (two a thread at most).
@@ -311,14 +321,23 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
           if (!mine(x)) continue;
           bool head = true;
           for (int e = 0; e < i; ++e) head &= s.bias_tok[e] != x;
-          if (head) atomicOr(words + entry(x), (uint32_t)(i + 1) << kBiasShift);
+          if (!head) continue;
+          float sum = s.bias[i];  // in list order
+          for (int e = i + 1; e < nb; ++e)
+            if (s.bias_tok[e] == x) sum += s.bias[e];
+          s.bias_sum[i] = sum;
+          atomicOr(words + entry(x), (uint32_t)(i + 1) << kBiasShift);
         }
       }
-      if (a.counted)
-        for (int i = tid; i < a.n; i += kThreads) {
-          const int now = s.on_path[i] & 1, was = anew ? 0 : s.on_path[i] >> 1;
-          if (now != was && mine(drafts[i])) atomicAdd(words + entry(drafts[i]), (uint32_t)(now - was));
+      // The row's drafts: a chain's row has one more than the row before.
+      if (a.counted) {
+        const bool chain = a.parents == nullptr;
+        const int i0 = chain && !anew ? j - 1 : 0, i1 = chain ? j : a.n;
+        for (int i = i0 + tid; i < i1; i += kThreads) {
+          const int now = chain ? 1 : s.on_path[i] & 1, was = chain || anew ? 0 : s.on_path[i] >> 1;
+          if (now != was && mine(s.draft[i])) atomicAdd(words + entry(s.draft[i]), (uint32_t)(now - was));
         }
+      }
       __syncthreads();
     };
 
@@ -354,13 +373,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
           float y = widen1(here ? stage[at] : in[base + at]);
           if (w & (kCountMask | kPrompt)) y = y > 0.f ? y / rep : y * rep;
           if (w & kCountMask) y = y - freq * (float)(w & kCountMask) - pres;
-          if (w >> kBiasShift) {
-            const int head = (int)(w >> kBiasShift) - 1;
-            float sum = s.bias[head];  // in list order
-            for (int i = head + 1; i < nb; ++i)
-              if (s.bias_tok[i] == base + at) sum += s.bias[i];
-            y += sum;
-          }
+          if (w >> kBiasShift) y += s.bias_sum[(w >> kBiasShift) - 1];
           values[e] = y;
         }
 #pragma unroll
