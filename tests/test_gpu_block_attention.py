@@ -257,6 +257,30 @@ def test_scores_that_rise_along_a_sequence(vas_lib, kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+def test_scores_that_pass_the_reference_by_its_slack(vas_lib, kind):
+    """The second tile's largest score is above the first tile's by 7 in base 2, where a row's
+    reference moves, to within some last places, a sequence each."""
+    B, D = 400, 128
+    b = make([256] * B, [1] * B, 1, 1, D, 16, kind, seed=12)
+    b.q[...] = 0
+    b.q[..., 0] = 8.0
+    b.vs[...] = 2.0 ** -4
+    b.k[..., 0] = 0x38 if b.fp8 else 1  # 1.0 a score of every token
+    one = 8.0 / np.sqrt(D) * np.log2(np.e)  # a scale's score in base 2
+    rng = np.random.default_rng(13)
+    for i in range(B):
+        x = rng.uniform(0.2, 30)
+        b.ks[b.bt[i, :8], 0] = float(x / one)
+        y = np.float32((x + 7) / one)
+        for _ in range(i % 9):
+            y = np.nextafter(y, np.float32(np.inf))
+        for _ in range(i // 9 % 5):
+            y = np.nextafter(y, np.float32(0))
+        b.ks[b.bt[i, 8:16], 0] = float(y)
+    check(vas_lib, b)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_bad_pages_and_lengths(vas_lib, kind):
     v = vas_lib
     b = make([300, 300, 3000, 40], [1, 5, 1, 1], 16, 2, 128, 16, kind, seed=2)

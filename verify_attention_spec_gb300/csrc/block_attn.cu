@@ -514,9 +514,11 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
     const uint32_t s_at = x.tmem + lanes + kTmemS + 64 * b;
     const uint64_t c32 = pair(1.f / 32, 1.f / 32), ks2 = pair(ks, ks);
     uint64_t t2[RP / 2];  // scores relative to their rows' references
-    for (bool first = tile == u.tile0;; first = false) {
-      if (!first) {  // (the first tile's maxima come first)
-        float top = -INFINITY;
+    // The first tile's references come first.  They move once a tile at most: whether a score passes
+    // its row's by kSlack is rounded differently here and there, and asked again it could be so for
+    // ever.
+    for (bool moved = false;; moved = true) {
+      if (moved || tile > u.tile0) {
 #pragma unroll
         for (int r0 = 0; r0 < RP; r0 += kLd) {
           uint32_t hi[kLd], lo[kLd];
@@ -544,6 +546,8 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
             t2[r / 2] = pair(dropped(r) ? -INFINITY : y0, dropped(r + 1) ? -INFINITY : y1);
           }
         }
+        if (moved) break;
+        float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < RP; r += 2) {
           float y0, y1;
