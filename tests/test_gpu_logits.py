@@ -211,6 +211,36 @@ def test_infinite_and_extreme_logits(vas_lib):
     assert np.isnan(c.call(vas_lib)[2]).all()
 
 
+@pytest.mark.parametrize("V", [5000, 300007])
+def test_low_rows_with_masked_stretches(vas_lib, V):
+    """Rows whose largest logit is far below zero, and whole stretches that the mask takes away."""
+    c = Case(4, 1, V, penalties=False, mask=True)
+    c.temps[:] = [1.0, 0.1, 2.0, 0.0]
+    c.logits[0] -= 150.0
+    c.logits[1] -= 30.0
+    c.logits[2] -= 1e6
+    c.logits[3] = -3e38
+    c.mask[...] = 0
+    c.mask[..., 2::50] = -1
+    c.mask[:, 1, : c.mask.shape[-1] // 2] = 0
+    got = c.check(vas_lib)
+    assert np.allclose(got.sum(-1), 1.0, atol=1e-4)
+
+
+def test_smallest_temperatures(vas_lib):
+    c = Case(3, 0, 900, penalties=False)
+    c.temps[:] = [1e-39, 1e-45, 1e-36]
+    c.check(vas_lib)
+
+
+def test_greedy_rows_with_an_infinite_maximum(vas_lib):
+    c = Case(2, 0, 900, penalties=False)
+    c.temps[:] = 0.0
+    c.logits[1, 0, 5] = float("inf")
+    got = c.call(vas_lib)
+    assert np.isnan(got[1]).all() and np.isfinite(got[0]).all()
+
+
 def test_bad_rows_are_reported_and_alone(vas_lib):
     v = vas_lib
     c = Case(4, 5, 900)

@@ -459,9 +459,9 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
     // exponentials relative to m (0, or NaN, without a finite value); with temperature 0 best is
     // the first token at the maximum, and sum only carries a NaN.
     const bool greedy = temp == 0.f;
-    // (An infinite temperature keeps the sign of -inf.)
-    const float c = temp > 0.f ? fmaxf(1.4426950408889634f / temp, 0x1p-149f) : NAN;
-    float m = -INFINITY, sum = 0.f, ref = 0.f;  // ref: the thread's, 0 where that is not finite
+    // (An infinite temperature keeps the sign of -inf, the smallest ones the 0 of the maximum.)
+    const float c = temp > 0.f ? fminf(fmaxf(1.4426950408889634f / temp, 0x1p-149f), 0x1p127f) : NAN;
+    float m = -INFINITY, sum = 0.f, ref = -INFINITY;  // ref: the thread's maximum
     int best = 0x7fffffff;
     auto rescaled = [&](float v, float from, float to) {
       return greedy || from == -INFINITY ? v : v * exp2f((from - to) * c);
@@ -484,12 +484,13 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
           }
         best = cm > m || (cm == m && at < best) ? at : best;
       } else {
-        ref = cm == -INFINITY ? 0.f : cm;
+        ref = cm;
+        const float from = cm == -INFINITY ? 0.f : cm;
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float y = ex2_approx((z[v][e] - ref) * c);
+            const float y = ex2_approx((z[v][e] - from) * c);
             if (!MULTI) z[v][e] = y;
             cs += y;
           }
@@ -537,11 +538,12 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
     best = lane < C ? s.peer_at[side][lane] : 0x7fffffff;
     join_warp();
     const float row_ref = m == -INFINITY ? 0.f : m;
-    const bool wild = bad || isnan(sum);
+    const bool wild = bad || isnan(sum) || m == INFINITY;
     // A row without a token is 0 throughout.
     const float inv = wild ? NAN : (m == -INFINITY ? 0.f : 1.f / sum);
-    // What the held exponentials, relative to the thread's maximum, are short of the row's.
-    const float f = exp2f((ref - row_ref) * c) * inv;
+    // What the held exponentials, relative to the thread's maximum, are short of the row's.  (A
+    // thread without a token has zeros; against a low row's reference theirs would be infinite.)
+    const float f = (ref == -INFINITY ? 0.f : exp2f((ref - row_ref) * c)) * inv;
     for (int k = 0; k < chunks; ++k) {
       if (MULTI) take_chunk(k);
 #pragma unroll
