@@ -151,6 +151,28 @@ def test_q_of_any_size(vas_lib, kind, D):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,qlens", [(128, [1, 1, 1]), (64, [1, 1, 1]), (128, [1, 5, 40]), (64, [2, 5, 40])])
+def test_heads_far_apart(vas_lib, kind, D, qlens):
+    """Every third head's queries are one large element that the keys are zero at, or an infinity:
+    the heads beside it keep theirs."""
+    b = make([200, 50, 3000], qlens, 16, 4, D, 16, kind, seed=17)
+    b.k[..., 3] = 0
+    b.q[:, ::3] = 0
+    for big in (2.0 ** 30, 2.0 ** 126, -1.9 * 2.0 ** 127):
+        b.q[:, ::3, 3] = big
+        check(vas_lib, b)
+    b.k[..., 3] = 0x38 if b.fp8 else 1
+    b.q[..., 3] = 0
+    ref_o, ref_l = reference(b)
+    for wild in (float("inf"), float("-inf"), float("nan")):
+        b.q[:, ::3, 3] = wild
+        out, lse = run(vas_lib, b)
+        assert torch.isnan(out[:, ::3].float()).all() and torch.isnan(lse[:, ::3]).all()
+        rest = [h for h in range(16) if h % 3]
+        compare_attention(out[:, rest].contiguous(), lse[:, rest].contiguous(), ref_o[:, rest], ref_l[:, rest], wl.FP8)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("D,P", [(128, 16), (64, 32)])
 @pytest.mark.parametrize("qlens", [[1, 4, 2], [1, 1, 1], [17, 30, 33]])
 def test_slots_of_no_token_may_hold_anything(vas_lib, kind, D, P, qlens):

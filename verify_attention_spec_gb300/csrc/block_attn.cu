@@ -108,12 +108,11 @@ struct Misc {
   Unit ring[kRing];
   float scales[kScaleTiles][2][8];
   int32_t bad[kScaleTiles];       // a page of the tile is outside the pool
-  alignas(16) float neg_ref[kMaxRows];  // minus the reference of a row's weights
+  // By pairs of rows: minus the references of their weights, and what brings their scores to base 2.
+  alignas(16) float rows[kMaxRows / 2][2][2];
   alignas(16) float inv[kMaxRows];      // what a row of O is multiplied by at the end
   int64_t out_row[kMaxRows];            // its place in out, in rows
   alignas(16) float alpha[kMaxRows];    // what a new reference does to the old sums
-  uint32_t q_top[kSoftWarps];           // largest magnitudes of the unit's queries
-  float score_scale[2];                 // what brings a score to base 2, by the unit's parity
   float warp_max[kSoftWarps][kMaxRows];
   float warp_sum[kSoftWarps][kMaxRows];
   int32_t limit[kMaxRows];        // last position a row sees
@@ -324,29 +323,30 @@ struct Queries {
     }
   }
 
-  // Largest magnitude of a warp's, as bits.
-  __device__ __forceinline__ uint32_t top() const {
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) t = fmaxf(t, absmax_bf16x8(v[i]));
-    return __reduce_max_sync(0xffffffffu, __float_as_uint(t));
-  }
-
-  // As E4M3 pairs, or f16, in the K-major operand layout of rp rows; all is the unit's top().
-  // Returns what brings a score to base 2.
-  __device__ __forceinline__ float stage(const Args& a, uint8_t* q_tile, int rp, int thread,
-                                         uint32_t all) const {
+  // As E4M3 pairs, or f16, in the K-major operand layout of rp rows; and what brings the rows'
+  // scores to base 2.
+  __device__ __forceinline__ void stage(const Args& a, Misc& m, uint8_t* q_tile, int rp, int thread) const {
     const int c = thread % kLanes;
-    // 2^e brings the unit's largest magnitude into [128, 256): the remainder of hi is then at most
-    // 8, and 32 of it exact in E4M3 for elements down to 2^-15 of the largest (below, 2^-24 of the
+    // 2^e brings a row's largest magnitude into [128, 256): the remainder of hi is then at most 8,
+    // and 32 of it exact in E4M3 for elements down to 2^-15 of the largest (below, 2^-24 of the
     // largest is lost, as in an fp32 sum of the products).  f16: [2^14, 2^15), exact to 2^-28.
-    const int e = max(-112, min(112, (kFp8 ? 7 : 14) - ((int)(all >> 23) - 127)));
-    const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
+    // Each row by its own: others may be far smaller, or this one infinite (its scores are NaN).
+    float top[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) top[i] = absmax_bf16x8(v[i]);
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
     const int rows = kFp8 ? rp : max(rp, 16);  // of the operand (those from rp on may be anything)
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int r = i * kAtOnce + thread / kLanes;
       if (r >= rp) continue;
+      const int e = min(112, (kFp8 ? 7 : 14) - ((int)(__float_as_uint(top[i]) >> 23) - 127));
+      const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
+      if (c == 0)
+        m.rows[r / 2][1][r & 1] = top[i] < INFINITY ? a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
       if constexpr (!kFp8) {
         // Rows of D elements in column blocks of 64: chunk c of 16 bytes.
         *reinterpret_cast<uint4*>(q_tile + (c / 8) * (rows * 128) + r * 128 + (((c ^ r) & 7) << 4)) =
@@ -356,10 +356,8 @@ struct Queries {
         uint32_t hi[2], lo[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float y[4] = {bf16_lo_f32(w[2 * k]) * mul, bf16_hi_f32(w[2 * k]) * mul,
+          const float y[4] = {bf16_lo_f32(w[2 * k]) * mul, bf16_hi_f32(w[2 * k]) * mul,
                         bf16_lo_f32(w[2 * k + 1]) * mul, bf16_hi_f32(w[2 * k + 1]) * mul};
-#pragma unroll
-          for (int f = 0; f < 4; ++f) y[f] += y[f] - y[f];  // an infinity becomes NaN, not 448
           auto pack = [](const float (&z)[4]) {
             uint32_t p;
             asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
@@ -388,7 +386,6 @@ struct Queries {
       }
     }
     fence_proxy_async_smem();
-    return a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
   }
 };
 
@@ -398,7 +395,7 @@ __device__ __forceinline__ void start_rows(const Args& a, Misc& m, const Unit& u
   const int tid = threadIdx.x;
   if (tid >= RP) return;
   const int g = u.r0 + tid, j = min((int)a.by_G.div(g), u.ql - 1);
-  m.neg_ref[tid] = -kNoMax;
+  m.rows[tid / 2][0][tid & 1] = -kNoMax;
   m.out_row[tid] = (int64_t)(u.row0 + j) * a.Hq + (int64_t)u.head * a.G + (g - j * a.G);
   m.limit[tid] = tid < u.rows ? u.len - u.ql + j : -1;
   m.tree[tid] = tree ? (a.tree_mask[u.row0 + j] & (j ? ~0ull >> (64 - j) : 0ull)) | (1ull << j) : ~0ull;
@@ -461,14 +458,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
 
   const bool tree = a.tree_mask && u.ql > 1 && u.ql <= 64;
   start_rows<RP>(a, m, u, tree);
-  float score_scale = 0.f;
-  if constexpr (MR != 8) {
-    const uint32_t top = q.top();
-    if (lane == 0) m.q_top[warp] = top;
-    named_bar_sync(1, 128);
-    const uint32_t all = max(max(m.q_top[0], m.q_top[1]), max(m.q_top[2], m.q_top[3]));
-    score_scale = q.stage(a, x.smem + S::kQOff, RP, tid, all);
-  }
+  if constexpr (MR != 8) q.stage(a, m, x.smem + S::kQOff, RP, tid);
   named_bar_sync(1, 128);  // the rows' numbers may be read, the queries are staged
   if (MR != 8 && tid == 0) mbar_arrive(&m.q_full);
 
@@ -479,10 +469,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
   auto wait_for = [&](uint64_t* bar, uint32_t parity) {
     if (ok) ok = wait(bar, parity);
   };
-  if constexpr (MR == 8) {
-    wait_for(&m.q_full, nth_unit & 1);
-    score_scale = m.score_scale[nth_unit & 1];
-  }
+  if constexpr (MR == 8) wait_for(&m.q_full, nth_unit & 1);
   const int ctx = u.len - u.ql;
   const int seen_by_all = tree ? ctx - 1 : ctx + (int)a.by_G.div(u.r0);  // the last position all rows see
 
@@ -493,7 +480,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
     wait_for(&m.scaled[st], (tile_it / kScaleTiles) & 1);
     float vs = m.scales[st][1][tid >> a.log2P];
     // A V scale that is not finite makes its tokens' scores, and so its rows, NaN.
-    const float ks = (m.scales[st][0][tid >> a.log2P] + (vs - vs)) * score_scale;
+    const float ks = m.scales[st][0][tid >> a.log2P] + (vs - vs);
     if (vs - vs != 0.f) vs = 0.f;
     bad |= m.bad[st] != 0;
     const int pos = tile * kTile + tid;
@@ -528,12 +515,13 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
 #pragma unroll
           for (int r = 0; r < kLd; r += 2) {
             const uint64_t h2 = pair(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1]));
-            const uint64_t neg = *reinterpret_cast<const uint64_t*>(&m.neg_ref[r0 + r]);
+            const float4 row = *reinterpret_cast<const float4*>(m.rows[(r0 + r) / 2]);
+            const uint64_t neg = pair(row.x, row.y), by = mul2(ks2, pair(row.z, row.w));
             if constexpr (kFp8) {
               const uint64_t w2 = pair(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1]));
-              t2[(r0 + r) / 2] = fma2(fma2(w2, c32, h2), ks2, neg);
+              t2[(r0 + r) / 2] = fma2(fma2(w2, c32, h2), by, neg);
             } else {
-              t2[(r0 + r) / 2] = fma2(h2, ks2, neg);
+              t2[(r0 + r) / 2] = fma2(h2, by, neg);
             }
           }
         }
@@ -570,7 +558,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
           for (int r = 0; r < kLd; ++r) {
             const float raw = kFp8 ? fmaf(__uint_as_float(lo[r]), 1.f / 32, __uint_as_float(hi[r]))
                                    : __uint_as_float(hi[r]);
-            y[r0 + r] = fmaxf(fmaf(raw, ks, ve), -INFINITY);  // (not a NaN)
+            y[r0 + r] = fmaxf(fmaf(raw, ks * m.rows[(r0 + r) / 2][1][r & 1], ve), -INFINITY);  // (not a NaN)
           }
         }
         if (masked) {
@@ -585,10 +573,11 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
       if (tid < RP) {
         const float most = fmaxf(fmaxf(m.warp_max[0][tid], m.warp_max[1][tid]),
                                  fmaxf(m.warp_max[2][tid], m.warp_max[3][tid]));
-        const float old = -m.neg_ref[tid];
+        float& neg_ref = m.rows[tid / 2][0][tid & 1];
+        const float old = -neg_ref;
         const bool up = most > old + kSlack;
         m.alpha[tid] = up ? ex2_approx(old - most) : 1.f;
-        if (up) m.neg_ref[tid] = -most;
+        if (up) neg_ref = -most;
       }
       const bool have_o = tile > u.tile0;
       if (have_o) wait_for(&m.pv_done, (tile_it - 1) & 1);
@@ -706,7 +695,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
   bad = named_bar_or(1, 128, bad);
   if (tid < u.rows) {
     const float sum = (m.warp_sum[0][tid] + m.warp_sum[1][tid]) + (m.warp_sum[2][tid] + m.warp_sum[3][tid]);
-    float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - m.neg_ref[tid];
+    float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - m.rows[tid / 2][0][tid & 1];
     if (bad) lse2 = NAN;
     m.inv[tid] = isnan(lse2) ? NAN : (sum == 0.f ? 0.f : 1.f / (sum * kBase));
     if (u.part >= 0) a.part_lse[(size_t)u.part * kMaxRows + tid] = lse2;
@@ -1113,12 +1102,9 @@ __global__ void __launch_bounds__(threads_of(KV), ctas_of(KV))
         ok = wait(&m.q_full, (unit_it - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
       } else {
-        const float scale = q.stage(a, smem + S::kQOff, rp, lane, q.top());
+        q.stage(a, m, smem + S::kQOff, rp, lane);
         __syncwarp();
-        if (lane == 0) {
-          m.score_scale[(unit_it - 1) & 1] = scale;
-          mbar_arrive(&m.q_full);
-        }
+        if (lane == 0) mbar_arrive(&m.q_full);
       }
       bool have_next = false;
       uint64_t t0 = 0;
