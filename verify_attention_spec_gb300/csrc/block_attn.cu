@@ -108,11 +108,14 @@ struct Misc {
   Unit ring[kRing];
   float scales[kScaleTiles][2][8];
   int32_t bad[kScaleTiles];       // a page of the tile is outside the pool
-  // By pairs of rows: minus the references of their weights, and what brings their scores to base 2.
-  alignas(16) float rows[kMaxRows / 2][2][2];
+  alignas(16) float neg_ref[kMaxRows];  // minus the reference of a row's weights
   alignas(16) float inv[kMaxRows];      // what a row of O is multiplied by at the end
   int64_t out_row[kMaxRows];            // its place in out, in rows
   alignas(16) float alpha[kMaxRows];    // what a new reference does to the old sums
+  uint32_t q_top[kSoftWarps], q_low[kSoftWarps];  // of the rows' largest magnitudes, the ends
+  float score_scale;                    // what brings a score to base 2,
+  int32_t uneven;                       // after, where this is set, its row's factor
+  float row_scale[kMaxRows];
   float warp_max[kSoftWarps][kMaxRows];
   float warp_sum[kSoftWarps][kMaxRows];
   int32_t limit[kMaxRows];        // last position a row sees
@@ -323,30 +326,57 @@ struct Queries {
     }
   }
 
-  // As E4M3 pairs, or f16, in the K-major operand layout of rp rows; and what brings the rows'
-  // scores to base 2.
+  // As E4M3 pairs, or f16, in the K-major operand layout of rp rows; and what brings their scores to
+  // base 2.
   __device__ __forceinline__ void stage(const Args& a, Misc& m, uint8_t* q_tile, int rp, int thread) const {
     const int c = thread % kLanes;
-    // 2^e brings a row's largest magnitude into [128, 256): the remainder of hi is then at most 8,
-    // and 32 of it exact in E4M3 for elements down to 2^-15 of the largest (below, 2^-24 of the
-    // largest is lost, as in an fp32 sum of the products).  f16: [2^14, 2^15), exact to 2^-28.
-    // Each row by its own: others may be far smaller, or this one infinite (its scores are NaN).
-    float top[kSteps];
+    float top[kSteps];  // of a row
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) top[i] = absmax_bf16x8(v[i]);
 #pragma unroll
     for (int o = kLanes / 2; o; o >>= 1)
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+    uint32_t most = 0, least = 0xffffffffu;  // (rows of zeros are as any other)
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      most = max(most, __float_as_uint(top[i]));
+      least = min(least, __float_as_uint(top[i]) - 1);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
+    if constexpr (kThreads > 32) {
+      if (thread % 32 == 0) {
+        m.q_top[thread / 32] = most;
+        m.q_low[thread / 32] = least;
+      }
+      named_bar_sync(1, kThreads);
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        most = max(most, m.q_top[w]);
+        least = min(least, m.q_low[w]);
+      }
+    }
+    // 2^e brings the largest magnitude into [128, 256): the remainder of hi is then at most 8, and 32
+    // of it exact in E4M3 for elements down to 2^-15 of the largest (below, 2^-24 of the largest is
+    // lost, as in an fp32 sum of the products).  f16: [2^14, 2^15), exact to 2^-28.  The unit's
+    // largest, where its rows' are within 2^8.  Else each row's: others may be far smaller, or one
+    // infinite (its scores are NaN); then the scores take one more pass, for a factor of their own.
+    const bool even = most < 0x7f800000u && (least > most || (most >> 23) - (least >> 23) <= 8);
+    auto exponent = [&](uint32_t t) { return min(112, (kFp8 ? 7 : 14) - ((int)(t >> 23) - 127)); };
+    auto power = [](int e) { return __uint_as_float((uint32_t)(127 + e) << 23); };
+    if (thread == 0) {
+      m.score_scale = even ? a.scale_log2 * power(-exponent(most)) : a.scale_log2;
+      m.uneven = !even;
+    }
     const int rows = kFp8 ? rp : max(rp, 16);  // of the operand (those from rp on may be anything)
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int r = i * kAtOnce + thread / kLanes;
       if (r >= rp) continue;
-      const int e = min(112, (kFp8 ? 7 : 14) - ((int)(__float_as_uint(top[i]) >> 23) - 127));
-      const float mul = __uint_as_float((uint32_t)(127 + e) << 23);
-      if (c == 0)
-        m.rows[r / 2][1][r & 1] = top[i] < INFINITY ? a.scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) : NAN;
+      const int e = exponent(even ? most : __float_as_uint(top[i]));
+      const float mul = power(e);
+      if (!even && c == 0) m.row_scale[r] = top[i] < INFINITY ? power(-e) : NAN;
       if constexpr (!kFp8) {
         // Rows of D elements in column blocks of 64: chunk c of 16 bytes.
         *reinterpret_cast<uint4*>(q_tile + (c / 8) * (rows * 128) + r * 128 + (((c ^ r) & 7) << 4)) =
@@ -395,7 +425,7 @@ __device__ __forceinline__ void start_rows(const Args& a, Misc& m, const Unit& u
   const int tid = threadIdx.x;
   if (tid >= RP) return;
   const int g = u.r0 + tid, j = min((int)a.by_G.div(g), u.ql - 1);
-  m.rows[tid / 2][0][tid & 1] = -kNoMax;
+  m.neg_ref[tid] = -kNoMax;
   m.out_row[tid] = (int64_t)(u.row0 + j) * a.Hq + (int64_t)u.head * a.G + (g - j * a.G);
   m.limit[tid] = tid < u.rows ? u.len - u.ql + j : -1;
   m.tree[tid] = tree ? (a.tree_mask[u.row0 + j] & (j ? ~0ull >> (64 - j) : 0ull)) | (1ull << j) : ~0ull;
@@ -441,6 +471,21 @@ __device__ __forceinline__ float row_maxima(float (&v)[RP], int lane) {
   return v[0];
 }
 
+// Scores times their rows' factors, where they are (8 rows of INT8: columns 8 on are of none).  Kept
+// out of the loops that seldom need it.
+__device__ __noinline__ void scale_scores(uint32_t s_at, int columns, int row_mask, const float* row_scale) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < columns; c0 += 16) {
+    uint32_t w[16];
+    tmem_ld<16>(s_at + c0, w);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 16; ++c) w[c] = __float_as_uint(__uint_as_float(w[c]) * row_scale[(c0 + c) & row_mask]);
+    tmem_st16(s_at + c0, w);
+  }
+  tmem_wait_st();
+}
+
 // One unit; false after a wait that ran out.  Such a warp waits no more but keeps to the barriers
 // of the others, which leave with it at the end of the unit.
 template <int RP, int D, int MR, int KV>
@@ -470,6 +515,8 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
     if (ok) ok = wait(bar, parity);
   };
   if constexpr (MR == 8) wait_for(&m.q_full, nth_unit & 1);
+  const float score_scale = m.score_scale;
+  const bool uneven = m.uneven;
   const int ctx = u.len - u.ql;
   const int seen_by_all = tree ? ctx - 1 : ctx + (int)a.by_G.div(u.r0);  // the last position all rows see
 
@@ -480,7 +527,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
     wait_for(&m.scaled[st], (tile_it / kScaleTiles) & 1);
     float vs = m.scales[st][1][tid >> a.log2P];
     // A V scale that is not finite makes its tokens' scores, and so its rows, NaN.
-    const float ks = m.scales[st][0][tid >> a.log2P] + (vs - vs);
+    const float ks = (m.scales[st][0][tid >> a.log2P] + (vs - vs)) * score_scale;
     if (vs - vs != 0.f) vs = 0.f;
     bad |= m.bad[st] != 0;
     const int pos = tile * kTile + tid;
@@ -499,6 +546,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
     wait_for(&m.s_full[b], (tile_it >> 1) & 1);
     tc_fence_after();
     const uint32_t s_at = x.tmem + lanes + kTmemS + 64 * b;
+    if (uneven) scale_scores(s_at, kFp8 ? 2 * RP : RP, RP - 1, m.row_scale);
     const uint64_t c32 = pair(1.f / 32, 1.f / 32), ks2 = pair(ks, ks);
     uint64_t t2[RP / 2];  // scores relative to their rows' references
     // The first tile's references come first.  They move once a tile at most: whether a score passes
@@ -515,13 +563,12 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
 #pragma unroll
           for (int r = 0; r < kLd; r += 2) {
             const uint64_t h2 = pair(__uint_as_float(hi[r]), __uint_as_float(hi[r + 1]));
-            const float4 row = *reinterpret_cast<const float4*>(m.rows[(r0 + r) / 2]);
-            const uint64_t neg = pair(row.x, row.y), by = mul2(ks2, pair(row.z, row.w));
+            const uint64_t neg = *reinterpret_cast<const uint64_t*>(&m.neg_ref[r0 + r]);
             if constexpr (kFp8) {
               const uint64_t w2 = pair(__uint_as_float(lo[r]), __uint_as_float(lo[r + 1]));
-              t2[(r0 + r) / 2] = fma2(fma2(w2, c32, h2), by, neg);
+              t2[(r0 + r) / 2] = fma2(fma2(w2, c32, h2), ks2, neg);
             } else {
-              t2[(r0 + r) / 2] = fma2(h2, by, neg);
+              t2[(r0 + r) / 2] = fma2(h2, ks2, neg);
             }
           }
         }
@@ -558,7 +605,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
           for (int r = 0; r < kLd; ++r) {
             const float raw = kFp8 ? fmaf(__uint_as_float(lo[r]), 1.f / 32, __uint_as_float(hi[r]))
                                    : __uint_as_float(hi[r]);
-            y[r0 + r] = fmaxf(fmaf(raw, ks * m.rows[(r0 + r) / 2][1][r & 1], ve), -INFINITY);  // (not a NaN)
+            y[r0 + r] = fmaxf(fmaf(raw, ks, ve), -INFINITY);  // (not a NaN)
           }
         }
         if (masked) {
@@ -573,11 +620,10 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
       if (tid < RP) {
         const float most = fmaxf(fmaxf(m.warp_max[0][tid], m.warp_max[1][tid]),
                                  fmaxf(m.warp_max[2][tid], m.warp_max[3][tid]));
-        float& neg_ref = m.rows[tid / 2][0][tid & 1];
-        const float old = -neg_ref;
+        const float old = -m.neg_ref[tid];
         const bool up = most > old + kSlack;
         m.alpha[tid] = up ? ex2_approx(old - most) : 1.f;
-        if (up) neg_ref = -most;
+        if (up) m.neg_ref[tid] = -most;
       }
       const bool have_o = tile > u.tile0;
       if (have_o) wait_for(&m.pv_done, (tile_it - 1) & 1);
@@ -695,7 +741,7 @@ __device__ __forceinline__ bool soft_unit(const Ctx<D, MR, KV>& x, const Unit& u
   bad = named_bar_or(1, 128, bad);
   if (tid < u.rows) {
     const float sum = (m.warp_sum[0][tid] + m.warp_sum[1][tid]) + (m.warp_sum[2][tid] + m.warp_sum[3][tid]);
-    float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - m.rows[tid / 2][0][tid & 1];
+    float lse2 = sum == 0.f ? -INFINITY : log2f(sum) - m.neg_ref[tid];
     if (bad) lse2 = NAN;
     m.inv[tid] = isnan(lse2) ? NAN : (sum == 0.f ? 0.f : 1.f / (sum * kBase));
     if (u.part >= 0) a.part_lse[(size_t)u.part * kMaxRows + tid] = lse2;
