@@ -207,7 +207,8 @@ int paged_attn_fwd_tree(const void* q, const void* k_pages, const void* v_pages,
  *             VAS_FP8_BLOCK, VAS_INT8_BLOCK: [num_pages, Hkv], one scale for the codes of a
  *             page and head: k = k_scale[p * num_kv_heads + h] * code(k_pages[p][t][h][d]).
  * q, out      [T, Hq, D] bf16.  lse, block_table, seq_lens, query_lens, workspace: as for
- *             paged_attn_fwd (the workspace queries are the same for every kv_dtype).
+ *             paged_attn_fwd (the workspace queries are the same for every kv_dtype, but for the
+ *             block-scaled ones, whose workspace does not depend on the batch).
  * tree_mask   null (the causal window) or the draft-tree masks of paged_attn_fwd_tree.
  * Arithmetic: the codes are exact in f16; Q is taken to f16 (scaled by a power of two
  * when its magnitude nears the f16 range), products accumulate in fp32, and P enters
@@ -215,6 +216,12 @@ int paged_attn_fwd_tree(const void* q, const void* k_pages, const void* v_pages,
  * of two that follows the V scales, so that the largest lie between 2^6 and 2^15 and the
  * size of V does not matter (|v_scale| between 2^-60 and 2^66; weights times V scales
  * 2^20 below the largest lose bits, steps of 2^-24).
+ * Block-scaled pages: Q times a power of two (that of the largest of some query rows of a KV
+ * head, or the row's own) is taken to two E4M3 parts for E4M3 codes, exact for elements down to
+ * 2^-15 of the largest and to 2^-24 of it below, or to f16 for INT8; P enters as that f16, whole
+ * (INT8) or in E5M2 parts that hold all its bits (E4M3).  A query row with an infinity is NaN; a
+ * token with NaN codes makes NaN of the rows that see it (at least the elements whose values are).
+ * An attended page's scale that is not finite makes the rows NaN.
  * Errors: those of paged_attn_fwd; a kv_dtype that is not quantised, or a null scale
  * array, is VAS_E_INVALID_ARG.  paged_attn_fwd and paged_attn_fwd_tree reject the
  * quantised kv_dtypes with VAS_E_INVALID_ARG.

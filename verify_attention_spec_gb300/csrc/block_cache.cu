@@ -29,10 +29,13 @@ namespace cache {
 // applied), settles the scale, requantises the tokens the page held if the scale grew, and
 // writes the codes.  Between the magnitude and the codes the values wait in shared memory, each
 // lane's own (computed twice instead, with the rows held as they came, the angles' second reads
-// made eight 1024-token chunks 124 us and not 105).
+// cost 19 us of eight 1024-token chunks).
 // A block's first kv_warps warps take runs, the others the queries' rows as append_kernel does, and
 // so do the first when the runs are done: the pages' chains of look-ups go on under the queries'
 // stream.  A block has its tasks of either kind, its warps take the next one as they come to it.
+// Bytes bound large calls (eight 1024-token chunks of 64 + 8 + 8 heads of 128: 76 us, 0.62 of the copy
+// rate, norms, rotation and conversion taking 48 % of the issue slots), a task's chain of look-ups,
+// loads, maximum and stores small ones (64 tokens: 6.6 us).
 struct Runs {
   int32_t row0[kAppendSeqs + 1];  // first packed row of every `step`th sequence
   int32_t run0[kAppendSeqs + 1];  // and its first run; the last ones are the totals
@@ -459,7 +462,8 @@ __device__ __forceinline__ void write_elements(float* p, const float (&y)[4]) {
 
 // KV: element type of the pool; BLOCK: one scale per page and head.  A warp takes one token
 // at a time; a lane 16 bytes of output at a time, of K and then of V, kReadBatch of them in
-// flight, while the next token's page is looked up.  Bytes bound it.
+// flight, while the next token's page is looked up.  Bytes bound it (161 MB of codes to bf16: 79 us,
+// 0.90 of the copy rate; one in flight and no look-up ahead took 120).
 constexpr int kReadBatch = 4;
 template <int KV, bool BLOCK, typename OUT>
 __global__ void __launch_bounds__(kAppendThreads) read_kernel(const ReadArgs a) {

@@ -31,9 +31,11 @@ namespace logits {
 // the drafts' counts change.
 // Exponentials are taken once, relative to the thread's own maximum, and scaled by one product
 // when the row's maximum and sum are known.
-// Bytes bound it: V (2 or 4 + 4) a row.  Vocabularies past the registers' reach (8 * 512 * 64 =
-// 262144 logits) are taken in chunks, the table made anew and the logits read again for the
-// second pass.
+// Bytes are its floor, V (2 or 4 + 4) a row: 320 rows of 128256 bf16 logits 127 us, 0.29 of the copy
+// rate, 42 % of the issue slots taken.  Between lie the entries and the barriers of a row: its loads,
+// arithmetic and stores take turns in a CTA, two CTAs share an SM.
+// Vocabularies past the registers' reach (8 * 512 * 64 = 262144 logits) are taken in chunks, the table
+// made anew and the logits read again for the second pass.
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
