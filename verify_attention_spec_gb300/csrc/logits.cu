@@ -581,6 +581,11 @@ int entries_of(const Args& a, int tokens) {
   return (int)((std::min<int64_t>(most, tokens) + 8) / 8 * 8);
 }
 
+// Room for two CTAs of an SM, with a slice's entries and the next row's.
+bool room(const Args& a, int slice, int size) {
+  return entries_of(a, slice) * kEntryBytes + (slice * size + 15) / 16 * 16 <= 96 * 1024;
+}
+
 template <typename T, bool VEC, int NV, bool MULTI>
 int launch(Args& a, cudaStream_t stream) {
   constexpr int kTokens = Tile<T, VEC, NV>::kTokens;
@@ -598,8 +603,7 @@ int launch(Args& a, cudaStream_t stream) {
   a.entries = entries_of(a, MULTI ? kTokens : a.slice);
   const int fixed = a.entries * kEntryBytes;
   const int place = (int)((a.slice * sizeof(T) + 15) / 16 * 16);
-  // Rows by bulk copy where two CTAs of an SM still have room for it.
-  a.staged = VEC && !MULTI && fixed + place <= 96 * 1024;
+  a.staged = VEC && !MULTI && room(a, a.slice, sizeof(T));
   const int smem = fixed + (a.staged ? place : 0);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.cluster);
@@ -639,10 +643,16 @@ int launch(Args& a, cudaStream_t stream) {
 
 template <typename T, bool VEC>
 int launch_size(Args& a, cudaStream_t stream) {
-  // As many CTAs a row as have at least 8 logits a thread, at most a portable cluster.
-  int cluster = (a.V + kThreads * 8 - 1) / (kThreads * 8);
-  if (cluster > kMaxCluster) cluster = kMaxCluster;
-  a.slice = ((a.V + cluster - 1) / cluster + 31) / 32 * 32;
+  // Few rows: as many CTAs a row as have at least 8 logits a thread, at most a portable cluster.
+  // Rows that fill the GPU with fewer CTAs each: no more than that takes, or than keeps 32 logits a
+  // thread and the entries and next row of two CTAs in shared memory.  (A row is a chain of look-ups
+  // and barriers however many share it.)
+  const int widest = std::min((a.V + kThreads * 8 - 1) / (kThreads * 8), kMaxCluster);
+  const int wanted = (2 * vas::num_sms() + a.rows - 1) / a.rows;
+  auto slice_of = [&](int c) { return ((a.V + c - 1) / c + 31) / 32 * 32; };
+  int cluster = std::min(wanted, widest);
+  while (cluster < widest && (slice_of(cluster) > kThreads * 32 || !room(a, slice_of(cluster), sizeof(T)))) ++cluster;
+  a.slice = slice_of(cluster);
   a.cluster = cluster;
   const int per = (a.slice + kThreads * 8 - 1) / (kThreads * 8);
   if (per <= 1) return launch<T, VEC, 1, false>(a, stream);
