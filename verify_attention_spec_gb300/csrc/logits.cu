@@ -42,7 +42,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kMaxBias = 1024;
 constexpr int kMaxTokens = 1 << 20;  // of a list: a count fits its field
 constexpr int kMaxNodes = 255;
-// The word of an entry: count, prompt flag, bias entry + 1.
+// The word of an entry: count, prompt flag, kMaxBias less its bias's place.
 constexpr uint32_t kCountMask = (1u << 20) - 1, kPrompt = 1u << 20;
 constexpr int kBiasShift = 21;
 
@@ -133,8 +133,11 @@ __device__ __forceinline__ void load8(const float* p, float (&y)[8]) {
 __device__ __forceinline__ float widen1(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float widen1(float x) { return x; }
 
+// CTAs of an SM (three of 8 logits a thread: 40 rows of 32000 logits 13 us, with two 17).
+__host__ __device__ constexpr int ctas_of(int nv, bool multi) { return multi || nv > 4 ? 1 : (nv == 1 ? 3 : 2); }
+
 template <typename T, bool VEC, int NV, bool MULTI>
-__global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logits_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, ctas_of(NV, MULTI)) spec_logits_kernel(const Args a) {
   using L = Tile<T, VEC, NV>;
   constexpr int kMapWords = L::kTokens / 32;
   // The entries' words, adjusted logits and places, and the place of a row's slice.
@@ -311,24 +314,29 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
           }
         }
         __syncthreads();
+        if (nb) {
+          // Of a token's biases the first stands for all of them.
+          bool twice = false;
+          for (int i = tid; i < nb; i += kThreads) {
+            const int x = s.bias_tok[i];
+            if (mine(x)) twice |= atomicMax(words + entry(x), (uint32_t)(kMaxBias - i) << kBiasShift) != 0;
+            s.bias_sum[i] = s.bias[i];
+          }
+          if (__syncthreads_or(twice))
+            for (int i = tid; i < nb; i += kThreads) {
+              const int x = s.bias_tok[i];
+              if (!mine(x) || words[entry(x)] >> kBiasShift != (uint32_t)(kMaxBias - i)) continue;
+              float sum = s.bias[i];  // in list order
+              for (int e = i + 1; e < nb; ++e)
+                if (s.bias_tok[e] == x) sum += s.bias[e];
+              s.bias_sum[i] = sum;
+            }
+        }
         for (int i = tid; i < n_tok; i += kThreads) {
           const int32_t x = tokens[i];
           if (!mine(x)) continue;
           if (i < n_prompt) atomicOr(words + entry(x), kPrompt);
           else atomicAdd(words + entry(x), 1u);
-        }
-        // Of a token's biases the first stands for all of them.
-        for (int i = tid; i < nb; i += kThreads) {
-          const int x = s.bias_tok[i];
-          if (!mine(x)) continue;
-          bool head = true;
-          for (int e = 0; e < i; ++e) head &= s.bias_tok[e] != x;
-          if (!head) continue;
-          float sum = s.bias[i];  // in list order
-          for (int e = i + 1; e < nb; ++e)
-            if (s.bias_tok[e] == x) sum += s.bias[e];
-          s.bias_sum[i] = sum;
-          atomicOr(words + entry(x), (uint32_t)(i + 1) << kBiasShift);
         }
       }
       // The row's drafts: a chain's row has one more than the row before.
@@ -375,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, NV <= 4 && !MULTI ? 2 : 1) spec_logi
           float y = widen1(here ? stage[at] : in[base + at]);
           if (w & (kCountMask | kPrompt)) y = y > 0.f ? y / rep : y * rep;
           if (w & kCountMask) y = y - freq * (float)(w & kCountMask) - pres;
-          if (w >> kBiasShift) y += s.bias_sum[(w >> kBiasShift) - 1];
+          if (w >> kBiasShift) y += s.bias_sum[kMaxBias - (w >> kBiasShift)];
           values[e] = y;
         }
 #pragma unroll
@@ -646,7 +654,7 @@ int launch_size(Args& a, cudaStream_t stream) {
   // Few rows: as many CTAs a row as have at least 8 logits a thread, at most a portable cluster.
   // Rows that fill the GPU with fewer CTAs each: no more than that takes, or than keeps 32 logits a
   // thread and the entries and next row of two CTAs in shared memory.  (A row is a chain of look-ups
-  // and barriers however many share it.)
+  // and barriers however many share it: 280 sequences' rows of 32000 logits 33 us, with 8 CTAs 89.)
   const int widest = std::min((a.V + kThreads * 8 - 1) / (kThreads * 8), kMaxCluster);
   const int wanted = (2 * vas::num_sms() + a.rows - 1) / a.rows;
   auto slice_of = [&](int c) { return ((a.V + c - 1) / c + 31) / 32 * 32; };
