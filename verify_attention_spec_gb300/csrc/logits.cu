@@ -80,9 +80,9 @@ struct Shared {
   int32_t first_bad;               // the first draft out of range
   float red_max[kWarps], red_sum[kWarps];
   int32_t red_at[kWarps];
-  // Written by the cluster's CTAs, by the row's parity.
-  float peer_max[2][kMaxCluster], peer_sum[2][kMaxCluster];
-  int32_t peer_at[2][kMaxCluster];
+  // Maximum, sum and first place of the cluster's CTAs, by the row's parity, and their arrival.
+  alignas(16) uint32_t peer[2][kMaxCluster][4];
+  uint64_t joined[2];
   uint64_t landed;
   int32_t scan[kWarps];
 };
@@ -97,8 +97,12 @@ __device__ __forceinline__ uint32_t peer_address(const void* p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void peer_store(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+// 16 bytes to a peer's shared memory, counted by its barrier.
+__device__ __forceinline__ void peer_send(uint32_t addr, uint32_t bar, uint32_t a, uint32_t b, uint32_t c) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %3}, [%4];" ::"r"(addr),
+      "r"(a), "r"(b), "r"(c), "r"(bar)
+      : "memory");
 }
 // Order of floats as order of ints, for the warp-wide maximum.
 __device__ __forceinline__ int ordered(float x) {
@@ -156,6 +160,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV, MULTI)) spec_logits_kern
   const int nb = a.max_bias;
   if (tid == 0) {
     mbar_init(&s.landed, 1);
+    mbar_init(&s.joined[0], 1);
+    mbar_init(&s.joined[1], 1);
     mbar_fence_init();
   }
   __syncthreads();
@@ -535,17 +541,17 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV, MULTI)) spec_logits_kern
       sum = lane < kWarps ? s.red_sum[lane] : 0.f;
       best = lane < kWarps ? s.red_at[lane] : 0x7fffffff;
       join_warp();
-      if (lane < C) {
-        peer_store(peer_address(&s.peer_max[side][rank], lane), __float_as_uint(m));
-        peer_store(peer_address(&s.peer_sum[side][rank], lane), __float_as_uint(sum));
-        peer_store(peer_address(&s.peer_at[side][rank], lane), (uint32_t)best);
-      }
+      if (lane == 0) mbar_arrive_expect_tx(&s.joined[side], (uint32_t)C * 16);
+      // (A barrier of the cluster would wait for the stores of the row before.  A peer that sends the
+      // row after next has had this CTA's next one, sent when all its threads had read this.)
+      if (lane < C)
+        peer_send(peer_address(s.peer[side][rank], lane), peer_address(&s.joined[side], lane), __float_as_uint(m),
+                  __float_as_uint(sum), (uint32_t)best);
     }
-    cluster_arrive();
-    cluster_wait();
-    m = lane < C ? s.peer_max[side][lane] : -INFINITY;
-    sum = lane < C ? s.peer_sum[side][lane] : 0.f;
-    best = lane < C ? s.peer_at[side][lane] : 0x7fffffff;
+    if (!mbar_wait(&s.joined[side], (nth >> 1) & 1) && lane == 0) atomicOr(a.err, VAS_DEV_TIMEOUT);
+    m = lane < C ? __uint_as_float(s.peer[side][lane][0]) : -INFINITY;
+    sum = lane < C ? __uint_as_float(s.peer[side][lane][1]) : 0.f;
+    best = lane < C ? (int)s.peer[side][lane][2] : 0x7fffffff;
     join_warp();
     const float row_ref = m == -INFINITY ? 0.f : m;
     const bool wild = bad || isnan(sum) || m == INFINITY;
@@ -572,7 +578,12 @@ __global__ void __launch_bounds__(kThreads, ctas_of(NV, MULTI)) spec_logits_kern
       store_chunk(k);
     }
   }
-  if (arrived) cluster_wait();
+  // No CTA leaves before its peers have sent what they send.
+  if (a.probs) {
+    if (arrived) cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 namespace {
