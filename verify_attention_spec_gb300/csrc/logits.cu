@@ -136,11 +136,9 @@ __device__ __forceinline__ void load8(const float* p, float (&y)[8]) {
 __device__ __forceinline__ float widen1(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float widen1(float x) { return x; }
 
-// CTAs of an SM (three of 8 logits a thread: 40 rows of 32000 logits 13 us, with two 17).
-__host__ __device__ constexpr int ctas_of(int nv, bool multi) { return multi || nv > 4 ? 1 : (nv == 1 ? 3 : 2); }
-
-template <typename T, bool VEC, int NV, bool MULTI>
-__global__ void __launch_bounds__(kThreads, ctas_of(NV, MULTI)) spec_logits_kernel(const Args a) {
+// CTAS: of an SM.
+template <typename T, bool VEC, int NV, bool MULTI, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) spec_logits_kernel(const Args a) {
   using L = Tile<T, VEC, NV>;
   constexpr int kMapWords = L::kTokens / 32;
   // The entries' words, adjusted logits and places, and the place of a row's slice.
@@ -606,7 +604,7 @@ bool room(const Args& a, int slice, int size) {
   return entries_of(a, slice) * kEntryBytes + (slice * size + 15) / 16 * 16 <= 96 * 1024;
 }
 
-template <typename T, bool VEC, int NV, bool MULTI>
+template <typename T, bool VEC, int NV, bool MULTI, int CTAS>
 int launch(Args& a, cudaStream_t stream) {
   constexpr int kTokens = Tile<T, VEC, NV>::kTokens;
   constexpr int kMost = 200 * 1024;
@@ -615,7 +613,7 @@ int launch(Args& a, cudaStream_t stream) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxCachedDevices) return VAS_E_CUDA;
   std::call_once(once[dev], [&] {
-    attr_err[dev] = cudaFuncSetAttribute(spec_logits_kernel<T, VEC, NV, MULTI>,
+    attr_err[dev] = cudaFuncSetAttribute(spec_logits_kernel<T, VEC, NV, MULTI, CTAS>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
   });
   if (attr_err[dev] != cudaSuccess) return VAS_E_CUDA;
@@ -644,7 +642,7 @@ int launch(Args& a, cudaStream_t stream) {
   uint64_t k = known[dev].load(std::memory_order_relaxed);
   if (k >> 20 != shape >> 20) {
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, spec_logits_kernel<T, VEC, NV, MULTI>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, spec_logits_kernel<T, VEC, NV, MULTI, CTAS>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       return VAS_E_CUDA;
     }
@@ -654,7 +652,7 @@ int launch(Args& a, cudaStream_t stream) {
   const int most = (int)(k & 0xfffff);
   a.clusters = a.rows < most ? a.rows : most;
   cfg.gridDim = dim3((unsigned)(a.cluster * a.clusters));
-  if (cudaLaunchKernelEx(&cfg, spec_logits_kernel<T, VEC, NV, MULTI>, a) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, spec_logits_kernel<T, VEC, NV, MULTI, CTAS>, a) != cudaSuccess) {
     cudaGetLastError();
     return VAS_E_CUDA;
   }
@@ -670,15 +668,21 @@ int launch_size(Args& a, cudaStream_t stream) {
   const int widest = std::min((a.V + kThreads * 8 - 1) / (kThreads * 8), kMaxCluster);
   const int wanted = (2 * vas::num_sms() + a.rows - 1) / a.rows;
   auto slice_of = [&](int c) { return ((a.V + c - 1) / c + 31) / 32 * 32; };
-  int cluster = std::min(wanted, widest);
+  // (8 logits a thread and no more keep up with that for two rounds: 40 rows of 32000 logits 11 us, 18
+  // with 7 CTAs each.)
+  const bool narrow = a.V <= kThreads * 8 * kMaxCluster && (int64_t)a.rows * widest <= 6 * vas::num_sms();
+  int cluster = narrow ? widest : std::min(wanted, widest);
   while (cluster < widest && (slice_of(cluster) > kThreads * 32 || !room(a, slice_of(cluster), sizeof(T)))) ++cluster;
   a.slice = slice_of(cluster);
   a.cluster = cluster;
   const int per = (a.slice + kThreads * 8 - 1) / (kThreads * 8);
-  if (per <= 1) return launch<T, VEC, 1, false>(a, stream);
-  if (per <= 4) return launch<T, VEC, 4, false>(a, stream);
-  if (per <= 8 && entries_of(a, a.slice) * kEntryBytes <= 180 * 1024) return launch<T, VEC, 8, false>(a, stream);
-  return launch<T, VEC, 4, true>(a, stream);
+  // A third CTA of an SM costs registers (0.4 us of 4 rows): where there are so many.
+  if (per <= 1)
+    return (int64_t)a.rows * cluster > 2 * vas::num_sms() ? launch<T, VEC, 1, false, 3>(a, stream)
+                                                          : launch<T, VEC, 1, false, 2>(a, stream);
+  if (per <= 4) return launch<T, VEC, 4, false, 2>(a, stream);
+  if (per <= 8 && entries_of(a, a.slice) * kEntryBytes <= 180 * 1024) return launch<T, VEC, 8, false, 1>(a, stream);
+  return launch<T, VEC, 4, true, 1>(a, stream);
 }
 
 }  // namespace
