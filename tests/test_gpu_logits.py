@@ -152,6 +152,13 @@ def test_parts(vas_lib, kw, dtype, probs):
     Case(3, 6, 5000, dtype=dtype, **{"temps": probs, **kw}).check(vas_lib, probs)
 
 
+@pytest.mark.parametrize("B,n,V", [(120, 1, 20000), (60, 0, 32000), (300, 0, 9000), (40, 9, 2000), (50, 1, 16001)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_rows(vas_lib, B, n, V, dtype):
+    """Rows that fill the GPU several times over, shared by fewer CTAs each."""
+    Case(B, n, V, dtype=dtype, bias=9, mask=True, tree=n > 1).check(vas_lib)
+
+
 @pytest.mark.parametrize("n", [255])
 def test_long_windows(vas_lib, n):
     Case(2, n, 500, tree=True).check(vas_lib)
